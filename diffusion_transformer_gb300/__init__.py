@@ -10,7 +10,8 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_char_p, c_float, c_int, c_int64, c_size_t, c_void_p
+from ctypes import (POINTER, byref, c_char_p, c_double, c_float, c_int, c_int64, c_longlong, c_size_t, c_uint8, c_uint64,
+                    c_void_p)
 from typing import List, Optional, Sequence
 
 __all__ = [
@@ -24,7 +25,9 @@ __all__ = [
     "dit_parallel_block_forward_lora", "dit_double_block_forward_lora", "dit_parallel_block_forward_sandwich",
     "dit_double_block_forward_sandwich",
     "dit_block_forward_sandwich", "dit_euler_step",
-    "dit_rope_tables",
+    "dit_rope_tables", "RotaryPlan", "dit_rotary_plan_init", "dit_rotary_tables", "dit_rotary",
+    "DIT_FP4_NV", "DIT_FP4_MX", "Fp4Matrix", "dit_fp4_code_bytes", "dit_fp4_scale_bytes", "dit_fp4_quantize",
+    "dit_fp4_dequantize", "dit_fp4_matmul", "dit_linear_fp4", "dit_linear_fp4_workspace_bytes",
     "dit_denoise", "dit_block_forward_noalloc", "dit_block_noalloc_max_bytes", "dit_workspace_bytes", "dit_denoise_workspace_bytes", "dit_modnorm", "dit_qkv_rope",
     "dit_vt_stride", "dit_stream_k_workspace_bytes", "dit_attention", "dit_attention_qknorm", "dit_attention_workspace_bytes", "dit_linear_gated", "dit_linear_swiglu", "dit_linear",
     "dit_dequant_int8", "dit_linear_int8", "dit_linear_int8_workspace_bytes", "dit_check", "dit_selftest_bounded_wait", "dit_status_string", "dit_version",
@@ -33,6 +36,8 @@ __all__ = [
 _PKG = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_PKG, "libdit.so")
 
+DIT_BF16, DIT_F32 = 0, 1
+DIT_FP4_NV, DIT_FP4_MX = 0, 1
 DIT_OK, DIT_EINVAL, DIT_EUNSUPPORTED, DIT_EWORKSPACE, DIT_ECUDA, DIT_ETIMEOUT = 0, -1, -2, -3, -4, -5
 
 
@@ -84,7 +89,39 @@ class dit_model(ctypes.Structure):
                 ("w_out", c_void_p), ("block", POINTER(dit_block_w))]
 
 
+class dit_rotary_spec(ctypes.Structure):
+    _fields_ = [("axes", c_int), ("width", c_int * 4), ("layout", c_int), ("scaling", c_int), ("original", c_int),
+                ("theta", c_double), ("factor", c_double), ("beta_fast", c_double), ("beta_slow", c_double)]
+
+
+class dit_rotary_plan(ctypes.Structure):
+    _fields_ = [("pairs", c_int), ("axes", c_int), ("layout", c_int), ("amplitude", c_float),
+                ("turns", c_uint64 * 128), ("axis", c_uint8 * 128)]
+
+
+class dit_rotary_rows(ctypes.Structure):
+    _fields_ = [("x", c_void_p), ("out", c_void_p), ("heads", c_int), ("x_batch", c_longlong), ("x_row", c_longlong),
+                ("x_head", c_longlong), ("out_batch", c_longlong), ("out_row", c_longlong), ("out_head", c_longlong)]
+
+
+class dit_fp4_matrix(ctypes.Structure):
+    _fields_ = [("format", c_int), ("rows", c_int), ("cols", c_int), ("codes", c_void_p), ("scales", c_void_p),
+                ("row_scale", c_void_p)]
+
+
 _SIGNATURES = {
+    "dit_rotary_plan_init": (c_int, [POINTER(dit_rotary_spec), POINTER(dit_rotary_plan)]),
+    "dit_rotary_tables": (c_int, [POINTER(dit_rotary_plan), c_void_p, c_int, c_void_p, c_void_p, c_void_p]),
+    "dit_rotary": (c_int, [POINTER(dit_rotary_plan), POINTER(dit_rotary_rows), POINTER(dit_rotary_rows), c_int, c_int,
+                           c_int, c_int, c_void_p, c_int, c_void_p]),
+    "dit_fp4_code_bytes": (c_size_t, [c_int, c_int]),
+    "dit_fp4_scale_bytes": (c_size_t, [c_int, c_int, c_int]),
+    "dit_fp4_quantize": (c_int, [c_void_p, c_int, c_longlong, POINTER(dit_fp4_matrix), c_void_p]),
+    "dit_fp4_dequantize": (c_int, [POINTER(dit_fp4_matrix), c_void_p, c_int, c_longlong, c_void_p]),
+    "dit_fp4_matmul": (c_int, [POINTER(dit_fp4_matrix), POINTER(dit_fp4_matrix), c_void_p, c_int, c_longlong, c_void_p]),
+    "dit_linear_fp4": (c_int, [c_void_p, c_int, c_int, c_longlong, POINTER(dit_fp4_matrix), c_void_p, c_int,
+                               c_longlong, c_void_p, c_size_t, c_void_p]),
+    "dit_linear_fp4_workspace_bytes": (c_size_t, [c_int, c_int, c_int, c_int]),
     "dit_block_forward": (c_int, [POINTER(dit_dims), POINTER(dit_block_w), c_void_p, c_int, c_void_p, c_int,
                                   c_void_p, c_void_p, c_void_p, c_void_p, POINTER(dit_mod), c_void_p, c_size_t,
                                   c_void_p]),
@@ -561,6 +598,160 @@ def dit_rope_tables(L: int, grid_h: int, grid_w: int, head_dim: int, cos, sin, t
     import torch
     _ok(lib().dit_rope_tables(L, grid_h, grid_w, head_dim, theta, _ptr(cos, torch.float32, "cos"),
                               _ptr(sin, torch.float32, "sin"), _stream(stream)), "dit_rope_tables")
+
+
+def _typed(t, name):
+    """(device pointer, DIT_BF16 or DIT_F32) of a CUDA tensor on the current device whose last dimension is dense."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name}: expected a CUDA tensor on the current device")
+    if t.dtype is torch.bfloat16:
+        kind = DIT_BF16
+    elif t.dtype is torch.float32:
+        kind = DIT_F32
+    else:
+        raise TypeError(f"{name}: expected bfloat16 or float32, got {t.dtype}")
+    if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension must be dense")
+    return t.data_ptr(), kind
+
+
+class RotaryPlan:
+    """Frequencies of rotary positions (dit_rotary_spec), worked out once on the host. widths: rotated
+    values per position axis; layout "pairs" or "halves"; scaling "none", "linear", "ntk" or "yarn"."""
+
+    def __init__(self, widths: Sequence[int], layout: str = "pairs", theta: float = 10000.0, scaling: str = "none",
+                 factor: float = 1.0, original: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0):
+        widths = [int(w) for w in widths]
+        if not 1 <= len(widths) <= 4:
+            raise ValueError("widths: one to four axes")
+        self.spec = dit_rotary_spec(len(widths), (c_int * 4)(*widths), {"pairs": 0, "halves": 1}[layout],
+                                    {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}[scaling], original, theta, factor,
+                                    beta_fast, beta_slow)
+        self.c = dit_rotary_plan()
+        dit_rotary_plan_init(self.spec, self.c)
+        self.axes, self.dim = len(widths), sum(widths)
+
+
+def dit_rotary_plan_init(spec: dit_rotary_spec, plan: dit_rotary_plan):
+    _ok(lib().dit_rotary_plan_init(byref(spec), byref(plan)), "dit_rotary_plan_init")
+
+
+def _positions(plan: RotaryPlan, pos, rows: int):
+    import torch
+    if pos.numel() != rows * plan.axes:
+        raise ValueError(f"pos: expected {rows} x {plan.axes} positions")
+    if pos.is_cuda and pos.get_device() != torch.cuda.current_device():
+        raise ValueError("pos: expected a tensor on the current device")
+    return _ptr(pos, torch.int32, "pos")
+
+
+def dit_rotary_tables(plan: RotaryPlan, pos, cos, sin, stream=None):
+    """cos, sin [rows, plan.dim / 2] fp32 of pos [rows, plan.axes] int32 (or [rows] for one axis)."""
+    import torch
+    rows = cos.shape[0]
+    if cos.shape != (rows, plan.dim // 2) or sin.shape != cos.shape:
+        raise ValueError("cos, sin: expected [rows, dim / 2]")
+    _ok(lib().dit_rotary_tables(byref(plan.c), _positions(plan, pos, rows), rows, _ptr(cos, torch.float32, "cos"),
+                                _ptr(sin, torch.float32, "sin"), _stream(stream)), "dit_rotary_tables")
+
+
+def _rotary_rows(x, out, name):
+    if x.dim() not in (3, 4) or out.shape != x.shape or out.dtype != x.dtype:
+        raise ValueError(f"{name}: expected [batch, rows, heads, head_dim] or [rows, heads, head_dim], in and out alike")
+    px, kind = _typed(x, name)
+    po, _ = _typed(out, name)
+    sx, so = x.stride(), out.stride()
+    b = x.dim() == 4
+    return dit_rotary_rows(px, po, x.shape[-2], sx[0] if b else 0, sx[-3], sx[-2], so[0] if b else 0, so[-3], so[-2]), kind
+
+
+def dit_rotary(plan: RotaryPlan, q, k, pos, q_out=None, k_out=None, inverse: bool = False, stream=None):
+    """Turn q (and k, or None) [batch, rows, heads, head_dim] or [rows, heads, head_dim], any strides with a
+    dense head; q_out / k_out default to in place. pos [batch, rows, axes] int32 (axes may be left out
+    when there is one)."""
+    a, kind = _rotary_rows(q, q if q_out is None else q_out, "q")
+    c = None
+    if k is not None:
+        c, kk = _rotary_rows(k, k if k_out is None else k_out, "k")
+        if kk != kind or k.dim() != q.dim() or k.shape[:-2] != q.shape[:-2] or k.shape[-1] != q.shape[-1]:
+            raise ValueError("q and k: expected the same type, batch, rows and head_dim")
+    batch = q.shape[0] if q.dim() == 4 else 1
+    rows = q.shape[-3]
+    _ok(lib().dit_rotary(byref(plan.c), byref(a), byref(c) if c is not None else None, kind, batch, rows, q.shape[-1],
+                         _positions(plan, pos, batch * rows), 1 if inverse else 0, _stream(stream)), "dit_rotary")
+
+
+class Fp4Matrix:
+    """A microscaled 4-bit matrix [rows, cols] in the library's layout (dit_fp4_matrix): uint8 codes and
+    scales, fp32 row_scale (None for DIT_FP4_MX)."""
+
+    def __init__(self, format: int, rows: int, cols: int, codes, scales, row_scale=None):
+        import torch
+        if codes.numel() != dit_fp4_code_bytes(rows, cols) or scales.numel() != dit_fp4_scale_bytes(format, rows, cols):
+            raise ValueError("codes, scales: expected dit_fp4_code_bytes and dit_fp4_scale_bytes bytes")
+        if format == DIT_FP4_NV and (row_scale is None or row_scale.numel() != rows):
+            raise ValueError("row_scale: expected one value per row")
+        self.format, self.rows, self.cols = format, rows, cols
+        self.codes, self.scales, self.row_scale = codes, scales, row_scale
+        self.c = dit_fp4_matrix(format, rows, cols, _ptr(codes, torch.uint8, "codes"),
+                                _ptr(scales, torch.uint8, "scales"), _ptr(row_scale, torch.float32, "row_scale"))
+
+    @classmethod
+    def empty(cls, format: int, rows: int, cols: int, device="cuda"):
+        import torch
+        new = lambda n, dt: torch.empty(n, dtype=dt, device=device)  # noqa: E731
+        return cls(format, rows, cols, new(dit_fp4_code_bytes(rows, cols), torch.uint8),
+                   new(dit_fp4_scale_bytes(format, rows, cols), torch.uint8),
+                   new(rows, torch.float32) if format == DIT_FP4_NV else None)
+
+
+def _matrix(t, rows, cols, name):
+    p, kind = _typed(t, name)
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name}: expected [{rows}, {cols}], got {list(t.shape)}")
+    return p, kind, t.stride(0) if rows > 1 else cols
+
+
+def dit_fp4_code_bytes(rows: int, cols: int) -> int:
+    return lib().dit_fp4_code_bytes(rows, cols)
+
+
+def dit_fp4_scale_bytes(format: int, rows: int, cols: int) -> int:
+    return lib().dit_fp4_scale_bytes(format, rows, cols)
+
+
+def dit_fp4_quantize(x, m: Fp4Matrix, stream=None):
+    """x [m.rows, m.cols] bf16 or fp32 (rows may be strided) into m."""
+    p, kind, ld = _matrix(x, m.rows, m.cols, "x")
+    _ok(lib().dit_fp4_quantize(p, kind, ld, byref(m.c), _stream(stream)), "dit_fp4_quantize")
+
+
+def dit_fp4_dequantize(m: Fp4Matrix, out, stream=None):
+    """m's values into out [m.rows, m.cols] bf16 or fp32 (rows may be strided)."""
+    p, kind, ld = _matrix(out, m.rows, m.cols, "out")
+    _ok(lib().dit_fp4_dequantize(byref(m.c), p, kind, ld, _stream(stream)), "dit_fp4_dequantize")
+
+
+def dit_fp4_matmul(a: Fp4Matrix, b: Fp4Matrix, out, stream=None):
+    """out [a.rows, b.rows] bf16 or fp32 = a b^T."""
+    p, kind, ld = _matrix(out, a.rows, b.rows, "out")
+    _ok(lib().dit_fp4_matmul(byref(a.c), byref(b.c), p, kind, ld, _stream(stream)), "dit_fp4_matmul")
+
+
+def dit_linear_fp4_workspace_bytes(format: int, M: int, N: int, K: int) -> int:
+    return lib().dit_linear_fp4_workspace_bytes(format, M, N, K)
+
+
+def dit_linear_fp4(x, w: Fp4Matrix, out, ws, stream=None):
+    """out [M, w.rows] = fp4(x) w^T for x [M, w.cols], quantised per call into ws."""
+    M = x.shape[0]
+    p, kind, ld = _matrix(x, M, w.cols, "x")
+    po, ko, ldo = _matrix(out, M, w.rows, "out")
+    _ok(lib().dit_linear_fp4(p, kind, M, ld, byref(w.c), po, ko, ldo, _ptr(ws, None, "ws"),
+                             ws.numel() * ws.element_size(), _stream(stream)), "dit_linear_fp4")
 
 
 def dit_denoise(model: DenoiseModel, img_tokens, txt_feats, sigmas: Sequence[float], txt_cos, txt_sin, img_cos,

@@ -9,6 +9,7 @@
 #include <algorithm>
 #include <mutex>
 
+#include "fp4.cuh"
 #include "internal.h"
 #include "tmap.h"
 
@@ -67,6 +68,29 @@ struct BlockWs {
   uint16_t* a;   // [R, F]  SwiGLU output
   size_t bytes;
 };
+
+// A 4-bit matrix a caller hands over: format, sizes, pointers and their alignment.
+int check_fp4(const dit_fp4_matrix* m) {
+  if (!m || (m->format != DIT_FP4_NV && m->format != DIT_FP4_MX) || m->rows < 0 || m->cols < 1) return DIT_EINVAL;
+  if (m->rows == 0) return DIT_OK;
+  if (!m->codes || !m->scales || !al16(m->codes) || !al16(m->scales)) return DIT_EINVAL;
+  if (m->format == DIT_FP4_NV && (!m->row_scale || reinterpret_cast<uintptr_t>(m->row_scale) % 4)) return DIT_EINVAL;
+  return DIT_OK;
+}
+// Plain rows beside it: type, pointer (aligned to its type) and a row stride that holds `cols`.
+bool fp4_rows_ok(const void* p, int type, long long ld, int rows, int cols) {
+  if ((type != DIT_BF16 && type != DIT_F32) || ld < cols) return false;
+  return rows == 0 || (p && reinterpret_cast<uintptr_t>(p) % (type == DIT_BF16 ? 2 : 4) == 0);
+}
+// Codes, scales and row scales of a [rows, cols] matrix one after another at `base`, each 256-byte
+// aligned; returns the bytes they take.
+size_t carve_fp4(int format, int rows, int cols, void* base, dit_fp4_matrix* m) {
+  uint8_t* p = static_cast<uint8_t*>(base);
+  const size_t nc = round_up(size_t(rows) * size_t(fp4_code_row_bytes(cols)), 256);
+  const size_t ns = (size_t(rows) + 127) / 128 * size_t(fp4_groups(format, cols)) * 512;
+  *m = dit_fp4_matrix{format, rows, cols, p, p ? p + nc : nullptr, p ? reinterpret_cast<float*>(p + nc + ns) : nullptr};
+  return nc + ns + (format == DIT_FP4_NV ? round_up(size_t(rows) * 4, 256) : 0);
+}
 
 int vt_stride(int R) { return int(round_up(size_t(R), 8)); }
 
@@ -1300,6 +1324,67 @@ int dit_linear_w8a8(const uint16_t* a, int M, int K, const int8_t* q, const floa
   g.a_scale = sa;
   g.w_scale = scale;
   return gemm_launch(ac, K, wc, nullptr, kEpiStoreF32, g, st);
+}
+
+// --------------------------------------------------------------------------------------------
+// microscaled 4-bit matrices
+// --------------------------------------------------------------------------------------------
+size_t dit_fp4_code_bytes(int rows, int cols) {
+  return rows < 0 || cols < 1 ? 0 : size_t(rows) * size_t(fp4_code_row_bytes(cols));
+}
+
+size_t dit_fp4_scale_bytes(int format, int rows, int cols) {
+  if (rows < 0 || cols < 1 || (format != DIT_FP4_NV && format != DIT_FP4_MX)) return 0;
+  return (size_t(rows) + 127) / 128 * size_t(fp4_groups(format, cols)) * 512;
+}
+
+int dit_fp4_quantize(const void* x, int x_type, long long ldx, const dit_fp4_matrix* m, dit_stream_t stream) {
+  int rc = check_fp4(m);
+  if (rc != DIT_OK) return rc;
+  if (!fp4_rows_ok(x, x_type, ldx, m->rows, m->cols)) return DIT_EINVAL;
+  if (m->rows == 0) return DIT_OK;
+  return fp4_quantize_launch(x, x_type, ldx, *m, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int dit_fp4_dequantize(const dit_fp4_matrix* m, void* out, int out_type, long long ldo, dit_stream_t stream) {
+  int rc = check_fp4(m);
+  if (rc != DIT_OK) return rc;
+  if (!fp4_rows_ok(out, out_type, ldo, m->rows, m->cols)) return DIT_EINVAL;
+  if (m->rows == 0) return DIT_OK;
+  return fp4_dequantize_launch(*m, out, out_type, ldo, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int dit_fp4_matmul(const dit_fp4_matrix* a, const dit_fp4_matrix* b, void* out, int out_type, long long ldo,
+                   dit_stream_t stream) {
+  int rc = check_fp4(a);
+  if (rc == DIT_OK) rc = check_fp4(b);
+  if (rc != DIT_OK) return rc;
+  if (a->format != b->format || a->cols != b->cols) return DIT_EINVAL;
+  if (a->rows == 0 || b->rows == 0) return DIT_OK;
+  if (!fp4_rows_ok(out, out_type, ldo, a->rows, b->rows)) return DIT_EINVAL;
+  return fp4_matmul_launch(*a, *b, out, out_type, ldo, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t dit_linear_fp4_workspace_bytes(int format, int M, int N, int K) {
+  if (M < 0 || N < 0 || K < 1 || (format != DIT_FP4_NV && format != DIT_FP4_MX)) return 0;
+  dit_fp4_matrix a;
+  return carve_fp4(format, M, K, nullptr, &a);
+}
+
+int dit_linear_fp4(const void* x, int x_type, int M, long long ldx, const dit_fp4_matrix* w, void* out, int out_type,
+                   long long ldo, void* ws, size_t ws_bytes, dit_stream_t stream) {
+  int rc = check_fp4(w);
+  if (rc != DIT_OK) return rc;
+  if (M < 0) return DIT_EINVAL;
+  if (M == 0 || w->rows == 0) return DIT_OK;
+  if (!fp4_rows_ok(x, x_type, ldx, M, w->cols) || !fp4_rows_ok(out, out_type, ldo, M, w->rows)) return DIT_EINVAL;
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u)) return DIT_EINVAL;
+  if (ws_bytes < dit_linear_fp4_workspace_bytes(w->format, M, w->rows, w->cols)) return DIT_EWORKSPACE;
+  dit_fp4_matrix a;
+  carve_fp4(w->format, M, w->cols, ws, &a);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  rc = fp4_quantize_launch(x, x_type, ldx, a, st);
+  return rc == DIT_OK ? fp4_matmul_launch(a, *w, out, out_type, ldo, st) : rc;
 }
 
 int dit_block_forward_int8(const dit_dims* d, const dit_block_w8* w, float* txt, int L, float* img, int N,

@@ -1,0 +1,130 @@
+// The arithmetic and the memory layout of microscaled 4-bit matrices, shared by the kernels that
+// write, read and multiply them. (The conversions are PTX cvt instructions: one rounding each, to
+// nearest with ties to even.)
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "../../include/dit.h"
+
+namespace dit {
+
+// Code bytes of a row: two codes per byte (even column in the low half), rows padded with zero codes
+// to whole 32 columns, so every row starts on 16 bytes (the TMA's rule for strides).
+__host__ __device__ constexpr long long fp4_code_row_bytes(int cols) { return (cols + 31LL) / 32 * 16; }
+// Groups of four blocks along a row (the last one padded).
+__host__ __device__ constexpr int fp4_groups(int fmt, int cols) {
+  const int block = fmt == DIT_FP4_NV ? 16 : 32;
+  return (cols + 4 * block - 1) / (4 * block);
+}
+// Scale bytes stand in tiles of 128 rows x 4 blocks, 512 bytes each, the tiles of a 128-row band one
+// after another: inside a tile row r is at 16 (r % 32) + 4 (r / 32), its four blocks consecutive. This
+// is the order tcgen05.cp (32 x 128 bit) spreads over tensor memory for the block-scaled MMA.
+__host__ __device__ constexpr long long fp4_scale_row(int fmt, int row, int cols) {
+  return (long long)(row >> 7) * fp4_groups(fmt, cols) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4;
+}
+__host__ __device__ constexpr int fp4_scale_block(int block) { return (block >> 2) * 512 + (block & 3); }
+
+// A row's derived factors (NV) from the bits of its largest magnitude A: u = 448 / A maps a block's
+// magnitude to its e4m3 scale, t = 2688 / A = 1 / g, g = A / 2688 (448 * 6: the largest scale times the
+// largest code). Below 2^-100 the quotients would overflow: such a row counts as zero. An infinity or
+// NaN makes g NaN: the row's values, and its products, come out as NaN.
+struct Fp4Row {
+  float u, t, g;
+};
+__device__ __forceinline__ Fp4Row fp4_row(uint32_t bits) {
+  if (bits < 0x0d800000u) return Fp4Row{0.f, 0.f, 0.f};  // 2^-100
+  if (bits >= 0x7f800000u) return Fp4Row{0.f, 0.f, __uint_as_float(0x7fc00000u)};
+  const float a = __uint_as_float(bits);
+  return Fp4Row{__fdiv_rn(448.f, a), __fdiv_rn(2688.f, a), __fdiv_rn(a, 2688.f)};
+}
+
+struct Fp4Block {
+  uint32_t byte;  // the block scale
+  float inv;      // what a value is multiplied with before it is rounded to a code
+};
+
+__device__ __forceinline__ float fp4_e4m3(uint32_t byte) {
+  uint32_t h;
+  asm("{\n.reg .b16 p;\ncvt.u16.u32 p, %1;\ncvt.rn.f16x2.e4m3x2 %0, p;\n}" : "=r"(h) : "r"(byte));
+  float f;
+  asm("{\n.reg .b16 lo, hi;\nmov.b32 {lo, hi}, %1;\ncvt.f32.f16 %0, lo;\n}" : "=f"(f) : "r"(h));
+  return f;
+}
+__device__ __forceinline__ float fp4_e8m0(uint32_t byte) {
+  return byte == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float(byte == 0 ? 1u << 22 : byte << 23);
+}
+
+__device__ __forceinline__ Fp4Block fp4_block_nv(uint32_t bits, float u, float t) {
+  // a row with an infinity or NaN has u = t = 0; only finite products may reach the conversion
+  const float v = u > 0.f ? fminf(__fmul_rn(__uint_as_float(bits), u), 448.f) : 0.f;
+  uint32_t byte;
+  asm("{\n.reg .b16 p;\ncvt.rn.satfinite.e4m3x2.f32 p, %2, %1;\ncvt.u32.u16 %0, p;\n}" : "=r"(byte) : "f"(v), "f"(0.f));
+  const float s = fp4_e4m3(byte);
+  return Fp4Block{byte, s > 0.f ? __fdiv_rn(t, s) : 0.f};
+}
+__device__ __forceinline__ Fp4Block fp4_block_mx(uint32_t bits) {
+  if (bits >= 0x7f800000u) return Fp4Block{255u, 0.f};
+  if (bits == 0u) return Fp4Block{0u, 0.f};
+  // floor(log2) of a magnitude below 2^-126 clamps to the same lowest scale
+  const int e = max(int(bits >> 23) - 127 - 2, -127);
+  return Fp4Block{uint32_t(e + 127), __uint_as_float(uint32_t(127 - e) << 23)};
+}
+
+// 16 values times inv, rounded to codes: 8 bytes, the lower columns first. inv = 0 gives zero codes
+// whatever the values (a row or block with an infinity or NaN keeps no code).
+__device__ __forceinline__ uint32_t fp4_codes8(const float* v, float inv) {
+  uint32_t w;
+  asm("{\n.reg .b8 a, b, c, d;\n"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+      "mov.b32 %0, {a, b, c, d};\n}"
+      : "=r"(w)
+      : "f"(__fmul_rn(v[0], inv)), "f"(__fmul_rn(v[1], inv)), "f"(__fmul_rn(v[2], inv)), "f"(__fmul_rn(v[3], inv)),
+        "f"(__fmul_rn(v[4], inv)), "f"(__fmul_rn(v[5], inv)), "f"(__fmul_rn(v[6], inv)), "f"(__fmul_rn(v[7], inv)));
+  return w;
+}
+__device__ __forceinline__ void fp4_codes16(const float* v, float inv, uint32_t (&w)[2]) {
+  w[0] = inv != 0.f ? fp4_codes8(v, inv) : 0u;
+  w[1] = inv != 0.f ? fp4_codes8(v + 8, inv) : 0u;
+}
+
+__device__ __forceinline__ void fp4_values16(uint2 w, float* v) {
+  const uint32_t u[2] = {w.x, w.y};
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t p[4];
+    asm("{\n.reg .b8 a, b, c, d;\n"
+        "mov.b32 {a, b, c, d}, %4;\n"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n"
+        "cvt.rn.f16x2.e2m1x2 %1, b;\n"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n"
+        "cvt.rn.f16x2.e2m1x2 %3, d;\n}"
+        : "=r"(p[0]), "=r"(p[1]), "=r"(p[2]), "=r"(p[3])
+        : "r"(u[h]));
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      asm("{\n.reg .b16 lo, hi;\nmov.b32 {lo, hi}, %2;\ncvt.f32.f16 %0, lo;\ncvt.f32.f16 %1, hi;\n}"
+          : "=f"(v[8 * h + 2 * j]), "=f"(v[8 * h + 2 * j + 1])
+          : "r"(p[j]));
+  }
+}
+
+// 32 bytes of global memory (32-byte aligned) in one load
+__device__ __forceinline__ void ld_global_256(uint32_t (&w)[8], const void* p) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p));
+}
+
+struct Fp4View {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  const float* row_scale;
+  int rows;
+};
+
+}  // namespace dit

@@ -201,6 +201,12 @@ int quant_weight_launch(const uint16_t* w, int N, int K, const float* smooth, in
                         cudaStream_t stream);
 int codes_bf16_launch(const int8_t* q, uint16_t* w, long long n, cudaStream_t stream);
 
+// Microscaled 4-bit matrices (see dit_fp4_quantize and the calls after it), on validated arguments
+int fp4_quantize_launch(const void* x, int type, long long ldx, const dit_fp4_matrix& m, cudaStream_t stream);
+int fp4_dequantize_launch(const dit_fp4_matrix& m, void* out, int type, long long ldo, cudaStream_t stream);
+int fp4_matmul_launch(const dit_fp4_matrix& a, const dit_fp4_matrix& b, void* out, int type, long long ldo,
+                      cudaStream_t stream);
+
 int num_sms();
 
 // Launch `kern` on `stream` with programmatic dependent launch allowed (and a cluster of

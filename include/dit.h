@@ -395,6 +395,130 @@ DIT_API int dit_euler_step(float* x, const float* vel, int64_t n, float sigma, f
 DIT_API int dit_rope_tables(int L, int grid_h, int grid_w, int head_dim, float theta, float* cos, float* sin,
                     dit_stream_t stream);
 
+/* Rotary positions for any head: `axes` position axes side by side, axis a rotating width[a] values
+ * (even, the sum at most 2 * DIT_ROTARY_MAX_PAIRS); pair k of axis a has the frequency
+ * f = theta^(-2k / width[a]) and turns by f * (the row's position on that axis). The pairs of all axes
+ * follow one another and cover the first `dim` = sum(width) values of a head; the rest stay as they
+ * are. [host contract, section 4; gizai:dit, prepOf, HEAD; klein, section 4.4]
+ *   layout  DIT_ROTARY_PAIRS: pair i is the values (2i, 2i + 1)  [host contract, section 4]
+ *           DIT_ROTARY_HALVES: pair i is the values (i, i + dim / 2)  [gizai:dit, prepOf]
+ * scaling, for sequences (grids) longer than the trained ones, by `factor` >= 1:
+ *   DIT_ROTARY_LINEAR  f / factor
+ *   DIT_ROTARY_NTK     theta * factor^(w / (w - 2)) in theta's place (w = width[a]; w = 2: unscaled)
+ *   DIT_ROTARY_YARN    f (1 - r) + (f / factor) r with r = clamp((k - lo) / max(hi - lo, 0.001), 0, 1),
+ *                      lo = max(0, floor(at(beta_fast))), hi = min(w/2 - 1, ceil(at(beta_slow))),
+ *                      at(n) = w ln(original / (2 pi n)) / (2 ln theta), the pair that makes n turns over
+ *                      the `original` positions; cos and sin are times 0.1 ln(factor) + 1
+ * factor, original and the betas are read only by the scalings that name them. */
+#define DIT_ROTARY_MAX_AXES 4
+#define DIT_ROTARY_MAX_PAIRS 128
+#define DIT_ROTARY_PAIRS 0
+#define DIT_ROTARY_HALVES 1
+#define DIT_ROTARY_UNSCALED 0
+#define DIT_ROTARY_LINEAR 1
+#define DIT_ROTARY_NTK 2
+#define DIT_ROTARY_YARN 3
+typedef struct {
+  int axes;
+  int width[DIT_ROTARY_MAX_AXES];
+  int layout;
+  int scaling;
+  int original;
+  double theta; /* > 1 */
+  double factor;
+  double beta_fast, beta_slow; /* usual: 32, 1 */
+} dit_rotary_spec;
+
+/* What dit_rotary and dit_rotary_tables need of a spec, computed once on the host (64-bit arithmetic) by
+ * dit_rotary_plan_init: per pair the turns per position as a fraction of 2^64, and its axis. A host
+ * struct, passed by pointer and copied into each launch. DIT_EINVAL for a spec outside the ranges
+ * above, DIT_EUNSUPPORTED for more than DIT_ROTARY_MAX_PAIRS pairs; *plan is then left as it was. */
+typedef struct {
+  int pairs, axes, layout;
+  float amplitude;
+  uint64_t turns[DIT_ROTARY_MAX_PAIRS];
+  uint8_t axis[DIT_ROTARY_MAX_PAIRS];
+} dit_rotary_plan;
+DIT_API int dit_rotary_plan_init(const dit_rotary_spec* spec, dit_rotary_plan* plan);
+
+/* Rotary tables from positions: pos [rows, axes] int32 (any value, negative ones too) -> cos, sin
+ * [rows, pairs] fp32, the angle reduced modulo one turn in integers before it is rounded, so far
+ * positions are as exact as near ones. With widths (16, 56, 56) or (8, 28, 28) and DIT_ROTARY_PAIRS
+ * these are tables for every block form here (rows of the text, then of the image), with any of the
+ * scalings above; with one axis of 3d/4 and DIT_ROTARY_HALVES, for rope_split blocks. */
+DIT_API int dit_rotary_tables(const dit_rotary_plan* plan, const int32_t* pos, int rows, float* cos, float* sin,
+                              dit_stream_t stream);
+
+/* The heads of one tensor: value j of head h of row t of batch entry b is at
+ * x[b * x_batch + t * x_row + h * x_head + j] (strides in values), likewise for out. out may be x with
+ * the same strides (in place); otherwise the two must not overlap. */
+typedef struct {
+  const void* x;
+  void* out;
+  int heads;
+  long long x_batch, x_row, x_head;
+  long long out_batch, out_row, out_head;
+} dit_rotary_rows;
+
+/* Rotary positions applied: per pair (a, b) of a head at angle t, out = (a cos t - b sin t,
+ * a sin t + b cos t), in fp32 with one rounding to the tensor's type; values behind the rotated part are
+ * copied. q and k (k may be NULL) are done in one launch, with their own head counts and strides: they
+ * may be columns of one QKV product and be written head-major, as dit_attention reads them. pos
+ * [batch * rows, axes] int32. inverse != 0 turns back by the same angles, times the same amplitude:
+ * the transpose of the forward map, which takes the gradient of its output to that of its input.
+ * type: DIT_BF16 or DIT_F32. head_dim at most 2 * DIT_ROTARY_MAX_PAIRS, at least the rotated part. Rows,
+ * heads and tensors on 16-byte boundaries run with 16-byte accesses; any other alignment is served too.
+ * batch, rows or heads of 0: nothing to do. */
+#define DIT_BF16 0
+#define DIT_F32 1
+DIT_API int dit_rotary(const dit_rotary_plan* plan, const dit_rotary_rows* q, const dit_rotary_rows* k, int type,
+                       int batch, int rows, int head_dim, const int32_t* pos, int inverse, dit_stream_t stream);
+
+/* Microscaled 4-bit matrices (no counterpart on the pages, whose lowest tiers are int8 and INT4: an
+ * opt-in lossy tier in the tensor cores' 4-bit floating point). A matrix [rows, cols] is stored as e2m1
+ * codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 with a sign) with a scale per block of consecutive columns:
+ *   DIT_FP4_NV  blocks of 16, e4m3 scale s, and an fp32 scale g per row: value = (code * s) * g.
+ *               With A the row's and a the block's largest magnitude, in single fp32 operations:
+ *               g = A / 2688, s = e4m3(min(a * (448 / A), 448)), code = e2m1(x * ((2688 / A) / s)) (0
+ *               where s = 0), each conversion to nearest, ties to even, codes saturating at 6. A row with
+ *               A < 2^-100 counts as zero (g = 0). A row with an infinity or a NaN has g = NaN and zero
+ *               codes: all its values, and its products, are NaN.
+ *   DIT_FP4_MX  blocks of 32, scale 2^e (e8m0), no row scale: value = code * 2^e, e = floor(log2 a) - 2
+ *               clamped to [-127, 127]; a block with an infinity or a NaN has a NaN scale.
+ * Layout: codes [rows, dit_fp4_code_bytes / rows], two per byte, even column in the low half, rows
+ * padded with zero codes to whole 32 columns; scales in tiles of 128 rows x 4 blocks of 512 bytes, the
+ * tiles of a 128-row band one after another, row r of a tile at byte 16 (r % 32) + 4 (r / 32), its four
+ * blocks consecutive (blocks past cols: zero; bytes of rows past the last are not written and never
+ * matter); row_scale [rows] fp32 (NV; ignored for MX). codes and scales 16-byte aligned. */
+#define DIT_FP4_NV 0
+#define DIT_FP4_MX 1
+typedef struct {
+  int format;
+  int rows, cols;
+  uint8_t* codes;
+  uint8_t* scales;
+  float* row_scale;
+} dit_fp4_matrix;
+DIT_API size_t dit_fp4_code_bytes(int rows, int cols);               /* 0 for rows < 0 or cols < 1 */
+DIT_API size_t dit_fp4_scale_bytes(int format, int rows, int cols);  /* 0 also for an unknown format */
+
+/* x [m->rows, m->cols] (bf16 or fp32, row stride ldx >= cols) quantised into m; and m's values as bf16 or
+ * fp32 (row stride ldo). rows = 0: nothing to do. */
+DIT_API int dit_fp4_quantize(const void* x, int x_type, long long ldx, const dit_fp4_matrix* m, dit_stream_t stream);
+DIT_API int dit_fp4_dequantize(const dit_fp4_matrix* m, void* out, int out_type, long long ldo, dit_stream_t stream);
+
+/* out [a->rows, b->rows] = a b^T over the matrices' values (same format and cols), fp32 accumulation,
+ * stored as bf16 or fp32 with row stride ldo >= b->rows. Any sizes. out must not overlap the inputs. */
+DIT_API int dit_fp4_matmul(const dit_fp4_matrix* a, const dit_fp4_matrix* b, void* out, int out_type, long long ldo,
+                           dit_stream_t stream);
+
+/* One 4-bit linear: out [M, w->rows] = fp4(x) w^T, x [M, w->cols] bf16 or fp32 (row stride ldx) quantised
+ * per call into the workspace in w's format. x is not modified. Workspace:
+ * dit_linear_fp4_workspace_bytes(format, M, N, K), 256-byte aligned. M = 0: nothing to do. */
+DIT_API int dit_linear_fp4(const void* x, int x_type, int M, long long ldx, const dit_fp4_matrix* w, void* out,
+                           int out_type, long long ldo, void* ws, size_t ws_bytes, dit_stream_t stream);
+DIT_API size_t dit_linear_fp4_workspace_bytes(int format, int M, int N, int K);
+
 /* Denoise model: the 32 (or `blocks`) stacked blocks plus the plain DiT around them.
  *   w_in   [H, C] bf16    patch-in of the packed latent tokens (C = latent_channels)
  *   w_t1   [H, 256] bf16  time MLP first linear;  w_t2 [H, H] bf16 second linear

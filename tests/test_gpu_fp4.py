@@ -1,0 +1,243 @@
+"""Microscaled 4-bit matrices on the GPU against the oracle (oracle/fp4.py): codes, scales and row scales
+bit for bit, the values bit for bit, and products against 64 bits.
+
+Product gate. The values are exact in fp32 and every product of two code-times-scale values is exact;
+what is rounded is the fp32 accumulation. A tensor-core step sums 64 columns and the accumulator with
+the terms aligned to the largest: allow one unit (2^-23) of the magnitude of everything summed so far
+per step, in either direction, so |error| <= (K / 64 + 2) 2^-23 S with S = sum |a||b| (one extra step for
+split sums joined at the end, one for the two row-scale products' half units). A store as bf16 adds half
+a step, 2^-8 of the value. A fp32 FMA loop stays within the same bound only for short K; the largest here
+through such a loop would err randomly, far below K 2^-24 S."""
+
+import numpy as np
+import pytest
+import torch
+
+import diffusion_transformer_gb300 as D
+import oracle as O
+from tests.gpu_util import bf16_bits, dev, workspace
+
+pytestmark = pytest.mark.gpu
+
+NV, MX = D.DIT_FP4_NV, D.DIT_FP4_MX
+FMT = pytest.mark.parametrize("fmt", [NV, MX], ids=["nv", "mx"])
+
+
+def _rows(g, R, K, bf16=True):
+    """Activations with rows of unlike size and a few wide columns, as float32 (bf16 values if asked)."""
+    x = g.standard_normal((R, K)) * np.exp(g.standard_normal((R, 1))) * np.where(g.random(K) < 0.02, 20, 1)
+    return _as_bf16(x) if bf16 else x.astype(np.float32)
+
+
+def _as_bf16(x):
+    return torch.from_numpy(np.asarray(x, np.float32)).bfloat16().float().numpy()
+
+
+def _on_gpu(x, dtype, pad=0, shift=0):
+    """x on the GPU with `pad` values between rows and its first value `shift` values into its memory."""
+    R, K = x.shape
+    mem = torch.full((R * (K + pad) + shift + 64,), 77.0, dtype=dtype, device="cuda")
+    v = mem[shift:shift + R * (K + pad)].view(R, K + pad)[:, :K]
+    v.copy_(torch.from_numpy(x))
+    return v
+
+
+def _stored(codes, scale, fmt, R, K):
+    return O.fp4_pack(codes, scale, fmt)
+
+
+def _check_quantised(m, x, fmt):
+    codes, scale, row = O.fp4_quantize(x, fmt)
+    packed, tiles = O.fp4_pack(codes, scale, fmt)
+    R = x.shape[0]
+    assert np.array_equal(m.codes.cpu().numpy().reshape(R, -1), packed)
+    got = m.scales.cpu().numpy().reshape(-1, tiles.size // 512 // max(1, -(-R // 128)), 32, 4, 4)
+    want = tiles.reshape(got.shape)
+    r = np.arange(R)
+    at = (r // 128, slice(None), r % 32, (r % 128) // 32)
+    assert np.array_equal(got[at], want[at])
+    if fmt == NV:
+        assert np.array_equal(m.row_scale.cpu().numpy(), row, equal_nan=True)
+    return codes, scale, row
+
+
+@FMT
+@pytest.mark.parametrize("R,K,dtype,pad,shift", [
+    (1, 1, torch.bfloat16, 0, 0), (1, 16, torch.float32, 0, 0), (3, 31, torch.bfloat16, 0, 0),
+    (5, 64, torch.bfloat16, 0, 0), (130, 100, torch.float32, 28, 0), (33, 1000, torch.bfloat16, 3, 5),
+    (7, 1003, torch.float32, 0, 1), (2, 4096, torch.bfloat16, 0, 0), (9, 5000, torch.bfloat16, 8, 8),
+    (300, 48, torch.float32, 0, 0), (4, 12288, torch.bfloat16, 0, 0), (3, 20011, torch.float32, 0, 0)])
+def test_quantize_is_bit_exact(fmt, R, K, dtype, pad, shift):
+    g = np.random.default_rng(R * 7919 + K)
+    x = _rows(g, R, K, dtype == torch.bfloat16)
+    if R > 2:
+        x[1] = 0
+        x[2] *= _as_bf16(np.full(1, 1e-30))[0]
+        x = _as_bf16(x) if dtype == torch.bfloat16 else x
+    xd = _on_gpu(x, dtype, pad, shift)
+    m = D.Fp4Matrix.empty(fmt, R, K)
+    m.codes.fill_(255)
+    m.scales.fill_(255)
+    D.dit_fp4_quantize(xd, m)
+    codes, scale, row = _check_quantised(m, x, fmt)
+    want = O.fp4_values(codes, scale, row, fmt, K)
+    for odt in (torch.float32, torch.bfloat16):
+        out = _on_gpu(np.zeros((R, K), np.float32), odt, pad, shift)
+        D.dit_fp4_dequantize(m, out)
+        w = torch.from_numpy(want).to(odt).float().numpy()
+        assert np.array_equal(out.float().cpu().numpy(), w)
+        if pad:  # what lies between the rows stays
+            whole = torch.as_strided(out, (R, K + pad), (K + pad, 1))
+            assert (whole[:-1, K:] == 77).all()
+    D.dit_check()
+
+
+@FMT
+def test_quantize_extremes(fmt):
+    K = 96
+    x = np.ones((14, K), np.float32)
+    x[0, 5] = np.inf
+    x[1, 40] = -np.inf
+    x[2, 95] = np.nan
+    x[3] = 2.0 ** -99
+    x[4] = 2.0 ** -100
+    x[5] = np.nextafter(np.float32(2.0 ** -100), np.float32(0))
+    x[6] = 2.0 ** -140
+    x[7] = 3.3e38
+    x[8, ::2] = -3.4e38
+    x[9] = -0.0
+    x[10, :] = np.float32(2.0 ** -126)
+    x[11, :16] = 1e-30
+    x[12] = np.linspace(-6, 6, K)
+    x[13] = np.repeat([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0], 12) * np.float32(1.5)
+    m = D.Fp4Matrix.empty(fmt, *x.shape)
+    D.dit_fp4_quantize(dev(x), m)
+    codes, scale, row = _check_quantised(m, x, fmt)
+    out = torch.empty(x.shape, device="cuda")
+    D.dit_fp4_dequantize(m, out)
+    assert np.array_equal(out.cpu().numpy(), O.fp4_values(codes, scale, row, fmt, K), equal_nan=True)
+
+
+def _product_gate(a, b, K):
+    S = np.abs(a) @ np.abs(b).T
+    return (K / 64 + 2) * 2.0 ** -23 * S
+
+
+def _quantised(x, fmt):
+    codes, scale, row = O.fp4_quantize(x, fmt)
+    packed, tiles = O.fp4_pack(codes, scale, fmt)
+    m = D.Fp4Matrix(fmt, *x.shape, dev(packed), dev(tiles), None if row is None else dev(row))
+    return m, O.fp4_values(codes, scale, row, fmt, x.shape[1]).astype(np.float64)
+
+
+def _check_product(out, a, b, K, what=""):
+    ref = a @ b.T
+    got = out.float().cpu().numpy().astype(np.float64)
+    gate = _product_gate(a, b, K) + (2.0 ** -8 * np.abs(ref) if out.dtype == torch.bfloat16 else 0) + 1e-37
+    bad = np.abs(got - ref) > gate
+    assert not bad.any(), (what, int(bad.sum()), np.argwhere(bad)[:4], float((np.abs(got - ref) / gate).max()))
+
+
+SIZES = [(1, 16, 16), (1, 1, 1), (1, 1000, 256), (2, 130, 100), (8, 128, 4096), (16, 77, 333), (17, 256, 1000),
+         (64, 1000, 512), (65, 384, 64), (127, 129, 31), (128, 128, 128), (129, 257, 257), (200, 1024, 1056),
+         (256, 256, 4096), (333, 777, 1000), (513, 640, 2048), (1088, 512, 3104), (40, 4096, 8000), (1, 9000, 2000)]
+
+
+@FMT
+@pytest.mark.parametrize("M,N,K", SIZES)
+def test_matmul(fmt, M, N, K):
+    g = np.random.default_rng(M + 31 * N + 1009 * K)
+    a, av = _quantised(_rows(g, M, K), fmt)
+    b, bv = _quantised(_rows(g, N, K) * np.float32(0.02), fmt)
+    for dt, pad, shift in ((torch.float32, 0, 0), (torch.bfloat16, 0, 0), (torch.bfloat16, 3, 1)):
+        out = _on_gpu(np.full((M, N), 9.0, np.float32), dt, pad, shift)
+        D.dit_fp4_matmul(a, b, out)
+        D.dit_check()
+        _check_product(out, av, bv, K, (dt, pad))
+        if pad:
+            assert (torch.as_strided(out, (M, N + pad), (N + pad, 1))[:-1, N:] == 77).all()
+
+
+@FMT
+@pytest.mark.parametrize("M,N,K,dtype", [(1, 300, 1000, torch.bfloat16), (70, 130, 96, torch.float32),
+                                         (300, 512, 768, torch.bfloat16)])
+def test_linear_equals_quantise_and_product(fmt, M, N, K, dtype):
+    g = np.random.default_rng(M * N)
+    x = _rows(g, M, K, dtype == torch.bfloat16)
+    w, wv = _quantised(_rows(g, N, K) * np.float32(0.02), fmt)
+    xd = _on_gpu(x, dtype, 5, 0)
+    out, two = torch.empty(M, N, device="cuda"), torch.empty(M, N, device="cuda")
+    D.dit_linear_fp4(xd, w, out, workspace(D.dit_linear_fp4_workspace_bytes(fmt, M, N, K)))
+    a = D.Fp4Matrix.empty(fmt, M, K)
+    D.dit_fp4_quantize(xd, a)
+    D.dit_fp4_matmul(a, w, two)
+    D.dit_check()
+    assert torch.equal(out, two)
+    codes, scale, row = O.fp4_quantize(x, fmt)
+    _check_product(out, O.fp4_values(codes, scale, row, fmt, K).astype(np.float64), wv, K)
+    assert np.array_equal(xd.float().cpu().numpy(), x)
+
+
+@FMT
+def test_non_finite_rows_stay_in_their_row(fmt):
+    g = np.random.default_rng(5)
+    M, N, K = 140, 150, 320
+    x, w = _rows(g, M, K, False), _rows(g, N, K, False)
+    x[3, 17], x[130, 300], x[60] = np.inf, np.nan, 0
+    w[149, 5] = np.nan
+    w[10] = 0
+    a, b = D.Fp4Matrix.empty(fmt, M, K), D.Fp4Matrix.empty(fmt, N, K)
+    D.dit_fp4_quantize(dev(x), a)
+    D.dit_fp4_quantize(dev(w), b)
+    out = torch.empty(M, N, device="cuda")
+    D.dit_fp4_matmul(a, b, out)
+    D.dit_check()
+    o = out.cpu().numpy()
+    nan = np.zeros((M, N), bool)
+    nan[[3, 130]] = True
+    nan[:, 149] = True
+    assert np.array_equal(np.isnan(o), nan)
+    assert (o[60, :149] == 0).all() and (o[np.delete(np.arange(M), [3, 130]), 10] == 0).all()
+
+
+def test_empty_and_streams_and_graph():
+    g = np.random.default_rng(6)
+    w, wv = _quantised(_rows(g, 96, 256), NV)
+    ws = workspace(D.dit_linear_fp4_workspace_bytes(NV, 50, 96, 256))
+    D.dit_linear_fp4(torch.empty(0, 256, device="cuda"), w, torch.empty(0, 96, device="cuda"), ws)
+    xs = [_rows(g, 50, 256) for _ in range(2)]
+    x, out = dev(xs[0]), torch.empty(50, 96, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        D.dit_linear_fp4(x, w, out, ws)
+    side.synchronize()
+    first = out.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        D.dit_linear_fp4(x, w, out, ws)
+    out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, first)
+    x.copy_(dev(xs[1]))
+    graph.replay()
+    torch.cuda.synchronize()
+    codes, scale, row = O.fp4_quantize(xs[1], NV)
+    _check_product(out, O.fp4_values(codes, scale, row, NV, 256).astype(np.float64), wv, 256)
+
+
+def test_binding_refusals():
+    w = D.Fp4Matrix.empty(NV, 8, 64)
+    x, out, ws = torch.zeros(4, 64, device="cuda"), torch.zeros(4, 8, device="cuda"), workspace(1 << 16)
+    for bad in (x.half(), x.cpu(), x.t().contiguous().t(), x[:, :63], x[0]):
+        with pytest.raises((TypeError, ValueError)):
+            D.dit_linear_fp4(bad if bad.dim() == 2 else bad, w, out, ws)
+    with pytest.raises(ValueError):
+        D.dit_linear_fp4(x, w, out[:, :7], ws)
+    with pytest.raises(D.DitError):
+        D.dit_linear_fp4(x, w, out, ws[:64])
+    with pytest.raises(ValueError):
+        D.Fp4Matrix(NV, 9, 64, w.codes, w.scales, w.row_scale)
+    with pytest.raises(D.DitError):
+        D.dit_fp4_matmul(D.Fp4Matrix.empty(MX, 8, 64), w, torch.zeros(8, 8, device="cuda"))
