@@ -1362,7 +1362,9 @@ int dit_fp4_matmul(const dit_fp4_matrix* a, const dit_fp4_matrix* b, void* out, 
   if (a->format != b->format || a->cols != b->cols) return DIT_EINVAL;
   if (a->rows == 0 || b->rows == 0) return DIT_OK;
   if (!fp4_rows_ok(out, out_type, ldo, a->rows, b->rows)) return DIT_EINVAL;
-  return fp4_matmul_launch(*a, *b, out, out_type, ldo, reinterpret_cast<cudaStream_t>(stream));
+  int* err = err_word();
+  if (!err) return DIT_ECUDA;
+  return fp4_matmul_launch(*a, *b, out, out_type, ldo, err, reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t dit_linear_fp4_workspace_bytes(int format, int M, int N, int K) {
@@ -1382,9 +1384,11 @@ int dit_linear_fp4(const void* x, int x_type, int M, long long ldx, const dit_fp
   if (ws_bytes < dit_linear_fp4_workspace_bytes(w->format, M, w->rows, w->cols)) return DIT_EWORKSPACE;
   dit_fp4_matrix a;
   carve_fp4(w->format, M, w->cols, ws, &a);
+  int* err = err_word();
+  if (!err) return DIT_ECUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   rc = fp4_quantize_launch(x, x_type, ldx, a, st);
-  return rc == DIT_OK ? fp4_matmul_launch(a, *w, out, out_type, ldo, st) : rc;
+  return rc == DIT_OK ? fp4_matmul_launch(a, *w, out, out_type, ldo, err, st) : rc;
 }
 
 int dit_block_forward_int8(const dit_dims* d, const dit_block_w8* w, float* txt, int L, float* img, int N,

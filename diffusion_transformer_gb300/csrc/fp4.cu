@@ -1,5 +1,5 @@
-// Microscaled 4-bit floating point (e2m1 codes with a scale per block): quantisation, its inverse and
-// the product of two quantised matrices.
+// Microscaled 4-bit floating point (e2m1 codes with a scale per block): quantisation and its inverse
+// (the product is in fp4_gemm.cu).
 //
 // A code stands for 0, 0.5, 1, 1.5, 2, 3, 4 or 6 with a sign. Two formats:
 //   DIT_FP4_NV  blocks of 16 values, e4m3 block scale s, fp32 scale g per row: value = code * s * g
@@ -159,48 +159,6 @@ __global__ void __launch_bounds__(256) fp4_dequantize_kernel(int fmt, const uint
   }
 }
 
-// ---------------------------------------------------------------------------------------------
-// product, plain form: 64 x 64 tiles of the values in shared memory, fp32 FMA
-// ---------------------------------------------------------------------------------------------
-template <typename T>
-__global__ void __launch_bounds__(256) fp4_matmul_plain_kernel(int fmt, const Fp4View a, const Fp4View b, int K, T* out,
-                                                               long long ldo) {
-  pdl_wait();
-  pdl_trigger();
-  __shared__ float sA[kUnit][65], sB[kUnit][65];
-  const int m0 = blockIdx.y * 64, n0 = blockIdx.x * 64;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float acc[4][4] = {};
-  for (int u = 0; u * kUnit < K; ++u) {
-    if (threadIdx.x < 128) {
-      const Fp4View& p = threadIdx.x < 64 ? a : b;
-      const int rr = threadIdx.x & 63, r = (threadIdx.x < 64 ? m0 : n0) + rr;
-      float v[kUnit] = {};
-      if (r < p.rows) {
-        fp4_values16(*reinterpret_cast<const uint2*>(p.codes + (long long)r * fp4_code_row_bytes(K) + 8 * u), v);
-        const int by = p.scales[fp4_scale_row(fmt, r, K) + fp4_scale_block(fmt == DIT_FP4_NV ? u : u >> 1)];
-        const float s = fmt == DIT_FP4_NV ? fp4_e4m3(by) : fp4_e8m0(by);
-        for (int j = 0; j < kUnit; ++j) v[j] *= s;
-      }
-      float(*d)[65] = threadIdx.x < 64 ? sA : sB;
-      for (int j = 0; j < kUnit; ++j) d[j][rr] = v[j];
-    }
-    __syncthreads();
-    for (int j = 0; j < kUnit; ++j)
-      for (int y = 0; y < 4; ++y)
-        for (int z = 0; z < 4; ++z) acc[y][z] = fmaf(sA[j][ty * 4 + y], sB[j][tx * 4 + z], acc[y][z]);
-    __syncthreads();
-  }
-  for (int y = 0; y < 4; ++y)
-    for (int z = 0; z < 4; ++z) {
-      const int m = m0 + ty * 4 + y, n = n0 + tx * 4 + z;
-      if (m >= a.rows || n >= b.rows) continue;
-      float v = acc[y][z];
-      if (fmt == DIT_FP4_NV) v = v * a.row_scale[m] * b.row_scale[n];
-      out[m * ldo + n] = T(v);
-    }
-}
-
 template <typename T, int FMT>
 cudaError_t quantize_go(const T* x, long long ldx, const dit_fp4_matrix& m, cudaStream_t st) {
   const int units = fp4_groups(FMT, m.cols) * (FMT == DIT_FP4_NV ? 4 : 8);
@@ -241,17 +199,6 @@ int fp4_dequantize_launch(const dit_fp4_matrix& m, void* out, int type, long lon
                        m.scales, m.row_scale, n, row_units, m.cols, static_cast<__nv_bfloat16*>(out), ldo, vec)
           : launch_pdl(fp4_dequantize_kernel<float>, dim3(unsigned(ctas)), dim3(256), 0, st, 1, m.format, m.codes,
                        m.scales, m.row_scale, n, row_units, m.cols, static_cast<float*>(out), ldo, vec);
-  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? DIT_OK : DIT_ECUDA;
-}
-
-int fp4_matmul_launch(const dit_fp4_matrix& a, const dit_fp4_matrix& b, void* out, int type, long long ldo,
-                      cudaStream_t st) {
-  const Fp4View va{a.codes, a.scales, a.row_scale, a.rows}, vb{b.codes, b.scales, b.row_scale, b.rows};
-  const dim3 grid((b.rows + 63) / 64, (a.rows + 63) / 64);
-  const cudaError_t e = type == DIT_BF16 ? launch_pdl(fp4_matmul_plain_kernel<__nv_bfloat16>, grid, dim3(256), 0, st, 1,
-                                                      a.format, va, vb, a.cols, static_cast<__nv_bfloat16*>(out), ldo)
-                                         : launch_pdl(fp4_matmul_plain_kernel<float>, grid, dim3(256), 0, st, 1, a.format,
-                                                      va, vb, a.cols, static_cast<float*>(out), ldo);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? DIT_OK : DIT_ECUDA;
 }
 

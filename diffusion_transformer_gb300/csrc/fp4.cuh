@@ -120,11 +120,4 @@ __device__ __forceinline__ void ld_global_256(uint32_t (&w)[8], const void* p) {
                : "l"(p));
 }
 
-struct Fp4View {
-  const uint8_t* codes;
-  const uint8_t* scales;
-  const float* row_scale;
-  int rows;
-};
-
 }  // namespace dit

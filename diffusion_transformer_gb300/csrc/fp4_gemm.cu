@@ -1,0 +1,550 @@
+// Product of two microscaled 4-bit matrices on the block-scaled tcgen05 MMA: out = A B^T, A [M, K], B
+// [N, K] in the layout of fp4.cuh, fp32 accumulators in tensor memory, the NV format's row scales applied
+// to the accumulator as it is drained.
+//
+// A 128-byte swizzled shared-memory row holds 256 codes, so a pipeline stage is K = 256: four MMAs of
+// K = 64, preceded by the copies of the stage's scale chunks from shared to tensor memory.
+//
+// Two kernels:
+//   pair   256 x 256 tiles on CTA pairs (cta_group::2), persistent, for products with enough tiles
+//   split  128 rows of B against up to 128 rows of A per CTA, a cluster of CTAs sharing the K loop and
+//          adding their partial tiles through distributed shared memory, for few rows or few tiles
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "fp4.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+#include "tmap.h"
+
+namespace dit {
+namespace {
+
+constexpr int kStageK = 256;                  // codes per stage and row: 128 bytes
+constexpr uint32_t kTileBytes = 128 * 128;    // 128 rows of a stage
+template <int FMT>
+struct Scales {
+  static constexpr bool kNv = FMT == DIT_FP4_NV;
+  static constexpr int kGroups = kNv ? 4 : 2;             // 512-byte scale chunks per stage and 128 rows
+  static constexpr uint32_t kBytes = kGroups * 512;
+};
+
+struct Fp4Params {
+  int M, N, K;
+  int* err;
+  void* out;
+  long long ldo;
+  const float* a_scale;  // NV: row scales
+  const float* b_scale;
+  int tma_out;           // rows of `out` start on 16 bytes: tiles leave through TMA stores
+  int n_fast;
+  int bn, stages;        // split kernel: rows of A per tile, pipeline depth
+};
+
+__device__ __forceinline__ int stage_steps(int K, int kb) { return min(4, (K - kb * kStageK + 63) / 64); }
+
+// ---------------------------------------------------------------------------------------------
+// pair kernel
+// ---------------------------------------------------------------------------------------------
+// Tensor memory, 512 columns: two 256-column accumulators that overlap by 48 columns ([0, 256) and
+// [208, 464)) and 48 columns of scales. An accumulator's overlapped columns are drained first and then
+// handed over, so the next tile's MMAs wait for a quarter of an epilogue, not for all of it.
+constexpr int kAcc1 = 208, kSfCol = 464, kPairStages = 5;
+constexpr int kPairThreads = 192;
+
+template <int FMT>
+struct PairCfg {
+  using S = Scales<FMT>;
+  static constexpr uint32_t kStage = 2 * kTileBytes + 3 * S::kBytes;  // A, B, scales of 128 A and 256 B rows
+  static constexpr uint32_t kStaging = 4 * 2 * 4096;                  // two 4 KB output tiles per epilogue warp
+  static constexpr uint32_t kSmem = 1024 + kPairStages * kStage + kStaging + 4 * 256 + 256;
+};
+
+template <typename T>
+__device__ __forceinline__ void put_chunk(uint8_t* tile, int lane, int q, const float* v) {
+  uint4 u;
+  if constexpr (sizeof(T) == 2)
+    u = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+  else
+    u = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+  *reinterpret_cast<uint4*>(tile + sw128_offset(lane, q)) = u;
+}
+
+template <int FMT, typename T>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                    const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
+                    const __grid_constant__ CUtensorMap tmO, const Fp4Params p) {
+  using Cfg = PairCfg<FMT>;
+  using SC = Scales<FMT>;
+  constexpr int S = kPairStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sA = smem;
+  uint8_t* sB = sA + S * kTileBytes;
+  uint8_t* sSA = sB + S * kTileBytes;
+  uint8_t* sSB = sSA + S * SC::kBytes;
+  uint8_t* sE = sSB + S * 2 * SC::kBytes;
+  float* sC = reinterpret_cast<float*>(sE + Cfg::kStaging);  // 64 column factors per epilogue warp
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sC + 4 * 64);
+  uint64_t *full = bars, *empty = bars + S, *tfull = bars + 2 * S, *tempty = tfull + 2, *drain = tempty + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+
+  const int warp = threadIdx.x >> 5, lane = lane_id();
+  const uint32_t rank = cluster_ctarank();
+  const int unit = int(blockIdx.x >> 1), units = int(gridDim.x >> 1);
+  const int num_m = (p.M + 255) / 256, num_n = (p.N + 255) / 256, tiles = num_m * num_n;
+  const int KB = (p.K + kStageK - 1) / kStageK;
+  auto tile_mn = [&](int tile, int& mb, int& nb) {
+    mb = p.n_fast ? tile / num_n : tile % num_m;
+    nb = p.n_fast ? tile % num_n : tile / num_m;
+  };
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    for (int a = 0; a < 2; ++a) mbar_init(smem_u32(&tfull[a]), 1);
+    mbar_init(smem_u32(tempty), 2 * 128);  // both CTAs' epilogue threads
+    mbar_init(smem_u32(drain), 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&tmSA);
+    tma_prefetch_desc(&tmSB);
+  }
+  __syncthreads();
+  cluster_barrier();  // barriers of both CTAs are up
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_slot), 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  pdl_trigger();
+
+  if (warp == 0) {
+    if (elect_one()) {
+      int stage = 0;
+      uint32_t phase = 0, issued = 0, parity = 0;
+      bool ok = true;
+      const uint32_t full0 = mapa_shared(smem_u32(&full[0]), 0);  // both CTAs' copies count on the first's barriers
+      for (int tile = unit; tile < tiles && ok; tile += units) {
+        int mb, nb;
+        tile_mn(tile, mb, nb);
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1, p.err, kErrTimeoutProducer)) { ok = false; break; }
+          if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full[stage]), 2 * Cfg::kStage);
+          const uint32_t fb = full0 + uint32_t(stage) * 8u;
+          tma_load_2d_pair(smem_u32(sA + stage * kTileBytes), &tmA, fb, kb * 128, mb * 256 + int(rank) * 128);
+          tma_load_2d_pair(smem_u32(sB + stage * kTileBytes), &tmB, fb, kb * 128, nb * 256 + int(rank) * 128);
+          tma_load_3d_pair(smem_u32(sSA + stage * SC::kBytes), &tmSA, fb, 0, kb * SC::kGroups, mb * 2 + int(rank));
+          tma_load_3d_pair(smem_u32(sSB + stage * 2 * SC::kBytes), &tmSB, fb, 0, kb * SC::kGroups, nb * 2);
+          issued |= 1u << stage;
+          parity = (parity & ~(1u << stage)) | (phase << stage);
+          if (++stage == S) { stage = 0; phase ^= 1; }
+        }
+      }
+      if (rank == 0)  // every copy has landed before the CTAs leave
+        for (int s = 0; s < S; ++s)
+          if (issued & (1u << s)) mbar_wait(smem_u32(&full[s]), (parity >> s) & 1u, p.err, kErrTimeoutDrain);
+    }
+  } else if (warp == 1) {
+    if (rank == 0 && elect_one()) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      int it = 0;
+      for (int tile = unit; tile < tiles && ok; tile += units, ++it) {
+        // the previous tile's overlapped columns are drained (and, before them, the tile before it)
+        if (it > 0 && !mbar_wait_cluster(smem_u32(tempty), uint32_t(it - 1) & 1u, p.err, kErrTimeoutMma)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + ((it & 1) ? kAcc1 : 0);
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!mbar_wait(smem_u32(&full[stage]), phase, p.err, kErrTimeoutMma)) { ok = false; break; }
+          tc_fence_after();
+          const int steps = stage_steps(p.K, kb);
+          const uint32_t sfa = tmem + kSfCol, sfb = sfa + SC::kGroups * 4;
+          const uint64_t da = scale_chunk_desc(smem_u32(sSA + stage * SC::kBytes));
+          const uint64_t db = scale_chunk_desc(smem_u32(sSB + stage * 2 * SC::kBytes));
+          const uint64_t ad = sw128_desc(smem_u32(sA + stage * kTileBytes));
+          const uint64_t bd = sw128_desc(smem_u32(sB + stage * kTileBytes));
+#pragma unroll
+          for (int g = 0; g < SC::kGroups; ++g) {
+            tmem_cp_scales<true>(sfa + 4 * g, da + uint64_t(32 * g));
+            tmem_cp_scales<true>(sfb + 8 * g, db + uint64_t(32 * g));
+            tmem_cp_scales<true>(sfb + 8 * g + 4, db + uint64_t(32 * (SC::kGroups + g)));
+          }
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            if (kk < steps) {
+              const int g = SC::kNv ? kk : kk >> 1;
+              umma_fp4<SC::kNv, true>(d, ad + uint64_t(2 * kk), bd + uint64_t(2 * kk),
+                                      idesc_fp4(SC::kNv, 256, 256, SC::kNv ? 0 : (kk & 1) * 2), sfa + 4 * g,
+                                      sfb + 8 * g, kb != 0 || kk != 0);
+            }
+          }
+          umma_commit_pair_both(smem_u32(&empty[stage]));
+          if (++stage == S) { stage = 0; phase ^= 1; }
+        }
+        if (!ok) break;
+        umma_commit_pair_both(smem_u32(&tfull[it & 1]));
+      }
+      umma_commit_pair(smem_u32(drain));
+      mbar_wait(smem_u32(drain), 0, p.err, kErrTimeoutDrain);
+    }
+  } else {
+    const int quad = warp & 3;
+    uint8_t* stage0 = sE + (warp - 2) * 8192;
+    float* cf = sC + (warp - 2) * 64;
+    const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0);
+    int it = 0, buf = 0;
+    for (int tile = unit; tile < tiles; tile += units, ++it) {
+      int mb, nb;
+      tile_mn(tile, mb, nb);
+      const int acc = it & 1;
+      const int row0 = mb * 256 + int(rank) * 128 + quad * 32, row = row0 + lane;
+      const float ra = SC::kNv ? (row < p.M ? __ldg(p.a_scale + row) : 0.f) : 1.f;
+      if (!mbar_wait_warp(smem_u32(&tfull[acc]), uint32_t(it >> 1) & 1u, p.err, kErrTimeoutEpilogue)) break;
+      tc_fence_after();
+      const uint32_t taddr = tmem + (uint32_t(quad * 32) << 16) + (acc ? kAcc1 : 0);
+      // 64 columns at a time, the overlapped ones first
+#pragma unroll 1
+      for (int j = 0; j < 4; ++j) {
+        const int g = acc ? j : 3 - j, n = nb * 256 + g * 64;
+        uint32_t w[2][32];
+        tmem_ld32(taddr + g * 64, w[0]);
+        tmem_ld32(taddr + g * 64 + 32, w[1]);
+        if constexpr (SC::kNv) {
+          __syncwarp();
+          cf[lane] = n + lane < p.N ? __ldg(p.b_scale + n + lane) : 0.f;
+          cf[lane + 32] = n + lane + 32 < p.N ? __ldg(p.b_scale + n + lane + 32) : 0.f;
+          __syncwarp();
+        }
+        tmem_ld_wait();
+        if (j == 0) {
+          tc_fence_before();
+          mbar_arrive_cluster(tempty0);
+        }
+        if (n >= p.N || row0 >= p.M) continue;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float v[32];
+#pragma unroll
+          for (int c = 0; c < 32; c += 4) {
+            const float4 f = SC::kNv ? *reinterpret_cast<const float4*>(cf + 32 * h + c) : make_float4(1.f, 1.f, 1.f, 1.f);
+            const float* ff = &f.x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float x = __uint_as_float(w[h][c + e]);
+              v[c + e] = SC::kNv ? x * ra * ff[e] : x;
+            }
+          }
+          // a 4 KB staging tile: 32 rows of 64 bf16 (both halves) or 32 fp32 (one half)
+          constexpr int kHalves = sizeof(T) == 2 ? 2 : 1;
+          uint8_t* st = stage0 + buf * 4096;
+          if (kHalves == 1 || h == 0) {
+            if (p.tma_out && lane == 0) bulk_wait_read_but_one();
+            __syncwarp();
+          }
+          constexpr int kPer = 16 / sizeof(T);
+#pragma unroll
+          for (int q = 0; q < 32 / kPer; ++q) put_chunk<T>(st, lane, (kHalves == 2 ? h * 4 : 0) + q, v + q * kPer);
+          if (kHalves == 2 && h == 0) continue;
+          const int nn = n + (kHalves == 2 ? 0 : 32 * h);
+          if (p.tma_out) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (nn < p.N) tma_store_2d(&tmO, smem_u32(st), nn, row0);
+              bulk_commit();
+            }
+            buf ^= 1;
+          } else {
+            __syncwarp();
+            T* o = static_cast<T*>(p.out) + (long long)row0 * p.ldo + nn;
+            const int rows = min(32, p.M - row0);
+            for (int r = 0; r < rows; ++r)
+#pragma unroll
+              for (int c = lane; c < int(128 / sizeof(T)); c += 32)
+                if (nn + c < p.N)
+                  o[r * p.ldo + c] = *reinterpret_cast<const T*>(st + sw128_offset(r, c * sizeof(T) / 16) + c * sizeof(T) % 16);
+          }
+        }
+      }
+    }
+    if (p.tma_out && lane == 0) bulk_wait_all();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_barrier();  // no CTA frees or leaves what the other may still use
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, 512);
+}
+
+// ---------------------------------------------------------------------------------------------
+// split kernel: D [128 rows of B, bn rows of A], so that few rows of A still fill the MMA's 128 lanes
+// ---------------------------------------------------------------------------------------------
+constexpr int kSplitThreads = 192;
+constexpr uint32_t kSplitMinSmem = 116 * 1024;
+constexpr uint32_t split_stage_bytes(int bn, uint32_t sf) { return kTileBytes + uint32_t(bn) * 128 + 2 * sf; }
+
+template <int FMT, typename T>
+__global__ void __launch_bounds__(kSplitThreads, 1)
+    fp4_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                     const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
+                     const Fp4Params p) {
+  using SC = Scales<FMT>;
+  const int S = p.stages, bn = p.bn;
+  const uint32_t aBytes = uint32_t(bn) * 128;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sB = smem;                      // 128 rows of B per stage (the MMA's A side)
+  uint8_t* sA = sB + S * kTileBytes;       // bn rows of A (multiples of 16: 1024-byte swizzle atoms stay whole)
+  uint8_t* sSB = sA + S * aBytes;
+  uint8_t* sSA = sSB + S * SC::kBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sSA + S * SC::kBytes);
+  uint64_t *full = bars, *empty = bars + S, *tfull = bars + 2 * S;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tfull + 1);
+
+  const int warp = threadIdx.x >> 5, lane = lane_id();
+  const int parts = int(cluster_nctarank()), part = int(cluster_ctarank());
+  const int n0 = int(blockIdx.x / parts) * 128, m0 = int(blockIdx.y) * bn;
+  const int KB = (p.K + kStageK - 1) / kStageK;
+  const int k0 = int((long long)KB * part / parts), k1 = int((long long)KB * (part + 1) / parts);
+  const uint32_t cols = bn <= 32 ? 64 : (bn <= 64 ? 128 : 256);  // bn accumulator columns, then the scales
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    mbar_init(smem_u32(tfull), 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&tmSA);
+    tma_prefetch_desc(&tmSB);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  pdl_trigger();
+
+  if (warp == 0) {
+    if (elect_one()) {
+      int stage = 0;
+      uint32_t phase = 0, issued = 0, parity = 0;
+      for (int kb = k0; kb < k1; ++kb) {
+        if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1, p.err, kErrTimeoutProducer)) break;
+        const uint32_t fb = smem_u32(&full[stage]);
+        mbar_arrive_expect_tx(fb, kTileBytes + aBytes + 2 * SC::kBytes);
+        tma_load_2d(smem_u32(sB + stage * kTileBytes), &tmB, fb, kb * 128, n0);
+        tma_load_3d(smem_u32(sSB + stage * SC::kBytes), &tmSB, fb, 0, kb * SC::kGroups, n0 >> 7);
+        tma_load_2d(smem_u32(sA + stage * aBytes), &tmA, fb, kb * 128, m0);
+        tma_load_3d(smem_u32(sSA + stage * SC::kBytes), &tmSA, fb, 0, kb * SC::kGroups, m0 >> 7);
+        issued |= 1u << stage;
+        parity = (parity & ~(1u << stage)) | (phase << stage);
+        if (++stage == S) { stage = 0; phase ^= 1; }
+      }
+      for (int s = 0; s < S; ++s)  // every copy has landed before the CTA leaves
+        if (issued & (1u << s)) mbar_wait(smem_u32(&full[s]), (parity >> s) & 1u, p.err, kErrTimeoutDrain);
+    }
+  } else if (warp == 1) {
+    if (elect_one()) {
+      int stage = 0;
+      uint32_t phase = 0;
+      const uint32_t sfb = tmem + bn, sfa = sfb + SC::kGroups * 4;  // B's scales (MMA A side), A's scales
+      for (int kb = k0; kb < k1; ++kb) {
+        if (!mbar_wait(smem_u32(&full[stage]), phase, p.err, kErrTimeoutMma)) break;
+        tc_fence_after();
+        const int steps = stage_steps(p.K, kb);
+        const uint64_t db = scale_chunk_desc(smem_u32(sSB + stage * SC::kBytes));
+        const uint64_t da = scale_chunk_desc(smem_u32(sSA + stage * SC::kBytes));
+        const uint64_t bd = sw128_desc(smem_u32(sB + stage * kTileBytes));
+        const uint64_t ad = sw128_desc(smem_u32(sA + stage * aBytes));
+#pragma unroll
+        for (int g = 0; g < SC::kGroups; ++g) {
+          tmem_cp_scales<false>(sfb + 4 * g, db + uint64_t(32 * g));
+          tmem_cp_scales<false>(sfa + 4 * g, da + uint64_t(32 * g));
+        }
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          if (kk < steps) {
+            const int g = SC::kNv ? kk : kk >> 1;
+            umma_fp4<SC::kNv, false>(tmem, bd + uint64_t(2 * kk), ad + uint64_t(2 * kk),
+                                     idesc_fp4(SC::kNv, 128, bn, SC::kNv ? 0 : (kk & 1) * 2), sfb + 4 * g,
+                                     sfa + 4 * g, kb != k0 || kk != 0);
+          }
+        }
+        umma_commit(smem_u32(&empty[stage]));
+        if (++stage == S) { stage = 0; phase ^= 1; }
+      }
+      umma_commit(smem_u32(tfull));
+      mbar_wait(smem_u32(tfull), 0, p.err, kErrTimeoutDrain);
+    }
+  } else {
+    (void)mbar_wait_warp(smem_u32(tfull), 0, p.err, kErrTimeoutEpilogue);
+    tc_fence_after();
+  }
+  // Epilogue. A lone CTA stores its tile; the CTAs of a cluster put their partial tiles into shared
+  // memory ([column of A][128 rows of B] fp32, the pipeline's memory), and each adds up its share of the
+  // columns, part by part in order.
+  const int quad = warp & 3;
+  const uint32_t taddr = tmem + (uint32_t(quad * 32) << 16);
+  const int n = n0 + quad * 32 + lane;
+  T* out = static_cast<T*>(p.out);
+  float* tile = reinterpret_cast<float*>(smem);
+  __syncthreads();
+  tc_fence_after();
+  if (warp >= 2) {
+    const float rb = SC::kNv ? (n < p.N ? __ldg(p.b_scale + n) : 0.f) : 1.f;
+    for (int c = 0; c < bn; c += 8) {
+      if (m0 + c >= p.M) break;
+      uint32_t w[8];
+      tmem_ld8(taddr + c, w);
+      tmem_ld_wait();
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int m = m0 + c + e;
+        float v = __uint_as_float(w[e]);
+        if (parts > 1) {
+          tile[(c + e) * 128 + quad * 32 + lane] = v;
+        } else if (m < p.M && n < p.N) {
+          if (SC::kNv) v = v * __ldg(p.a_scale + m) * rb;
+          out[m * p.ldo + n] = T(v);
+        }
+      }
+    }
+  }
+  if (parts > 1) {
+    cluster_barrier();
+    const int live = min(bn, p.M - m0);
+    const uint32_t base = smem_u32(tile);
+    // four rows of B per thread, 32 threads to a column
+    for (int i = part * kSplitThreads + int(threadIdx.x); i < live * 32; i += parts * kSplitThreads) {
+      const int c = i >> 5, r4 = (i & 31) * 4;
+      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int q = 0; q < parts; ++q) {
+        const float4 v = ld_shared_cluster_v4(mapa_shared(base + uint32_t(c * 128 + r4) * 4, uint32_t(q)));
+        s.x += v.x;
+        s.y += v.y;
+        s.z += v.z;
+        s.w += v.w;
+      }
+      const float* sv = &s.x;
+      const int m = m0 + c;
+      const float ra = SC::kNv ? __ldg(p.a_scale + m) : 1.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int nn = n0 + r4 + e;
+        if (nn < p.N) out[m * p.ldo + nn] = T(SC::kNv ? sv[e] * ra * __ldg(p.b_scale + nn) : sv[e]);
+      }
+    }
+    cluster_barrier();  // no CTA leaves while another reads its shared memory
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) tmem_dealloc(tmem, cols);
+}
+
+// ---------------------------------------------------------------------------------------------
+// launch
+// ---------------------------------------------------------------------------------------------
+bool tmap_codes(CUtensorMap* m, const uint8_t* codes, int rows, int K, int box_rows) {
+  return make_tmap_2d(m, codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, fp4_code_row_bytes(K), rows, fp4_code_row_bytes(K), 128,
+                      box_rows, true);
+}
+bool tmap_sf(CUtensorMap* m, const dit_fp4_matrix& x, int box_groups, int box_bands) {
+  return make_tmap_scales(m, x.scales, fp4_groups(x.format, x.cols), (x.rows + 127) / 128, box_groups, box_bands);
+}
+
+template <int FMT, typename T>
+int launch_pair(const dit_fp4_matrix& a, const dit_fp4_matrix& b, Fp4Params p, cudaStream_t st) {
+  using Cfg = PairCfg<FMT>;
+  static_assert(Cfg::kSmem <= 227 * 1024, "shared memory budget");
+  CUtensorMap ma, mb, msa, msb, mo;
+  constexpr int G = Scales<FMT>::kGroups;
+  if (!tmap_codes(&ma, a.codes, a.rows, p.K, 128) || !tmap_codes(&mb, b.codes, b.rows, p.K, 128) ||
+      !tmap_sf(&msa, a, G, 1) || !tmap_sf(&msb, b, G, 2))
+    return DIT_ECUDA;
+  p.tma_out = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && p.ldo * (long long)sizeof(T) % 16 == 0;
+  mo = ma;
+  if (p.tma_out && !make_tmap_2d(&mo, p.out, sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                                 sizeof(T), p.N, p.M, p.ldo * (long long)sizeof(T), 128 / sizeof(T), 32, true))
+    return DIT_ECUDA;
+  p.n_fast = p.M > p.N;  // consecutive tiles share the smaller operand's rows, which stay in L2
+  auto kern = fp4_pair_kernel<FMT, T>;
+  if (!smem_attr_once(reinterpret_cast<const void*>(kern), Cfg::kSmem)) return DIT_ECUDA;
+  const int tiles = ((p.M + 255) / 256) * ((p.N + 255) / 256);
+  const int units = std::min(tiles, num_sms() / 2);
+  const cudaError_t e = launch_pdl(kern, dim3(unsigned(2 * units)), dim3(kPairThreads), Cfg::kSmem, st, 2, ma, mb, msa,
+                                   msb, mo, p);
+  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? DIT_OK : DIT_ECUDA;
+}
+
+template <int FMT, typename T>
+int launch_split(const dit_fp4_matrix& a, const dit_fp4_matrix& b, Fp4Params p, cudaStream_t st) {
+  constexpr int G = Scales<FMT>::kGroups;
+  p.bn = p.M <= 16 ? 16 : (p.M <= 32 ? 32 : (p.M <= 64 ? 64 : 128));
+  const int nt = (p.N + 127) / 128, mt = (p.M + p.bn - 1) / p.bn, KB = (p.K + kStageK - 1) / kStageK;
+  int parts = 1;
+  while (parts < 8 && 2 * parts <= KB && (long long)nt * mt * parts * 2 <= num_sms()) parts *= 2;
+  const uint32_t sb = split_stage_bytes(p.bn, Scales<FMT>::kBytes);
+  p.stages = std::min((KB + parts - 1) / parts, int((227 * 1024 - 1024 - 512) / sb));
+  p.stages = std::max(1, std::min(p.stages, 24));
+  uint32_t smem = 1024 + uint32_t(p.stages) * sb + 8 * (2 * uint32_t(p.stages) + 2) + 16;
+  // More than half of an SM's shared memory, as every kernel here that allocates tensor memory: no two of
+  // them share an SM, so no CTA of a cluster waits for tensor memory that another cluster's CTA holds
+  // (also covers the partial tile, at most 64 KB).
+  smem = std::max(smem, kSplitMinSmem);
+  CUtensorMap ma, mb, msa, msb;
+  if (!tmap_codes(&ma, a.codes, a.rows, p.K, p.bn) || !tmap_codes(&mb, b.codes, b.rows, p.K, 128) ||
+      !tmap_sf(&msa, a, G, 1) || !tmap_sf(&msb, b, G, 1))
+    return DIT_ECUDA;
+  if (mt > 65535) return DIT_EUNSUPPORTED;
+  auto kern = fp4_split_kernel<FMT, T>;
+  if (!smem_attr_once(reinterpret_cast<const void*>(kern), 227 * 1024)) return DIT_ECUDA;
+  const cudaError_t e = launch_pdl(kern, dim3(unsigned(nt * parts), unsigned(mt)), dim3(kSplitThreads), smem, st, parts,
+                                   ma, mb, msa, msb, p);
+  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? DIT_OK : DIT_ECUDA;
+}
+
+template <int FMT, typename T>
+int launch_product(const dit_fp4_matrix& a, const dit_fp4_matrix& b, const Fp4Params& p, cudaStream_t st) {
+  const long long tiles = (long long)((p.M + 255) / 256) * ((p.N + 255) / 256);
+  return p.M <= 128 || tiles < 24 ? launch_split<FMT, T>(a, b, p, st) : launch_pair<FMT, T>(a, b, p, st);
+}
+
+}  // namespace
+
+int fp4_matmul_launch(const dit_fp4_matrix& a, const dit_fp4_matrix& b, void* out, int type, long long ldo, int* err,
+                      cudaStream_t st) {
+  Fp4Params p{};
+  p.M = a.rows;
+  p.N = b.rows;
+  p.K = a.cols;
+  p.err = err;
+  p.out = out;
+  p.ldo = ldo;
+  p.a_scale = a.row_scale;
+  p.b_scale = b.row_scale;
+  if (a.format == DIT_FP4_NV)
+    return type == DIT_BF16 ? launch_product<DIT_FP4_NV, __nv_bfloat16>(a, b, p, st)
+                            : launch_product<DIT_FP4_NV, float>(a, b, p, st);
+  return type == DIT_BF16 ? launch_product<DIT_FP4_MX, __nv_bfloat16>(a, b, p, st)
+                          : launch_product<DIT_FP4_MX, float>(a, b, p, st);
+}
+
+}  // namespace dit

@@ -204,7 +204,7 @@ int codes_bf16_launch(const int8_t* q, uint16_t* w, long long n, cudaStream_t st
 // Microscaled 4-bit matrices (see dit_fp4_quantize and the calls after it), on validated arguments
 int fp4_quantize_launch(const void* x, int type, long long ldx, const dit_fp4_matrix& m, cudaStream_t stream);
 int fp4_dequantize_launch(const dit_fp4_matrix& m, void* out, int type, long long ldo, cudaStream_t stream);
-int fp4_matmul_launch(const dit_fp4_matrix& a, const dit_fp4_matrix& b, void* out, int type, long long ldo,
+int fp4_matmul_launch(const dit_fp4_matrix& a, const dit_fp4_matrix& b, void* out, int type, long long ldo, int* err,
                       cudaStream_t stream);
 
 int num_sms();

@@ -140,7 +140,8 @@ def _check_product(out, a, b, K, what=""):
 
 SIZES = [(1, 16, 16), (1, 1, 1), (1, 1000, 256), (2, 130, 100), (8, 128, 4096), (16, 77, 333), (17, 256, 1000),
          (64, 1000, 512), (65, 384, 64), (127, 129, 31), (128, 128, 128), (129, 257, 257), (200, 1024, 1056),
-         (256, 256, 4096), (333, 777, 1000), (513, 640, 2048), (1088, 512, 3104), (40, 4096, 8000), (1, 9000, 2000)]
+         (256, 256, 4096), (333, 777, 1000), (513, 640, 2048), (1088, 512, 3104), (40, 4096, 8000), (1, 9000, 2000),
+         (1100, 1500, 777), (1537, 1025, 2000), (2304, 768, 96), (300, 5200, 520)]
 
 
 @FMT
