@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from ctypes import (POINTER, byref, c_char_p, c_double, c_float, c_int, c_int64, c_longlong, c_size_t, c_uint8, c_uint64,
                     c_void_p)
 from typing import List, Optional, Sequence
@@ -112,8 +113,8 @@ class dit_fp4_matrix(ctypes.Structure):
 _SIGNATURES = {
     "dit_rotary_plan_init": (c_int, [POINTER(dit_rotary_spec), POINTER(dit_rotary_plan)]),
     "dit_rotary_tables": (c_int, [POINTER(dit_rotary_plan), c_void_p, c_int, c_void_p, c_void_p, c_void_p]),
-    "dit_rotary": (c_int, [POINTER(dit_rotary_plan), POINTER(dit_rotary_rows), POINTER(dit_rotary_rows), c_int, c_int,
-                           c_int, c_int, c_void_p, c_int, c_void_p]),
+    "dit_rotary": (c_int, [POINTER(dit_rotary_plan), c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_void_p, c_int,
+                           c_void_p]),
     "dit_fp4_code_bytes": (c_size_t, [c_int, c_int]),
     "dit_fp4_scale_bytes": (c_size_t, [c_int, c_int, c_int]),
     "dit_fp4_quantize": (c_int, [c_void_p, c_int, c_longlong, POINTER(dit_fp4_matrix), c_void_p]),
@@ -600,22 +601,42 @@ def dit_rope_tables(L: int, grid_h: int, grid_w: int, head_dim: int, cos, sin, t
                               _ptr(sin, torch.float32, "sin"), _stream(stream)), "dit_rope_tables")
 
 
-def _typed(t, name):
-    """(device pointer, DIT_BF16 or DIT_F32) of a CUDA tensor on the current device whose last dimension is dense."""
-    import torch
+# The calls below take microseconds on the device, so their marshalling is kept short: torch is looked
+# up once, and the current stream's handle is asked for without building a Stream object.
+_torch_mod = None
+
+
+def _torch():
+    global _torch_mod
+    if _torch_mod is None:
+        import torch
+        _torch_mod = torch
+    return _torch_mod
+
+
+def _current(stream):
+    """(current device, stream handle)"""
+    torch = _torch()
+    dev = torch.cuda.current_device()
+    if stream is None:
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return dev, raw(dev) if raw is not None else torch.cuda.current_stream().cuda_stream
+    return dev, stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _kind(t, dev, name):
+    """DIT_BF16 or DIT_F32 of a CUDA tensor on device `dev`."""
+    torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+    if t.get_device() != dev:
         raise ValueError(f"{name}: expected a CUDA tensor on the current device")
-    if t.dtype is torch.bfloat16:
-        kind = DIT_BF16
-    elif t.dtype is torch.float32:
-        kind = DIT_F32
-    else:
-        raise TypeError(f"{name}: expected bfloat16 or float32, got {t.dtype}")
-    if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name}: the last dimension must be dense")
-    return t.data_ptr(), kind
+    dt = t.dtype
+    if dt is torch.bfloat16:
+        return DIT_BF16
+    if dt is torch.float32:
+        return DIT_F32
+    raise TypeError(f"{name}: expected bfloat16 or float32, got {dt}")
 
 
 class RotaryPlan:
@@ -632,20 +653,22 @@ class RotaryPlan:
                                     beta_fast, beta_slow)
         self.c = dit_rotary_plan()
         dit_rotary_plan_init(self.spec, self.c)
-        self.axes, self.dim = len(widths), sum(widths)
+        self.axes, self.dim, self.ref = len(widths), sum(widths), byref(self.c)
 
 
 def dit_rotary_plan_init(spec: dit_rotary_spec, plan: dit_rotary_plan):
     _ok(lib().dit_rotary_plan_init(byref(spec), byref(plan)), "dit_rotary_plan_init")
 
 
-def _positions(plan: RotaryPlan, pos, rows: int):
-    import torch
+def _positions(plan: RotaryPlan, pos, rows: int, dev: int):
+    torch = _torch()
+    if not isinstance(pos, torch.Tensor) or pos.dtype is not torch.int32:
+        raise TypeError("pos: expected an int32 tensor")
+    if pos.get_device() != dev or not pos.is_contiguous():
+        raise ValueError("pos: expected a contiguous CUDA tensor on the current device")
     if pos.numel() != rows * plan.axes:
         raise ValueError(f"pos: expected {rows} x {plan.axes} positions")
-    if pos.is_cuda and pos.get_device() != torch.cuda.current_device():
-        raise ValueError("pos: expected a tensor on the current device")
-    return _ptr(pos, torch.int32, "pos")
+    return pos.data_ptr()
 
 
 def dit_rotary_tables(plan: RotaryPlan, pos, cos, sin, stream=None):
@@ -654,34 +677,54 @@ def dit_rotary_tables(plan: RotaryPlan, pos, cos, sin, stream=None):
     rows = cos.shape[0]
     if cos.shape != (rows, plan.dim // 2) or sin.shape != cos.shape:
         raise ValueError("cos, sin: expected [rows, dim / 2]")
-    _ok(lib().dit_rotary_tables(byref(plan.c), _positions(plan, pos, rows), rows, _ptr(cos, torch.float32, "cos"),
-                                _ptr(sin, torch.float32, "sin"), _stream(stream)), "dit_rotary_tables")
+    dev, st = _current(stream)
+    if cos.get_device() != dev or sin.get_device() != dev:
+        raise ValueError("cos, sin: expected CUDA tensors on the current device")
+    _ok(lib().dit_rotary_tables(plan.ref, _positions(plan, pos, rows, dev), rows, _ptr(cos, torch.float32, "cos"),
+                                _ptr(sin, torch.float32, "sin"), st), "dit_rotary_tables")
 
 
-def _rotary_rows(x, out, name):
-    if x.dim() not in (3, 4) or out.shape != x.shape or out.dtype != x.dtype:
-        raise ValueError(f"{name}: expected [batch, rows, heads, head_dim] or [rows, heads, head_dim], in and out alike")
-    px, kind = _typed(x, name)
-    po, _ = _typed(out, name)
-    sx, so = x.stride(), out.stride()
-    b = x.dim() == 4
-    return dit_rotary_rows(px, po, x.shape[-2], sx[0] if b else 0, sx[-3], sx[-2], so[0] if b else 0, so[-3], so[-2]), kind
+_rows_struct = struct.Struct("@PPiqqqqqq")  # dit_rotary_rows
+
+
+def _rotary_rows(x, out, dev, name):
+    kind = _kind(x, dev, name)
+    shape, sx = x.shape, x.stride()
+    if out is x:
+        so = sx
+    else:
+        if _kind(out, dev, name) != kind or out.shape != shape:
+            raise ValueError(f"{name}: expected an output like the input")
+        so = out.stride()
+    n = len(shape)
+    if n == 4:
+        bx, bo = sx[0], so[0]
+    elif n == 3:
+        bx = bo = 0
+    else:
+        raise ValueError(f"{name}: expected [batch, rows, heads, head_dim] or [rows, heads, head_dim]")
+    if (sx[-1] != 1 or so[-1] != 1) and shape[-1] > 1:
+        raise ValueError(f"{name}: the last dimension must be dense")
+    return kind, shape, _rows_struct.pack(x.data_ptr(), out.data_ptr(), shape[-2], bx, sx[-3], sx[-2], bo, so[-3], so[-2])
 
 
 def dit_rotary(plan: RotaryPlan, q, k, pos, q_out=None, k_out=None, inverse: bool = False, stream=None):
     """Turn q (and k, or None) [batch, rows, heads, head_dim] or [rows, heads, head_dim], any strides with a
     dense head; q_out / k_out default to in place. pos [batch, rows, axes] int32 (axes may be left out
     when there is one)."""
-    a, kind = _rotary_rows(q, q if q_out is None else q_out, "q")
+    dev, st = _current(stream)
+    kind, shape, a = _rotary_rows(q, q if q_out is None else q_out, dev, "q")
     c = None
     if k is not None:
-        c, kk = _rotary_rows(k, k if k_out is None else k_out, "k")
-        if kk != kind or k.dim() != q.dim() or k.shape[:-2] != q.shape[:-2] or k.shape[-1] != q.shape[-1]:
+        kk, sk, c = _rotary_rows(k, k if k_out is None else k_out, dev, "k")
+        if kk != kind or sk[:-2] != shape[:-2] or sk[-1] != shape[-1]:
             raise ValueError("q and k: expected the same type, batch, rows and head_dim")
-    batch = q.shape[0] if q.dim() == 4 else 1
-    rows = q.shape[-3]
-    _ok(lib().dit_rotary(byref(plan.c), byref(a), byref(c) if c is not None else None, kind, batch, rows, q.shape[-1],
-                         _positions(plan, pos, batch * rows), 1 if inverse else 0, _stream(stream)), "dit_rotary")
+    batch = shape[0] if len(shape) == 4 else 1
+    rows = shape[-3]
+    rc = lib().dit_rotary(plan.ref, a, c, kind, batch, rows, shape[-1], _positions(plan, pos, batch * rows, dev),
+                          1 if inverse else 0, st)
+    if rc:
+        _ok(rc, "dit_rotary")
 
 
 class Fp4Matrix:
@@ -698,6 +741,9 @@ class Fp4Matrix:
         self.codes, self.scales, self.row_scale = codes, scales, row_scale
         self.c = dit_fp4_matrix(format, rows, cols, _ptr(codes, torch.uint8, "codes"),
                                 _ptr(scales, torch.uint8, "scales"), _ptr(row_scale, torch.float32, "row_scale"))
+        self.ref, self.device = byref(self.c), codes.get_device()
+        if scales.get_device() != self.device or (row_scale is not None and row_scale.get_device() != self.device):
+            raise ValueError("codes, scales, row_scale: expected tensors on one device")
 
     @classmethod
     def empty(cls, format: int, rows: int, cols: int, device="cuda"):
@@ -708,11 +754,21 @@ class Fp4Matrix:
                    new(rows, torch.float32) if format == DIT_FP4_NV else None)
 
 
-def _matrix(t, rows, cols, name):
-    p, kind = _typed(t, name)
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+def _matrix(t, rows, cols, dev, name):
+    """(pointer, type, row stride) of a plain [rows, cols] tensor whose rows are dense."""
+    kind = _kind(t, dev, name)
+    if t.shape != (rows, cols):
         raise ValueError(f"{name}: expected [{rows}, {cols}], got {list(t.shape)}")
-    return p, kind, t.stride(0) if rows > 1 else cols
+    s0, s1 = t.stride()
+    if s1 != 1 and cols > 1:
+        raise ValueError(f"{name}: the last dimension must be dense")
+    return t.data_ptr(), kind, s0 if rows > 1 else cols
+
+
+def _on(m: "Fp4Matrix", dev, name):
+    if m.device != dev:
+        raise ValueError(f"{name}: expected a matrix on the current device")
+    return m.ref
 
 
 def dit_fp4_code_bytes(rows: int, cols: int) -> int:
@@ -725,20 +781,29 @@ def dit_fp4_scale_bytes(format: int, rows: int, cols: int) -> int:
 
 def dit_fp4_quantize(x, m: Fp4Matrix, stream=None):
     """x [m.rows, m.cols] bf16 or fp32 (rows may be strided) into m."""
-    p, kind, ld = _matrix(x, m.rows, m.cols, "x")
-    _ok(lib().dit_fp4_quantize(p, kind, ld, byref(m.c), _stream(stream)), "dit_fp4_quantize")
+    dev, st = _current(stream)
+    p, kind, ld = _matrix(x, m.rows, m.cols, dev, "x")
+    rc = lib().dit_fp4_quantize(p, kind, ld, _on(m, dev, "m"), st)
+    if rc:
+        _ok(rc, "dit_fp4_quantize")
 
 
 def dit_fp4_dequantize(m: Fp4Matrix, out, stream=None):
     """m's values into out [m.rows, m.cols] bf16 or fp32 (rows may be strided)."""
-    p, kind, ld = _matrix(out, m.rows, m.cols, "out")
-    _ok(lib().dit_fp4_dequantize(byref(m.c), p, kind, ld, _stream(stream)), "dit_fp4_dequantize")
+    dev, st = _current(stream)
+    p, kind, ld = _matrix(out, m.rows, m.cols, dev, "out")
+    rc = lib().dit_fp4_dequantize(_on(m, dev, "m"), p, kind, ld, st)
+    if rc:
+        _ok(rc, "dit_fp4_dequantize")
 
 
 def dit_fp4_matmul(a: Fp4Matrix, b: Fp4Matrix, out, stream=None):
     """out [a.rows, b.rows] bf16 or fp32 = a b^T."""
-    p, kind, ld = _matrix(out, a.rows, b.rows, "out")
-    _ok(lib().dit_fp4_matmul(byref(a.c), byref(b.c), p, kind, ld, _stream(stream)), "dit_fp4_matmul")
+    dev, st = _current(stream)
+    p, kind, ld = _matrix(out, a.rows, b.rows, dev, "out")
+    rc = lib().dit_fp4_matmul(_on(a, dev, "a"), _on(b, dev, "b"), p, kind, ld, st)
+    if rc:
+        _ok(rc, "dit_fp4_matmul")
 
 
 def dit_linear_fp4_workspace_bytes(format: int, M: int, N: int, K: int) -> int:
@@ -747,11 +812,16 @@ def dit_linear_fp4_workspace_bytes(format: int, M: int, N: int, K: int) -> int:
 
 def dit_linear_fp4(x, w: Fp4Matrix, out, ws, stream=None):
     """out [M, w.rows] = fp4(x) w^T for x [M, w.cols], quantised per call into ws."""
+    dev, st = _current(stream)
     M = x.shape[0]
-    p, kind, ld = _matrix(x, M, w.cols, "x")
-    po, ko, ldo = _matrix(out, M, w.rows, "out")
-    _ok(lib().dit_linear_fp4(p, kind, M, ld, byref(w.c), po, ko, ldo, _ptr(ws, None, "ws"),
-                             ws.numel() * ws.element_size(), _stream(stream)), "dit_linear_fp4")
+    p, kind, ld = _matrix(x, M, w.cols, dev, "x")
+    po, ko, ldo = _matrix(out, M, w.rows, dev, "out")
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("ws: expected a contiguous CUDA tensor on the current device")
+    rc = lib().dit_linear_fp4(p, kind, M, ld, _on(w, dev, "w"), po, ko, ldo, ws.data_ptr(),
+                              ws.numel() * ws.element_size(), st)
+    if rc:
+        _ok(rc, "dit_linear_fp4")
 
 
 def dit_denoise(model: DenoiseModel, img_tokens, txt_feats, sigmas: Sequence[float], txt_cos, txt_sin, img_cos,

@@ -9,6 +9,9 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <type_traits>
+
 #include "fp4.cuh"
 #include "internal.h"
 #include "ptx.cuh"
@@ -21,153 +24,220 @@ constexpr int kUnit = 16;  // values per thread step: one NV block, half an MX b
 // ---------------------------------------------------------------------------------------------
 // quantisation
 // ---------------------------------------------------------------------------------------------
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
-
-// 16 values of row x from column c on (zero past cols) as fp32
-template <typename T, bool VEC>
-__device__ __forceinline__ void load16(float (&v)[kUnit], const T* x, int c, int cols) {
-  if (VEC && c + kUnit <= cols) {
-    if constexpr (sizeof(T) == 2) {
-      uint32_t w[8];
-      ld_global_256(w, x + c);
+// 16 consecutive values as they are stored
+template <typename T>
+struct Unit {
+  uint32_t w[kUnit * sizeof(T) / 4];
+};
+template <typename T>
+__device__ __forceinline__ void unit_values(const Unit<T>& u, float (&v)[kUnit]) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v[2 * j] = __uint_as_float(w[j] << 16);
-        v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-      }
-    } else {
-      uint32_t w[8];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        ld_global_256(w, x + c + 8 * h);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[8 * h + j] = __uint_as_float(w[j]);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < kUnit; ++j) v[j] = c + j < cols ? float(x[c + j]) : 0.f;
+  for (int j = 0; j < kUnit; ++j) {
+    if constexpr (sizeof(T) == 2)
+      v[j] = __uint_as_float(j & 1 ? u.w[j >> 1] & 0xffff0000u : u.w[j >> 1] << 16);
+    else
+      v[j] = __uint_as_float(u.w[j]);
   }
 }
-
-__device__ __forceinline__ uint32_t unit_max(const float (&v)[kUnit]) {
+// The bits of the largest magnitude; their order is finite < infinity < NaN.
+template <typename T>
+__device__ __forceinline__ uint32_t unit_max(const Unit<T>& u) {
   uint32_t m = 0;
+  if constexpr (sizeof(T) == 2) {
 #pragma unroll
-  for (int j = 0; j < kUnit; ++j) m = max(m, abs_bits(v[j]));  // bit order: finite < inf < NaN
+    for (int j = 0; j < 8; ++j) m = __vmaxu2(m, u.w[j] & 0x7fff7fffu);
+    m = max(m & 0xffff0000u, m << 16);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kUnit; ++j) m = max(m, u.w[j] & 0x7fffffffu);
+  }
   return m;
 }
+// 16 values from column c of a row (global, or the staged copy in shared memory), zero past cols
+template <typename T, bool VEC>
+__device__ __forceinline__ Unit<T> unit_load(const T* x, int c, int cols) {
+  Unit<T> u;
+  if (VEC && c + kUnit <= cols) {
+#pragma unroll
+    for (int h = 0; h < int(sizeof(T)) / 2; ++h)
+      ld_global_256(u.w + 8 * h, reinterpret_cast<const uint8_t*>(x + c) + 32 * h);
+  } else {
+    using Bits = typename std::conditional<sizeof(T) == 2, uint16_t, uint32_t>::type;
+    const Bits* b = reinterpret_cast<const Bits*>(x);
+#pragma unroll
+    for (int j = 0; j < kUnit; ++j) {
+      const uint32_t e = c + j < cols ? b[c + j] : 0u;
+      if constexpr (sizeof(T) == 4) u.w[j] = e;
+      else u.w[j >> 1] = j & 1 ? u.w[j >> 1] | e << 16 : e;
+    }
+  }
+  return u;
+}
 
-// One row per CTA. A thread takes units of 16 values; the row is read once for its largest magnitude
-// (NV) and again, out of L1/L2, for the codes. Units run to whole groups of four blocks, so that
-// every scale byte a K = 64 step of the product may read is written; codes run to whole 32 values.
-template <typename T, int FMT, bool VEC>
+// One row per CTA; a thread holds NU units of 16 values (one NV block, half an MX block) in registers, so
+// the row is read once, all its loads in flight together, for its largest magnitude and for its codes.
+// Rows longer than NU units per thread repeat the passes over chunks (NV: the second pass rereads the
+// row, which a row's worth of L2 holds). A row that starts off 32 bytes (VEC = false) is staged through
+// shared memory with coalesced single loads. Units run to whole groups of four blocks, so that every
+// scale byte a K = 64 step of the product may read is written; codes run to whole 32 values.
+// Bound by HBM: the values in, 9/16 byte per value out.
+template <typename T, int FMT, bool VEC, int NU>
 __global__ void __launch_bounds__(256) fp4_quantize_kernel(const T* x, long long ldx, int cols, uint8_t* codes,
                                                            uint8_t* scales, float* row_scale) {
   pdl_wait();
   pdl_trigger();
-  const int r = blockIdx.x;
+  const int r = blockIdx.x, nt = blockDim.x;
   x += r * ldx;
-  const int code_units = fp4_code_row_bytes(cols) / 8;              // 8 code bytes per unit
+  const int code_units = int(fp4_code_row_bytes(cols) / 8);  // 8 code bytes per unit
   const int units = fp4_groups(FMT, cols) * (FMT == DIT_FP4_NV ? 4 : 8);
   uint8_t* crow = codes + (long long)r * fp4_code_row_bytes(cols);
   uint8_t* srow = scales + fp4_scale_row(FMT, r, cols);
-  float u = 0.f, t = 0.f, g = 0.f;
-  __shared__ uint32_t part[8];
+  extern __shared__ uint32_t staged[];
+  T* sx = reinterpret_cast<T*>(staged);
+  const int span = nt * NU;  // units per chunk
+  const int chunks = (units + span - 1) / span;
+  Unit<T> v[NU];
+  auto load = [&](int c) {
+    const int c0 = c * span * kUnit;
+    if constexpr (!VEC) {
+      __syncthreads();
+      const int n = min(cols - c0, span * kUnit);
+      for (int i = threadIdx.x; i < n; i += nt) sx[i] = x[c0 + i];
+      __syncthreads();
+    }
+#pragma unroll
+    for (int k = 0; k < NU; ++k) {
+      const int u = threadIdx.x + k * nt;
+      v[k] = VEC ? unit_load<T, true>(x, c0 + u * kUnit, cols) : unit_load<T, false>(sx, u * kUnit, cols - c0);
+    }
+  };
+  float fu = 0.f, ft = 0.f;
   if constexpr (FMT == DIT_FP4_NV) {
+    __shared__ uint32_t part[8];
     uint32_t m = 0;
-    for (int i = threadIdx.x; i * kUnit < cols; i += blockDim.x) {
-      float v[kUnit];
-      load16<T, VEC>(v, x, i * kUnit, cols);
-      m = max(m, unit_max(v));
+    for (int c = chunks - 1; c >= 0; --c) {  // the first chunk last: it stays in the registers
+      load(c);
+#pragma unroll
+      for (int k = 0; k < NU; ++k) m = max(m, unit_max(v[k]));
     }
     m = __reduce_max_sync(0xffffffffu, m);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
     __syncthreads();
     m = 0;
-    for (int w = 0; w < int(blockDim.x >> 5); ++w) m = max(m, part[w]);
+    for (int w = 0; w < (nt >> 5); ++w) m = max(m, part[w]);
     const Fp4Row fr = fp4_row(m);
-    u = fr.u;
-    t = fr.t;
-    g = fr.g;
-    if (threadIdx.x == 0) row_scale[r] = g;
+    fu = fr.u;
+    ft = fr.t;
+    if (threadIdx.x == 0) row_scale[r] = fr.g;
   }
-  const int rounds = (units + blockDim.x - 1) / blockDim.x;  // whole warps stay together for the shuffle
-  for (int k = 0; k < rounds; ++k) {
-    const int i = threadIdx.x + k * blockDim.x;
-    float v[kUnit];
+  for (int c = 0; c < chunks; ++c) {
+    if (c > 0 || FMT == DIT_FP4_MX) load(c);
 #pragma unroll
-    for (int j = 0; j < kUnit; ++j) v[j] = 0.f;
-    if (i * kUnit < cols) load16<T, VEC>(v, x, i * kUnit, cols);
-    uint32_t m = unit_max(v);
-    float inv;
-    if constexpr (FMT == DIT_FP4_NV) {
-      const Fp4Block b = fp4_block_nv(m, u, t);
-      inv = b.inv;
-      if (i < units) srow[fp4_scale_block(i)] = uint8_t(b.byte);
-    } else {
-      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      const Fp4Block b = fp4_block_mx(m);
-      inv = b.inv;
-      if (i < units && (i & 1) == 0) srow[fp4_scale_block(i >> 1)] = uint8_t(b.byte);
-    }
-    if (i < code_units) {
-      uint32_t w[2];
-      fp4_codes16(v, inv, w);
-      *reinterpret_cast<uint2*>(crow + 8 * i) = make_uint2(w[0], w[1]);
+    for (int k = 0; k < NU; ++k) {
+      const int i = c * span + k * nt + threadIdx.x;
+      uint32_t m = unit_max(v[k]);
+      float inv;
+      // a group's four scale bytes are gathered in one thread
+      if constexpr (FMT == DIT_FP4_NV) {
+        const Fp4Block b = fp4_block_nv(m, fu, ft);
+        inv = b.inv;
+        uint32_t w = b.byte << (8 * (i & 3));
+        w |= __shfl_xor_sync(0xffffffffu, w, 1);
+        w |= __shfl_xor_sync(0xffffffffu, w, 2);
+        if (i < units && (i & 3) == 0) *reinterpret_cast<uint32_t*>(srow + fp4_scale_block(i)) = w;
+      } else {
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        const Fp4Block b = fp4_block_mx(m);
+        inv = b.inv;
+        uint32_t w = b.byte << (8 * ((i >> 1) & 3));
+        w |= __shfl_xor_sync(0xffffffffu, w, 2);
+        w |= __shfl_xor_sync(0xffffffffu, w, 4);
+        if (i < units && (i & 7) == 0) *reinterpret_cast<uint32_t*>(srow + fp4_scale_block(i >> 1)) = w;
+      }
+      if (i < code_units) {
+        float f[kUnit];
+        unit_values(v[k], f);
+        uint32_t w[2];
+        fp4_codes16(f, inv, w);
+        *reinterpret_cast<uint2*>(crow + 8 * i) = make_uint2(w[0], w[1]);
+      }
     }
   }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) fp4_dequantize_kernel(int fmt, const uint8_t* codes, const uint8_t* scales,
-                                                             const float* row_scale, long long n_units, int row_units,
-                                                             int cols, T* out, long long ldo, bool vec) {
+// One row per blockIdx.x, units of 16 values: 8 code bytes and a scale byte in, 32 or 64 bytes out.
+// Bound by HBM, the values out above all.
+template <typename T, int FMT>
+__global__ void __launch_bounds__(256) fp4_dequantize_kernel(const uint8_t* codes, const uint8_t* scales,
+                                                             const float* row_scale, int cols, T* out, long long ldo,
+                                                             bool vec) {
   pdl_wait();
   pdl_trigger();
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (i >= n_units) return;
-  const long long r = i / row_units;
-  const int u = int(i - r * row_units), c = u * kUnit;
-  const uint2 w = *reinterpret_cast<const uint2*>(codes + r * fp4_code_row_bytes(cols) + 8 * u);
-  const int byte = scales[fp4_scale_row(fmt, int(r), cols) + fp4_scale_block(fmt == DIT_FP4_NV ? u : u >> 1)];
-  float v[kUnit];
-  fp4_values16(w, v);
-  if (fmt == DIT_FP4_NV) {
-    const float s = fp4_e4m3(byte), g = row_scale[r];
+  const int r = blockIdx.x;
+  const int units = (cols + kUnit - 1) / kUnit;
+  const uint8_t* crow = codes + (long long)r * fp4_code_row_bytes(cols);
+  const uint8_t* srow = scales + fp4_scale_row(FMT, r, cols);
+  const float g = FMT == DIT_FP4_NV ? __ldg(row_scale + r) : 1.f;
+  T* orow = out + r * ldo;
+#pragma unroll 4
+  for (int u = threadIdx.x; u < units; u += blockDim.x) {
+    const int c = u * kUnit;
+    const uint2 w = *reinterpret_cast<const uint2*>(crow + 8 * u);
+    const int byte = srow[fp4_scale_block(FMT == DIT_FP4_NV ? u : u >> 1)];
+    float v[kUnit];
+    fp4_values16(w, v);
+    const float s = FMT == DIT_FP4_NV ? fp4_e4m3(byte) : fp4_e8m0(byte);
 #pragma unroll
-    for (int j = 0; j < kUnit; ++j) v[j] = v[j] * s * g;
-  } else {
-    const float s = fp4_e8m0(byte);
+    for (int j = 0; j < kUnit; ++j) v[j] = FMT == DIT_FP4_NV ? v[j] * s * g : v[j] * s;
+    T* o = orow + c;
+    if (vec && c + kUnit <= cols) {
+      uint32_t q[8];
+      if constexpr (sizeof(T) == 2) {
 #pragma unroll
-    for (int j = 0; j < kUnit; ++j) v[j] *= s;
-  }
-  T* o = out + r * ldo + c;
-  if (vec && c + kUnit <= cols) {
-    if constexpr (sizeof(T) == 2) {
-      uint4* d = reinterpret_cast<uint4*>(o);
+        for (int j = 0; j < 8; ++j) q[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+        st_global_256(o, q);
+      } else {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        d[h] = make_uint4(pack_bf16x2(v[8 * h], v[8 * h + 1]), pack_bf16x2(v[8 * h + 2], v[8 * h + 3]),
-                          pack_bf16x2(v[8 * h + 4], v[8 * h + 5]), pack_bf16x2(v[8 * h + 6], v[8 * h + 7]));
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) q[j] = __float_as_uint(v[8 * h + j]);
+          st_global_256(o + 8 * h, q);
+        }
+      }
     } else {
-      float4* d = reinterpret_cast<float4*>(o);
 #pragma unroll
-      for (int h = 0; h < 4; ++h) d[h] = make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
+      for (int j = 0; j < kUnit; ++j)
+        if (c + j < cols) o[j] = T(v[j]);
     }
-  } else {
-    for (int j = 0; j < kUnit && c + j < cols; ++j) o[j] = T(v[j]);
   }
 }
 
+template <typename T, int FMT, bool VEC>
+cudaError_t quantize_nu(const T* x, long long ldx, const dit_fp4_matrix& m, cudaStream_t st) {
+  const int units = fp4_groups(FMT, m.cols) * (FMT == DIT_FP4_NV ? 4 : 8);
+  auto go = [&](auto kern, int nu) {
+    const int threads = std::min(256, (units + 32 * nu - 1) / (32 * nu) * 32);
+    const size_t smem = VEC ? 0 : std::min<size_t>(size_t(threads) * nu * kUnit, size_t(m.cols)) * sizeof(T);
+    return launch_pdl(kern, dim3(m.rows), dim3(threads), smem, st, 1, x, ldx, m.cols, m.codes, m.scales, m.row_scale);
+  };
+  // units per thread: as few as cover the row with 256 threads, four (two in fp32) at most
+  if (units <= 256) return go(fp4_quantize_kernel<T, FMT, VEC, 1>, 1);
+  if constexpr (sizeof(T) == 2)
+    if (units > 512) return go(fp4_quantize_kernel<T, FMT, VEC, 4>, 4);
+  return go(fp4_quantize_kernel<T, FMT, VEC, 2>, 2);
+}
 template <typename T, int FMT>
 cudaError_t quantize_go(const T* x, long long ldx, const dit_fp4_matrix& m, cudaStream_t st) {
-  const int units = fp4_groups(FMT, m.cols) * (FMT == DIT_FP4_NV ? 4 : 8);
-  const int threads = units >= 256 ? 256 : (units + 31) / 32 * 32;
-  const bool vec = reinterpret_cast<uintptr_t>(x) % 32 == 0 && ldx * (long long)sizeof(T) % 32 == 0;
-  return vec ? launch_pdl(fp4_quantize_kernel<T, FMT, true>, dim3(m.rows), dim3(threads), 0, st, 1, x, ldx, m.cols,
-                          m.codes, m.scales, m.row_scale)
-             : launch_pdl(fp4_quantize_kernel<T, FMT, false>, dim3(m.rows), dim3(threads), 0, st, 1, x, ldx, m.cols,
-                          m.codes, m.scales, m.row_scale);
+  const bool vec = reinterpret_cast<uintptr_t>(x) % 32 == 0 && (m.rows == 1 || ldx * (long long)sizeof(T) % 32 == 0);
+  return vec ? quantize_nu<T, FMT, true>(x, ldx, m, st) : quantize_nu<T, FMT, false>(x, ldx, m, st);
+}
+template <typename T, int FMT>
+cudaError_t dequantize_go(const dit_fp4_matrix& m, T* out, long long ldo, cudaStream_t st) {
+  const int units = (m.cols + kUnit - 1) / kUnit;
+  const int threads = std::min(256, (units + 31) / 32 * 32);
+  const bool vec = reinterpret_cast<uintptr_t>(out) % 32 == 0 && (m.rows == 1 || ldo * (long long)sizeof(T) % 32 == 0);
+  return launch_pdl(fp4_dequantize_kernel<T, FMT>, dim3(m.rows), dim3(threads), 0, st, 1, m.codes, m.scales,
+                    m.row_scale, m.cols, out, ldo, vec);
 }
 
 }  // namespace
@@ -187,18 +257,16 @@ int fp4_quantize_launch(const void* x, int type, long long ldx, const dit_fp4_ma
 }
 
 int fp4_dequantize_launch(const dit_fp4_matrix& m, void* out, int type, long long ldo, cudaStream_t st) {
-  const int row_units = (m.cols + kUnit - 1) / kUnit;
-  const long long n = (long long)m.rows * row_units;
-  const long long ctas = (n + 255) / 256;
-  if (ctas > 0x7fffffffLL) return DIT_EUNSUPPORTED;
-  const int size = type == DIT_BF16 ? 2 : 4;
-  const bool vec = reinterpret_cast<uintptr_t>(out) % 16 == 0 && ldo * size % 16 == 0;
-  const cudaError_t e =
-      type == DIT_BF16
-          ? launch_pdl(fp4_dequantize_kernel<__nv_bfloat16>, dim3(unsigned(ctas)), dim3(256), 0, st, 1, m.format, m.codes,
-                       m.scales, m.row_scale, n, row_units, m.cols, static_cast<__nv_bfloat16*>(out), ldo, vec)
-          : launch_pdl(fp4_dequantize_kernel<float>, dim3(unsigned(ctas)), dim3(256), 0, st, 1, m.format, m.codes,
-                       m.scales, m.row_scale, n, row_units, m.cols, static_cast<float*>(out), ldo, vec);
+  cudaError_t e;
+  if (type == DIT_BF16) {
+    __nv_bfloat16* p = static_cast<__nv_bfloat16*>(out);
+    e = m.format == DIT_FP4_NV ? dequantize_go<__nv_bfloat16, DIT_FP4_NV>(m, p, ldo, st)
+                               : dequantize_go<__nv_bfloat16, DIT_FP4_MX>(m, p, ldo, st);
+  } else {
+    float* p = static_cast<float*>(out);
+    e = m.format == DIT_FP4_NV ? dequantize_go<float, DIT_FP4_NV>(m, p, ldo, st)
+                               : dequantize_go<float, DIT_FP4_MX>(m, p, ldo, st);
+  }
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? DIT_OK : DIT_ECUDA;
 }
 

@@ -15,6 +15,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -25,19 +26,20 @@ namespace dit {
 namespace {
 
 constexpr int kRotThreads = 256;
-constexpr int kRotUnroll = 4;  // units in flight per thread
+constexpr int kRotUnroll = 4;    // units in flight per thread
+constexpr int kRotMaxRows = 32;  // rows per CTA at most
 
 struct RotArgs {
   const void* x[2];
   void* out[2];
   long long xb[2], xr[2], xh[2], ob[2], orow[2], oh[2];  // strides in values
-  int heads[2];
-  int copy[2];       // values behind the rotated part are copied (not in place)
-  int rows;          // rows per batch entry
-  long long total;   // batch * rows
+  int q_heads, heads;  // q's, q's and k's together
+  int copy[2];         // values behind the rotated part are copied (not in place)
+  int rows;            // rows per batch entry
+  long long total;     // batch * rows
   int rows_per_cta;
-  int head_dim;
-  int lanes_log2;    // threads along one head (a power of two, at least the units of a head)
+  int units;           // units of a head
+  int step_unit, step_head, step_row;  // kRotThreads units further, as (unit, head, row)
   int inverse;
   const int32_t* pos;
   dit_rotary_plan plan;
@@ -55,147 +57,162 @@ __device__ __forceinline__ float2 rot_cos_sin(long long p, unsigned long long U,
   return make_float2((q == 1 || q == 2) ? -cc * amp : cc * amp, (q == 2 || q == 3) ? -ss * amp : ss * amp);
 }
 
-template <int N>
-__device__ __forceinline__ void rot_load(float (&v)[N], const __nv_bfloat16* p) {
-  if constexpr (N == 8) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// VE consecutive values as they are stored: one 16-byte access, or one value
+template <typename T, int VE>
+struct Raw {
+  uint4 u;
+};
+template <typename T>
+struct Raw<T, 1> {
+  T u;
+};
+template <typename T, int VE>
+__device__ __forceinline__ Raw<T, VE> rot_load(const T* p) {
+  Raw<T, VE> r;
+  if constexpr (VE == 1) r.u = *p;
+  else r.u = *reinterpret_cast<const uint4*>(p);
+  return r;
+}
+template <typename T, int VE>
+__device__ __forceinline__ void rot_store(T* p, const Raw<T, VE>& r) {
+  if constexpr (VE == 1) *p = r.u;
+  else *reinterpret_cast<uint4*>(p) = r.u;
+}
+template <typename T, int VE>
+__device__ __forceinline__ void rot_values(const Raw<T, VE>& r, float (&v)[VE]) {
+  if constexpr (VE == 1) {
+    v[0] = float(r.u);
+  } else {
+    const uint32_t w[4] = {r.u.x, r.u.y, r.u.z, r.u.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      v[2 * j] = __uint_as_float(w[j] << 16);
-      v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+      if constexpr (VE == 8) {
+        v[2 * j] = __uint_as_float(w[j] << 16);
+        v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+      } else {
+        v[j] = __uint_as_float(w[j]);
+      }
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < N; ++j) v[j] = __bfloat162float(p[j]);
   }
 }
-template <int N>
-__device__ __forceinline__ void rot_load(float (&v)[N], const float* p) {
-  if constexpr (N == 4) {
-    const float4 u = *reinterpret_cast<const float4*>(p);
-    v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
-  } else {
-#pragma unroll
-    for (int j = 0; j < N; ++j) v[j] = p[j];
-  }
-}
-template <int N>
-__device__ __forceinline__ void rot_store(__nv_bfloat16* p, const float (&v)[N]) {
-  if constexpr (N == 8) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                              pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-  } else {
-#pragma unroll
-    for (int j = 0; j < N; ++j) p[j] = __float2bfloat16_rn(v[j]);
-  }
-}
-template <int N>
-__device__ __forceinline__ void rot_store(float* p, const float (&v)[N]) {
-  if constexpr (N == 4) {
-    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < N; ++j) p[j] = v[j];
-  }
+template <typename T, int VE>
+__device__ __forceinline__ Raw<T, VE> rot_raw(const float (&v)[VE]) {
+  Raw<T, VE> r;
+  if constexpr (VE == 1) r.u = T(v[0]);
+  else if constexpr (VE == 8)
+    r.u = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+  else
+    r.u = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+  return r;
 }
 
-// A unit is what one thread turns: VE consecutive values (adjacent pairs; two values when VE = 1), or
-// VE values of the first half and their VE partners in the second, or VE values that pass unturned.
-// VE = 16 bytes' worth of values where every row and head starts on 16 bytes and the rotated part ends
-// on such a boundary, else 1. blockIdx.x: rows, blockIdx.y: which of q and k.
+// A unit is what one thread turns: VE consecutive values in the adjacent-pair layout (two values when
+// VE = 1), VE values of the first half and their VE partners in the second, or VE values that pass
+// unturned. VE = 16 bytes' worth of values where every row and head starts on 16 bytes and the rotated
+// part ends on such a boundary, else 1.
+// A CTA takes the units of rows_per_cta rows, all heads of q and then of k, kRotThreads at a time in
+// memory order; (unit, head, row) advance by a fixed mixed-radix step, so no thread divides in the loop.
+// The first loads are issued before the CTA works out its cosines and sines.
 template <typename T, int VE, bool HALVES>
-__global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_constant__ RotArgs a) {
+__global__ void __launch_bounds__(kRotThreads, 3) rotary_kernel(const __grid_constant__ RotArgs a) {
+  constexpr bool kTwo = HALVES || VE == 1;                     // a turned unit is two accesses
   constexpr int kTurn = HALVES ? VE : (VE == 1 ? 1 : VE / 2);  // pairs per turned unit
-  constexpr int kA = HALVES ? VE : (VE == 1 ? 2 : VE);         // values of a turned unit's first load
-  constexpr int kAll = HALVES ? 2 * VE : kA;
+  using R = Raw<T, VE>;
   extern __shared__ float2 cs[];  // [rows_per_cta][pairs]
+  __shared__ long long base[kRotMaxRows][4];  // x and out of q, x and out of k at each row
   const int pairs = a.plan.pairs;
   const long long row0 = (long long)blockIdx.x * a.rows_per_cta;
   const int nrows = int(a.total - row0 < a.rows_per_cta ? a.total - row0 : a.rows_per_cta);
-  pdl_wait();
-  pdl_trigger();
-  for (int i = threadIdx.x; i < nrows * pairs; i += kRotThreads) {
-    const int rr = i / pairs, k = i - rr * pairs;
-    const int32_t p = __ldg(a.pos + (row0 + rr) * a.plan.axes + a.plan.axis[k]);
-    float2 v = rot_cos_sin(p, a.plan.turns[k], a.plan.amplitude);
-    if (a.inverse) v.y = -v.y;
-    cs[i] = v;
+  if (threadIdx.x < unsigned(nrows)) {
+    const long long r = row0 + threadIdx.x, b = r / a.rows, t = r - b * a.rows;
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      base[threadIdx.x][2 * z] = b * a.xb[z] + t * a.xr[z];
+      base[threadIdx.x][2 * z + 1] = b * a.ob[z] + t * a.orow[z];
+    }
   }
   __syncthreads();
-  const int z = blockIdx.y;
-  const int unit = threadIdx.x & ((1 << a.lanes_log2) - 1);
-  const int group = threadIdx.x >> a.lanes_log2, groups = kRotThreads >> a.lanes_log2;
+  pdl_wait();
+  pdl_trigger();
   const int turned = pairs / kTurn;
-  const int tail = a.copy[z] ? (a.head_dim - 2 * pairs) / VE : 0;
-  if (unit >= turned + tail) return;
-  const bool turn = unit < turned;
-  const int off = turn ? (HALVES ? unit * VE : unit * kA) : 2 * pairs + (unit - turned) * VE;
-  const T* x = static_cast<const T*>(a.x[z]);
-  T* out = static_cast<T*>(a.out[z]);
-  const int H = a.heads[z];
-  // one (row, head) after another, kRotUnroll of them loaded before the first is turned
-  for (int g0 = group; g0 < nrows * H; g0 += groups * kRotUnroll) {
-    float v[kRotUnroll][kAll];
-    long long dst[kRotUnroll];
-    int rr_[kRotUnroll];
+  int unit = int(threadIdx.x) % a.units, h = int(threadIdx.x) / a.units, rr = h / a.heads;
+  h -= rr * a.heads;
+  bool first = true;
+  do {  // every thread makes the first turn, for the barrier in it
+    R v[kRotUnroll][kTwo ? 2 : 1];
+    T* dst[kRotUnroll];
+    const float2* c[kRotUnroll];  // the unit's angles, null: passes unturned
 #pragma unroll
     for (int u = 0; u < kRotUnroll; ++u) {
-      const int g = g0 + u * groups;
-      if (g < nrows * H) {
-        const int rr = g / H, h = g - rr * H;
-        const long long r = row0 + rr;
-        const long long b = r / a.rows, t = r - b * a.rows;
-        const long long src = b * a.xb[z] + t * a.xr[z] + h * a.xh[z] + off;
-        dst[u] = b * a.ob[z] + t * a.orow[z] + h * a.oh[z] + off;
-        rr_[u] = rr;
-        if (turn) {
-          float p0[kA];
-          rot_load<kA>(p0, x + src);
-#pragma unroll
-          for (int j = 0; j < kA; ++j) v[u][j] = p0[j];
-          if constexpr (HALVES) {
-            rot_load<kA>(p0, x + src + pairs);
-#pragma unroll
-            for (int j = 0; j < kA; ++j) v[u][kA + j] = p0[j];
-          }
-        } else {
-          float p0[VE];
-          rot_load<VE>(p0, x + src);
-#pragma unroll
-          for (int j = 0; j < VE; ++j) v[u][j] = p0[j];
+      dst[u] = nullptr;
+      if (rr < nrows) {
+        const int z = h >= a.q_heads, hz = z ? h - a.q_heads : h;
+        const bool turn = unit < turned;
+        if (turn || a.copy[z]) {
+          const int off = turn ? (HALVES ? unit * VE : unit * 2 * kTurn) : 2 * pairs + (unit - turned) * VE;
+          const T* src = static_cast<const T*>(a.x[z]) + base[rr][2 * z] + hz * a.xh[z] + off;
+          dst[u] = static_cast<T*>(a.out[z]) + base[rr][2 * z + 1] + hz * a.oh[z] + off;
+          c[u] = turn ? cs + rr * pairs + unit * kTurn : nullptr;
+          v[u][0] = rot_load<T, VE>(src);
+          if constexpr (kTwo)
+            if (turn) v[u][1] = rot_load<T, VE>(src + (HALVES ? pairs : 1));
+        }
+        unit += a.step_unit;
+        h += a.step_head;
+        rr += a.step_row;
+        if (unit >= a.units) {
+          unit -= a.units;
+          ++h;
+        }
+        if (h >= a.heads) {
+          h -= a.heads;
+          ++rr;
         }
       }
     }
+    if (first) {
+      for (int i = threadIdx.x; i < nrows * pairs; i += kRotThreads) {
+        const int r = i / pairs, k = i - r * pairs;
+        const int32_t p = __ldg(a.pos + (row0 + r) * a.plan.axes + a.plan.axis[k]);
+        float2 t = rot_cos_sin(p, a.plan.turns[k], a.plan.amplitude);
+        if (a.inverse) t.y = -t.y;
+        cs[i] = t;
+      }
+      __syncthreads();
+      first = false;
+    }
 #pragma unroll
     for (int u = 0; u < kRotUnroll; ++u) {
-      const int g = g0 + u * groups;
-      if (g < nrows * H) {
-        if (turn) {
-          const float2* c = cs + rr_[u] * pairs + unit * kTurn;
-          float w0[kA], w1[kA];
+      if (!dst[u]) continue;
+      if (c[u]) {
+        float x0[VE];
+        rot_values<T, VE>(v[u][0], x0);
+        if constexpr (kTwo) {
+          float x1[VE], y0[VE], y1[VE];
+          rot_values<T, VE>(v[u][1], x1);
+#pragma unroll
+          for (int j = 0; j < VE; ++j) {
+            const float2 t = c[u][j];
+            y0[j] = x0[j] * t.x - x1[j] * t.y;
+            y1[j] = x0[j] * t.y + x1[j] * t.x;
+          }
+          rot_store<T, VE>(dst[u], rot_raw<T, VE>(y0));
+          rot_store<T, VE>(dst[u] + (HALVES ? pairs : 1), rot_raw<T, VE>(y1));
+        } else {
+          float y[VE];
 #pragma unroll
           for (int j = 0; j < kTurn; ++j) {
-            const float2 t = c[j];
-            if constexpr (HALVES) {
-              w0[j] = v[u][j] * t.x - v[u][kA + j] * t.y;
-              w1[j] = v[u][j] * t.y + v[u][kA + j] * t.x;
-            } else {
-              w0[2 * j] = v[u][2 * j] * t.x - v[u][2 * j + 1] * t.y;
-              w0[2 * j + 1] = v[u][2 * j] * t.y + v[u][2 * j + 1] * t.x;
-            }
+            const float2 t = c[u][j];
+            y[2 * j] = x0[2 * j] * t.x - x0[2 * j + 1] * t.y;
+            y[2 * j + 1] = x0[2 * j] * t.y + x0[2 * j + 1] * t.x;
           }
-          rot_store<kA>(out + dst[u], w0);
-          if constexpr (HALVES) rot_store<kA>(out + dst[u] + pairs, w1);
-        } else {
-          float p0[VE];
-#pragma unroll
-          for (int j = 0; j < VE; ++j) p0[j] = v[u][j];
-          rot_store<VE>(out + dst[u], p0);
+          rot_store<T, VE>(dst[u], rot_raw<T, VE>(y));
         }
+      } else {
+        rot_store<T, VE>(dst[u], v[u][0]);
       }
     }
-  }
+  } while (rr < nrows);
 }
 
 __global__ void __launch_bounds__(kRotThreads) rotary_tables_kernel(const __grid_constant__ dit_rotary_plan plan,
@@ -310,50 +327,55 @@ int dit_rotary(const dit_rotary_plan* plan, const dit_rotary_rows* q, const dit_
   if (!pos) return DIT_EINVAL;
   RotArgs a;
   std::memset(&a, 0, sizeof(a));
-  int n = 0;
   bool vec = head_dim % ve == 0 && (plan->layout == DIT_ROTARY_HALVES ? plan->pairs : 2 * plan->pairs) % ve == 0;
-  for (const dit_rotary_rows* r : part) {
+  for (int z = 0; z < 2; ++z) {
+    const dit_rotary_rows* r = part[z];
     if (!r || r->heads == 0) continue;
     if (!r->x || !r->out || reinterpret_cast<uintptr_t>(r->x) % size || reinterpret_cast<uintptr_t>(r->out) % size)
       return DIT_EINVAL;
     // rows that share their place in the output would race
     if ((batch > 1 && r->out_batch == 0) || (rows > 1 && r->out_row == 0) || (r->heads > 1 && r->out_head == 0))
       return DIT_EINVAL;
-    a.x[n] = r->x;
-    a.out[n] = r->out;
-    a.xb[n] = r->x_batch;
-    a.xr[n] = r->x_row;
-    a.xh[n] = r->x_head;
-    a.ob[n] = r->out_batch;
-    a.orow[n] = r->out_row;
-    a.oh[n] = r->out_head;
-    a.heads[n] = r->heads;
+    a.x[z] = r->x;
+    a.out[z] = r->out;
+    a.xb[z] = r->x_batch;
+    a.xr[z] = r->x_row;
+    a.xh[z] = r->x_head;
+    a.ob[z] = r->out_batch;
+    a.orow[z] = r->out_row;
+    a.oh[z] = r->out_head;
+    a.heads += r->heads;
+    if (z == 0) a.q_heads = r->heads;
     const bool same = r->x == r->out && (rows == 1 || r->x_row == r->out_row) &&
                       (r->heads == 1 || r->x_head == r->out_head) && (batch == 1 || r->x_batch == r->out_batch);
-    a.copy[n] = !same;
+    a.copy[z] = !same;
     auto on16 = [&](const void* p, long long s0, long long s1, long long s2) {
       return reinterpret_cast<uintptr_t>(p) % 16 == 0 && s0 % ve == 0 && s1 % ve == 0 && s2 % ve == 0;
     };
     vec = vec && on16(r->x, batch > 1 ? r->x_batch : 0, rows > 1 ? r->x_row : 0, r->heads > 1 ? r->x_head : 0) &&
           on16(r->out, batch > 1 ? r->out_batch : 0, rows > 1 ? r->out_row : 0, r->heads > 1 ? r->out_head : 0);
-    ++n;
   }
-  if (n == 0) return DIT_OK;
+  if (a.heads == 0) return DIT_OK;
   a.rows = rows;
   a.total = (long long)batch * rows;
-  a.head_dim = head_dim;
   a.inverse = inverse != 0;
   a.pos = pos;
   a.plan = *plan;
   const int v = vec ? ve : 1;
   const int turned = plan->pairs / (plan->layout == DIT_ROTARY_HALVES ? v : (v == 1 ? 1 : v / 2));
-  const int units = turned + (head_dim - 2 * plan->pairs) / v;
-  while ((1 << a.lanes_log2) < units) ++a.lanes_log2;
-  a.rows_per_cta = 2;
-  const long long ctas = (a.total + a.rows_per_cta - 1) / a.rows_per_cta;
+  a.units = turned + (head_dim - 2 * plan->pairs) / v;
+  a.step_unit = kRotThreads % a.units;
+  a.step_head = kRotThreads / a.units % a.heads;
+  a.step_row = kRotThreads / a.units / a.heads;
+  // Two rounds of kRotUnroll units per thread, while there are CTAs for every SM several times over.
+  const long long row_units = (long long)a.units * a.heads;
+  long long per = std::min<long long>(kRotMaxRows, 2LL * kRotThreads * kRotUnroll / row_units);
+  per = std::max(1LL, std::min(per, a.total / (4LL * num_sms())));
+  a.rows_per_cta = int(per);
+  const long long ctas = (a.total + per - 1) / per;
   if (ctas > 0x7fffffffLL) return DIT_EUNSUPPORTED;
-  const dim3 grid{unsigned(ctas), unsigned(n), 1u};
-  const size_t smem = size_t(a.rows_per_cta) * plan->pairs * sizeof(float2);
+  const dim3 grid{unsigned(ctas), 1u, 1u};
+  const size_t smem = size_t(per) * plan->pairs * sizeof(float2);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (type == DIT_BF16)
