@@ -1364,7 +1364,7 @@ int dit_fp4_matmul(const dit_fp4_matrix* a, const dit_fp4_matrix* b, void* out, 
   if (!fp4_rows_ok(out, out_type, ldo, a->rows, b->rows)) return DIT_EINVAL;
   int* err = err_word();
   if (!err) return DIT_ECUDA;
-  return fp4_matmul_launch(*a, *b, out, out_type, ldo, err, reinterpret_cast<cudaStream_t>(stream));
+  return fp4_matmul_launch(*a, *b, out, out_type, ldo, err, false, reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t dit_linear_fp4_workspace_bytes(int format, int M, int N, int K) {
@@ -1388,7 +1388,7 @@ int dit_linear_fp4(const void* x, int x_type, int M, long long ldx, const dit_fp
   if (!err) return DIT_ECUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   rc = fp4_quantize_launch(x, x_type, ldx, a, st);
-  return rc == DIT_OK ? fp4_matmul_launch(a, *w, out, out_type, ldo, err, st) : rc;
+  return rc == DIT_OK ? fp4_matmul_launch(a, *w, out, out_type, ldo, err, true, st) : rc;
 }
 
 int dit_block_forward_int8(const dit_dims* d, const dit_block_w8* w, float* txt, int L, float* img, int N,

@@ -42,16 +42,20 @@ __device__ __forceinline__ void unit_values(const Unit<T>& u, float (&v)[kUnit])
 // The bits of the largest magnitude; their order is finite < infinity < NaN.
 template <typename T>
 __device__ __forceinline__ uint32_t unit_max(const Unit<T>& u) {
-  uint32_t m = 0;
   if constexpr (sizeof(T) == 2) {
+    uint32_t m[4];  // max.xorsign.abs: the larger magnitude of each half (with a sign that is masked below)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = __vmaxu2(m, u.w[j] & 0x7fff7fffu);
-    m = max(m & 0xffff0000u, m << 16);
+    for (int j = 0; j < 4; ++j) asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(m[j]) : "r"(u.w[2 * j]), "r"(u.w[2 * j + 1]));
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(m[0]) : "r"(m[1]));
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(m[2]) : "r"(m[3]));
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(m[0]) : "r"(m[2]));
+    return max(m[0] & 0x7fff0000u, (m[0] << 16) & 0x7fff0000u);
   } else {
+    uint32_t m = u.w[0] & 0x7fffffffu;
 #pragma unroll
-    for (int j = 0; j < kUnit; ++j) m = max(m, u.w[j] & 0x7fffffffu);
+    for (int j = 1; j < kUnit; ++j) m = max(m, u.w[j] & 0x7fffffffu);
+    return m;
   }
-  return m;
 }
 // 16 values from column c of a row (global, or the staged copy in shared memory), zero past cols
 template <typename T, bool VEC>
@@ -74,13 +78,86 @@ __device__ __forceinline__ Unit<T> unit_load(const T* x, int c, int cols) {
   return u;
 }
 
-// One row per CTA; a thread holds NU units of 16 values (one NV block, half an MX block) in registers, so
-// the row is read once, all its loads in flight together, for its largest magnitude and for its codes.
-// Rows longer than NU units per thread repeat the passes over chunks (NV: the second pass rereads the
-// row, which a row's worth of L2 holds). A row that starts off 32 bytes (VEC = false) is staged through
-// shared memory with coalesced single loads. Units run to whole groups of four blocks, so that every
-// scale byte a K = 64 step of the product may read is written; codes run to whole 32 values.
-// Bound by HBM: the values in, 9/16 byte per value out.
+// Codes and scale byte of the unit i in v. A group's four scale bytes are gathered in one thread, so every
+// lane of the warp takes part.
+template <typename T, int FMT>
+__device__ __forceinline__ void unit_quantize(const Unit<T>& v, int i, float fu, float ft, int units, int code_units,
+                                              uint8_t* crow, uint8_t* srow) {
+  uint32_t m = unit_max(v);
+  float inv;
+  if constexpr (FMT == DIT_FP4_NV) {
+    const Fp4Block b = fp4_block_nv(m, fu, ft);
+    inv = b.inv;
+    uint32_t w = b.byte << (8 * (i & 3));
+    w |= __shfl_xor_sync(0xffffffffu, w, 1);
+    w |= __shfl_xor_sync(0xffffffffu, w, 2);
+    if (i < units && (i & 3) == 0) *reinterpret_cast<uint32_t*>(srow + fp4_scale_block(i)) = w;
+  } else {
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    const Fp4Block b = fp4_block_mx(m);
+    inv = b.inv;
+    uint32_t w = b.byte << (8 * ((i >> 1) & 3));
+    w |= __shfl_xor_sync(0xffffffffu, w, 2);
+    w |= __shfl_xor_sync(0xffffffffu, w, 4);
+    if (i < units && (i & 7) == 0) *reinterpret_cast<uint32_t*>(srow + fp4_scale_block(i >> 1)) = w;
+  }
+  if (i < code_units) {
+    float f[kUnit];
+    unit_values(v, f);
+    *reinterpret_cast<uint2*>(crow + 8 * i) = fp4_codes16(f, inv);
+  }
+}
+
+// Sizes of a row's parts. Units run to whole groups of four blocks, so that every scale byte a K = 64
+// step of the product may read is written; codes run to whole 32 values.
+template <int FMT>
+struct RowShape {
+  int units, code_units;
+  __device__ explicit RowShape(int cols)
+      : units(fp4_groups(FMT, cols) * (FMT == DIT_FP4_NV ? 4 : 8)), code_units(int(fp4_code_row_bytes(cols) / 8)) {}
+};
+
+// Many rows of up to 32 NU units: one warp per row. A lane holds NU units of 16 values (one NV block, half
+// an MX block) in registers, so the row is read once, all its loads in flight together, for its largest
+// magnitude and for its codes, and no barrier joins the warps. Bound by HBM: the values in, 9/16 byte
+// per value out.
+constexpr int kRowWarps = 4;
+template <typename T, int FMT, int NU>
+__global__ void __launch_bounds__(32 * kRowWarps) fp4_quantize_warp_kernel(const T* x, long long ldx, int rows, int cols,
+                                                                           uint8_t* codes, uint8_t* scales,
+                                                                           float* row_scale) {
+  pdl_wait();
+  pdl_trigger();
+  const int r = blockIdx.x * kRowWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (r >= rows) return;
+  x += r * ldx;
+  const RowShape<FMT> sh(cols);
+  Unit<T> v[NU];
+#pragma unroll
+  for (int k = 0; k < NU; ++k)
+    if (k * 32 < sh.units) v[k] = unit_load<T, true>(x, (k * 32 + lane) * kUnit, cols);
+  float fu = 0.f, ft = 0.f;
+  if constexpr (FMT == DIT_FP4_NV) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < NU; ++k)
+      if (k * 32 < sh.units) m = max(m, unit_max(v[k]));
+    const Fp4Row fr = fp4_row(__reduce_max_sync(0xffffffffu, m));
+    fu = fr.u;
+    ft = fr.t;
+    if (lane == 0) row_scale[r] = fr.g;
+  }
+  uint8_t* crow = codes + (long long)r * fp4_code_row_bytes(cols);
+  uint8_t* srow = scales + fp4_scale_row(FMT, r, cols);
+#pragma unroll
+  for (int k = 0; k < NU; ++k)
+    if (k * 32 < sh.units) unit_quantize<T, FMT>(v[k], k * 32 + lane, fu, ft, sh.units, sh.code_units, crow, srow);
+}
+
+// Few rows, long rows, or rows off 32 bytes: one CTA per row, NU units per thread and chunk. Rows longer
+// than NU units per thread repeat the passes over chunks (NV: the second pass rereads the row, which L2
+// holds). A row that starts off 32 bytes (VEC = false) is staged through shared memory with coalesced
+// single loads.
 template <typename T, int FMT, bool VEC, int NU>
 __global__ void __launch_bounds__(256) fp4_quantize_kernel(const T* x, long long ldx, int cols, uint8_t* codes,
                                                            uint8_t* scales, float* row_scale) {
@@ -88,14 +165,13 @@ __global__ void __launch_bounds__(256) fp4_quantize_kernel(const T* x, long long
   pdl_trigger();
   const int r = blockIdx.x, nt = blockDim.x;
   x += r * ldx;
-  const int code_units = int(fp4_code_row_bytes(cols) / 8);  // 8 code bytes per unit
-  const int units = fp4_groups(FMT, cols) * (FMT == DIT_FP4_NV ? 4 : 8);
+  const RowShape<FMT> sh(cols);
   uint8_t* crow = codes + (long long)r * fp4_code_row_bytes(cols);
   uint8_t* srow = scales + fp4_scale_row(FMT, r, cols);
   extern __shared__ uint32_t staged[];
   T* sx = reinterpret_cast<T*>(staged);
   const int span = nt * NU;  // units per chunk
-  const int chunks = (units + span - 1) / span;
+  const int chunks = (sh.units + span - 1) / span;
   Unit<T> v[NU];
   auto load = [&](int c) {
     const int c0 = c * span * kUnit;
@@ -123,8 +199,8 @@ __global__ void __launch_bounds__(256) fp4_quantize_kernel(const T* x, long long
     m = __reduce_max_sync(0xffffffffu, m);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
     __syncthreads();
-    m = 0;
-    for (int w = 0; w < (nt >> 5); ++w) m = max(m, part[w]);
+    m = part[0];
+    for (int w = 1; w < (nt >> 5); ++w) m = max(m, part[w]);
     const Fp4Row fr = fp4_row(m);
     fu = fr.u;
     ft = fr.t;
@@ -133,42 +209,15 @@ __global__ void __launch_bounds__(256) fp4_quantize_kernel(const T* x, long long
   for (int c = 0; c < chunks; ++c) {
     if (c > 0 || FMT == DIT_FP4_MX) load(c);
 #pragma unroll
-    for (int k = 0; k < NU; ++k) {
-      const int i = c * span + k * nt + threadIdx.x;
-      uint32_t m = unit_max(v[k]);
-      float inv;
-      // a group's four scale bytes are gathered in one thread
-      if constexpr (FMT == DIT_FP4_NV) {
-        const Fp4Block b = fp4_block_nv(m, fu, ft);
-        inv = b.inv;
-        uint32_t w = b.byte << (8 * (i & 3));
-        w |= __shfl_xor_sync(0xffffffffu, w, 1);
-        w |= __shfl_xor_sync(0xffffffffu, w, 2);
-        if (i < units && (i & 3) == 0) *reinterpret_cast<uint32_t*>(srow + fp4_scale_block(i)) = w;
-      } else {
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        const Fp4Block b = fp4_block_mx(m);
-        inv = b.inv;
-        uint32_t w = b.byte << (8 * ((i >> 1) & 3));
-        w |= __shfl_xor_sync(0xffffffffu, w, 2);
-        w |= __shfl_xor_sync(0xffffffffu, w, 4);
-        if (i < units && (i & 7) == 0) *reinterpret_cast<uint32_t*>(srow + fp4_scale_block(i >> 1)) = w;
-      }
-      if (i < code_units) {
-        float f[kUnit];
-        unit_values(v[k], f);
-        uint32_t w[2];
-        fp4_codes16(f, inv, w);
-        *reinterpret_cast<uint2*>(crow + 8 * i) = make_uint2(w[0], w[1]);
-      }
-    }
+    for (int k = 0; k < NU; ++k)
+      unit_quantize<T, FMT>(v[k], c * span + k * nt + threadIdx.x, fu, ft, sh.units, sh.code_units, crow, srow);
   }
 }
 
 // One row per blockIdx.x, units of 16 values: 8 code bytes and a scale byte in, 32 or 64 bytes out.
 // Bound by HBM, the values out above all.
 template <typename T, int FMT>
-__global__ void __launch_bounds__(256) fp4_dequantize_kernel(const uint8_t* codes, const uint8_t* scales,
+__global__ void __launch_bounds__(256, 6) fp4_dequantize_kernel(const uint8_t* codes, const uint8_t* scales,
                                                              const float* row_scale, int cols, T* out, long long ldo,
                                                              bool vec) {
   pdl_wait();
@@ -179,7 +228,7 @@ __global__ void __launch_bounds__(256) fp4_dequantize_kernel(const uint8_t* code
   const uint8_t* srow = scales + fp4_scale_row(FMT, r, cols);
   const float g = FMT == DIT_FP4_NV ? __ldg(row_scale + r) : 1.f;
   T* orow = out + r * ldo;
-#pragma unroll 4
+#pragma unroll 1
   for (int u = threadIdx.x; u < units; u += blockDim.x) {
     const int c = u * kUnit;
     const uint2 w = *reinterpret_cast<const uint2*>(crow + 8 * u);
@@ -220,6 +269,19 @@ cudaError_t quantize_nu(const T* x, long long ldx, const dit_fp4_matrix& m, cuda
     const size_t smem = VEC ? 0 : std::min<size_t>(size_t(threads) * nu * kUnit, size_t(m.cols)) * sizeof(T);
     return launch_pdl(kern, dim3(m.rows), dim3(threads), smem, st, 1, x, ldx, m.cols, m.codes, m.scales, m.row_scale);
   };
+  if constexpr (VEC) {
+    // a warp per row: 8 units of bf16, 4 of fp32 per lane at most (64 registers of values)
+    constexpr int kMost = sizeof(T) == 2 ? 8 : 4;
+    if (units <= 32 * kMost && m.rows >= 4 * num_sms()) {
+      auto rows = [&](auto kern) {
+        return launch_pdl(kern, dim3((m.rows + kRowWarps - 1) / kRowWarps), dim3(32 * kRowWarps), 0, st, 1, x, ldx, m.rows,
+                          m.cols, m.codes, m.scales, m.row_scale);
+      };
+      if (units <= 64) return rows(fp4_quantize_warp_kernel<T, FMT, 2>);
+      if (units <= 128) return rows(fp4_quantize_warp_kernel<T, FMT, 4>);
+      return rows(fp4_quantize_warp_kernel<T, FMT, kMost>);
+    }
+  }
   // units per thread: as few as cover the row with 256 threads, four (two in fp32) at most
   if (units <= 256) return go(fp4_quantize_kernel<T, FMT, VEC, 1>, 1);
   if constexpr (sizeof(T) == 2)

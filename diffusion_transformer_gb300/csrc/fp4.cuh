@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/dit.h"
+#include "ptx.cuh"
 
 namespace dit {
 
@@ -72,24 +73,29 @@ __device__ __forceinline__ Fp4Block fp4_block_mx(uint32_t bits) {
   return Fp4Block{uint32_t(e + 127), __uint_as_float(uint32_t(127 - e) << 23)};
 }
 
-// 16 values times inv, rounded to codes: 8 bytes, the lower columns first. inv = 0 gives zero codes
-// whatever the values (a row or block with an infinity or NaN keeps no code).
-__device__ __forceinline__ uint32_t fp4_codes8(const float* v, float inv) {
+// Eight codes of (pairs of) products, the lower columns first; conversions saturate at 6.
+__device__ __forceinline__ uint32_t fp4_codes8(const uint64_t (&y)[4]) {
   uint32_t w;
-  asm("{\n.reg .b8 a, b, c, d;\n"
-      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n"
-      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
-      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n"
-      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+  asm("{\n.reg .b8 a, b, c, d;\n.reg .f32 l, h;\n"
+      "mov.b64 {l, h}, %1;\ncvt.rn.satfinite.e2m1x2.f32 a, h, l;\n"
+      "mov.b64 {l, h}, %2;\ncvt.rn.satfinite.e2m1x2.f32 b, h, l;\n"
+      "mov.b64 {l, h}, %3;\ncvt.rn.satfinite.e2m1x2.f32 c, h, l;\n"
+      "mov.b64 {l, h}, %4;\ncvt.rn.satfinite.e2m1x2.f32 d, h, l;\n"
       "mov.b32 %0, {a, b, c, d};\n}"
       : "=r"(w)
-      : "f"(__fmul_rn(v[0], inv)), "f"(__fmul_rn(v[1], inv)), "f"(__fmul_rn(v[2], inv)), "f"(__fmul_rn(v[3], inv)),
-        "f"(__fmul_rn(v[4], inv)), "f"(__fmul_rn(v[5], inv)), "f"(__fmul_rn(v[6], inv)), "f"(__fmul_rn(v[7], inv)));
+      : "l"(y[0]), "l"(y[1]), "l"(y[2]), "l"(y[3]));
   return w;
 }
-__device__ __forceinline__ void fp4_codes16(const float* v, float inv, uint32_t (&w)[2]) {
-  w[0] = inv != 0.f ? fp4_codes8(v, inv) : 0u;
-  w[1] = inv != 0.f ? fp4_codes8(v + 8, inv) : 0u;
+// 16 values times inv (two products per instruction, each rounded as a single one), rounded to codes: 8
+// bytes. inv = 0 gives zero codes whatever the values (a row or block with an infinity or NaN keeps none).
+__device__ __forceinline__ uint2 fp4_codes16(const float* v, float inv) {
+  const uint64_t i2 = f2_pack(inv, inv);
+  uint64_t y[2][4];
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(y[j >> 2][j & 3]) : "l"(f2_pack(v[2 * j], v[2 * j + 1])), "l"(i2));
+  const uint2 w = make_uint2(fp4_codes8(y[0]), fp4_codes8(y[1]));
+  return inv != 0.f ? w : make_uint2(0u, 0u);
 }
 
 __device__ __forceinline__ void fp4_values16(uint2 w, float* v) {

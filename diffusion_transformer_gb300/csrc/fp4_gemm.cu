@@ -6,7 +6,8 @@
 // K = 64, preceded by the copies of the stage's scale chunks from shared to tensor memory.
 //
 // Two kernels:
-//   pair   256 x 256 tiles on CTA pairs (cta_group::2), persistent, for products with enough tiles
+//   pair   tiles of 256 rows of one operand by up to 256 of the other on CTA pairs (cta_group::2),
+//          persistent, for products with enough tiles
 //   split  128 rows of B against up to 128 rows of A per CTA, a cluster of CTAs sharing the K loop and
 //          adding their partial tiles through distributed shared memory, for few rows or few tiles
 #include <cuda.h>
@@ -39,9 +40,10 @@ struct Fp4Params {
   long long ldo;
   const float* a_scale;  // NV: row scales
   const float* b_scale;
+  int early;             // B was complete before the kernel ahead of this one in the stream began
   int tma_out;           // rows of `out` start on 16 bytes: tiles leave through TMA stores
-  int n_fast;
-  int bn, stages;        // split kernel: rows of A per tile, pipeline depth
+  int n_fast;            // tile order
+  int bn, stages;        // rows of the narrow operand per tile (see each kernel), pipeline depth
 };
 
 __device__ __forceinline__ int stage_steps(int K, int kb) { return min(4, (K - kb * kStageK + 63) / 64); }
@@ -49,20 +51,23 @@ __device__ __forceinline__ int stage_steps(int K, int kb) { return min(4, (K - k
 // ---------------------------------------------------------------------------------------------
 // pair kernel
 // ---------------------------------------------------------------------------------------------
-// Tensor memory, 512 columns: two 256-column accumulators that overlap by 48 columns ([0, 256) and
-// [208, 464)) and 48 columns of scales. An accumulator's overlapped columns are drained first and then
-// handed over, so the next tile's MMAs wait for a quarter of an epilogue, not for all of it.
-constexpr int kAcc1 = 208, kSfCol = 464, kPairStages = 5;
+// D [256 rows of P, bn rows of Q] per tile: P and Q are A and B, or (SWAP) B and A. Each CTA of the pair
+// brings its 128 rows of P, half of the rows of Q, and the scales of its P rows and of all Q rows.
+//
+// Tensor memory, 512 columns: two accumulators and 48 columns of scales from 464 on. With bn = 256 the
+// accumulators overlap by 48 columns ([0, 256) and [208, 464)): the overlapped columns are drained first
+// and then handed over, so the next tile's MMAs wait for a quarter of an epilogue, not for all of it.
+constexpr int kOverlapAt = 208, kSfCol = 464, kMaxStages = 8;
 constexpr int kPairThreads = 192;
+constexpr uint32_t kStaging = 4 * 2 * 4096;                                   // two 4 KB output tiles per epilogue warp
+constexpr uint32_t kPairFixed = 1024 + kStaging + 4 * 256 + 8 * (2 * kMaxStages + 5) + 16;
 
 template <int FMT>
-struct PairCfg {
-  using S = Scales<FMT>;
-  static constexpr uint32_t kStage = 2 * kTileBytes + 3 * S::kBytes;  // A, B, scales of 128 A and 256 B rows
-  static constexpr uint32_t kStaging = 4 * 2 * 4096;                  // two 4 KB output tiles per epilogue warp
-  static constexpr uint32_t kSmem = 1024 + kPairStages * kStage + kStaging + 4 * 256 + 256;
-};
+__host__ __device__ constexpr uint32_t pair_stage_bytes(int bn) {
+  return kTileBytes + uint32_t(bn) * 64 + 3 * Scales<FMT>::kBytes;
+}
 
+// 16 bytes of the staging row `lane`, rows of 128 bytes swizzled as the TMA store expects
 template <typename T>
 __device__ __forceinline__ void put_chunk(uint8_t* tile, int lane, int q, const float* v) {
   uint4 u;
@@ -73,51 +78,81 @@ __device__ __forceinline__ void put_chunk(uint8_t* tile, int lane, int q, const 
   *reinterpret_cast<uint4*>(tile + sw128_offset(lane, q)) = u;
 }
 
-template <int FMT, typename T>
+template <int FMT, typename T, bool SWAP>
 __global__ void __launch_bounds__(kPairThreads, 1)
-    fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                    const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
+    fp4_pair_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
+                    const __grid_constant__ CUtensorMap tmSP, const __grid_constant__ CUtensorMap tmSQ,
                     const __grid_constant__ CUtensorMap tmO, const Fp4Params p) {
-  using Cfg = PairCfg<FMT>;
   using SC = Scales<FMT>;
-  constexpr int S = kPairStages;
+  const int S = p.stages, bn = p.bn;
+  const uint32_t qBytes = uint32_t(bn) * 64;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sA = smem;
-  uint8_t* sB = sA + S * kTileBytes;
-  uint8_t* sSA = sB + S * kTileBytes;
-  uint8_t* sSB = sSA + S * SC::kBytes;
-  uint8_t* sE = sSB + S * 2 * SC::kBytes;
-  float* sC = reinterpret_cast<float*>(sE + Cfg::kStaging);  // 64 column factors per epilogue warp
+  uint8_t* sE = smem;  // output staging first: its tiles, and the operands' after it, on 1024 bytes
+  uint8_t* sP = sE + kStaging;
+  uint8_t* sQ = sP + S * kTileBytes;
+  uint8_t* sSP = sQ + S * qBytes;
+  uint8_t* sSQ = sSP + S * SC::kBytes;
+  float* sC = reinterpret_cast<float*>(sSQ + S * 2 * SC::kBytes);  // 64 column factors per epilogue warp
   uint64_t* bars = reinterpret_cast<uint64_t*>(sC + 4 * 64);
-  uint64_t *full = bars, *empty = bars + S, *tfull = bars + 2 * S, *tempty = tfull + 2, *drain = tempty + 1;
+  uint64_t *full = bars, *empty = bars + S, *tfull = bars + 2 * S, *tempty = tfull + 2, *drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
 
   const int warp = threadIdx.x >> 5, lane = lane_id();
   const uint32_t rank = cluster_ctarank();
   const int unit = int(blockIdx.x >> 1), units = int(gridDim.x >> 1);
-  const int num_m = (p.M + 255) / 256, num_n = (p.N + 255) / 256, tiles = num_m * num_n;
+  const int rowsP = SWAP ? p.N : p.M, rowsQ = SWAP ? p.M : p.N;
+  const int num_p = (rowsP + 255) / 256, num_q = (rowsQ + bn - 1) / bn, tiles = num_p * num_q;
   const int KB = (p.K + kStageK - 1) / kStageK;
-  auto tile_mn = [&](int tile, int& mb, int& nb) {
-    mb = p.n_fast ? tile / num_n : tile % num_m;
-    nb = p.n_fast ? tile % num_n : tile / num_m;
+  const bool overlap = bn == 256;
+  const uint32_t acc1 = overlap ? kOverlapAt : bn;
+  auto tile_pq = [&](int tile, int& pb, int& qb) {
+    pb = p.n_fast ? tile / num_q : tile % num_p;
+    qb = p.n_fast ? tile % num_q : tile / num_p;
   };
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
       mbar_init(smem_u32(&empty[s]), 1);
     }
-    for (int a = 0; a < 2; ++a) mbar_init(smem_u32(&tfull[a]), 1);
-    mbar_init(smem_u32(tempty), 2 * 128);  // both CTAs' epilogue threads
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(smem_u32(&tfull[a]), 1);
+      mbar_init(smem_u32(&tempty[a]), 2 * 128);  // both CTAs' epilogue threads
+    }
     mbar_init(smem_u32(drain), 1);
     fence_mbar_init();
-    tma_prefetch_desc(&tmA);
-    tma_prefetch_desc(&tmB);
-    tma_prefetch_desc(&tmSA);
-    tma_prefetch_desc(&tmSB);
+    tma_prefetch_desc(&tmP);
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmSP);
+    tma_prefetch_desc(&tmSQ);
   }
   __syncthreads();
   cluster_barrier();  // barriers of both CTAs are up
+  const uint32_t full0 = mapa_shared(smem_u32(&full[0]), 0);  // both CTAs' copies count on the first's barriers
+  auto load_p = [&](int stage, int kb, int pb) {
+    const uint32_t fb = full0 + uint32_t(stage) * 8u;
+    tma_load_2d_pair(smem_u32(sP + stage * kTileBytes), &tmP, fb, kb * 128, pb * 256 + int(rank) * 128);
+    tma_load_3d_pair(smem_u32(sSP + stage * SC::kBytes), &tmSP, fb, 0, kb * SC::kGroups, pb * 2 + int(rank));
+  };
+  auto load_q = [&](int stage, int kb, int qb) {
+    const uint32_t fb = full0 + uint32_t(stage) * 8u;
+    tma_load_2d_pair(smem_u32(sQ + stage * qBytes), &tmQ, fb, kb * 128, qb * bn + int(rank) * (bn / 2));
+    tma_load_3d_pair(smem_u32(sSQ + stage * 2 * SC::kBytes), &tmSQ, fb, 0, kb * SC::kGroups, (qb * bn) >> 7);
+  };
+  auto expect = [&](int stage) {
+    if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full[stage]), 2 * pair_stage_bytes<FMT>(bn));
+  };
+  // B's part of the first stages does not wait for the kernel that writes A
+  const int ahead = p.early ? min(S, KB) : 0;
+  if (warp == 0 && ahead > 0 && elect_one()) {
+    int pb, qb;
+    tile_pq(unit, pb, qb);
+    for (int s = 0; s < ahead; ++s) {
+      expect(s);
+      if constexpr (SWAP) load_p(s, s, pb);
+      else load_q(s, s, qb);
+    }
+  }
   if (warp == 1) {
     tmem_alloc_pair(smem_u32(tmem_slot), 512);
     tmem_relinquish_pair();
@@ -134,18 +169,20 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       int stage = 0;
       uint32_t phase = 0, issued = 0, parity = 0;
       bool ok = true;
-      const uint32_t full0 = mapa_shared(smem_u32(&full[0]), 0);  // both CTAs' copies count on the first's barriers
+      int done = 0;  // stages filled so far
       for (int tile = unit; tile < tiles && ok; tile += units) {
-        int mb, nb;
-        tile_mn(tile, mb, nb);
-        for (int kb = 0; kb < KB; ++kb) {
-          if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1, p.err, kErrTimeoutProducer)) { ok = false; break; }
-          if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full[stage]), 2 * Cfg::kStage);
-          const uint32_t fb = full0 + uint32_t(stage) * 8u;
-          tma_load_2d_pair(smem_u32(sA + stage * kTileBytes), &tmA, fb, kb * 128, mb * 256 + int(rank) * 128);
-          tma_load_2d_pair(smem_u32(sB + stage * kTileBytes), &tmB, fb, kb * 128, nb * 256 + int(rank) * 128);
-          tma_load_3d_pair(smem_u32(sSA + stage * SC::kBytes), &tmSA, fb, 0, kb * SC::kGroups, mb * 2 + int(rank));
-          tma_load_3d_pair(smem_u32(sSB + stage * 2 * SC::kBytes), &tmSB, fb, 0, kb * SC::kGroups, nb * 2);
+        int pb, qb;
+        tile_pq(tile, pb, qb);
+        for (int kb = 0; kb < KB; ++kb, ++done) {
+          if (done < ahead) {
+            if constexpr (SWAP) load_q(stage, kb, qb);
+            else load_p(stage, kb, pb);
+          } else {
+            if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1, p.err, kErrTimeoutProducer)) { ok = false; break; }
+            expect(stage);
+            load_p(stage, kb, pb);
+            load_q(stage, kb, qb);
+          }
           issued |= 1u << stage;
           parity = (parity & ~(1u << stage)) | (phase << stage);
           if (++stage == S) { stage = 0; phase ^= 1; }
@@ -162,32 +199,39 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       bool ok = true;
       int it = 0;
       for (int tile = unit; tile < tiles && ok; tile += units, ++it) {
-        // the previous tile's overlapped columns are drained (and, before them, the tile before it)
-        if (it > 0 && !mbar_wait_cluster(smem_u32(tempty), uint32_t(it - 1) & 1u, p.err, kErrTimeoutMma)) break;
+        int pb, qb;
+        tile_pq(tile, pb, qb);
+        // this accumulator is free: the tile before last was drained (overlap: the last one's shared
+        // columns are, and it drained the tile before it first)
+        const int prev = overlap ? it - 1 : it - 2;
+        if (prev >= 0 &&
+            !mbar_wait_cluster(smem_u32(&tempty[prev & 1]), uint32_t(prev >> 1) & 1u, p.err, kErrTimeoutMma))
+          break;
         tc_fence_after();
-        const uint32_t d = tmem + ((it & 1) ? kAcc1 : 0);
+        const uint32_t d = tmem + ((it & 1) ? acc1 : 0);
+        // Q rows may start in the middle of a band of 128: two columns per 64 rows
+        const uint32_t sfp = tmem + kSfCol, sfq = sfp + SC::kGroups * 4, sub = uint32_t((qb * bn) & 127) >> 5;
         for (int kb = 0; kb < KB; ++kb) {
           if (!mbar_wait(smem_u32(&full[stage]), phase, p.err, kErrTimeoutMma)) { ok = false; break; }
           tc_fence_after();
           const int steps = stage_steps(p.K, kb);
-          const uint32_t sfa = tmem + kSfCol, sfb = sfa + SC::kGroups * 4;
-          const uint64_t da = scale_chunk_desc(smem_u32(sSA + stage * SC::kBytes));
-          const uint64_t db = scale_chunk_desc(smem_u32(sSB + stage * 2 * SC::kBytes));
-          const uint64_t ad = sw128_desc(smem_u32(sA + stage * kTileBytes));
-          const uint64_t bd = sw128_desc(smem_u32(sB + stage * kTileBytes));
+          const uint64_t dp = scale_chunk_desc(smem_u32(sSP + stage * SC::kBytes));
+          const uint64_t dq = scale_chunk_desc(smem_u32(sSQ + stage * 2 * SC::kBytes));
+          const uint64_t pd = sw128_desc(smem_u32(sP + stage * kTileBytes));
+          const uint64_t qd = sw128_desc(smem_u32(sQ + stage * qBytes));
 #pragma unroll
           for (int g = 0; g < SC::kGroups; ++g) {
-            tmem_cp_scales<true>(sfa + 4 * g, da + uint64_t(32 * g));
-            tmem_cp_scales<true>(sfb + 8 * g, db + uint64_t(32 * g));
-            tmem_cp_scales<true>(sfb + 8 * g + 4, db + uint64_t(32 * (SC::kGroups + g)));
+            tmem_cp_scales<true>(sfp + 4 * g, dp + uint64_t(32 * g));
+            tmem_cp_scales<true>(sfq + 8 * g, dq + uint64_t(32 * g));
+            if (bn > 128) tmem_cp_scales<true>(sfq + 8 * g + 4, dq + uint64_t(32 * (SC::kGroups + g)));
           }
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
             if (kk < steps) {
               const int g = SC::kNv ? kk : kk >> 1;
-              umma_fp4<SC::kNv, true>(d, ad + uint64_t(2 * kk), bd + uint64_t(2 * kk),
-                                      idesc_fp4(SC::kNv, 256, 256, SC::kNv ? 0 : (kk & 1) * 2), sfa + 4 * g,
-                                      sfb + 8 * g, kb != 0 || kk != 0);
+              umma_fp4<SC::kNv, true>(d, pd + uint64_t(2 * kk), qd + uint64_t(2 * kk),
+                                      idesc_fp4(SC::kNv, 256, bn, SC::kNv ? 0 : (kk & 1) * 2), sfp + 4 * g,
+                                      sfq + 8 * g + sub, kb != 0 || kk != 0);
             }
           }
           umma_commit_pair_both(smem_u32(&empty[stage]));
@@ -200,39 +244,52 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       mbar_wait(smem_u32(drain), 0, p.err, kErrTimeoutDrain);
     }
   } else {
-    const int quad = warp & 3;
+    const int quad = warp & 3, groups = bn / 64;
     uint8_t* stage0 = sE + (warp - 2) * 8192;
     float* cf = sC + (warp - 2) * 64;
-    const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0);
+    const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
+    const float* p_scale = SWAP ? p.b_scale : p.a_scale;
+    const float* q_scale = SWAP ? p.a_scale : p.b_scale;
     int it = 0, buf = 0;
     for (int tile = unit; tile < tiles; tile += units, ++it) {
-      int mb, nb;
-      tile_mn(tile, mb, nb);
+      int pb, qb;
+      tile_pq(tile, pb, qb);
       const int acc = it & 1;
-      const int row0 = mb * 256 + int(rank) * 128 + quad * 32, row = row0 + lane;
-      const float ra = SC::kNv ? (row < p.M ? __ldg(p.a_scale + row) : 0.f) : 1.f;
+      const int row0 = pb * 256 + int(rank) * 128 + quad * 32, row = row0 + lane;  // P rows of this warp
+      float rp = 1.f, f0 = 1.f, f1 = 1.f;
+      // 64 columns at a time, overlapped ones first; a group's factors are fetched a group ahead
+      auto group_at = [&](int j) { return overlap && acc == 0 ? groups - 1 - j : j; };
+      auto fetch = [&](int j) {
+        const int q = qb * bn + group_at(j) * 64 + lane;
+        f0 = q < rowsQ ? __ldg(q_scale + q) : 0.f;
+        f1 = q + 32 < rowsQ ? __ldg(q_scale + q + 32) : 0.f;
+      };
+      if constexpr (SC::kNv) {
+        rp = row < rowsP ? __ldg(p_scale + row) : 0.f;
+        fetch(0);
+      }
       if (!mbar_wait_warp(smem_u32(&tfull[acc]), uint32_t(it >> 1) & 1u, p.err, kErrTimeoutEpilogue)) break;
       tc_fence_after();
-      const uint32_t taddr = tmem + (uint32_t(quad * 32) << 16) + (acc ? kAcc1 : 0);
-      // 64 columns at a time, the overlapped ones first
+      const uint32_t taddr = tmem + (uint32_t(quad * 32) << 16) + (acc ? acc1 : 0);
 #pragma unroll 1
-      for (int j = 0; j < 4; ++j) {
-        const int g = acc ? j : 3 - j, n = nb * 256 + g * 64;
+      for (int j = 0; j < groups; ++j) {
+        const int g = group_at(j), q0 = qb * bn + g * 64;
         uint32_t w[2][32];
         tmem_ld32(taddr + g * 64, w[0]);
         tmem_ld32(taddr + g * 64 + 32, w[1]);
         if constexpr (SC::kNv) {
           __syncwarp();
-          cf[lane] = n + lane < p.N ? __ldg(p.b_scale + n + lane) : 0.f;
-          cf[lane + 32] = n + lane + 32 < p.N ? __ldg(p.b_scale + n + lane + 32) : 0.f;
+          cf[lane] = f0;
+          cf[lane + 32] = f1;
+          if (j + 1 < groups) fetch(j + 1);
           __syncwarp();
         }
         tmem_ld_wait();
-        if (j == 0) {
+        if (j == (overlap ? 0 : groups - 1)) {
           tc_fence_before();
-          mbar_arrive_cluster(tempty0);
+          mbar_arrive_cluster(tempty0 + uint32_t(acc) * 8u);
         }
-        if (n >= p.N || row0 >= p.M) continue;
+        if (q0 >= rowsQ || row0 >= rowsP) continue;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           float v[32];
@@ -243,38 +300,63 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float x = __uint_as_float(w[h][c + e]);
-              v[c + e] = SC::kNv ? x * ra * ff[e] : x;
+              v[c + e] = SC::kNv ? x * rp * ff[e] : x;
             }
           }
-          // a 4 KB staging tile: 32 rows of 64 bf16 (both halves) or 32 fp32 (one half)
-          constexpr int kHalves = sizeof(T) == 2 ? 2 : 1;
-          uint8_t* st = stage0 + buf * 4096;
-          if (kHalves == 1 || h == 0) {
-            if (p.tma_out && lane == 0) bulk_wait_read_but_one();
-            __syncwarp();
-          }
-          constexpr int kPer = 16 / sizeof(T);
+          const int q = q0 + 32 * h;
+          if constexpr (SWAP) {
+            // out[q][p]: lanes hold consecutive columns of one output row
+            if (p.tma_out) {
+              if (q >= rowsQ) continue;
+              T* st = reinterpret_cast<T*>(stage0 + buf * 4096);
+              if (lane == 0) bulk_wait_read_but_one();
+              __syncwarp();
 #pragma unroll
-          for (int q = 0; q < 32 / kPer; ++q) put_chunk<T>(st, lane, (kHalves == 2 ? h * 4 : 0) + q, v + q * kPer);
-          if (kHalves == 2 && h == 0) continue;
-          const int nn = n + (kHalves == 2 ? 0 : 32 * h);
-          if (p.tma_out) {
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              if (nn < p.N) tma_store_2d(&tmO, smem_u32(st), nn, row0);
-              bulk_commit();
+              for (int c = 0; c < 32; ++c) st[c * 32 + lane] = T(v[c]);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                tma_store_2d(&tmO, smem_u32(st), row0, q);
+                bulk_commit();
+              }
+              buf ^= 1;
+            } else if (row < rowsP) {
+              T* o = static_cast<T*>(p.out) + (long long)q * p.ldo + row;
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (q + c < rowsQ) o[c * p.ldo] = T(v[c]);
             }
-            buf ^= 1;
           } else {
-            __syncwarp();
-            T* o = static_cast<T*>(p.out) + (long long)row0 * p.ldo + nn;
-            const int rows = min(32, p.M - row0);
-            for (int r = 0; r < rows; ++r)
+            // a 4 KB staging tile: 32 rows of 64 bf16 (both halves) or 32 fp32 (one half)
+            constexpr int kHalves = sizeof(T) == 2 ? 2 : 1;
+            uint8_t* st = stage0 + buf * 4096;
+            if (kHalves == 1 || h == 0) {
+              if (p.tma_out && lane == 0) bulk_wait_read_but_one();
+              __syncwarp();
+            }
+            constexpr int kPer = 16 / sizeof(T);
 #pragma unroll
-              for (int c = lane; c < int(128 / sizeof(T)); c += 32)
-                if (nn + c < p.N)
-                  o[r * p.ldo + c] = *reinterpret_cast<const T*>(st + sw128_offset(r, c * sizeof(T) / 16) + c * sizeof(T) % 16);
+            for (int i = 0; i < 32 / kPer; ++i) put_chunk<T>(st, lane, (kHalves == 2 ? h * 4 : 0) + i, v + i * kPer);
+            if (kHalves == 2 && h == 0) continue;
+            const int n = kHalves == 2 ? q0 : q;
+            if (p.tma_out) {
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                if (n < rowsQ) tma_store_2d(&tmO, smem_u32(st), n, row0);
+                bulk_commit();
+              }
+              buf ^= 1;
+            } else {
+              __syncwarp();
+              T* o = static_cast<T*>(p.out) + (long long)row0 * p.ldo + n;
+              const int rows = min(32, rowsP - row0);
+              for (int r = 0; r < rows; ++r)
+#pragma unroll
+                for (int c = lane; c < int(128 / sizeof(T)); c += 32)
+                  if (n + c < rowsQ)
+                    o[r * p.ldo + c] = *reinterpret_cast<const T*>(st + sw128_offset(r, c * sizeof(T) / 16) + c * sizeof(T) % 16);
+            }
           }
         }
       }
@@ -293,7 +375,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 // ---------------------------------------------------------------------------------------------
 constexpr int kSplitThreads = 192;
 constexpr uint32_t kSplitMinSmem = 116 * 1024;
-constexpr uint32_t split_stage_bytes(int bn, uint32_t sf) { return kTileBytes + uint32_t(bn) * 128 + 2 * sf; }
+__host__ __device__ constexpr uint32_t split_stage_bytes(int bn, uint32_t sf) { return kTileBytes + uint32_t(bn) * 128 + 2 * sf; }
 
 template <int FMT, typename T>
 __global__ void __launch_bounds__(kSplitThreads, 1)
@@ -331,6 +413,16 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
     tma_prefetch_desc(&tmSA);
     tma_prefetch_desc(&tmSB);
   }
+  auto load_b = [&](int stage, int kb) {
+    const uint32_t fb = smem_u32(&full[stage]);
+    mbar_arrive_expect_tx(fb, kTileBytes + aBytes + 2 * SC::kBytes);
+    tma_load_2d(smem_u32(sB + stage * kTileBytes), &tmB, fb, kb * 128, n0);
+    tma_load_3d(smem_u32(sSB + stage * SC::kBytes), &tmSB, fb, 0, kb * SC::kGroups, n0 >> 7);
+  };
+  // B's part of the first stages does not wait for the kernel that writes A
+  const int ahead = p.early ? min(S, k1 - k0) : 0;
+  if (threadIdx.x == 0)
+    for (int s = 0; s < ahead; ++s) load_b(s, k0 + s);
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), cols);
     tmem_relinquish();
@@ -347,11 +439,11 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
       int stage = 0;
       uint32_t phase = 0, issued = 0, parity = 0;
       for (int kb = k0; kb < k1; ++kb) {
-        if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1, p.err, kErrTimeoutProducer)) break;
+        if (kb - k0 >= ahead) {
+          if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1, p.err, kErrTimeoutProducer)) break;
+          load_b(stage, kb);
+        }
         const uint32_t fb = smem_u32(&full[stage]);
-        mbar_arrive_expect_tx(fb, kTileBytes + aBytes + 2 * SC::kBytes);
-        tma_load_2d(smem_u32(sB + stage * kTileBytes), &tmB, fb, kb * 128, n0);
-        tma_load_3d(smem_u32(sSB + stage * SC::kBytes), &tmSB, fb, 0, kb * SC::kGroups, n0 >> 7);
         tma_load_2d(smem_u32(sA + stage * aBytes), &tmA, fb, kb * 128, m0);
         tma_load_3d(smem_u32(sSA + stage * SC::kBytes), &tmSA, fb, 0, kb * SC::kGroups, m0 >> 7);
         issued |= 1u << stage;
@@ -432,24 +524,38 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
     cluster_barrier();
     const int live = min(bn, p.M - m0);
     const uint32_t base = smem_u32(tile);
-    // four rows of B per thread, 32 threads to a column
-    for (int i = part * kSplitThreads + int(threadIdx.x); i < live * 32; i += parts * kSplitThreads) {
-      const int c = i >> 5, r4 = (i & 31) * 4;
-      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int q = 0; q < parts; ++q) {
-        const float4 v = ld_shared_cluster_v4(mapa_shared(base + uint32_t(c * 128 + r4) * 4, uint32_t(q)));
-        s.x += v.x;
-        s.y += v.y;
-        s.z += v.z;
-        s.w += v.w;
-      }
-      const float* sv = &s.x;
-      const int m = m0 + c;
-      const float ra = SC::kNv ? __ldg(p.a_scale + m) : 1.f;
+    // four rows of B per thread, 32 threads to a column; all parts of two columns in flight together
+    constexpr int kMaxParts = 8;
+    const int step = parts * kSplitThreads;
+    for (int i0 = part * kSplitThreads + int(threadIdx.x); i0 < live * 32; i0 += 2 * step) {
+      float4 v[2][kMaxParts];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int nn = n0 + r4 + e;
-        if (nn < p.N) out[m * p.ldo + nn] = T(SC::kNv ? sv[e] * ra * __ldg(p.b_scale + nn) : sv[e]);
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int q = 0; q < kMaxParts; ++q)
+          if (q < parts && i0 + u * step < live * 32)
+            v[u][q] = ld_shared_cluster_v4(mapa_shared(base + uint32_t(i0 + u * step) * 16u, uint32_t(q)));
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int i = i0 + u * step;
+        if (i >= live * 32) continue;
+        float4 s = v[u][0];
+#pragma unroll
+        for (int q = 1; q < kMaxParts; ++q)
+          if (q < parts) {
+            s.x += v[u][q].x;
+            s.y += v[u][q].y;
+            s.z += v[u][q].z;
+            s.w += v[u][q].w;
+          }
+        const float* sv = &s.x;
+        const int m = m0 + (i >> 5), r4 = (i & 31) * 4;
+        const float ra = SC::kNv ? __ldg(p.a_scale + m) : 1.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int nn = n0 + r4 + e;
+          if (nn < p.N) out[m * p.ldo + nn] = T(SC::kNv ? sv[e] * ra * __ldg(p.b_scale + nn) : sv[e]);
+        }
       }
     }
     cluster_barrier();  // no CTA leaves while another reads its shared memory
@@ -470,27 +576,30 @@ bool tmap_sf(CUtensorMap* m, const dit_fp4_matrix& x, int box_groups, int box_ba
   return make_tmap_scales(m, x.scales, fp4_groups(x.format, x.cols), (x.rows + 127) / 128, box_groups, box_bands);
 }
 
-template <int FMT, typename T>
-int launch_pair(const dit_fp4_matrix& a, const dit_fp4_matrix& b, Fp4Params p, cudaStream_t st) {
-  using Cfg = PairCfg<FMT>;
-  static_assert(Cfg::kSmem <= 227 * 1024, "shared memory budget");
-  CUtensorMap ma, mb, msa, msb, mo;
+template <int FMT, typename T, bool SWAP>
+int launch_pair(const dit_fp4_matrix& a, const dit_fp4_matrix& b, Fp4Params p, int bn, cudaStream_t st) {
+  const dit_fp4_matrix &P = SWAP ? b : a, &Q = SWAP ? a : b;
+  CUtensorMap mp, mq, msp, msq, mo;
   constexpr int G = Scales<FMT>::kGroups;
-  if (!tmap_codes(&ma, a.codes, a.rows, p.K, 128) || !tmap_codes(&mb, b.codes, b.rows, p.K, 128) ||
-      !tmap_sf(&msa, a, G, 1) || !tmap_sf(&msb, b, G, 2))
+  p.bn = bn;
+  p.stages = std::min(kMaxStages, int((227 * 1024 - kPairFixed) / pair_stage_bytes<FMT>(bn)));
+  const uint32_t smem = kPairFixed + uint32_t(p.stages) * pair_stage_bytes<FMT>(bn);
+  if (!tmap_codes(&mp, P.codes, P.rows, p.K, 128) || !tmap_codes(&mq, Q.codes, Q.rows, p.K, bn / 2) ||
+      !tmap_sf(&msp, P, G, 1) || !tmap_sf(&msq, Q, G, 2))
     return DIT_ECUDA;
   p.tma_out = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && p.ldo * (long long)sizeof(T) % 16 == 0;
-  mo = ma;
+  mo = mp;
   if (p.tma_out && !make_tmap_2d(&mo, p.out, sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
-                                 sizeof(T), p.N, p.M, p.ldo * (long long)sizeof(T), 128 / sizeof(T), 32, true))
+                                 sizeof(T), p.N, p.M, p.ldo * (long long)sizeof(T), SWAP ? 32 : 128 / int(sizeof(T)), 32,
+                                 !SWAP))
     return DIT_ECUDA;
-  p.n_fast = p.M > p.N;  // consecutive tiles share the smaller operand's rows, which stay in L2
-  auto kern = fp4_pair_kernel<FMT, T>;
-  if (!smem_attr_once(reinterpret_cast<const void*>(kern), Cfg::kSmem)) return DIT_ECUDA;
-  const int tiles = ((p.M + 255) / 256) * ((p.N + 255) / 256);
-  const int units = std::min(tiles, num_sms() / 2);
-  const cudaError_t e = launch_pdl(kern, dim3(unsigned(2 * units)), dim3(kPairThreads), Cfg::kSmem, st, 2, ma, mb, msa,
-                                   msb, mo, p);
+  p.n_fast = P.rows > Q.rows;  // consecutive tiles share the smaller operand's rows, which stay in L2
+  auto kern = fp4_pair_kernel<FMT, T, SWAP>;
+  if (!smem_attr_once(reinterpret_cast<const void*>(kern), 227 * 1024)) return DIT_ECUDA;
+  const long long tiles = (long long)((P.rows + 255) / 256) * ((Q.rows + bn - 1) / bn);
+  if (tiles > 0x7fffffffLL - num_sms()) return DIT_EUNSUPPORTED;
+  const int units = int(std::min<long long>(tiles, num_sms() / 2));
+  const cudaError_t e = launch_pdl(kern, dim3(unsigned(2 * units)), dim3(kPairThreads), smem, st, 2, mp, mq, msp, msq, mo, p);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? DIT_OK : DIT_ECUDA;
 }
 
@@ -524,13 +633,30 @@ int launch_split(const dit_fp4_matrix& a, const dit_fp4_matrix& b, Fp4Params p, 
 template <int FMT, typename T>
 int launch_product(const dit_fp4_matrix& a, const dit_fp4_matrix& b, const Fp4Params& p, cudaStream_t st) {
   const long long tiles = (long long)((p.M + 255) / 256) * ((p.N + 255) / 256);
-  return p.M <= 128 || tiles < 24 ? launch_split<FMT, T>(a, b, p, st) : launch_pair<FMT, T>(a, b, p, st);
+  if (p.M <= 128 || tiles < 24) return launch_split<FMT, T>(a, b, p, st);
+  // rows of P and of Q per tile, in rounds over the CTA pairs: the shape with the least work on the
+  // longest path
+  const int units = num_sms() / 2;
+  long long best = -1;
+  int bn = 256;
+  bool swap = false;
+  for (int s = 0; s < 2; ++s)
+    for (int n : {256, 192, 128}) {
+      const long long P = s ? p.N : p.M, Q = s ? p.M : p.N;
+      const long long t = (P + 255) / 256 * ((Q + n - 1) / n), cost = (t + units - 1) / units * (n + 32);
+      if (best < 0 || cost < best) {
+        best = cost;
+        bn = n;
+        swap = s != 0;
+      }
+    }
+  return swap ? launch_pair<FMT, T, true>(a, b, p, bn, st) : launch_pair<FMT, T, false>(a, b, p, bn, st);
 }
 
 }  // namespace
 
 int fp4_matmul_launch(const dit_fp4_matrix& a, const dit_fp4_matrix& b, void* out, int type, long long ldo, int* err,
-                      cudaStream_t st) {
+                      bool b_early, cudaStream_t st) {
   Fp4Params p{};
   p.M = a.rows;
   p.N = b.rows;
@@ -540,6 +666,7 @@ int fp4_matmul_launch(const dit_fp4_matrix& a, const dit_fp4_matrix& b, void* ou
   p.ldo = ldo;
   p.a_scale = a.row_scale;
   p.b_scale = b.row_scale;
+  p.early = b_early;
   if (a.format == DIT_FP4_NV)
     return type == DIT_BF16 ? launch_product<DIT_FP4_NV, __nv_bfloat16>(a, b, p, st)
                             : launch_product<DIT_FP4_NV, float>(a, b, p, st);

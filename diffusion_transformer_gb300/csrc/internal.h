@@ -201,11 +201,14 @@ int quant_weight_launch(const uint16_t* w, int N, int K, const float* smooth, in
                         cudaStream_t stream);
 int codes_bf16_launch(const int8_t* q, uint16_t* w, long long n, cudaStream_t stream);
 
-// Microscaled 4-bit matrices (see dit_fp4_quantize and the calls after it), on validated arguments
+// Microscaled 4-bit matrices (see dit_fp4_quantize and the calls after it), on validated arguments.
+// b_early: the kernel enqueued just before the product does not write b and itself called pdl_wait before
+// pdl_trigger (as every kernel here does), so b was complete when the product's launch began; its loads
+// may then run ahead of that kernel's end.
 int fp4_quantize_launch(const void* x, int type, long long ldx, const dit_fp4_matrix& m, cudaStream_t stream);
 int fp4_dequantize_launch(const dit_fp4_matrix& m, void* out, int type, long long ldo, cudaStream_t stream);
 int fp4_matmul_launch(const dit_fp4_matrix& a, const dit_fp4_matrix& b, void* out, int type, long long ldo, int* err,
-                      cudaStream_t stream);
+                      bool b_early, cudaStream_t stream);
 
 int num_sms();
 

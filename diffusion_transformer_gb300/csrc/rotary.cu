@@ -38,8 +38,8 @@ struct RotArgs {
   int rows;            // rows per batch entry
   long long total;     // batch * rows
   int rows_per_cta;
-  int units;           // units of a head
-  int step_unit, step_head, step_row;  // kRotThreads units further, as (unit, head, row)
+  int units, row_units;  // units of a head, of a row
+  int groups;            // rows taken at a time (1 where a row has more units than the CTA threads)
   int inverse;
   const int32_t* pos;
   dit_rotary_plan plan;
@@ -110,15 +110,16 @@ __device__ __forceinline__ Raw<T, VE> rot_raw(const float (&v)[VE]) {
 // VE = 1), VE values of the first half and their VE partners in the second, or VE values that pass
 // unturned. VE = 16 bytes' worth of values where every row and head starts on 16 bytes and the rotated
 // part ends on such a boundary, else 1.
-// A CTA takes the units of rows_per_cta rows, all heads of q and then of k, kRotThreads at a time in
-// memory order; (unit, head, row) advance by a fixed mixed-radix step, so no thread divides in the loop.
-// The first loads are issued before the CTA works out its cosines and sines.
+// A CTA takes rows_per_cta rows. A thread keeps one unit of one head (of q or k) through the rows, so its
+// addresses inside a row are worked out once; it then goes on to its next unit. Rows with fewer units
+// than threads are taken several at a time. kRotUnroll rows are loaded before the first is turned, and
+// the first of them before the CTA works out its cosines and sines.
 template <typename T, int VE, bool HALVES>
-__global__ void __launch_bounds__(kRotThreads, 3) rotary_kernel(const __grid_constant__ RotArgs a) {
+__global__ void __launch_bounds__(kRotThreads, HALVES && VE > 1 ? 3 : 4) rotary_kernel(const __grid_constant__ RotArgs a) {
   constexpr bool kTwo = HALVES || VE == 1;                     // a turned unit is two accesses
   constexpr int kTurn = HALVES ? VE : (VE == 1 ? 1 : VE / 2);  // pairs per turned unit
   using R = Raw<T, VE>;
-  extern __shared__ float2 cs[];  // [rows_per_cta][pairs]
+  extern __shared__ float2 cs[];              // [rows_per_cta][pairs]
   __shared__ long long base[kRotMaxRows][4];  // x and out of q, x and out of k at each row
   const int pairs = a.plan.pairs;
   const long long row0 = (long long)blockIdx.x * a.rows_per_cta;
@@ -135,56 +136,62 @@ __global__ void __launch_bounds__(kRotThreads, 3) rotary_kernel(const __grid_con
   pdl_wait();
   pdl_trigger();
   const int turned = pairs / kTurn;
-  int unit = int(threadIdx.x) % a.units, h = int(threadIdx.x) / a.units, rr = h / a.heads;
-  h -= rr * a.heads;
   bool first = true;
+  const int group = int(threadIdx.x) / a.row_units;  // rows taken at a time when a row has few units
+  int i = int(threadIdx.x) - group * a.row_units;    // the unit among the row's
+  if (group >= a.groups) i = a.row_units;            // threads left over
   do {  // every thread makes the first turn, for the barrier in it
-    R v[kRotUnroll][kTwo ? 2 : 1];
-    T* dst[kRotUnroll];
-    const float2* c[kRotUnroll];  // the unit's angles, null: passes unturned
+    const int hh = i / a.units, unit = i - hh * a.units;
+    const int z = hh >= a.q_heads, h = z ? hh - a.q_heads : hh;
+    const bool turn = unit < turned, live = i < a.row_units && (turn || a.copy[z]);
+    const int off = turn ? (HALVES ? unit * VE : unit * 2 * kTurn) : 2 * pairs + (unit - turned) * VE;
+    const T* x = static_cast<const T*>(a.x[z]) + h * a.xh[z] + off;
+    T* out = static_cast<T*>(a.out[z]) + h * a.oh[z] + off;
+    int rr = group;
+    do {
+      R v[kRotUnroll][kTwo ? 2 : 1];
 #pragma unroll
-    for (int u = 0; u < kRotUnroll; ++u) {
-      dst[u] = nullptr;
-      if (rr < nrows) {
-        const int z = h >= a.q_heads, hz = z ? h - a.q_heads : h;
-        const bool turn = unit < turned;
-        if (turn || a.copy[z]) {
-          const int off = turn ? (HALVES ? unit * VE : unit * 2 * kTurn) : 2 * pairs + (unit - turned) * VE;
-          const T* src = static_cast<const T*>(a.x[z]) + base[rr][2 * z] + hz * a.xh[z] + off;
-          dst[u] = static_cast<T*>(a.out[z]) + base[rr][2 * z + 1] + hz * a.oh[z] + off;
-          c[u] = turn ? cs + rr * pairs + unit * kTurn : nullptr;
+      for (int u = 0; u < kRotUnroll; ++u) {
+        const int r = rr + u * a.groups;
+        if (live && r < nrows) {
+          const T* src = x + base[r][2 * z];
           v[u][0] = rot_load<T, VE>(src);
           if constexpr (kTwo)
             if (turn) v[u][1] = rot_load<T, VE>(src + (HALVES ? pairs : 1));
         }
-        unit += a.step_unit;
-        h += a.step_head;
-        rr += a.step_row;
-        if (unit >= a.units) {
-          unit -= a.units;
-          ++h;
-        }
-        if (h >= a.heads) {
-          h -= a.heads;
-          ++rr;
-        }
       }
-    }
-    if (first) {
-      for (int i = threadIdx.x; i < nrows * pairs; i += kRotThreads) {
-        const int r = i / pairs, k = i - r * pairs;
-        const int32_t p = __ldg(a.pos + (row0 + r) * a.plan.axes + a.plan.axis[k]);
-        float2 t = rot_cos_sin(p, a.plan.turns[k], a.plan.amplitude);
-        if (a.inverse) t.y = -t.y;
-        cs[i] = t;
+      if (first) {
+        for (int k = threadIdx.x; k < nrows * pairs; k += kRotThreads) {
+          const int r = k / pairs, f = k - r * pairs;
+          const int32_t p = __ldg(a.pos + (row0 + r) * a.plan.axes + a.plan.axis[f]);
+          float2 t = rot_cos_sin(p, a.plan.turns[f], a.plan.amplitude);
+          if (a.inverse) t.y = -t.y;
+          cs[k] = t;
+        }
+        __syncthreads();
+        first = false;
       }
-      __syncthreads();
-      first = false;
-    }
 #pragma unroll
-    for (int u = 0; u < kRotUnroll; ++u) {
-      if (!dst[u]) continue;
-      if (c[u]) {
+      for (int u = 0; u < kRotUnroll; ++u) {
+        const int r = rr + u * a.groups;
+        if (!live || r >= nrows) continue;
+        T* dst = out + base[r][2 * z + 1];
+        if (!turn) {
+          rot_store<T, VE>(dst, v[u][0]);
+          continue;
+        }
+        float2 t[kTurn];
+        if constexpr (kTurn >= 2) {  // pairs and kTurn even: 16 bytes hold two angles
+          const float4* c = reinterpret_cast<const float4*>(cs + r * pairs + unit * kTurn);
+#pragma unroll
+          for (int j = 0; j < kTurn / 2; ++j) {
+            const float4 q = c[j];
+            t[2 * j] = make_float2(q.x, q.y);
+            t[2 * j + 1] = make_float2(q.z, q.w);
+          }
+        } else {
+          t[0] = cs[r * pairs + unit];
+        }
         float x0[VE];
         rot_values<T, VE>(v[u][0], x0);
         if constexpr (kTwo) {
@@ -192,27 +199,25 @@ __global__ void __launch_bounds__(kRotThreads, 3) rotary_kernel(const __grid_con
           rot_values<T, VE>(v[u][1], x1);
 #pragma unroll
           for (int j = 0; j < VE; ++j) {
-            const float2 t = c[u][j];
-            y0[j] = x0[j] * t.x - x1[j] * t.y;
-            y1[j] = x0[j] * t.y + x1[j] * t.x;
+            y0[j] = x0[j] * t[j].x - x1[j] * t[j].y;
+            y1[j] = x0[j] * t[j].y + x1[j] * t[j].x;
           }
-          rot_store<T, VE>(dst[u], rot_raw<T, VE>(y0));
-          rot_store<T, VE>(dst[u] + (HALVES ? pairs : 1), rot_raw<T, VE>(y1));
+          rot_store<T, VE>(dst, rot_raw<T, VE>(y0));
+          rot_store<T, VE>(dst + (HALVES ? pairs : 1), rot_raw<T, VE>(y1));
         } else {
           float y[VE];
 #pragma unroll
           for (int j = 0; j < kTurn; ++j) {
-            const float2 t = c[u][j];
-            y[2 * j] = x0[2 * j] * t.x - x0[2 * j + 1] * t.y;
-            y[2 * j + 1] = x0[2 * j] * t.y + x0[2 * j + 1] * t.x;
+            y[2 * j] = x0[2 * j] * t[j].x - x0[2 * j + 1] * t[j].y;
+            y[2 * j + 1] = x0[2 * j] * t[j].y + x0[2 * j + 1] * t[j].x;
           }
-          rot_store<T, VE>(dst[u], rot_raw<T, VE>(y));
+          rot_store<T, VE>(dst, rot_raw<T, VE>(y));
         }
-      } else {
-        rot_store<T, VE>(dst[u], v[u][0]);
       }
-    }
-  } while (rr < nrows);
+      rr += kRotUnroll * a.groups;
+    } while (rr < nrows);
+    i += kRotThreads;
+  } while (i < a.row_units);
 }
 
 __global__ void __launch_bounds__(kRotThreads) rotary_tables_kernel(const __grid_constant__ dit_rotary_plan plan,
@@ -364,12 +369,14 @@ int dit_rotary(const dit_rotary_plan* plan, const dit_rotary_rows* q, const dit_
   const int v = vec ? ve : 1;
   const int turned = plan->pairs / (plan->layout == DIT_ROTARY_HALVES ? v : (v == 1 ? 1 : v / 2));
   a.units = turned + (head_dim - 2 * plan->pairs) / v;
-  a.step_unit = kRotThreads % a.units;
-  a.step_head = kRotThreads / a.units % a.heads;
-  a.step_row = kRotThreads / a.units / a.heads;
-  // Two rounds of kRotUnroll units per thread, while there are CTAs for every SM several times over.
   const long long row_units = (long long)a.units * a.heads;
-  long long per = std::min<long long>(kRotMaxRows, 2LL * kRotThreads * kRotUnroll / row_units);
+  if (row_units > 0x7fffffffLL - kRotThreads) return DIT_EUNSUPPORTED;
+  a.row_units = int(row_units);
+  a.groups = std::max(1, kRotThreads / a.row_units);
+  // A round of kRotUnroll rows per thread and two units, while there are CTAs for every SM several times
+  // over.
+  long long per = std::max<long long>(kRotUnroll * a.groups, 2LL * kRotThreads * kRotUnroll / row_units);
+  per = std::min<long long>(per, kRotMaxRows);
   per = std::max(1LL, std::min(per, a.total / (4LL * num_sms())));
   a.rows_per_cta = int(per);
   const long long ctas = (a.total + per - 1) / per;
