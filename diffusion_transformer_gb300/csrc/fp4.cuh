@@ -92,8 +92,7 @@ __device__ __forceinline__ uint2 fp4_codes16(const float* v, float inv) {
   const uint64_t i2 = f2_pack(inv, inv);
   uint64_t y[2][4];
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(y[j >> 2][j & 3]) : "l"(f2_pack(v[2 * j], v[2 * j + 1])), "l"(i2));
+  for (int j = 0; j < 8; ++j) y[j >> 2][j & 3] = f2_mul(f2_pack(v[2 * j], v[2 * j + 1]), i2);
   const uint2 w = make_uint2(fp4_codes8(y[0]), fp4_codes8(y[1]));
   return inv != 0.f ? w : make_uint2(0u, 0u);
 }

@@ -41,7 +41,6 @@ struct Fp4Params {
   const float* a_scale;  // NV: row scales
   const float* b_scale;
   int early;             // B was complete before the kernel ahead of this one in the stream began
-  int tma_out;           // rows of `out` start on 16 bytes: tiles leave through TMA stores
   int n_fast;            // tile order
   int bn, stages;        // rows of the narrow operand per tile (see each kernel), pipeline depth
 };
@@ -58,43 +57,30 @@ __device__ __forceinline__ int stage_steps(int K, int kb) { return min(4, (K - k
 // accumulators overlap by 48 columns ([0, 256) and [208, 464)): the overlapped columns are drained first
 // and then handed over, so the next tile's MMAs wait for a quarter of an epilogue, not for all of it.
 constexpr int kOverlapAt = 208, kSfCol = 464, kMaxStages = 8;
-constexpr int kPairThreads = 192;
-constexpr uint32_t kStaging = 4 * 2 * 4096;                                   // two 4 KB output tiles per epilogue warp
-constexpr uint32_t kPairFixed = 1024 + kStaging + 4 * 256 + 8 * (2 * kMaxStages + 5) + 16;
+constexpr int kEpiWarps = 8, kPairThreads = 64 + 32 * kEpiWarps;
+constexpr uint32_t kPairFixed = 1024 + kEpiWarps * 256 + 8 * (2 * kMaxStages + 5) + 16;
 
 template <int FMT>
 __host__ __device__ constexpr uint32_t pair_stage_bytes(int bn) {
   return kTileBytes + uint32_t(bn) * 64 + 3 * Scales<FMT>::kBytes;
 }
 
-// 16 bytes of the staging row `lane`, rows of 128 bytes swizzled as the TMA store expects
-template <typename T>
-__device__ __forceinline__ void put_chunk(uint8_t* tile, int lane, int q, const float* v) {
-  uint4 u;
-  if constexpr (sizeof(T) == 2)
-    u = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-  else
-    u = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-  *reinterpret_cast<uint4*>(tile + sw128_offset(lane, q)) = u;
-}
-
 template <int FMT, typename T, bool SWAP>
 __global__ void __launch_bounds__(kPairThreads, 1)
     fp4_pair_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
                     const __grid_constant__ CUtensorMap tmSP, const __grid_constant__ CUtensorMap tmSQ,
-                    const __grid_constant__ CUtensorMap tmO, const Fp4Params p) {
+                    const Fp4Params p) {
   using SC = Scales<FMT>;
   const int S = p.stages, bn = p.bn;
   const uint32_t qBytes = uint32_t(bn) * 64;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sE = smem;  // output staging first: its tiles, and the operands' after it, on 1024 bytes
-  uint8_t* sP = sE + kStaging;
+  uint8_t* sP = smem;
   uint8_t* sQ = sP + S * kTileBytes;
   uint8_t* sSP = sQ + S * qBytes;
   uint8_t* sSQ = sSP + S * SC::kBytes;
   float* sC = reinterpret_cast<float*>(sSQ + S * 2 * SC::kBytes);  // 64 column factors per epilogue warp
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sC + 4 * 64);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sC + kEpiWarps * 64);
   uint64_t *full = bars, *empty = bars + S, *tfull = bars + 2 * S, *tempty = tfull + 2, *drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
 
@@ -117,7 +103,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(smem_u32(&tfull[a]), 1);
-      mbar_init(smem_u32(&tempty[a]), 2 * 128);  // both CTAs' epilogue threads
+      mbar_init(smem_u32(&tempty[a]), 2 * 32 * kEpiWarps);  // both CTAs' epilogue threads
     }
     mbar_init(smem_u32(drain), 1);
     fence_mbar_init();
@@ -244,13 +230,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       mbar_wait(smem_u32(drain), 0, p.err, kErrTimeoutDrain);
     }
   } else {
-    const int quad = warp & 3, groups = bn / 64;
-    uint8_t* stage0 = sE + (warp - 2) * 8192;
+    // two warps to each quadrant of 32 lanes, taking its 64-column groups in turn
+    const int quad = warp & 3, half = (warp - 2) >> 2, groups = bn / 64;
     float* cf = sC + (warp - 2) * 64;
     const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
     const float* p_scale = SWAP ? p.b_scale : p.a_scale;
     const float* q_scale = SWAP ? p.a_scale : p.b_scale;
-    int it = 0, buf = 0;
+    int it = 0;
     for (int tile = unit; tile < tiles; tile += units, ++it) {
       int pb, qb;
       tile_pq(tile, pb, qb);
@@ -266,13 +252,16 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       };
       if constexpr (SC::kNv) {
         rp = row < rowsP ? __ldg(p_scale + row) : 0.f;
-        fetch(0);
+        fetch(half);
       }
       if (!mbar_wait_warp(smem_u32(&tfull[acc]), uint32_t(it >> 1) & 1u, p.err, kErrTimeoutEpilogue)) break;
       tc_fence_after();
       const uint32_t taddr = tmem + (uint32_t(quad * 32) << 16) + (acc ? acc1 : 0);
+      // what this warp holds back from the next tile: nothing of the overlapped columns (group 0), or
+      // nothing at all
+      if (overlap && half == 1) mbar_arrive_cluster(tempty0 + uint32_t(acc) * 8u);
 #pragma unroll 1
-      for (int j = 0; j < groups; ++j) {
+      for (int j = half; j < groups; j += 2) {
         const int g = group_at(j), q0 = qb * bn + g * 64;
         uint32_t w[2][32];
         tmem_ld32(taddr + g * 64, w[0]);
@@ -281,87 +270,64 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           __syncwarp();
           cf[lane] = f0;
           cf[lane + 32] = f1;
-          if (j + 1 < groups) fetch(j + 1);
+          if (j + 2 < groups) fetch(j + 2);
           __syncwarp();
         }
         tmem_ld_wait();
-        if (j == (overlap ? 0 : groups - 1)) {
+        if (overlap ? j == 0 : j + 2 >= groups) {
           tc_fence_before();
           mbar_arrive_cluster(tempty0 + uint32_t(acc) * 8u);
         }
         if (q0 >= rowsQ || row0 >= rowsP) continue;
+        if constexpr (SC::kNv) {
+          const uint64_t rp2 = f2_pack(rp, rp);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float v[32];
+          for (int c = 0; c < 64; c += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(cf + c);
+            uint32_t* x = w[c >> 5] + (c & 31);
+            const uint64_t lo = f2_mul(f2_mul(f2_pack(__uint_as_float(x[0]), __uint_as_float(x[1])), rp2), f2_pack(f.x, f.y));
+            const uint64_t hi = f2_mul(f2_mul(f2_pack(__uint_as_float(x[2]), __uint_as_float(x[3])), rp2), f2_pack(f.z, f.w));
+            x[0] = uint32_t(lo);
+            x[1] = uint32_t(lo >> 32);
+            x[2] = uint32_t(hi);
+            x[3] = uint32_t(hi >> 32);
+          }
+        }
+        auto val = [&](int c) { return __uint_as_float(w[c >> 5][c & 31]); };
+        if constexpr (SWAP) {
+          // out[q][p]: the lanes hold 32 consecutive values of each output row
+          if (row < rowsP) {
+            T* o = static_cast<T*>(p.out) + (long long)q0 * p.ldo + row;
+            if (q0 + 64 <= rowsQ) {
 #pragma unroll
-          for (int c = 0; c < 32; c += 4) {
-            const float4 f = SC::kNv ? *reinterpret_cast<const float4*>(cf + 32 * h + c) : make_float4(1.f, 1.f, 1.f, 1.f);
-            const float* ff = &f.x;
+              for (int c = 0; c < 64; ++c) o[c * p.ldo] = T(val(c));
+            } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float x = __uint_as_float(w[h][c + e]);
-              v[c + e] = SC::kNv ? x * rp * ff[e] : x;
+              for (int c = 0; c < 64; ++c)
+                if (q0 + c < rowsQ) o[c * p.ldo] = T(val(c));
             }
           }
-          const int q = q0 + 32 * h;
-          if constexpr (SWAP) {
-            // out[q][p]: lanes hold consecutive columns of one output row
-            if (p.tma_out) {
-              if (q >= rowsQ) continue;
-              T* st = reinterpret_cast<T*>(stage0 + buf * 4096);
-              if (lane == 0) bulk_wait_read_but_one();
-              __syncwarp();
+        } else if (row < rowsP) {
+          // out[p][q]: a lane holds 64 consecutive values of its row, stored 32 bytes at a time
+          T* o = static_cast<T*>(p.out) + (long long)row * p.ldo + q0;
+          constexpr int kPer = 32 / sizeof(T);
 #pragma unroll
-              for (int c = 0; c < 32; ++c) st[c * 32 + lane] = T(v[c]);
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) {
-                tma_store_2d(&tmO, smem_u32(st), row0, q);
-                bulk_commit();
-              }
-              buf ^= 1;
-            } else if (row < rowsP) {
-              T* o = static_cast<T*>(p.out) + (long long)q * p.ldo + row;
+          for (int c = 0; c < 64; c += kPer) {
+            if (q0 + c + kPer <= rowsQ) {
+              uint32_t u[8];
 #pragma unroll
-              for (int c = 0; c < 32; ++c)
-                if (q + c < rowsQ) o[c * p.ldo] = T(v[c]);
-            }
-          } else {
-            // a 4 KB staging tile: 32 rows of 64 bf16 (both halves) or 32 fp32 (one half)
-            constexpr int kHalves = sizeof(T) == 2 ? 2 : 1;
-            uint8_t* st = stage0 + buf * 4096;
-            if (kHalves == 1 || h == 0) {
-              if (p.tma_out && lane == 0) bulk_wait_read_but_one();
-              __syncwarp();
-            }
-            constexpr int kPer = 16 / sizeof(T);
-#pragma unroll
-            for (int i = 0; i < 32 / kPer; ++i) put_chunk<T>(st, lane, (kHalves == 2 ? h * 4 : 0) + i, v + i * kPer);
-            if (kHalves == 2 && h == 0) continue;
-            const int n = kHalves == 2 ? q0 : q;
-            if (p.tma_out) {
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) {
-                if (n < rowsQ) tma_store_2d(&tmO, smem_u32(st), n, row0);
-                bulk_commit();
-              }
-              buf ^= 1;
+              for (int e = 0; e < 8; ++e)
+                u[e] = sizeof(T) == 2 ? pack_bf16x2(val(c + 2 * e), val(c + 2 * e + 1)) : w[(c + e) >> 5][(c + e) & 31];
+              st_global_256(o + c, u);
             } else {
-              __syncwarp();
-              T* o = static_cast<T*>(p.out) + (long long)row0 * p.ldo + n;
-              const int rows = min(32, rowsP - row0);
-              for (int r = 0; r < rows; ++r)
 #pragma unroll
-                for (int c = lane; c < int(128 / sizeof(T)); c += 32)
-                  if (n + c < rowsQ)
-                    o[r * p.ldo + c] = *reinterpret_cast<const T*>(st + sw128_offset(r, c * sizeof(T) / 16) + c * sizeof(T) % 16);
+              for (int e = 0; e < kPer; ++e)
+                if (q0 + c + e < rowsQ) o[c + e] = T(val(c + e));
             }
           }
         }
       }
     }
-    if (p.tma_out && lane == 0) bulk_wait_all();
   }
   tc_fence_before();
   __syncthreads();
@@ -579,7 +545,7 @@ bool tmap_sf(CUtensorMap* m, const dit_fp4_matrix& x, int box_groups, int box_ba
 template <int FMT, typename T, bool SWAP>
 int launch_pair(const dit_fp4_matrix& a, const dit_fp4_matrix& b, Fp4Params p, int bn, cudaStream_t st) {
   const dit_fp4_matrix &P = SWAP ? b : a, &Q = SWAP ? a : b;
-  CUtensorMap mp, mq, msp, msq, mo;
+  CUtensorMap mp, mq, msp, msq;
   constexpr int G = Scales<FMT>::kGroups;
   p.bn = bn;
   p.stages = std::min(kMaxStages, int((227 * 1024 - kPairFixed) / pair_stage_bytes<FMT>(bn)));
@@ -587,19 +553,13 @@ int launch_pair(const dit_fp4_matrix& a, const dit_fp4_matrix& b, Fp4Params p, i
   if (!tmap_codes(&mp, P.codes, P.rows, p.K, 128) || !tmap_codes(&mq, Q.codes, Q.rows, p.K, bn / 2) ||
       !tmap_sf(&msp, P, G, 1) || !tmap_sf(&msq, Q, G, 2))
     return DIT_ECUDA;
-  p.tma_out = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && p.ldo * (long long)sizeof(T) % 16 == 0;
-  mo = mp;
-  if (p.tma_out && !make_tmap_2d(&mo, p.out, sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
-                                 sizeof(T), p.N, p.M, p.ldo * (long long)sizeof(T), SWAP ? 32 : 128 / int(sizeof(T)), 32,
-                                 !SWAP))
-    return DIT_ECUDA;
   p.n_fast = P.rows > Q.rows;  // consecutive tiles share the smaller operand's rows, which stay in L2
   auto kern = fp4_pair_kernel<FMT, T, SWAP>;
   if (!smem_attr_once(reinterpret_cast<const void*>(kern), 227 * 1024)) return DIT_ECUDA;
   const long long tiles = (long long)((P.rows + 255) / 256) * ((Q.rows + bn - 1) / bn);
   if (tiles > 0x7fffffffLL - num_sms()) return DIT_EUNSUPPORTED;
   const int units = int(std::min<long long>(tiles, num_sms() / 2));
-  const cudaError_t e = launch_pdl(kern, dim3(unsigned(2 * units)), dim3(kPairThreads), smem, st, 2, mp, mq, msp, msq, mo, p);
+  const cudaError_t e = launch_pdl(kern, dim3(unsigned(2 * units)), dim3(kPairThreads), smem, st, 2, mp, mq, msp, msq, p);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? DIT_OK : DIT_ECUDA;
 }
 
@@ -637,10 +597,12 @@ int launch_product(const dit_fp4_matrix& a, const dit_fp4_matrix& b, const Fp4Pa
   // rows of P and of Q per tile, in rounds over the CTA pairs: the shape with the least work on the
   // longest path
   const int units = num_sms() / 2;
+  // unswapped tiles store 32 bytes of a row at a time
+  const bool rows32 = reinterpret_cast<uintptr_t>(p.out) % 32 == 0 && (p.M == 1 || p.ldo * (long long)sizeof(T) % 32 == 0);
   long long best = -1;
   int bn = 256;
   bool swap = false;
-  for (int s = 0; s < 2; ++s)
+  for (int s = rows32 ? 0 : 1; s < 2; ++s)
     for (int n : {256, 192, 128}) {
       const long long P = s ? p.N : p.M, Q = s ? p.M : p.N;
       const long long t = (P + 255) / 256 * ((Q + n - 1) / n), cost = (t + units - 1) / units * (n + 32);

@@ -374,8 +374,6 @@ __device__ __forceinline__ float4 ld_shared_cluster_v4(uint32_t addr) {
                : "r"(addr));
   return v;
 }
-// All but the last committed bulk group of this thread have read their shared memory.
-__device__ __forceinline__ void bulk_wait_read_but_one() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 
 // ------------------------------------------------------------------------------------------
 // Block-scaled MMA of e2m1 operands: D += sum over blocks of sa sb (codes_a . codes_b), K = 64 per
@@ -514,6 +512,11 @@ __device__ __forceinline__ float f2_hi(uint64_t v) { return __uint_as_float(uint
 __device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t d;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
 __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
