@@ -34,11 +34,14 @@ __host__ __device__ constexpr int fp4_scale_block(int block) { return (block >> 
 struct Fp4Row {
   float u, t, g;
 };
+// Called by a whole warp with one value of `bits`: lanes 0 to 2 make one of the three quotients each.
 __device__ __forceinline__ Fp4Row fp4_row(uint32_t bits) {
   if (bits < 0x0d800000u) return Fp4Row{0.f, 0.f, 0.f};  // 2^-100
   if (bits >= 0x7f800000u) return Fp4Row{0.f, 0.f, __uint_as_float(0x7fc00000u)};
   const float a = __uint_as_float(bits);
-  return Fp4Row{__fdiv_rn(448.f, a), __fdiv_rn(2688.f, a), __fdiv_rn(a, 2688.f)};
+  const int lane = threadIdx.x & 31;
+  const float q = __fdiv_rn(lane == 2 ? a : (lane == 1 ? 2688.f : 448.f), lane == 2 ? 2688.f : a);
+  return Fp4Row{__shfl_sync(0xffffffffu, q, 0), __shfl_sync(0xffffffffu, q, 1), __shfl_sync(0xffffffffu, q, 2)};
 }
 
 struct Fp4Block {

@@ -26,8 +26,12 @@ namespace dit {
 namespace {
 
 constexpr int kRotThreads = 256;
-constexpr int kRotUnroll = 4;    // units in flight per thread
+// rows in flight per thread: two where a row is four 16-byte accesses, which leaves room for five CTAs
+// (two against four: 131 against 146 us on 131072 rows of 10 heads)
+__host__ __device__ constexpr int rot_unroll(bool wide) { return wide ? 2 : 4; }
 constexpr int kRotMaxRows = 32;  // rows per CTA at most
+
+constexpr int kRotPad = 2;
 
 struct RotArgs {
   const void* x[2];
@@ -36,9 +40,8 @@ struct RotArgs {
   int q_heads, heads;  // q's, q's and k's together
   int copy[2];         // values behind the rotated part are copied (not in place)
   int rows;            // rows per batch entry
-  long long total;     // batch * rows
-  int rows_per_cta;
-  int units, row_units;  // units of a head, of a row
+  int rows_per_cta, row_ctas;           // row_ctas CTAs per batch entry
+  int units, turned_units, row_units;  // units of a head, turned units of a row, units of a row
   int groups;            // rows taken at a time (1 where a row has more units than the CTA threads)
   int inverse;
   const int32_t* pos;
@@ -110,87 +113,82 @@ __device__ __forceinline__ Raw<T, VE> rot_raw(const float (&v)[VE]) {
 // VE = 1), VE values of the first half and their VE partners in the second, or VE values that pass
 // unturned. VE = 16 bytes' worth of values where every row and head starts on 16 bytes and the rotated
 // part ends on such a boundary, else 1.
-// A CTA takes rows_per_cta rows. A thread keeps one unit of one head (of q or k) through the rows, so its
-// addresses inside a row are worked out once; it then goes on to its next unit. Rows with fewer units
-// than threads are taken several at a time. kRotUnroll rows are loaded before the first is turned, and
-// the first of them before the CTA works out its cosines and sines.
+// A CTA takes rows_per_cta rows of one batch entry. A thread keeps one unit of one head (of q or k) through
+// the rows, so its addresses are worked out once; it then goes on to its next unit. The turned units of
+// all heads come first and the passing ones after them, so a warp rarely holds both kinds. Rows with fewer
+// units than threads are taken several at a time. A few rows are loaded before the first is turned, and
+// the first of them before the CTA works out its cosines and sines. Those stand in shared memory as
+// [row][angle of a unit][unit], so neighbouring threads read neighbouring 16 bytes.
 template <typename T, int VE, bool HALVES>
-__global__ void __launch_bounds__(kRotThreads, HALVES && VE > 1 ? 3 : 4) rotary_kernel(const __grid_constant__ RotArgs a) {
+__global__ void __launch_bounds__(kRotThreads, HALVES && VE > 1 ? 5 : 4) rotary_kernel(const __grid_constant__ RotArgs a) {
   constexpr bool kTwo = HALVES || VE == 1;                     // a turned unit is two accesses
   constexpr int kTurn = HALVES ? VE : (VE == 1 ? 1 : VE / 2);  // pairs per turned unit
+  constexpr int kU = rot_unroll(HALVES && VE > 1);
+  constexpr int kPack = kTurn > 1 ? 2 : 1;                     // angles per shared-memory access
   using R = Raw<T, VE>;
-  extern __shared__ float2 cs[];              // [rows_per_cta][pairs]
-  __shared__ long long base[kRotMaxRows][4];  // x and out of q, x and out of k at each row
-  const int pairs = a.plan.pairs;
-  const long long row0 = (long long)blockIdx.x * a.rows_per_cta;
-  const int nrows = int(a.total - row0 < a.rows_per_cta ? a.total - row0 : a.rows_per_cta);
-  if (threadIdx.x < unsigned(nrows)) {
-    const long long r = row0 + threadIdx.x, b = r / a.rows, t = r - b * a.rows;
-#pragma unroll
-    for (int z = 0; z < 2; ++z) {
-      base[threadIdx.x][2 * z] = b * a.xb[z] + t * a.xr[z];
-      base[threadIdx.x][2 * z + 1] = b * a.ob[z] + t * a.orow[z];
-    }
-  }
-  __syncthreads();
+  extern __shared__ float2 cs[];
+  const int pairs = a.plan.pairs, turned = pairs / kTurn;
+  const int stride = pairs + kRotPad;  // off the multiples of the banks, where the rows' angles are written
+  const int b = int(blockIdx.x / a.row_ctas), t0 = int(blockIdx.x - b * a.row_ctas) * a.rows_per_cta;
+  const int nrows = min(a.rows_per_cta, a.rows - t0);
   pdl_wait();
   pdl_trigger();
-  const int turned = pairs / kTurn;
   bool first = true;
   const int group = int(threadIdx.x) / a.row_units;  // rows taken at a time when a row has few units
   int i = int(threadIdx.x) - group * a.row_units;    // the unit among the row's
   if (group >= a.groups) i = a.row_units;            // threads left over
   do {  // every thread makes the first turn, for the barrier in it
-    const int hh = i / a.units, unit = i - hh * a.units;
+    const bool turn = i < a.turned_units;
+    const int per = turn ? turned : a.units - turned, i0 = turn ? i : i - a.turned_units;
+    const int hh = per > 0 ? i0 / per : 0, unit = i0 - hh * per;
     const int z = hh >= a.q_heads, h = z ? hh - a.q_heads : hh;
-    const bool turn = unit < turned, live = i < a.row_units && (turn || a.copy[z]);
-    const int off = turn ? (HALVES ? unit * VE : unit * 2 * kTurn) : 2 * pairs + (unit - turned) * VE;
-    const T* x = static_cast<const T*>(a.x[z]) + h * a.xh[z] + off;
-    T* out = static_cast<T*>(a.out[z]) + h * a.oh[z] + off;
-    int rr = group;
+    const bool live = i < a.row_units && (turn || a.copy[z]);
+    const int off = turn ? (HALVES ? unit * VE : unit * 2 * kTurn) : 2 * pairs + unit * VE;
+    const T* x = static_cast<const T*>(a.x[z]) + b * a.xb[z] + (t0 + group) * a.xr[z] + h * a.xh[z] + off;
+    T* out = static_cast<T*>(a.out[z]) + b * a.ob[z] + (t0 + group) * a.orow[z] + h * a.oh[z] + off;
+    const long long dx = a.groups * a.xr[z], dy = a.groups * a.orow[z];
+    const float2* c = cs + (group * stride + unit * kPack);
+    int left = live ? (nrows - group + a.groups - 1) / a.groups : 0;  // rows of this thread
     do {
-      R v[kRotUnroll][kTwo ? 2 : 1];
+      R v[kU][kTwo ? 2 : 1];
 #pragma unroll
-      for (int u = 0; u < kRotUnroll; ++u) {
-        const int r = rr + u * a.groups;
-        if (live && r < nrows) {
-          const T* src = x + base[r][2 * z];
-          v[u][0] = rot_load<T, VE>(src);
+      for (int u = 0; u < kU; ++u)
+        if (u < left) {
+          v[u][0] = rot_load<T, VE>(x + u * dx);
           if constexpr (kTwo)
-            if (turn) v[u][1] = rot_load<T, VE>(src + (HALVES ? pairs : 1));
+            if (turn) v[u][1] = rot_load<T, VE>(x + u * dx + (HALVES ? pairs : 1));
         }
-      }
       if (first) {
         for (int k = threadIdx.x; k < nrows * pairs; k += kRotThreads) {
-          const int r = k / pairs, f = k - r * pairs;
-          const int32_t p = __ldg(a.pos + (row0 + r) * a.plan.axes + a.plan.axis[f]);
+          const int f = k / nrows, r = k - f * nrows;  // neighbours share a pair: its plan entry is one constant
+          const int32_t p = __ldg(a.pos + ((long long)b * a.rows + t0 + r) * a.plan.axes + a.plan.axis[f]);
           float2 t = rot_cos_sin(p, a.plan.turns[f], a.plan.amplitude);
           if (a.inverse) t.y = -t.y;
-          cs[k] = t;
+          const int j = f % kTurn;
+          cs[r * stride + (j / kPack * turned + f / kTurn) * kPack + j % kPack] = t;
         }
         __syncthreads();
         first = false;
       }
 #pragma unroll
-      for (int u = 0; u < kRotUnroll; ++u) {
-        const int r = rr + u * a.groups;
-        if (!live || r >= nrows) continue;
-        T* dst = out + base[r][2 * z + 1];
+      for (int u = 0; u < kU; ++u) {
+        if (u >= left) continue;
+        T* dst = out + u * dy;
         if (!turn) {
           rot_store<T, VE>(dst, v[u][0]);
           continue;
         }
         float2 t[kTurn];
-        if constexpr (kTurn >= 2) {  // pairs and kTurn even: 16 bytes hold two angles
-          const float4* c = reinterpret_cast<const float4*>(cs + r * pairs + unit * kTurn);
+        const float2* cu = c + u * a.groups * stride;
+        if constexpr (kPack == 2) {  // pairs even, so 16-byte steps stay on 16 bytes
 #pragma unroll
           for (int j = 0; j < kTurn / 2; ++j) {
-            const float4 q = c[j];
+            const float4 q = *reinterpret_cast<const float4*>(cu + j * 2 * turned);
             t[2 * j] = make_float2(q.x, q.y);
             t[2 * j + 1] = make_float2(q.z, q.w);
           }
         } else {
-          t[0] = cs[r * pairs + unit];
+          t[0] = *cu;
         }
         float x0[VE];
         rot_values<T, VE>(v[u][0], x0);
@@ -214,8 +212,11 @@ __global__ void __launch_bounds__(kRotThreads, HALVES && VE > 1 ? 3 : 4) rotary_
           rot_store<T, VE>(dst, rot_raw<T, VE>(y));
         }
       }
-      rr += kRotUnroll * a.groups;
-    } while (rr < nrows);
+      left -= kU;
+      x += kU * dx;
+      out += kU * dy;
+      c += kU * a.groups * stride;
+    } while (left > 0);
     i += kRotThreads;
   } while (i < a.row_units);
 }
@@ -361,8 +362,15 @@ int dit_rotary(const dit_rotary_plan* plan, const dit_rotary_rows* q, const dit_
           on16(r->out, batch > 1 ? r->out_batch : 0, rows > 1 ? r->out_row : 0, r->heads > 1 ? r->out_head : 0);
   }
   if (a.heads == 0) return DIT_OK;
+  // batch entries that follow one another in every tensor are rows of one entry
+  auto joined = [&](const dit_rotary_rows* r) {
+    return !r || r->heads == 0 || (r->x_batch == rows * r->x_row && r->out_batch == rows * r->out_row);
+  };
+  if (batch > 1 && joined(q) && joined(k) && (long long)batch * rows <= 0x7fffffffLL) {
+    rows *= batch;
+    batch = 1;
+  }
   a.rows = rows;
-  a.total = (long long)batch * rows;
   a.inverse = inverse != 0;
   a.pos = pos;
   a.plan = *plan;
@@ -372,17 +380,21 @@ int dit_rotary(const dit_rotary_plan* plan, const dit_rotary_rows* q, const dit_
   const long long row_units = (long long)a.units * a.heads;
   if (row_units > 0x7fffffffLL - kRotThreads) return DIT_EUNSUPPORTED;
   a.row_units = int(row_units);
+  a.turned_units = turned * a.heads;
   a.groups = std::max(1, kRotThreads / a.row_units);
-  // A round of kRotUnroll rows per thread and two units, while there are CTAs for every SM several times
-  // over.
-  long long per = std::max<long long>(kRotUnroll * a.groups, 2LL * kRotThreads * kRotUnroll / row_units);
+  // Two rounds per thread and two units, while there are CTAs for every SM several times over.
+  const int round = rot_unroll(plan->layout == DIT_ROTARY_HALVES && vec);
+  long long per = std::max<long long>(2 * round * a.groups, 8LL * kRotThreads / row_units);
   per = std::min<long long>(per, kRotMaxRows);
-  per = std::max(1LL, std::min(per, a.total / (4LL * num_sms())));
+  per = std::max(1LL, std::min(per, (long long)batch * rows / (3LL * num_sms())));
+  if (per > round * a.groups) per -= per % (round * a.groups);  // whole rounds: 6 rows 22.5, 8 rows 18.5 us at 4224 rows
+  per = std::min<long long>(per, rows);
   a.rows_per_cta = int(per);
-  const long long ctas = (a.total + per - 1) / per;
+  a.row_ctas = int((rows + per - 1) / per);
+  const long long ctas = (long long)batch * a.row_ctas;
   if (ctas > 0x7fffffffLL) return DIT_EUNSUPPORTED;
   const dim3 grid{unsigned(ctas), 1u, 1u};
-  const size_t smem = size_t(per) * plan->pairs * sizeof(float2);
+  const size_t smem = size_t(per) * (plan->pairs + kRotPad) * sizeof(float2);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (type == DIT_BF16)
