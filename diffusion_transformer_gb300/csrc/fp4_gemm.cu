@@ -341,6 +341,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 // ---------------------------------------------------------------------------------------------
 constexpr int kSplitThreads = 192;
 constexpr uint32_t kSplitMinSmem = 116 * 1024;
+constexpr int kSplitMaxStages = 12;
+constexpr uint32_t kSplitFixed = 1024 + 2 * 128 * 4 + 8 * (2 * kSplitMaxStages + 1) + 16;
 __host__ __device__ constexpr uint32_t split_stage_bytes(int bn, uint32_t sf) { return kTileBytes + uint32_t(bn) * 128 + 2 * sf; }
 
 template <int FMT, typename T>
@@ -353,7 +355,9 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
   const uint32_t aBytes = uint32_t(bn) * 128;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sB = smem;                      // 128 rows of B per stage (the MMA's A side)
+  float* sFa = reinterpret_cast<float*>(smem);  // row factors of the tile's A and B rows (1 KB)
+  float* sFb = sFa + 128;
+  uint8_t* sB = smem + 1024;               // 128 rows of B per stage (the MMA's A side)
   uint8_t* sA = sB + S * kTileBytes;       // bn rows of A (multiples of 16: 1024-byte swizzle atoms stay whole)
   uint8_t* sSB = sA + S * aBytes;
   uint8_t* sSA = sSB + S * SC::kBytes;
@@ -453,6 +457,11 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
       mbar_wait(smem_u32(tfull), 0, p.err, kErrTimeoutDrain);
     }
   } else {
+    if constexpr (SC::kNv) {
+      const int i = int(threadIdx.x) - 64;
+      sFa[i] = i < bn && m0 + i < p.M ? __ldg(p.a_scale + m0 + i) : 0.f;
+      sFb[i] = n0 + i < p.N ? __ldg(p.b_scale + n0 + i) : 0.f;
+    }
     (void)mbar_wait_warp(smem_u32(tfull), 0, p.err, kErrTimeoutEpilogue);
     tc_fence_after();
   }
@@ -463,36 +472,32 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
   const uint32_t taddr = tmem + (uint32_t(quad * 32) << 16);
   const int n = n0 + quad * 32 + lane;
   T* out = static_cast<T*>(p.out);
-  float* tile = reinterpret_cast<float*>(smem);
+  float* tile = reinterpret_cast<float*>(sB);
   __syncthreads();
   tc_fence_after();
+  const int live = min(bn, p.M - m0);
   if (warp >= 2) {
-    const float rb = SC::kNv ? (n < p.N ? __ldg(p.b_scale + n) : 0.f) : 1.f;
-    for (int c = 0; c < bn; c += 8) {
-      if (m0 + c >= p.M) break;
-      uint32_t w[8];
-      tmem_ld8(taddr + c, w);
+    const float rb = SC::kNv ? sFb[quad * 32 + lane] : 1.f;
+    for (int c = 0; c < live; c += 16) {
+      uint32_t w[2][8];
+      tmem_ld8(taddr + c, w[0]);
+      tmem_ld8(taddr + c + 8, w[1]);
       tmem_ld_wait();
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int m = m0 + c + e;
-        float v = __uint_as_float(w[e]);
-        if (parts > 1) {
-          tile[(c + e) * 128 + quad * 32 + lane] = v;
-        } else if (m < p.M && n < p.N) {
-          if (SC::kNv) v = v * __ldg(p.a_scale + m) * rb;
-          out[m * p.ldo + n] = T(v);
-        }
+      for (int e = 0; e < 16; ++e) {
+        const float v = __uint_as_float(w[e >> 3][e & 7]);
+        if (parts > 1) tile[(c + e) * 128 + quad * 32 + lane] = v;
+        else if (c + e < live && n < p.N) out[(long long)(m0 + c + e) * p.ldo + n] = T(SC::kNv ? v * sFa[c + e] * rb : v);
       }
     }
   }
   if (parts > 1) {
     cluster_barrier();
-    const int live = min(bn, p.M - m0);
     const uint32_t base = smem_u32(tile);
     // four rows of B per thread, 32 threads to a column; all parts of two columns in flight together
     constexpr int kMaxParts = 8;
     const int step = parts * kSplitThreads;
+    const bool whole = n0 + 128 <= p.N && p.ldo % 4 == 0 && reinterpret_cast<uintptr_t>(out) % (4 * sizeof(T)) == 0;
     for (int i0 = part * kSplitThreads + int(threadIdx.x); i0 < live * 32; i0 += 2 * step) {
       float4 v[2][kMaxParts];
 #pragma unroll
@@ -514,13 +519,23 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
             s.z += v[u][q].z;
             s.w += v[u][q].w;
           }
-        const float* sv = &s.x;
-        const int m = m0 + (i >> 5), r4 = (i & 31) * 4;
-        const float ra = SC::kNv ? __ldg(p.a_scale + m) : 1.f;
+        const int c = i >> 5, r4 = (i & 31) * 4;
+        if constexpr (SC::kNv) {
+          const float ra = sFa[c];
+          const float4 f = *reinterpret_cast<const float4*>(sFb + r4);
+          s = make_float4(s.x * ra * f.x, s.y * ra * f.y, s.z * ra * f.z, s.w * ra * f.w);
+        }
+        T* o = out + (long long)(m0 + c) * p.ldo + n0 + r4;
+        if (whole) {
+          if constexpr (sizeof(T) == 2)
+            *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+          else
+            *reinterpret_cast<float4*>(o) = s;
+        } else {
+          const float* sv = &s.x;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int nn = n0 + r4 + e;
-          if (nn < p.N) out[m * p.ldo + nn] = T(SC::kNv ? sv[e] * ra * __ldg(p.b_scale + nn) : sv[e]);
+          for (int e = 0; e < 4; ++e)
+            if (n0 + r4 + e < p.N) o[e] = T(sv[e]);
         }
       }
     }
@@ -571,9 +586,9 @@ int launch_split(const dit_fp4_matrix& a, const dit_fp4_matrix& b, Fp4Params p, 
   int parts = 1;
   while (parts < 8 && 2 * parts <= KB && (long long)nt * mt * parts * 2 <= num_sms()) parts *= 2;
   const uint32_t sb = split_stage_bytes(p.bn, Scales<FMT>::kBytes);
-  p.stages = std::min((KB + parts - 1) / parts, int((227 * 1024 - 1024 - 512) / sb));
-  p.stages = std::max(1, std::min(p.stages, 24));
-  uint32_t smem = 1024 + uint32_t(p.stages) * sb + 8 * (2 * uint32_t(p.stages) + 2) + 16;
+  p.stages = std::min((KB + parts - 1) / parts, int((227 * 1024 - kSplitFixed) / sb));
+  p.stages = std::max(1, std::min(p.stages, kSplitMaxStages));
+  uint32_t smem = kSplitFixed + uint32_t(p.stages) * sb;
   // More than half of an SM's shared memory, as every kernel here that allocates tensor memory: no two of
   // them share an SM, so no CTA of a cluster waits for tensor memory that another cluster's CTA holds
   // (also covers the partial tile, at most 64 KB).
