@@ -478,16 +478,32 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
   const int live = min(bn, p.M - m0);
   if (warp >= 2) {
     const float rb = SC::kNv ? sFb[quad * 32 + lane] : 1.f;
-    for (int c = 0; c < live; c += 16) {
-      uint32_t w[2][8];
-      tmem_ld8(taddr + c, w[0]);
-      tmem_ld8(taddr + c + 8, w[1]);
+    T* o = out + (long long)m0 * p.ldo + n;
+    for (int c = 0; c < live; c += 16, o += 16 * p.ldo) {
+      uint32_t w[16];
+      tmem_ld16(taddr + c, w);
       tmem_ld_wait();
+      if (parts > 1) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const float v = __uint_as_float(w[e >> 3][e & 7]);
-        if (parts > 1) tile[(c + e) * 128 + quad * 32 + lane] = v;
-        else if (c + e < live && n < p.N) out[(long long)(m0 + c + e) * p.ldo + n] = T(SC::kNv ? v * sFa[c + e] * rb : v);
+        for (int e = 0; e < 16; ++e) tile[(c + e) * 128 + quad * 32 + lane] = __uint_as_float(w[e]);
+        continue;
+      }
+      // every value first, then the stores: a store between them would hold back the next factor's load
+      T v[16];
+#pragma unroll
+      for (int e = 0; e < 16; e += 4) {
+        const float4 f = SC::kNv ? *reinterpret_cast<const float4*>(sFa + c + e) : make_float4(1.f, 1.f, 1.f, 1.f);
+        const float* ff = &f.x;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float x = __uint_as_float(w[e + k]);
+          v[e + k] = T(SC::kNv ? x * ff[k] * rb : x);
+        }
+      }
+      if (n < p.N) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (c + e < live) o[e * p.ldo] = v[e];
       }
     }
   }
@@ -579,25 +595,26 @@ int launch_pair(const dit_fp4_matrix& a, const dit_fp4_matrix& b, Fp4Params p, i
 }
 
 template <int FMT, typename T>
-int launch_split(const dit_fp4_matrix& a, const dit_fp4_matrix& b, Fp4Params p, cudaStream_t st) {
+int launch_split(const dit_fp4_matrix& a, const dit_fp4_matrix& b, Fp4Params p, int bn, int parts, cudaStream_t st) {
   constexpr int G = Scales<FMT>::kGroups;
-  p.bn = p.M <= 16 ? 16 : (p.M <= 32 ? 32 : (p.M <= 64 ? 64 : 128));
-  const int nt = (p.N + 127) / 128, mt = (p.M + p.bn - 1) / p.bn, KB = (p.K + kStageK - 1) / kStageK;
-  int parts = 1;
-  while (parts < 8 && 2 * parts <= KB && (long long)nt * mt * parts * 2 <= num_sms()) parts *= 2;
-  const uint32_t sb = split_stage_bytes(p.bn, Scales<FMT>::kBytes);
-  p.stages = std::min((KB + parts - 1) / parts, int((227 * 1024 - kSplitFixed) / sb));
+  p.bn = bn;
+  const long long nt = (p.N + 127) / 128, mt = (p.M + bn - 1) / bn;
+  if (nt * parts > 0x7fffffffLL || mt > 65535) return DIT_EUNSUPPORTED;
+  const int KB = (p.K + kStageK - 1) / kStageK;
+  const uint32_t sb = split_stage_bytes(bn, Scales<FMT>::kBytes);
+  // A cluster's CTA asks for more than half of an SM's shared memory, as every kernel here that allocates
+  // tensor memory and waits for another CTA: no two of them share an SM, so none waits for tensor memory
+  // that another cluster holds. (The half also covers the partial tile, at most 64 KB.) A lone CTA waits
+  // for nobody: where there are more than SMs, two share one.
+  const uint32_t most = parts == 1 && nt * mt > num_sms() ? 113 * 1024 : 227 * 1024;
+  p.stages = std::min((KB + parts - 1) / parts, int((most - kSplitFixed) / sb));
   p.stages = std::max(1, std::min(p.stages, kSplitMaxStages));
   uint32_t smem = kSplitFixed + uint32_t(p.stages) * sb;
-  // More than half of an SM's shared memory, as every kernel here that allocates tensor memory: no two of
-  // them share an SM, so no CTA of a cluster waits for tensor memory that another cluster's CTA holds
-  // (also covers the partial tile, at most 64 KB).
-  smem = std::max(smem, kSplitMinSmem);
+  if (parts > 1) smem = std::max(smem, kSplitMinSmem);
   CUtensorMap ma, mb, msa, msb;
-  if (!tmap_codes(&ma, a.codes, a.rows, p.K, p.bn) || !tmap_codes(&mb, b.codes, b.rows, p.K, 128) ||
-      !tmap_sf(&msa, a, G, 1) || !tmap_sf(&msb, b, G, 1))
+  if (!tmap_codes(&ma, a.codes, a.rows, p.K, bn) || !tmap_codes(&mb, b.codes, b.rows, p.K, 128) || !tmap_sf(&msa, a, G, 1) ||
+      !tmap_sf(&msb, b, G, 1))
     return DIT_ECUDA;
-  if (mt > 65535) return DIT_EUNSUPPORTED;
   auto kern = fp4_split_kernel<FMT, T>;
   if (!smem_attr_once(reinterpret_cast<const void*>(kern), 227 * 1024)) return DIT_ECUDA;
   const cudaError_t e = launch_pdl(kern, dim3(unsigned(nt * parts), unsigned(mt)), dim3(kSplitThreads), smem, st, parts,
@@ -605,28 +622,46 @@ int launch_split(const dit_fp4_matrix& a, const dit_fp4_matrix& b, Fp4Params p, 
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? DIT_OK : DIT_ECUDA;
 }
 
+// The kernel and tile with the least estimated time, in ns, fitted to what 28 sizes from 1 x 18432 to
+// 4224 x 24576 took with every tile. A pair kernel takes 3000 once, half of the operands' bytes at the memory's
+// rate, and per round of tiles over the CTA pairs 900 (1100 swapped) and 215, 250 or 320 per stage of 256
+// columns for 128, 192 or 256 rows of Q. A split kernel takes 2200 once, per wave of CTAs 10 per row of its
+// tile and 60 + 1.6 per row for a stage, at least B's bytes at the memory's rate, and 1800 + 5 per row to join
+// the parts of a cluster. Both sides, in us: 1088 x 3072 x 12288 17.4 with 192 rows swapped, 20.9 with 256;
+// 4224 x 24576 x 3072 104 with 256, 117 with 192; 333 x 777 x 1000 4.6 split, 5.4 in pairs; 200 x 24576 x 3072
+// 18.1 split, 13.7 in pairs; 33 x 3072 x 12288 13.3 with one CTA per tile, 6.9 with four.
 template <int FMT, typename T>
 int launch_product(const dit_fp4_matrix& a, const dit_fp4_matrix& b, const Fp4Params& p, cudaStream_t st) {
-  const long long tiles = (long long)((p.M + 255) / 256) * ((p.N + 255) / 256);
-  if (p.M <= 128 || tiles < 24) return launch_split<FMT, T>(a, b, p, st);
-  // rows of P and of Q per tile, in rounds over the CTA pairs: the shape with the least work on the
-  // longest path
-  const int units = num_sms() / 2;
+  const int sms = num_sms(), units = sms / 2;
+  const long long KB = (p.K + kStageK - 1) / kStageK;
+  auto up = [](long long x, long long y) { return (x + y - 1) / y; };
   // unswapped tiles store 32 bytes of a row at a time
   const bool rows32 = reinterpret_cast<uintptr_t>(p.out) % 32 == 0 && (p.M == 1 || p.ldo * (long long)sizeof(T) % 32 == 0);
   long long best = -1;
-  int bn = 256;
+  int bn = 0, parts = 0;
   bool swap = false;
   for (int s = rows32 ? 0 : 1; s < 2; ++s)
-    for (int n : {256, 192, 128}) {
-      const long long P = s ? p.N : p.M, Q = s ? p.M : p.N;
-      const long long t = (P + 255) / 256 * ((Q + n - 1) / n), cost = (t + units - 1) / units * (n + 32);
+    for (int i = 0; i < 3; ++i) {
+      constexpr int kRows[3] = {256, 192, 128}, kStageNs[3] = {320, 250, 215};
+      const long long tiles = up(s ? p.N : p.M, 256) * up(s ? p.M : p.N, kRows[i]);
+      const long long cost = 3000 + (p.M + (long long)p.N) * p.K / 24000 + up(tiles, units) * (900 + 200 * s + KB * kStageNs[i]);
       if (best < 0 || cost < best) {
         best = cost;
-        bn = n;
+        bn = kRows[i];
         swap = s != 0;
       }
     }
+  const int sn = p.M <= 16 ? 16 : (p.M <= 32 ? 32 : (p.M <= 64 ? 64 : 128));
+  const long long ctas = up(p.N, 128) * up(p.M, sn);
+  for (int k = 1; k <= 8 && k <= KB && (k == 1 || ctas * k <= sms); k *= 2) {
+    const long long busy = up(ctas * k, sms) * (10 * sn + up(KB, k) * (60 + 8 * sn / 5));
+    const long long cost = 2200 + std::max(busy, (long long)p.N * p.K / 9800) + (k > 1 ? 1800 + 5 * sn : 0);
+    if (cost < best) {
+      best = cost;
+      parts = k;
+    }
+  }
+  if (parts > 0) return launch_split<FMT, T>(a, b, p, sn, parts, st);
   return swap ? launch_pair<FMT, T, true>(a, b, p, bn, st) : launch_pair<FMT, T, false>(a, b, p, bn, st);
 }
 
