@@ -57,14 +57,19 @@ __device__ __forceinline__ uint32_t unit_max(const Unit<T>& u) {
     return m;
   }
 }
-// 16 values from column c of a row (global, or the staged copy in shared memory), zero past cols
-template <typename T, bool VEC>
+// 16 values from column c of a row that starts on 16 bytes, zero past cols
+template <typename T>
 __device__ __forceinline__ Unit<T> unit_load(const T* x, int c, int cols) {
   Unit<T> u;
-  if (VEC && c + kUnit <= cols) {
+  if (c + kUnit <= cols) {
 #pragma unroll
-    for (int h = 0; h < int(sizeof(T)) / 2; ++h)
-      ld_global_256(u.w + 8 * h, reinterpret_cast<const uint8_t*>(x + c) + 32 * h);
+    for (int h = 0; h < int(sizeof(T)); ++h) {
+      const uint4 q = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(x + c) + 16 * h);
+      u.w[4 * h] = q.x;
+      u.w[4 * h + 1] = q.y;
+      u.w[4 * h + 2] = q.z;
+      u.w[4 * h + 3] = q.w;
+    }
   } else {
     using Bits = typename std::conditional<sizeof(T) == 2, uint16_t, uint32_t>::type;
     const Bits* b = reinterpret_cast<const Bits*>(x);
@@ -77,6 +82,14 @@ __device__ __forceinline__ Unit<T> unit_load(const T* x, int c, int cols) {
   }
   return u;
 }
+// Rows staged in shared memory: a word of padding behind every unit, so that the units of a warp lie on
+// different banks. The place of value i, in values:
+template <typename T>
+__device__ __forceinline__ int staged_at(int i) {
+  return i + i / kUnit * int(4 / sizeof(T));
+}
+template <typename T>
+constexpr size_t kStagedUnit = kUnit * sizeof(T) + 4;
 
 // Codes and scale byte of the unit i in v. A group's four scale bytes are gathered in one thread, so every
 // lane of the warp takes part.
@@ -135,7 +148,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) fp4_quantize_warp_kernel(const
   Unit<T> v[NU];
 #pragma unroll
   for (int k = 0; k < NU; ++k)
-    if (k * 32 < sh.units) v[k] = unit_load<T, true>(x, (k * 32 + lane) * kUnit, cols);
+    if (k * 32 < sh.units) v[k] = unit_load(x, (k * 32 + lane) * kUnit, cols);
   float fu = 0.f, ft = 0.f;
   if constexpr (FMT == DIT_FP4_NV) {
     uint32_t m = 0;
@@ -154,9 +167,9 @@ __global__ void __launch_bounds__(32 * kRowWarps) fp4_quantize_warp_kernel(const
     if (k * 32 < sh.units) unit_quantize<T, FMT>(v[k], k * 32 + lane, fu, ft, sh.units, sh.code_units, crow, srow);
 }
 
-// Few rows, long rows, or rows off 32 bytes: one CTA per row, NU units per thread and chunk. Rows longer
+// Few rows, long rows, or rows off 16 bytes: one CTA per row, NU units per thread and chunk. Rows longer
 // than NU units per thread repeat the passes over chunks (NV: the second pass rereads the row, which L2
-// holds). A row that starts off 32 bytes (VEC = false) is staged through shared memory with coalesced
+// holds). A row that starts off 16 bytes (VEC = false) is staged through shared memory with coalesced
 // single loads.
 template <typename T, int FMT, bool VEC, int NU>
 __global__ void __launch_bounds__(256) fp4_quantize_kernel(const T* x, long long ldx, int cols, uint8_t* codes,
@@ -177,14 +190,26 @@ __global__ void __launch_bounds__(256) fp4_quantize_kernel(const T* x, long long
     const int c0 = c * span * kUnit;
     if constexpr (!VEC) {
       __syncthreads();
-      const int n = min(cols - c0, span * kUnit);
-      for (int i = threadIdx.x; i < n; i += nt) sx[i] = x[c0 + i];
+      T t[NU * kUnit];
+#pragma unroll
+      for (int k = 0; k < NU * kUnit; ++k) {  // all loads in flight before the first is stored
+        const int i = int(threadIdx.x) + k * nt;
+        t[k] = c0 + i < cols ? x[c0 + i] : T(0.f);
+      }
+#pragma unroll
+      for (int k = 0; k < NU * kUnit; ++k) sx[staged_at<T>(int(threadIdx.x) + k * nt)] = t[k];
       __syncthreads();
     }
 #pragma unroll
     for (int k = 0; k < NU; ++k) {
       const int u = threadIdx.x + k * nt;
-      v[k] = VEC ? unit_load<T, true>(x, c0 + u * kUnit, cols) : unit_load<T, false>(sx, u * kUnit, cols - c0);
+      if constexpr (VEC) {
+        v[k] = unit_load(x, c0 + u * kUnit, cols);
+      } else {
+        const uint32_t* w = staged + u * (kStagedUnit<T> / 4);
+#pragma unroll
+        for (int j = 0; j < int(kUnit * sizeof(T) / 4); ++j) v[k].w[j] = w[j];
+      }
     }
   };
   float fu = 0.f, ft = 0.f;
@@ -214,49 +239,63 @@ __global__ void __launch_bounds__(256) fp4_quantize_kernel(const T* x, long long
   }
 }
 
-// One row per blockIdx.x, units of 16 values: 8 code bytes and a scale byte in, 32 or 64 bytes out.
-// Bound by HBM, the values out above all.
-template <typename T, int FMT>
+// `lanes` threads to a row, units of 16 values: 8 code bytes and a scale byte in, 32 or 64
+// bytes out, or (VEC = false: rows off 32 bytes) through shared memory in whole lines. Bound by HBM, the
+// values out above all.
+template <typename T, int FMT, bool VEC>
 __global__ void __launch_bounds__(256, 6) fp4_dequantize_kernel(const uint8_t* codes, const uint8_t* scales,
-                                                             const float* row_scale, int cols, T* out, long long ldo,
-                                                             bool vec) {
+                                                                const float* row_scale, int rows, int cols,
+                                                                int lanes, T* out, long long ldo) {
   pdl_wait();
   pdl_trigger();
-  const int r = blockIdx.x;
-  const int units = (cols + kUnit - 1) / kUnit;
-  const uint8_t* crow = codes + (long long)r * fp4_code_row_bytes(cols);
-  const uint8_t* srow = scales + fp4_scale_row(FMT, r, cols);
-  const float g = FMT == DIT_FP4_NV ? __ldg(row_scale + r) : 1.f;
+  const int in_cta = int(threadIdx.x) / lanes, lane = int(threadIdx.x) - in_cta * lanes;
+  const long long r = (long long)blockIdx.x * (int(blockDim.x) / lanes) + in_cta;
+  const int units = r < rows ? (cols + kUnit - 1) / kUnit : 0;
+  const uint8_t* crow = codes + r * fp4_code_row_bytes(cols);
+  const uint8_t* srow = scales + fp4_scale_row(FMT, int(r), cols);
+  const float g = FMT == DIT_FP4_NV && r < rows ? __ldg(row_scale + r) : 1.f;
   T* orow = out + r * ldo;
+  __shared__ uint8_t staging[VEC ? 1 : 256 * kStagedUnit<T>];
+  T* staged = reinterpret_cast<T*>(staging + (VEC ? 0 : (threadIdx.x - lane) * kStagedUnit<T>));
 #pragma unroll 1
-  for (int u = threadIdx.x; u < units; u += blockDim.x) {
-    const int c = u * kUnit;
-    const uint2 w = *reinterpret_cast<const uint2*>(crow + 8 * u);
-    const int byte = srow[fp4_scale_block(FMT == DIT_FP4_NV ? u : u >> 1)];
-    float v[kUnit];
-    fp4_values16(w, v);
-    const float s = FMT == DIT_FP4_NV ? fp4_e4m3(byte) : fp4_e8m0(byte);
+  for (int u0 = 0; u0 * kUnit < cols; u0 += lanes) {
+    const int u = u0 + lane, c = u * kUnit;
+    if (u < units) {
+      const uint2 w = *reinterpret_cast<const uint2*>(crow + 8 * u);
+      const int byte = srow[fp4_scale_block(FMT == DIT_FP4_NV ? u : u >> 1)];
+      float v[kUnit];
+      fp4_values16(w, v);
+      const float s = FMT == DIT_FP4_NV ? fp4_e4m3(byte) : fp4_e8m0(byte);
 #pragma unroll
-    for (int j = 0; j < kUnit; ++j) v[j] = FMT == DIT_FP4_NV ? v[j] * s * g : v[j] * s;
-    T* o = orow + c;
-    if (vec && c + kUnit <= cols) {
-      uint32_t q[8];
-      if constexpr (sizeof(T) == 2) {
+      for (int j = 0; j < kUnit; ++j) v[j] = FMT == DIT_FP4_NV ? v[j] * s * g : v[j] * s;
+      if (VEC && c + kUnit <= cols) {
+        uint32_t q[8];
+        if constexpr (sizeof(T) == 2) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) q[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
-        st_global_256(o, q);
+          for (int j = 0; j < 8; ++j) q[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+          st_global_256(orow + c, q);
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) q[j] = __float_as_uint(v[8 * h + j]);
+            st_global_256(orow + c + 8 * h, q);
+          }
+        }
+      } else if (VEC) {
+#pragma unroll
+        for (int j = 0; j < kUnit; ++j)
+          if (c + j < cols) orow[c + j] = T(v[j]);
       } else {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) q[j] = __float_as_uint(v[8 * h + j]);
-          st_global_256(o + 8 * h, q);
-        }
+        for (int j = 0; j < kUnit; ++j) staged[staged_at<T>(lane * kUnit) + j] = T(v[j]);
       }
-    } else {
-#pragma unroll
-      for (int j = 0; j < kUnit; ++j)
-        if (c + j < cols) o[j] = T(v[j]);
+    }
+    if constexpr (!VEC) {
+      __syncthreads();
+      const int n = units > 0 ? min(lanes * kUnit, cols - u0 * kUnit) : 0;
+      for (int i = lane; i < n; i += lanes) orow[u0 * kUnit + i] = staged[staged_at<T>(i)];
+      __syncthreads();
     }
   }
 }
@@ -266,7 +305,7 @@ cudaError_t quantize_nu(const T* x, long long ldx, const dit_fp4_matrix& m, cuda
   const int units = fp4_groups(FMT, m.cols) * (FMT == DIT_FP4_NV ? 4 : 8);
   auto go = [&](auto kern, int nu) {
     const int threads = std::min(256, (units + 32 * nu - 1) / (32 * nu) * 32);
-    const size_t smem = VEC ? 0 : std::min<size_t>(size_t(threads) * nu * kUnit, size_t(m.cols)) * sizeof(T);
+    const size_t smem = VEC ? 0 : size_t(threads) * nu * kStagedUnit<T>;
     return launch_pdl(kern, dim3(m.rows), dim3(threads), smem, st, 1, x, ldx, m.cols, m.codes, m.scales, m.row_scale);
   };
   if constexpr (VEC) {
@@ -285,7 +324,7 @@ cudaError_t quantize_nu(const T* x, long long ldx, const dit_fp4_matrix& m, cuda
     }
   }
   // units per thread: few for short rows, whose threads are few already
-  if (units <= 256) return go(fp4_quantize_kernel<T, FMT, VEC, 1>, 1);
+  if (units <= (sizeof(T) == 4 && m.rows >= 4 * num_sms() ? 128 : 256)) return go(fp4_quantize_kernel<T, FMT, VEC, 1>, 1);
   if constexpr (sizeof(T) == 2)
     if (units > 512) {
       constexpr int kLong = 4;  // (8: 29.5 against 27.4 us on 4224 rows of 12288)
@@ -295,16 +334,18 @@ cudaError_t quantize_nu(const T* x, long long ldx, const dit_fp4_matrix& m, cuda
 }
 template <typename T, int FMT>
 cudaError_t quantize_go(const T* x, long long ldx, const dit_fp4_matrix& m, cudaStream_t st) {
-  const bool vec = reinterpret_cast<uintptr_t>(x) % 32 == 0 && (m.rows == 1 || ldx * (long long)sizeof(T) % 32 == 0);
+  const bool vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && (m.rows == 1 || ldx * (long long)sizeof(T) % 16 == 0);
   return vec ? quantize_nu<T, FMT, true>(x, ldx, m, st) : quantize_nu<T, FMT, false>(x, ldx, m, st);
 }
 template <typename T, int FMT>
 cudaError_t dequantize_go(const dit_fp4_matrix& m, T* out, long long ldo, cudaStream_t st) {
   const int units = (m.cols + kUnit - 1) / kUnit;
-  const int threads = std::min(256, (units + 31) / 32 * 32);
+  // threads along a row; short rows share a CTA
+  const int lanes = std::min(256, units > 128 ? (units + 31) / 32 * 32 : units), rows = units > 128 ? 1 : 256 / lanes;
   const bool vec = reinterpret_cast<uintptr_t>(out) % 32 == 0 && (m.rows == 1 || ldo * (long long)sizeof(T) % 32 == 0);
-  return launch_pdl(fp4_dequantize_kernel<T, FMT>, dim3(m.rows), dim3(threads), 0, st, 1, m.codes, m.scales,
-                    m.row_scale, m.cols, out, ldo, vec);
+  auto kern = vec ? fp4_dequantize_kernel<T, FMT, true> : fp4_dequantize_kernel<T, FMT, false>;
+  return launch_pdl(kern, dim3(unsigned((m.rows + (long long)rows - 1) / rows)), dim3(lanes * rows), 0, st, 1, m.codes,
+                    m.scales, m.row_scale, m.rows, m.cols, lanes, out, ldo);
 }
 
 }  // namespace

@@ -121,13 +121,7 @@ __device__ __forceinline__ void fp4_values16(uint2 w, float* v) {
   }
 }
 
-// 32 bytes of global memory (32-byte aligned) in one load
-__device__ __forceinline__ void ld_global_256(uint32_t* w, const void* p) {
-  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-               : "l"(p));
-}
-
+// 32 bytes of global memory (32-byte aligned) in one store
 __device__ __forceinline__ void st_global_256(void* p, const uint32_t (&w)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
                "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
