@@ -15,6 +15,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "fp4.cuh"
 #include "internal.h"
@@ -266,17 +267,17 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         uint32_t w[2][32];
         tmem_ld32(taddr + g * 64, w[0]);
         tmem_ld32(taddr + g * 64 + 32, w[1]);
+        tmem_ld_wait();
+        if (overlap ? j == 0 : j + 2 >= groups) {
+          tc_fence_before();
+          mbar_arrive_cluster(tempty0 + uint32_t(acc) * 8u);
+        }
         if constexpr (SC::kNv) {
           __syncwarp();
           cf[lane] = f0;
           cf[lane + 32] = f1;
           if (j + 2 < groups) fetch(j + 2);
           __syncwarp();
-        }
-        tmem_ld_wait();
-        if (overlap ? j == 0 : j + 2 >= groups) {
-          tc_fence_before();
-          mbar_arrive_cluster(tempty0 + uint32_t(acc) * 8u);
         }
         if (q0 >= rowsQ || row0 >= rowsP) continue;
         if constexpr (SC::kNv) {
@@ -565,6 +566,18 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
 // ---------------------------------------------------------------------------------------------
 // launch
 // ---------------------------------------------------------------------------------------------
+// All of an SM's shared memory for `kern`; asked for once per device (a bit of `ready`), since a call here
+// takes microseconds and the library's table of kernels is searched under a lock.
+bool allow_smem(const void* kern, std::atomic<uint64_t>& ready) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return false;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (ready.load(std::memory_order_acquire) & bit) return true;
+  if (!smem_attr_once(kern, 227 * 1024)) return false;
+  ready.fetch_or(bit, std::memory_order_release);
+  return true;
+}
+
 bool tmap_codes(CUtensorMap* m, const uint8_t* codes, int rows, int K, int box_rows) {
   return make_tmap_2d(m, codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, fp4_code_row_bytes(K), rows, fp4_code_row_bytes(K), 128,
                       box_rows, true);
@@ -586,7 +599,8 @@ int launch_pair(const dit_fp4_matrix& a, const dit_fp4_matrix& b, Fp4Params p, i
     return DIT_ECUDA;
   p.n_fast = P.rows > Q.rows;  // consecutive tiles share the smaller operand's rows, which stay in L2
   auto kern = fp4_pair_kernel<FMT, T, SWAP>;
-  if (!smem_attr_once(reinterpret_cast<const void*>(kern), 227 * 1024)) return DIT_ECUDA;
+  static std::atomic<uint64_t> ready{0};
+  if (!allow_smem(reinterpret_cast<const void*>(kern), ready)) return DIT_ECUDA;
   const long long tiles = (long long)((P.rows + 255) / 256) * ((Q.rows + bn - 1) / bn);
   if (tiles > 0x7fffffffLL - num_sms()) return DIT_EUNSUPPORTED;
   const int units = int(std::min<long long>(tiles, num_sms() / 2));
@@ -616,7 +630,8 @@ int launch_split(const dit_fp4_matrix& a, const dit_fp4_matrix& b, Fp4Params p, 
       !tmap_sf(&msb, b, G, 1))
     return DIT_ECUDA;
   auto kern = fp4_split_kernel<FMT, T>;
-  if (!smem_attr_once(reinterpret_cast<const void*>(kern), 227 * 1024)) return DIT_ECUDA;
+  static std::atomic<uint64_t> ready{0};
+  if (!allow_smem(reinterpret_cast<const void*>(kern), ready)) return DIT_ECUDA;
   const cudaError_t e = launch_pdl(kern, dim3(unsigned(nt * parts), unsigned(mt)), dim3(kSplitThreads), smem, st, parts,
                                    ma, mb, msa, msb, p);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? DIT_OK : DIT_ECUDA;
