@@ -29,6 +29,7 @@ __all__ = [
     "dit_rope_tables", "RotaryPlan", "dit_rotary_plan_init", "dit_rotary_tables", "dit_rotary",
     "DIT_FP4_NV", "DIT_FP4_MX", "Fp4Matrix", "dit_fp4_code_bytes", "dit_fp4_scale_bytes", "dit_fp4_quantize",
     "dit_fp4_dequantize", "dit_fp4_matmul", "dit_linear_fp4", "dit_linear_fp4_workspace_bytes",
+    "Fp4BlockWeights", "dit_block_forward_fp4", "dit_block_fp4_workspace_bytes",
     "dit_denoise", "dit_block_forward_noalloc", "dit_block_noalloc_max_bytes", "dit_workspace_bytes", "dit_denoise_workspace_bytes", "dit_modnorm", "dit_qkv_rope",
     "dit_vt_stride", "dit_stream_k_workspace_bytes", "dit_attention", "dit_attention_qknorm", "dit_attention_workspace_bytes", "dit_linear_gated", "dit_linear_swiglu", "dit_linear",
     "dit_dequant_int8", "dit_linear_int8", "dit_linear_int8_workspace_bytes", "dit_check", "dit_selftest_bounded_wait", "dit_status_string", "dit_version",
@@ -110,7 +111,16 @@ class dit_fp4_matrix(ctypes.Structure):
                 ("row_scale", c_void_p)]
 
 
+class dit_block_wfp4(ctypes.Structure):
+    _fields_ = [("w", dit_fp4_matrix * 4), ("norm1", c_void_p), ("norm2", c_void_p), ("q_norm", c_void_p),
+                ("k_norm", c_void_p)]
+
+
 _SIGNATURES = {
+    "dit_block_forward_fp4": (c_int, [POINTER(dit_dims), POINTER(dit_block_wfp4), c_void_p, c_int, c_void_p, c_int,
+                                      c_void_p, c_void_p, c_void_p, c_void_p, POINTER(dit_mod), c_void_p, c_size_t,
+                                      c_void_p]),
+    "dit_block_fp4_workspace_bytes": (c_size_t, [POINTER(dit_dims), c_int, c_int, c_int]),
     "dit_rotary_plan_init": (c_int, [POINTER(dit_rotary_spec), POINTER(dit_rotary_plan)]),
     "dit_rotary_tables": (c_int, [POINTER(dit_rotary_plan), c_void_p, c_int, c_void_p, c_void_p, c_void_p]),
     "dit_rotary": (c_int, [POINTER(dit_rotary_plan), c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_void_p, c_int,
@@ -822,6 +832,31 @@ def dit_linear_fp4(x, w: Fp4Matrix, out, ws, stream=None):
                               ws.numel() * ws.element_size(), st)
     if rc:
         _ok(rc, "dit_linear_fp4")
+
+
+class Fp4BlockWeights:
+    """The 4-bit weights of one block: four Fp4Matrix (qkv, out, up, down) of one format and the norm weights."""
+
+    def __init__(self, w: Sequence[Fp4Matrix], norm1=None, norm2=None, q_norm=None, k_norm=None):
+        f32 = _torch().float32
+        self.w, self.tensors = tuple(w), (norm1, norm2, q_norm, k_norm)
+        self.format = self.w[0].format
+        self.c = dit_block_wfp4((dit_fp4_matrix * 4)(*[m.c for m in self.w]), _ptr(norm1, f32, "norm1"),
+                                _ptr(norm2, f32, "norm2"), _ptr(q_norm, f32, "q_norm"), _ptr(k_norm, f32, "k_norm"))
+
+
+def dit_block_fp4_workspace_bytes(dims: DitDims, format: int, L: int, N: int) -> int:
+    return lib().dit_block_fp4_workspace_bytes(byref(dims.c), format, L, N)
+
+
+def dit_block_forward_fp4(dims: DitDims, w: Fp4BlockWeights, txt, img, txt_cos, txt_sin, img_cos, img_sin,
+                          mod: Modulation, ws, stream=None):
+    f32 = _torch().float32
+    L = 0 if txt is None else txt.shape[0]
+    _ok(lib().dit_block_forward_fp4(byref(dims.c), byref(w.c), _ptr(txt, f32, "txt"), L, _ptr(img, f32, "img"),
+                                    img.shape[0], _ptr(txt_cos, f32), _ptr(txt_sin, f32), _ptr(img_cos, f32),
+                                    _ptr(img_sin, f32), byref(mod.c), _ptr(ws, None, "ws"),
+                                    ws.numel() * ws.element_size(), _stream(stream)), "dit_block_forward_fp4")
 
 
 def dit_denoise(model: DenoiseModel, img_tokens, txt_feats, sigmas: Sequence[float], txt_cos, txt_sin, img_cos,

@@ -931,6 +931,51 @@ int check_block_args(const dit_dims* d, const float* txt, int L, const float* im
   return DIT_OK;
 }
 
+// The 4-bit block on already-validated arguments: before each linear its bf16 activation is quantised into
+// one scratch matrix behind the block workspace, then the 4-bit product runs through the linear's epilogue.
+int run_block_fp4(const dit_dims* d, const dit_block_wfp4* w, float* txt, int L, float* img, int N, const float* tc,
+                  const float* ts, const float* ic, const float* is, const ModRef& mod, void* ws, cudaStream_t st) {
+  int* err = err_word();
+  if (!err) return DIT_ECUDA;
+  const int R = L + N, H = d->hidden, F = d->ffn;
+  const BlockWs b = carve_block_ws(d, R, ws);
+  auto linear = [&](int i, const uint16_t* x, int K, int epi, const GemmParams& g) -> int {
+    dit_fp4_matrix a;
+    carve_fp4(w->w[i].format, R, K, static_cast<uint8_t*>(ws) + b.bytes, &a);
+    const int r = fp4_quantize_launch(x, DIT_BF16, K, a, st);
+    return r == DIT_OK ? fp4_block_linear_launch(a, w->w[i], epi, g, st) : r;
+  };
+  auto gated = [&](int K, long long gate_row) {
+    GemmParams g = base_params(R, H, K, err);
+    g.txt = txt;
+    g.img = img;
+    g.L = L;
+    g.gate = mod.rows + gate_row * H;
+    g.map = mod.map;
+    g.gate_stride = 6LL * H;
+    return g;
+  };
+  int rc;
+  ModNormParams mp{txt, img, L, R, H, H, H, w->norm1, mod.rows, mod.rows + H, 6LL * H, mod.map, d->eps, b.h};
+  if ((rc = modnorm_launch(mp, st)) != DIT_OK) return rc;
+  if ((rc = linear(0, b.h, H, kEpiQKV, qkv_params(d, R, R, L, b, tc, ts, ic, is, w->q_norm, w->k_norm, err))) != DIT_OK)
+    return rc;
+  AttnParams ap{R, d->heads, d->head_dim, vt_stride(R), b.q, b.k, b.vt, b.o, err, 1, w->q_norm, w->k_norm, nullptr,
+                nullptr};
+  lend_h(ap, b, R, H);
+  if ((rc = attention_launch(ap, st)) != DIT_OK) return rc;
+  if ((rc = linear(1, b.o, H, kEpiGated, gated(H, 2))) != DIT_OK) return rc;
+  mp.w = w->norm2;
+  mp.shift = mod.rows + 3LL * H;
+  mp.scale = mod.rows + 4LL * H;
+  if ((rc = modnorm_launch(mp, st)) != DIT_OK) return rc;
+  GemmParams g = base_params(R, 2 * F, H, err);
+  g.out = b.a;
+  g.ldo = F;
+  if ((rc = linear(2, b.h, H, kEpiSwiGLU, g)) != DIT_OK) return rc;
+  return linear(3, b.a, F, kEpiGated, gated(F, 5));
+}
+
 }  // namespace
 
 int check_block_call_without_workspace(const dit_dims* d, const dit_block_w* w, const float* txt, int L,
@@ -1371,6 +1416,30 @@ size_t dit_linear_fp4_workspace_bytes(int format, int M, int N, int K) {
   if (M < 0 || N < 0 || K < 1 || (format != DIT_FP4_NV && format != DIT_FP4_MX)) return 0;
   dit_fp4_matrix a;
   return carve_fp4(format, M, K, nullptr, &a);
+}
+
+size_t dit_block_fp4_workspace_bytes(const dit_dims* d, int format, int L, int N) {
+  if (!dims_ok(d) || L < 0 || N < 1 || (long long)L + N > 0x7fffffffLL) return 0;
+  if (format != DIT_FP4_NV && format != DIT_FP4_MX) return 0;
+  dit_fp4_matrix a;
+  return carve_block_ws(d, L + N, nullptr).bytes + carve_fp4(format, L + N, std::max(d->hidden, d->ffn), nullptr, &a);
+}
+
+int dit_block_forward_fp4(const dit_dims* d, const dit_block_wfp4* w, float* txt, int L, float* img, int N,
+                          const float* tc, const float* ts, const float* ic, const float* is, const dit_mod* mod,
+                          void* ws, size_t ws_bytes, dit_stream_t stream) {
+  int rc = check_block_args(d, txt, L, img, N, tc, ts, ic, is, mod, ws, ws_bytes, 0);
+  if (rc != DIT_OK) return rc;
+  if (!w) return DIT_EINVAL;
+  for (int i = 0; i < 4; ++i) {
+    int n, k;
+    linear_shape(d, i, &n, &k);
+    if ((rc = check_fp4(&w->w[i])) != DIT_OK) return rc;
+    if (w->w[i].format != w->w[0].format || w->w[i].rows != n || w->w[i].cols != k) return DIT_EINVAL;
+  }
+  if (ws_bytes < dit_block_fp4_workspace_bytes(d, w->w[0].format, L, N)) return DIT_EWORKSPACE;
+  return run_block_fp4(d, w, txt, L, img, N, tc, ts, ic, is, ModRef{mod->rows, mod->map, mod->M}, ws,
+                       reinterpret_cast<cudaStream_t>(stream));
 }
 
 int dit_linear_fp4(const void* x, int x_type, int M, long long ldx, const dit_fp4_matrix* w, void* out, int out_type,

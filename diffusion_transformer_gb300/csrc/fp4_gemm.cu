@@ -16,8 +16,10 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "fp4.cuh"
+#include "gemm_epilogue.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 #include "tmap.h"
@@ -66,11 +68,21 @@ __host__ __device__ constexpr uint32_t pair_stage_bytes(int bn) {
   return kTileBytes + uint32_t(bn) * 64 + 3 * Scales<FMT>::kBytes;
 }
 
-template <int FMT, typename T, bool SWAP>
+// EPI: kEpiStoreF32 / kEpiStoreBF16 store the products, kEpiSwiGLU pairs of columns through SwiGLU as bf16;
+// kEpiQKV and kEpiGated are the bf16 GEMMs' epilogues on the scaled accumulator (bn = 128; `g` holds what
+// they need).
+struct NoParams {};
+constexpr bool epi_drains_tmem(int epi) { return epi == kEpiQKV || epi == kEpiGated; }
+template <int EPI>
+using EpiParams = typename std::conditional<epi_drains_tmem(EPI), GemmParams, NoParams>::type;
+
+template <int FMT, int EPI, bool SWAP>
 __global__ void __launch_bounds__(kPairThreads, 1)
     fp4_pair_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
                     const __grid_constant__ CUtensorMap tmSP, const __grid_constant__ CUtensorMap tmSQ,
-                    const Fp4Params p) {
+                    const Fp4Params p, const __grid_constant__ EpiParams<EPI> g) {
+  using T = typename std::conditional<EPI == kEpiStoreF32, float, __nv_bfloat16>::type;
+  constexpr bool kDrain = EPI == kEpiQKV || EPI == kEpiGated;
   using SC = Scales<FMT>;
   const int S = p.stages, bn = p.bn;
   const uint32_t qBytes = uint32_t(bn) * 64;
@@ -80,8 +92,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   uint8_t* sQ = sP + S * kTileBytes;
   uint8_t* sSP = sQ + S * qBytes;
   uint8_t* sSQ = sSP + S * SC::kBytes;
-  float* sC = reinterpret_cast<float*>(sSQ + S * 2 * SC::kBytes);  // 64 column factors per epilogue warp
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sC + kEpiWarps * 64);
+  // per epilogue warp: 64 column factors, or the 4 KB scratch of the draining epilogues
+  uint8_t* sC = sSQ + S * 2 * SC::kBytes;
+  constexpr int kScratch = kDrain ? 4096 : 256;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sC + kEpiWarps * kScratch);
   uint64_t *full = bars, *empty = bars + S, *tfull = bars + 2 * S, *tempty = tfull + 2, *drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
 
@@ -104,7 +118,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(smem_u32(&tfull[a]), 1);
-      mbar_init(smem_u32(&tempty[a]), 2 * 32 * kEpiWarps);  // both CTAs' epilogue threads
+      // both CTAs' epilogue threads (draining epilogues: the half that takes this accumulator)
+      mbar_init(smem_u32(&tempty[a]), 2 * 32 * kEpiWarps / (kDrain ? 2 : 1));
     }
     mbar_init(smem_u32(drain), 1);
     fence_mbar_init();
@@ -230,10 +245,42 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       umma_commit_pair(smem_u32(drain));
       mbar_wait(smem_u32(drain), 0, p.err, kErrTimeoutDrain);
     }
+  } else if constexpr (kDrain) {
+    // four warps to each accumulator, one per quadrant of 32 lanes, each draining all of its columns
+    const int quad = warp & 3, acc = (warp - 2) >> 2;
+    uint8_t* scratch = sC + (warp - 2) * kScratch;
+    const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[acc]), 0);
+    const uint32_t taddr = tmem + (uint32_t(quad * 32) << 16) + (acc ? acc1 : 0);
+    int it = acc;
+    for (int tile = unit + acc * units; tile < tiles; tile += 2 * units, it += 2) {
+      int pb, qb;
+      tile_pq(tile, pb, qb);
+      const int row0 = pb * 256 + int(rank) * 128 + quad * 32, row = row0 + lane, n0 = qb * 128;
+      if (!mbar_wait_warp(smem_u32(&tfull[acc]), uint32_t(it >> 1) & 1u, p.err, kErrTimeoutEpilogue)) break;
+      tc_fence_after();
+      if constexpr (SC::kNv) {
+        const float ra = row < p.M ? __ldg(p.a_scale + row) : 0.f;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          const float fb = __ldg(p.b_scale + n0 + c * 32 + lane);  // N is whole tiles here
+          uint32_t w[32];
+          tmem_ld32(taddr + c * 32, w);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            w[j] = __float_as_uint(__uint_as_float(w[j]) * ra * __shfl_sync(0xffffffffu, fb, j));
+          tmem_st32(taddr + c * 32, w);
+        }
+        tmem_st_wait();
+      }
+      epilogue_tile<128, EPI, false>(g, taddr, row0, p.M, lane, n0, scratch);
+      tc_fence_before();
+      mbar_arrive_cluster(tempty0);
+    }
   } else {
     // two warps to each quadrant of 32 lanes, taking its 64-column groups in turn
     const int quad = warp & 3, half = (warp - 2) >> 2, groups = bn / 64;
-    float* cf = sC + (warp - 2) * 64;
+    float* cf = reinterpret_cast<float*>(sC + (warp - 2) * kScratch);
     const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
     const float* p_scale = SWAP ? p.b_scale : p.a_scale;
     const float* q_scale = SWAP ? p.a_scale : p.b_scale;
@@ -306,6 +353,19 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
               for (int c = 0; c < 64; ++c)
                 if (q0 + c < rowsQ) o[c * p.ldo] = T(val(c));
+            }
+          }
+        } else if constexpr (EPI == kEpiSwiGLU) {
+          // out[p][q / 2] = silu(even column) * odd column (whole 64-column groups: N is a multiple of 256)
+          if (row < rowsP) {
+            T* o = static_cast<T*>(p.out) + (long long)row * p.ldo + q0 / 2;
+#pragma unroll
+            for (int c = 0; c < 64; c += 32) {
+              uint32_t u[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                u[e] = pack_bf16x2(silu_f(val(c + 4 * e)) * val(c + 4 * e + 1), silu_f(val(c + 4 * e + 2)) * val(c + 4 * e + 3));
+              st_global_256(o + c / 2, u);
             }
           }
         } else if (row < rowsP) {
@@ -586,25 +646,27 @@ bool tmap_sf(CUtensorMap* m, const dit_fp4_matrix& x, int box_groups, int box_ba
   return make_tmap_scales(m, x.scales, fp4_groups(x.format, x.cols), (x.rows + 127) / 128, box_groups, box_bands);
 }
 
-template <int FMT, typename T, bool SWAP>
-int launch_pair(const dit_fp4_matrix& a, const dit_fp4_matrix& b, Fp4Params p, int bn, cudaStream_t st) {
+template <int FMT, int EPI, bool SWAP>
+int launch_pair(const dit_fp4_matrix& a, const dit_fp4_matrix& b, Fp4Params p, const EpiParams<EPI>& g, int bn,
+                cudaStream_t st) {
   const dit_fp4_matrix &P = SWAP ? b : a, &Q = SWAP ? a : b;
   CUtensorMap mp, mq, msp, msq;
   constexpr int G = Scales<FMT>::kGroups;
   p.bn = bn;
-  p.stages = std::min(kMaxStages, int((227 * 1024 - kPairFixed) / pair_stage_bytes<FMT>(bn)));
-  const uint32_t smem = kPairFixed + uint32_t(p.stages) * pair_stage_bytes<FMT>(bn);
+  const uint32_t fixed = kPairFixed + (epi_drains_tmem(EPI) ? kEpiWarps * (4096 - 256) : 0);
+  p.stages = std::min(kMaxStages, int((227 * 1024 - fixed) / pair_stage_bytes<FMT>(bn)));
+  const uint32_t smem = fixed + uint32_t(p.stages) * pair_stage_bytes<FMT>(bn);
   if (!tmap_codes(&mp, P.codes, P.rows, p.K, 128) || !tmap_codes(&mq, Q.codes, Q.rows, p.K, bn / 2) ||
       !tmap_sf(&msp, P, G, 1) || !tmap_sf(&msq, Q, G, 2))
     return DIT_ECUDA;
   p.n_fast = P.rows > Q.rows;  // consecutive tiles share the smaller operand's rows, which stay in L2
-  auto kern = fp4_pair_kernel<FMT, T, SWAP>;
+  auto kern = fp4_pair_kernel<FMT, EPI, SWAP>;
   static std::atomic<uint64_t> ready{0};
   if (!allow_smem(reinterpret_cast<const void*>(kern), ready)) return DIT_ECUDA;
   const long long tiles = (long long)((P.rows + 255) / 256) * ((Q.rows + bn - 1) / bn);
   if (tiles > 0x7fffffffLL - num_sms()) return DIT_EUNSUPPORTED;
   const int units = int(std::min<long long>(tiles, num_sms() / 2));
-  const cudaError_t e = launch_pdl(kern, dim3(unsigned(2 * units)), dim3(kPairThreads), smem, st, 2, mp, mq, msp, msq, p);
+  const cudaError_t e = launch_pdl(kern, dim3(unsigned(2 * units)), dim3(kPairThreads), smem, st, 2, mp, mq, msp, msq, p, g);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? DIT_OK : DIT_ECUDA;
 }
 
@@ -677,13 +739,22 @@ int launch_product(const dit_fp4_matrix& a, const dit_fp4_matrix& b, const Fp4Pa
     }
   }
   if (parts > 0) return launch_split<FMT, T>(a, b, p, sn, parts, st);
-  return swap ? launch_pair<FMT, T, true>(a, b, p, bn, st) : launch_pair<FMT, T, false>(a, b, p, bn, st);
+  constexpr int kStore = sizeof(T) == 2 ? kEpiStoreBF16 : kEpiStoreF32;
+  return swap ? launch_pair<FMT, kStore, true>(a, b, p, {}, bn, st) : launch_pair<FMT, kStore, false>(a, b, p, {}, bn, st);
 }
 
-}  // namespace
+template <int FMT>
+int launch_block_linear(const dit_fp4_matrix& a, const dit_fp4_matrix& b, const Fp4Params& p, const GemmParams& g, int epi,
+                        cudaStream_t st) {
+  switch (epi) {
+    case kEpiQKV: return launch_pair<FMT, kEpiQKV, false>(a, b, p, g, 128, st);
+    case kEpiGated: return launch_pair<FMT, kEpiGated, false>(a, b, p, g, 128, st);
+    case kEpiSwiGLU: return launch_pair<FMT, kEpiSwiGLU, false>(a, b, p, {}, 256, st);
+    default: return DIT_EINVAL;
+  }
+}
 
-int fp4_matmul_launch(const dit_fp4_matrix& a, const dit_fp4_matrix& b, void* out, int type, long long ldo, int* err,
-                      bool b_early, cudaStream_t st) {
+Fp4Params product_params(const dit_fp4_matrix& a, const dit_fp4_matrix& b, void* out, long long ldo, int* err, bool b_early) {
   Fp4Params p{};
   p.M = a.rows;
   p.N = b.rows;
@@ -694,6 +765,22 @@ int fp4_matmul_launch(const dit_fp4_matrix& a, const dit_fp4_matrix& b, void* ou
   p.a_scale = a.row_scale;
   p.b_scale = b.row_scale;
   p.early = b_early;
+  return p;
+}
+
+}  // namespace
+
+int fp4_block_linear_launch(const dit_fp4_matrix& a, const dit_fp4_matrix& b, int epi, const GemmParams& g,
+                            cudaStream_t st) {
+  if (b.rows % (epi == kEpiSwiGLU ? 256 : 128) != 0 || (epi == kEpiQKV && 128 % g.head_dim != 0)) return DIT_EUNSUPPORTED;
+  const Fp4Params p = product_params(a, b, g.out, g.ldo, g.err, true);
+  return a.format == DIT_FP4_NV ? launch_block_linear<DIT_FP4_NV>(a, b, p, g, epi, st)
+                                : launch_block_linear<DIT_FP4_MX>(a, b, p, g, epi, st);
+}
+
+int fp4_matmul_launch(const dit_fp4_matrix& a, const dit_fp4_matrix& b, void* out, int type, long long ldo, int* err,
+                      bool b_early, cudaStream_t st) {
+  const Fp4Params p = product_params(a, b, out, ldo, err, b_early);
   if (a.format == DIT_FP4_NV)
     return type == DIT_BF16 ? launch_product<DIT_FP4_NV, __nv_bfloat16>(a, b, p, st)
                             : launch_product<DIT_FP4_NV, float>(a, b, p, st);

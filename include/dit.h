@@ -519,6 +519,27 @@ DIT_API int dit_linear_fp4(const void* x, int x_type, int M, long long ldx, cons
                            int out_type, long long ldo, void* ws, size_t ws_bytes, dit_stream_t stream);
 DIT_API size_t dit_linear_fp4_workspace_bytes(int format, int M, int N, int K);
 
+/* 4-bit weights of one block: the four linears (0 qkv, 1 out, 2 up, 3 down; row orders as in dit_block_w)
+ * quantised by dit_fp4_quantize, all in one format. Norm weights as in dit_block_w. */
+typedef struct {
+  dit_fp4_matrix w[4];
+  const float* norm1;
+  const float* norm2;
+  const float* q_norm;
+  const float* k_norm;
+} dit_block_wfp4;
+
+/* The sequential block with 4-bit linears (an opt-in lossy tier, below dit_block_forward_w8a8): before
+ * each linear its bf16 activation (h, o, h2, a) is quantised in the weights' format, and the 4-bit
+ * product runs through the linear's usual epilogue; everything else as dit_block_forward, including
+ * tables from dit_rotary_tables. Workspace: dit_block_fp4_workspace_bytes(dims, format, L, N), 256-byte
+ * aligned. Errors as dit_block_forward; DIT_EINVAL for weights of other sizes or mixed formats. */
+DIT_API int dit_block_forward_fp4(const dit_dims* dims, const dit_block_wfp4* w, float* txt, int L, float* img, int N,
+                                  const float* txt_cos, const float* txt_sin, const float* img_cos,
+                                  const float* img_sin, const dit_mod* mod, void* ws, size_t ws_bytes,
+                                  dit_stream_t stream);
+DIT_API size_t dit_block_fp4_workspace_bytes(const dit_dims* dims, int format, int L, int N);
+
 /* Denoise model: the 32 (or `blocks`) stacked blocks plus the plain DiT around them.
  *   w_in   [H, C] bf16    patch-in of the packed latent tokens (C = latent_channels)
  *   w_t1   [H, 256] bf16  time MLP first linear;  w_t2 [H, H] bf16 second linear

@@ -19,5 +19,5 @@ is "parity unpinned".
 
 from .dit import *  # noqa: F401,F403
 from .w8a8 import *  # noqa: F401,F403
-from .fp4 import e4m3_values, fp4_pack, fp4_quantize, fp4_values  # noqa: F401
+from .fp4 import block_forward_fp4_rows, e4m3_values, fp4_linear_f, fp4_pack, fp4_quantize, fp4_values  # noqa: F401
 from .rotary import rotary_apply, rotary_frequencies, rotary_tables  # noqa: F401

@@ -7,6 +7,9 @@ comparing with the midpoints of neighbouring values, rounding to an e4m3 scale b
 
 import numpy as np
 
+from .dit import (attention, bf16_rne_bits, bf16_to_f64, modulated_rmsnorm, qk_rmsnorm, rotate, swiglu_interleaved,
+                  _mod_rows)
+
 NV, MX = 0, 1
 BLOCK = {NV: 16, MX: 32}
 VALUES = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
@@ -109,3 +112,31 @@ def fp4_pack(codes, scale, fmt):
         padded[:nb] = scale[r]
         tiles[r // 128, :, r % 32, (r % 128) // 32, :] = padded.reshape(groups, 4)
     return packed, tiles.reshape(-1)
+
+
+def fp4_linear_f(x, wvalues, fmt):
+    """The 4-bit linear of an activation x (taken at its bfloat16 value, quantised per row) with the
+    values wvalues [out, in] that the quantised weight stands for; the product in float64."""
+    xb = bf16_to_f64(bf16_rne_bits(np.asarray(x, np.float64).astype(F32))).astype(F32)
+    v = fp4_values(*fp4_quantize(xb, fmt), fmt, xb.shape[1]).astype(np.float64)
+    return v @ np.asarray(wvalues, np.float64).T
+
+
+def block_forward_fp4_rows(x, wvalues, fmt, mod, mod_map, cos, sin, heads, head_dim, rows=None, norm1=None,
+                           norm2=None, q_norm=None, k_norm=None, eps=1e-6, qk_eps=1e-6):
+    """The AdaLN block (see oracle.dit.block_forward_rows for its nine steps) whose four linears (qkv, out,
+    up, down) are 4-bit ones: each activation (h, o, h2, a) enters at its bfloat16 value and is quantised
+    per row. wvalues: the four weights' values. Float64 otherwise; rows as in block_forward_rows."""
+    x = np.asarray(x, dtype=np.float64)
+    R, H = x.shape
+    nh, d = heads, head_dim
+    rows = np.arange(R) if rows is None else np.asarray(rows)
+    sa, ca, _, _, _, _ = _mod_rows(mod, mod_map, np.arange(R))
+    qkv = fp4_linear_f(modulated_rmsnorm(x, norm1, sa, ca, eps), wvalues[0], fmt)
+    q = rotate(qk_rmsnorm(qkv[:, :H].reshape(R, nh, d), q_norm, qk_eps), cos, sin)
+    k = rotate(qk_rmsnorm(qkv[:, H:2 * H].reshape(R, nh, d), k_norm, qk_eps), cos, sin)
+    o = attention(q, k, qkv[:, 2 * H:].reshape(R, nh, d), rows)
+    _, _, ga, sm, cm, gm = _mod_rows(mod, mod_map, rows)
+    xr = x[rows] + ga * fp4_linear_f(o, wvalues[1], fmt)
+    a = swiglu_interleaved(fp4_linear_f(modulated_rmsnorm(xr, norm2, sm, cm, eps), wvalues[2], fmt))
+    return xr + gm * fp4_linear_f(a, wvalues[3], fmt)

@@ -85,3 +85,22 @@ def test_layout_of_a_scale_byte():
     assert packed.shape == (200, 144) and packed[0, 0] == 0xC3 and len(tiles) == 2 * 3 * 512
     for r, b in ((0, 0), (31, 3), (32, 4), (127, 8), (128, 0), (199, 8)):
         assert tiles[((r // 128) * 3 + b // 4) * 512 + (r % 32) * 16 + (r % 128) // 32 * 4 + b % 4] == s[r, b]
+
+
+@pytest.mark.parametrize("fmt", [NV, MX])
+def test_block_with_exact_operands_is_the_plain_block(fmt, monkeypatch):
+    # with a quantiser that loses nothing the 4-bit block is the block of the same weights
+    import dit_inputs as DI
+    import oracle.fp4 as F
+    inp = DI.block_inputs("tiny")
+    sh = inp.shape
+    monkeypatch.setattr(F, "fp4_quantize", lambda x, f: (x, None, None))
+    monkeypatch.setattr(F, "fp4_values", lambda x, s, r, f, K: x)
+    W = [O.bf16_to_f64(w) for w in (inp.wqkv, inp.wout, inp.wup, inp.wdown)]
+    x = np.concatenate([inp.txt, inp.img])
+    cos, sin = O.rope_tables(O.positions(sh.L, sh.grid_h, sh.grid_w), sh.head_dim)
+    got = F.block_forward_fp4_rows(x, W, fmt, inp.mod, inp.mod_map, cos, sin, sh.heads, sh.head_dim, eps=sh.eps,
+                                   qk_eps=sh.qk_eps)
+    ref = np.concatenate(O.block_forward(inp))
+    # only the activations' rounding to bf16 (2^-8 each) is between them
+    assert np.abs(got - ref).max() <= 4 * 2.0 ** -8 * np.sqrt(np.mean(ref ** 2))
