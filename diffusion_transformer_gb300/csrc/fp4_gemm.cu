@@ -68,6 +68,17 @@ __host__ __device__ constexpr uint32_t pair_stage_bytes(int bn) {
   return kTileBytes + uint32_t(bn) * 64 + 3 * Scales<FMT>::kBytes;
 }
 
+// Four neighbouring products of one row times the row's factor, then times their columns' (two at a time,
+// each product rounded by itself).
+__device__ __forceinline__ void scale4(uint32_t* x, uint64_t row2, const float4& f) {
+  const uint64_t lo = f2_mul(f2_mul(f2_pack(__uint_as_float(x[0]), __uint_as_float(x[1])), row2), f2_pack(f.x, f.y));
+  const uint64_t hi = f2_mul(f2_mul(f2_pack(__uint_as_float(x[2]), __uint_as_float(x[3])), row2), f2_pack(f.z, f.w));
+  x[0] = uint32_t(lo);
+  x[1] = uint32_t(lo >> 32);
+  x[2] = uint32_t(hi);
+  x[3] = uint32_t(hi >> 32);
+}
+
 // EPI: kEpiStoreF32 / kEpiStoreBF16 store the products, kEpiSwiGLU pairs of columns through SwiGLU as bf16;
 // kEpiQKV and kEpiGated are the bf16 GEMMs' epilogues on the scaled accumulator (bn = 128; `g` holds what
 // they need).
@@ -259,18 +270,25 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       if (!mbar_wait_warp(smem_u32(&tfull[acc]), uint32_t(it >> 1) & 1u, p.err, kErrTimeoutEpilogue)) break;
       tc_fence_after();
       if constexpr (SC::kNv) {
+        float* cf = reinterpret_cast<float*>(scratch);  // the tile's 128 column factors (N is whole tiles here)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) cf[c * 32 + lane] = __ldg(p.b_scale + n0 + c * 32 + lane);
+        __syncwarp();
         const float ra = row < p.M ? __ldg(p.a_scale + row) : 0.f;
+        const uint64_t ra2 = f2_pack(ra, ra);
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
-          const float fb = __ldg(p.b_scale + n0 + c * 32 + lane);  // N is whole tiles here
           uint32_t w[32];
           tmem_ld32(taddr + c * 32, w);
           tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            w[j] = __float_as_uint(__uint_as_float(w[j]) * ra * __shfl_sync(0xffffffffu, fb, j));
+          for (int j = 0; j < 32; j += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(cf + c * 32 + j);
+            scale4(w + j, ra2, f);
+          }
           tmem_st32(taddr + c * 32, w);
         }
+        __syncwarp();
         tmem_st_wait();
       }
       epilogue_tile<128, EPI, false>(g, taddr, row0, p.M, lane, n0, scratch);
@@ -332,13 +350,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
           for (int c = 0; c < 64; c += 4) {
             const float4 f = *reinterpret_cast<const float4*>(cf + c);
-            uint32_t* x = w[c >> 5] + (c & 31);
-            const uint64_t lo = f2_mul(f2_mul(f2_pack(__uint_as_float(x[0]), __uint_as_float(x[1])), rp2), f2_pack(f.x, f.y));
-            const uint64_t hi = f2_mul(f2_mul(f2_pack(__uint_as_float(x[2]), __uint_as_float(x[3])), rp2), f2_pack(f.z, f.w));
-            x[0] = uint32_t(lo);
-            x[1] = uint32_t(lo >> 32);
-            x[2] = uint32_t(hi);
-            x[3] = uint32_t(hi >> 32);
+            scale4(w[c >> 5] + (c & 31), rp2, f);
           }
         }
         auto val = [&](int c) { return __uint_as_float(w[c >> 5][c & 31]); };
