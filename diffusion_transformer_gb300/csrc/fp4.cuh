@@ -121,6 +121,19 @@ __device__ __forceinline__ void fp4_values16(uint2 w, float* v) {
   }
 }
 
+// Eight fp32 values of global memory, as one 32-byte access where `whole` (32-byte aligned), else two of 16.
+__device__ __forceinline__ void ld_global_8(float (&v)[8], const float* p, bool whole) {
+  if (whole) {
+    asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                 : "l"(p));
+  } else {
+    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+}
+__device__ __forceinline__ bool on_32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 // 32 bytes of global memory (32-byte aligned) in one store
 __device__ __forceinline__ void st_global_256(void* p, const uint32_t (&w)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),

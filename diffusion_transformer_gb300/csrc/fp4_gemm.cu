@@ -19,7 +19,6 @@
 #include <type_traits>
 
 #include "fp4.cuh"
-#include "gemm_epilogue.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 #include "tmap.h"
@@ -79,21 +78,115 @@ __device__ __forceinline__ void scale4(uint32_t* x, uint64_t row2, const float4&
   x[3] = uint32_t(hi >> 32);
 }
 
-// EPI: kEpiStoreF32 / kEpiStoreBF16 store the products, kEpiSwiGLU pairs of columns through SwiGLU as bf16;
-// kEpiQKV and kEpiGated are the bf16 GEMMs' epilogues on the scaled accumulator (bn = 128; `g` holds what
-// they need).
+// z / (1 + e^-z); the approximate division is within two units of the fp32 result, which goes on to bf16
+__device__ __forceinline__ float silu_bf16(float z) { return __fdividef(z, 1.f + __expf(-z)); }
+
+// The QKV epilogue's part of one warp (the gizai:dit reference's prepOf; klein article, section 4.4): 128
+// columns of the product, one head of 128 or two of 64, in the registers of the lanes that own the rows.
+// Query and key heads are RMS-normed, weighted, rotated by the row's tables and stored head-major; value
+// heads are transposed through the warp's 4 KB of shared memory (chunks of 32 columns: 64 bytes per row,
+// 16-byte pieces swizzled by (row >> 1) & 3), so that a lane stores 32 rows of one value as 64 bytes.
+template <int D>
+__device__ __forceinline__ void qkv_store(const GemmParams& g, const uint32_t* w, int row0, int lane, int n0,
+                                          uint8_t* scratch) {
+  const int row = row0 + lane, H = g.H, R = g.M;
+  const int which = n0 / H, head = (n0 - which * H) / D;
+  auto val = [&](int c) { return __uint_as_float(w[c]); };
+  if (which == 2) {
+#pragma unroll
+    for (int c = 0; c < D; c += 32) {
+      __syncwarp();
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t u[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[e] = pack_bf16x2(val(c + 8 * q + 2 * e), val(c + 8 * q + 2 * e + 1));
+        *reinterpret_cast<uint4*>(scratch + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
+      }
+      __syncwarp();
+      uint32_t col[16];
+#pragma unroll
+      for (int r = 0; r < 32; ++r) {
+        const int at = r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2;
+        const uint32_t x = *reinterpret_cast<const uint16_t*>(scratch + at);
+        col[r >> 1] = r & 1 ? col[r >> 1] | x << 16 : x;
+      }
+      uint16_t* dst = g.vt + ((long long)head * D + c + lane) * g.Rp + row0;  // row0 % 32 == 0, Rp % 8 == 0
+      if (row0 + 32 <= R) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          reinterpret_cast<uint4*>(dst)[q] = make_uint4(col[4 * q], col[4 * q + 1], col[4 * q + 2], col[4 * q + 3]);
+      } else {
+#pragma unroll
+        for (int r = 0; r < 32; ++r)
+          if (row0 + r < R) dst[r] = uint16_t(r & 1 ? col[r >> 1] >> 16 : col[r >> 1]);
+      }
+    }
+    return;
+  }
+  if (row >= R) return;
+  float ss = 0.f;
+#pragma unroll
+  for (int c = 0; c < D; ++c) ss = fmaf(val(c), val(c), ss);
+  const float rstd = rsqrtf(ss / float(D) + g.qk_eps);
+  const float* wn = which == 0 ? g.q_norm : g.k_norm;
+  const int tw = g.rope_split ? 3 * D / 8 : D / 2;
+  const float* cs = row < g.L ? g.txt_cos + (long long)row * tw : g.img_cos + (long long)(row - g.L) * tw;
+  const float* sn = row < g.L ? g.txt_sin + (long long)row * tw : g.img_sin + (long long)(row - g.L) * tw;
+  uint16_t* dst = (which == 0 ? g.q : g.k) + ((long long)head * R + row) * D;
+  auto normed = [&](int c) { return wn ? val(c) * rstd * __ldg(wn + c) : val(c) * rstd; };
+  if (!g.rope_split) {
+    const bool whole = on_32(cs) && on_32(sn);  // the lanes are on different rows: fewer, wider accesses
+#pragma unroll
+    for (int c = 0; c < D; c += 16) {
+      float cc[8], ss8[8];
+      ld_global_8(cc, cs + c / 2, whole);
+      ld_global_8(ss8, sn + c / 2, whole);
+      uint32_t u[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float x = normed(c + 2 * e), y = normed(c + 2 * e + 1);
+        u[e] = pack_bf16x2(x * cc[e] - y * ss8[e], x * ss8[e] + y * cc[e]);
+      }
+      st_global_256(dst + c, u);
+    }
+  } else {
+    constexpr int hr = 3 * D / 8;  // values i and i + hr by angle i; the last quarter only normed
+#pragma unroll
+    for (int c = 0; c < hr; c += 8) {
+      float x[8], y[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float p = normed(c + e), q = normed(c + hr + e), t = __ldg(cs + c + e), s = __ldg(sn + c + e);
+        x[e] = p * t - q * s;
+        y[e] = p * s + q * t;
+      }
+      *reinterpret_cast<uint4*>(dst + c) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                                      pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+      *reinterpret_cast<uint4*>(dst + c + hr) = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
+                                                           pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+    }
+#pragma unroll
+    for (int c = 2 * hr; c < D; c += 8)
+      *reinterpret_cast<uint4*>(dst + c) =
+          make_uint4(pack_bf16x2(normed(c), normed(c + 1)), pack_bf16x2(normed(c + 2), normed(c + 3)),
+                     pack_bf16x2(normed(c + 4), normed(c + 5)), pack_bf16x2(normed(c + 6), normed(c + 7)));
+  }
+}
+
+// EPI: kEpiStoreF32 / kEpiStoreBF16 store the products; kEpiSwiGLU takes pairs of columns through SwiGLU,
+// kEpiGated adds gate * product to the residual rows, kEpiQKV prepares queries, keys and values: a block's
+// linears, with bn = 256, whole tiles of columns, and `ep` holding what their epilogues need.
 struct NoParams {};
-constexpr bool epi_drains_tmem(int epi) { return epi == kEpiQKV || epi == kEpiGated; }
 template <int EPI>
-using EpiParams = typename std::conditional<epi_drains_tmem(EPI), GemmParams, NoParams>::type;
+using EpiParams = typename std::conditional<EPI == kEpiQKV || EPI == kEpiGated, GemmParams, NoParams>::type;
 
 template <int FMT, int EPI, bool SWAP>
 __global__ void __launch_bounds__(kPairThreads, 1)
     fp4_pair_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
                     const __grid_constant__ CUtensorMap tmSP, const __grid_constant__ CUtensorMap tmSQ,
-                    const Fp4Params p, const __grid_constant__ EpiParams<EPI> g) {
+                    const Fp4Params p, const __grid_constant__ EpiParams<EPI> ep) {
   using T = typename std::conditional<EPI == kEpiStoreF32, float, __nv_bfloat16>::type;
-  constexpr bool kDrain = EPI == kEpiQKV || EPI == kEpiGated;
   using SC = Scales<FMT>;
   const int S = p.stages, bn = p.bn;
   const uint32_t qBytes = uint32_t(bn) * 64;
@@ -103,9 +196,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   uint8_t* sQ = sP + S * kTileBytes;
   uint8_t* sSP = sQ + S * qBytes;
   uint8_t* sSQ = sSP + S * SC::kBytes;
-  // per epilogue warp: 64 column factors, or the 4 KB scratch of the draining epilogues
+  // per epilogue warp: 64 column factors, or (QKV) 128 of them and then 4 KB to transpose values in
   uint8_t* sC = sSQ + S * 2 * SC::kBytes;
-  constexpr int kScratch = kDrain ? 4096 : 256;
+  constexpr int kScratch = EPI == kEpiQKV ? 4096 : 256;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sC + kEpiWarps * kScratch);
   uint64_t *full = bars, *empty = bars + S, *tfull = bars + 2 * S, *tempty = tfull + 2, *drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -129,8 +222,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(smem_u32(&tfull[a]), 1);
-      // both CTAs' epilogue threads (draining epilogues: the half that takes this accumulator)
-      mbar_init(smem_u32(&tempty[a]), 2 * 32 * kEpiWarps / (kDrain ? 2 : 1));
+      mbar_init(smem_u32(&tempty[a]), 2 * 32 * kEpiWarps);  // both CTAs' epilogue threads
     }
     mbar_init(smem_u32(drain), 1);
     fence_mbar_init();
@@ -256,44 +348,49 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       umma_commit_pair(smem_u32(drain));
       mbar_wait(smem_u32(drain), 0, p.err, kErrTimeoutDrain);
     }
-  } else if constexpr (kDrain) {
-    // four warps to each accumulator, one per quadrant of 32 lanes, each draining all of its columns
-    const int quad = warp & 3, acc = (warp - 2) >> 2;
+  } else if constexpr (EPI == kEpiQKV) {
+    // two warps to each quadrant of 32 lanes, 128 columns each, all of them in registers at once: the
+    // accumulator is free as soon as every warp has loaded its part
+    const int quad = warp & 3, half = (warp - 2) >> 2;
     uint8_t* scratch = sC + (warp - 2) * kScratch;
-    const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[acc]), 0);
-    const uint32_t taddr = tmem + (uint32_t(quad * 32) << 16) + (acc ? acc1 : 0);
-    int it = acc;
-    for (int tile = unit + acc * units; tile < tiles; tile += 2 * units, it += 2) {
+    float* cf = reinterpret_cast<float*>(scratch);
+    const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
+    int it = 0;
+    for (int tile = unit; tile < tiles; tile += units, ++it) {
       int pb, qb;
       tile_pq(tile, pb, qb);
-      const int row0 = pb * 256 + int(rank) * 128 + quad * 32, row = row0 + lane, n0 = qb * 128;
-      if (!mbar_wait_warp(smem_u32(&tfull[acc]), uint32_t(it >> 1) & 1u, p.err, kErrTimeoutEpilogue)) break;
-      tc_fence_after();
+      const int acc = it & 1, row0 = pb * 256 + int(rank) * 128 + quad * 32, row = row0 + lane;
+      const int n0 = qb * 256 + half * 128;
+      float rp = 1.f;
       if constexpr (SC::kNv) {
-        float* cf = reinterpret_cast<float*>(scratch);  // the tile's 128 column factors (N is whole tiles here)
+        rp = row < rowsP ? __ldg(p.a_scale + row) : 0.f;
+        __syncwarp();
 #pragma unroll
         for (int c = 0; c < 4; ++c) cf[c * 32 + lane] = __ldg(p.b_scale + n0 + c * 32 + lane);
         __syncwarp();
-        const float ra = row < p.M ? __ldg(p.a_scale + row) : 0.f;
-        const uint64_t ra2 = f2_pack(ra, ra);
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t w[32];
-          tmem_ld32(taddr + c * 32, w);
-          tmem_ld_wait();
-#pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(cf + c * 32 + j);
-            scale4(w + j, ra2, f);
-          }
-          tmem_st32(taddr + c * 32, w);
-        }
-        __syncwarp();
-        tmem_st_wait();
       }
-      epilogue_tile<128, EPI, false>(g, taddr, row0, p.M, lane, n0, scratch);
+      if (!mbar_wait_warp(smem_u32(&tfull[acc]), uint32_t(it >> 1) & 1u, p.err, kErrTimeoutEpilogue)) break;
+      tc_fence_after();
+      const uint32_t taddr = tmem + (uint32_t(quad * 32) << 16) + (acc ? acc1 : 0) + half * 128;
+      uint32_t w[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(taddr + c * 32, w[c]);
+      tmem_ld_wait();
       tc_fence_before();
-      mbar_arrive_cluster(tempty0);
+      mbar_arrive_cluster(tempty0 + uint32_t(acc) * 8u);
+      if (row0 >= rowsP) continue;
+      if constexpr (SC::kNv) {
+        const uint64_t rp2 = f2_pack(rp, rp);
+#pragma unroll
+        for (int c = 0; c < 128; c += 4) scale4(w[c >> 5] + (c & 31), rp2, *reinterpret_cast<const float4*>(cf + c));
+      }
+      if (ep.head_dim == 128) {
+        qkv_store<128>(ep, w[0], row0, lane, n0, scratch);
+      } else {
+        qkv_store<64>(ep, w[0], row0, lane, n0, scratch);
+        qkv_store<64>(ep, w[2], row0, lane, n0 + 64, scratch);
+      }
+      __syncwarp();
     }
   } else {
     // two warps to each quadrant of 32 lanes, taking its 64-column groups in turn
@@ -376,8 +473,37 @@ __global__ void __launch_bounds__(kPairThreads, 1)
               uint32_t u[8];
 #pragma unroll
               for (int e = 0; e < 8; ++e)
-                u[e] = pack_bf16x2(silu_f(val(c + 4 * e)) * val(c + 4 * e + 1), silu_f(val(c + 4 * e + 2)) * val(c + 4 * e + 3));
+                u[e] = pack_bf16x2(silu_bf16(val(c + 4 * e)) * val(c + 4 * e + 1),
+                                   silu_bf16(val(c + 4 * e + 2)) * val(c + 4 * e + 3));
               st_global_256(o + c / 2, u);
+            }
+          }
+        } else if constexpr (EPI == kEpiGated) {
+          // x[p][q] += gate[map[p]][q] * product (the gizai:dit reference's gatedInto)
+          if (row < rowsP) {
+            float* x = (row < ep.L ? ep.txt + (long long)row * ep.N : ep.img + (long long)(row - ep.L) * ep.N) + q0;
+            const float* gate = ep.gate + (ep.map ? __ldg(ep.map + row) : 0) * ep.gate_stride + q0;
+            const bool wx = on_32(x), wg = on_32(gate);
+#pragma unroll
+            for (int h = 0; h < 64; h += 32) {
+              float xv[4][8], gv[4][8];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                ld_global_8(xv[e], x + h + 8 * e, wx);
+                ld_global_8(gv[e], gate + h + 8 * e, wg);
+              }
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                uint32_t u[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) u[k] = __float_as_uint(fmaf(gv[e][k], val(h + 8 * e + k), xv[e][k]));
+                if (wx) {
+                  st_global_256(x + h + 8 * e, u);
+                } else {
+                  reinterpret_cast<uint4*>(x + h + 8 * e)[0] = make_uint4(u[0], u[1], u[2], u[3]);
+                  reinterpret_cast<uint4*>(x + h + 8 * e)[1] = make_uint4(u[4], u[5], u[6], u[7]);
+                }
+              }
             }
           }
         } else if (row < rowsP) {
@@ -665,7 +791,7 @@ int launch_pair(const dit_fp4_matrix& a, const dit_fp4_matrix& b, Fp4Params p, c
   CUtensorMap mp, mq, msp, msq;
   constexpr int G = Scales<FMT>::kGroups;
   p.bn = bn;
-  const uint32_t fixed = kPairFixed + (epi_drains_tmem(EPI) ? kEpiWarps * (4096 - 256) : 0);
+  const uint32_t fixed = kPairFixed + (EPI == kEpiQKV ? kEpiWarps * (4096 - 256) : 0);
   p.stages = std::min(kMaxStages, int((227 * 1024 - fixed) / pair_stage_bytes<FMT>(bn)));
   const uint32_t smem = fixed + uint32_t(p.stages) * pair_stage_bytes<FMT>(bn);
   if (!tmap_codes(&mp, P.codes, P.rows, p.K, 128) || !tmap_codes(&mq, Q.codes, Q.rows, p.K, bn / 2) ||
@@ -759,8 +885,8 @@ template <int FMT>
 int launch_block_linear(const dit_fp4_matrix& a, const dit_fp4_matrix& b, const Fp4Params& p, const GemmParams& g, int epi,
                         cudaStream_t st) {
   switch (epi) {
-    case kEpiQKV: return launch_pair<FMT, kEpiQKV, false>(a, b, p, g, 128, st);
-    case kEpiGated: return launch_pair<FMT, kEpiGated, false>(a, b, p, g, 128, st);
+    case kEpiQKV: return launch_pair<FMT, kEpiQKV, false>(a, b, p, g, 256, st);
+    case kEpiGated: return launch_pair<FMT, kEpiGated, false>(a, b, p, g, 256, st);
     case kEpiSwiGLU: return launch_pair<FMT, kEpiSwiGLU, false>(a, b, p, {}, 256, st);
     default: return DIT_EINVAL;
   }
@@ -784,7 +910,7 @@ Fp4Params product_params(const dit_fp4_matrix& a, const dit_fp4_matrix& b, void*
 
 int fp4_block_linear_launch(const dit_fp4_matrix& a, const dit_fp4_matrix& b, int epi, const GemmParams& g,
                             cudaStream_t st) {
-  if (b.rows % (epi == kEpiSwiGLU ? 256 : 128) != 0 || (epi == kEpiQKV && 128 % g.head_dim != 0)) return DIT_EUNSUPPORTED;
+  if (b.rows % 256 != 0 || (epi == kEpiQKV && g.head_dim != 64 && g.head_dim != 128)) return DIT_EUNSUPPORTED;
   const Fp4Params p = product_params(a, b, g.out, g.ldo, g.err, true);
   return a.format == DIT_FP4_NV ? launch_block_linear<DIT_FP4_NV>(a, b, p, g, epi, st)
                                 : launch_block_linear<DIT_FP4_MX>(a, b, p, g, epi, st);

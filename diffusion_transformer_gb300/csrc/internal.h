@@ -210,7 +210,7 @@ int fp4_dequantize_launch(const dit_fp4_matrix& m, void* out, int type, long lon
 int fp4_matmul_launch(const dit_fp4_matrix& a, const dit_fp4_matrix& b, void* out, int type, long long ldo, int* err,
                       bool b_early, cudaStream_t stream);
 // A block's linear a b^T through kEpiQKV, kEpiSwiGLU or kEpiGated (g.out, g.ldo, g.err and what the epilogue
-// reads; b as with b_early), for the widths a block has: b->rows a multiple of 128 (SwiGLU 256).
+// reads; b as with b_early), for the widths a block has: b->rows a multiple of 256.
 int fp4_block_linear_launch(const dit_fp4_matrix& a, const dit_fp4_matrix& b, int epi, const GemmParams& g,
                             cudaStream_t stream);
 
