@@ -69,9 +69,11 @@ struct BlockWs {
   size_t bytes;
 };
 
+constexpr int kFp4MaxSize = 1 << 30;  // rows and columns: tile indexes stay within 32 bits
 // A 4-bit matrix a caller hands over: format, sizes, pointers and their alignment.
 int check_fp4(const dit_fp4_matrix* m) {
   if (!m || (m->format != DIT_FP4_NV && m->format != DIT_FP4_MX) || m->rows < 0 || m->cols < 1) return DIT_EINVAL;
+  if (m->rows > kFp4MaxSize || m->cols > kFp4MaxSize) return DIT_EUNSUPPORTED;
   if (m->rows == 0) return DIT_OK;
   if (!m->codes || !m->scales || !al16(m->codes) || !al16(m->scales)) return DIT_EINVAL;
   if (m->format == DIT_FP4_NV && (!m->row_scale || reinterpret_cast<uintptr_t>(m->row_scale) % 4)) return DIT_EINVAL;
@@ -1447,6 +1449,7 @@ int dit_linear_fp4(const void* x, int x_type, int M, long long ldx, const dit_fp
   int rc = check_fp4(w);
   if (rc != DIT_OK) return rc;
   if (M < 0) return DIT_EINVAL;
+  if (M > kFp4MaxSize) return DIT_EUNSUPPORTED;
   if (M == 0 || w->rows == 0) return DIT_OK;
   if (!fp4_rows_ok(x, x_type, ldx, M, w->cols) || !fp4_rows_ok(out, out_type, ldo, M, w->rows)) return DIT_EINVAL;
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u)) return DIT_EINVAL;

@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 // ---------------------------------------------------------------------------------------------
 constexpr int kSplitThreads = 192;
 constexpr uint32_t kSplitMinSmem = 116 * 1024;
-constexpr int kSplitMaxStages = 12;
+constexpr int kSplitMaxStages = 12, kMaxGridY = 65535;
 constexpr uint32_t kSplitFixed = 1024 + 2 * 128 * 4 + 8 * (2 * kSplitMaxStages + 1) + 16;
 __host__ __device__ constexpr uint32_t split_stage_bytes(int bn, uint32_t sf) { return kTileBytes + uint32_t(bn) * 128 + 2 * sf; }
 
@@ -813,7 +813,7 @@ int launch_split(const dit_fp4_matrix& a, const dit_fp4_matrix& b, Fp4Params p, 
   constexpr int G = Scales<FMT>::kGroups;
   p.bn = bn;
   const long long nt = (p.N + 127) / 128, mt = (p.M + bn - 1) / bn;
-  if (nt * parts > 0x7fffffffLL || mt > 65535) return DIT_EUNSUPPORTED;
+  if (nt * parts > 0x7fffffffLL || mt > kMaxGridY) return DIT_EUNSUPPORTED;
   const int KB = (p.K + kStageK - 1) / kStageK;
   const uint32_t sb = split_stage_bytes(bn, Scales<FMT>::kBytes);
   // A cluster's CTA asks for more than half of an SM's shared memory, as every kernel here that allocates
@@ -868,7 +868,7 @@ int launch_product(const dit_fp4_matrix& a, const dit_fp4_matrix& b, const Fp4Pa
     }
   const int sn = p.M <= 16 ? 16 : (p.M <= 32 ? 32 : (p.M <= 64 ? 64 : 128));
   const long long ctas = up(p.N, 128) * up(p.M, sn);
-  for (int k = 1; k <= 8 && k <= KB && (k == 1 || ctas * k <= sms); k *= 2) {
+  for (int k = 1; k <= 8 && k <= KB && (k == 1 || ctas * k <= sms) && up(p.M, sn) <= kMaxGridY; k *= 2) {
     const long long busy = up(ctas * k, sms) * (10 * sn + up(KB, k) * (60 + 8 * sn / 5));
     const long long cost = 2200 + std::max(busy, (long long)p.N * p.K / 9800) + (k > 1 ? 1800 + 5 * sn : 0);
     if (cost < best) {

@@ -489,7 +489,8 @@ DIT_API int dit_rotary(const dit_rotary_plan* plan, const dit_rotary_rows* q, co
  * padded with zero codes to whole 32 columns; scales in tiles of 128 rows x 4 blocks of 512 bytes, the
  * tiles of a 128-row band one after another, row r of a tile at byte 16 (r % 32) + 4 (r / 32), its four
  * blocks consecutive (blocks past cols: zero; bytes of rows past the last are not written and never
- * matter); row_scale [rows] fp32 (NV; ignored for MX). codes and scales 16-byte aligned. */
+ * matter); row_scale [rows] fp32 (NV; ignored for MX). codes and scales 16-byte aligned. Rows and cols up to
+ * 2^30 (DIT_EUNSUPPORTED above). */
 #define DIT_FP4_NV 0
 #define DIT_FP4_MX 1
 typedef struct {

@@ -228,6 +228,77 @@ def test_empty_and_streams_and_graph():
     _check_product(out, O.fp4_values(codes, scale, row, NV, 256).astype(np.float64), wv, 256)
 
 
+def test_offsets_past_32_bits():
+    g = np.random.default_rng(7)
+    ld, R, K, N = 1_100_000_016, 3, 96, 64
+    x = _rows(g, R, K)
+    mem = torch.empty(2 * ld + 4096, dtype=torch.bfloat16, device="cuda")
+    xd = torch.as_strided(mem, (R, K), (ld, 1))
+    xd.copy_(torch.from_numpy(x))
+    m = D.Fp4Matrix.empty(NV, R, K)
+    D.dit_fp4_quantize(xd, m)
+    codes, scale, row = _check_quantised(m, x, NV)
+    back = torch.as_strided(mem, (R, K), (ld, 1), 2048)
+    D.dit_fp4_dequantize(m, back)
+    v = O.fp4_values(codes, scale, row, NV, K)
+    assert np.array_equal(back.float().cpu().numpy(), torch.from_numpy(v).bfloat16().float().numpy())
+    w, wv = _quantised(_rows(g, N, K), NV)
+    out = torch.as_strided(mem, (R, N), (ld, 1), 1024)
+    D.dit_fp4_matmul(m, w, out)
+    _check_product(out, v.astype(np.float64), wv, K)
+    # many rows, so that the pair kernel stores them: 1300 rows of 2^21 values
+    a, av = _quantised(_rows(g, 1300, K), MX)
+    b, bv = _quantised(_rows(g, 1100, K), MX)
+    out = torch.as_strided(mem, (1300, 1100), (1 << 20, 1))
+    D.dit_fp4_matmul(a, b, out)
+    D.dit_check()
+    _check_product(out, av, bv, K)
+
+
+def test_two_streams_at_once():
+    # two streams with products of both kernels, each with its own workspace, give what one alone gives
+    g = np.random.default_rng(11)
+    jobs = []
+    for M, N, K in ((1300, 1536, 512), (20, 512, 4096), (900, 2048, 768), (64, 3000, 2000)):
+        w, _ = _quantised(_rows(g, N, K), NV)
+        x = dev(_rows(g, M, K)).bfloat16()
+        jobs.append((x, w, workspace(D.dit_linear_fp4_workspace_bytes(NV, M, N, K)), torch.empty(M, N, device="cuda")))
+    want = []
+    for x, w, ws, out in jobs:
+        D.dit_linear_fp4(x, w, out, ws)
+        want.append(out.clone())
+        out.zero_()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(20):
+        for i, (x, w, ws, out) in enumerate(jobs):
+            D.dit_linear_fp4(x, w, out, ws, stream=streams[i % 2])
+    torch.cuda.synchronize()
+    D.dit_check()
+    for (x, w, ws, out), ref in zip(jobs, want):
+        assert torch.equal(out, ref)
+
+
+def test_quantise_then_use_at_once():
+    # a weight quantised by the call just before the linear is complete when the linear reads it
+    g = np.random.default_rng(12)
+    M, N, K = 48, 4096, 2048
+    x, w = dev(_rows(g, M, K)).bfloat16(), dev(_rows(g, N, K)).bfloat16()
+    m, ws = D.Fp4Matrix.empty(NV, N, K), workspace(D.dit_linear_fp4_workspace_bytes(NV, M, N, K))
+    ref, out = torch.empty(M, N, device="cuda"), torch.empty(M, N, device="cuda")
+    D.dit_fp4_quantize(w, m)
+    torch.cuda.synchronize()
+    D.dit_linear_fp4(x, m, ref, ws)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        m.codes.fill_(0x77)
+        m.row_scale.fill_(float("nan"))
+        D.dit_fp4_quantize(w, m)
+        D.dit_linear_fp4(x, m, out, ws)
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref)
+
+
 def test_binding_refusals():
     w = D.Fp4Matrix.empty(NV, 8, 64)
     x, out, ws = torch.zeros(4, 64, device="cuda"), torch.zeros(4, 8, device="cuda"), workspace(1 << 16)

@@ -159,6 +159,95 @@ def test_block_sizes(fmt, H, heads, F, L, N):
            8e-2, 2e-1, f"fp4 block {H} {heads} {F} {L}+{N}")
 
 
+def _small(g, H, heads, F, R, fmt, rope_split=False, weights=False):
+    d = H // heads
+    dims = D.DitDims(H, heads, d, F, rope_split=rope_split)
+    t = lambda *s: torch.from_numpy(g.standard_normal(s).astype(np.float32)).cuda()  # noqa: E731
+    mats = []
+    for s in ((3 * H, H), (H, H), (2 * F, H), (H, F)):
+        m = D.Fp4Matrix.empty(fmt, *s)
+        D.dit_fp4_quantize((t(*s) * 0.05).bfloat16(), m)
+        mats.append(m)
+    nw = [1 + 0.2 * t(n) for n in (H, H, d, d)] if weights else [None] * 4
+    ang = t(R, 3 * d // 8 if rope_split else d // 2) * 2
+    return dims, mats, nw, t(R, H), t(3, 6, H) * 0.1, torch.from_numpy(g.integers(0, 3, R).astype(np.int32)).cuda(), ang
+
+
+@FMT
+@pytest.mark.parametrize("heads", [2, 4])
+def test_block_with_norm_weights_and_split_halves(fmt, heads):
+    # the first linear's epilogue against dit_qkv_rope's on the same values: the bf16 linear of the dequantised
+    # weights, from a residual stream whose 4-bit codes lose nothing (h a multiple of the grid)
+    H, R, d = 256, 150, 256 // heads
+    g = np.random.default_rng(heads)
+    for rope_split in (False, True):
+        dims, mats, nw, x, rows, mp, ang = _small(g, H, heads, 256, R, fmt, rope_split, True)
+        w = D.Fp4BlockWeights(mats, *nw)
+        c, s = ang.cos(), ang.sin()
+        img, ws = x.clone(), workspace(D.dit_block_fp4_workspace_bytes(dims, fmt, 0, R))
+        D.dit_block_forward_fp4(dims, w, None, img, None, None, c, s, D.Modulation(rows, mp), ws)
+        D.dit_check()
+        # step by step: the library's norm, 4-bit linears, attention; torch for what lies between
+        m = rows[mp.long()]
+        lws = workspace(max(D.dit_linear_fp4_workspace_bytes(fmt, R, a.rows, a.cols) for a in mats))
+
+        def lin(i, t):
+            o = torch.empty(R, mats[i].rows, device="cuda")
+            D.dit_linear_fp4(t, mats[i], o, lws)
+            return o
+
+        def norm(t, which, wn):
+            return (t * torch.rsqrt(t.pow(2).mean(-1, keepdim=True) + 1e-6) * wn * (1 + m[:, which + 1]) + m[:, which]).bfloat16()
+
+        qkv = lin(0, norm(x, 0, nw[0])).view(R, 3, heads, d)
+        q, k = (t * torch.rsqrt(t.pow(2).mean(-1, keepdim=True) + 1e-6) * wn for t, wn in ((qkv[:, 0], nw[2]), (qkv[:, 1], nw[3])))
+
+        def rot(t):
+            cc, ss = c[:, None], s[:, None]
+            if rope_split:
+                n = 3 * d // 8
+                a, b = t[..., :n], t[..., n:2 * n]
+                return torch.cat([a * cc - b * ss, a * ss + b * cc, t[..., 2 * n:]], -1)
+            a, b = t[..., ::2], t[..., 1::2]
+            return torch.stack([a * cc - b * ss, a * ss + b * cc], -1).flatten(-2)
+
+        q, k = (rot(t).bfloat16().transpose(0, 1).contiguous() for t in (q, k))
+        vt = torch.zeros(heads, d, D.dit_vt_stride(R), dtype=torch.bfloat16, device="cuda")
+        vt[:, :, :R] = qkv[:, 2].bfloat16().permute(1, 2, 0)
+        o = torch.empty(R, H, dtype=torch.bfloat16, device="cuda")
+        D.dit_attention_qknorm(dims, R, q, k, vt, nw[2], nw[3], o)
+        y = x + m[:, 2] * lin(1, o)
+        u = lin(2, norm(y, 3, nw[1]))
+        y = y + m[:, 5] * lin(3, (torch.nn.functional.silu(u[:, ::2]) * u[:, 1::2]).bfloat16())
+        f64 = lambda t: t.cpu().numpy().astype(np.float64)  # noqa: E731
+        _check(f64(img), f64(y), f64(x), 8e-2, 2e-1, f"fp4 block weights split={rope_split} d={d}")
+
+
+def test_block_on_16_byte_boundaries():
+    # residual rows, tables and modulation rows that start on 16 bytes and not on 32: the same bits
+    g = np.random.default_rng(9)
+    R, L = 140, 9
+    dims, mats, nw, x, rows, mp, ang = _small(g, 256, 2, 128, R, NV, weights=True)
+    w = D.Fp4BlockWeights(mats, *nw)
+
+    def at(t, shift):
+        mem = torch.empty(t.numel() + 16, dtype=t.dtype, device="cuda")
+        v = mem[shift:shift + t.numel()].view(t.shape)
+        v.copy_(t)
+        return v
+
+    def run(shift):
+        c, s = ang.cos(), ang.sin()
+        parts = [at(t, shift) for t in (c[:L], s[:L], c[L:], s[L:])]
+        txt, img, mod = at(x[:L], shift), at(x[L:], shift), D.Modulation(at(rows, shift), mp)
+        ws = workspace(D.dit_block_fp4_workspace_bytes(dims, NV, L, R - L))
+        D.dit_block_forward_fp4(dims, w, txt, img, *parts, mod, ws)
+        D.dit_check()
+        return torch.cat([txt, img])
+
+    assert torch.equal(run(0), run(4))
+
+
 def test_linear_rotary_attention_linear_together():
     # modulated norm -> 4-bit QKV -> rotary, head-major -> attention -> 4-bit output projection
     R, heads, d = 200, 4, 64

@@ -155,6 +155,37 @@ def test_tables_feed_the_blocks_rotary():
     assert (a - c).abs().max() <= 2.0 ** -22 and (b - e).abs().max() <= 2.0 ** -22
 
 
+@pytest.mark.parametrize("B,T,Hq,Hk,d", [(1, 3000, 3, 1, 64), (700, 1, 2, 2, 128), (4, 9, 70, 0, 32), (2, 500, 1, 1, 16)])
+def test_rotary_many_rows_and_heads(B, T, Hq, Hk, d):
+    # rows grouped in a CTA, batches of single rows, more units than threads, one tensor alone
+    g = np.random.default_rng(B + T)
+    plan, pos = D.RotaryPlan([d // 2], layout="halves"), _positions(g, (B, T, 1), 10 ** 6)
+    q, k = (torch.from_numpy(g.standard_normal((B, T, h, d)).astype(np.float32)).bfloat16() for h in (Hq, Hk))
+    qd, kd = q.cuda(), k.cuda()
+    qo, ko = torch.empty(B, Hq, T, d, dtype=q.dtype, device="cuda"), torch.empty_like(kd)
+    D.dit_rotary(plan, qd, kd if Hk else None, dev(pos), qo.transpose(1, 2), ko if Hk else None)
+    for x, y in ((q, qo.transpose(1, 2)), (k, ko))[:2 if Hk else 1]:
+        x64 = x.float().numpy().astype(np.float64)
+        ref, mag, dim = _expected(dict(widths=[d // 2], layout="halves"), x64, pos, False)
+        _check(y, ref, mag, dim, x64, torch.bfloat16)
+    D.dit_check()
+
+
+def test_rotary_offsets_past_32_bits():
+    g = np.random.default_rng(4)
+    ld = 1_200_000_008
+    mem = torch.empty(2 * ld + 1024, dtype=torch.bfloat16, device="cuda")
+    x = torch.from_numpy(g.standard_normal((3, 2, 64)).astype(np.float32)).bfloat16()
+    v = torch.as_strided(mem, (3, 2, 64), (ld, 64, 1))
+    v.copy_(x)
+    out = torch.as_strided(mem, (3, 2, 64), (ld, 64, 1), 512)
+    pos = _positions(g, (3, 1), 10 ** 5)
+    D.dit_rotary(D.RotaryPlan([64]), v, None, dev(pos), out)
+    x64 = x.float().numpy().astype(np.float64)
+    ref, mag, dim = _expected(dict(widths=[64]), x64, pos, False)
+    _check(out, ref, mag, dim, x64, torch.bfloat16)
+
+
 def test_rotary_graph_and_empty_and_binding():
     plan = D.RotaryPlan([64], layout="halves")
     q = torch.randn(3, 4, 2, 64, device="cuda")

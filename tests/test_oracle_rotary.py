@@ -128,4 +128,20 @@ def test_fp4_refusals_before_any_cuda_call():
     assert L.dit_linear_fp4(None, 0, 0, 40, r(good), None, 0, 4, None, 0, None) == 0
     assert L.dit_fp4_code_bytes(3, 33) == 96 and L.dit_fp4_code_bytes(-1, 3) == 0
     assert L.dit_fp4_scale_bytes(0, 129, 65) == 2 * 2 * 512 and L.dit_fp4_scale_bytes(1, 129, 65) == 2 * 512
+    assert L.dit_fp4_quantize(x, 0, 1 << 30, r(M(0, 4, (1 << 30) + 1, 256, 512, 1024)), None) == -2
+    assert L.dit_fp4_matmul(r(good), r(M(0, (1 << 30) + 1, 40, 256, 512, 1024)), x, 0, 1 << 31, None) == -2
+    assert L.dit_linear_fp4(x, 0, (1 << 30) + 1, 40, r(good), x, 0, 4, x, n, None) == -2
+    dims, mod = D.dit_dims(256, 4, 64, 128, 1e-6, 1e-6, 0), D.dit_mod(256, None, 1)
+    ok = D.dit_block_wfp4((M * 4)(*[M(0, a, b, 256, 512, 1024) for a, b in ((768, 256), (256, 256), (256, 256), (256, 128))]))
+    need = L.dit_block_fp4_workspace_bytes(r(dims), 0, 0, 5)
+
+    def block(w, nbytes=need, ws=x, img=x, N=5):
+        return L.dit_block_forward_fp4(r(dims), r(w) if w is not None else None, None, 0, img, N, None, None, x, x,
+                                       r(mod), ws, nbytes, None)
+
+    assert need > 0 and block(None) == -1 and block(ok, need - 1) == -3 and block(ok, ws=None) == -3
+    assert block(ok, img=None) == -1 and block(ok, N=0) == -1 and block(ok, ws=ctypes.c_void_p(128)) == -1
+    mixed = D.dit_block_wfp4((M * 4)(*[M(i == 3, a, b, 256, 512, 1024) for i, (a, b) in
+                                       enumerate(((768, 256), (256, 256), (256, 256), (256, 128)))]))
+    assert block(mixed) == -1
     assert L.dit_fp4_scale_bytes(2, 1, 1) == 0 and L.dit_linear_fp4_workspace_bytes(0, 1, 1, 0) == 0
