@@ -142,6 +142,10 @@ SIZES = [(1, 16, 16), (1, 1, 1), (1, 1000, 256), (2, 130, 100), (8, 128, 4096), 
          (64, 1000, 512), (65, 384, 64), (127, 129, 31), (128, 128, 128), (129, 257, 257), (200, 1024, 1056),
          (256, 256, 4096), (333, 777, 1000), (513, 640, 2048), (1088, 512, 3104), (40, 4096, 8000), (1, 9000, 2000),
          (1100, 1500, 777), (1537, 1025, 2000), (2304, 768, 96), (300, 5200, 520)]
+# one or more for every kernel and tile: pairs with 128, 192 and 256 rows (several rounds, so that accumulators
+# and their overlap are reused), either operand first; clusters of two, four and eight
+SIZES += [(4911, 784, 96), (1044, 3856, 2100), (1030, 7712, 96), (1037, 8720, 520), (1030, 8672, 96), (1155, 8194, 96),
+          (250, 3000, 5000), (60, 3000, 5000), (100, 300, 5003), (40, 777, 9001)]
 
 
 @FMT
