@@ -611,42 +611,43 @@ def dit_rope_tables(L: int, grid_h: int, grid_w: int, head_dim: int, cos, sin, t
                               _ptr(sin, torch.float32, "sin"), _stream(stream)), "dit_rope_tables")
 
 
-# The calls below take microseconds on the device, so their marshalling is kept short: torch is looked
-# up once, and the current stream's handle is asked for without building a Stream object.
+# The calls below take microseconds on the device, so their marshalling is kept short: torch's parts are
+# looked up once, and the current stream's handle is asked for without building a Stream object.
 _torch_mod = None
+_kinds = {}  # torch dtype -> DIT_BF16 / DIT_F32
+_get_device = _raw_stream = None
 
 
 def _torch():
-    global _torch_mod
+    global _torch_mod, _get_device, _raw_stream
     if _torch_mod is None:
         import torch
+        _kinds.update({torch.bfloat16: DIT_BF16, torch.float32: DIT_F32})
+        _get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda dev: torch.cuda.current_stream(dev).cuda_stream)
         _torch_mod = torch
     return _torch_mod
 
 
 def _current(stream):
     """(current device, stream handle)"""
-    torch = _torch()
-    dev = torch.cuda.current_device()
+    if _torch_mod is None:
+        _torch()
+    dev = _get_device()
     if stream is None:
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        return dev, raw(dev) if raw is not None else torch.cuda.current_stream().cuda_stream
+        return dev, _raw_stream(dev)
     return dev, stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _kind(t, dev, name):
-    """DIT_BF16 or DIT_F32 of a CUDA tensor on device `dev`."""
+def _wrong(t, dev, name):
+    """The reason why `t` is no bf16 or fp32 tensor on device `dev`."""
     torch = _torch()
     if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch.Tensor")
+        return TypeError(f"{name}: expected a torch.Tensor")
     if t.get_device() != dev:
-        raise ValueError(f"{name}: expected a CUDA tensor on the current device")
-    dt = t.dtype
-    if dt is torch.bfloat16:
-        return DIT_BF16
-    if dt is torch.float32:
-        return DIT_F32
-    raise TypeError(f"{name}: expected bfloat16 or float32, got {dt}")
+        return ValueError(f"{name}: expected a CUDA tensor on the current device")
+    return TypeError(f"{name}: expected bfloat16 or float32 (an output its input's type), got {t.dtype}")
 
 
 class RotaryPlan:
@@ -671,8 +672,7 @@ def dit_rotary_plan_init(spec: dit_rotary_spec, plan: dit_rotary_plan):
 
 
 def _positions(plan: RotaryPlan, pos, rows: int, dev: int):
-    torch = _torch()
-    if not isinstance(pos, torch.Tensor) or pos.dtype is not torch.int32:
+    if not isinstance(pos, _torch_mod.Tensor) or pos.dtype is not _torch_mod.int32:
         raise TypeError("pos: expected an int32 tensor")
     if pos.get_device() != dev or not pos.is_contiguous():
         raise ValueError("pos: expected a contiguous CUDA tensor on the current device")
@@ -698,24 +698,29 @@ _rows_struct = struct.Struct("@PPiqqqqqq")  # dit_rotary_rows
 
 
 def _rotary_rows(x, out, dev, name):
-    kind = _kind(x, dev, name)
+    """(dit_rotary_rows, type, shape) of the heads x and their output."""
+    kind = _kinds.get(getattr(x, "dtype", None))
+    if kind is None or x.get_device() != dev:
+        raise _wrong(x, dev, name)
     shape, sx = x.shape, x.stride()
     if out is x:
         so = sx
     else:
-        if _kind(out, dev, name) != kind or out.shape != shape:
+        if getattr(out, "dtype", None) is not x.dtype or out.get_device() != dev:
+            raise _wrong(out, dev, name)
+        if out.shape != shape:
             raise ValueError(f"{name}: expected an output like the input")
         so = out.stride()
-    n = len(shape)
-    if n == 4:
-        bx, bo = sx[0], so[0]
-    elif n == 3:
-        bx = bo = 0
+    if len(shape) == 4:
+        bx, rx, hx, ex = sx
+        bo, ro, ho, eo = so
+    elif len(shape) == 3:
+        (rx, hx, ex), (ro, ho, eo), bx, bo = sx, so, 0, 0
     else:
         raise ValueError(f"{name}: expected [batch, rows, heads, head_dim] or [rows, heads, head_dim]")
-    if (sx[-1] != 1 or so[-1] != 1) and shape[-1] > 1:
+    if (ex != 1 or eo != 1) and shape[-1] > 1:
         raise ValueError(f"{name}: the last dimension must be dense")
-    return kind, shape, _rows_struct.pack(x.data_ptr(), out.data_ptr(), shape[-2], bx, sx[-3], sx[-2], bo, so[-3], so[-2])
+    return _rows_struct.pack(x.data_ptr(), out.data_ptr(), shape[-2], bx, rx, hx, bo, ro, ho), kind, shape
 
 
 def dit_rotary(plan: RotaryPlan, q, k, pos, q_out=None, k_out=None, inverse: bool = False, stream=None):
@@ -723,10 +728,10 @@ def dit_rotary(plan: RotaryPlan, q, k, pos, q_out=None, k_out=None, inverse: boo
     dense head; q_out / k_out default to in place. pos [batch, rows, axes] int32 (axes may be left out
     when there is one)."""
     dev, st = _current(stream)
-    kind, shape, a = _rotary_rows(q, q if q_out is None else q_out, dev, "q")
+    a, kind, shape = _rotary_rows(q, q if q_out is None else q_out, dev, "q")
     c = None
     if k is not None:
-        kk, sk, c = _rotary_rows(k, k if k_out is None else k_out, dev, "k")
+        c, kk, sk = _rotary_rows(k, k if k_out is None else k_out, dev, "k")
         if kk != kind or sk[:-2] != shape[:-2] or sk[-1] != shape[-1]:
             raise ValueError("q and k: expected the same type, batch, rows and head_dim")
     batch = shape[0] if len(shape) == 4 else 1
@@ -766,7 +771,9 @@ class Fp4Matrix:
 
 def _matrix(t, rows, cols, dev, name):
     """(pointer, type, row stride) of a plain [rows, cols] tensor whose rows are dense."""
-    kind = _kind(t, dev, name)
+    kind = _kinds.get(getattr(t, "dtype", None))
+    if kind is None or t.get_device() != dev:
+        raise _wrong(t, dev, name)
     if t.shape != (rows, cols):
         raise ValueError(f"{name}: expected [{rows}, {cols}], got {list(t.shape)}")
     s0, s1 = t.stride()
