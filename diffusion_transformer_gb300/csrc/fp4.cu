@@ -133,7 +133,8 @@ struct RowShape {
 // Many rows of up to 32 NU units: one warp per row. A lane holds NU units of 16 values (one NV block, half
 // an MX block) in registers, so the row is read once, all its loads in flight together, for its largest
 // magnitude and for its codes, and no barrier joins the warps. Bound by HBM: the values in, 9/16 byte
-// per value out.
+// per value out. 4224 x 3072 bf16: 6.7 us, 5.0 TB/s (one CTA of 192 threads per row: 9.5 us; eight units
+// per lane where six cover the row: 7.9 us, their registers leaving fewer rows on an SM).
 constexpr int kRowWarps = 4;
 template <typename T, int FMT, int NU>
 __global__ void __launch_bounds__(32 * kRowWarps) fp4_quantize_warp_kernel(const T* x, long long ldx, int rows, int cols,
@@ -170,7 +171,9 @@ __global__ void __launch_bounds__(32 * kRowWarps) fp4_quantize_warp_kernel(const
 // Few rows, long rows, or rows off 16 bytes: one CTA per row, NU units per thread and chunk. Rows longer
 // than NU units per thread repeat the passes over chunks (NV: the second pass rereads the row, which L2
 // holds). A row that starts off 16 bytes (VEC = false) is staged through shared memory with coalesced
-// single loads.
+// single loads. 4224 x 12288 bf16: 25.5 us, 5.2 TB/s (eight units per thread: 29.5 us); 9216 x 3072 fp32: 20.5 us
+// in 32-value blocks, 21.2 in 16-value ones, 6.2 TB/s; 4000 x 5001 fp32, staged: 31 us, 3.0 TB/s (114 us with
+// the units read off one bank).
 template <typename T, int FMT, bool VEC, int NU>
 __global__ void __launch_bounds__(256) fp4_quantize_kernel(const T* x, long long ldx, int cols, uint8_t* codes,
                                                            uint8_t* scales, float* row_scale) {
@@ -241,7 +244,7 @@ __global__ void __launch_bounds__(256) fp4_quantize_kernel(const T* x, long long
 
 // `lanes` threads to a row, units of 16 values: 8 code bytes and a scale byte in, 32 or 64
 // bytes out, or (VEC = false: rows off 32 bytes) through shared memory in whole lines. Bound by HBM, the
-// values out above all.
+// values out above all. 4224 x 12288 to bf16: 23 us, 5.7 TB/s; 9216 x 3072 to fp32: 20 us, 6.4 TB/s.
 template <typename T, int FMT, bool VEC>
 __global__ void __launch_bounds__(256, 6) fp4_dequantize_kernel(const uint8_t* codes, const uint8_t* scales,
                                                                 const float* row_scale, int rows, int cols,

@@ -10,6 +10,19 @@
 //          persistent, for products with enough tiles
 //   split  128 rows of B against up to 128 rows of A per CTA, a cluster of CTAs sharing the K loop and
 //          adding their partial tiles through distributed shared memory, for few rows or few tiles
+//
+// What bounds the pair kernel. A stage of a 256 x 256 tile takes each SM 512 cycles of MMA, and 38 KB of
+// operands and scales into shared memory and out of it again to the tensor core: 120 of the 128 bytes per
+// cycle that shared memory moves. Measured per stage at 2070 MHz, 4096 x 24320 x 3072: 247 ns of MMA, 327
+// ns without an epilogue, 348 with all of it but the stores, 394 in all (94.5 us; 32-value blocks, with half
+// the scales and no factors: 87); 4096 x 4864 x 12288: 330 ns. So the output's way through the same data path
+// counts: 32-byte stores from registers 94.5 us, staged in shared memory and stored by TMA 104, lanes
+// exchanging pieces to store whole 128-byte lines 99.8, evict-first hints 96, four epilogue warps in place
+// of eight 93 (104 when staged). 4224 x 24576 x 3072 with data that toggles bits: 104 us (6.1 PFLOP/s, tensor
+// pipe 72 % active) in a burst, 112 to 123 back to back, where the power limit lowers the clock; 8192^3:
+// 151 us, 7.3 PFLOP/s.
+// What bounds the split kernel: B's bytes where rows are few (1 x 18432 x 3072: 6.2 us, 5.1 TB/s with B partly
+// in L2), else the fixed 2 to 4 us of start, first loads and epilogue.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -11,7 +11,9 @@
 // fp32, so the residual, at most an eighth of a turn, carries 24 bits (2^-28 turns) into sincospif.
 //
 // What bounds it: HBM. Each value is read once and written once; a row's cosines and sines are
-// computed once into shared memory and serve all of its heads.
+// computed once into shared memory and serve all of its heads. 131072 rows of 10 heads (96 of 128 values
+// turned, bf16, written head-major): 109 us, 6.2 TB/s; 4224 rows of 48 heads out of packed QKV rows: 18.5 us,
+// 5.6 TB/s; one row: 3.8 us, the launch and one chain of loads.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -118,7 +120,10 @@ __device__ __forceinline__ Raw<T, VE> rot_raw(const float (&v)[VE]) {
 // all heads come first and the passing ones after them, so a warp rarely holds both kinds. Rows with fewer
 // units than threads are taken several at a time. A few rows are loaded before the first is turned, and
 // the first of them before the CTA works out its cosines and sines. Those stand in shared memory as
-// [row][angle of a unit][unit], so neighbouring threads read neighbouring 16 bytes.
+// [row][angle of a unit][unit], so neighbouring threads read neighbouring 16 bytes. (On 131072 rows of 10
+// heads: 168 us with a unit's angles side by side and turned and passing units mixed, 146 with both mended, 120
+// with neighbouring threads on neighbouring rows of one pair where the angles are made, 109 with two rows in
+// flight and five CTAs per SM.)
 template <typename T, int VE, bool HALVES>
 __global__ void __launch_bounds__(kRotThreads, HALVES && VE > 1 ? 5 : 4) rotary_kernel(const __grid_constant__ RotArgs a) {
   constexpr bool kTwo = HALVES || VE == 1;                     // a turned unit is two accesses
