@@ -789,6 +789,31 @@ bool allow_smem(const void* kern, std::atomic<uint64_t>& ready) {
   return true;
 }
 
+// CTA pairs that are resident at once, asked for once per kernel and device (`cached`, by device).
+int resident_pairs(const void* kern, unsigned smem, std::atomic<int>* cached) {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return num_sms() / 2;
+  if ((n = cached[dev].load(std::memory_order_relaxed)) > 0) return n;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(num_sms() & ~1));
+  cfg.blockDim = dim3(kPairThreads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) {
+    cudaGetLastError();
+    n = num_sms() / 2;
+  }
+  n = std::min(n, num_sms() / 2);
+  cached[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
 bool tmap_codes(CUtensorMap* m, const uint8_t* codes, int rows, int K, int box_rows) {
   return make_tmap_2d(m, codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, fp4_code_row_bytes(K), rows, fp4_code_row_bytes(K), 128,
                       box_rows, true);
@@ -816,7 +841,8 @@ int launch_pair(const dit_fp4_matrix& a, const dit_fp4_matrix& b, Fp4Params p, c
   if (!allow_smem(reinterpret_cast<const void*>(kern), ready)) return DIT_ECUDA;
   const long long tiles = (long long)((P.rows + 255) / 256) * ((Q.rows + bn - 1) / bn);
   if (tiles > 0x7fffffffLL - num_sms()) return DIT_EUNSUPPORTED;
-  const int units = int(std::min<long long>(tiles, num_sms() / 2));
+  static std::atomic<int> pairs[64];  // one smem size counts for all: more than half an SM's, so a CTA per SM
+  const int units = int(std::min<long long>(tiles, resident_pairs(reinterpret_cast<const void*>(kern), smem, pairs)));
   const cudaError_t e = launch_pdl(kern, dim3(unsigned(2 * units)), dim3(kPairThreads), smem, st, 2, mp, mq, msp, msq, p, g);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? DIT_OK : DIT_ECUDA;
 }

@@ -336,6 +336,8 @@ int dit_rotary(const dit_rotary_plan* plan, const dit_rotary_rows* q, const dit_
     else if (r && r->heads > 1 << 20) return DIT_EUNSUPPORTED;
   if (batch == 0 || rows == 0) return DIT_OK;
   if (!pos) return DIT_EINVAL;
+  // one tensor as q and k, written by one of them at least: which of the two is read first would be chance
+  if (k && q->heads > 0 && k->heads > 0 && (q->out == k->out || q->out == k->x || k->out == q->x)) return DIT_EINVAL;
   RotArgs a;
   std::memset(&a, 0, sizeof(a));
   bool vec = head_dim % ve == 0 && (plan->layout == DIT_ROTARY_HALVES ? plan->pairs : 2 * plan->pairs) % ve == 0;

@@ -89,6 +89,10 @@ def test_rotary_refusals_before_any_cuda_call():
     assert call(q=D.dit_rotary_rows(256, 256, 4, 0, 256, 64, 0, 0, 64)) == -1            # output rows on one place
     assert call(q=D.dit_rotary_rows(256, 256, 4, 0, 256, 64, 0, 256, 0)) == -1
     assert call(batch=2, q=D.dit_rotary_rows(256, 256, 4, 0, 256, 64, 0, 256, 64)) == -1
+    # one tensor as q and as k, with an output on it
+    assert call(q=q, k=q) == -1
+    k = D.dit_rotary_rows(512, 256, 4, 0, 256, 64, 0, 256, 64)
+    assert call(q=q, k=k) == -1 and call(q=D.dit_rotary_rows(256, 1024, 4, 0, 256, 64, 0, 256, 64), k=k) == -1
     bad = D.dit_rotary_plan()
     ctypes.memmove(ctypes.byref(bad), ctypes.byref(p.c), ctypes.sizeof(bad))
     bad.axis[5] = 7
