@@ -10,6 +10,7 @@
 #include <mutex>
 
 #include "fp4.cuh"
+#include "fp4.h"
 #include "internal.h"
 #include "tmap.h"
 

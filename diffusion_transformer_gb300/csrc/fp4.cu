@@ -13,6 +13,7 @@
 #include <type_traits>
 
 #include "fp4.cuh"
+#include "fp4.h"
 #include "internal.h"
 #include "ptx.cuh"
 

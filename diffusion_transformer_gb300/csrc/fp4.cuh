@@ -7,7 +7,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/dit.h"
-#include "ptx.cuh"
+#include "fp4_ptx.cuh"
 
 namespace dit {
 

@@ -32,8 +32,9 @@
 #include <type_traits>
 
 #include "fp4.cuh"
+#include "fp4.h"
+#include "fp4_ptx.cuh"
 #include "internal.h"
-#include "ptx.cuh"
 #include "tmap.h"
 
 namespace dit {
@@ -812,6 +813,20 @@ int resident_pairs(const void* kern, unsigned smem, std::atomic<int>* cached) {
   n = std::min(n, num_sms() / 2);
   cached[dev].store(n, std::memory_order_relaxed);
   return n;
+}
+
+// Scale tiles as a 3-D map: chunks of 512 bytes (as 128 words) x groups of four blocks x bands of 128 rows; box
+// = one chunk x box_groups x box_bands.
+bool make_tmap_scales(CUtensorMap* m, const void* base, long long groups, long long bands, int box_groups, int box_bands) {
+  EncodeTiledFn fn = encode_tiled_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {128, cuuint64_t(groups), cuuint64_t(bands)};
+  cuuint64_t strides[2] = {512, cuuint64_t(groups) * 512};
+  cuuint32_t box[3] = {128, cuuint32_t(box_groups), cuuint32_t(box_bands)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool tmap_codes(CUtensorMap* m, const uint8_t* codes, int rows, int K, int box_rows) {

@@ -201,19 +201,6 @@ int quant_weight_launch(const uint16_t* w, int N, int K, const float* smooth, in
                         cudaStream_t stream);
 int codes_bf16_launch(const int8_t* q, uint16_t* w, long long n, cudaStream_t stream);
 
-// Microscaled 4-bit matrices (see dit_fp4_quantize and the calls after it), on validated arguments.
-// b_early: the kernel enqueued just before the product does not write b and itself called pdl_wait before
-// pdl_trigger (as every kernel here does), so b was complete when the product's launch began; its loads
-// may then run ahead of that kernel's end.
-int fp4_quantize_launch(const void* x, int type, long long ldx, const dit_fp4_matrix& m, cudaStream_t stream);
-int fp4_dequantize_launch(const dit_fp4_matrix& m, void* out, int type, long long ldo, cudaStream_t stream);
-int fp4_matmul_launch(const dit_fp4_matrix& a, const dit_fp4_matrix& b, void* out, int type, long long ldo, int* err,
-                      bool b_early, cudaStream_t stream);
-// A block's linear a b^T through kEpiQKV, kEpiSwiGLU or kEpiGated (g.out, g.ldo, g.err and what the epilogue
-// reads; b as with b_early), for the widths a block has: b->rows a multiple of 256.
-int fp4_block_linear_launch(const dit_fp4_matrix& a, const dit_fp4_matrix& b, int epi, const GemmParams& g,
-                            cudaStream_t stream);
-
 int num_sms();
 
 // Launch `kern` on `stream` with programmatic dependent launch allowed (and a cluster of

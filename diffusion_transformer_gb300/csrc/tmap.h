@@ -32,21 +32,6 @@ inline bool make_tmap_2d(CUtensorMap* m, const void* base, CUtensorMapDataType d
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Scale tiles of a microscaled 4-bit matrix as a 3-D map: chunks of 512 bytes (as 128 words) x groups
-// of four blocks x bands of 128 rows; box = one chunk x box_groups x box_bands.
-inline bool make_tmap_scales(CUtensorMap* m, const void* base, long long groups, long long bands, int box_groups,
-                             int box_bands) {
-  EncodeTiledFn fn = encode_tiled_fn();
-  if (!fn) return false;
-  cuuint64_t dims[3] = {128, cuuint64_t(groups), cuuint64_t(bands)};
-  cuuint64_t strides[2] = {512, cuuint64_t(groups) * 512};
-  cuuint32_t box[3] = {128, cuuint32_t(box_groups), cuuint32_t(box_bands)};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // 3-D map (bf16, 128-byte swizzle): dims {d0 (contiguous), d1, d2}, strides in bytes of d1 and d2.
 inline bool make_tmap_3d_bf16(CUtensorMap* m, const void* base, long long d0, long long d1, long long d2,
                               long long stride1_bytes, long long stride2_bytes, int box0, int box1) {
