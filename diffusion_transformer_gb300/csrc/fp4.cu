@@ -58,19 +58,39 @@ __device__ __forceinline__ uint32_t unit_max(const Unit<T>& u) {
     return m;
   }
 }
-// 16 values from column c of a row that starts on 16 bytes, zero past cols
-template <typename T>
+// words[i] <- words[i + bytes / 4] (a byte offset below 16, even), as if the words were one string of bytes
+template <int N>
+__device__ __forceinline__ void shift_down(uint32_t (&w)[N], int bytes) {
+#pragma unroll
+  for (int i = 0; i + 2 < N; ++i) w[i] = bytes & 8 ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i + 1 < N; ++i) w[i] = bytes & 4 ? w[i + 1] : w[i];
+#pragma unroll
+  for (int i = 0; i + 1 < N; ++i) w[i] = bytes & 2 ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
+}
+
+// 16 values from column c of a row, zero past cols. Rows on 16 bytes (VEC) are read as they lie. Others are
+// read through the aligned 16-byte words around the values and shifted into place, but for the units whose
+// words would reach over either end of the row, which are read value by value.
+template <typename T, bool VEC>
 __device__ __forceinline__ Unit<T> unit_load(const T* x, int c, int cols) {
   Unit<T> u;
-  if (c + kUnit <= cols) {
+  constexpr int kWords = kUnit * sizeof(T) / 4, kSpill = VEC ? 0 : 16 / int(sizeof(T));
+  if ((VEC || c > 0) && c + kUnit + kSpill <= cols) {
+    const int off = VEC ? 0 : int(reinterpret_cast<uintptr_t>(x + c) & 15u);
+    const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(x + c) - off);
+    uint32_t w[kWords + (VEC ? 0 : 4)];
 #pragma unroll
-    for (int h = 0; h < int(sizeof(T)); ++h) {
-      const uint4 q = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(x + c) + 16 * h);
-      u.w[4 * h] = q.x;
-      u.w[4 * h + 1] = q.y;
-      u.w[4 * h + 2] = q.z;
-      u.w[4 * h + 3] = q.w;
+    for (int h = 0; h < kWords / 4 + (VEC ? 0 : 1); ++h) {
+      const uint4 q = p[h];
+      w[4 * h] = q.x;
+      w[4 * h + 1] = q.y;
+      w[4 * h + 2] = q.z;
+      w[4 * h + 3] = q.w;
     }
+    if constexpr (!VEC) shift_down(w, off);
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) u.w[j] = w[j];
   } else {
     using Bits = typename std::conditional<sizeof(T) == 2, uint16_t, uint32_t>::type;
     const Bits* b = reinterpret_cast<const Bits*>(x);
@@ -83,14 +103,6 @@ __device__ __forceinline__ Unit<T> unit_load(const T* x, int c, int cols) {
   }
   return u;
 }
-// Rows staged in shared memory: a word of padding behind every unit, so that the units of a warp lie on
-// different banks. The place of value i, in values:
-template <typename T>
-__device__ __forceinline__ int staged_at(int i) {
-  return i + i / kUnit * int(4 / sizeof(T));
-}
-template <typename T>
-constexpr size_t kStagedUnit = kUnit * sizeof(T) + 4;
 
 // Codes and scale byte of the unit i in v. A group's four scale bytes are gathered in one thread, so every
 // lane of the warp takes part.
@@ -137,7 +149,7 @@ struct RowShape {
 // per value out. 4224 x 3072 bf16: 6.7 us, 5.0 TB/s (one CTA of 192 threads per row: 9.5 us; eight units
 // per lane where six cover the row: 7.9 us, their registers leaving fewer rows on an SM).
 constexpr int kRowWarps = 4;
-template <typename T, int FMT, int NU>
+template <typename T, int FMT, bool VEC, int NU>
 __global__ void __launch_bounds__(32 * kRowWarps) fp4_quantize_warp_kernel(const T* x, long long ldx, int rows, int cols,
                                                                            uint8_t* codes, uint8_t* scales,
                                                                            float* row_scale) {
@@ -150,7 +162,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) fp4_quantize_warp_kernel(const
   Unit<T> v[NU];
 #pragma unroll
   for (int k = 0; k < NU; ++k)
-    if (k * 32 < sh.units) v[k] = unit_load(x, (k * 32 + lane) * kUnit, cols);
+    if (k * 32 < sh.units) v[k] = unit_load<T, VEC>(x, (k * 32 + lane) * kUnit, cols);
   float fu = 0.f, ft = 0.f;
   if constexpr (FMT == DIT_FP4_NV) {
     uint32_t m = 0;
@@ -169,12 +181,11 @@ __global__ void __launch_bounds__(32 * kRowWarps) fp4_quantize_warp_kernel(const
     if (k * 32 < sh.units) unit_quantize<T, FMT>(v[k], k * 32 + lane, fu, ft, sh.units, sh.code_units, crow, srow);
 }
 
-// Few rows, long rows, or rows off 16 bytes: one CTA per row, NU units per thread and chunk. Rows longer
-// than NU units per thread repeat the passes over chunks (NV: the second pass rereads the row, which L2
-// holds). A row that starts off 16 bytes (VEC = false) is staged through shared memory with coalesced
-// single loads. 4224 x 12288 bf16: 25.5 us, 5.2 TB/s (eight units per thread: 29.5 us); 9216 x 3072 fp32: 20.5 us
-// in 32-value blocks, 21.2 in 16-value ones, 6.2 TB/s; 4000 x 5001 fp32, staged: 31 us, 3.0 TB/s (114 us with
-// the units read off one bank).
+// Few or long rows: one CTA per row, NU units per thread and chunk. Rows longer than NU units per thread
+// repeat the passes over chunks (NV: the second pass rereads the row, which L2 holds).
+// 4224 x 12288 bf16: 25.5 us, 5.2 TB/s (eight units per thread: 29.5 us); 9216 x 3072 fp32: 20.5 us in 32-value blocks,
+// 21.2 in 16-value ones, 6.2 TB/s. Rows off 16 bytes, one call between events: 4224 x 12289 bf16 39 us (MX) and 47
+// (NV), 4000 x 5001 fp32 25 and 29; through shared memory with single loads they took 151, 180, 39 and 37.
 template <typename T, int FMT, bool VEC, int NU>
 __global__ void __launch_bounds__(256) fp4_quantize_kernel(const T* x, long long ldx, int cols, uint8_t* codes,
                                                            uint8_t* scales, float* row_scale) {
@@ -185,36 +196,12 @@ __global__ void __launch_bounds__(256) fp4_quantize_kernel(const T* x, long long
   const RowShape<FMT> sh(cols);
   uint8_t* crow = codes + (long long)r * fp4_code_row_bytes(cols);
   uint8_t* srow = scales + fp4_scale_row(FMT, r, cols);
-  extern __shared__ uint32_t staged[];
-  T* sx = reinterpret_cast<T*>(staged);
   const int span = nt * NU;  // units per chunk
   const int chunks = (sh.units + span - 1) / span;
   Unit<T> v[NU];
   auto load = [&](int c) {
-    const int c0 = c * span * kUnit;
-    if constexpr (!VEC) {
-      __syncthreads();
-      T t[NU * kUnit];
 #pragma unroll
-      for (int k = 0; k < NU * kUnit; ++k) {  // all loads in flight before the first is stored
-        const int i = int(threadIdx.x) + k * nt;
-        t[k] = c0 + i < cols ? x[c0 + i] : T(0.f);
-      }
-#pragma unroll
-      for (int k = 0; k < NU * kUnit; ++k) sx[staged_at<T>(int(threadIdx.x) + k * nt)] = t[k];
-      __syncthreads();
-    }
-#pragma unroll
-    for (int k = 0; k < NU; ++k) {
-      const int u = threadIdx.x + k * nt;
-      if constexpr (VEC) {
-        v[k] = unit_load(x, c0 + u * kUnit, cols);
-      } else {
-        const uint32_t* w = staged + u * (kStagedUnit<T> / 4);
-#pragma unroll
-        for (int j = 0; j < int(kUnit * sizeof(T) / 4); ++j) v[k].w[j] = w[j];
-      }
-    }
+    for (int k = 0; k < NU; ++k) v[k] = unit_load<T, VEC>(x, (c * span + k * nt + int(threadIdx.x)) * kUnit, cols);
   };
   float fu = 0.f, ft = 0.f;
   if constexpr (FMT == DIT_FP4_NV) {
@@ -243,13 +230,16 @@ __global__ void __launch_bounds__(256) fp4_quantize_kernel(const T* x, long long
   }
 }
 
-// `lanes` threads to a row, units of 16 values: 8 code bytes and a scale byte in, 32 or 64
-// bytes out, or (VEC = false: rows off 32 bytes) through shared memory in whole lines. Bound by HBM, the
-// values out above all. 4224 x 12288 to bf16: 23 us, 5.7 TB/s; 9216 x 3072 to fp32: 20 us, 6.4 TB/s.
+// `lanes` threads to a row, units of 16 values: 8 code bytes and a scale byte in, 32 or 64 bytes out. Rows on 32
+// bytes (VEC) are stored as they come. Elsewhere a unit straddles aligned 16-byte words: a lane takes the
+// end of its neighbour's unit before its own and stores whole words, shifted into place; only the ends of a
+// row and of a warp are stored value by value. Bound by HBM, the values out above all. 4224 x 12288 to bf16: 23
+// us, 5.7 TB/s; 9216 x 3072 to fp32: 20 us, 6.4 TB/s. Rows off 32 bytes, one call between events: 4224 x 12289
+// to bf16 35 us, 4000 x 5001 to fp32 29-31; through shared memory in single values 49-53 and 27-29.
 template <typename T, int FMT, bool VEC>
-__global__ void __launch_bounds__(256, 6) fp4_dequantize_kernel(const uint8_t* codes, const uint8_t* scales,
-                                                                const float* row_scale, int rows, int cols,
-                                                                int lanes, T* out, long long ldo) {
+__global__ void __launch_bounds__(256, VEC ? 6 : 4) fp4_dequantize_kernel(const uint8_t* codes, const uint8_t* scales,
+                                                                          const float* row_scale, int rows, int cols,
+                                                                          int lanes, T* out, long long ldo) {
   pdl_wait();
   pdl_trigger();
   const int in_cta = int(threadIdx.x) / lanes, lane = int(threadIdx.x) - in_cta * lanes;
@@ -259,11 +249,13 @@ __global__ void __launch_bounds__(256, 6) fp4_dequantize_kernel(const uint8_t* c
   const uint8_t* srow = scales + fp4_scale_row(FMT, int(r), cols);
   const float g = FMT == DIT_FP4_NV && r < rows ? __ldg(row_scale + r) : 1.f;
   T* orow = out + r * ldo;
-  __shared__ uint8_t staging[VEC ? 1 : 256 * kStagedUnit<T>];
-  T* staged = reinterpret_cast<T*>(staging + (VEC ? 0 : (threadIdx.x - lane) * kStagedUnit<T>));
+  constexpr int kWords = kUnit * sizeof(T) / 4;
+  const int in_warp = threadIdx.x & 31, in_last = int(blockDim.x) - int(threadIdx.x & ~31u);
+  const uint32_t warp = in_last >= 32 ? 0xffffffffu : (1u << in_last) - 1;  // the last warp may be a part of one
 #pragma unroll 1
-  for (int u0 = 0; u0 * kUnit < cols; u0 += lanes) {
+  for (int u0 = 0; u0 * kUnit < cols; u0 += lanes) {  // the same turns for every lane: they exchange values
     const int u = u0 + lane, c = u * kUnit;
+    uint32_t q[kWords] = {};
     if (u < units) {
       const uint2 w = *reinterpret_cast<const uint2*>(crow + 8 * u);
       const int byte = srow[fp4_scale_block(FMT == DIT_FP4_NV ? u : u >> 1)];
@@ -272,34 +264,56 @@ __global__ void __launch_bounds__(256, 6) fp4_dequantize_kernel(const uint8_t* c
       const float s = FMT == DIT_FP4_NV ? fp4_e4m3(byte) : fp4_e8m0(byte);
 #pragma unroll
       for (int j = 0; j < kUnit; ++j) v[j] = FMT == DIT_FP4_NV ? v[j] * s * g : v[j] * s;
-      if (VEC && c + kUnit <= cols) {
-        uint32_t q[8];
-        if constexpr (sizeof(T) == 2) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) q[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
-          st_global_256(orow + c, q);
-        } else {
+      for (int j = 0; j < kWords; ++j)
+        q[j] = sizeof(T) == 2 ? pack_bf16x2(v[(2 * j) % kUnit], v[(2 * j + 1) % kUnit]) : __float_as_uint(v[j]);
+    }
+    using Bits = typename std::conditional<sizeof(T) == 2, uint16_t, uint32_t>::type;
+    Bits* o = reinterpret_cast<Bits*>(orow + c);
+    auto one = [&](int j) { o[j] = Bits(sizeof(T) == 2 && j & 1 ? q[j >> 1] >> 16 : q[j * kWords / kUnit]); };
+    const bool whole = u < units && c + kUnit <= cols;
+    if constexpr (VEC) {
+      if (whole) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) q[j] = __float_as_uint(v[8 * h + j]);
-            st_global_256(orow + c + 8 * h, q);
-          }
+        for (int h = 0; h < kWords; h += 8) {
+          const uint32_t t[8] = {q[h], q[h + 1], q[h + 2], q[h + 3], q[h + 4], q[h + 5], q[h + 6], q[h + 7]};
+          st_global_256(reinterpret_cast<uint32_t*>(o) + h, t);
         }
-      } else if (VEC) {
+      }
+    } else {
+      uint32_t w[4 + kWords];  // the neighbour's last 16 bytes, then this unit
 #pragma unroll
-        for (int j = 0; j < kUnit; ++j)
-          if (c + j < cols) orow[c + j] = T(v[j]);
-      } else {
+      for (int j = 0; j < 4; ++j) w[j] = __shfl_up_sync(warp, q[kWords - 4 + j], 1);
 #pragma unroll
-        for (int j = 0; j < kUnit; ++j) staged[staged_at<T>(lane * kUnit) + j] = T(v[j]);
+      for (int j = 0; j < kWords; ++j) w[4 + j] = q[j];
+      if (whole) {
+        const int off = int(reinterpret_cast<uintptr_t>(o) & 15u);  // bytes of the first word before this unit
+        const bool before = in_warp > 0 && lane > 0;  // the lane below holds the unit before, whole too
+        const bool after = in_warp < 31 && lane + 1 < lanes && c + 2 * kUnit <= cols;  // the lane above stores the end
+        shift_down(w, (16 - off) & 15);
+        uint4* p = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(o) - off);
+        const int skip = off == 0 ? 4 : 0;  // on 16 bytes nothing was shifted: the words start with the unit
+#pragma unroll
+        for (int h = 0; h < kWords; h += 4)
+          if (off == 0 || h > 0 || before)
+            p[h / 4] = make_uint4(skip ? w[h + 4] : w[h], skip ? w[h + 5] : w[h + 1], skip ? w[h + 6] : w[h + 2],
+                                  skip ? w[h + 7] : w[h + 3]);
+        if (off > 0 && !before) {
+#pragma unroll
+          for (int j = 0; j < 16 / int(sizeof(T)); ++j)
+            if (j * int(sizeof(T)) < 16 - off) one(j);
+        }
+        if (off > 0 && !after) {
+#pragma unroll
+          for (int j = kUnit - 16 / int(sizeof(T)); j < kUnit; ++j)
+            if ((kUnit - j) * int(sizeof(T)) <= off) one(j);
+        }
       }
     }
-    if constexpr (!VEC) {
-      __syncthreads();
-      const int n = units > 0 ? min(lanes * kUnit, cols - u0 * kUnit) : 0;
-      for (int i = lane; i < n; i += lanes) orow[u0 * kUnit + i] = staged[staged_at<T>(i)];
-      __syncthreads();
+    if (u < units && !whole) {
+#pragma unroll
+      for (int j = 0; j < kUnit; ++j)
+        if (c + j < cols) one(j);
     }
   }
 }
@@ -309,23 +323,20 @@ cudaError_t quantize_nu(const T* x, long long ldx, const dit_fp4_matrix& m, cuda
   const int units = fp4_groups(FMT, m.cols) * (FMT == DIT_FP4_NV ? 4 : 8);
   auto go = [&](auto kern, int nu) {
     const int threads = std::min(256, (units + 32 * nu - 1) / (32 * nu) * 32);
-    const size_t smem = VEC ? 0 : size_t(threads) * nu * kStagedUnit<T>;
-    return launch_pdl(kern, dim3(m.rows), dim3(threads), smem, st, 1, x, ldx, m.cols, m.codes, m.scales, m.row_scale);
+    return launch_pdl(kern, dim3(m.rows), dim3(threads), 0, st, 1, x, ldx, m.cols, m.codes, m.scales, m.row_scale);
   };
-  if constexpr (VEC) {
-    // a warp per row: 8 units of bf16, 4 of fp32 per lane at most (64 registers of values)
-    constexpr int kMost = sizeof(T) == 2 ? 8 : 4;
-    if (units <= 32 * kMost && m.rows >= 4 * num_sms()) {
-      auto rows = [&](auto kern) {
-        return launch_pdl(kern, dim3((m.rows + kRowWarps - 1) / kRowWarps), dim3(32 * kRowWarps), 0, st, 1, x, ldx, m.rows,
-                          m.cols, m.codes, m.scales, m.row_scale);
-      };
-      if (units <= 64) return rows(fp4_quantize_warp_kernel<T, FMT, 2>);
-      if (units <= 128) return rows(fp4_quantize_warp_kernel<T, FMT, 4>);
-      if constexpr (kMost > 6)
-        if (units <= 192) return rows(fp4_quantize_warp_kernel<T, FMT, 6>);
-      return rows(fp4_quantize_warp_kernel<T, FMT, kMost>);
-    }
+  // a warp per row: 8 units of bf16, 4 of fp32 per lane at most (64 registers of values)
+  constexpr int kMost = sizeof(T) == 2 ? 8 : 4;
+  if (units <= 32 * kMost && m.rows >= 4 * num_sms()) {
+    auto rows = [&](auto kern) {
+      return launch_pdl(kern, dim3((m.rows + kRowWarps - 1) / kRowWarps), dim3(32 * kRowWarps), 0, st, 1, x, ldx, m.rows,
+                        m.cols, m.codes, m.scales, m.row_scale);
+    };
+    if (units <= 64) return rows(fp4_quantize_warp_kernel<T, FMT, VEC, 2>);
+    if (units <= 128) return rows(fp4_quantize_warp_kernel<T, FMT, VEC, 4>);
+    if constexpr (kMost > 6)
+      if (units <= 192) return rows(fp4_quantize_warp_kernel<T, FMT, VEC, 6>);
+    return rows(fp4_quantize_warp_kernel<T, FMT, VEC, kMost>);
   }
   // units per thread: few for short rows, whose threads are few already
   if (units <= (sizeof(T) == 4 && m.rows >= 4 * num_sms() ? 128 : 256)) return go(fp4_quantize_kernel<T, FMT, VEC, 1>, 1);

@@ -66,7 +66,8 @@ def _check_quantised(m, x, fmt):
     (1, 1, torch.bfloat16, 0, 0), (1, 16, torch.float32, 0, 0), (3, 31, torch.bfloat16, 0, 0),
     (5, 64, torch.bfloat16, 0, 0), (130, 100, torch.float32, 28, 0), (33, 1000, torch.bfloat16, 3, 5),
     (7, 1003, torch.float32, 0, 1), (2, 4096, torch.bfloat16, 0, 0), (9, 5000, torch.bfloat16, 8, 8),
-    (300, 48, torch.float32, 0, 0), (4, 12288, torch.bfloat16, 0, 0), (3, 20011, torch.float32, 0, 0)])
+    (300, 48, torch.float32, 0, 0), (1001, 17, torch.float32, 0, 0), (613, 128, torch.bfloat16, 0, 0),
+    (2045, 192, torch.bfloat16, 8, 0), (4, 12288, torch.bfloat16, 0, 0), (3, 20011, torch.float32, 0, 0)])
 def test_quantize_is_bit_exact(fmt, R, K, dtype, pad, shift):
     g = np.random.default_rng(R * 7919 + K)
     x = _rows(g, R, K, dtype == torch.bfloat16)
@@ -89,6 +90,38 @@ def test_quantize_is_bit_exact(fmt, R, K, dtype, pad, shift):
         if pad:  # what lies between the rows stays
             whole = torch.as_strided(out, (R, K + pad), (K + pad, 1))
             assert (whole[:-1, K:] == 77).all()
+    D.dit_check()
+
+
+@FMT
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("R,K", [(3, 15), (5, 65), (5003, 65), (5003, 229), (700, 533), (640, 4009), (4, 9001)])
+def test_rows_at_every_alignment(fmt, dtype, R, K):
+    """Rows that start at every offset from 16 bytes, and what lies around them left as it was."""
+    per = 16 // torch.empty(0, dtype=dtype).element_size()
+    x = _rows(np.random.default_rng(R + K), R, K)
+    m, back = D.Fp4Matrix.empty(fmt, R, K), None
+    for shift in range(per):
+        for pad in (0, 1) if R < 10 else (1,):
+            xd = _on_gpu(x, dtype, pad, shift)
+            m.codes.fill_(255)
+            m.scales.fill_(255)
+            D.dit_fp4_quantize(xd, m)
+            if back is None:
+                codes, scale, row = _check_quantised(m, x, fmt)
+                want = torch.from_numpy(O.fp4_values(codes, scale, row, fmt, K)).to(dtype).cuda()
+                back = m.codes.clone(), m.scales.clone()
+            else:
+                assert torch.equal(m.codes, back[0])
+                r = torch.arange(R, device="cuda")
+                got, ref = (t.view(-(-R // 128), -1, 32, 4, 4)[r // 128, :, r % 32, r % 128 // 32]
+                            for t in (m.scales, back[1]))
+                assert torch.equal(got, ref)
+            mem = torch.full((shift + R * (K + pad) + 64,), 77.0, dtype=dtype, device="cuda")
+            D.dit_fp4_dequantize(m, mem[shift:shift + R * (K + pad)].view(R, K + pad)[:, :K])
+            body = mem[shift:shift + R * (K + pad)].view(R, K + pad)
+            assert torch.equal(body[:, :K], want)
+            assert (body[:, K:] == 77).all() and (mem[:shift] == 77).all() and (mem[shift + R * (K + pad):] == 77).all()
     D.dit_check()
 
 
