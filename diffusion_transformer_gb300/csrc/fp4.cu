@@ -143,42 +143,53 @@ struct RowShape {
       : units(fp4_groups(FMT, cols) * (FMT == DIT_FP4_NV ? 4 : 8)), code_units(int(fp4_code_row_bytes(cols) / 8)) {}
 };
 
-// Many rows of up to 32 NU units: one warp per row. A lane holds NU units of 16 values (one NV block, half
-// an MX block) in registers, so the row is read once, all its loads in flight together, for its largest
-// magnitude and for its codes, and no barrier joins the warps. Bound by HBM: the values in, 9/16 byte
-// per value out. 4224 x 3072 bf16: 6.7 us, 5.0 TB/s (one CTA of 192 threads per row: 9.5 us; eight units
-// per lane where six cover the row: 7.9 us, their registers leaving fewer rows on an SM).
+// Many rows of up to LANES x NU units: LANES (8, 16 or 32) lanes of a warp per row. A lane holds NU units of 16
+// values (one NV block, half an MX block) in registers, so the row is read once, all its loads in flight
+// together, for its largest magnitude and for its codes, and no barrier joins the warps. Bound by HBM: the
+// values in, 9/16 byte per value out. 4224 x 3072 bf16: 6.7 us, 5.0 TB/s (one CTA of 192 threads per row: 9.5
+// us; eight units per lane where six cover the row: 7.9 us, their registers leaving fewer rows on an SM).
+// Several short rows share a warp: 100000 x 64 and x 128 bf16 take 12 us between events, 33 with a warp each.
 constexpr int kRowWarps = 4;
-template <typename T, int FMT, bool VEC, int NU>
+template <typename T, int FMT, bool VEC, int NU, int LANES>
 __global__ void __launch_bounds__(32 * kRowWarps) fp4_quantize_warp_kernel(const T* x, long long ldx, int rows, int cols,
                                                                            uint8_t* codes, uint8_t* scales,
                                                                            float* row_scale) {
   pdl_wait();
   pdl_trigger();
-  const int r = blockIdx.x * kRowWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (r >= rows) return;
+  const int lane = threadIdx.x & (LANES - 1), first = blockIdx.x * (32 * kRowWarps / LANES);
+  if (first + int(threadIdx.x & ~31u) / LANES >= rows) return;
+  int r = first + int(threadIdx.x) / LANES;
+  const bool live = r < rows;  // a warp stays whole: its lanes past the last row hold an empty row
+  if (!live) r = 0, cols = 0;
   x += r * ldx;
   const RowShape<FMT> sh(cols);
   Unit<T> v[NU];
 #pragma unroll
   for (int k = 0; k < NU; ++k)
-    if (k * 32 < sh.units) v[k] = unit_load<T, VEC>(x, (k * 32 + lane) * kUnit, cols);
+    if (LANES < 32 || k * 32 < sh.units) v[k] = unit_load<T, VEC>(x, (k * LANES + lane) * kUnit, cols);
   float fu = 0.f, ft = 0.f;
   if constexpr (FMT == DIT_FP4_NV) {
     uint32_t m = 0;
 #pragma unroll
     for (int k = 0; k < NU; ++k)
-      if (k * 32 < sh.units) m = max(m, unit_max(v[k]));
-    const Fp4Row fr = fp4_row(__reduce_max_sync(0xffffffffu, m));
+      if (LANES < 32 || k * 32 < sh.units) m = max(m, unit_max(v[k]));
+    if constexpr (LANES == 32) {
+      m = __reduce_max_sync(0xffffffffu, m);
+    } else {
+#pragma unroll
+      for (int o = LANES / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    }
+    const Fp4Row fr = LANES == 32 ? fp4_row(m) : fp4_row_of_lane(m);
     fu = fr.u;
     ft = fr.t;
-    if (lane == 0) row_scale[r] = fr.g;
+    if (lane == 0 && live) row_scale[r] = fr.g;
   }
   uint8_t* crow = codes + (long long)r * fp4_code_row_bytes(cols);
   uint8_t* srow = scales + fp4_scale_row(FMT, r, cols);
 #pragma unroll
   for (int k = 0; k < NU; ++k)
-    if (k * 32 < sh.units) unit_quantize<T, FMT>(v[k], k * 32 + lane, fu, ft, sh.units, sh.code_units, crow, srow);
+    if (LANES < 32 || k * 32 < sh.units)
+      unit_quantize<T, FMT>(v[k], k * LANES + lane, fu, ft, sh.units, sh.code_units, crow, srow);
 }
 
 // Few or long rows: one CTA per row, NU units per thread and chunk. Rows longer than NU units per thread
@@ -328,15 +339,18 @@ cudaError_t quantize_nu(const T* x, long long ldx, const dit_fp4_matrix& m, cuda
   // a warp per row: 8 units of bf16, 4 of fp32 per lane at most (64 registers of values)
   constexpr int kMost = sizeof(T) == 2 ? 8 : 4;
   if (units <= 32 * kMost && m.rows >= 4 * num_sms()) {
-    auto rows = [&](auto kern) {
-      return launch_pdl(kern, dim3((m.rows + kRowWarps - 1) / kRowWarps), dim3(32 * kRowWarps), 0, st, 1, x, ldx, m.rows,
+    auto rows = [&](auto kern, int lanes) {
+      const int per_cta = 32 * kRowWarps / lanes;
+      return launch_pdl(kern, dim3((m.rows + per_cta - 1) / per_cta), dim3(32 * kRowWarps), 0, st, 1, x, ldx, m.rows,
                         m.cols, m.codes, m.scales, m.row_scale);
     };
-    if (units <= 64) return rows(fp4_quantize_warp_kernel<T, FMT, VEC, 2>);
-    if (units <= 128) return rows(fp4_quantize_warp_kernel<T, FMT, VEC, 4>);
+    if (units <= 8) return rows(fp4_quantize_warp_kernel<T, FMT, VEC, 1, 8>, 8);
+    if (units <= 16) return rows(fp4_quantize_warp_kernel<T, FMT, VEC, 1, 16>, 16);
+    if (units <= 64) return rows(fp4_quantize_warp_kernel<T, FMT, VEC, 2, 32>, 32);
+    if (units <= 128) return rows(fp4_quantize_warp_kernel<T, FMT, VEC, 4, 32>, 32);
     if constexpr (kMost > 6)
-      if (units <= 192) return rows(fp4_quantize_warp_kernel<T, FMT, VEC, 6>);
-    return rows(fp4_quantize_warp_kernel<T, FMT, VEC, kMost>);
+      if (units <= 192) return rows(fp4_quantize_warp_kernel<T, FMT, VEC, 6, 32>, 32);
+    return rows(fp4_quantize_warp_kernel<T, FMT, VEC, kMost, 32>, 32);
   }
   // units per thread: few for short rows, whose threads are few already
   if (units <= (sizeof(T) == 4 && m.rows >= 4 * num_sms() ? 128 : 256)) return go(fp4_quantize_kernel<T, FMT, VEC, 1>, 1);

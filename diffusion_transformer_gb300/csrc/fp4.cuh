@@ -43,6 +43,13 @@ __device__ __forceinline__ Fp4Row fp4_row(uint32_t bits) {
   const float q = __fdiv_rn(lane == 2 ? a : (lane == 1 ? 2688.f : 448.f), lane == 2 ? 2688.f : a);
   return Fp4Row{__shfl_sync(0xffffffffu, q, 0), __shfl_sync(0xffffffffu, q, 1), __shfl_sync(0xffffffffu, q, 2)};
 }
+// The same by each lane for itself, where the rows of a warp's lanes differ: no lane waits for another.
+__device__ __forceinline__ Fp4Row fp4_row_of_lane(uint32_t bits) {
+  if (bits < 0x0d800000u) return Fp4Row{0.f, 0.f, 0.f};
+  if (bits >= 0x7f800000u) return Fp4Row{0.f, 0.f, __uint_as_float(0x7fc00000u)};
+  const float a = __uint_as_float(bits);
+  return Fp4Row{__fdiv_rn(448.f, a), __fdiv_rn(2688.f, a), __fdiv_rn(a, 2688.f)};
+}
 
 struct Fp4Block {
   uint32_t byte;  // the block scale
