@@ -195,8 +195,9 @@ __global__ void __launch_bounds__(32 * kRowWarps) fp4_quantize_warp_kernel(const
 // Few or long rows: one CTA per row, NU units per thread and chunk. Rows longer than NU units per thread
 // repeat the passes over chunks (NV: the second pass rereads the row, which L2 holds).
 // 4224 x 12288 bf16: 25.5 us, 5.2 TB/s (eight units per thread: 29.5 us); 9216 x 3072 fp32: 20.5 us in 32-value blocks,
-// 21.2 in 16-value ones, 6.2 TB/s. Rows off 16 bytes, one call between events: 4224 x 12289 bf16 39 us (MX) and 47
-// (NV), 4000 x 5001 fp32 25 and 29; through shared memory with single loads they took 151, 180, 39 and 37.
+// 21.2 in 16-value ones, 6.2 TB/s. Rows off 16 bytes, one call between events: 4224 x 12288 bf16 at a
+// stride of 12289 39 us (MX) and 47 (NV), 4000 x 5001 fp32 25 and 29; through shared memory with single loads
+// they took 151, 180, 39 and 37.
 template <typename T, int FMT, bool VEC, int NU>
 __global__ void __launch_bounds__(256) fp4_quantize_kernel(const T* x, long long ldx, int cols, uint8_t* codes,
                                                            uint8_t* scales, float* row_scale) {
@@ -245,8 +246,8 @@ __global__ void __launch_bounds__(256) fp4_quantize_kernel(const T* x, long long
 // bytes (VEC) are stored as they come. Elsewhere a unit straddles aligned 16-byte words: a lane takes the
 // end of its neighbour's unit before its own and stores whole words, shifted into place; only the ends of a
 // row and of a warp are stored value by value. Bound by HBM, the values out above all. 4224 x 12288 to bf16: 23
-// us, 5.7 TB/s; 9216 x 3072 to fp32: 20 us, 6.4 TB/s. Rows off 32 bytes, one call between events: 4224 x 12289
-// to bf16 35 us, 4000 x 5001 to fp32 29-31; through shared memory in single values 49-53 and 27-29.
+// us, 5.7 TB/s; 9216 x 3072 to fp32: 20 us, 6.4 TB/s. Rows off 32 bytes, one call between events: 4224 x 12288
+// to bf16 at a stride of 12289 35 us, 4000 x 5001 to fp32 29-31; through shared memory in single values 49-53 and 27-29.
 template <typename T, int FMT, bool VEC>
 __global__ void __launch_bounds__(256, VEC ? 6 : 4) fp4_dequantize_kernel(const uint8_t* codes, const uint8_t* scales,
                                                                           const float* row_scale, int rows, int cols,
