@@ -361,6 +361,7 @@ int dit_rotary(const dit_rotary_plan* plan, const dit_rotary_rows* q, const dit_
     if (z == 0) a.q_heads = r->heads;
     const bool same = r->x == r->out && (rows == 1 || r->x_row == r->out_row) &&
                       (r->heads == 1 || r->x_head == r->out_head) && (batch == 1 || r->x_batch == r->out_batch);
+    if (r->x == r->out && !same) return DIT_EINVAL;  // in place under other strides: rows over one another
     a.copy[z] = !same;
     auto on16 = [&](const void* p, long long s0, long long s1, long long s2) {
       return reinterpret_cast<uintptr_t>(p) % 16 == 0 && s0 % ve == 0 && s1 % ve == 0 && s2 % ve == 0;

@@ -451,8 +451,8 @@ DIT_API int dit_rotary_tables(const dit_rotary_plan* plan, const int32_t* pos, i
 
 /* The heads of one tensor: value j of head h of row t of batch entry b is at
  * x[b * x_batch + t * x_row + h * x_head + j] (strides in values), likewise for out. out may be x with
- * the same strides (in place); otherwise the two must not overlap. Nor may q's output and k's, or either's
- * output and the other's input (equal pointers are refused). */
+ * the same strides (in place; refused with others); otherwise the two must not overlap. Nor may q's output
+ * and k's, or either's output and the other's input (equal pointers are refused). */
 typedef struct {
   const void* x;
   void* out;

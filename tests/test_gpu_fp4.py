@@ -238,6 +238,26 @@ def test_non_finite_rows_stay_in_their_row(fmt):
     assert (o[60, :149] == 0).all() and (o[np.delete(np.arange(M), [3, 130]), 10] == 0).all()
 
 
+@FMT
+@pytest.mark.parametrize("M,N,K", [(1, 97, 40), (130, 300, 328), (700, 1500, 1000)])
+def test_what_lies_past_the_rows_never_matters(fmt, M, N, K):
+    """Scale bytes of rows past the last, and the workspace, may hold anything (255 is NaN in both formats)."""
+    g = np.random.default_rng(M + N)
+    x, w = dev(_rows(g, M, K, False)), dev(_rows(g, N, K, False))
+    outs = []
+    for fill in (0, 255):
+        b = D.Fp4Matrix.empty(fmt, N, K)
+        b.codes.fill_(fill)
+        b.scales.fill_(fill)
+        D.dit_fp4_quantize(w, b)
+        ws = workspace(D.dit_linear_fp4_workspace_bytes(fmt, M, N, K))
+        ws.view(torch.uint8).fill_(fill)
+        outs.append(torch.full((M, N), 77.0, device="cuda"))
+        D.dit_linear_fp4(x, b, outs[-1], ws)
+    D.dit_check()
+    assert torch.isfinite(outs[0]).all() and torch.equal(outs[0], outs[1])
+
+
 def test_empty_and_streams_and_graph():
     g = np.random.default_rng(6)
     w, wv = _quantised(_rows(g, 96, 256), NV)

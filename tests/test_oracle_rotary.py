@@ -89,6 +89,9 @@ def test_rotary_refusals_before_any_cuda_call():
     assert call(q=D.dit_rotary_rows(256, 256, 4, 0, 256, 64, 0, 0, 64)) == -1            # output rows on one place
     assert call(q=D.dit_rotary_rows(256, 256, 4, 0, 256, 64, 0, 256, 0)) == -1
     assert call(batch=2, q=D.dit_rotary_rows(256, 256, 4, 0, 256, 64, 0, 256, 64)) == -1
+    # in place under other strides
+    assert call(q=D.dit_rotary_rows(256, 256, 4, 0, 256, 64, 0, 64, 192)) == -1
+    assert call(rows=1, d=64, q=D.dit_rotary_rows(256, 256, 4, 0, 256, 64, 0, 256, 128)) == -1
     # one tensor as q and as k, with an output on it
     assert call(q=q, k=q) == -1
     k = D.dit_rotary_rows(512, 256, 4, 0, 256, 64, 0, 256, 64)
