@@ -109,9 +109,15 @@ def test_block_with_scaled_tables():
 
 
 @FMT
-@pytest.mark.parametrize("H,heads,F,L,N", [(256, 4, 128, 0, 1), (256, 2, 384, 3, 130), (512, 8, 640, 17, 300)])
+@pytest.mark.parametrize("H,heads,F,L,N", [(256, 4, 128, 0, 1), (256, 2, 384, 3, 130), (512, 8, 640, 17, 300),
+                                           (1280, 10, 128, 5, 60), (3328, 26, 128, 2, 41)])
 def test_block_sizes(fmt, H, heads, F, L, N):
-    # odd row counts, an empty text, head widths 128 and 64: against the same linears called one by one
+    # odd row counts, an empty text, head widths 128 and 64: against the same linears called one by one.
+    # The attention is torch's in fp32 at the narrow sizes and the library's own at the wide ones: a code flips
+    # with probability e / (1/4) for an input off by e of itself and moves it by 1/4, sqrt(e / 4) RMS, so what the
+    # attentions differ by (0.026 of the out linear, a fifth of the residual at width 3328, e = 0.005) is 0.036 of
+    # the up linear's input, 0.05 of the SwiGLU's two factors and 0.11 after the down linear's quantiser: past
+    # the gate through no fault of the linears. With one attention the inputs agree to fp32 rounding.
     g = np.random.default_rng(H + N)
     R, d = L + N, H // heads
     dims = D.DitDims(H, heads, d, F)
@@ -150,13 +156,19 @@ def test_block_sizes(fmt, H, heads, F, L, N):
     rot = lambda t: torch.stack([t[..., ::2] * c[:, None] - t[..., 1::2] * s[:, None],  # noqa: E731
                                  t[..., ::2] * s[:, None] + t[..., 1::2] * c[:, None]], -1).flatten(-2)
     q, k, v = (t.bfloat16().float().transpose(0, 1) for t in (rot(q), rot(k), qkv[:, 2]))
-    o = (torch.softmax(q @ k.transpose(1, 2) / d ** 0.5, -1) @ v).transpose(0, 1).reshape(R, H)
+    if H < 1024:
+        o = (torch.softmax(q @ k.transpose(1, 2) / d ** 0.5, -1) @ v).transpose(0, 1).reshape(R, H)
+    else:
+        vt = torch.zeros(heads, d, D.dit_vt_stride(R), dtype=torch.bfloat16, device="cuda")
+        vt[:, :, :R] = v.bfloat16().transpose(1, 2)
+        o = torch.empty(R, H, dtype=torch.bfloat16, device="cuda")
+        D.dit_attention_qknorm(dims, R, q.bfloat16().contiguous(), k.bfloat16().contiguous(), vt, None, None, o)
     y = x + rows[:, 2] * lin(1, o)
     u = lin(2, norm(y, 3))
     y = y + rows[:, 5] * lin(3, torch.nn.functional.silu(u[:, ::2]) * u[:, 1::2])
     got = torch.cat([txt, img])
     _check(got.cpu().numpy().astype(np.float64), y.cpu().numpy().astype(np.float64), x.cpu().numpy().astype(np.float64),
-           8e-2, 2e-1, f"fp4 block {H} {heads} {F} {L}+{N}")
+           8e-2 if H < 1024 else 1e-2, 2e-1, f"fp4 block {H} {heads} {F} {L}+{N}")
 
 
 def _small(g, H, heads, F, R, fmt, rope_split=False, weights=False):
