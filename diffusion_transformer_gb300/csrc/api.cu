@@ -9,7 +9,7 @@
 #include <algorithm>
 #include <mutex>
 
-#include "fp4.cuh"
+#include "fp4_layout.h"
 #include "fp4.h"
 #include "internal.h"
 #include "tmap.h"

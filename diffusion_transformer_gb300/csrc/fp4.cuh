@@ -1,5 +1,5 @@
-// The arithmetic and the memory layout of microscaled 4-bit matrices, shared by the kernels that
-// write, read and multiply them. (The conversions are PTX cvt instructions: one rounding each, to
+// The arithmetic of microscaled 4-bit matrices, shared by the kernels that write, read and multiply
+// them (fp4_layout.h: where their bytes stand). (The conversions are PTX cvt instructions: one rounding each, to
 // nearest with ties to even.)
 #pragma once
 
@@ -7,25 +7,10 @@
 #include <cuda_runtime.h>
 
 #include "../../include/dit.h"
+#include "fp4_layout.h"
 #include "fp4_ptx.cuh"
 
 namespace dit {
-
-// Code bytes of a row: two codes per byte (even column in the low half), rows padded with zero codes
-// to whole 32 columns, so every row starts on 16 bytes (the TMA's rule for strides).
-__host__ __device__ constexpr long long fp4_code_row_bytes(int cols) { return (cols + 31LL) / 32 * 16; }
-// Groups of four blocks along a row (the last one padded).
-__host__ __device__ constexpr int fp4_groups(int fmt, int cols) {
-  const int block = fmt == DIT_FP4_NV ? 16 : 32;
-  return (cols + 4 * block - 1) / (4 * block);
-}
-// Scale bytes stand in tiles of 128 rows x 4 blocks, 512 bytes each, the tiles of a 128-row band one
-// after another: inside a tile row r is at 16 (r % 32) + 4 (r / 32), its four blocks consecutive. This
-// is the order tcgen05.cp (32 x 128 bit) spreads over tensor memory for the block-scaled MMA.
-__host__ __device__ constexpr long long fp4_scale_row(int fmt, int row, int cols) {
-  return (long long)(row >> 7) * fp4_groups(fmt, cols) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4;
-}
-__host__ __device__ constexpr int fp4_scale_block(int block) { return (block >> 2) * 512 + (block & 3); }
 
 // A row's derived factors (NV) from the bits of its largest magnitude A: u = 448 / A maps a block's
 // magnitude to its e4m3 scale, t = 2688 / A = 1 / g, g = A / 2688 (448 * 6: the largest scale times the

@@ -1,5 +1,5 @@
 // Product of two microscaled 4-bit matrices on the block-scaled tcgen05 MMA: out = A B^T, A [M, K], B
-// [N, K] in the layout of fp4.cuh, fp32 accumulators in tensor memory, the NV format's row scales applied
+// [N, K] in the layout of fp4_layout.h, fp32 accumulators in tensor memory, the NV format's row scales applied
 // to the accumulator as it is drained.
 //
 // A 128-byte swizzled shared-memory row holds 256 codes, so a pipeline stage is K = 256: four MMAs of

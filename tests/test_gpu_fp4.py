@@ -370,3 +370,46 @@ def test_binding_refusals():
         D.Fp4Matrix(NV, 9, 64, w.codes, w.scales, w.row_scale)
     with pytest.raises(D.DitError):
         D.dit_fp4_matmul(D.Fp4Matrix.empty(MX, 8, 64), w, torch.zeros(8, 8, device="cuda"))
+
+
+@FMT
+def test_columns_past_2_to_24_blocks(fmt):
+    # one row so long that its scale bytes reach past 2 GB: a short row's values at its two ends and in front of that
+    # border, zeros between; codes and scales are the short row's, the rest zero, and the product is the short rows'
+    g = np.random.default_rng(21)
+    block, n = (16, 32)[fmt], 256
+    K = (1 << 24) * block + 1024 + 16
+    starts = [0, (1 << 24) * block - n, K - 16 - n]  # multiples of a group of four blocks
+    short = [_rows(g, 1, 3 * n) for _ in range(2)]
+    ms = []
+    for x in short:
+        xd = torch.zeros(1, K, dtype=torch.bfloat16, device="cuda")
+        for i, s in enumerate(starts):
+            xd[0, s:s + n] = torch.from_numpy(x[0, i * n:(i + 1) * n])
+        m, few = D.Fp4Matrix.empty(fmt, 1, K), D.Fp4Matrix.empty(fmt, 1, 3 * n)
+        D.dit_fp4_quantize(xd, m)
+        D.dit_fp4_quantize(dev(x).bfloat16(), few)
+        scales, tiles = m.scales.view(-1, 512)[:, :4], few.scales.view(-1, 512)[:, :4]  # row 0 of each tile
+        per = n // (4 * block)
+        for i, s in enumerate(starts):
+            assert torch.equal(m.codes[s // 2:(s + n) // 2], few.codes[i * n // 2:(i + 1) * n // 2])
+            assert torch.equal(scales[s // (4 * block):][:per], tiles[i * per:(i + 1) * per])
+        assert int(scales.count_nonzero()) == int(tiles.count_nonzero())
+        xd.fill_(77)
+        D.dit_fp4_dequantize(m, xd)
+        back = torch.empty(1, 3 * n, dtype=torch.bfloat16, device="cuda")
+        D.dit_fp4_dequantize(few, back)
+        for i, s in enumerate(starts):
+            assert torch.equal(xd[0, s:s + n], back[0, i * n:(i + 1) * n])
+        assert int(xd.count_nonzero()) == int(back.count_nonzero())
+        del xd, scales
+        ms.append((m, few))
+    D.dit_check()
+    out, ref = torch.empty(1, 1, device="cuda"), torch.empty(1, 1, device="cuda")
+    D.dit_fp4_matmul(ms[0][0], ms[1][0], out)
+    D.dit_fp4_matmul(ms[0][1], ms[1][1], ref)
+    D.dit_check()
+    codes = [O.fp4_quantize(x, fmt) for x in short]
+    a, b = (O.fp4_values(*c, fmt, 3 * n).astype(np.float64) for c in codes)
+    for o in (out, ref):  # zeros add no rounding of their own: both as the short product
+        _check_product(o, a, b, 3 * n)
