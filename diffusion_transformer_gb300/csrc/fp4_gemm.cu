@@ -91,6 +91,27 @@ __device__ __forceinline__ void scale4(uint32_t* x, uint64_t row2, const float4&
   x[2] = uint32_t(hi);
   x[3] = uint32_t(hi >> 32);
 }
+// Row factors that may be multiplied first whatever the other factor is. An accumulator that is not zero lies
+// between 2^-20 (the smallest codes and scales) and 2^53 (2688^2 times the longest K), so its product with a factor
+// between 2^-100 and 2^64 is neither infinite nor subnormal; a NaN is left to scale_far.
+__device__ __forceinline__ bool near_factor(float f) { return f == 0.f || (f >= 0x1p-100f && f <= 0x1p64f); }
+// x times two row factors of any size, finite wherever the result is: the larger one first, and where that one is past
+// 2^64 and the other below 1, 2^64 is taken from the one and given to the other, which is exact.
+__device__ __forceinline__ float scale_far(float x, float a, float b) {
+  float hi = a > b ? a : b, lo = a > b ? b : a;  // each of them once, so that a NaN stays
+  if (hi > 0x1p64f && lo < 1.f) {
+    hi *= 0x1p-64f;
+    lo *= 0x1p64f;
+  }
+  return x * hi * lo;
+}
+// N neighbouring products of one row by the row's factor and their columns', in any order of size. The column
+// factors are read one by one, so that this rare way holds no registers that the usual one would spill.
+template <int N>
+__device__ __forceinline__ void scale_row_far(uint32_t* x, float row, const volatile float* cols) {
+#pragma unroll
+  for (int c = 0; c < N; ++c) x[c] = __float_as_uint(scale_far(__uint_as_float(x[c]), row, cols[c]));
+}
 
 // z / (1 + e^-z); the approximate division is within two units of the fp32 result, which goes on to bf16
 __device__ __forceinline__ float silu_bf16(float z) { return __fdividef(z, 1.f + __expf(-z)); }
@@ -394,9 +415,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       mbar_arrive_cluster(tempty0 + uint32_t(acc) * 8u);
       if (row0 >= rowsP) continue;
       if constexpr (SC::kNv) {
-        const uint64_t rp2 = f2_pack(rp, rp);
+        if (__all_sync(0xffffffffu, near_factor(rp))) {
+          const uint64_t rp2 = f2_pack(rp, rp);
 #pragma unroll
-        for (int c = 0; c < 128; c += 4) scale4(w[c >> 5] + (c & 31), rp2, *reinterpret_cast<const float4*>(cf + c));
+          for (int c = 0; c < 128; c += 4) scale4(w[c >> 5] + (c & 31), rp2, *reinterpret_cast<const float4*>(cf + c));
+        } else {
+          scale_row_far<128>(w[0], rp, cf);
+        }
       }
       if (ep.head_dim == 128) {
         qkv_store<128>(ep, w[0], row0, lane, n0, scratch);
@@ -457,11 +482,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         if (q0 >= rowsQ || row0 >= rowsP) continue;
         if constexpr (SC::kNv) {
-          const uint64_t rp2 = f2_pack(rp, rp);
+          if (__all_sync(0xffffffffu, near_factor(rp))) {
+            const uint64_t rp2 = f2_pack(rp, rp);
 #pragma unroll
-          for (int c = 0; c < 64; c += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(cf + c);
-            scale4(w[c >> 5] + (c & 31), rp2, f);
+            for (int c = 0; c < 64; c += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(cf + c);
+              scale4(w[c >> 5] + (c & 31), rp2, f);
+            }
+          } else {
+            scale_row_far<64>(w[0], rp, cf);
           }
         }
         auto val = [&](int c) { return __uint_as_float(w[c >> 5][c & 31]); };
@@ -616,6 +645,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
   pdl_trigger();
+  bool near = true;  // the tile's A factors may be multiplied first
 
   if (warp == 0) {
     if (elect_one()) {
@@ -672,7 +702,9 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
   } else {
     if constexpr (SC::kNv) {
       const int i = int(threadIdx.x) - 64;
-      sFa[i] = i < bn && m0 + i < p.M ? __ldg(p.a_scale + m0 + i) : 0.f;
+      const float ra = i < bn && m0 + i < p.M ? __ldg(p.a_scale + m0 + i) : 0.f;
+      near = near_factor(ra);
+      sFa[i] = ra;
       sFb[i] = n0 + i < p.N ? __ldg(p.b_scale + n0 + i) : 0.f;
     }
     (void)mbar_wait_warp(smem_u32(tfull), 0, p.err, kErrTimeoutEpilogue);
@@ -686,7 +718,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
   const int n = n0 + quad * 32 + lane;
   T* out = static_cast<T*>(p.out);
   float* tile = reinterpret_cast<float*>(sB);
-  __syncthreads();
+  near = __syncthreads_and(near);
   tc_fence_after();
   const int live = min(bn, p.M - m0);
   if (warp >= 2) {
@@ -710,7 +742,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const float x = __uint_as_float(w[e + k]);
-          v[e + k] = T(SC::kNv ? x * ff[k] * rb : x);
+          v[e + k] = T(!SC::kNv ? x : (near ? x * ff[k] * rb : scale_far(x, ff[k], rb)));
         }
       }
       if (n < p.N) {
@@ -752,7 +784,8 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
         if constexpr (SC::kNv) {
           const float ra = sFa[c];
           const float4 f = *reinterpret_cast<const float4*>(sFb + r4);
-          s = make_float4(s.x * ra * f.x, s.y * ra * f.y, s.z * ra * f.z, s.w * ra * f.w);
+          s = near ? make_float4(s.x * ra * f.x, s.y * ra * f.y, s.z * ra * f.z, s.w * ra * f.w)
+                   : make_float4(scale_far(s.x, ra, f.x), scale_far(s.y, ra, f.y), scale_far(s.z, ra, f.z), scale_far(s.w, ra, f.w));
         }
         T* o = out + (long long)(m0 + c) * p.ldo + n0 + r4;
         if (whole) {

@@ -413,3 +413,36 @@ def test_columns_past_2_to_24_blocks(fmt):
     a, b = (O.fp4_values(*c, fmt, 3 * n).astype(np.float64) for c in codes)
     for o in (out, ref):  # zeros add no rounding of their own: both as the short product
         _check_product(o, a, b, 3 * n)
+
+
+@pytest.mark.parametrize("out,pad,shift", [(torch.float32, 0, 0), (torch.float32, 3, 1), (torch.bfloat16, 0, 0)],
+                         ids=["fp32", "fp32-off", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(1, 1000, 256), (17, 256, 1000), (100, 300, 5003), (129, 257, 257), (1100, 1500, 777)])
+def test_rows_of_any_size_multiply_without_overflow(M, N, K, out, pad, shift):
+    # rows from 2^-98 to 2^126 against one another, huge ones against tiny ones among them: wherever the value is finite
+    # the product is, and as exact as the gate says; wherever it is past fp32 it is infinite. Every kernel: pairs
+    # of CTAs with either operand first (off 32 bytes the second), one CTA and a cluster of them. A store below 2^-126
+    # is off by half of 2^-149 (a bf16 one, which the 2^-126 steps of its type, by half of 2^-133).
+    g = np.random.default_rng(M + N + K)
+    x, w = (_as_bf16(g.standard_normal((n, K)).clip(-3, 3)) for n in (M, N))
+    ex, ew = (g.integers(-98, 126, (n, 1)) for n in (M, N))
+    ex[:1], ew[:3] = 120, [[-20], [-90], [-110 + 14]]
+    if M > 8:
+        ex[1:4], ew[3:5] = [[-97], [70], [0]], [[96], [64]]
+    x, w = ((v * 2.0 ** (e - 2.0)).astype(np.float32) for v, e in ((x, ex), (w, ew)))
+    a, av = _quantised(x, NV)
+    b, bv = _quantised(w, NV)
+    o = _on_gpu(np.full((M, N), 9.0, np.float32), out, pad, shift)
+    D.dit_fp4_matmul(a, b, o)
+    D.dit_check()
+    ref, S = av @ bv.T, np.abs(av) @ np.abs(bv).T
+    got = o.float().cpu().numpy().astype(np.float64)
+    half = 2.0 ** -8 if out == torch.bfloat16 else 0.0
+    gate = (K / 64 + 2) * 2.0 ** -23 * S + half * np.abs(ref) + 2.0 ** (-134 if half else -149)
+    top = 2.0 ** 128 * (1 - (2.0 ** -9 if half else 2.0 ** -25))  # what rounds to infinity from here on
+    finite, past = np.abs(ref) + gate < top, np.abs(ref) - gate > top
+    assert finite.sum() > 0.2 * M * N and (M * N < 20000 or past.any())
+    with np.errstate(invalid="ignore"):
+        bad = finite & ~(np.abs(got - ref) <= gate)
+    assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:4], got[bad][:4], ref[bad][:4])
+    assert np.array_equal(got[past], np.sign(ref[past]) * np.inf)
