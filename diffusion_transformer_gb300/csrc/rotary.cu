@@ -293,7 +293,7 @@ int dit_rotary_plan_init(const dit_rotary_spec* s, dit_rotary_plan* plan) {
     if (s->scaling == DIT_ROTARY_YARN) {
       auto at = [&](double turns) { return w * std::log(s->original / (turns * two_pi)) / (2 * std::log(theta)); };
       lo = std::fmax(0.0, std::floor(at(s->beta_fast)));
-      const double hi = std::fmin(double(w / 2 - 1), std::ceil(at(s->beta_slow)));
+      const double hi = std::fmin(double(w - 1), std::ceil(at(s->beta_slow)));  // may lie past the last pair
       span = std::fmax(hi - lo, 1e-3);
       p.amplitude = float(0.1 * std::log(s->factor) + 1.0);
     }

@@ -406,7 +406,7 @@ DIT_API int dit_rope_tables(int L, int grid_h, int grid_w, int head_dim, float t
  *   DIT_ROTARY_LINEAR  f / factor
  *   DIT_ROTARY_NTK     theta * factor^(w / (w - 2)) in theta's place (w = width[a]; w = 2: unscaled)
  *   DIT_ROTARY_YARN    f (1 - r) + (f / factor) r with r = clamp((k - lo) / max(hi - lo, 0.001), 0, 1),
- *                      lo = max(0, floor(at(beta_fast))), hi = min(w/2 - 1, ceil(at(beta_slow))),
+ *                      lo = max(0, floor(at(beta_fast))), hi = min(w - 1, ceil(at(beta_slow))),
  *                      at(n) = w ln(original / (2 pi n)) / (2 ln theta), the pair that makes n turns over
  *                      the `original` positions; cos and sin are times 0.1 ln(factor) + 1
  * factor, original and the betas are read only by the scalings that name them. */

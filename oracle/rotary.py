@@ -20,7 +20,7 @@ def rotary_frequencies(widths, theta=10000.0, scaling="none", factor=1.0, origin
             elif scaling == "yarn":
                 def at(turns):
                     return w * math.log(original / (2 * math.pi * turns)) / (2 * math.log(theta))
-                lo, hi = max(0.0, math.floor(at(beta_fast))), min(w / 2 - 1.0, math.ceil(at(beta_slow)))
+                lo, hi = max(0.0, math.floor(at(beta_fast))), min(w - 1.0, math.ceil(at(beta_slow)))
                 r = min(1.0, max(0.0, (k - lo) / max(hi - lo, 1e-3)))
                 f = f * (1 - r) + f / factor * r
             freq.append(f)

@@ -152,3 +152,32 @@ def test_fp4_refusals_before_any_cuda_call():
                                        enumerate(((768, 256), (256, 256), (256, 256), (256, 128)))]))
     assert block(mixed) == -1
     assert L.dit_fp4_scale_bytes(2, 1, 1) == 0 and L.dit_linear_fp4_workspace_bytes(0, 1, 1, 0) == 0
+
+
+@pytest.mark.parametrize("w,theta,factor,original,fast,slow", [
+    (4, 1e4, 16.0, 4096, 32.0, 1.0), (6, 1e4, 4.0, 4096, 32.0, 1.0), (32, 256.0, 2.0, 1536, 32.0, 1.0),
+    (48, 256.0, 4.0, 1536, 32.0, 1.0), (64, 1e4, 4.0, 131072, 32.0, 1.0), (128, 1e4, 4.0, 65536, 32.0, 1.0),
+    (128, 1e4, 16.0, 4096, 32.0, 1.0), (96, 5e5, 8.0, 8192, 16.0, 2.0)])
+def test_by_parts_is_the_published_range(w, theta, factor, original, fast, slow):
+    # the published range of pairs ends at the rotated width less one, not at the last pair, so that a narrow axis (or a
+    # long trained length) stops inside the ramp: pairs up to floor(at(fast)) as they are, from ceil(at(slow)) on divided
+    def at(turns):
+        return w * math.log(original / (turns * 2 * math.pi)) / (2 * math.log(theta))
+
+    lo, hi = max(math.floor(at(fast)), 0), min(math.ceil(at(slow)), w - 1)
+    want = []
+    for k in range(w // 2):
+        f = theta ** (-2.0 * k / w)
+        keep = 1.0 - min(1.0, max(0.0, (k - lo) / (hi - lo)))
+        want.append(f / factor * (1.0 - keep) + f * keep)
+    spec = dict(widths=[w], theta=theta, scaling="yarn", factor=factor, original=original, beta_fast=fast, beta_slow=slow)
+    f, _, amp = O.rotary_frequencies(**spec)
+    assert np.allclose(f, want, rtol=1e-13) and amp == 0.1 * math.log(factor) + 1.0
+    got = [D.RotaryPlan(**spec).c.turns[i] * 2.0 ** -64 * 2 * math.pi for i in range(w // 2)]
+    assert np.allclose(got, want, rtol=1e-13, atol=2 * math.pi * 2.0 ** -63)
+
+
+def test_by_parts_of_two_pairs_by_hand():
+    # width 4: at(1) = 4 ln(4096 / 2 pi) / (2 ln 10^4) = 1.41, so the ramp runs from pair 0 to 2 and pair 1 is half way
+    f, _, _ = O.rotary_frequencies([4], scaling="yarn", factor=16.0, original=4096)
+    assert np.allclose(f, [1.0, 0.01 * (0.5 + 0.5 / 16)], rtol=1e-15)
