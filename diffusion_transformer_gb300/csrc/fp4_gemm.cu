@@ -459,9 +459,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       if (!mbar_wait_warp(smem_u32(&tfull[acc]), uint32_t(it >> 1) & 1u, p.err, kErrTimeoutEpilogue)) break;
       tc_fence_after();
       const uint32_t taddr = tmem + (uint32_t(quad * 32) << 16) + (acc ? acc1 : 0);
-      // what this warp holds back from the next tile: nothing of the overlapped columns (group 0), or
-      // nothing at all
-      if (overlap && half == 1) mbar_arrive_cluster(tempty0 + uint32_t(acc) * 8u);
+      // what this warp holds back from the next tile: nothing of the overlapped columns (group 0), or nothing at all.
+      // Its arrival also stands for its reads of the tile before, which end ahead of the fence
+      if (overlap && half == 1) {
+        tc_fence_before();
+        mbar_arrive_cluster(tempty0 + uint32_t(acc) * 8u);
+      }
 #pragma unroll 1
       for (int j = half; j < groups; j += 2) {
         const int g = group_at(j), q0 = qb * bn + g * 64;
