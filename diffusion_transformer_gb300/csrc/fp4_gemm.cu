@@ -33,6 +33,7 @@
 
 #include "fp4.cuh"
 #include "fp4.h"
+#include "fp4_choice.h"
 #include "fp4_ptx.cuh"
 #include "internal.h"
 #include "tmap.h"
@@ -40,7 +41,7 @@
 namespace dit {
 namespace {
 
-constexpr int kStageK = 256;                  // codes per stage and row: 128 bytes
+constexpr int kStageK = kFp4StageK;           // codes per stage and row: 128 bytes
 constexpr uint32_t kTileBytes = 128 * 128;    // 128 rows of a stage
 template <int FMT>
 struct Scales {
@@ -586,7 +587,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 // ---------------------------------------------------------------------------------------------
 constexpr int kSplitThreads = 192;
 constexpr uint32_t kSplitMinSmem = 116 * 1024;
-constexpr int kSplitMaxStages = 12, kMaxGridY = 65535;
+constexpr int kSplitMaxStages = 12;
 constexpr uint32_t kSplitFixed = 1024 + 2 * 128 * 4 + 8 * (2 * kSplitMaxStages + 1) + 16;
 __host__ __device__ constexpr uint32_t split_stage_bytes(int bn, uint32_t sf) { return kTileBytes + uint32_t(bn) * 128 + 2 * sf; }
 
@@ -903,7 +904,7 @@ int launch_split(const dit_fp4_matrix& a, const dit_fp4_matrix& b, Fp4Params p, 
   constexpr int G = Scales<FMT>::kGroups;
   p.bn = bn;
   const long long nt = (p.N + 127) / 128, mt = (p.M + bn - 1) / bn;
-  if (nt * parts > 0x7fffffffLL || mt > kMaxGridY) return DIT_EUNSUPPORTED;
+  if (nt * parts > 0x7fffffffLL || mt > kFp4MaxGridY) return DIT_EUNSUPPORTED;
   const int KB = (p.K + kStageK - 1) / kStageK;
   const uint32_t sb = split_stage_bytes(bn, Scales<FMT>::kBytes);
   // A cluster's CTA asks for more than half of an SM's shared memory, as every kernel here that allocates
@@ -927,48 +928,13 @@ int launch_split(const dit_fp4_matrix& a, const dit_fp4_matrix& b, Fp4Params p, 
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? DIT_OK : DIT_ECUDA;
 }
 
-// The kernel and tile with the least estimated time, in ns, fitted to what 28 sizes from 1 x 18432 to
-// 4224 x 24576 took with every tile. A pair kernel takes 3000 once, half of the operands' bytes at the memory's
-// rate, and per round of tiles over the CTA pairs 900 (1100 swapped) and 215, 250 or 320 per stage of 256
-// columns for 128, 192 or 256 rows of Q. A split kernel takes 2200 once, per wave of CTAs 10 per row of its
-// tile and 60 + 1.6 per row for a stage, at least B's bytes at the memory's rate, and 1800 + 5 per row to join
-// the parts of a cluster. Both sides, in us: 1088 x 3072 x 12288 17.4 with 192 rows swapped, 20.9 with 256;
-// 4224 x 24576 x 3072 104 with 256, 117 with 192; 333 x 777 x 1000 4.6 split, 5.4 in pairs; 200 x 24576 x 3072
-// 18.1 split, 13.7 in pairs; 33 x 3072 x 12288 13.3 with one CTA per tile, 6.9 with four.
 template <int FMT, typename T>
 int launch_product(const dit_fp4_matrix& a, const dit_fp4_matrix& b, const Fp4Params& p, cudaStream_t st) {
-  const int sms = num_sms(), units = sms / 2;
-  const long long KB = (p.K + kStageK - 1) / kStageK;
-  auto up = [](long long x, long long y) { return (x + y - 1) / y; };
-  // unswapped tiles store 32 bytes of a row at a time
   const bool rows32 = reinterpret_cast<uintptr_t>(p.out) % 32 == 0 && (p.M == 1 || p.ldo * (long long)sizeof(T) % 32 == 0);
-  long long best = -1;
-  int bn = 0, parts = 0;
-  bool swap = false;
-  for (int s = rows32 ? 0 : 1; s < 2; ++s)
-    for (int i = 0; i < 3; ++i) {
-      constexpr int kRows[3] = {256, 192, 128}, kStageNs[3] = {320, 250, 215};
-      const long long tiles = up(s ? p.N : p.M, 256) * up(s ? p.M : p.N, kRows[i]);
-      const long long cost = 3000 + (p.M + (long long)p.N) * p.K / 24000 + up(tiles, units) * (900 + 200 * s + KB * kStageNs[i]);
-      if (best < 0 || cost < best) {
-        best = cost;
-        bn = kRows[i];
-        swap = s != 0;
-      }
-    }
-  const int sn = p.M <= 16 ? 16 : (p.M <= 32 ? 32 : (p.M <= 64 ? 64 : 128));
-  const long long ctas = up(p.N, 128) * up(p.M, sn);
-  for (int k = 1; k <= 8 && k <= KB && (k == 1 || ctas * k <= sms) && up(p.M, sn) <= kMaxGridY; k *= 2) {
-    const long long busy = up(ctas * k, sms) * (10 * sn + up(KB, k) * (60 + 8 * sn / 5));
-    const long long cost = 2200 + std::max(busy, (long long)p.N * p.K / 9800) + (k > 1 ? 1800 + 5 * sn : 0);
-    if (cost < best) {
-      best = cost;
-      parts = k;
-    }
-  }
-  if (parts > 0) return launch_split<FMT, T>(a, b, p, sn, parts, st);
+  const Fp4Choice c = fp4_choose(p.M, p.N, p.K, rows32, num_sms());
+  if (c.parts > 0) return launch_split<FMT, T>(a, b, p, c.bn, c.parts, st);
   constexpr int kStore = sizeof(T) == 2 ? kEpiStoreBF16 : kEpiStoreF32;
-  return swap ? launch_pair<FMT, kStore, true>(a, b, p, {}, bn, st) : launch_pair<FMT, kStore, false>(a, b, p, {}, bn, st);
+  return c.swap ? launch_pair<FMT, kStore, true>(a, b, p, {}, c.bn, st) : launch_pair<FMT, kStore, false>(a, b, p, {}, c.bn, st);
 }
 
 template <int FMT>

@@ -446,3 +446,14 @@ def test_rows_of_any_size_multiply_without_overflow(M, N, K, out, pad, shift):
         bad = finite & ~(np.abs(got - ref) <= gate)
     assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:4], got[bad][:4], ref[bad][:4])
     assert np.array_equal(got[past], np.sign(ref[past]) * np.inf)
+
+
+# clusters of two, four and eight CTAs for each height of the split kernel's tiles, from a single row on
+CLUSTER_SIZES = [(1, 77, 6659), (16, 1024, 14000), (1, 1000, 14000), (3, 2048, 13315), (17, 77, 5123), (32, 2048, 9000),
+                 (23, 3000, 12035), (65, 3000, 3331), (100, 4000, 3400)]
+
+
+@FMT
+@pytest.mark.parametrize("M,N,K", CLUSTER_SIZES)
+def test_matmul_of_few_rows_on_clusters(fmt, M, N, K):
+    test_matmul(fmt, M, N, K)
