@@ -630,6 +630,16 @@ def _torch():
     return _torch_mod
 
 
+_INT_MAX = 0x7fffffff
+
+
+def _fits(*sizes):
+    """The library's sizes are C ints, of which ctypes would keep the low 32 bits without a word."""
+    for n in sizes:
+        if not -_INT_MAX <= n <= _INT_MAX:
+            raise ValueError(f"a size of {n}: past 32 bits")
+
+
 def _current(stream):
     """(current device, stream handle)"""
     if _torch_mod is None:
@@ -659,6 +669,7 @@ class RotaryPlan:
         widths = [int(w) for w in widths]
         if not 1 <= len(widths) <= 4:
             raise ValueError("widths: one to four axes")
+        _fits(original, *widths)
         self.spec = dit_rotary_spec(len(widths), (c_int * 4)(*widths), {"pairs": 0, "halves": 1}[layout],
                                     {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}[scaling], original, theta, factor,
                                     beta_fast, beta_slow)
@@ -685,6 +696,7 @@ def dit_rotary_tables(plan: RotaryPlan, pos, cos, sin, stream=None):
     """cos, sin [rows, plan.dim / 2] fp32 of pos [rows, plan.axes] int32 (or [rows] for one axis)."""
     import torch
     rows = cos.shape[0]
+    _fits(rows)
     if cos.shape != (rows, plan.dim // 2) or sin.shape != cos.shape:
         raise ValueError("cos, sin: expected [rows, dim / 2]")
     dev, st = _current(stream)
@@ -720,7 +732,10 @@ def _rotary_rows(x, out, dev, name):
         raise ValueError(f"{name}: expected [batch, rows, heads, head_dim] or [rows, heads, head_dim]")
     if (ex != 1 or eo != 1) and shape[-1] > 1:
         raise ValueError(f"{name}: the last dimension must be dense")
-    return _rows_struct.pack(x.data_ptr(), out.data_ptr(), shape[-2], bx, rx, hx, bo, ro, ho), kind, shape
+    try:
+        return _rows_struct.pack(x.data_ptr(), out.data_ptr(), shape[-2], bx, rx, hx, bo, ro, ho), kind, shape
+    except struct.error:
+        raise ValueError(f"{name}: {shape[-2]} heads") from None
 
 
 def dit_rotary(plan: RotaryPlan, q, k, pos, q_out=None, k_out=None, inverse: bool = False, stream=None):
@@ -735,8 +750,10 @@ def dit_rotary(plan: RotaryPlan, q, k, pos, q_out=None, k_out=None, inverse: boo
         if kk != kind or sk[:-2] != shape[:-2] or sk[-1] != shape[-1]:
             raise ValueError("q and k: expected the same type, batch, rows and head_dim")
     batch = shape[0] if len(shape) == 4 else 1
-    rows = shape[-3]
-    rc = lib().dit_rotary(plan.ref, a, c, kind, batch, rows, shape[-1], _positions(plan, pos, batch * rows, dev),
+    rows, dim = shape[-3], shape[-1]
+    if batch > _INT_MAX or rows > _INT_MAX or dim > _INT_MAX:
+        _fits(batch, rows, dim)
+    rc = lib().dit_rotary(plan.ref, a, c, kind, batch, rows, dim, _positions(plan, pos, batch * rows, dev),
                           1 if inverse else 0, st)
     if rc:
         _ok(rc, "dit_rotary")
@@ -789,10 +806,12 @@ def _on(m: "Fp4Matrix", dev, name):
 
 
 def dit_fp4_code_bytes(rows: int, cols: int) -> int:
+    _fits(rows, cols)
     return lib().dit_fp4_code_bytes(rows, cols)
 
 
 def dit_fp4_scale_bytes(format: int, rows: int, cols: int) -> int:
+    _fits(rows, cols)
     return lib().dit_fp4_scale_bytes(format, rows, cols)
 
 
@@ -824,6 +843,7 @@ def dit_fp4_matmul(a: Fp4Matrix, b: Fp4Matrix, out, stream=None):
 
 
 def dit_linear_fp4_workspace_bytes(format: int, M: int, N: int, K: int) -> int:
+    _fits(M, N, K)
     return lib().dit_linear_fp4_workspace_bytes(format, M, N, K)
 
 
@@ -831,6 +851,8 @@ def dit_linear_fp4(x, w: Fp4Matrix, out, ws, stream=None):
     """out [M, w.rows] = fp4(x) w^T for x [M, w.cols], quantised per call into ws."""
     dev, st = _current(stream)
     M = x.shape[0]
+    if M > _INT_MAX:
+        _fits(M)
     p, kind, ld = _matrix(x, M, w.cols, dev, "x")
     po, ko, ldo = _matrix(out, M, w.rows, dev, "out")
     if ws.get_device() != dev or not ws.is_contiguous():
@@ -853,6 +875,7 @@ class Fp4BlockWeights:
 
 
 def dit_block_fp4_workspace_bytes(dims: DitDims, format: int, L: int, N: int) -> int:
+    _fits(L, N)
     return lib().dit_block_fp4_workspace_bytes(byref(dims.c), format, L, N)
 
 
