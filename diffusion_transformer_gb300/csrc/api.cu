@@ -50,6 +50,11 @@ int* err_word() {
 inline bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
+// The QKV epilogues read the rotary tables in 16-byte words (the text's only where there are text rows).
+bool tables_al16(int L, const float* tc, const float* ts, const float* ic, const float* is) {
+  return (L == 0 || (al16(tc) && al16(ts))) && al16(ic) && al16(is);
+}
+
 bool dims_ok(const dit_dims* d) {
   if (!d) return false;
   if (d->head_dim != 64 && d->head_dim != 128) return false;
@@ -927,7 +932,7 @@ int check_block_args(const dit_dims* d, const float* txt, int L, const float* im
   if (!dims_ok(d)) return DIT_EUNSUPPORTED;
   if (L < 0 || N < 1 || (L > 0 && (!txt || !tc || !ts)) || !img || !ic || !is) return DIT_EINVAL;
   if (!mod->rows || mod->M < 1) return DIT_EINVAL;
-  if (!al16(txt) || !al16(img) || !al16(mod->rows)) return DIT_EINVAL;
+  if (!al16(txt) || !al16(img) || !al16(mod->rows) || !tables_al16(L, tc, ts, ic, is)) return DIT_EINVAL;
   if (!ws) return DIT_EWORKSPACE;
   if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return DIT_EINVAL;
   if (ws_bytes < dit_workspace_bytes(d, L, N, variant)) return DIT_EWORKSPACE;
@@ -988,7 +993,7 @@ int check_block_call_without_workspace(const dit_dims* d, const dit_block_w* w, 
   if (!dims_ok(d)) return DIT_EUNSUPPORTED;
   if (L < 0 || N < 1 || (L > 0 && (!txt || !tc || !ts)) || !img || !ic || !is) return DIT_EINVAL;
   if (!mod->rows || mod->M < 1) return DIT_EINVAL;
-  if (!al16(txt) || !al16(img) || !al16(mod->rows)) return DIT_EINVAL;
+  if (!al16(txt) || !al16(img) || !al16(mod->rows) || !tables_al16(L, tc, ts, ic, is)) return DIT_EINVAL;
   if (!w || !w->wqkv || !w->wout || !w->wup || !w->wdown) return DIT_EINVAL;
   if (!al16(w->wqkv) || !al16(w->wout) || !al16(w->wup) || !al16(w->wdown)) return DIT_EINVAL;
   return DIT_OK;
@@ -1433,7 +1438,9 @@ int dit_block_forward_fp4(const dit_dims* d, const dit_block_wfp4* w, float* txt
                           void* ws, size_t ws_bytes, dit_stream_t stream) {
   int rc = check_block_args(d, txt, L, img, N, tc, ts, ic, is, mod, ws, ws_bytes, 0);
   if (rc != DIT_OK) return rc;
-  if (!w) return DIT_EINVAL;
+  if (!w || !al16(w->norm1) || !al16(w->norm2)) return DIT_EINVAL;
+  auto al4 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; };
+  if (!al4(w->q_norm) || !al4(w->k_norm) || !al4(mod->map)) return DIT_EINVAL;
   for (int i = 0; i < 4; ++i) {
     int n, k;
     linear_shape(d, i, &n, &k);

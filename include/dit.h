@@ -81,7 +81,7 @@ typedef struct {
  *   wdown [H, F]
  *   norm1, norm2 [H] fp32 affine weights of the two modulated norms, or NULL for ones
  *   q_norm, k_norm [d] fp32 head-norm weights, or NULL for ones
- * Weight pointers must be 16-byte aligned. */
+ * Weight pointers must be 16-byte aligned, and so must the rotary tables of every block form. */
 typedef struct {
   const uint16_t* wqkv;
   const uint16_t* wout;
@@ -535,7 +535,8 @@ typedef struct {
  * each linear its bf16 activation (h, o, h2, a) is quantised in the weights' format, and the 4-bit
  * product runs through the linear's usual epilogue; everything else as dit_block_forward, including
  * tables from dit_rotary_tables. Workspace: dit_block_fp4_workspace_bytes(dims, format, L, N), 256-byte
- * aligned. Errors as dit_block_forward; DIT_EINVAL for weights of other sizes or mixed formats. */
+ * aligned. Errors as dit_block_forward; DIT_EINVAL for weights of other sizes or mixed formats, and for norm1 or
+ * norm2 off 16 bytes. */
 DIT_API int dit_block_forward_fp4(const dit_dims* dims, const dit_block_wfp4* w, float* txt, int L, float* img, int N,
                                   const float* txt_cos, const float* txt_sin, const float* img_cos,
                                   const float* img_sin, const dit_mod* mod, void* ws, size_t ws_bytes,
