@@ -247,6 +247,8 @@ cudaError_t rotary_go(const RotArgs& a, dim3 grid, size_t smem, cudaStream_t st)
              : launch_pdl(rotary_kernel<T, VE, false>, grid, dim3(kRotThreads), smem, st, 1, a);
 }
 
+bool al4(const void* p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; }
+
 bool plan_ok(const dit_rotary_plan* p) {
   if (!p || p->pairs < 1 || p->pairs > DIT_ROTARY_MAX_PAIRS || p->axes < 1 || p->axes > DIT_ROTARY_MAX_AXES) return false;
   if (p->layout != DIT_ROTARY_PAIRS && p->layout != DIT_ROTARY_HALVES) return false;
@@ -316,7 +318,7 @@ int dit_rotary_tables(const dit_rotary_plan* plan, const int32_t* pos, int rows,
                       dit_stream_t stream) {
   if (!plan_ok(plan) || rows < 0) return DIT_EINVAL;
   if (rows == 0) return DIT_OK;
-  if (!pos || !cos || !sin) return DIT_EINVAL;
+  if (!pos || !cos || !sin || !al4(pos) || !al4(cos) || !al4(sin)) return DIT_EINVAL;
   const long long n = (long long)rows * plan->pairs;
   if (launch_pdl(rotary_tables_kernel, dim3(unsigned((n + kRotThreads - 1) / kRotThreads)), dim3(kRotThreads), 0,
                  reinterpret_cast<cudaStream_t>(stream), 1, *plan, pos, n, cos, sin) != cudaSuccess)
@@ -335,7 +337,7 @@ int dit_rotary(const dit_rotary_plan* plan, const dit_rotary_rows* q, const dit_
     if (r && r->heads < 0) return DIT_EINVAL;
     else if (r && r->heads > 1 << 20) return DIT_EUNSUPPORTED;
   if (batch == 0 || rows == 0) return DIT_OK;
-  if (!pos) return DIT_EINVAL;
+  if (!pos || !al4(pos)) return DIT_EINVAL;
   // one tensor as q and k, written by one of them at least: which of the two is read first would be chance
   if (k && q->heads > 0 && k->heads > 0 && (q->out == k->out || q->out == k->x || k->out == q->x)) return DIT_EINVAL;
   RotArgs a;

@@ -43,3 +43,13 @@ def test_bf16_block_tables(name):
                                      r(mod), 4096, 1 << 30, None) == D.DIT_EINVAL
     assert D.lib().dit_block_forward_noalloc(r(dims), r(w), 4096, 4, 4096, 5, p["txt_cos"], p["txt_sin"], p["img_cos"],
                                              p["img_sin"], r(mod), None) == D.DIT_EINVAL
+
+
+def test_rotary_positions_and_tables():
+    p, r, at = D.RotaryPlan([64], layout="halves"), ctypes.byref, ctypes.c_void_p
+    q = D.dit_rotary_rows(4096, 4096, 4, 0, 256, 64, 0, 256, 64)
+    for off in (1, 2, 3):
+        assert D.lib().dit_rotary(r(p.c), r(q), None, 0, 1, 3, 64, at(4096 + off), 0, None) == D.DIT_EINVAL
+        for bad in range(3):
+            pos, cos, sin = (at(4096 + (off if i == bad else 0)) for i in range(3))
+            assert D.lib().dit_rotary_tables(r(p.c), pos, 3, cos, sin, None) == D.DIT_EINVAL
