@@ -336,7 +336,7 @@ int dit_rotary(const dit_rotary_plan* plan, const dit_rotary_rows* q, const dit_
   for (const dit_rotary_rows* r : part)
     if (r && r->heads < 0) return DIT_EINVAL;
     else if (r && r->heads > 1 << 20) return DIT_EUNSUPPORTED;
-  if (batch == 0 || rows == 0) return DIT_OK;
+  if (batch == 0 || rows == 0 || (q->heads == 0 && (!k || k->heads == 0))) return DIT_OK;
   if (!pos || !al4(pos)) return DIT_EINVAL;
   // one tensor as q and k, written by one of them at least: which of the two is read first would be chance
   if (k && q->heads > 0 && k->heads > 0 && (q->out == k->out || q->out == k->x || k->out == q->x)) return DIT_EINVAL;
@@ -371,7 +371,6 @@ int dit_rotary(const dit_rotary_plan* plan, const dit_rotary_rows* q, const dit_
     vec = vec && on16(r->x, batch > 1 ? r->x_batch : 0, rows > 1 ? r->x_row : 0, r->heads > 1 ? r->x_head : 0) &&
           on16(r->out, batch > 1 ? r->out_batch : 0, rows > 1 ? r->out_row : 0, r->heads > 1 ? r->out_head : 0);
   }
-  if (a.heads == 0) return DIT_OK;
   // batch entries that follow one another in every tensor are rows of one entry
   auto joined = [&](const dit_rotary_rows* r) {
     return !r || r->heads == 0 || (r->x_batch == rows * r->x_row && r->out_batch == rows * r->out_row);

@@ -469,7 +469,7 @@ typedef struct {
  * the transpose of the forward map, which takes the gradient of its output to that of its input.
  * type: DIT_BF16 or DIT_F32. head_dim at most 2 * DIT_ROTARY_MAX_PAIRS, at least the rotated part. Rows,
  * heads and tensors on 16-byte boundaries run with 16-byte accesses; any other alignment is served too.
- * batch, rows or heads of 0: nothing to do. */
+ * batch, rows or heads of 0: nothing to do (pos may then be NULL). DIT_EUNSUPPORTED for more than 2^20 heads. */
 #define DIT_BF16 0
 #define DIT_F32 1
 DIT_API int dit_rotary(const dit_rotary_plan* plan, const dit_rotary_rows* q, const dit_rotary_rows* k, int type,

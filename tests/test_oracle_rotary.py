@@ -181,3 +181,13 @@ def test_by_parts_of_two_pairs_by_hand():
     # width 4: at(1) = 4 ln(4096 / 2 pi) / (2 ln 10^4) = 1.41, so the ramp runs from pair 0 to 2 and pair 1 is half way
     f, _, _ = O.rotary_frequencies([4], scaling="yarn", factor=16.0, original=4096)
     assert np.allclose(f, [1.0, 0.01 * (0.5 + 0.5 / 16)], rtol=1e-15)
+
+
+def test_rotary_without_heads_looks_at_nothing():
+    import ctypes
+    p, r = D.RotaryPlan([64], layout="halves"), ctypes.byref
+    none = D.dit_rotary_rows(None, None, 0, 0, 0, 0, 0, 0, 0)
+    assert D.lib().dit_rotary(r(p.c), r(none), None, 0, 2, 3, 64, None, 0, None) == D.DIT_OK
+    assert D.lib().dit_rotary(r(p.c), r(none), r(none), 0, 2, 3, 64, None, 0, None) == D.DIT_OK
+    some = D.dit_rotary_rows(256, 256, 4, 0, 256, 64, 0, 256, 64)
+    assert D.lib().dit_rotary(r(p.c), r(none), r(some), 0, 1, 3, 64, None, 0, None) == D.DIT_EINVAL
