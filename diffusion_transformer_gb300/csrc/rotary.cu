@@ -4,10 +4,11 @@
 // frequencies rescaled for sequences longer than the trained ones.
 //
 // Mathematics. Pair i of a head belongs to position axis a(i) and turns by p_a f_i radians; with
-// u_i = f_i / 2 pi (turns per position, below 1) as a 64-bit binary fraction U_i = rint(2^64 u_i), the
-// angle modulo one turn is the low 64 bits of p U_i: one integer product, exact for every 32-bit
-// position of either sign, so far positions lose nothing (|error| <= |p| 2^-65 turns: 2^-34 at the
-// last 32-bit position). The nearest quarter turn is taken off in integers before the conversion to
+// u_i = f_i / 2 pi (turns per position, below 1) as a 64-bit binary fraction U_i, the angle modulo one turn is
+// the low 64 bits of p U_i: one integer product, exact for every 32-bit position of either sign. U_i itself comes of
+// 64-bit floating point (a power and a quotient, then rounded at 2^-62): off by less than 2^-54 turns, most by
+// 2^-56, so an angle is off by |p| 2^-54 turns: 2^-30 at 2^24 positions, below what fp32 keeps of it, and 2^-23 at the
+// last 32-bit position. The nearest quarter turn is taken off in integers before the conversion to
 // fp32, so the residual, at most an eighth of a turn, carries 24 bits (2^-28 turns) into sincospif.
 //
 // What bounds it: HBM. Each value is read once and written once; a row's cosines and sines are

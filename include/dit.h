@@ -442,8 +442,9 @@ typedef struct {
 DIT_API int dit_rotary_plan_init(const dit_rotary_spec* spec, dit_rotary_plan* plan);
 
 /* Rotary tables from positions: pos [rows, axes] int32 (any value, negative ones too) -> cos, sin
- * [rows, pairs] fp32, the angle reduced modulo one turn in integers before it is rounded, so far
- * positions are as exact as near ones. With widths (16, 56, 56) or (8, 28, 28) and DIT_ROTARY_PAIRS
+ * [rows, pairs] fp32, the angle reduced modulo one turn in integers before it is rounded: positions up to
+ * 2^24 are as exact as near ones, and the last 32-bit position is off by at most 2^-23 turns (the frequencies are
+ * those of 64-bit arithmetic, within 2^-54 turns per position). With widths (16, 56, 56) or (8, 28, 28) and DIT_ROTARY_PAIRS
  * these are tables for every block form here (rows of the text, then of the image), with any of the
  * scalings above; with one axis of 3d/4 and DIT_ROTARY_HALVES, for rope_split blocks. */
 DIT_API int dit_rotary_tables(const dit_rotary_plan* plan, const int32_t* pos, int rows, float* cos, float* sin,

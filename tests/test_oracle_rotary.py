@@ -191,3 +191,34 @@ def test_rotary_without_heads_looks_at_nothing():
     assert D.lib().dit_rotary(r(p.c), r(none), r(none), 0, 2, 3, 64, None, 0, None) == D.DIT_OK
     some = D.dit_rotary_rows(256, 256, 4, 0, 256, 64, 0, 256, 64)
     assert D.lib().dit_rotary(r(p.c), r(none), r(some), 0, 1, 3, 64, None, 0, None) == D.DIT_EINVAL
+
+
+@pytest.mark.parametrize("spec", SPECS + [
+    dict(widths=[4], theta=100.0), dict(widths=[256], theta=100.0), dict(widths=[64], theta=2.5e8, scaling="ntk", factor=2.0),
+    dict(widths=[256], theta=100.0, scaling="yarn", factor=40.0, original=64),
+    dict(widths=[256], theta=100.0, scaling="linear", factor=1.5)])
+def test_fractions_against_sixty_digits(spec):
+    # the plan's turns per position are off by less than 2^-54: the stated bound (64-bit floating point takes them, so
+    # 2^-65, the last bit of the fraction, is out of reach)
+    from decimal import Decimal, getcontext
+    getcontext().prec = 60
+    two_pi = 2 * Decimal("3.14159265358979323846264338327950288419716939937510582097494459")
+    theta, scaling = Decimal(spec.get("theta", 10000.0)), spec.get("scaling", "none")
+    factor, turns = Decimal(spec.get("factor", 1.0)), []
+    for w in spec["widths"]:
+        base = theta * (factor.ln() * w / (w - 2)).exp() if scaling == "ntk" else theta
+        lo, hi = (w * (spec["original"] / (n * two_pi)).ln() / (2 * theta.ln()) if scaling == "yarn" else Decimal(0)
+                  for n in (32, 1))
+        lo, hi = max(0, math.floor(lo)), min(w - 1, math.ceil(hi))
+        for k in range(w // 2):
+            f = (base.ln() * -2 * k / w).exp()
+            if scaling == "linear":
+                f /= factor
+            elif scaling == "yarn":
+                r = min(Decimal(1), max(Decimal(0), Decimal(k - lo) / max(Decimal(hi - lo), Decimal("0.001"))))
+                f = f * (1 - r) + f / factor * r
+            turns.append(f / two_pi)
+    plan = D.RotaryPlan(**spec)
+    assert plan.c.pairs == len(turns)
+    off = max(abs(Decimal(plan.c.turns[i]) / 2 ** 64 - t) for i, t in enumerate(turns))
+    assert off < Decimal(2) ** -54, float(off)
