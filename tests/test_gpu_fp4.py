@@ -457,3 +457,51 @@ CLUSTER_SIZES = [(1, 77, 6659), (16, 1024, 14000), (1, 1000, 14000), (3, 2048, 1
 @pytest.mark.parametrize("M,N,K", CLUSTER_SIZES)
 def test_matmul_of_few_rows_on_clusters(fmt, M, N, K):
     test_matmul(fmt, M, N, K)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 1000, 256), (100, 300, 5003), (1100, 1500, 777)])
+def test_power_of_two_blocks_of_any_size_multiply(M, N, K):
+    # blocks of 2^90 against blocks of 2^-110: scales meet inside the product, as exact as any others. (Sums below 2^-90
+    # are left out: terms there may be subnormal.)
+    g = np.random.default_rng(M + K)
+    x, w = (_as_bf16(g.standard_normal((n, K))) for n in (M, N))
+    x, w = ((v * 2.0 ** g.integers(lo, hi, (v.shape[0], 1))).astype(np.float32) for v, lo, hi in ((x, 0, 90), (w, -110, 0)))
+    a, av = _quantised(x, MX)
+    b, bv = _quantised(w, MX)
+    o = torch.empty(M, N, device="cuda")
+    D.dit_fp4_matmul(a, b, o)
+    D.dit_check()
+    ref, S = av @ bv.T, np.abs(av) @ np.abs(bv).T
+    seen = S > 2.0 ** -90
+    assert seen.mean() > 0.7
+    assert (np.abs(o.cpu().numpy() - ref) <= (K / 64 + 2) * 2.0 ** -23 * S)[seen].all()
+
+
+@FMT
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("R,K,pad", [(40, 64, 0), (40, 5003, 1), (700, 40, 0), (700, 64, 1), (700, 200, 0), (700, 250, 1),
+                                     (700, 900, 0), (700, 1999, 1), (700, 2900, 0), (613, 4000, 0), (613, 4096, 1)])
+def test_quantize_of_non_finite_rows_by_every_kernel(fmt, dtype, R, K, pad):
+    # infinities and NaN of either sign and of both kinds, the largest and the smallest values, zeros of either sign: in the
+    # kernel with a CTA per row (40 rows) and those with 8, 16 or 32 lanes per row and 1 to 8 units per lane
+    g = np.random.default_rng(R + K + pad)
+    x = _rows(g, R, K).astype(np.float32)
+    odd = np.array([0x7f800000, 0xff800000, 0x7fc00000, 0xffc00000, 0x7f810000, 0xff810000, 0x7fff0000], np.uint32)
+    odd = np.concatenate([odd, np.array([0x7f7f0000, 0xff7f0000, 0x00010000, 0x80000000, 0x00800000], np.uint32)])
+    at = g.permutation(R)[:3 * len(odd)]
+    for i, r in enumerate(at):
+        x.view(np.uint32)[r, (0, K - 1, int(g.integers(K)))[i // len(odd)]] = odd[i % len(odd)]
+    x[g.permutation(R)[:3]] = np.array([0.0, -0.0, 2.0 ** -126], np.float32)[:, None]
+    mem = torch.full((R, K + pad), 77.0, dtype=dtype, device="cuda")
+    bits = np.ascontiguousarray(x).view(np.uint32)
+    mem[:, :K] = dev((bits >> 16).astype(np.uint16).view(np.int16)).view(torch.bfloat16) if dtype == torch.bfloat16 \
+        else dev(bits.view(np.int32)).view(torch.float32)
+    m, out = D.Fp4Matrix.empty(fmt, R, K), torch.empty(R, K, device="cuda")
+    m.codes.fill_(255)
+    m.scales.fill_(254)
+    D.dit_fp4_quantize(mem[:, :K], m)
+    codes, scale, row = _check_quantised(m, x, fmt)
+    assert (~np.isfinite(row)).sum() >= 15 if fmt == NV else (scale == 255).sum() >= 15
+    D.dit_fp4_dequantize(m, out)
+    D.dit_check()
+    assert np.array_equal(out.cpu().numpy(), O.fp4_values(codes, scale, row, fmt, K), equal_nan=True)

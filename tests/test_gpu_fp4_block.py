@@ -335,3 +335,31 @@ def test_block_refusals():
         call(good, ws[:-256])
     assert e.value.status == -3
     assert D.dit_block_fp4_workspace_bytes(dims, 2, 0, 5) == 0 and D.dit_block_fp4_workspace_bytes(dims, NV, 0, 0) == 0
+
+
+@FMT
+@pytest.mark.parametrize("heads,part", [(h, p) for h in (2, 4) for p in range(8)])
+def test_every_part_of_a_head_shows(fmt, heads, part, monkeypatch):
+    # As test_block_with_norm_weights_and_split_halves (both rotary layouts), with head-norm weights of zero but for an
+    # eighth of the head's columns and without the MLP, so that a wrong weight, angle or place in any of the columns
+    # changes the scores by about their own size. Both sides share the attention and differ by fp32 rounding ahead of it:
+    # 2^-22 of q and k, which moves 2^-13 of their bf16 values by 2^-8, a score by less than 2^-13, and the attention's
+    # output, rounded to bf16, by about 2^-12 of itself. Codes are a quarter apart: sqrt(2^-12) / 2 = 0.008 of the out
+    # linear, and 0.005 for the block scales that turn over (9 2^-12 of them, by a tenth). Gate: three times their root sum.
+    import sys
+    here = sys.modules[__name__]
+    small, check = here._small, here._check
+
+    def weights(*a):
+        dims, mats, nw, x, rows, mp, ang = small(*a)
+        n = len(nw[2]) // 8
+        for w in nw[2:]:
+            keep = w[part * n:(part + 1) * n] * 8 ** 0.5
+            w.zero_()
+            w[part * n:(part + 1) * n] = keep
+        rows[:, 5] = 0
+        return dims, mats, nw, x, rows, mp, ang
+
+    monkeypatch.setattr(here, "_small", weights)
+    monkeypatch.setattr(here, "_check", lambda got, ref, x, _, top, label: check(got, ref, x, 3e-2, top, label))
+    test_block_with_norm_weights_and_split_halves(fmt, heads)
