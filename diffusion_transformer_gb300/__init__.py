@@ -869,7 +869,11 @@ class Fp4BlockWeights:
     def __init__(self, w: Sequence[Fp4Matrix], norm1=None, norm2=None, q_norm=None, k_norm=None):
         f32 = _torch().float32
         self.w, self.tensors = tuple(w), (norm1, norm2, q_norm, k_norm)
-        self.format = self.w[0].format
+        if len(self.w) != 4:
+            raise ValueError("w: expected four matrices")
+        self.format, self.device = self.w[0].format, self.w[0].device
+        if any(m.device != self.device for m in self.w):
+            raise ValueError("w: expected matrices on one device")
         self.c = dit_block_wfp4((dit_fp4_matrix * 4)(*[m.c for m in self.w]), _ptr(norm1, f32, "norm1"),
                                 _ptr(norm2, f32, "norm2"), _ptr(q_norm, f32, "q_norm"), _ptr(k_norm, f32, "k_norm"))
 
@@ -882,7 +886,20 @@ def dit_block_fp4_workspace_bytes(dims: DitDims, format: int, L: int, N: int) ->
 def dit_block_forward_fp4(dims: DitDims, w: Fp4BlockWeights, txt, img, txt_cos, txt_sin, img_cos, img_sin,
                           mod: Modulation, ws, stream=None):
     f32 = _torch().float32
-    L = 0 if txt is None else txt.shape[0]
+    dev, _ = _current(stream)
+    L, N, H, d = 0 if txt is None else txt.shape[0], img.shape[0], dims.hidden, dims.head_dim
+    if w.device != dev:
+        raise ValueError("w: expected weights on the current device")
+    for name, t, n in (("img", img, N * H), ("txt", txt, L * H)):
+        if t is not None and t.numel() != n:
+            raise ValueError(f"{name}: expected rows of {H} values")
+    angles = 3 * d // 8 if dims.rope_split else d // 2
+    least = dict(img=N * H, txt=L * H, txt_cos=L * angles, txt_sin=L * angles, img_cos=N * angles, img_sin=N * angles, ws=0,
+                 norm1=H, norm2=H, q_norm=d, k_norm=d, mod_rows=6 * H * mod.c.M, mod_map=L + N)
+    given = (img, txt, txt_cos, txt_sin, img_cos, img_sin, ws, *w.tensors, *mod.tensors)
+    for (name, n), t in zip(least.items(), given):
+        if t is not None and (t.get_device() != dev or t.numel() < n):
+            raise ValueError(f"{name}: expected {n} values on the current device")
     _ok(lib().dit_block_forward_fp4(byref(dims.c), byref(w.c), _ptr(txt, f32, "txt"), L, _ptr(img, f32, "img"),
                                     img.shape[0], _ptr(txt_cos, f32), _ptr(txt_sin, f32), _ptr(img_cos, f32),
                                     _ptr(img_sin, f32), byref(mod.c), _ptr(ws, None, "ws"),
