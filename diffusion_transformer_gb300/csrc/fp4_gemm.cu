@@ -92,26 +92,19 @@ __device__ __forceinline__ void scale4(uint32_t* x, uint64_t row2, const float4&
   x[2] = uint32_t(hi);
   x[3] = uint32_t(hi >> 32);
 }
-// Row factors that may be multiplied first whatever the other factor is. An accumulator that is not zero lies
-// between 2^-20 (the smallest codes and scales) and 2^53 (2688^2 times the longest K), so its product with a factor
-// between 2^-100 and 2^64 is neither infinite nor subnormal; a NaN is left to scale_far.
-__device__ __forceinline__ bool near_factor(float f) { return f == 0.f || (f >= 0x1p-100f && f <= 0x1p64f); }
-// x times two row factors of any size, finite wherever the result is: the larger one first, and where that one is past
-// 2^64 and the other below 1, 2^64 is taken from the one and given to the other, which is exact.
-__device__ __forceinline__ float scale_far(float x, float a, float b) {
-  float hi = a > b ? a : b, lo = a > b ? b : a;  // each of them once, so that a NaN stays
-  if (hi > 0x1p64f && lo < 1.f) {
-    hi *= 0x1p-64f;
-    lo *= 0x1p64f;
-  }
-  return x * hi * lo;
+// Row factors of any size, so that a product is finite wherever its value is. An accumulator that is not zero lies
+// between 2^-20 (the smallest codes and scales) and 2^53 (2688^2 times the longest K), a factor between 2^-112 and
+// 2^117. The first factor as it is between 2^-100 and 2^64 makes neither an infinity nor a subnormal of any
+// accumulator; a larger one is taken by 2^44 smaller, a smaller one by 2^44 larger, which is exact and keeps the
+// products with the second factor in range too (past 2^128 the value itself is), and the result is put back after.
+__device__ __forceinline__ float factor_back(float f) { return f > 0x1p64f ? 0x1p44f : (f > 0.f && f < 0x1p-100f ? 0x1p-44f : 1.f); }
+__device__ __forceinline__ float factor_first(float f) {
+  return f > 0x1p64f ? f * 0x1p-44f : (f > 0.f && f < 0x1p-100f ? f * 0x1p44f : f);
 }
-// N neighbouring products of one row by the row's factor and their columns', in any order of size. The column
-// factors are read one by one, so that this rare way holds no registers that the usual one would spill.
 template <int N>
-__device__ __forceinline__ void scale_row_far(uint32_t* x, float row, const volatile float* cols) {
+__device__ __forceinline__ void put_back(uint32_t* x, float back) {
 #pragma unroll
-  for (int c = 0; c < N; ++c) x[c] = __float_as_uint(scale_far(__uint_as_float(x[c]), row, cols[c]));
+  for (int c = 0; c < N; ++c) x[c] = __float_as_uint(__uint_as_float(x[c]) * back);
 }
 
 // z / (1 + e^-z); the approximate division is within two units of the fp32 result, which goes on to bf16
@@ -416,13 +409,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       mbar_arrive_cluster(tempty0 + uint32_t(acc) * 8u);
       if (row0 >= rowsP) continue;
       if constexpr (SC::kNv) {
-        if (__all_sync(0xffffffffu, near_factor(rp))) {
-          const uint64_t rp2 = f2_pack(rp, rp);
+        const float first = factor_first(rp), back = factor_back(rp);
+        const uint64_t rp2 = f2_pack(first, first);
 #pragma unroll
-          for (int c = 0; c < 128; c += 4) scale4(w[c >> 5] + (c & 31), rp2, *reinterpret_cast<const float4*>(cf + c));
-        } else {
-          scale_row_far<128>(w[0], rp, cf);
-        }
+        for (int c = 0; c < 128; c += 4) scale4(w[c >> 5] + (c & 31), rp2, *reinterpret_cast<const float4*>(cf + c));
+        if (__any_sync(0xffffffffu, back != 1.f)) put_back<128>(w[0], back);
       }
       if (ep.head_dim == 128) {
         qkv_store<128>(ep, w[0], row0, lane, n0, scratch);
@@ -486,16 +477,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         if (q0 >= rowsQ || row0 >= rowsP) continue;
         if constexpr (SC::kNv) {
-          if (__all_sync(0xffffffffu, near_factor(rp))) {
-            const uint64_t rp2 = f2_pack(rp, rp);
+          const float first = factor_first(rp), back = factor_back(rp);
+          const uint64_t rp2 = f2_pack(first, first);
 #pragma unroll
-            for (int c = 0; c < 64; c += 4) {
-              const float4 f = *reinterpret_cast<const float4*>(cf + c);
-              scale4(w[c >> 5] + (c & 31), rp2, f);
-            }
-          } else {
-            scale_row_far<64>(w[0], rp, cf);
+          for (int c = 0; c < 64; c += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(cf + c);
+            scale4(w[c >> 5] + (c & 31), rp2, f);
           }
+          if (__any_sync(0xffffffffu, back != 1.f)) put_back<64>(w[0], back);
         }
         auto val = [&](int c) { return __uint_as_float(w[c >> 5][c & 31]); };
         if constexpr (SWAP) {
@@ -649,7 +638,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
   pdl_trigger();
-  bool near = true;  // the tile's A factors may be multiplied first
+  bool far = false;  // one of the tile's A factors goes first as another (factor_first)
 
   if (warp == 0) {
     if (elect_one()) {
@@ -707,8 +696,8 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
     if constexpr (SC::kNv) {
       const int i = int(threadIdx.x) - 64;
       const float ra = i < bn && m0 + i < p.M ? __ldg(p.a_scale + m0 + i) : 0.f;
-      near = near_factor(ra);
-      sFa[i] = ra;
+      far = factor_back(ra) != 1.f;
+      sFa[i] = factor_first(ra);
       sFb[i] = n0 + i < p.N ? __ldg(p.b_scale + n0 + i) : 0.f;
     }
     (void)mbar_wait_warp(smem_u32(tfull), 0, p.err, kErrTimeoutEpilogue);
@@ -722,10 +711,11 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
   const int n = n0 + quad * 32 + lane;
   T* out = static_cast<T*>(p.out);
   float* tile = reinterpret_cast<float*>(sB);
-  near = __syncthreads_and(near);
+  if constexpr (SC::kNv) far = __syncthreads_or(far);
+  else __syncthreads();
   tc_fence_after();
   const int live = min(bn, p.M - m0);
-  if (warp >= 2) {
+  auto drain = [&](auto back) {  // back: A factors that were taken smaller or larger are put back (a loop of its own)
     const float rb = SC::kNv ? sFb[quad * 32 + lane] : 1.f;
     T* o = out + (long long)m0 * p.ldo + n;
     for (int c = 0; c < live; c += 16, o += 16 * p.ldo) {
@@ -746,7 +736,10 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const float x = __uint_as_float(w[e + k]);
-          v[e + k] = T(!SC::kNv ? x : (near ? x * ff[k] * rb : scale_far(x, ff[k], rb)));
+          float y = SC::kNv ? x * ff[k] * rb : x;
+          if constexpr (back.value)
+            if (c + e + k < live) y *= factor_back(__ldg(p.a_scale + m0 + c + e + k));
+          v[e + k] = T(y);
         }
       }
       if (n < p.N) {
@@ -755,6 +748,10 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
           if (c + e < live) o[e * p.ldo] = v[e];
       }
     }
+  };
+  if (warp >= 2) {
+    if (SC::kNv && far) drain(std::true_type{});
+    else drain(std::false_type{});
   }
   if (parts > 1) {
     cluster_barrier();
@@ -788,8 +785,11 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
         if constexpr (SC::kNv) {
           const float ra = sFa[c];
           const float4 f = *reinterpret_cast<const float4*>(sFb + r4);
-          s = near ? make_float4(s.x * ra * f.x, s.y * ra * f.y, s.z * ra * f.z, s.w * ra * f.w)
-                   : make_float4(scale_far(s.x, ra, f.x), scale_far(s.y, ra, f.y), scale_far(s.z, ra, f.z), scale_far(s.w, ra, f.w));
+          s = make_float4(s.x * ra * f.x, s.y * ra * f.y, s.z * ra * f.z, s.w * ra * f.w);
+          if (far) {
+            const float back = factor_back(__ldg(p.a_scale + m0 + c));
+            s = make_float4(s.x * back, s.y * back, s.z * back, s.w * back);
+          }
         }
         T* o = out + (long long)(m0 + c) * p.ldo + n0 + r4;
         if (whole) {
