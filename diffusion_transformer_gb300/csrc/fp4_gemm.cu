@@ -11,12 +11,14 @@
 //   split  128 rows of B against up to 128 rows of A per CTA, a cluster of CTAs sharing the K loop and
 //          adding their partial tiles through distributed shared memory, for few rows or few tiles
 //
-// What bounds the pair kernel. A stage of a 256 x 256 tile takes each SM 512 cycles of MMA, and 38 KB of
-// operands and scales into shared memory and out of it again to the tensor core: 120 of the 128 bytes per
-// cycle that shared memory moves. Measured per stage at 2070 MHz, 4096 x 24320 x 3072: 247 ns of MMA, 327
-// ns without an epilogue, 348 with all of it but the stores, 394 in all (94.5 us; 32-value blocks, with half
-// the scales and no factors: 87); 4096 x 4864 x 12288: 330 ns. So the output's way through the same data path
-// counts: 32-byte stores from registers 94.5 us, staged in shared memory and stored by TMA 104, lanes
+// What bounds the pair kernel. A stage of a 256 x 256 tile takes each SM 512 cycles of MMA (247 ns at 2070 MHz).
+// Measured per stage, 4096 x 24320 x 3072: 327 ns without an epilogue, 348 with all of it but the stores, 394
+// in all (94.5 us; 32-value blocks, with half the scales and no factors: 87); 4096 x 4864 x 12288: 330 ns. What the 80
+// ns over the MMA's own time are is not shown. A stage's 38 KB go into shared memory and out of it again: 152
+// bytes per cycle at the MMA's pace, 115 at the measured one, where it moves 128; but tiles of 128 and 192 rows,
+// with 31 and 35 KB and 124 and 185 ns of MMA, take 215 and 250 ns, about the same 65 to 90 more, so a wait in each
+// stage (its scale copies for the MMAs before them, its MMAs for the copies) may be the cause as well. The output
+// counts beside it: 32-byte stores from registers 94.5 us, staged in shared memory and stored by TMA 104, lanes
 // exchanging pieces to store whole 128-byte lines 99.8, evict-first hints 96, four epilogue warps in place
 // of eight 93 (104 when staged). 4224 x 24576 x 3072 with data that toggles bits: 104 us (6.1 PFLOP/s, tensor
 // pipe 72 % active) in a burst, 112 to 123 back to back, where the power limit lowers the clock; 8192^3:
@@ -107,7 +109,8 @@ __device__ __forceinline__ void put_back(uint32_t* x, float back) {
   for (int c = 0; c < N; ++c) x[c] = __float_as_uint(__uint_as_float(x[c]) * back);
 }
 
-// z / (1 + e^-z); the approximate division is within two units of the fp32 result, which goes on to bf16
+// z / (1 + e^-z); the approximate division is within two units of the fp32 result, which goes on to bf16 (for z from
+// -88.7 to -87.3, where 1 + e^-z passes 2^126, it gives 0 in place of -5e-37 at most)
 __device__ __forceinline__ float silu_bf16(float z) { return __fdividef(z, 1.f + __expf(-z)); }
 
 // The QKV epilogue's part of one warp (the gizai:dit reference's prepOf; klein article, section 4.4): 128
@@ -115,6 +118,9 @@ __device__ __forceinline__ float silu_bf16(float z) { return __fdividef(z, 1.f +
 // Query and key heads are RMS-normed, weighted, rotated by the row's tables and stored head-major; value
 // heads are transposed through the warp's 4 KB of shared memory (chunks of 32 columns: 64 bytes per row,
 // 16-byte pieces swizzled by (row >> 1) & 3), so that a lane stores 32 rows of one value as 64 bytes.
+// 128 columns in registers are more than the 168 that ten warps leave a thread: 88 bytes of them spill (16-value
+// blocks; 144 for 32-value ones), and a lane per row makes a warp's access 32 pieces of 32 bytes in 32 lines. Both hold
+// the QKV linear of 4224 x 9216 x 3072 at 83 us (78 for 32-value blocks), where its operations take 31.
 template <int D>
 __device__ __forceinline__ void qkv_store(const GemmParams& g, const uint32_t* w, int row0, int lane, int n0,
                                           uint8_t* scratch) {
@@ -515,7 +521,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             }
           }
         } else if constexpr (EPI == kEpiGated) {
-          // x[p][q] += gate[map[p]][q] * product (the gizai:dit reference's gatedInto)
+          // x[p][q] += gate[map[p]][q] * product (the gizai:dit reference's gatedInto). A lane per row: 32 pieces
+          // of 32 bytes in 32 lines per access, which hold 4224 x 3072 x 3072 at 39 us (15 by its bytes)
           if (row < rowsP) {
             float* x = (row < ep.L ? ep.txt + (long long)row * ep.N : ep.img + (long long)(row - ep.L) * ep.N) + q0;
             const float* gate = ep.gate + (ep.map ? __ldg(ep.map + row) : 0) * ep.gate_stride + q0;

@@ -452,8 +452,9 @@ DIT_API int dit_rotary_tables(const dit_rotary_plan* plan, const int32_t* pos, i
 
 /* The heads of one tensor: value j of head h of row t of batch entry b is at
  * x[b * x_batch + t * x_row + h * x_head + j] (strides in values), likewise for out. out may be x with
- * the same strides (in place; refused with others); otherwise the two must not overlap. Nor may q's output
- * and k's, or either's output and the other's input (equal pointers are refused). */
+ * the same strides (in place; refused with others); otherwise the two must not overlap, nor may q's output and k's,
+ * or either's output and the other's input (equal pointers are refused). No two values of an output may share a
+ * place (a stride of 0 over more than one row, head or batch entry is refused). */
 typedef struct {
   const void* x;
   void* out;
@@ -517,7 +518,7 @@ DIT_API int dit_fp4_matmul(const dit_fp4_matrix* a, const dit_fp4_matrix* b, voi
 
 /* One 4-bit linear: out [M, w->rows] = fp4(x) w^T, x [M, w->cols] bf16 or fp32 (row stride ldx) quantised
  * per call into the workspace in w's format. x is not modified. Workspace:
- * dit_linear_fp4_workspace_bytes(format, M, N, K), 256-byte aligned. M = 0: nothing to do. */
+ * dit_linear_fp4_workspace_bytes(format, M, N, K), 256-byte aligned (N is not used at present). M = 0: nothing to do. */
 DIT_API int dit_linear_fp4(const void* x, int x_type, int M, long long ldx, const dit_fp4_matrix* w, void* out,
                            int out_type, long long ldo, void* ws, size_t ws_bytes, dit_stream_t stream);
 DIT_API size_t dit_linear_fp4_workspace_bytes(int format, int M, int N, int K);
