@@ -328,9 +328,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           if (++stage == S) { stage = 0; phase ^= 1; }
         }
       }
-      if (rank == 0)  // every copy has landed before the CTAs leave
+      // Every copy has landed before the CTAs leave: the first CTA's barriers count both CTAs' copies, but not those
+      // that one of them issued after the other gave up
+      if (aborted(p.err)) outlast_copies();
+      else if (rank == 0)
         for (int s = 0; s < S; ++s)
-          if (issued & (1u << s)) mbar_wait(smem_u32(&full[s]), (parity >> s) & 1u, p.err, kErrTimeoutDrain);
+          if (issued & (1u << s)) mbar_drain(smem_u32(&full[s]), (parity >> s) & 1u, p.err);
     }
   } else if (warp == 1) {
     if (rank == 0 && elect_one()) {
@@ -381,7 +384,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         umma_commit_pair_both(smem_u32(&tfull[it & 1]));
       }
       umma_commit_pair(smem_u32(drain));
-      mbar_wait(smem_u32(drain), 0, p.err, kErrTimeoutDrain);
+      mbar_drain(smem_u32(drain), 0, p.err);
     }
   } else if constexpr (EPI == kEpiQKV) {
     // two warps to each quadrant of 32 lanes, 128 columns each, all of them in registers at once: the
@@ -664,7 +667,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
         if (++stage == S) { stage = 0; phase ^= 1; }
       }
       for (int s = 0; s < S; ++s)  // every copy has landed before the CTA leaves
-        if (issued & (1u << s)) mbar_wait(smem_u32(&full[s]), (parity >> s) & 1u, p.err, kErrTimeoutDrain);
+        if (issued & (1u << s)) mbar_drain(smem_u32(&full[s]), (parity >> s) & 1u, p.err);
     }
   } else if (warp == 1) {
     if (elect_one()) {
@@ -697,7 +700,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
         if (++stage == S) { stage = 0; phase ^= 1; }
       }
       umma_commit(smem_u32(tfull));
-      mbar_wait(smem_u32(tfull), 0, p.err, kErrTimeoutDrain);
+      mbar_drain(smem_u32(tfull), 0, p.err);
     }
   } else {
     if constexpr (SC::kNv) {

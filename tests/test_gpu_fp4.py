@@ -505,3 +505,28 @@ def test_quantize_of_non_finite_rows_by_every_kernel(fmt, dtype, R, K, pad):
     D.dit_fp4_dequantize(m, out)
     D.dit_check()
     assert np.array_equal(out.cpu().numpy(), O.fp4_values(codes, scale, row, fmt, K), equal_nan=True)
+
+
+def test_products_under_a_set_error_word():
+    # after a wait that gave up (the library's own diagnostic sets the word) a product may stop short, but what it has in
+    # flight is waited for; the word is reported, and from then on products are right again
+    g = np.random.default_rng(31)
+    jobs = []
+    for fmt, M, N, K in ((NV, 1300, 1536, 3000), (MX, 1037, 1500, 777), (NV, 3, 2048, 9000), (MX, 100, 3000, 3331), (NV, 333, 777, 1000)):
+        a, av = _quantised(_rows(g, M, K), fmt)
+        b, bv = _quantised(_rows(g, N, K), fmt)
+        jobs.append((a, b, torch.empty(M, N, device="cuda"), av, bv, K))
+    D.dit_check()
+    D.dit_selftest_bounded_wait(False)
+    for _ in range(4):
+        for a, b, out, *_ in jobs:
+            D.dit_fp4_matmul(a, b, out)
+    with pytest.raises(D.DitError) as e:
+        D.dit_check()
+    assert e.value.status == D.DIT_ETIMEOUT
+    D.dit_check()
+    for a, b, out, av, bv, K in jobs:
+        out.fill_(9)
+        D.dit_fp4_matmul(a, b, out)
+        D.dit_check()
+        _check_product(out, av, bv, K)
