@@ -27,6 +27,7 @@ __all__ = [
     "dit_double_block_forward_sandwich",
     "dit_block_forward_sandwich", "dit_euler_step",
     "dit_rope_tables", "RotaryPlan", "dit_rotary_plan_init", "dit_rotary_tables", "dit_rotary",
+    "dit_qknorm_rotary", "dit_qknorm_rotary_backward", "dit_qknorm_rotary_backward_workspace_bytes",
     "DIT_FP4_NV", "DIT_FP4_MX", "Fp4Matrix", "dit_fp4_code_bytes", "dit_fp4_scale_bytes", "dit_fp4_quantize",
     "dit_fp4_dequantize", "dit_fp4_matmul", "dit_linear_fp4", "dit_linear_fp4_workspace_bytes",
     "Fp4BlockWeights", "dit_block_forward_fp4", "dit_block_fp4_workspace_bytes",
@@ -106,6 +107,12 @@ class dit_rotary_rows(ctypes.Structure):
                 ("x_head", c_longlong), ("out_batch", c_longlong), ("out_row", c_longlong), ("out_head", c_longlong)]
 
 
+class dit_rotary_grad(ctypes.Structure):
+    _fields_ = [("x", c_void_p), ("dy", c_void_p), ("dx", c_void_p), ("heads", c_int), ("x_batch", c_longlong),
+                ("x_row", c_longlong), ("x_head", c_longlong), ("dy_batch", c_longlong), ("dy_row", c_longlong),
+                ("dy_head", c_longlong), ("dx_batch", c_longlong), ("dx_row", c_longlong), ("dx_head", c_longlong)]
+
+
 class dit_fp4_matrix(ctypes.Structure):
     _fields_ = [("format", c_int), ("rows", c_int), ("cols", c_int), ("codes", c_void_p), ("scales", c_void_p),
                 ("row_scale", c_void_p)]
@@ -125,6 +132,12 @@ _SIGNATURES = {
     "dit_rotary_tables": (c_int, [POINTER(dit_rotary_plan), c_void_p, c_int, c_void_p, c_void_p, c_void_p]),
     "dit_rotary": (c_int, [POINTER(dit_rotary_plan), c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_void_p, c_int,
                            c_void_p]),
+    "dit_qknorm_rotary": (c_int, [POINTER(dit_rotary_plan), c_void_p, c_void_p, c_void_p, c_void_p, c_float, c_int, c_int,
+                                  c_int, c_int, c_void_p, c_void_p]),
+    "dit_qknorm_rotary_backward": (c_int, [POINTER(dit_rotary_plan), c_void_p, c_void_p, c_void_p, c_void_p, c_float,
+                                           c_int, c_int, c_int, c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t,
+                                           c_void_p]),
+    "dit_qknorm_rotary_backward_workspace_bytes": (c_size_t, [c_int]),
     "dit_fp4_code_bytes": (c_size_t, [c_int, c_int]),
     "dit_fp4_scale_bytes": (c_size_t, [c_int, c_int, c_int]),
     "dit_fp4_quantize": (c_int, [c_void_p, c_int, c_longlong, POINTER(dit_fp4_matrix), c_void_p]),
@@ -757,6 +770,100 @@ def dit_rotary(plan: RotaryPlan, q, k, pos, q_out=None, k_out=None, inverse: boo
                           1 if inverse else 0, st)
     if rc:
         _ok(rc, "dit_rotary")
+
+
+def _head_weights(t, dim, dev, name):
+    """Pointer of fp32 [dim] weights (or of their gradient) on the current device; None -> NULL."""
+    if t is None:
+        return None
+    if getattr(t, "dtype", None) is not _torch_mod.float32:
+        raise TypeError(f"{name}: expected float32")
+    if t.get_device() != dev or not t.is_contiguous() or t.numel() != dim:
+        raise ValueError(f"{name}: expected {dim} dense values on the current device")
+    return t.data_ptr()
+
+
+def _same_rows(kind, shape, kk, sk):
+    if kk != kind or sk[:-2] != shape[:-2] or sk[-1] != shape[-1]:
+        raise ValueError("q and k: expected the same type, batch, rows and head_dim")
+
+
+def dit_qknorm_rotary(plan: RotaryPlan, q, k, pos, q_norm=None, k_norm=None, q_out=None, k_out=None, eps: float = 1e-6,
+                      stream=None):
+    """Norm the heads of q (and k, or None), times q_norm / k_norm [head_dim] fp32 (None: ones), and turn them, as
+    dit_rotary does; q_out / k_out default to in place."""
+    dev, st = _current(stream)
+    a, kind, shape = _rotary_rows(q, q if q_out is None else q_out, dev, "q")
+    c = None
+    if k is not None:
+        c, kk, sk = _rotary_rows(k, k if k_out is None else k_out, dev, "k")
+        _same_rows(kind, shape, kk, sk)
+    batch = shape[0] if len(shape) == 4 else 1
+    rows, dim = shape[-3], shape[-1]
+    if batch > _INT_MAX or rows > _INT_MAX or dim > _INT_MAX:
+        _fits(batch, rows, dim)
+    rc = lib().dit_qknorm_rotary(plan.ref, a, c, _head_weights(q_norm, dim, dev, "q_norm"),
+                                 _head_weights(k_norm, dim, dev, "k_norm"), eps, kind, batch, rows, dim,
+                                 _positions(plan, pos, batch * rows, dev), st)
+    if rc:
+        _ok(rc, "dit_qknorm_rotary")
+
+
+def dit_qknorm_rotary_backward_workspace_bytes(head_dim: int) -> int:
+    _fits(head_dim)
+    return lib().dit_qknorm_rotary_backward_workspace_bytes(head_dim)
+
+
+_grad_struct = struct.Struct("@PPPiqqqqqqqqq")  # dit_rotary_grad
+
+
+def _rotary_grad(x, dy, dx, dev, name):
+    """(dit_rotary_grad, type, shape) of the heads x, the gradient dy of their output and the place of theirs."""
+    kind = _kinds.get(getattr(x, "dtype", None))
+    if kind is None or x.get_device() != dev:
+        raise _wrong(x, dev, name)
+    strides = []
+    for t in (x, dy, dx):
+        if getattr(t, "dtype", None) is not x.dtype or t.get_device() != dev:
+            raise _wrong(t, dev, name)
+        if t.shape != x.shape:
+            raise ValueError(f"{name}: expected gradients like the input")
+        s = t.stride()
+        if len(s) not in (3, 4):
+            raise ValueError(f"{name}: expected [batch, rows, heads, head_dim] or [rows, heads, head_dim]")
+        if s[-1] != 1 and x.shape[-1] > 1:
+            raise ValueError(f"{name}: the last dimension must be dense")
+        strides += [s[0] if len(s) == 4 else 0, s[-3], s[-2]]
+    try:
+        return _grad_struct.pack(x.data_ptr(), dy.data_ptr(), dx.data_ptr(), x.shape[-2], *strides), kind, x.shape
+    except struct.error:
+        raise ValueError(f"{name}: {x.shape[-2]} heads") from None
+
+
+def dit_qknorm_rotary_backward(plan: RotaryPlan, q, k, dq, dk, pos, q_norm=None, k_norm=None, dq_out=None, dk_out=None,
+                               q_norm_grad=None, k_norm_grad=None, ws=None, eps: float = 1e-6, stream=None):
+    """The gradients of dit_qknorm_rotary: q, k its inputs (k, dk may be None), dq, dk the gradients of its outputs,
+    dq_out / dk_out those of its inputs (default: over dq / dk), q_norm_grad / k_norm_grad [head_dim] fp32 those of
+    the weights (None: not wanted). ws: dit_qknorm_rotary_backward_workspace_bytes(head_dim) bytes."""
+    dev, st = _current(stream)
+    a, kind, shape = _rotary_grad(q, dq, dq if dq_out is None else dq_out, dev, "q")
+    c = None
+    if k is not None:
+        c, kk, sk = _rotary_grad(k, dk, dk if dk_out is None else dk_out, dev, "k")
+        _same_rows(kind, shape, kk, sk)
+    batch = shape[0] if len(shape) == 4 else 1
+    rows, dim = shape[-3], shape[-1]
+    _fits(batch, rows, dim)
+    if ws is not None and (ws.get_device() != dev or not ws.is_contiguous()):
+        raise ValueError("ws: expected a contiguous CUDA tensor on the current device")
+    w = [_head_weights(t, dim, dev, n) for t, n in ((q_norm, "q_norm"), (k_norm, "k_norm"), (q_norm_grad, "q_norm_grad"),
+                                                    (k_norm_grad, "k_norm_grad"))]
+    rc = lib().dit_qknorm_rotary_backward(plan.ref, a, c, w[0], w[1], eps, kind, batch, rows, dim,
+                                          _positions(plan, pos, batch * rows, dev), w[2], w[3],
+                                          None if ws is None else ws.data_ptr(),
+                                          0 if ws is None else ws.numel() * ws.element_size(), st)
+    if rc:
+        _ok(rc, "dit_qknorm_rotary_backward")
 
 
 class Fp4Matrix:

@@ -477,6 +477,37 @@ typedef struct {
 DIT_API int dit_rotary(const dit_rotary_plan* plan, const dit_rotary_rows* q, const dit_rotary_rows* k, int type,
                        int batch, int rows, int head_dim, const int32_t* pos, int inverse, dit_stream_t stream);
 
+/* Per-head RMS norm and rotary positions in one pass [gizai:dit, prepOf; klein, section 4.4], what dit_qkv_rope
+ * does behind the bf16 QKV product, for heads out of any other linear: per head x of head_dim values
+ *   out = R (x r w),   r = 1 / sqrt(mean(x^2) + eps),   R the turn of dit_rotary
+ * in fp32 (the squares' sum too) with one rounding to the tensor's type. w: q_norm / k_norm [head_dim] fp32, or NULL for ones. The
+ * tensors, types, alignments, aliasing rules and refusals are those of dit_rotary; q's and k's head counts may
+ * differ. eps >= 0 and finite. */
+DIT_API int dit_qknorm_rotary(const dit_rotary_plan* plan, const dit_rotary_rows* q, const dit_rotary_rows* k,
+                              const float* q_norm, const float* k_norm, float eps, int type, int batch, int rows,
+                              int head_dim, const int32_t* pos, dit_stream_t stream);
+
+/* The gradient of dit_qknorm_rotary. Per tensor x (its input), dy (the gradient of its output) and dx (the gradient
+ * of x, written), each with strides as in dit_rotary_rows. With g = R^T dy:
+ *   dx = r (g w - x r mean(g w x r)),    q_norm_grad / k_norm_grad [head_dim] fp32 = sum over rows and heads of g x r
+ * (written, not added to; NULL: not wanted; zeros where there are no rows). dx may be x or dy with the same strides;
+ * otherwise no tensor written may overlap another. The sums run in a fixed order. Workspace:
+ * dit_qknorm_rotary_backward_workspace_bytes(head_dim), 256-byte aligned; its contents need not be kept. */
+typedef struct {
+  const void* x;
+  const void* dy;
+  void* dx;
+  int heads;
+  long long x_batch, x_row, x_head;
+  long long dy_batch, dy_row, dy_head;
+  long long dx_batch, dx_row, dx_head;
+} dit_rotary_grad;
+DIT_API int dit_qknorm_rotary_backward(const dit_rotary_plan* plan, const dit_rotary_grad* q, const dit_rotary_grad* k,
+                                       const float* q_norm, const float* k_norm, float eps, int type, int batch,
+                                       int rows, int head_dim, const int32_t* pos, float* q_norm_grad,
+                                       float* k_norm_grad, void* ws, size_t ws_bytes, dit_stream_t stream);
+DIT_API size_t dit_qknorm_rotary_backward_workspace_bytes(int head_dim);
+
 /* Microscaled 4-bit matrices (no counterpart on the pages, whose lowest tiers are int8 and INT4: an
  * opt-in lossy tier in the tensor cores' 4-bit floating point). A matrix [rows, cols] is stored as e2m1
  * codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 with a sign) with a scale per block of consecutive columns:

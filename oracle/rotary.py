@@ -47,3 +47,21 @@ def rotary_apply(x, cos, sin, halves, inverse=False):
     out[..., a] = x[..., a] * c - x[..., b] * s
     out[..., b] = x[..., a] * s + x[..., b] * c
     return out
+
+
+def qknorm_rotary(x, w, eps, cos, sin, halves):
+    """Heads x [..., rows, heads, d] normed over d, times w [d] (or None), then turned."""
+    x = np.asarray(x, np.float64)
+    y = x / np.sqrt(np.mean(x * x, -1, keepdims=True) + eps)
+    return rotary_apply(y if w is None else y * w, cos, sin, halves)
+
+
+def qknorm_rotary_gradient(x, dy, w, eps, cos, sin, halves):
+    """(dx, dw) of sum(dy * qknorm_rotary(x, w, ...)): by the quotient rule, value by value of the head."""
+    x = np.asarray(x, np.float64)
+    d = x.shape[-1]
+    g = rotary_apply(dy, cos, sin, halves, inverse=True)
+    u = g if w is None else g * w
+    size = np.sqrt(np.sum(x * x, -1, keepdims=True) / d + eps)
+    dx = u / size - x * np.sum(u * x, -1, keepdims=True) / (d * size ** 3)
+    return dx, np.sum(g * x / size, axis=tuple(range(x.ndim - 1)))
