@@ -25,7 +25,7 @@ namespace {
 
 constexpr int kQkThreads = 256;
 constexpr int kQkMaxRows = 32;   // rows of a chunk at most
-constexpr int kQkMaxCtas = 640;  // CTAs of the backward pass at most: each leaves one row of partial sums
+constexpr int kQkMaxCtas = 320;  // CTAs of the backward pass at most: each leaves one row of partial sums
 
 struct QkArgs {
   const void* x[2];
@@ -48,13 +48,18 @@ struct QkArgs {
 // neighbouring lanes, NU units on each, so its sum of squares is a butterfly within a warp and the values stay in
 // registers between the sum and the turn. The CTA's groups of lanes go through the heads of a few rows, U heads
 // in flight each; the rows' cosines and sines are worked out once into shared memory.
+// Heads in flight per group. Two, and four CTAs to an SM in the forward pass: 26.8 us at 4224 rows of 24 + 24 heads
+// in bf16, against 30.0 with four heads and two CTAs; backward, two heads and two CTAs: 50 us, one head 61.
+__host__ __device__ constexpr int qk_flight(int nu) {
+  return nu > 1 ? 1 : 2;
+}
 template <typename T, int VE, bool HALVES, int NU, bool GRAD>
 struct QkCfg {
   static constexpr bool kTwo = HALVES || VE == 1;
   static constexpr int kTurn = HALVES ? VE : (VE == 1 ? 1 : VE / 2);  // pairs of a turned unit
   static constexpr int kVals = kTwo ? 2 * VE : VE;
   static constexpr int kPiece = kTurn < 4 ? kTurn : 4;  // angles per shared-memory access
-  static constexpr int kU = NU > 2 ? 1 : (kTwo && VE > 1 ? 2 : (GRAD ? 2 : 4)) / (NU > 1 ? 2 : 1);
+  static constexpr int kU = qk_flight(NU);
 };
 
 // n = kPiece floats at 4 n bytes alignment
@@ -72,7 +77,7 @@ __device__ __forceinline__ void ld_piece(const float* p, float* v) {
 }
 
 template <typename T, int VE, bool HALVES, int NU, bool GRAD>
-__global__ void __launch_bounds__(kQkThreads) qknorm_kernel(const __grid_constant__ QkArgs a) {
+__global__ void __launch_bounds__(kQkThreads, VE > 1 && NU == 1 ? (GRAD ? 2 : 4) : 1) qknorm_kernel(const __grid_constant__ QkArgs a) {
   using C = QkCfg<T, VE, HALVES, NU, GRAD>;
   using R = Raw<T, VE>;
   constexpr int kU = C::kU, kVals = C::kVals, kTurn = C::kTurn, kPiece = C::kPiece;
@@ -91,6 +96,7 @@ __global__ void __launch_bounds__(kQkThreads) qknorm_kernel(const __grid_constan
     turn[n] = u < turned;
     off[n] = turn[n] ? (HALVES ? u * VE : u * 2 * kTurn) : 2 * pairs + (u - turned) * VE;
   }
+  const float inv_d = 1.f / float(a.d);
   const int far = HALVES ? pairs : 1;  // from a unit's first values to their partners
   float acc[GRAD ? 2 : 1][NU][kVals];
 #pragma unroll
@@ -119,19 +125,43 @@ __global__ void __launch_bounds__(kQkThreads) qknorm_kernel(const __grid_constan
 #pragma unroll
         for (int j = 0; j < kVals; ++j)
           w[n][j] = a.w[z] && live[n] && (j < VE || turn[n]) ? __ldg(a.w[z] + off[n] + (j < VE ? j : far + j - VE)) : 1.f;
-      const int items = nrows * heads;
-      for (int base = 0; base < items; base += groups * kU) {
+      // the group's heads of the chunk: every `groups`-th, its row, head and addresses stepped along
+      const int r0 = group / heads, dr = groups / heads, dh = groups - dr * heads;
+      int at = group - r0 * heads, row = r0;
+      x += r0 * a.xr[z] + at * a.xh[z];
+      out += r0 * a.orow[z] + at * a.oh[z];
+      const long long xs = dr * a.xr[z] + dh * a.xh[z], xw = a.xr[z] - heads * a.xh[z];
+      const long long os = dr * a.orow[z] + dh * a.oh[z], ow = a.orow[z] - heads * a.oh[z];
+      long long ys = 0, yw = 0;
+      if constexpr (GRAD) {
+        dy += r0 * a.yr[z] + at * a.yh[z];
+        ys = dr * a.yr[z] + dh * a.yh[z];
+        yw = a.yr[z] - heads * a.yh[z];
+      }
+      const int rounds = (nrows * heads + groups * kU - 1) / (groups * kU);
+      for (int round = 0; round < rounds; ++round) {
         R v[kU][NU][kTwo ? 2 : 1], e[GRAD ? kU : 1][NU][kTwo ? 2 : 1];
-        int row[kU], head[kU];
+        int angle[kU];  // the row's place among the angles
+        T* po[kU];
         bool ok[kU];
 #pragma unroll
         for (int k = 0; k < kU; ++k) {
-          const int item = base + k * groups + group;
-          ok[k] = item < items;
-          row[k] = ok[k] ? item / heads : 0;
-          head[k] = ok[k] ? item - row[k] * heads : 0;
-          const T* px = x + row[k] * a.xr[z] + head[k] * a.xh[z];
-          const T* py = GRAD ? dy + row[k] * a.yr[z] + head[k] * a.yh[z] : nullptr;
+          ok[k] = row < nrows;
+          angle[k] = ok[k] ? row * pairs : 0;
+          po[k] = out;
+          const T *px = x, *py = dy;
+          at += dh;
+          row += dr;
+          x += xs;
+          out += os;
+          if constexpr (GRAD) dy += ys;
+          if (at >= heads) {
+            at -= heads;
+            ++row;
+            x += xw;
+            out += ow;
+            if constexpr (GRAD) dy += yw;
+          }
 #pragma unroll
           for (int n = 0; n < NU; ++n) {
 #pragma unroll
@@ -157,9 +187,9 @@ __global__ void __launch_bounds__(kQkThreads) qknorm_kernel(const __grid_constan
             const int32_t p = __ldg(a.pos + ((long long)b * a.rows + t0 + r) * a.plan.axes + a.plan.axis[f]);
             const float2 t = rot_cos_sin(p, a.plan.turns[f], a.plan.amplitude);
             const int u = f / kTurn, j = f - u * kTurn;
-            const int at = r * pairs + (j / kPiece) * (kPiece * turned) + u * kPiece + j % kPiece;
-            sc[at] = t.x;
-            ss[at] = GRAD ? -t.y : t.y;
+            const int place = r * pairs + (j / kPiece) * (kPiece * turned) + u * kPiece + j % kPiece;
+            sc[place] = t.x;
+            ss[place] = GRAD ? -t.y : t.y;
           }
           __syncthreads();
           angles = true;
@@ -182,12 +212,14 @@ __global__ void __launch_bounds__(kQkThreads) qknorm_kernel(const __grid_constan
 #pragma unroll
             for (int j = 0; j < kVals; ++j) sum = fmaf(y[n][j], y[n][j], sum);
           }
-          for (int o = a.lanes >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          const float r = rsqrtf(sum / float(a.d) + a.eps);
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1)
+            if (o < a.lanes) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          const float r = rsqrtf(fmaf(sum, inv_d, a.eps));
           // the turn of one unit: (p, q) -> (p c - q s, p s + q c)
           auto spin = [&](float* m, int n) {
-            const float* pc = sc + row[k] * pairs + (u0 + n * a.lanes) * kPiece;
-            const float* ps = ss + row[k] * pairs + (u0 + n * a.lanes) * kPiece;
+            const float* pc = sc + angle[k] + (u0 + n * a.lanes) * kPiece;
+            const float* ps = ss + angle[k] + (u0 + n * a.lanes) * kPiece;
 #pragma unroll
             for (int i = 0; i < kTurn / kPiece; ++i) {
               float c[kPiece], s[kPiece];
@@ -232,27 +264,28 @@ __global__ void __launch_bounds__(kQkThreads) qknorm_kernel(const __grid_constan
                 dot = fmaf(g[n][j], y[n][j], dot);
               }
             }
-            for (int o = a.lanes >> 1; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-            dot /= float(a.d);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+              if (o < a.lanes) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+            dot *= inv_d;
 #pragma unroll
             for (int n = 0; n < NU; ++n)
 #pragma unroll
               for (int j = 0; j < kVals; ++j) y[n][j] = r * (g[n][j] - y[n][j] * dot);
           }
           if (!ok[k]) continue;
-          T* po = out + row[k] * a.orow[z] + head[k] * a.oh[z];
 #pragma unroll
           for (int n = 0; n < NU; ++n) {
             if (!live[n]) continue;
             float h[VE];
 #pragma unroll
             for (int j = 0; j < VE; ++j) h[j] = y[n][j];
-            rot_store<T, VE>(po + off[n], rot_raw<T, VE>(h));
+            rot_store<T, VE>(po[k] + off[n], rot_raw<T, VE>(h));
             if constexpr (kTwo)
               if (turn[n]) {
 #pragma unroll
                 for (int j = 0; j < VE; ++j) h[j] = y[n][VE + j];
-                rot_store<T, VE>(po + off[n] + far, rot_raw<T, VE>(h));
+                rot_store<T, VE>(po[k] + off[n] + far, rot_raw<T, VE>(h));
               }
           }
         }
@@ -282,25 +315,32 @@ __global__ void __launch_bounds__(kQkThreads) qknorm_kernel(const __grid_constan
   }
 }
 
-// The weights' gradients from the CTAs' sums: a block per 32 values of one norm, eight slices of the CTAs summed in
-// 64 bits, then the slices in order.
-__global__ void __launch_bounds__(256) qknorm_sum_kernel(const float* partial, int ctas, int d, float* dq, float* dk) {
-  __shared__ double part[8][32];
+// The weights' gradients from the CTAs' sums: a block per 32 values of one norm, 32 slices of the CTAs, each with all
+// of its loads in flight, then a butterfly over the slices.
+constexpr int kSumSlices = 32, kSumLoads = kQkMaxCtas / kSumSlices;
+__global__ void __launch_bounds__(1024) qknorm_sum_kernel(const float* partial, int ctas, int d, float* dq, float* dk) {
+  __shared__ float part[kSumSlices][33];
   pdl_wait();
   pdl_trigger();
-  const int z = blockIdx.y, j = blockIdx.x * 32 + (threadIdx.x & 31), slice = threadIdx.x >> 5;
+  const int z = blockIdx.y, lane = threadIdx.x & 31, j = blockIdx.x * 32 + lane, slice = threadIdx.x >> 5;
   float* out = z ? dk : dq;
   if (!out) return;
-  double s = 0.0;
-  if (j < d)
-#pragma unroll 4
-    for (int c = slice; c < ctas; c += 8) s += partial[((long long)c * 2 + z) * d + j];
-  part[slice][threadIdx.x & 31] = s;
-  __syncthreads();
-  if (slice == 0 && j < d) {
-    for (int i = 1; i < 8; ++i) s += part[i][threadIdx.x];
-    out[j] = float(s);
+  float v[kSumLoads];
+#pragma unroll
+  for (int i = 0; i < kSumLoads; ++i) {
+    const int c = slice + i * kSumSlices;
+    v[i] = c < ctas && j < d ? partial[((long long)c * 2 + z) * d + j] : 0.f;
   }
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < kSumLoads; ++i) s += v[i];
+  part[slice][lane] = s;
+  __syncthreads();
+  s = part[lane][slice];  // a warp per value now
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  const int col = blockIdx.x * 32 + slice;
+  if (lane == 0 && col < d) out[col] = s;
 }
 
 template <typename T, int VE, bool HALVES, bool GRAD>
@@ -394,18 +434,28 @@ int qk_launch(const dit_rotary_plan* plan, const int heads[2], const Tensor x[2]
   const int per_lane = a.units <= 32 ? 1 : (a.units <= 64 ? 2 : 8);
   while (a.lanes * per_lane < a.units) a.lanes *= 2;
   const int groups = kQkThreads / a.lanes, all = heads[0] + heads[1];
-  // Enough heads in a chunk for two rounds of the CTA's groups, while there are chunks for every SM several times over
-  long long per = std::max<long long>(1, (8LL * groups + all - 1) / all);
-  per = std::min<long long>(per, kQkMaxRows);
-  per = std::max(1LL, std::min(per, (long long)batch * rows / (3LL * num_sms())));
-  per = std::min<long long>(per, rows);
+  // Rows of a chunk: few heads left over in the last round of q's and of k's (a round costs the same half empty), a
+  // round's worth for the angles and the barrier, and chunks for every SM several times over. (4224 rows of 24 + 24
+  // heads: 40 us with 3 rows to a chunk, where 8 take 27.)
+  const int flight = groups * qk_flight(per_lane);
+  const long long most = std::max(1LL, std::min<long long>(std::min(kQkMaxRows, rows), (long long)batch * rows / (3LL * num_sms())));
+  long long per = 1;
+  double least = 0;
+  for (long long n = 1; n <= most; ++n) {
+    double rounds = 1;
+    for (int z = 0; z < 2; ++z) rounds += double((n * heads[z] + flight - 1) / flight);
+    if (n == 1 || rounds / n < least) {
+      least = rounds / n;
+      per = n;
+    }
+  }
   if (per * all > 0x7fffffffLL / 4) return DIT_EUNSUPPORTED;
   a.rows_per_chunk = int(per);
   a.row_chunks = int((rows + per - 1) / per);
   const long long chunks = (long long)batch * a.row_chunks;
   if (chunks > 0x7fffffffLL) return DIT_EUNSUPPORTED;
   a.chunks = int(chunks);
-  const unsigned ctas = grad ? unsigned(std::min<long long>(chunks, std::min(4 * num_sms(), kQkMaxCtas))) : unsigned(chunks);
+  const unsigned ctas = grad ? unsigned(std::min<long long>(chunks, std::min(2 * num_sms(), kQkMaxCtas))) : unsigned(chunks);
   size_t smem = size_t(per) * plan->pairs * 2 * sizeof(float);
   if (grad) smem = std::max(smem, size_t(groups) * head_dim * sizeof(float));
   cudaError_t e;
@@ -485,7 +535,7 @@ int dit_qknorm_rotary_backward(const dit_rotary_plan* plan, const dit_rotary_gra
   }
   if (!q_norm_grad && !k_norm_grad) return DIT_OK;
   // no rows: sums of nothing, which are written too
-  if (launch_pdl(qknorm_sum_kernel, dim3(unsigned((head_dim + 31) / 32), 2), dim3(256), 0, st, 1,
+  if (launch_pdl(qknorm_sum_kernel, dim3(unsigned((head_dim + 31) / 32), 2), dim3(1024), 0, st, 1,
                  static_cast<const float*>(ws), int(ctas), head_dim, q_norm_grad, k_norm_grad) != cudaSuccess)
     return DIT_ECUDA;
   return cudaGetLastError() == cudaSuccess ? DIT_OK : DIT_ECUDA;
