@@ -32,7 +32,7 @@ __all__ = [
     "dit_fp4_dequantize", "dit_fp4_matmul", "dit_linear_fp4", "dit_linear_fp4_workspace_bytes",
     "Fp4BlockWeights", "dit_block_forward_fp4", "dit_block_fp4_workspace_bytes",
     "dit_denoise", "dit_block_forward_noalloc", "dit_block_noalloc_max_bytes", "dit_workspace_bytes", "dit_denoise_workspace_bytes", "dit_modnorm", "dit_qkv_rope",
-    "dit_vt_stride", "dit_stream_k_workspace_bytes", "dit_attention", "dit_attention_qknorm", "dit_attention_workspace_bytes", "dit_linear_gated", "dit_linear_swiglu", "dit_linear",
+    "dit_vt_stride", "dit_stream_k_workspace_bytes", "dit_attention", "dit_attention_packed", "dit_attention_packed_workspace_bytes", "dit_attention_qknorm", "dit_attention_workspace_bytes", "dit_linear_gated", "dit_linear_swiglu", "dit_linear",
     "dit_dequant_int8", "dit_linear_int8", "dit_linear_int8_workspace_bytes", "dit_check", "dit_selftest_bounded_wait", "dit_status_string", "dit_version",
 ]
 
@@ -111,6 +111,13 @@ class dit_rotary_grad(ctypes.Structure):
     _fields_ = [("x", c_void_p), ("dy", c_void_p), ("dx", c_void_p), ("heads", c_int), ("x_batch", c_longlong),
                 ("x_row", c_longlong), ("x_head", c_longlong), ("dy_batch", c_longlong), ("dy_row", c_longlong),
                 ("dy_head", c_longlong), ("dx_batch", c_longlong), ("dx_row", c_longlong), ("dx_head", c_longlong)]
+
+
+class dit_packed_attention(ctypes.Structure):
+    _fields_ = ([(n, c_void_p) for n in ("q", "k", "v", "o", "lse", "q_start", "k_start", "visible", "slope")] +
+                [(n, c_longlong) for n in ("q_row", "q_head", "k_row", "k_head", "v_row", "v_head", "o_row", "o_head")] +
+                [(n, c_int) for n in ("q_rows", "k_rows", "segments", "heads", "kv_heads", "head_dim")] +
+                [("scale", c_float), ("cap", c_float)])
 
 
 class dit_fp4_matrix(ctypes.Structure):
@@ -221,6 +228,8 @@ _SIGNATURES = {
     "dit_attention_workspace_bytes": (c_size_t, [POINTER(dit_dims), c_int]),
     "dit_attention_qknorm": (c_int, [POINTER(dit_dims), c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                      c_void_p, c_void_p, c_size_t, c_void_p]),
+    "dit_attention_packed": (c_int, [c_void_p, c_void_p, c_size_t, c_void_p]),
+    "dit_attention_packed_workspace_bytes": (c_size_t, [c_int, c_int, c_int, c_int, c_int, c_int]),
     "dit_linear_gated": (c_int, [POINTER(dit_dims), c_void_p, c_int, c_int, c_void_p, POINTER(dit_mod), c_int,
                                  c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
     "dit_linear_swiglu": (c_int, [POINTER(dit_dims), c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_size_t,
@@ -1073,6 +1082,79 @@ def dit_attention_qknorm(dims: DitDims, R: int, q, k, vt, q_norm, k_norm, o, ws=
                                    _ptr(q_norm, f32), _ptr(k_norm, f32), _ptr(o, bf, "o"), _ptr(ws), _ws_bytes(ws),
                                    _stream(stream)),
         "dit_attention_qknorm")
+
+
+_packed_struct = struct.Struct("@" + "P" * 9 + "q" * 8 + "i" * 6 + "ff")  # dit_packed_attention
+
+
+def _heads_of(t, name, dev, shape=None):
+    """(pointer, row stride, head stride) of bf16 [rows, heads, head_dim] with dense heads."""
+    if getattr(t, "dtype", None) is not _torch_mod.bfloat16:
+        raise TypeError(f"{name}: expected a bfloat16 tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: expected a CUDA tensor on the current device")
+    if len(t.shape) != 3 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name}: expected [rows, heads, head_dim]{'' if shape is None else ' ' + str(list(shape))}")
+    s = t.stride()
+    if s[2] != 1:
+        raise ValueError(f"{name}: the last dimension must be dense")
+    return t.data_ptr(), s[0], s[1]
+
+
+def _dense(t, dtype, n, name, dev):
+    """Pointer of a dense tensor of n values on the current device; None -> 0."""
+    if t is None:
+        return 0
+    if getattr(t, "dtype", None) is not dtype:
+        raise TypeError(f"{name}: expected {dtype}")
+    if t.get_device() != dev or not t.is_contiguous() or t.numel() != n:
+        raise ValueError(f"{name}: expected {n} dense values on the current device")
+    return t.data_ptr()
+
+
+def dit_attention_packed_workspace_bytes(q_rows: int, k_rows: int, segments: int, heads: int, kv_heads: int,
+                                         head_dim: int) -> int:
+    _fits(q_rows, k_rows, segments, heads, kv_heads, head_dim)
+    return lib().dit_attention_packed_workspace_bytes(q_rows, k_rows, segments, heads, kv_heads, head_dim)
+
+
+def dit_attention_packed(q, k, v, o, q_start=None, k_start=None, visible=None, scale: Optional[float] = None,
+                         cap: float = 0.0, slope=None, lse=None, ws=None, stream=None):
+    """Attention of q [q_rows, heads, d] over k, v [k_rows, kv_heads, d] (bf16, any strides with dense heads), segment by
+    segment: q_start, k_start [segments + 1] int32 (None: one segment), visible [q_rows] int32 the keys each row sees (None:
+    its segment's), scale (None: d ** -0.5), cap of the scores (0: none), slope [heads] fp32 of the distance bias. o like q,
+    lse [heads, q_rows] fp32 or None. ws: scratch of dit_attention_packed_workspace_bytes or None."""
+    dev, st = _current(stream)
+    torch = _torch_mod
+    pq, qr, qh = _heads_of(q, "q", dev)
+    pk, kr, kh = _heads_of(k, "k", dev)
+    pv, vr, vh = _heads_of(v, "v", dev, k.shape)
+    po, orow, oh = _heads_of(o, "o", dev, q.shape)
+    q_rows, heads, d = q.shape
+    k_rows, kv_heads, dk = k.shape
+    if dk != d:
+        raise ValueError("q and k: expected one head_dim")
+    segments = 1
+    if q_start is not None or k_start is not None:
+        if q_start is None or k_start is None or q_start.numel() < 1:
+            raise ValueError("q_start, k_start: expected both, segments + 1 values each")
+        segments = q_start.numel() - 1
+    i32, f32 = torch.int32, torch.float32
+    try:
+        a = _packed_struct.pack(pq, pk, pv, po, _dense(lse, f32, heads * q_rows, "lse", dev),
+                                _dense(q_start, i32, segments + 1, "q_start", dev),
+                                _dense(k_start, i32, segments + 1, "k_start", dev),
+                                _dense(visible, i32, q_rows, "visible", dev), _dense(slope, f32, heads, "slope", dev), qr, qh, kr,
+                                kh, vr, vh, orow, oh, q_rows, k_rows, segments, heads, kv_heads, d,
+                                d ** -0.5 if scale is None else scale, cap)
+    except struct.error:
+        raise ValueError("a size past 32 bits") from None
+    if ws is not None and (ws.get_device() != dev or not ws.is_contiguous()):
+        raise ValueError("ws: expected a contiguous CUDA tensor on the current device")
+    rc = lib().dit_attention_packed(a, None if ws is None else ws.data_ptr(),
+                                    0 if ws is None else ws.numel() * ws.element_size(), st)
+    if rc:
+        _ok(rc, "dit_attention_packed")
 
 
 def dit_linear_gated(dims: DitDims, a, L: int, N: int, w, mod: Modulation, which: int, txt, img, ws=None,

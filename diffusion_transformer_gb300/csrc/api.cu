@@ -1578,6 +1578,14 @@ int dit_attention_qknorm(const dit_dims* d, int R, const uint16_t* q, const uint
   return attention_launch(ap, reinterpret_cast<cudaStream_t>(stream));
 }
 
+int dit_attention_packed(const dit_packed_attention* a, void* ws, size_t ws_bytes, dit_stream_t stream) {
+  const int rc = packed_attention_check(a, ws);
+  if (rc != DIT_OK || a->q_rows == 0 || a->segments == 0) return rc;
+  int* err = err_word();
+  if (!err) return DIT_ECUDA;
+  return packed_attention_launch(*a, ws, ws_bytes, err, reinterpret_cast<cudaStream_t>(stream));
+}
+
 int dit_linear_gated(const dit_dims* d, const uint16_t* a, int L, int N, const uint16_t* w, const dit_mod* mod,
                      int which, float* txt, float* img, void* ws, size_t ws_bytes, dit_stream_t stream) {
   if (!d || !a || !w || !mod || !mod->rows || mod->M < 1 || !img || L < 0 || N < 1 || (L > 0 && !txt) ||

@@ -1,0 +1,784 @@
+// Attention over packed sequences on tcgen05 for sm_103a: many sequences of unlike length in one call, grouped key
+// heads, per-row visible keys, capped scores and a distance bias; single rows over long key ranges.
+//
+// Mathematics. Segment s has the query rows [q_start[s], q_start[s + 1]) and the keys [k_start[s], k_start[s + 1]).
+// Row i of a segment (of nq rows, nk keys) sees its keys j < c_i (all without `visible`):
+//   x_ij = cap tanh(scale q_i.k_j / cap) - slope_h |i + nk - nq - j|       (either part left out where not given)
+//   o_i = sum_j softmax_j(x_ij) v_j,    lse_i = ln sum_j exp(x_ij);    no key seen: o_i = 0, lse_i = -inf
+// The softmax runs over key tiles with a running maximum and sum (klein article, section 4.3), in fp32 in log2 units;
+// only the weights round to bf16 for the product with V, whose sum is fp32 in tensor memory.
+//
+// GB300 mapping. The query heads that share a key head stand side by side in one 128-row tile (row r G + g: query row
+// r, head g of the G), so K and V are read once for all of them. A CTA takes two such tiles of one segment (NT = 2), or,
+// where segments have few rows, one tile whose two halves of the key tiles, even and odd, run like the two tiles
+// (NT = 1) and meet at the end in shared memory. Roles as in the joint attention: warp 0 loads with TMA, warp 1 issues
+// the MMAs, warps 2-5 and 6-9 turn the scores of the two tiles into weights, so that one tile's exponentials overlap the
+// other's MMAs. K and V are rows of any stride: both come by TMA as [keys, d] boxes, and V enters its MMA as an
+// MN-major operand, so nothing is transposed in memory. CTAs find their segment by a scan over q_start: no lengths on
+// the host, and a captured graph serves other lengths. Where there are too few tiles for the SMs the key range is
+// split over CTAs (blockIdx.z) and a second kernel joins the parts in order.
+// Masked places: weights of masked keys are zero, the rows of V behind the last key that any row of the CTA sees are
+// zeroed in shared memory (they may be the next segment's, or anything), and a row whose result is not finite while
+// its tile held keys that it does not see is summed again over its own keys (resum_row): NaN or infinity in a masked
+// place never reaches it.
+//
+// Tensor memory (512 columns): [0, 128) S0, P0 over it   [128, 256) S1 / P1   [256, 256 + d) O0   [256 + d, 256 + 2 d) O1
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstring>
+
+#include "internal.h"
+#include "ptx.cuh"
+#include "tmap.h"
+
+namespace dit {
+namespace {
+
+constexpr float kRescaleStep = 8.0f;  // log2 units: the running maximum moves only past this, so weights stay below 2^8
+constexpr int kMaxSplits = 32;
+constexpr int kPackedThreads = 320;
+
+struct PackedParams {
+  dit_packed_attention a;
+  int G, rpt;  // query heads per key head, query rows of a tile
+  int splits;
+  float scale_log2;  // scale log2(e)
+  float cap_in, cap_out;  // 2 scale log2(e) / cap and cap log2(e); cap_out = 0: no cap
+  float* part_o;   // [split][q_rows][heads][d]
+  float2* part_ml;  // [split][q_rows][heads]: running maximum (log2 units) and sum
+  int* err;
+};
+
+template <int D, int NT>
+struct PackedCfg {
+  static constexpr uint32_t kTile = 128 * D * 2;  // 128 rows of q, k or v
+  static constexpr uint32_t kAtom = 128 * 128;    // [128 rows x 64 bf16], 128-byte swizzled
+  static constexpr int kKS = D == 128 ? 3 : (NT == 2 ? 4 : 5);
+  static constexpr int kVS = D == 128 ? (NT == 2 ? 2 : 3) : (NT == 2 ? 4 : 5);
+  static constexpr int kBars = 2 + 2 * kKS + 2 * kVS + 6;
+  static constexpr uint32_t kSmem = 1024 + NT * kTile + (kKS + kVS) * kTile + kBars * 8 + 64 + (NT == 1 ? 1024 : 0);
+  static_assert(kSmem <= 227 * 1024, "shared memory budget");
+  static_assert(kSmem > 114 * 1024, "one CTA per SM: each takes all of tensor memory");
+};
+
+// V as the MN-major operand of O += P V: 64-value rows of a key (128 bytes), swizzled; the next eight keys 1024 bytes on
+// (stride byte offset), the next 64 values of d a box of 128 keys on (leading byte offset).
+__device__ __forceinline__ uint64_t v_desc(uint32_t saddr) {
+  return uint64_t((saddr & 0x3FFFFu) >> 4) | (uint64_t(16384 >> 4) << 16) | (uint64_t(1024 >> 4) << 32) |
+         (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// cap log2(e) tanh(scale s / cap) as c - 2 c / (1 + 2^(2 scale log2(e) s / cap)): absolute error a few 2^-24 of c
+__device__ __forceinline__ float capped(float s, float cap_in, float cap_out) {
+  return fmaf(-2.f * cap_out, rcp_approx(1.f + ex2_approx(s * cap_in)), cap_out);
+}
+
+struct Segment {
+  int q0, nq, k0, nk;
+  int tile;  // of the segment; < 0: none left
+};
+
+// The segment and tile of CTA x: tiles of `rows` query rows each, counted segment by segment (warp-collective).
+__device__ Segment find_tile(const dit_packed_attention& a, int rows, int x) {
+  const int lane = lane_id();
+  auto at = [&](const int32_t* p, int s, int top) { return p ? min(max(__ldg(p + s), 0), top) : (s == 0 ? 0 : top); };
+  int before = 0;
+  for (int base = 0; base < a.segments; base += 128) {
+    int n[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int s = base + 32 * u + lane;
+      n[u] = 0;
+      if (s < a.segments) n[u] = max(at(a.q_start, s + 1, a.q_rows) - at(a.q_start, s, a.q_rows), 0);
+      n[u] = (n[u] + rows - 1) / rows;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      int sum = n[u];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += v;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, before + sum > x);
+      if (past) {
+        const int l = __ffs(past) - 1, s = base + 32 * u + l;
+        const int first = before + __shfl_sync(0xffffffffu, sum - n[u], l);
+        Segment g;
+        g.q0 = at(a.q_start, s, a.q_rows);
+        g.nq = at(a.q_start, s + 1, a.q_rows) - g.q0;
+        g.k0 = at(a.k_start, s, a.k_rows);
+        g.nk = max(at(a.k_start, s + 1, a.k_rows) - g.k0, 0);
+        g.tile = x - first;
+        return g;
+      }
+      before += __shfl_sync(0xffffffffu, sum, 31);
+    }
+  }
+  return Segment{0, 0, 0, 0, -1};
+}
+
+// The weighted sum of V over the keys [j0, j1) that a row does see, on the plain cores: only for rows that the matrix
+// product left not finite beside keys they do not see (0 x NaN). A warp per row; lane l ends with values l D / 32 and on.
+template <int D, bool GEN>
+__device__ __noinline__ void resum_row(const PackedParams& p, int q_at, int k0, int j0, int j1, int head, int kvh, float where,
+                                       float m, float (&acc)[D / 32]) {
+  constexpr int V = D / 32;
+  const dit_packed_attention& a = p.a;
+  const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) + q_at * a.q_row + head * a.q_head + lane_id() * V;
+  const __nv_bfloat16* k = reinterpret_cast<const __nv_bfloat16*>(a.k) + kvh * a.k_head + lane_id() * V;
+  const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(a.v) + kvh * a.v_head + lane_id() * V;
+  float qv[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    qv[i] = __bfloat162float(q[i]);
+    acc[i] = 0.f;
+  }
+  for (int j = j0; j < j1; ++j) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) s = fmaf(qv[i], __bfloat162float(k[(k0 + (long long)j) * a.k_row + i]), s);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    float x = s * p.scale_log2;
+    if constexpr (GEN) {
+      if (p.cap_out > 0.f) x = capped(s, p.cap_in, p.cap_out);
+      if (a.slope) x = fmaf(-1.4426950408889634f * __ldg(a.slope + head), fabsf(where - float(j)), x);
+    }
+    const float w = ex2_approx(x - m);
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = fmaf(w, __bfloat162float(v[(k0 + (long long)j) * a.v_row + i]), acc[i]);
+  }
+}
+
+template <int D, int NT, bool GEN>
+__global__ void __launch_bounds__(kPackedThreads, 1)
+    packed_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                  const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PackedParams p) {
+  using Cfg = PackedCfg<D, NT>;
+  constexpr int KS = Cfg::kKS, VS = Cfg::kVS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem;
+  uint8_t* sK = sQ + NT * Cfg::kTile;
+  uint8_t* sV = sK + KS * Cfg::kTile;
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(sV + VS * Cfg::kTile);
+  uint64_t* drain = q_full + 1;
+  uint64_t* k_full = drain + 1;      // [KS]
+  uint64_t* k_empty = k_full + KS;   // [KS]
+  uint64_t* v_full = k_empty + KS;   // [VS]
+  uint64_t* v_empty = v_full + VS;   // [VS]
+  uint64_t* s_full = v_empty + VS;   // [2]
+  uint64_t* p_full = s_full + 2;     // [2]
+  uint64_t* o_done = p_full + 2;     // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_done + 2);
+  int* s_lim = reinterpret_cast<int*>(tmem_slot + 1);              // [2] keys that any row of the tile sees
+  Segment* s_seg = reinterpret_cast<Segment*>(s_lim + 2);          // 20 bytes
+  float2* s_ml = reinterpret_cast<float2*>(tmem_slot + 16);        // NT = 1: [128] the odd half's maximum and sum
+
+  const dit_packed_attention& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = lane_id();
+  const int kvh = blockIdx.y, G = p.G, rpt = p.rpt;
+
+  pdl_wait();
+  pdl_trigger();
+  if (warp == 0) {
+    const Segment g = find_tile(a, NT * rpt, blockIdx.x);
+    if (lane == 0) *s_seg = g;
+  } else if (threadIdx.x == 32) {
+    s_lim[0] = s_lim[1] = 0;
+    mbar_init(smem_u32(q_full), 1);
+    mbar_init(smem_u32(drain), 1);
+    for (int s = 0; s < KS; ++s) {
+      mbar_init(smem_u32(&k_full[s]), 1);
+      mbar_init(smem_u32(&k_empty[s]), 1);
+    }
+    for (int s = 0; s < VS; ++s) {
+      mbar_init(smem_u32(&v_full[s]), 1);
+      mbar_init(smem_u32(&v_empty[s]), 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(smem_u32(&s_full[t]), 1);
+      mbar_init(smem_u32(&p_full[t]), 4);  // one arrival per warp of the tile's group
+      mbar_init(smem_u32(&o_done[t]), 1);
+    }
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const Segment seg = *s_seg;
+  if (seg.tile < 0) return;  // more CTAs than tiles: the bound counts a part-filled tile for every segment
+
+  // a softmax thread's row: query row `i` of the segment, head `head`, seeing `lim` keys
+  const int t = (warp - 2) >> 2, quad = warp & 3, row = quad * 32 + lane;
+  const int r = row / G, g = row - r * G;
+  const int i = seg.tile * NT * rpt + (NT == 2 ? t * rpt : 0) + r;
+  const int head = kvh * G + g;
+  const bool valid = warp >= 2 && r < rpt && i < seg.nq;
+  int lim = 0;
+  if (warp >= 2) {
+    if (valid) lim = a.visible ? min(max(__ldg(a.visible + seg.q0 + i), 0), seg.nk) : seg.nk;
+    const int top = __reduce_max_sync(0xffffffffu, lim);
+    if (lane == 0 && top > 0) atomicMax(&s_lim[t], top);
+  } else if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  // this CTA's key tiles [ta, tb), and how many of them each tile (or half) takes
+  const int lmax = max(s_lim[0], s_lim[1]);
+  const int tiles = (lmax + 127) >> 7;
+  const int ta = int((long long)tiles * blockIdx.z / p.splits), tb = int((long long)tiles * (blockIdx.z + 1) / p.splits);
+  int n0, n1;
+  if constexpr (NT == 2) {
+    n0 = min(max((s_lim[0] + 127) >> 7, ta), tb) - ta;
+    n1 = min(max((s_lim[1] + 127) >> 7, ta), tb) - ta;
+  } else {
+    n0 = (tb - ta + 1) >> 1;
+    n1 = (tb - ta) >> 1;
+  }
+  auto key_tile = [&](int tt, int it) { return NT == 2 ? it : 2 * it + tt; };  // of the CTA's
+  const int loads = NT == 2 ? max(n0, n1) : n0 + n1;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ TMA producer
+    if (loads > 0 && elect_one()) {
+      const uint32_t qb = smem_u32(q_full);
+      const bool both = NT == 2 && n1 > 0, first = NT == 1 || n0 > 0;
+      mbar_arrive_expect_tx(qb, uint32_t(int(first) + int(both)) * (D / 64) * 128u * uint32_t(G * rpt));
+      for (int tt = 0; tt < NT; ++tt) {
+        if (tt == 0 ? !first : !both) continue;
+        for (int c = 0; c < D / 64; ++c)
+          tma_load_3d(smem_u32(sQ + tt * Cfg::kTile + c * Cfg::kAtom), &tmQ, qb, c * 64, kvh * G,
+                      seg.q0 + (seg.tile * NT + tt) * rpt);
+      }
+      int nk = 0, nv = 0;
+      for (int j = 0; j < loads; ++j) {
+        const int key = seg.k0 + (ta + j) * 128;
+        const int ks = j % KS, vs = j % VS;
+        if (!mbar_wait(smem_u32(&k_empty[ks]), ((j / KS) & 1) ^ 1, p.err, kErrTimeoutProducer)) break;
+        const uint32_t kb = smem_u32(&k_full[ks]);
+        mbar_arrive_expect_tx(kb, Cfg::kTile);
+        for (int c = 0; c < D / 64; ++c) tma_load_3d(smem_u32(sK + ks * Cfg::kTile + c * Cfg::kAtom), &tmK, kb, c * 64, kvh, key);
+        ++nk;
+        if (!mbar_wait(smem_u32(&v_empty[vs]), ((j / VS) & 1) ^ 1, p.err, kErrTimeoutProducer)) break;
+        const uint32_t vb = smem_u32(&v_full[vs]);
+        mbar_arrive_expect_tx(vb, Cfg::kTile);
+        for (int c = 0; c < D / 64; ++c) tma_load_3d(smem_u32(sV + vs * Cfg::kTile + c * Cfg::kAtom), &tmV, vb, c * 64, kvh, key);
+        ++nv;
+      }
+      // every issued copy lands before the CTA exits, whatever the error word says
+      auto landed = [&](uint64_t* bar, uint32_t parity) {
+        mbar_wait_cluster(smem_u32(bar), parity, p.err, kErrTimeoutDrain, 4 * kWaitLimitNs, false);
+      };
+      landed(q_full, 0);
+      for (int j = max(0, nk - KS); j < nk; ++j) landed(&k_full[j % KS], (j / KS) & 1);
+      for (int j = max(0, nv - VS); j < nv; ++j) landed(&v_full[j % VS], (j / VS) & 1);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA issuer
+    if (loads > 0 && elect_one()) {
+      constexpr uint32_t idesc_s = idesc_bf16(128, 128);
+      constexpr uint32_t idesc_o = idesc_bf16(128, D) | (1u << 16);  // B is MN-major
+      const uint64_t dq = sw128_desc(smem_u32(sQ)), dv = v_desc(smem_u32(sV));
+      const uint32_t q_lo = uint32_t(dq), hi = uint32_t(dq >> 32);  // the high words agree: 1024-byte strides, same swizzle
+      const uint32_t k_lo = uint32_t(sw128_desc(smem_u32(sK))), v_lo = uint32_t(dv);
+      bool ok = mbar_wait(smem_u32(q_full), 0, p.err, kErrTimeoutMma);
+      auto count = [&](int tt) { return tt == 0 ? n0 : n1; };
+      auto issue_s = [&](int tt, int it) {
+        const int j = key_tile(tt, it), ks = j % KS;
+        const uint32_t d = tmem_base + uint32_t(tt * 128);
+        const uint32_t qt = q_lo + uint32_t((NT == 2 ? tt : 0) * (Cfg::kTile >> 4)), kt = k_lo + uint32_t(ks * (Cfg::kTile >> 4));
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t c = uint32_t((kk >> 2) * (Cfg::kAtom >> 4) + 2 * (kk & 3));
+          umma_bf16_lo(d, qt + c, kt + c, hi, idesc_s, kk != 0);
+        }
+        umma_commit(smem_u32(&s_full[tt]));
+        if (NT == 1 || tt == 1 || it >= n1) umma_commit(smem_u32(&k_empty[ks]));  // the tile's last user
+      };
+      auto wait_k = [&](int tt, int it) {
+        const int j = key_tile(tt, it);
+        return mbar_wait(smem_u32(&k_full[j % KS]), (j / KS) & 1, p.err, kErrTimeoutMma);
+      };
+      for (int tt = 0; tt < 2 && ok; ++tt)
+        if (count(tt) > 0) {
+          ok = wait_k(tt, 0);
+          if (!ok) break;
+          tc_fence_after();
+          issue_s(tt, 0);
+        }
+      const int most = max(n0, n1);
+      for (int it = 0; it < most && ok; ++it) {
+#pragma unroll 1
+        for (int tt = 0; tt < 2; ++tt) {
+          const int n = count(tt);
+          if (it >= n) continue;
+          const int j = key_tile(tt, it), vs = j % VS;
+          // the next K lands long before this tile's weights are ready: waited for first, so that P V and the next S
+          // go out back to back
+          if (it + 1 < n && !wait_k(tt, it + 1)) { ok = false; break; }
+          if (!mbar_wait(smem_u32(&v_full[vs]), (j / VS) & 1, p.err, kErrTimeoutMma)) { ok = false; break; }
+          if (!mbar_wait(smem_u32(&p_full[tt]), it & 1, p.err, kErrTimeoutMma)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t d = tmem_base + 256u + uint32_t(tt * D), pt = tmem_base + uint32_t(tt * 128);
+          const uint32_t vt = v_lo + uint32_t(vs * (Cfg::kTile >> 4));
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)  // 16 keys a step: 2048 bytes of every box
+            umma_bf16_ts_lo(d, pt + uint32_t(kk * 8), vt + uint32_t(kk * 128), hi, idesc_o, it != 0 || kk != 0);
+          if (NT == 1 || tt == 1 || it >= n1) umma_commit(smem_u32(&v_empty[vs]));
+          if (it + 1 == n) umma_commit(smem_u32(&o_done[tt]));
+          else issue_s(tt, it + 1);
+        }
+      }
+      umma_commit(smem_u32(drain));
+      mbar_wait_cluster(smem_u32(drain), 0, p.err, kErrTimeoutDrain, 4 * kWaitLimitNs, false);
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax warps, one row per thread
+    const uint32_t lane_off = uint32_t(quad * 32) << 16;
+    const uint32_t tS = tmem_base + lane_off + uint32_t(t * 128);
+    const uint32_t tO = tmem_base + lane_off + 256u + uint32_t(t * D);
+    const int n = t == 0 ? n0 : n1;
+    const bool live = __any_sync(0xffffffffu, lim > 0);  // warps without a row that sees a key only keep the barriers
+    const float where = float(i + seg.nk - seg.nq);      // the row's place among the keys
+    float slope2 = 0.f;
+    if constexpr (GEN)
+      if (a.slope && valid) slope2 = 1.4426950408889634f * __ldg(a.slope + head);
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int it = 0; it < n; ++it) {
+      const int j = key_tile(t, it), key0 = (ta + j) * 128;
+      if (!mbar_wait_warp(smem_u32(&s_full[t]), it & 1, p.err, kErrTimeoutSoftmax)) { ok = false; break; }
+      tc_fence_after();
+      if (live) {
+        uint32_t x[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(tS + uint32_t(c * 32), *reinterpret_cast<uint32_t(*)[32]>(&x[c * 32]));
+        tmem_ld_wait();
+        if constexpr (GEN) {
+          if (p.cap_out > 0.f) {
+#pragma unroll
+            for (int c = 0; c < 128; ++c) x[c] = __float_as_uint(capped(__uint_as_float(x[c]), p.cap_in, p.cap_out));
+          } else {
+#pragma unroll
+            for (int c = 0; c < 128; ++c) x[c] = __float_as_uint(__uint_as_float(x[c]) * p.scale_log2);
+          }
+          if (a.slope) {
+            const float at = where - float(key0);
+#pragma unroll
+            for (int c = 0; c < 128; ++c) x[c] = __float_as_uint(fmaf(-slope2, fabsf(at - float(c)), __uint_as_float(x[c])));
+          }
+        }
+        const int seen = lim - key0;
+        if (!__all_sync(0xffffffffu, seen >= 128)) {
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (c >= seen) x[c] = 0xff800000u;
+        }
+        float m8[8];
+#pragma unroll
+        for (int v = 0; v < 8; ++v) m8[v] = fmax3(__uint_as_float(x[v]), __uint_as_float(x[v + 8]), __uint_as_float(x[v + 16]));
+#pragma unroll
+        for (int c = 24; c < 120; c += 16)
+#pragma unroll
+          for (int v = 0; v < 8; ++v) m8[v] = fmax3(m8[v], __uint_as_float(x[c + v]), __uint_as_float(x[c + 8 + v]));
+#pragma unroll
+        for (int v = 0; v < 8; ++v) m8[v] = fmaxf(m8[v], __uint_as_float(x[120 + v]));
+        float mx = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
+        if constexpr (!GEN) mx *= p.scale_log2;
+        float alpha = 1.f;
+        if (mx > m + kRescaleStep) {  // also on the first tile with a key (m = -inf)
+          alpha = ex2_approx(m - mx);
+          m = mx;
+        }
+        const float base = m == -INFINITY ? 0.f : m;  // nothing seen yet: weights 2^-inf = 0
+        const float scale = GEN ? 1.f : p.scale_log2;
+        const uint64_t scale2 = f2_pack(scale, scale), neg2 = f2_pack(-base, -base);
+        uint64_t sum2[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int v = 0; v < 16; ++v) {
+            const int k0 = c * 32 + 2 * v;
+            const uint64_t s2 = f2_pack(__uint_as_float(x[k0]), __uint_as_float(x[k0 + 1]));
+            const uint64_t e2 = GEN ? f2_add(s2, neg2) : f2_fma(s2, scale2, neg2);
+            const float w0 = ex2_approx(f2_lo(e2)), w1 = ex2_approx(f2_hi(e2));
+            sum2[v & 3] = f2_add(sum2[v & 3], f2_pack(w0, w1));
+            pk[v] = pack_bf16x2(w0, w1);
+          }
+          tmem_st16(tS + uint32_t(c * 16), pk);
+        }
+        const uint64_t s4 = f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3]));
+        l = fmaf(l, alpha, f2_lo(s4) + f2_hi(s4));
+        if (it > 0 && __any_sync(0xffffffffu, alpha < 1.0f)) {
+          // O holds earlier tiles; this S came after the P V before it, which is done
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tO + uint32_t(c * 32), o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int v = 0; v < 32; ++v) o[v] = __float_as_uint(__uint_as_float(o[v]) * alpha);
+            tmem_st32(tO + uint32_t(c * 32), o);
+          }
+        }
+        tmem_st_wait();
+      }
+      // rows of V that no row of the CTA sees, zeroed by the first group that uses the tile
+      const int vz = lmax - key0;
+      if (vz < 128 && (NT == 1 || t == 0 || it >= n0)) {
+        if (!mbar_wait_warp(smem_u32(&v_full[j % VS]), (j / VS) & 1, p.err, kErrTimeoutSoftmax)) { ok = false; break; }
+        if (row >= vz)
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+            for (int v = 0; v < 8; ++v)
+              *reinterpret_cast<uint4*>(sV + (j % VS) * Cfg::kTile + c * Cfg::kAtom + row * 128 + v * 16) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&p_full[t]));
+    }
+
+    // ---- the end of the key range. `mine`: this group stores rows (both, or the first after the halves have met)
+    if (n > 0 && ok) ok = mbar_wait_warp(smem_u32(&o_done[t]), 0, p.err, kErrTimeoutSoftmax);
+    bool mine = NT == 2 || t == 0;
+    float c0 = 1.f, c1 = 0.f;  // factors of the own and of the odd half's O
+    const float4* other = reinterpret_cast<const float4*>(sK) + row;  // [D / 4][128 rows]
+    if constexpr (NT == 1) {
+      // the odd half goes through the K ring, which both halves' MMAs have read by then
+      if (t == 1 && n1 > 0) {
+        if (ok && n0 > 0) ok = mbar_wait_warp(smem_u32(&o_done[0]), 0, p.err, kErrTimeoutSoftmax);
+        if (ok && live) {
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tO + uint32_t(c * 32), o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int v = 0; v < 8; ++v)
+              reinterpret_cast<uint4*>(sK)[(c * 8 + v) * 128 + row] = make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+          }
+        }
+        s_ml[row] = make_float2(m, l);
+      }
+      if (n1 > 0) asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (t == 0 && n1 > 0) {
+        const float2 ml = s_ml[row];
+        const float top = fmaxf(m, ml.x), base = top == -INFINITY ? 0.f : top;
+        c0 = ex2_approx(m - base);
+        c1 = ex2_approx(ml.x - base);
+        l = l * c0 + ml.y * c1;
+        m = top;
+      }
+    }
+    if (mine && ok) {
+      tc_fence_after();
+      const bool whole = p.splits == 1;
+      const int covered = NT == 2 ? (ta + n) * 128 : tb * 128;  // keys behind the last tile of this row's sums
+      const int last = min(lmax, covered);
+      uint8_t* stage = sQ + (NT == 2 ? t : 0) * Cfg::kTile;  // Q has been read; [row][D] bf16, chunks swizzled by the row
+      const float inv = whole ? (l > 0.f || l != l ? 1.f / l : 0.f) : 1.f;
+      const long long at = (long long)blockIdx.z * a.q_rows + seg.q0 + i;  // row of the partial sums
+      float4* po = reinterpret_cast<float4*>(p.part_o + (at * a.heads + head) * D);
+      float bad = 0.f;
+      if (live && n0 + n1 > 0) {
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          float o[32];
+          uint32_t raw[32];
+          if (NT == 2 ? n > 0 : true) {
+            tmem_ld32(tO + uint32_t(c * 32), raw);
+            tmem_ld_wait();
+          }
+#pragma unroll
+          for (int v = 0; v < 32; ++v) o[v] = n > 0 && c0 > 0.f ? __uint_as_float(raw[v]) * c0 : 0.f;
+          if (NT == 1 && n1 > 0) {
+#pragma unroll
+            for (int v = 0; v < 8; ++v) {
+              const float4 q = other[(c * 8 + v) * 128];
+              if (c1 > 0.f) {
+                o[4 * v] = fmaf(q.x, c1, o[4 * v]);
+                o[4 * v + 1] = fmaf(q.y, c1, o[4 * v + 1]);
+                o[4 * v + 2] = fmaf(q.z, c1, o[4 * v + 2]);
+                o[4 * v + 3] = fmaf(q.w, c1, o[4 * v + 3]);
+              }
+            }
+          }
+#pragma unroll
+          for (int v = 0; v < 32; ++v) {
+            if (lim == 0) o[v] = 0.f;
+            bad = fmaf(o[v], 0.f, bad);
+            o[v] *= inv;
+          }
+          if (whole) {
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              *reinterpret_cast<uint4*>(stage + row * (D * 2) + (((c * 4 + v) ^ (row & 7)) << 4)) =
+                  make_uint4(pack_bf16x2(o[8 * v], o[8 * v + 1]), pack_bf16x2(o[8 * v + 2], o[8 * v + 3]),
+                             pack_bf16x2(o[8 * v + 4], o[8 * v + 5]), pack_bf16x2(o[8 * v + 6], o[8 * v + 7]));
+          } else if (valid) {
+#pragma unroll
+            for (int v = 0; v < 8; ++v) po[c * 8 + v] = make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+          }
+        }
+        // rows with something that is not finite beside keys they do not see
+        unsigned again = __ballot_sync(0xffffffffu, valid && bad != 0.f && lim < last);
+        while (again) {
+          const int src = __ffs(again) - 1;
+          again &= again - 1;
+          const int si = __shfl_sync(0xffffffffu, i, src), sh = __shfl_sync(0xffffffffu, head, src);
+          const int end = __shfl_sync(0xffffffffu, min(lim, covered), src);
+          const float sm = __shfl_sync(0xffffffffu, m == -INFINITY ? 0.f : m, src), sinv = __shfl_sync(0xffffffffu, inv, src);
+          float acc[D / 32];
+          resum_row<D, GEN>(p, seg.q0 + si, seg.k0, ta * 128, end, sh, kvh, __shfl_sync(0xffffffffu, where, src), sm, acc);
+          if (whole) {
+            const int srow = quad * 32 + src, at2 = lane * (D / 32) * 2;  // byte of the row
+            uint32_t* dst = reinterpret_cast<uint32_t*>(stage + srow * (D * 2) + (((at2 >> 4) ^ (srow & 7)) << 4) + (at2 & 15));
+#pragma unroll
+            for (int v = 0; v < D / 64; ++v) dst[v] = pack_bf16x2(acc[2 * v] * sinv, acc[2 * v + 1] * sinv);
+          } else {
+            float* dst = p.part_o + (((long long)blockIdx.z * a.q_rows + seg.q0 + si) * a.heads + sh) * D + lane * (D / 32);
+#pragma unroll
+            for (int v = 0; v < D / 32; ++v) dst[v] = acc[v];
+          }
+        }
+      } else if (whole) {
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c)
+          *reinterpret_cast<uint4*>(stage + row * (D * 2) + ((c ^ (row & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+      }
+      if (valid) {
+        if (!whole) p.part_ml[at * a.heads + head] = make_float2(m == -INFINITY && l != l ? 0.f : m, l);  // scores all NaN: seen
+        else if (a.lse)
+          a.lse[(long long)head * a.q_rows + seg.q0 + i] =
+              l > 0.f || l != l ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+      }
+      if (whole) {
+        // whole rows out of the staged tile: D / 8 lanes of 16 bytes to a row; each warp its own 32 rows
+        __syncwarp();
+        constexpr int per = 32 / (D / 8);
+        for (int rr = lane / (D / 8); rr < 32; rr += per) {
+          const int srow = quad * 32 + rr, sr = srow / G, sg = srow - sr * G, c = lane % (D / 8);
+          const int si = seg.tile * NT * rpt + (NT == 2 ? t * rpt : 0) + sr;
+          if (sr >= rpt || si >= seg.nq) continue;
+          const uint4 v = *reinterpret_cast<const uint4*>(stage + srow * (D * 2) + ((c ^ (srow & 7)) << 4));
+          *reinterpret_cast<uint4*>(a.o + (seg.q0 + si) * a.o_row + (kvh * G + sg) * a.o_head + c * 8) = v;
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem_base, 512);
+}
+
+// The parts of a split key range joined, a warp per (row, head): weights 2^(m_z - max m), parts without a key skipped
+// (their sums were never written).
+template <int D>
+__global__ void __launch_bounds__(256) packed_join_kernel(const __grid_constant__ PackedParams p) {
+  constexpr int V = D / 32;
+  const dit_packed_attention& a = p.a;
+  pdl_wait();
+  pdl_trigger();
+  const long long unit = (long long)blockIdx.x * 8 + (threadIdx.x >> 5), units = (long long)a.q_rows * a.heads;
+  if (unit >= units) return;
+  const int q = int(unit / a.heads), head = int(unit - (long long)q * a.heads), lane = lane_id();
+  if (a.q_start) {  // rows of no segment stay as they are
+    const int first = max(__ldg(a.q_start), 0), end = min(__ldg(a.q_start + a.segments), a.q_rows);
+    if (q < first || q >= end) return;
+  }
+  float2 ml = make_float2(-INFINITY, 0.f);
+  if (lane < p.splits) ml = p.part_ml[((long long)lane * a.q_rows + q) * a.heads + head];
+  float top = ml.x;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const float w = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - top);
+  float l = w * ml.y;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+  const unsigned some = __ballot_sync(0xffffffffu, ml.x != -INFINITY);
+  float acc[V] = {};
+#pragma unroll 4
+  for (int z = 0; z < p.splits; ++z) {
+    const float wz = __shfl_sync(0xffffffffu, w, z);
+    if (!((some >> z) & 1u)) continue;
+    const float* src = p.part_o + (((long long)z * a.q_rows + q) * a.heads + head) * D + lane * V;
+    if constexpr (V == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(src);
+      acc[0] = fmaf(v.x, wz, acc[0]); acc[1] = fmaf(v.y, wz, acc[1]);
+      acc[2] = fmaf(v.z, wz, acc[2]); acc[3] = fmaf(v.w, wz, acc[3]);
+    } else {
+      const float2 v = *reinterpret_cast<const float2*>(src);
+      acc[0] = fmaf(v.x, wz, acc[0]); acc[1] = fmaf(v.y, wz, acc[1]);
+    }
+  }
+  uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + q * a.o_row + head * a.o_head + lane * V);
+#pragma unroll
+  for (int v = 0; v < V / 2; ++v) dst[v] = pack_bf16x2(acc[2 * v] * inv, acc[2 * v + 1] * inv);
+  if (a.lse && lane == 0)
+    a.lse[(long long)head * a.q_rows + q] = l > 0.f || l != l ? (top + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
+// Tiles, CTAs and key splits of a call. Segments of few rows (no more than a tile holds, on average) take one tile per
+// CTA. The key range is split where the tiles leave SMs idle: one wave's worth for whole tiles, several for single
+// rows, whose segments are of unlike length; never below four key tiles to a part of an average segment.
+struct PackedPlan {
+  int G, rpt, nt, splits;
+  long long tiles;
+  size_t part_bytes;
+};
+PackedPlan packed_plan(int q_rows, int k_rows, int segments, int heads, int kv_heads, int d) {
+  PackedPlan r{};
+  r.G = heads / kv_heads;
+  r.rpt = 128 / r.G;
+  r.nt = (long long)q_rows <= (long long)segments * r.rpt ? 1 : 2;
+  const long long rows = (long long)r.nt * r.rpt;
+  r.tiles = std::min<long long>((q_rows + segments * (rows - 1)) / rows, q_rows);
+  const long long units = r.tiles * kv_heads, sms = std::max(num_sms(), 1);
+  const long long key_tiles = (k_rows / segments + 127) / 128;
+  const long long want = r.nt == 1 ? (4 * sms + units - 1) / units : sms / units;
+  r.splits = int(std::max<long long>(1, std::min<long long>({want, key_tiles / 4, (long long)kMaxSplits})));
+  r.part_bytes = r.splits > 1 ? (size_t(r.splits) * q_rows * heads * (size_t(d) * 4 + 8) + 255) / 256 * 256 : 0;
+  return r;
+}
+
+bool packed_map(CUtensorMap* m, const void* base, int d, int heads, int rows, long long head, long long row, int box_heads,
+                int box_rows) {
+  EncodeTiledFn fn = encode_tiled_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {cuuint64_t(d), cuuint64_t(heads), cuuint64_t(rows)};
+  cuuint64_t strides[2] = {cuuint64_t(heads > 1 ? head : d) * 2, cuuint64_t(rows > 1 ? row : d) * 2};
+  cuuint32_t box[3] = {64, cuuint32_t(box_heads), cuuint32_t(box_rows)}, estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int NT, bool GEN>
+int packed_go(const PackedParams& p, const PackedPlan& pl, cudaStream_t st) {
+  using Cfg = PackedCfg<D, NT>;
+  const dit_packed_attention& a = p.a;
+  CUtensorMap tq, tk, tv;
+  const bool keys = a.k_rows > 0;  // none: the maps are not read
+  if (!packed_map(&tq, a.q, D, a.heads, a.q_rows, a.q_head, a.q_row, pl.G, pl.rpt) ||
+      !packed_map(&tk, keys ? a.k : a.q, D, a.kv_heads, keys ? a.k_rows : 1, keys ? a.k_head : a.q_head, a.k_row, 1, 128) ||
+      !packed_map(&tv, keys ? a.v : a.q, D, a.kv_heads, keys ? a.k_rows : 1, keys ? a.v_head : a.q_head, a.v_row, 1, 128))
+    return DIT_ECUDA;
+  auto kern = packed_kernel<D, NT, GEN>;
+  if (!smem_attr_once(reinterpret_cast<const void*>(kern), Cfg::kSmem)) return DIT_ECUDA;
+  if (launch_pdl(kern, dim3(unsigned(pl.tiles), unsigned(a.kv_heads), unsigned(p.splits)), dim3(kPackedThreads), Cfg::kSmem,
+                 st, 1, tq, tk, tv, p) != cudaSuccess)
+    return DIT_ECUDA;
+  if (p.splits > 1) {
+    const long long units = (long long)a.q_rows * a.heads;
+    if (launch_pdl(packed_join_kernel<D>, dim3(unsigned((units + 7) / 8)), dim3(256), 0, st, 1, p) != cudaSuccess) return DIT_ECUDA;
+  }
+  return cudaGetLastError() == cudaSuccess ? DIT_OK : DIT_ECUDA;
+}
+
+template <int D>
+int packed_kind(const PackedParams& p, const PackedPlan& pl, cudaStream_t st) {
+  const bool gen = p.cap_out > 0.f || p.a.slope;
+  if (pl.nt == 1) return gen ? packed_go<D, 1, true>(p, pl, st) : packed_go<D, 1, false>(p, pl, st);
+  return gen ? packed_go<D, 2, true>(p, pl, st) : packed_go<D, 2, false>(p, pl, st);
+}
+
+bool packed_al16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+bool packed_al4(const void* p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; }
+
+int packed_sizes(int q_rows, int k_rows, int segments, int heads, int kv_heads, int d) {
+  if (q_rows < 0 || k_rows < 0 || segments < 0 || heads < 1 || kv_heads < 1 || d < 1) return DIT_EINVAL;
+  if ((d != 64 && d != 128) || heads % kv_heads != 0 || heads / kv_heads > 128 || kv_heads > 65535) return DIT_EUNSUPPORTED;
+  // coordinates of a tile's rows stay within 32 bits; a join has a warp per row and head
+  if (q_rows > INT_MAX - 256 || k_rows > INT_MAX - 256 || (long long)q_rows * heads > (1LL << 33)) return DIT_EUNSUPPORTED;
+  return DIT_OK;
+}
+
+}  // namespace
+}  // namespace dit
+
+using namespace dit;
+
+extern "C" {
+
+size_t dit_attention_packed_workspace_bytes(int q_rows, int k_rows, int segments, int heads, int kv_heads, int head_dim) {
+  if (packed_sizes(q_rows, k_rows, segments, heads, kv_heads, head_dim) != DIT_OK || q_rows == 0 || segments == 0) return 0;
+  return packed_plan(q_rows, k_rows, segments, heads, kv_heads, head_dim).part_bytes;
+}
+
+}  // extern "C"
+
+namespace dit {
+
+int packed_attention_launch(const dit_packed_attention& a, void* ws, size_t ws_bytes, int* err, cudaStream_t st) {
+  PackedPlan pl = packed_plan(a.q_rows, a.k_rows, a.segments, a.heads, a.kv_heads, a.head_dim);
+  PackedParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.a = a;
+  p.G = pl.G;
+  p.rpt = pl.rpt;
+  p.splits = pl.splits > 1 && ws && ws_bytes >= pl.part_bytes ? pl.splits : 1;
+  p.part_o = static_cast<float*>(ws);
+  p.part_ml = reinterpret_cast<float2*>(p.part_o + size_t(p.splits) * a.q_rows * a.heads * a.head_dim);
+  const double log2e = 1.4426950408889634;
+  p.scale_log2 = float(a.scale * log2e);
+  if (a.cap > 0.f) {
+    p.cap_in = float(2.0 * a.scale * log2e / a.cap);
+    p.cap_out = float(a.cap * log2e);
+  }
+  p.err = err;
+  return a.head_dim == 64 ? packed_kind<64>(p, pl, st) : packed_kind<128>(p, pl, st);
+}
+
+int packed_attention_check(const dit_packed_attention* a, const void* ws) {
+  if (!a) return DIT_EINVAL;
+  const int rc = packed_sizes(a->q_rows, a->k_rows, a->segments, a->heads, a->kv_heads, a->head_dim);
+  if (rc != DIT_OK) return rc;
+  if (!(a->scale > 0.f) || !std::isfinite(a->scale) || !(a->cap >= 0.f) || !std::isfinite(a->cap)) return DIT_EINVAL;
+  if (a->q_rows == 0 || a->segments == 0) return DIT_OK;
+  if (a->segments > 1 && (!a->q_start || !a->k_start)) return DIT_EINVAL;
+  if ((a->q_start == nullptr) != (a->k_start == nullptr)) return DIT_EINVAL;
+  if (!packed_al4(a->q_start) || !packed_al4(a->k_start) || !packed_al4(a->visible) || !packed_al4(a->slope) ||
+      !packed_al4(a->lse) || !packed_al16(ws))
+    return DIT_EINVAL;
+  struct Side {
+    const void* p;
+    long long row, head;
+    int rows, heads;
+  } side[4] = {{a->q, a->q_row, a->q_head, a->q_rows, a->heads},
+               {a->k, a->k_row, a->k_head, a->k_rows, a->kv_heads},
+               {a->v, a->v_row, a->v_head, a->k_rows, a->kv_heads},
+               {a->o, a->o_row, a->o_head, a->q_rows, a->heads}};
+  for (const Side& s : side) {
+    if (s.rows == 0) continue;
+    if (!s.p || !packed_al16(s.p)) return DIT_EINVAL;
+    // tensor maps take strides of whole 16 bytes, above zero and below 2^40 bytes
+    if (s.rows > 1 && (s.row < 8 || s.row % 8 || s.row >= 1LL << 39)) return DIT_EINVAL;
+    if (s.heads > 1 && (s.head < 8 || s.head % 8 || s.head >= 1LL << 39)) return DIT_EINVAL;
+  }
+  if (a->o == a->q || a->o == a->k || a->o == a->v) return DIT_EINVAL;
+  return DIT_OK;
+}
+
+}  // namespace dit

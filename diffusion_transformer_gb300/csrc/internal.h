@@ -134,6 +134,10 @@ int attention_launch(const AttnParams& p, cudaStream_t stream);
 // Scratch the persistent schedule wants for R rows (0: it is not used for this shape).
 size_t attention_part_bytes(int R, int heads, int head_dim);
 
+// Attention over packed sequences: the checks of a call (no CUDA state touched) and its launches.
+int packed_attention_check(const dit_packed_attention* a, const void* ws);
+int packed_attention_launch(const dit_packed_attention& a, void* ws, size_t ws_bytes, int* err, cudaStream_t stream);
+
 // ------------------------------------------------------------------------------------------
 // elementwise / row kernels
 // ------------------------------------------------------------------------------------------

@@ -682,6 +682,38 @@ DIT_API int dit_attention_qknorm(const dit_dims* dims, int R, const uint16_t* q,
                                  const float* q_norm, const float* k_norm, uint16_t* o, void* ws, size_t ws_bytes,
                                  dit_stream_t stream);
 
+/* Attention over packed sequences (the pages attend over one sequence without a mask [klein, section 4.3]; this one is for
+ * batches of unlike lengths, padded or causal rows, grouped key heads, and new rows over cached keys). Segment s has the query
+ * rows q_start[s] .. q_start[s + 1] - 1 and the keys k_start[s] .. k_start[s + 1] - 1 (device arrays of segments + 1 int32, not
+ * decreasing; both NULL: one segment of all rows). Row i of a segment of nq rows and nk keys sees its keys j < c,
+ * c = visible[row] clamped to [0, nk] (device [q_rows] int32, NULL: nk): padded keys, prefixes, causal rows (i + 1 + nk - nq),
+ * frames that see the frames before them. Per query head h, its key head being h / (heads / kv_heads):
+ *   x_ij = cap * tanh(scale * q_i.k_j / cap) - slope[h] * |i + nk - nq - j|
+ * (cap = 0: scale * q_i.k_j itself; slope fp32 [heads], NULL: none),
+ *   o_i = sum_j softmax_j(x_ij) v_j,   lse[h, row] = ln sum_j exp(x_ij)   (fp32 [heads, q_rows], NULL: not wanted)
+ * A row that sees nothing has o = 0 and lse = -inf. Rows of o and lse outside every segment are not written. NaN and infinities
+ * in keys and values that a row does not see do not reach it. Value j of head h of row r is at [r * *_row + h * *_head + j]
+ * (strides in values, positive multiples of 8 where there is more than one; pointers 16-byte aligned); q, k and v may be columns
+ * of one product. bf16 in and out; scores, softmax and sums in fp32, the weights rounded to bf16 for the product with V.
+ * head_dim 64 or 128; heads a multiple of kv_heads, at most 128 times it. scale > 0, cap >= 0, finite. o must not overlap
+ * the inputs. ws: optional scratch of dit_attention_packed_workspace_bytes (16-byte aligned) for splitting long key ranges
+ * over the SMs where there are few rows (0 bytes where that does not pay); with it a result differs by the order of fp32 additions only.
+ * q_rows = 0 or segments = 0: nothing to do. */
+typedef struct {
+  const uint16_t *q, *k, *v;
+  uint16_t* o;
+  float* lse;
+  const int32_t *q_start, *k_start, *visible;
+  const float* slope;
+  long long q_row, q_head, k_row, k_head, v_row, v_head, o_row, o_head;
+  int q_rows, k_rows, segments;
+  int heads, kv_heads, head_dim;
+  float scale, cap;
+} dit_packed_attention;
+DIT_API int dit_attention_packed(const dit_packed_attention* a, void* ws, size_t ws_bytes, dit_stream_t stream);
+DIT_API size_t dit_attention_packed_workspace_bytes(int q_rows, int k_rows, int segments, int heads, int kv_heads,
+                                                    int head_dim);
+
 /* Linear with gated residual [gizai:dit, gatedInto]: x[r] += gate[map[r]] * (a[r] W^T) for the
  * attention (which = 0, W = wout [H, H], a [R, H]) or the MLP (which = 1, W = wdown [H, F],
  * a [R, F]) gate of the modulation rows. x rows < L in txt, others in img.

@@ -22,3 +22,4 @@ from .w8a8 import *  # noqa: F401,F403
 from .fp4 import block_forward_fp4_rows, e4m3_values, fp4_linear_f, fp4_pack, fp4_quantize, fp4_values  # noqa: F401
 from .rotary import (qknorm_rotary, qknorm_rotary_gradient, rotary_apply, rotary_frequencies,  # noqa: F401
                      rotary_tables)  # noqa: F401
+from .packed import attention_packed  # noqa: F401
