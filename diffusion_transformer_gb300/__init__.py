@@ -33,7 +33,7 @@ __all__ = [
     "Fp4BlockWeights", "dit_block_forward_fp4", "dit_block_fp4_workspace_bytes",
     "dit_denoise", "dit_block_forward_noalloc", "dit_block_noalloc_max_bytes", "dit_workspace_bytes", "dit_denoise_workspace_bytes", "dit_modnorm", "dit_qkv_rope",
     "dit_vt_stride", "dit_stream_k_workspace_bytes", "dit_attention", "dit_attention_packed", "dit_attention_packed_workspace_bytes", "dit_attention_qknorm", "dit_attention_workspace_bytes", "dit_linear_gated", "dit_linear_swiglu", "dit_linear",
-    "dit_dequant_int8", "dit_linear_int8", "dit_linear_int8_workspace_bytes", "dit_check", "dit_selftest_bounded_wait", "dit_status_string", "dit_version",
+    "dit_dequant_int8", "dit_linear_epilogue", "dit_linear_epilogue_workspace_bytes", "dit_linear_int8", "dit_linear_int8_workspace_bytes", "dit_check", "dit_selftest_bounded_wait", "dit_status_string", "dit_version",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -118,6 +118,11 @@ class dit_packed_attention(ctypes.Structure):
                 [(n, c_longlong) for n in ("q_row", "q_head", "k_row", "k_head", "v_row", "v_head", "o_row", "o_head")] +
                 [(n, c_int) for n in ("q_rows", "k_rows", "segments", "heads", "kv_heads", "head_dim")] +
                 [("scale", c_float), ("cap", c_float)])
+
+
+class dit_epilogue(ctypes.Structure):
+    _fields_ = [("bias", c_void_p), ("gate", c_void_p), ("gate_map", c_void_p), ("residual", c_void_p),
+                ("ld_gate", c_longlong), ("ld_residual", c_longlong), ("gate_rows", c_int), ("activation", c_int)]
 
 
 class dit_fp4_matrix(ctypes.Structure):
@@ -235,6 +240,9 @@ _SIGNATURES = {
     "dit_linear_swiglu": (c_int, [POINTER(dit_dims), c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_size_t,
                                   c_void_p]),
     "dit_linear": (c_int, [c_void_p, c_int, c_int, c_void_p, c_int, c_void_p, c_int, c_void_p]),
+    "dit_linear_epilogue": (c_int, [c_void_p, c_int, c_longlong, c_int, c_void_p, c_int, c_longlong, c_void_p, c_void_p,
+                                    c_int, c_longlong, c_void_p, c_size_t, c_void_p]),
+    "dit_linear_epilogue_workspace_bytes": (c_size_t, [c_int, c_int, c_int]),
     "dit_dequant_int8": (c_int, [c_void_p, c_void_p, c_int64, c_int64, c_void_p, c_void_p]),
     "dit_linear_int8": (c_int, [c_void_p, c_int, c_int, c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_size_t,
                                 c_void_p]),
@@ -1182,6 +1190,59 @@ def dit_linear(a, w, out, stream=None):
     out_bf16 = 1 if out.dtype != torch.float32 else 0
     _ok(lib().dit_linear(_ptr(a, bf, "a"), M, K, _ptr(w, bf, "w"), N, _ptr(out, None, "out"), out_bf16,
                          _stream(stream)), "dit_linear")
+
+
+def dit_linear_epilogue_workspace_bytes(M: int, N: int, K: int) -> int:
+    _fits(M, N, K)
+    return lib().dit_linear_epilogue_workspace_bytes(M, N, K)
+
+
+_epilogue_struct = struct.Struct("@PPPPqqii")  # dit_epilogue
+_activations = {"none": 0, "silu": 1, "gelu": 2, "gelu_tanh": 3}
+
+
+def dit_linear_epilogue(a, w, out, bias=None, activation: str = "none", gate=None, gate_map=None, residual=None, ws=None,
+                        stream=None):
+    """out = residual + gate[gate_map] * act(a w^T + bias): a [M, K], w [N, K] bf16, out and residual [M, N] bf16 or fp32 (rows
+    may be strided; residual may be out), bias [N], gate [rows, N] fp32, gate_map [M] int32, each of them or None; activation
+    "none", "silu", "gelu" or "gelu_tanh". ws: scratch of dit_linear_epilogue_workspace_bytes or None."""
+    dev, st = _current(stream)
+    torch = _torch_mod
+    act = _activations.get(activation)
+    if act is None:
+        raise ValueError(f"activation: expected one of {', '.join(_activations)}")
+    if a.dim() != 2 or w.dim() != 2:
+        raise ValueError("a, w: expected matrices")
+    (M, K), N = a.shape, w.shape[0]
+    _fits(M, K, N)
+    pa, ka, lda = _matrix(a, M, K, dev, "a")
+    pw, kw, ldw = _matrix(w, N, K, dev, "w")
+    if ka != DIT_BF16 or kw != DIT_BF16:
+        raise TypeError("a, w: expected bfloat16")
+    po, ko, ldo = _matrix(out, M, N, dev, "out")
+    pr = ldr = pg = ldg = rows = 0
+    if residual is not None:
+        pr, kr, ldr = _matrix(residual, M, N, dev, "residual")
+        if kr != ko:
+            raise TypeError("residual: expected the output's type")
+    if gate is not None:
+        rows = gate.shape[0]
+        _fits(rows)
+        pg, kg, ldg = _matrix(gate, rows, N, dev, "gate")
+        if kg != DIT_F32 or rows < 1:
+            raise TypeError("gate: expected float32 [rows, N]")
+        if gate_map is None and rows != 1:
+            raise ValueError("gate_map: expected with more than one gate row")
+    elif gate_map is not None:
+        raise ValueError("gate_map: without a gate")
+    if ws is not None and (ws.get_device() != dev or not ws.is_contiguous()):
+        raise ValueError("ws: expected a contiguous CUDA tensor on the current device")
+    e = _epilogue_struct.pack(_dense(bias, torch.float32, N, "bias", dev), pg, _dense(gate_map, torch.int32, M, "gate_map", dev),
+                              pr, ldg, ldr, rows, act)
+    rc = lib().dit_linear_epilogue(pa, M, lda, K, pw, N, ldw, e, po, ko, ldo, None if ws is None else ws.data_ptr(),
+                                   0 if ws is None else ws.numel() * ws.element_size(), st)
+    if rc:
+        _ok(rc, "dit_linear_epilogue")
 
 
 def dit_linear_int8_workspace_bytes(N: int, K: int) -> int:

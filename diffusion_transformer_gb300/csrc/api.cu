@@ -1639,6 +1639,49 @@ int dit_linear(const uint16_t* a, int M, int K, const uint16_t* w, int N, void* 
                      reinterpret_cast<cudaStream_t>(stream));
 }
 
+size_t dit_linear_epilogue_workspace_bytes(int M, int N, int K) {
+  return M < 1 || N < 1 || K < 1 || K % 8 != 0 ? 0 : gemm_full_scratch_bytes(M, N, K);
+}
+
+int dit_linear_epilogue(const uint16_t* a, int M, long long lda, int K, const uint16_t* w, int N, long long ldw,
+                        const dit_epilogue* e, void* out, int out_type, long long ldo, void* ws, size_t ws_bytes,
+                        dit_stream_t stream) {
+  if (!e || M < 0 || N < 0 || K < 1 || (out_type != DIT_BF16 && out_type != DIT_F32)) return DIT_EINVAL;
+  if (e->activation < DIT_ACT_NONE || e->activation > DIT_ACT_GELU_TANH) return DIT_EINVAL;
+  if (K % 8 != 0 || M > kFp4MaxSize || N > kFp4MaxSize || K > kFp4MaxSize) return DIT_EUNSUPPORTED;
+  if (M == 0 || N == 0) return DIT_OK;
+  const int size = out_type == DIT_BF16 ? 2 : 4;
+  auto on = [](const void* p, int n) { return reinterpret_cast<uintptr_t>(p) % n == 0; };
+  if (!a || !w || !out || !al16(a) || !al16(w) || !on(out, size) || (ws && !al16(ws))) return DIT_EINVAL;
+  // strides that tensor maps take: whole 16 bytes, below 2^40; rows that do not run into each other
+  auto ld_ok = [&](long long ld, int rows) { return rows == 1 || (ld >= K && ld % 8 == 0 && ld < (1LL << 39)); };
+  if (!ld_ok(lda, M) || !ld_ok(ldw, N) || (M > 1 && ldo < N)) return DIT_EINVAL;
+  if (!on(e->bias, 4) || !on(e->gate, 4) || !on(e->gate_map, 4) || !on(e->residual, size)) return DIT_EINVAL;
+  if (e->gate && (e->gate_rows < 1 || (e->gate_rows > 1 && e->ld_gate < N))) return DIT_EINVAL;
+  if (e->residual && M > 1 && e->ld_residual < N) return DIT_EINVAL;
+  if (e->residual == out && M > 1 && e->ld_residual != ldo) return DIT_EINVAL;
+  if (out == static_cast<const void*>(a) || out == static_cast<const void*>(w)) return DIT_EINVAL;
+  int* err = err_word();
+  if (!err) return DIT_ECUDA;
+  GemmParams g = base_params(M, N, K, err);
+  g.out = out;
+  g.out_f32 = out_type == DIT_F32;
+  g.ldo = ldo;
+  g.bias = e->bias;
+  g.activation = e->activation;
+  g.gate = e->gate;
+  g.map = e->gate ? e->gate_map : nullptr;
+  g.gate_stride = e->ld_gate;
+  g.gate_rows = e->gate_rows;
+  g.residual = e->residual;
+  g.ldr = e->ld_residual;
+  const int quad = 4 * size;
+  g.vec = on(out, quad) && on(e->residual, quad) && on(e->bias, 16) && on(e->gate, 16) && (M == 1 || ldo % 4 == 0) &&
+          (!e->residual || M == 1 || e->ld_residual % 4 == 0) && (!e->gate || e->gate_rows == 1 || e->ld_gate % 4 == 0);
+  return gemm_full_launch(a, M == 1 ? (K + 7) / 8 * 8 : lda, w, N == 1 ? K : ldw, g, ws, ws_bytes,
+                          reinterpret_cast<cudaStream_t>(stream));
+}
+
 size_t dit_linear_int8_workspace_bytes(int N, int K) {
   if (N < 1 || K < 1) return 0;
   return gemm_int8_scratch_bytes(N, K);

@@ -22,6 +22,8 @@
 //   kEpiQKV     per-head RMS norm * weight, rotary pairs (2i, 2i+1), head-major q/k stores and a
 //               transposed v store for the attention kernel (klein article, section 4.4)
 //   kEpiQKVSwiGLU  kEpiQKV on the columns below n_split, kEpiSwiGLU above (the parallel block)
+//   kEpiFull    residual + gate * act(acc + bias), any of them left out, any N (checkpoints with biases)
+#include <algorithm>
 #include <atomic>
 #include <mutex>
 
@@ -99,9 +101,76 @@ __device__ __forceinline__ void store_bf16x32(uint16_t* dst, const float* v) {
 // 4 KB shared-memory scratch (the transposed v store, the gated residual's transpose). BN here is
 // the warp's column count.
 // ----------------------------------------------------------------------------------------------
+// The activations of kEpiFull. exp and erf are CUDA's full-precision ones; the sigmoid's quotient is within 2 units.
+__device__ __forceinline__ float activate(float y, int kind) {
+  switch (kind) {
+    case DIT_ACT_SILU: return __fdividef(y, 1.f + expf(-y));
+    case DIT_ACT_GELU: return 0.5f * y * (1.f + erff(y * 0.70710678118654752f));
+    case DIT_ACT_GELU_TANH:  // y (1 + tanh u) / 2 = y / (1 + e^-2u)
+      return __fdividef(y, 1.f + expf(-1.5957691216057308f * fmaf(0.044715f * y * y, y, y)));
+    default: return y;
+  }
+}
+
+// Four consecutive values of a row of out (or residual), fp32 or bf16
+__device__ __forceinline__ float4 full_load4(const void* base, long long at, int f32) {
+  if (f32) return *reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
+  const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + at);
+  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                     __uint_as_float(u.y & 0xffff0000u));
+}
+__device__ __forceinline__ float full_load1(const void* base, long long at, int f32) {
+  return f32 ? static_cast<const float*>(base)[at] : __uint_as_float(uint32_t(static_cast<const uint16_t*>(base)[at]) << 16);
+}
+
+// kEpiFull on four consecutive columns n .. n + 3 of one row, a the products' sums: `whole` with vector accesses (p.vec and
+// n + 3 < N), else value by value up to N. res: the residual's values (whole rows only, loaded ahead).
+__device__ __forceinline__ void full_store4(const GemmParams& p, int row, int n, float4 a, float4 bias, float4 res,
+                                            const float* gate, bool whole) {
+  const long long at = (long long)row * p.ldo + n;
+  if (whole) {
+    float v[4] = {activate(a.x + bias.x, p.activation), activate(a.y + bias.y, p.activation),
+                  activate(a.z + bias.z, p.activation), activate(a.w + bias.w, p.activation)};
+    if (gate) {
+      const float4 g = __ldg(reinterpret_cast<const float4*>(gate + n));
+      v[0] *= g.x; v[1] *= g.y; v[2] *= g.z; v[3] *= g.w;
+    }
+    if (p.residual) {
+      v[0] += res.x; v[1] += res.y; v[2] += res.z; v[3] += res.w;
+    }
+    if (p.out_f32) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
+    else
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    return;
+  }
+  const float in[4] = {a.x, a.y, a.z, a.w}, b[4] = {bias.x, bias.y, bias.z, bias.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (n + j >= p.N) break;
+    float v = activate(in[j] + b[j], p.activation);
+    if (gate) v *= __ldg(gate + n + j);
+    if (p.residual) v += full_load1(p.residual, (long long)row * p.ldr + n + j, p.out_f32);
+    if (p.out_f32) static_cast<float*>(p.out)[at + j] = v;
+    else static_cast<uint16_t*>(p.out)[at + j] = uint16_t(pack_bf16x2(v, 0.f));
+  }
+}
+__device__ __forceinline__ const float* full_gate(const GemmParams& p, int row) {
+  return p.gate + (p.map ? min(max(__ldg(p.map + row), 0), p.gate_rows - 1) : 0) * p.gate_stride;
+}
+__device__ __forceinline__ float4 full_bias4(const GemmParams& p, int n) {
+  float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (!p.bias) return b;
+  if (p.vec && n + 3 < p.N) return __ldg(reinterpret_cast<const float4*>(p.bias + n));
+  if (n < p.N) b.x = __ldg(p.bias + n);
+  if (n + 1 < p.N) b.y = __ldg(p.bias + n + 1);
+  if (n + 2 < p.N) b.z = __ldg(p.bias + n + 2);
+  if (n + 3 < p.N) b.w = __ldg(p.bias + n + 3);
+  return b;
+}
+
 template <int BN, int EPI, bool kRowPerThread>
 __device__ __forceinline__ void epilogue_tile(const GemmParams& p, uint32_t taddr, int row0, int row_end, int lane,
-                                              int n0, uint8_t* stage) {
+                                              int n0, uint8_t* stage, int part = 0) {
   const int row = row0 + lane;
   const bool row_ok = row < row_end;
   if constexpr (EPI == kEpiQKV) {
@@ -358,6 +427,47 @@ __device__ __forceinline__ void epilogue_tile(const GemmParams& p, uint32_t tadd
           }
       }
     }
+  } else if constexpr (EPI == kEpiFull) {
+    // Chunks of 32 columns go through the warp's shared tile as in the gated epilogue: a lane then holds four columns
+    // of the rows (lane >> 3) + 4 i, so a warp instruction moves four whole lines of out, residual or gate, and a lane's bias is one load.
+    // The residual is loaded before the accumulator is waited for.
+    const int cq = lane & 7;
+#pragma unroll 1
+    for (int c = 0; c < BN / 32; ++c) {
+      if (n0 + c * 32 >= p.N) break;  // the same for the warp
+      const int n = n0 + c * 32 + cq * 4;
+      const bool whole = p.vec && n + 3 < p.N;
+      float4 res[8];
+      const float4 bias = full_bias4(p, n);
+      if (p.residual && whole && p.k_parts <= 1) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = row0 + (lane >> 3) + 4 * i;
+          if (r < row_end) res[i] = full_load4(p.residual, (long long)r * p.ldr + n, p.out_f32);
+        }
+      }
+      uint32_t v[32];
+      tmem_ld32(taddr + c * 32, v);
+      tmem_ld_wait();
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        *reinterpret_cast<uint4*>(stage + lane * 128 + ((q ^ (lane & 7)) << 4)) =
+            make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int rl = (lane >> 3) + 4 * i, r = row0 + rl;
+        const float4 a = *reinterpret_cast<const float4*>(stage + rl * 128 + ((cq ^ (rl & 7)) << 4));
+        if (r >= row_end || n >= p.N) continue;
+        if (p.k_parts > 1) {
+          *reinterpret_cast<float4*>(p.parts + ((long long)part * p.M + r) * p.parts_ld + n) = a;  // parts_ld % 4 == 0
+          continue;
+        }
+        const float* gate = p.gate ? full_gate(p, r) : nullptr;
+        full_store4(p, r, n, a, bias, res[i], gate, whole);
+      }
+      __syncwarp();
+    }
   } else {
 #pragma unroll 1
     for (int c = 0; c < BN / 32; ++c) {
@@ -460,11 +570,18 @@ __host__ __device__ __forceinline__ int sk_segments(const GemmParams& p, int u, 
   return a1 > a0 ? (a1 - 1) / KB - a0 / KB + 1 : 0;
 }
 __host__ __device__ __forceinline__ int unit_items(const GemmParams& p, int u, int units, int tiles, int KB) {
-  if (p.sk_tiles <= 0) return u < tiles ? (tiles - u + units - 1) / units : 0;
+  if (p.sk_tiles <= 0) {
+    const int all = p.k_parts > 1 ? tiles * p.k_parts : tiles;
+    return u < all ? (all - u + units - 1) / units : 0;
+  }
   return sk_segments(p, u, KB) + (tiles - p.sk_tiles) / units;
 }
 __host__ __device__ __forceinline__ WorkItem unit_item(const GemmParams& p, int u, int i, int units, int tiles,
                                                        int KB) {
+  if (p.k_parts > 1) {  // item x is part x / tiles (in trel) of tile x % tiles
+    const int x = u + i * units, z = x / tiles;
+    return WorkItem{x - z * tiles, int((long long)KB * z / p.k_parts), int((long long)KB * (z + 1) / p.k_parts), -1, 1, 0, z};
+  }
   if (p.sk_tiles <= 0) return WorkItem{u + i * units, 0, KB, -1, 1, 0, 0};
   const int nseg = sk_segments(p, u, KB);
   if (i >= nseg) return WorkItem{u + (i - nseg) * units, 0, KB, -1, 1, 0, 0};
@@ -632,7 +749,7 @@ __global__ void __launch_bounds__(GemmCfg<BN, B8, PAIR>::kThreads, 1)
   const int unit = PAIR ? int(blockIdx.x >> 1) : int(blockIdx.x);
   const int units = PAIR ? int(gridDim.x >> 1) : int(gridDim.x);
   const int num_m = row_tiles(p, Cfg::kTileM);
-  const int num_n = p.N / BN;
+  const int num_n = (p.N + BN - 1) / BN;  // only kEpiFull has a part-filled tile or k-block (read as zeros)
   // Tile order: consecutive tiles share the smaller operand's panel set, so the CTAs running at
   // once keep it in L2 and the larger operand streams from DRAM once. m fastest (A resident) when A
   // is the smaller operand, n fastest (B resident) otherwise.
@@ -647,7 +764,7 @@ __global__ void __launch_bounds__(GemmCfg<BN, B8, PAIR>::kThreads, 1)
     }
   };
   const int tiles = num_m * num_n;
-  const int KB = p.K / BK;
+  const int KB = (p.K + BK - 1) / BK;
   const int items = unit_items(p, unit, units, tiles, KB);  // this unit's work items
 
   if (threadIdx.x == 0) {
@@ -914,7 +1031,7 @@ __global__ void __launch_bounds__(GemmCfg<BN, B8, PAIR>::kThreads, 1)
           else
             epilogue_tile<Cfg::kEpiCols, kEpiSwiGLU, B8>(p, taddr, row0, tr.end, lane, n0 - p.n_split, stage);
         } else {
-          epilogue_tile<Cfg::kEpiCols, EPI, B8>(p, taddr, row0, tr.end, lane, n0, stage);
+          epilogue_tile<Cfg::kEpiCols, EPI, B8>(p, taddr, row0, tr.end, lane, n0, stage, w.trel);
         }
       }
       tc_fence_before();
@@ -1061,9 +1178,9 @@ int launch_one(const Maps& m, const GemmParams& p, cudaStream_t stream) {
   if (units_cached[dev] <= 0)
     units_cached[dev] = resident_units(reinterpret_cast<const void*>(kern), PAIR, Cfg::kThreads, Cfg::kSmemBytes);
   const int units_max = units_cached[dev];
-  const int tiles = row_tiles(p, Cfg::kTileM) * (p.N / BN);
+  const int tiles = row_tiles(p, Cfg::kTileM) * ((p.N + BN - 1) / BN) * (EPI == kEpiFull && p.k_parts > 1 ? p.k_parts : 1);
   GemmParams q = p;
-  if constexpr (!B8) plan_stream_k(q, tiles, units_max, PAIR ? 2 : 1, BN);
+  if constexpr (!B8 && EPI != kEpiFull) plan_stream_k(q, tiles, units_max, PAIR ? 2 : 1, BN);
   else q.sk_tiles = 0;
   const int units = q.sk_tiles > 0 ? units_max : (tiles < units_max ? tiles : units_max);
   if constexpr (PAIR) {
@@ -1088,6 +1205,9 @@ int dispatch_epi(int epi, const Maps& m, const GemmParams& p, cudaStream_t strea
     case kEpiQKV: return launch_one<BN, kEpiQKV, B8, PAIR>(m, p, stream);
     case kEpiQKVSwiGLU:
       if constexpr (BN == 256 && !B8) return launch_one<BN, kEpiQKVSwiGLU, B8, PAIR>(m, p, stream);
+      return DIT_EUNSUPPORTED;
+    case kEpiFull:
+      if constexpr (!B8) return launch_one<BN, kEpiFull, B8, PAIR>(m, p, stream);
       return DIT_EUNSUPPORTED;
     default: return DIT_EINVAL;
   }
@@ -1228,6 +1348,96 @@ int gemm_launch_cat(const uint16_t* a, long long lda, const uint16_t* a2, long l
   }
   m.s = m.b;
   return launch_bf16(m, BN, epi, p, pair, stream);
+}
+
+// ----------------------------------------------------------------------------------------------
+// kEpiFull
+// ----------------------------------------------------------------------------------------------
+namespace {
+
+// The epilogue of a product whose k-blocks were divided: the parts of four columns summed in order, a thread each.
+__global__ void __launch_bounds__(256) full_join_kernel(const __grid_constant__ GemmParams p) {
+  pdl_wait();
+  pdl_trigger();
+  const long long quads = (p.N + 3) / 4, x = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (x >= quads * p.M) return;
+  const int row = int(x / quads), n = int(x - row * quads) * 4;
+  const bool whole = p.vec && n + 3 < p.N;
+  const float* src = p.parts + (long long)row * p.parts_ld + n;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int z = 0; z < p.k_parts; ++z) {
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(src + (long long)z * p.M * p.parts_ld));
+    a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
+  }
+  const float4 bias = full_bias4(p, n);
+  float4 res = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (p.residual && whole) res = full_load4(p.residual, (long long)row * p.ldr + n, p.out_f32);
+  const float* gate = p.gate ? full_gate(p, row) : nullptr;
+  full_store4(p, row, n, a, bias, res, gate, whole);
+}
+
+// Tile and division of the k-blocks, by an estimate of time: rounds of work items over the units (SMs, or pairs), each
+// its k-blocks and its epilogue. A k-block costs what its MMAs take or what its bytes take on an SM's share of HBM
+// (44 KB a microsecond), rows past M being free.
+struct FullPlan {
+  int bn, parts;
+  bool pair;
+};
+FullPlan full_plan(int M, int N, int K) {
+  const int KB = (K + BK - 1) / BK, sms = num_sms() > 0 ? num_sms() : 1;
+  struct Shape {
+    int bn, rows;
+    float mma;  // us a k-block
+  };
+  const Shape shapes[] = {{256, 256, 0.40f}, {128, 256, 0.24f}, {128, 128, 0.24f}, {64, 128, 0.16f}};
+  FullPlan best{64, 1, false};
+  float least = 0.f;
+  for (const Shape& s : shapes) {
+    const bool pair = s.rows == 256;
+    if (pair && (M <= BM || sms < 2)) continue;
+    const long long tiles = ((long long)M + s.rows - 1) / s.rows * ((N + s.bn - 1) / s.bn);
+    const long long units = pair ? sms / 2 : sms;
+    const float kb = std::max(s.mma, (float(std::min(M, BM)) + float(pair ? s.bn / 2 : s.bn)) * (BK * 2 / 1024.f) / 44.f);
+    for (int parts = 1; parts <= 32 && (parts == 1 || (tiles * parts <= units && KB / parts >= 4)); ++parts) {
+      const long long rounds = (tiles * parts + units - 1) / units;
+      const float t = rounds * (kb * ((KB + parts - 1) / parts)) + 2.f + (parts > 1 ? 4.f + 0.1f * parts : 0.f);
+      if (least == 0.f || t < least) {
+        least = t;
+        best = FullPlan{s.bn, parts, pair};
+      }
+    }
+  }
+  return best;
+}
+long long parts_ld(int N) { return (N + 3) / 4 * 4; }
+
+}  // namespace
+
+size_t gemm_full_scratch_bytes(int M, int N, int K) {
+  const FullPlan f = full_plan(M, N, K);
+  return f.parts > 1 ? size_t(f.parts) * M * parts_ld(N) * sizeof(float) : 0;
+}
+
+int gemm_full_launch(const uint16_t* a, long long lda, const uint16_t* b, long long ldb, const GemmParams& p0, void* ws,
+                     size_t ws_bytes, cudaStream_t stream) {
+  GemmParams p = p0;
+  const FullPlan f = full_plan(p.M, p.N, p.K);
+  p.k_parts = 1;
+  if (f.parts > 1 && ws && ws_bytes >= gemm_full_scratch_bytes(p.M, p.N, p.K)) {
+    p.k_parts = f.parts;
+    p.parts = static_cast<float*>(ws);
+    p.parts_ld = parts_ld(p.N);
+  }
+  Maps m;
+  if (!tmap_bf16(&m.a, a, p.K, p.M, lda, BM) || !tmap_bf16(&m.b, b, p.K, p.N, ldb, f.pair ? f.bn / 2 : f.bn)) return DIT_ECUDA;
+  m.s = m.a2 = m.a;
+  m.b2 = m.b;
+  const int rc = launch_bf16(m, f.bn, kEpiFull, p, f.pair, stream);
+  if (rc != DIT_OK || p.k_parts <= 1) return rc;
+  const long long threads = (long long)((p.N + 3) / 4) * p.M;
+  if (launch_pdl(full_join_kernel, dim3(unsigned((threads + 255) / 256)), dim3(256), 0, stream, 1, p) != cudaSuccess) return DIT_ECUDA;
+  return cudaGetLastError() == cudaSuccess ? DIT_OK : DIT_ECUDA;
 }
 
 }  // namespace dit

@@ -23,6 +23,7 @@ enum GemmEpilogue : int {
   kEpiSwiGLU = 4,       // out bf16 [M, N/2]: a_j = silu(acc_{2j}) * acc_{2j+1}
   kEpiQKV = 5,          // QK-RMSNorm + RoPE on q/k columns -> q, k [heads, R, d]; v -> vt [heads, d, Rp]
   kEpiQKVSwiGLU = 6,    // columns < n_split as kEpiQKV, the rest as kEpiSwiGLU (parallel block)
+  kEpiFull = 7,         // out = residual + gate[map[r]][n] * act(acc + bias[n]), any N and K (dit_linear_epilogue)
 };
 
 struct GemmParams {
@@ -77,6 +78,17 @@ struct GemmParams {
   // before the epilogue (per-token and per-output-channel scales of integer codes); rows of the
   // second row group (m_split) take w_scale2 when it is given (the second stream's weight scales)
   const float *a_scale, *w_scale, *w_scale2;
+  // kEpiFull: parts left null are left out. ldo and ldr are the row strides of out and residual, both of type out_f32
+  // (1: fp32, 0: bf16); vec: every row of out, residual, gate and bias stands on four values. k_parts > 1: the
+  // k-blocks of a tile are divided over k_parts work items, whose sums go to parts [k_parts][M][parts_ld] (fp32) and
+  // through the epilogue in a kernel of their own.
+  const float* bias;
+  const void* residual;
+  long long ldr;
+  int activation, out_f32, vec, gate_rows;
+  int k_parts;
+  float* parts;
+  long long parts_ld;
 };
 
 // B operand in int8 with one bf16 scale per 32 consecutive K elements (int8lin weights). For row
@@ -102,6 +114,11 @@ int gemm_launch_cat(const uint16_t* a, long long lda, const uint16_t* a2, long l
                     cudaStream_t stream);
 int gemm_launch(const uint16_t* a, long long lda, const uint16_t* b, const GemmInt8B* b8, int epi,
                 const GemmParams& p, cudaStream_t stream);
+// The kEpiFull product: any M and N, K a multiple of 8 (row strides of 16 bytes); k_parts and parts are set here from
+// the caller's scratch (ws may be null: whole tiles). gemm_full_scratch_bytes: what it would use.
+int gemm_full_launch(const uint16_t* a, long long lda, const uint16_t* b, long long ldb, const GemmParams& p, void* ws,
+                     size_t ws_bytes, cudaStream_t stream);
+size_t gemm_full_scratch_bytes(int M, int N, int K);
 // Zero the stream-K arrival counters of the current device (after an aborted launch, which may
 // leave some counted; dit_check does this when it finds the error word set). Synchronous.
 int gemm_clear_stream_k_counters();

@@ -733,6 +733,38 @@ DIT_API int dit_linear_swiglu(const dit_dims* dims, const uint16_t* h2, int R, c
 DIT_API int dit_linear(const uint16_t* a, int M, int K, const uint16_t* w, int N, void* out, int out_bf16,
                dit_stream_t stream);
 
+/* A linear with its whole epilogue, for checkpoints with biases and MLPs without gates (no counterpart on the pages, whose
+ * linears have neither):
+ *   out[r, n] = residual[r, n] + gate[gate_map[r], n] * act(sum_k a[r, k] w[n, k] + bias[n])
+ * with any of residual, gate and bias left out (NULL); act by `activation`: none, silu y / (1 + e^-y), gelu
+ * y (1 + erf(y / sqrt 2)) / 2, or its tanh form y (1 + tanh(sqrt(2 / pi) (y + 0.044715 y^3))) / 2.
+ *   a [M, K] bf16 (row stride lda), w [N, K] bf16 (row stride ldw): 16-byte aligned, K, lda and ldw multiples of 8
+ *   bias fp32 [N]; gate fp32 [gate_rows, N] (row stride ld_gate); gate_map [M] int32, 0 <= gate_map[r] < gate_rows (NULL: row 0; a
+ *   value out of range is taken as the nearest row)
+ *   out [M, N] and residual [M, N] of out_type (DIT_BF16 or DIT_F32), row strides ldo and ld_residual; residual may be out
+ *   with the same stride (in place), otherwise out must not overlap the inputs.
+ * fp32 accumulation and epilogue, one rounding to out_type. Any M and N; rows on 16 bytes (8 in bf16) run with vector accesses.
+ * ws: optional scratch of dit_linear_epilogue_workspace_bytes (16-byte aligned) for dividing K over the SMs where there
+ * are few output tiles (0 bytes where that does not pay): the sums then differ by the order of fp32 additions only. M = 0 or
+ * N = 0: nothing to do; K = 0 is refused. */
+#define DIT_ACT_NONE 0
+#define DIT_ACT_SILU 1
+#define DIT_ACT_GELU 2
+#define DIT_ACT_GELU_TANH 3
+typedef struct {
+  const float* bias;
+  const float* gate;
+  const int32_t* gate_map;
+  const void* residual;
+  long long ld_gate, ld_residual;
+  int gate_rows;
+  int activation;
+} dit_epilogue;
+DIT_API int dit_linear_epilogue(const uint16_t* a, int M, long long lda, int K, const uint16_t* w, int N, long long ldw,
+                                const dit_epilogue* e, void* out, int out_type, long long ldo, void* ws, size_t ws_bytes,
+                                dit_stream_t stream);
+DIT_API size_t dit_linear_epilogue_workspace_bytes(int M, int N, int K);
+
 /* int8lin dequantisation [host contract, section 1]: w[o, i] = bf16_rne(q[o, i] * s[o, i/32]),
  * the same arithmetic the int8 GEMM mainloop performs. cols % 32 == 0. */
 DIT_API int dit_dequant_int8(const int8_t* q, const uint16_t* s, int64_t rows, int64_t cols, uint16_t* w,
