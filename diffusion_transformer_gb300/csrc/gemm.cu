@@ -43,7 +43,7 @@ constexpr int BM = 128;
 constexpr int BK = 64;
 constexpr int kSkMaxParts = 3;  // stream-K segments per tile at most (the plan guarantees it)
 
-template <int BN, bool B8, bool PAIR = false>
+template <int BN, bool B8, bool PAIR = false, int EPI = -1>
 struct GemmCfg {
   // int8lin: 256-row CTA tiles (two M=128 MMAs share each converted B k-block), halving the
   // conversions per FLOP; bf16: 128-row tiles, or 256 x BN tiles shared by a CTA pair (PAIR: each CTA
@@ -65,8 +65,9 @@ struct GemmCfg {
   static constexpr int kConvThreads = 128;           // B8: converter warps 6..9, one per SM sub-partition
   static constexpr uint32_t kTmemCols = (kAccBufs * kMH * BN < 32) ? 32 : kAccBufs * kMH * BN;
   // epilogue warps: one per TMEM lane quadrant (two per quadrant, each taking half of the columns,
-  // measured no faster)
-  static constexpr int kEpiWarps = 4;
+  // measured no faster), but two under kEpiFull, whose activations keep one warp per SM sub-partition busy longer than
+  // the next tile's mainloop (4224 x 12288 x 3072 with gelu_tanh: 209 us with four warps, 171 with eight)
+  static constexpr int kEpiWarps = EPI == kEpiFull ? 8 : 4;
   static constexpr int kEpiThreads = 32 * kEpiWarps;
   static constexpr int kEpiCols = BN / (kEpiWarps / 4);   // columns per epilogue warp
   static constexpr int kConvWarp0 = 2 + kEpiWarps;         // first converter warp (B8)
@@ -101,14 +102,37 @@ __device__ __forceinline__ void store_bf16x32(uint16_t* dst, const float* v) {
 // 4 KB shared-memory scratch (the transposed v store, the gated residual's transpose). BN here is
 // the warp's column count.
 // ----------------------------------------------------------------------------------------------
-// The activations of kEpiFull. exp and erf are CUDA's full-precision ones; the sigmoid's quotient is within 2 units.
-__device__ __forceinline__ float activate(float y, int kind) {
+// The activations of kEpiFull. Where the result is rounded to bf16 anyway the exponential and the quotient are the
+// hardware's (2^-21 of the value for arguments that matter); erf is CUDA's.
+template <bool kFine>
+__device__ __forceinline__ float over_one_plus_exp(float y, float x) {  // y / (1 + e^x)
+  if constexpr (kFine) return __fdividef(y, 1.f + expf(x));
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2_approx(1.4426950408889634f * x)));
+  return y * r;
+}
+template <bool kFine>
+__device__ __forceinline__ float gelu_tanh_f(float y) {  // y (1 + tanh u) / 2 = y / (1 + e^-2u)
+  return over_one_plus_exp<kFine>(y, y * fmaf(-0.07135481627f, y * y, -1.5957691216f));
+}
+// N values at once, so that the choice is made once and the values' chains overlap
+template <int N>
+__device__ __forceinline__ void activate(float (&v)[N], int kind, int fine) {
+  auto each = [&](auto f) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = f(v[j]);
+  };
   switch (kind) {
-    case DIT_ACT_SILU: return __fdividef(y, 1.f + expf(-y));
-    case DIT_ACT_GELU: return 0.5f * y * (1.f + erff(y * 0.70710678118654752f));
-    case DIT_ACT_GELU_TANH:  // y (1 + tanh u) / 2 = y / (1 + e^-2u)
-      return __fdividef(y, 1.f + expf(-1.5957691216057308f * fmaf(0.044715f * y * y, y, y)));
-    default: return y;
+    case DIT_ACT_SILU:
+      if (fine) each([](float y) { return over_one_plus_exp<true>(y, -y); });
+      else each([](float y) { return over_one_plus_exp<false>(y, -y); });
+      break;
+    case DIT_ACT_GELU: each([](float y) { return 0.5f * y * (1.f + erff(y * 0.70710678118654752f)); }); break;
+    case DIT_ACT_GELU_TANH:
+      if (fine) each([](float y) { return gelu_tanh_f<true>(y); });
+      else each([](float y) { return gelu_tanh_f<false>(y); });
+      break;
+    default: break;
   }
 }
 
@@ -123,31 +147,13 @@ __device__ __forceinline__ float full_load1(const void* base, long long at, int 
   return f32 ? static_cast<const float*>(base)[at] : __uint_as_float(uint32_t(static_cast<const uint16_t*>(base)[at]) << 16);
 }
 
-// kEpiFull on four consecutive columns n .. n + 3 of one row, a the products' sums: `whole` with vector accesses (p.vec and
-// n + 3 < N), else value by value up to N. res: the residual's values (whole rows only, loaded ahead).
-__device__ __forceinline__ void full_store4(const GemmParams& p, int row, int n, float4 a, float4 bias, float4 res,
-                                            const float* gate, bool whole) {
+// What follows the activation, value by value up to N, on the columns n .. n + 3 of one row
+__device__ __forceinline__ void full_store1(const GemmParams& p, int row, int n, const float (&y)[4], const float* gate) {
   const long long at = (long long)row * p.ldo + n;
-  if (whole) {
-    float v[4] = {activate(a.x + bias.x, p.activation), activate(a.y + bias.y, p.activation),
-                  activate(a.z + bias.z, p.activation), activate(a.w + bias.w, p.activation)};
-    if (gate) {
-      const float4 g = __ldg(reinterpret_cast<const float4*>(gate + n));
-      v[0] *= g.x; v[1] *= g.y; v[2] *= g.z; v[3] *= g.w;
-    }
-    if (p.residual) {
-      v[0] += res.x; v[1] += res.y; v[2] += res.z; v[3] += res.w;
-    }
-    if (p.out_f32) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
-    else
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-    return;
-  }
-  const float in[4] = {a.x, a.y, a.z, a.w}, b[4] = {bias.x, bias.y, bias.z, bias.w};
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     if (n + j >= p.N) break;
-    float v = activate(in[j] + b[j], p.activation);
+    float v = y[j];
     if (gate) v *= __ldg(gate + n + j);
     if (p.residual) v += full_load1(p.residual, (long long)row * p.ldr + n + j, p.out_f32);
     if (p.out_f32) static_cast<float*>(p.out)[at + j] = v;
@@ -429,23 +435,34 @@ __device__ __forceinline__ void epilogue_tile(const GemmParams& p, uint32_t tadd
     }
   } else if constexpr (EPI == kEpiFull) {
     // Chunks of 32 columns go through the warp's shared tile as in the gated epilogue: a lane then holds four columns
-    // of the rows (lane >> 3) + 4 i, so a warp instruction moves four whole lines of out, residual or gate, and a lane's bias is one load.
-    // The residual is loaded before the accumulator is waited for.
-    const int cq = lane & 7;
+    // of the rows (lane >> 3) + 4 i, so a warp instruction moves whole sectors of four rows of out, residual or gate, and
+    // a lane's bias is one load. Bias, residual and gate of the next chunk are loaded as soon as this one's are used.
+    (void)row_ok;
+    const int cq = lane & 7, rb = row0 + (lane >> 3);
+    const bool parts = p.k_parts > 1;
+    const float* gr[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) gr[i] = p.gate && rb + 4 * i < row_end ? full_gate(p, rb + 4 * i) : nullptr;
+    float4 res[8], gq[8], bias;
+    auto ahead = [&](int n) {
+      if (parts || n >= p.N) return;
+      bias = full_bias4(p, n);
+      if (!p.vec || n + 3 >= p.N) return;
+      if (p.residual)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (rb + 4 * i < row_end) res[i] = full_load4(p.residual, (rb + 4 * i) * p.ldr + n, p.out_f32);
+      if (p.gate)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (gr[i]) gq[i] = __ldg(reinterpret_cast<const float4*>(gr[i] + n));
+    };
+    ahead(n0 + cq * 4);
 #pragma unroll 1
     for (int c = 0; c < BN / 32; ++c) {
       if (n0 + c * 32 >= p.N) break;  // the same for the warp
       const int n = n0 + c * 32 + cq * 4;
       const bool whole = p.vec && n + 3 < p.N;
-      float4 res[8];
-      const float4 bias = full_bias4(p, n);
-      if (p.residual && whole && p.k_parts <= 1) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = row0 + (lane >> 3) + 4 * i;
-          if (r < row_end) res[i] = full_load4(p.residual, (long long)r * p.ldr + n, p.out_f32);
-        }
-      }
       uint32_t v[32];
       tmem_ld32(taddr + c * 32, v);
       tmem_ld_wait();
@@ -454,19 +471,65 @@ __device__ __forceinline__ void epilogue_tile(const GemmParams& p, uint32_t tadd
         *reinterpret_cast<uint4*>(stage + lane * 128 + ((q ^ (lane & 7)) << 4)) =
             make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
       __syncwarp();
+      float y[32];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int rl = (lane >> 3) + 4 * i, r = row0 + rl;
+        const int rl = (lane >> 3) + 4 * i;
         const float4 a = *reinterpret_cast<const float4*>(stage + rl * 128 + ((cq ^ (rl & 7)) << 4));
-        if (r >= row_end || n >= p.N) continue;
-        if (p.k_parts > 1) {
-          *reinterpret_cast<float4*>(p.parts + ((long long)part * p.M + r) * p.parts_ld + n) = a;  // parts_ld % 4 == 0
-          continue;
-        }
-        const float* gate = p.gate ? full_gate(p, r) : nullptr;
-        full_store4(p, r, n, a, bias, res[i], gate, whole);
+        y[4 * i] = a.x; y[4 * i + 1] = a.y; y[4 * i + 2] = a.z; y[4 * i + 3] = a.w;
       }
       __syncwarp();
+      if (n >= p.N) continue;
+      if (parts) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (rb + 4 * i < row_end)  // parts_ld % 4 == 0
+            *reinterpret_cast<float4*>(p.parts + ((long long)part * p.M + rb + 4 * i) * p.parts_ld + n) =
+                make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+        continue;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        y[4 * i] += bias.x; y[4 * i + 1] += bias.y; y[4 * i + 2] += bias.z; y[4 * i + 3] += bias.w;
+      }
+      activate(y, p.activation, p.out_f32);
+      if (whole) {
+        if (p.gate)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            y[4 * i] *= gq[i].x; y[4 * i + 1] *= gq[i].y; y[4 * i + 2] *= gq[i].z; y[4 * i + 3] *= gq[i].w;
+          }
+        if (p.residual)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            y[4 * i] += res[i].x; y[4 * i + 1] += res[i].y; y[4 * i + 2] += res[i].z; y[4 * i + 3] += res[i].w;
+          }
+        if (p.out_f32) {
+          float* o = static_cast<float*>(p.out) + rb * p.ldo + n;
+#pragma unroll
+          for (int i = 0; i < 8; ++i, o += 4 * p.ldo)
+            if (rb + 4 * i < row_end) *reinterpret_cast<float4*>(o) = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+        } else {
+          uint16_t* o = static_cast<uint16_t*>(p.out) + rb * p.ldo + n;
+#pragma unroll
+          for (int i = 0; i < 8; ++i, o += 4 * p.ldo)
+            if (rb + 4 * i < row_end)
+              *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(y[4 * i], y[4 * i + 1]), pack_bf16x2(y[4 * i + 2], y[4 * i + 3]));
+        }
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+          // (the values by a select over i: an index would put y into local memory)
+          float z[4] = {y[0], y[1], y[2], y[3]};
+#pragma unroll
+          for (int k = 1; k < 8; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) z[j] = k == i ? y[4 * k + j] : z[j];
+          const int r = rb + 4 * i;
+          if (r < row_end) full_store1(p, r, n, z, p.gate ? full_gate(p, r) : nullptr);
+        }
+      }
+      ahead(n + 32);
     }
   } else {
 #pragma unroll 1
@@ -716,11 +779,11 @@ constexpr int kSkSlots = 64, kSkMaxCounters = 2048;
 __device__ uint32_t g_sk_cnt[kSkSlots * kSkMaxCounters];
 
 template <int BN, int EPI, bool B8, bool PAIR>
-__global__ void __launch_bounds__(GemmCfg<BN, B8, PAIR>::kThreads, 1)
+__global__ void __launch_bounds__(GemmCfg<BN, B8, PAIR, EPI>::kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const __grid_constant__ CUtensorMap tmS, const __grid_constant__ CUtensorMap tmA2,
                 const __grid_constant__ CUtensorMap tmB2, const GemmParams p) {
-  using Cfg = GemmCfg<BN, B8, PAIR>;
+  using Cfg = GemmCfg<BN, B8, PAIR, EPI>;
   constexpr int S = Cfg::kStages;
   constexpr int CS = Cfg::kConvStages;
   extern __shared__ uint8_t smem_raw[];
@@ -969,7 +1032,7 @@ __global__ void __launch_bounds__(GemmCfg<BN, B8, PAIR>::kThreads, 1)
       const TileRows tr = tile_rows(p, Cfg::kTileM, mb);
       if (!mbar_wait_warp(smem_u32(&tfull[acc]), acc_phase, p.err, kErrTimeoutEpilogue)) break;
       tc_fence_after();
-      if constexpr (!B8) {
+      if constexpr (!B8 && EPI != kEpiFull) {  // neither stream-K nor W8A8 under kEpiFull
         static_assert(B8 || Cfg::kEpiCols == BN, "one epilogue warp per TMEM lane quadrant");
         const uint32_t taddr = tmem_base + (uint32_t(quad * 32) << 16) + uint32_t(acc * BN);
         const int row = tr.base + rows_of + quad * 32 + lane;
@@ -1168,7 +1231,7 @@ void plan_stream_k(GemmParams& q, int tiles, int units, int slabs, int BN) {
 
 template <int BN, int EPI, bool B8, bool PAIR>
 int launch_one(const Maps& m, const GemmParams& p, cudaStream_t stream) {
-  using Cfg = GemmCfg<BN, B8, PAIR>;
+  using Cfg = GemmCfg<BN, B8, PAIR, EPI>;
   static_assert(Cfg::kSmemBytes <= 227 * 1024, "shared memory budget");
   auto kern = gemm_kernel<BN, EPI, B8, PAIR>;
   if (!smem_attr_once(reinterpret_cast<const void*>(kern), Cfg::kSmemBytes)) return DIT_ECUDA;
@@ -1362,7 +1425,6 @@ __global__ void __launch_bounds__(256) full_join_kernel(const __grid_constant__ 
   const long long quads = (p.N + 3) / 4, x = (long long)blockIdx.x * 256 + threadIdx.x;
   if (x >= quads * p.M) return;
   const int row = int(x / quads), n = int(x - row * quads) * 4;
-  const bool whole = p.vec && n + 3 < p.N;
   const float* src = p.parts + (long long)row * p.parts_ld + n;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
@@ -1371,10 +1433,24 @@ __global__ void __launch_bounds__(256) full_join_kernel(const __grid_constant__ 
     a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
   }
   const float4 bias = full_bias4(p, n);
-  float4 res = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (p.residual && whole) res = full_load4(p.residual, (long long)row * p.ldr + n, p.out_f32);
+  float y[4] = {a.x + bias.x, a.y + bias.y, a.z + bias.z, a.w + bias.w};
+  activate(y, p.activation, p.out_f32);
   const float* gate = p.gate ? full_gate(p, row) : nullptr;
-  full_store4(p, row, n, a, bias, res, gate, whole);
+  if (!p.vec || n + 3 >= p.N) {
+    full_store1(p, row, n, y, gate);
+    return;
+  }
+  if (gate) {
+    const float4 g = __ldg(reinterpret_cast<const float4*>(gate + n));
+    y[0] *= g.x; y[1] *= g.y; y[2] *= g.z; y[3] *= g.w;
+  }
+  if (p.residual) {
+    const float4 r = full_load4(p.residual, row * p.ldr + n, p.out_f32);
+    y[0] += r.x; y[1] += r.y; y[2] += r.z; y[3] += r.w;
+  }
+  const long long at = row * p.ldo + n;
+  if (p.out_f32) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(y[0], y[1], y[2], y[3]);
+  else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
 }
 
 // Tile and division of the k-blocks, by an estimate of time: rounds of work items over the units (SMs, or pairs), each
