@@ -1453,9 +1453,112 @@ __global__ void __launch_bounds__(256) full_join_kernel(const __grid_constant__ 
   else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
 }
 
-// Tile and division of the k-blocks, by an estimate of time: rounds of work items over the units (SMs, or pairs), each
-// its k-blocks and its epilogue. A k-block costs what its MMAs take or what its bytes take on an SM's share of HBM
-// (44 KB a microsecond), rows past M being free.
+// A few rows against the weight, which is read once: HBM-bound on the plain cores, where a tile of 128 rows would have the
+// tensor cores multiply zeros and its 128-byte pieces of rows keep HBM at 3.6 TB/s (18432 x 3072: 1, 2 and 4 rows 19.8, 23.7 and
+// 26.5 us, as tiles 31 to 32; 8 rows 54 us, as tiles 32). A warp takes kVecRows rows of W, a lane
+// 16 bytes of each at a time, so a warp reads 512 consecutive bytes; a (L1 or L2) is read once for all of them. 2^split warps
+// of a CTA divide K between them, for few outputs. Sums in fp32, two per row and product (packed pairs), joined over the
+// lanes by a butterfly and over the warps in order.
+constexpr int kVecRows = 4, kVecMost = 4;
+template <int M>
+__global__ void __launch_bounds__(256) full_rows_kernel(const __grid_constant__ GemmParams p, const uint16_t* a, long long lda,
+                                                        const uint16_t* w, long long ldw, int split) {
+  __shared__ float sums[8][kVecRows * M];
+  const int warp = threadIdx.x >> 5, lane = lane_id(), ways = 1 << split;
+  const int part = warp & (ways - 1), group = warp >> split;
+  const int n0 = (blockIdx.x * (8 >> split) + group) * kVecRows;
+  const uint4* wr[kVecRows];
+#pragma unroll
+  for (int r = 0; r < kVecRows; ++r) wr[r] = reinterpret_cast<const uint4*>(w + (long long)min(n0 + r, p.N - 1) * ldw);
+  uint64_t acc[M][kVecRows];
+#pragma unroll
+  for (int m = 0; m < M; ++m)
+#pragma unroll
+    for (int r = 0; r < kVecRows; ++r) acc[m][r] = 0;
+  pdl_wait();
+  pdl_trigger();
+  const int chunks = p.K / 8, step = 32 * ways;
+  auto pairs = [](uint4 u, uint64_t (&v)[4]) {
+    const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = f2_pack(__uint_as_float(x[j] << 16), __uint_as_float(x[j] & 0xffff0000u));
+  };
+  auto load_w = [](const uint4* q) {
+    uint4 u;
+    asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                 : "l"(q));
+    return u;
+  };
+  constexpr int kDeep = 2;  // pieces in flight per row
+  for (int c = part * 32 + lane; c < chunks; c += kDeep * step) {
+    uint4 q[kDeep][kVecRows];
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d)
+#pragma unroll
+      for (int r = 0; r < kVecRows; ++r)
+        if (c + d * step < chunks) q[d][r] = load_w(wr[r] + c + d * step);
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) {
+      if (c + d * step >= chunks) break;
+      uint64_t x[M][4];
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+        pairs(__ldg(reinterpret_cast<const uint4*>(a + min(m, p.M - 1) * lda) + c + d * step), x[m]);
+#pragma unroll
+      for (int r = 0; r < kVecRows; ++r) {
+        uint64_t y[4];
+        pairs(q[d][r], y);
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[m][r] = f2_fma(x[m][j], y[j], acc[m][r]);
+      }
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < M; ++m)
+#pragma unroll
+    for (int r = 0; r < kVecRows; ++r) {
+      float v = f2_lo(acc[m][r]) + f2_hi(acc[m][r]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (lane == 0) sums[warp][m * kVecRows + r] = v;
+    }
+  __syncthreads();
+  if (part != 0 || lane >= kVecRows * M) return;
+  const int m = lane / kVecRows, n = n0 + lane % kVecRows;
+  if (m >= p.M || n >= p.N) return;
+  float y[1] = {p.bias ? __ldg(p.bias + n) : 0.f};
+  float v = 0.f;
+  for (int i = 0; i < ways; ++i) v += sums[warp + i][lane];
+  y[0] += v;
+  activate(y, p.activation, p.out_f32);
+  if (p.gate) y[0] *= __ldg(full_gate(p, m) + n);
+  if (p.residual) y[0] += full_load1(p.residual, m * p.ldr + n, p.out_f32);
+  if (p.out_f32) static_cast<float*>(p.out)[m * p.ldo + n] = y[0];
+  else static_cast<uint16_t*>(p.out)[m * p.ldo + n] = uint16_t(pack_bf16x2(y[0], 0.f));
+}
+
+int full_rows_launch(const uint16_t* a, long long lda, const uint16_t* w, long long ldw, const GemmParams& p, cudaStream_t st) {
+  // K is divided while the CTAs do not fill the SMs four times over and a warp keeps 16 rounds of loads
+  const int groups = (p.N + kVecRows - 1) / kVecRows;
+  int split = 0;
+  while (split < 3 && (long long)groups << split < 32LL * num_sms() && p.K >> (split + 1) >= 8 * 32) ++split;
+  const dim3 grid(unsigned((groups + (8 >> split) - 1) / (8 >> split))), block(256);
+  cudaError_t e;
+  if (p.M == 1) e = launch_pdl(full_rows_kernel<1>, grid, block, 0, st, 1, p, a, lda, w, ldw, split);
+  else if (p.M == 2) e = launch_pdl(full_rows_kernel<2>, grid, block, 0, st, 1, p, a, lda, w, ldw, split);
+  else if (p.M <= 4) e = launch_pdl(full_rows_kernel<4>, grid, block, 0, st, 1, p, a, lda, w, ldw, split);
+  else e = launch_pdl(full_rows_kernel<kVecMost>, grid, block, 0, st, 1, p, a, lda, w, ldw, split);
+  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? DIT_OK : DIT_ECUDA;
+}
+
+// Tile and division of the k-blocks, by an estimate of time fitted to 18 sizes on a GB300: rounds of work items over the
+// units (SMs, or pairs), a round as long as its k-blocks or as an epilogue (which overlaps the next round's k-blocks), the
+// last epilogue, the launch; for divided k-blocks the joining kernel and its bytes; never below what HBM takes for the
+// operands (tiles read it at 4.2 TB/s, those of 64 rows of W at 2.8). Measured best and chosen, us: 16 x 512 x 14000 10.0 / 10.0, 100 x 512 x 6144 8.6 / 8.6,
+// 333 x 1024 x 4096 11.9 / 11.9, 1088 x 4096 x 1024 15.0 / 15.1, 2627 x 3968 x 11200 155 / 155, 4224 x 12288 x 3072 171 / 171.
 struct FullPlan {
   int bn, parts;
   bool pair;
@@ -1464,20 +1567,23 @@ FullPlan full_plan(int M, int N, int K) {
   const int KB = (K + BK - 1) / BK, sms = num_sms() > 0 ? num_sms() : 1;
   struct Shape {
     int bn, rows;
-    float mma;  // us a k-block
+    float kblock, epilogue;  // us
   };
-  const Shape shapes[] = {{256, 256, 0.40f}, {128, 256, 0.24f}, {128, 128, 0.24f}, {64, 128, 0.16f}};
+  const Shape shapes[] = {{256, 256, 0.30f, 6.4f}, {128, 256, 0.177f, 3.7f}, {256, 128, 0.36f, 6.7f}, {128, 128, 0.21f, 4.3f},
+                          {64, 128, 0.168f, 2.3f}};
+  const float hbm = 2.f * K * (float(M) + float(N)) / 4.2e6f;
   FullPlan best{64, 1, false};
   float least = 0.f;
   for (const Shape& s : shapes) {
-    const bool pair = s.rows == 256;
+    const bool pair = s.rows != BM;
     if (pair && (M <= BM || sms < 2)) continue;
     const long long tiles = ((long long)M + s.rows - 1) / s.rows * ((N + s.bn - 1) / s.bn);
     const long long units = pair ? sms / 2 : sms;
-    const float kb = std::max(s.mma, (float(std::min(M, BM)) + float(pair ? s.bn / 2 : s.bn)) * (BK * 2 / 1024.f) / 44.f);
     for (int parts = 1; parts <= 32 && (parts == 1 || (tiles * parts <= units && KB / parts >= 4)); ++parts) {
-      const long long rounds = (tiles * parts + units - 1) / units;
-      const float t = rounds * (kb * ((KB + parts - 1) / parts)) + 2.f + (parts > 1 ? 4.f + 0.1f * parts : 0.f);
+      const float rounds = float((tiles * parts + units - 1) / units);
+      const float main = std::max(s.kblock * float((KB + parts - 1) / parts), rounds > 1 ? s.epilogue : 0.f);
+      float t = std::max(rounds * main, s.bn == 64 ? 1.5f * hbm : hbm) + s.epilogue + 2.f;
+      if (parts > 1) t += 2.5f + float(parts) * float(M) * float(N) * 4.f / 3.5e6f;
       if (least == 0.f || t < least) {
         least = t;
         best = FullPlan{s.bn, parts, pair};
@@ -1491,6 +1597,7 @@ long long parts_ld(int N) { return (N + 3) / 4 * 4; }
 }  // namespace
 
 size_t gemm_full_scratch_bytes(int M, int N, int K) {
+  if (M <= kVecMost) return 0;
   const FullPlan f = full_plan(M, N, K);
   return f.parts > 1 ? size_t(f.parts) * M * parts_ld(N) * sizeof(float) : 0;
 }
@@ -1498,8 +1605,9 @@ size_t gemm_full_scratch_bytes(int M, int N, int K) {
 int gemm_full_launch(const uint16_t* a, long long lda, const uint16_t* b, long long ldb, const GemmParams& p0, void* ws,
                      size_t ws_bytes, cudaStream_t stream) {
   GemmParams p = p0;
-  const FullPlan f = full_plan(p.M, p.N, p.K);
   p.k_parts = 1;
+  if (p.M <= kVecMost) return full_rows_launch(a, lda, b, ldb, p, stream);
+  const FullPlan f = full_plan(p.M, p.N, p.K);
   if (f.parts > 1 && ws && ws_bytes >= gemm_full_scratch_bytes(p.M, p.N, p.K)) {
     p.k_parts = f.parts;
     p.parts = static_cast<float*>(ws);
