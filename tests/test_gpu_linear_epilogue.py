@@ -89,13 +89,13 @@ def test_sizes_and_parts(M, K, N, dtype):
 def test_divided_k_is_repeatable(M, K, N):
     a, w, bias, gate, gmap, res = _make(M, K, N, 5, torch.float32, 2)
     n = D.dit_linear_epilogue_workspace_bytes(M, N, K)
-    assert n > 0
+    assert n > 0 or M <= 4  # up to four rows have a kernel of their own, which divides K within a CTA
     ref, err = _expect(a, w, bias, "silu", gate, gmap, res)
     outs = []
     for _ in range(3):
         out = torch.empty(M, N, device="cuda")
         D.dit_linear_epilogue(a, w, out, bias=bias, activation="silu", gate=gate, gate_map=gmap, residual=res,
-                              ws=torch.full((n,), 255, dtype=torch.uint8, device="cuda"))
+                              ws=torch.full((max(n, 16),), 255, dtype=torch.uint8, device="cuda"))
         outs.append(out)
     D.dit_check()
     _check(outs[0], ref, err)
