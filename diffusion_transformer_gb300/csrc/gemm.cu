@@ -434,35 +434,54 @@ __device__ __forceinline__ void epilogue_tile(const GemmParams& p, uint32_t tadd
       }
     }
   } else if constexpr (EPI == kEpiFull) {
-    // Chunks of 32 columns go through the warp's shared tile as in the gated epilogue: a lane then holds four columns
-    // of the rows (lane >> 3) + 4 i, so a warp instruction moves whole sectors of four rows of out, residual or gate, and
-    // a lane's bias is one load. Bias, residual and gate of the next chunk are loaded as soon as this one's are used.
-    (void)row_ok;
+    // Chunks of 32 columns go through the warp's shared tile as in the gated epilogue. Where rows stand on four values and the
+    // chunk is whole, a lane then holds four columns of the rows (lane >> 3) + 4 i, so a warp instruction moves whole
+    // sectors of four rows of out, residual or gate; else a lane holds one column of all 32 rows, and an instruction moves 32
+    // neighbouring values of one row. Bias, residual and gate of the next chunk are loaded as soon as this one's are used.
     const int cq = lane & 7, rb = row0 + (lane >> 3);
     const bool parts = p.k_parts > 1;
-    const float* gr[8];
+    int gate_row = 0;  // of row `row0 + lane`; the other rows' by shuffle
+    if (p.gate && p.map && row_ok) gate_row = min(max(__ldg(p.map + row), 0), p.gate_rows - 1);
+    float res[32], gq[32];
+    float4 bias = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto quads = [&](int nc) { return p.vec && nc + 32 <= p.N; };  // a whole chunk on four values (the same for the warp)
+    auto ahead = [&](int nc) {
+      if (parts || nc >= p.N) return;
+      if (quads(nc)) {
+        const int n = nc + cq * 4;
+        if (p.bias) bias = __ldg(reinterpret_cast<const float4*>(p.bias + n));
+        if (p.residual)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) gr[i] = p.gate && rb + 4 * i < row_end ? full_gate(p, rb + 4 * i) : nullptr;
-    float4 res[8], gq[8], bias;
-    auto ahead = [&](int n) {
-      if (parts || n >= p.N) return;
-      bias = full_bias4(p, n);
-      if (!p.vec || n + 3 >= p.N) return;
-      if (p.residual)
+          for (int i = 0; i < 8; ++i)
+            if (rb + 4 * i < row_end) {
+              const float4 r = full_load4(p.residual, (rb + 4 * i) * p.ldr + n, p.out_f32);
+              res[4 * i] = r.x; res[4 * i + 1] = r.y; res[4 * i + 2] = r.z; res[4 * i + 3] = r.w;
+            }
+        if (p.gate)
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (rb + 4 * i < row_end) res[i] = full_load4(p.residual, (rb + 4 * i) * p.ldr + n, p.out_f32);
-      if (p.gate)
+          for (int i = 0; i < 8; ++i) {
+            const int g = __shfl_sync(0xffffffffu, gate_row, (lane >> 3) + 4 * i);
+            const float4 r = __ldg(reinterpret_cast<const float4*>(p.gate + g * p.gate_stride + n));
+            gq[4 * i] = r.x; gq[4 * i + 1] = r.y; gq[4 * i + 2] = r.z; gq[4 * i + 3] = r.w;
+          }
+      } else {
+        const int n = min(nc + lane, p.N - 1);  // lanes past the last column load it too and store nothing
+        if (p.bias) bias.x = __ldg(p.bias + n);
+        if (p.residual)
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (gr[i]) gq[i] = __ldg(reinterpret_cast<const float4*>(gr[i] + n));
+          for (int i = 0; i < 32; ++i)
+            if (row0 + i < row_end) res[i] = full_load1(p.residual, (row0 + i) * p.ldr + n, p.out_f32);
+        if (p.gate)
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            gq[i] = __ldg(p.gate + __shfl_sync(0xffffffffu, gate_row, i) * p.gate_stride + n);
+      }
     };
-    ahead(n0 + cq * 4);
+    ahead(n0);
 #pragma unroll 1
     for (int c = 0; c < BN / 32; ++c) {
-      if (n0 + c * 32 >= p.N) break;  // the same for the warp
-      const int n = n0 + c * 32 + cq * 4;
-      const bool whole = p.vec && n + 3 < p.N;
+      const int nc = n0 + c * 32, n = nc + cq * 4;
+      if (nc >= p.N) break;  // the same for the warp
       uint32_t v[32];
       tmem_ld32(taddr + c * 32, v);
       tmem_ld_wait();
@@ -472,38 +491,37 @@ __device__ __forceinline__ void epilogue_tile(const GemmParams& p, uint32_t tadd
             make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
       __syncwarp();
       float y[32];
+      const bool four = parts || quads(nc);  // parts_ld is a multiple of 4
+      if (four) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int rl = (lane >> 3) + 4 * i;
-        const float4 a = *reinterpret_cast<const float4*>(stage + rl * 128 + ((cq ^ (rl & 7)) << 4));
-        y[4 * i] = a.x; y[4 * i + 1] = a.y; y[4 * i + 2] = a.z; y[4 * i + 3] = a.w;
+        for (int i = 0; i < 8; ++i) {
+          const int rl = (lane >> 3) + 4 * i;
+          const float4 a = *reinterpret_cast<const float4*>(stage + rl * 128 + ((cq ^ (rl & 7)) << 4));
+          y[4 * i] = a.x + bias.x; y[4 * i + 1] = a.y + bias.y; y[4 * i + 2] = a.z + bias.z; y[4 * i + 3] = a.w + bias.w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          y[i] = *reinterpret_cast<const float*>(stage + i * 128 + (((lane >> 2) ^ (i & 7)) << 4) + (lane & 3) * 4) + bias.x;
       }
       __syncwarp();
-      if (n >= p.N) continue;
       if (parts) {
+        if (n < p.N)
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (rb + 4 * i < row_end)  // parts_ld % 4 == 0
-            *reinterpret_cast<float4*>(p.parts + ((long long)part * p.M + rb + 4 * i) * p.parts_ld + n) =
-                make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+          for (int i = 0; i < 8; ++i)
+            if (rb + 4 * i < row_end)
+              *reinterpret_cast<float4*>(p.parts + ((long long)part * p.M + rb + 4 * i) * p.parts_ld + n) =
+                  make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
         continue;
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        y[4 * i] += bias.x; y[4 * i + 1] += bias.y; y[4 * i + 2] += bias.z; y[4 * i + 3] += bias.w;
-      }
       activate(y, p.activation, p.out_f32);
-      if (whole) {
-        if (p.gate)
+      if (p.gate)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            y[4 * i] *= gq[i].x; y[4 * i + 1] *= gq[i].y; y[4 * i + 2] *= gq[i].z; y[4 * i + 3] *= gq[i].w;
-          }
-        if (p.residual)
+        for (int i = 0; i < 32; ++i) y[i] *= gq[i];
+      if (p.residual)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            y[4 * i] += res[i].x; y[4 * i + 1] += res[i].y; y[4 * i + 2] += res[i].z; y[4 * i + 3] += res[i].w;
-          }
+        for (int i = 0; i < 32; ++i) y[i] += res[i];
+      if (four) {
         if (p.out_f32) {
           float* o = static_cast<float*>(p.out) + rb * p.ldo + n;
 #pragma unroll
@@ -516,20 +534,20 @@ __device__ __forceinline__ void epilogue_tile(const GemmParams& p, uint32_t tadd
             if (rb + 4 * i < row_end)
               *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(y[4 * i], y[4 * i + 1]), pack_bf16x2(y[4 * i + 2], y[4 * i + 3]));
         }
-      } else {
-#pragma unroll 1
-        for (int i = 0; i < 8; ++i) {
-          // (the values by a select over i: an index would put y into local memory)
-          float z[4] = {y[0], y[1], y[2], y[3]};
+      } else if (nc + lane < p.N) {
+        if (p.out_f32) {
+          float* o = static_cast<float*>(p.out) + row0 * p.ldo + nc + lane;
 #pragma unroll
-          for (int k = 1; k < 8; ++k)
+          for (int i = 0; i < 32; ++i, o += p.ldo)
+            if (row0 + i < row_end) *o = y[i];
+        } else {
+          uint16_t* o = static_cast<uint16_t*>(p.out) + row0 * p.ldo + nc + lane;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) z[j] = k == i ? y[4 * k + j] : z[j];
-          const int r = rb + 4 * i;
-          if (r < row_end) full_store1(p, r, n, z, p.gate ? full_gate(p, r) : nullptr);
+          for (int i = 0; i < 32; ++i, o += p.ldo)
+            if (row0 + i < row_end) *o = uint16_t(pack_bf16x2(y[i], 0.f));
         }
       }
-      ahead(n + 32);
+      ahead(nc + 32);
     }
   } else {
 #pragma unroll 1
