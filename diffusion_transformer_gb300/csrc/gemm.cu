@@ -175,8 +175,8 @@ __device__ __forceinline__ float4 full_bias4(const GemmParams& p, int n) {
 }
 
 template <int BN, int EPI, bool kRowPerThread>
-__device__ __forceinline__ void epilogue_tile(const GemmParams& p, uint32_t taddr, int row0, int row_end, int lane,
-                                              int n0, uint8_t* stage, int part = 0) {
+__device__ __forceinline__ bool epilogue_tile(const GemmParams& p, uint32_t taddr, int row0, int row_end, int lane,
+                                              int n0, uint8_t* stage, int part = 0, uint32_t tfull = 0, uint32_t phase = 0) {
   const int row = row0 + lane;
   const bool row_ok = row < row_end;
   if constexpr (EPI == kEpiQKV) {
@@ -477,7 +477,9 @@ __device__ __forceinline__ void epilogue_tile(const GemmParams& p, uint32_t tadd
             gq[i] = __ldg(p.gate + __shfl_sync(0xffffffffu, gate_row, i) * p.gate_stride + n);
       }
     };
-    ahead(n0);
+    ahead(n0);  // under the tile's mainloop
+    if (!mbar_wait_warp(tfull, phase, p.err, kErrTimeoutEpilogue)) return false;
+    tc_fence_after();
 #pragma unroll 1
     for (int c = 0; c < BN / 32; ++c) {
       const int nc = n0 + c * 32, n = nc + cq * 4;
@@ -585,6 +587,7 @@ __device__ __forceinline__ void epilogue_tile(const GemmParams& p, uint32_t tadd
       }
     }
   }
+  return true;
 }
 
 // ----------------------------------------------------------------------------------------------
@@ -1048,8 +1051,11 @@ __global__ void __launch_bounds__(GemmCfg<BN, B8, PAIR, EPI>::kThreads, 1)
       int mb, nb;
       tile_mn(w.tile, mb, nb);
       const TileRows tr = tile_rows(p, Cfg::kTileM, mb);
-      if (!mbar_wait_warp(smem_u32(&tfull[acc]), acc_phase, p.err, kErrTimeoutEpilogue)) break;
-      tc_fence_after();
+      if constexpr (EPI != kEpiFull) {  // whose epilogue loads what it can before it waits
+        if (!mbar_wait_warp(smem_u32(&tfull[acc]), acc_phase, p.err, kErrTimeoutEpilogue)) break;
+        tc_fence_after();
+      }
+      bool ok = true;
       if constexpr (!B8 && EPI != kEpiFull) {  // neither stream-K nor W8A8 under kEpiFull
         static_assert(B8 || Cfg::kEpiCols == BN, "one epilogue warp per TMEM lane quadrant");
         const uint32_t taddr = tmem_base + (uint32_t(quad * 32) << 16) + uint32_t(acc * BN);
@@ -1112,9 +1118,11 @@ __global__ void __launch_bounds__(GemmCfg<BN, B8, PAIR, EPI>::kThreads, 1)
           else
             epilogue_tile<Cfg::kEpiCols, kEpiSwiGLU, B8>(p, taddr, row0, tr.end, lane, n0 - p.n_split, stage);
         } else {
-          epilogue_tile<Cfg::kEpiCols, EPI, B8>(p, taddr, row0, tr.end, lane, n0, stage, w.trel);
+          ok = epilogue_tile<Cfg::kEpiCols, EPI, B8>(p, taddr, row0, tr.end, lane, n0, stage, w.trel, smem_u32(&tfull[acc]),
+                                                      acc_phase);
         }
       }
+      if (!ok) break;
       tc_fence_before();
       if constexpr (PAIR) mbar_arrive_cluster(tempty0 + uint32_t(acc) * 8u);
       else mbar_arrive(smem_u32(&tempty[acc]));
