@@ -9,14 +9,13 @@
 // only the weights round to bf16 for the product with V, whose sum is fp32 in tensor memory.
 //
 // GB300 mapping. The query heads that share a key head stand side by side in one 128-row tile (row r G + g: query row
-// r, head g of the G), so K and V are read once for all of them. A CTA takes two such tiles of one segment (NT = 2), or,
-// where segments have few rows, one tile whose two halves of the key tiles, even and odd, run like the two tiles
-// (NT = 1) and meet at the end in shared memory. Roles as in the joint attention: warp 0 loads with TMA, warp 1 issues
-// the MMAs, warps 2-5 and 6-9 turn the scores of the two tiles into weights, so that one tile's exponentials overlap the
-// other's MMAs. K and V are rows of any stride: both come by TMA as [keys, d] boxes, and V enters its MMA as an
-// MN-major operand, so nothing is transposed in memory. CTAs find their segment by a scan over q_start: no lengths on
-// the host, and a captured graph serves other lengths. Where there are too few tiles for the SMs the key range is
-// split over CTAs (blockIdx.z) and a second kernel joins the parts in order.
+// r, head g of the G), so K and V are read once for all of them. K and V are rows of any stride: both come by TMA as
+// [keys, d] boxes, and V enters its MMA as an MN-major operand, so nothing is transposed in memory. CTAs find their segment
+// by a scan over q_start: no lengths on the host, and a captured graph serves other lengths. packed_kernel takes two tiles
+// of a segment per CTA, roles as in the joint attention: warp 0 loads, warp 1 issues the MMAs, warps 2-5 and 6-9 turn the
+// scores of the two tiles into weights, so that one tile's exponentials overlap the other's MMAs. packed_rows_kernel takes
+// segments of few rows, two CTAs to an SM. Where there are too few tiles for the SMs the key range is split over CTAs
+// (blockIdx.z) and a second kernel joins the parts in order.
 // Masked places: weights of masked keys are zero, the rows of V behind the last key that any row of the CTA sees are
 // zeroed in shared memory (they may be the next segment's, or anything), and a row whose result is not finite while
 // its tile held keys that it does not see is summed again over its own keys (resum_row): NaN or infinity in a masked
@@ -46,7 +45,7 @@ constexpr int kPackedThreads = 320;
 struct PackedParams {
   dit_packed_attention a;
   int G, rpt;  // query heads per key head, query rows of a tile
-  int splits;
+  int splits, slots;  // CTAs along the keys; ring slots of the few-rows kernel
   float scale_log2;  // scale log2(e)
   float cap_in, cap_out;  // 2 scale log2(e) / cap and cap log2(e); cap_out = 0: no cap
   float* part_o;   // [split][q_rows][heads][d]
@@ -54,22 +53,21 @@ struct PackedParams {
   int* err;
 };
 
-template <int D, int NT>
+template <int D>
 struct PackedCfg {
   static constexpr uint32_t kTile = 128 * D * 2;  // 128 rows of q, k or v
   static constexpr uint32_t kAtom = 128 * 128;    // [128 rows x 64 bf16], 128-byte swizzled
-  static constexpr int kKS = D == 128 ? 3 : (NT == 2 ? 4 : 5);
-  static constexpr int kVS = D == 128 ? (NT == 2 ? 2 : 3) : (NT == 2 ? 4 : 5);
+  static constexpr int kKS = D == 128 ? 3 : 4, kVS = D == 128 ? 2 : 4;
   static constexpr int kBars = 2 + 2 * kKS + 2 * kVS + 6;
-  static constexpr uint32_t kSmem = 1024 + NT * kTile + (kKS + kVS) * kTile + kBars * 8 + 64 + (NT == 1 ? 1024 : 0);
+  static constexpr uint32_t kSmem = 1024 + (2 + kKS + kVS) * kTile + kBars * 8 + 64;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
   static_assert(kSmem > 114 * 1024, "one CTA per SM: each takes all of tensor memory");
 };
 
 // V as the MN-major operand of O += P V: 64-value rows of a key (128 bytes), swizzled; the next eight keys 1024 bytes on
-// (stride byte offset), the next 64 values of d a box of 128 keys on (leading byte offset).
-__device__ __forceinline__ uint64_t v_desc(uint32_t saddr) {
-  return uint64_t((saddr & 0x3FFFFu) >> 4) | (uint64_t(16384 >> 4) << 16) | (uint64_t(1024 >> 4) << 32) |
+// (stride byte offset), the next 64 values of d a box of keys on (leading byte offset).
+__device__ __forceinline__ uint64_t v_desc(uint32_t saddr, uint32_t box) {
+  return uint64_t((saddr & 0x3FFFFu) >> 4) | (uint64_t(box >> 4) << 16) | (uint64_t(1024 >> 4) << 32) |
          (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
 
@@ -82,6 +80,22 @@ __device__ __forceinline__ float rcp_approx(float x) {
 // cap log2(e) tanh(scale s / cap) as c - 2 c / (1 + 2^(2 scale log2(e) s / cap)): absolute error a few 2^-24 of c
 __device__ __forceinline__ float capped(float s, float cap_in, float cap_out) {
   return fmaf(-2.f * cap_out, rcp_approx(1.f + ex2_approx(s * cap_in)), cap_out);
+}
+
+// Raw sums of products into scores in log2 units: cap, then the distance bias (`at`: the row's place less the first key's)
+template <int N>
+__device__ __forceinline__ void general_scores(uint32_t (&x)[N], const PackedParams& p, bool bias, float slope2, float at) {
+  if (p.cap_out > 0.f) {
+#pragma unroll
+    for (int c = 0; c < N; ++c) x[c] = __float_as_uint(capped(__uint_as_float(x[c]), p.cap_in, p.cap_out));
+  } else {
+#pragma unroll
+    for (int c = 0; c < N; ++c) x[c] = __float_as_uint(__uint_as_float(x[c]) * p.scale_log2);
+  }
+  if (bias) {
+#pragma unroll
+    for (int c = 0; c < N; ++c) x[c] = __float_as_uint(fmaf(-slope2, fabsf(at - float(c)), __uint_as_float(x[c])));
+  }
 }
 
 struct Segment {
@@ -162,16 +176,16 @@ __device__ __noinline__ void resum_row(const PackedParams& p, int q_at, int k0, 
   }
 }
 
-template <int D, int NT, bool GEN>
+template <int D, bool GEN>
 __global__ void __launch_bounds__(kPackedThreads, 1)
     packed_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PackedParams p) {
-  using Cfg = PackedCfg<D, NT>;
+  using Cfg = PackedCfg<D>;
   constexpr int KS = Cfg::kKS, VS = Cfg::kVS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
-  uint8_t* sK = sQ + NT * Cfg::kTile;
+  uint8_t* sK = sQ + 2 * Cfg::kTile;
   uint8_t* sV = sK + KS * Cfg::kTile;
   uint64_t* q_full = reinterpret_cast<uint64_t*>(sV + VS * Cfg::kTile);
   uint64_t* drain = q_full + 1;
@@ -185,16 +199,14 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_done + 2);
   int* s_lim = reinterpret_cast<int*>(tmem_slot + 1);              // [2] keys that any row of the tile sees
   Segment* s_seg = reinterpret_cast<Segment*>(s_lim + 2);          // 20 bytes
-  float2* s_ml = reinterpret_cast<float2*>(tmem_slot + 16);        // NT = 1: [128] the odd half's maximum and sum
 
   const dit_packed_attention& a = p.a;
   const int warp = threadIdx.x >> 5, lane = lane_id();
   const int kvh = blockIdx.y, G = p.G, rpt = p.rpt;
 
   pdl_wait();
-  pdl_trigger();
   if (warp == 0) {
-    const Segment g = find_tile(a, NT * rpt, blockIdx.x);
+    const Segment g = find_tile(a, 2 * rpt, blockIdx.x);
     if (lane == 0) *s_seg = g;
   } else if (threadIdx.x == 32) {
     s_lim[0] = s_lim[1] = 0;
@@ -222,7 +234,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
   // a softmax thread's row: query row `i` of the segment, head `head`, seeing `lim` keys
   const int t = (warp - 2) >> 2, quad = warp & 3, row = quad * 32 + lane;
   const int r = row / G, g = row - r * G;
-  const int i = seg.tile * NT * rpt + (NT == 2 ? t * rpt : 0) + r;
+  const int i = (seg.tile * 2 + t) * rpt + r;
   const int head = kvh * G + g;
   const bool valid = warp >= 2 && r < rpt && i < seg.nq;
   int lim = 0;
@@ -237,33 +249,27 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // only now: a kernel that starts early on this SM finds this CTA's tensor memory taken, never the other way round
+  pdl_trigger();
   const uint32_t tmem_base = *tmem_slot;
   // this CTA's key tiles [ta, tb), and how many of them each tile (or half) takes
   const int lmax = max(s_lim[0], s_lim[1]);
   const int tiles = (lmax + 127) >> 7;
   const int ta = int((long long)tiles * blockIdx.z / p.splits), tb = int((long long)tiles * (blockIdx.z + 1) / p.splits);
-  int n0, n1;
-  if constexpr (NT == 2) {
-    n0 = min(max((s_lim[0] + 127) >> 7, ta), tb) - ta;
-    n1 = min(max((s_lim[1] + 127) >> 7, ta), tb) - ta;
-  } else {
-    n0 = (tb - ta + 1) >> 1;
-    n1 = (tb - ta) >> 1;
-  }
-  auto key_tile = [&](int tt, int it) { return NT == 2 ? it : 2 * it + tt; };  // of the CTA's
-  const int loads = NT == 2 ? max(n0, n1) : n0 + n1;
+  const int n0 = min(max((s_lim[0] + 127) >> 7, ta), tb) - ta, n1 = min(max((s_lim[1] + 127) >> 7, ta), tb) - ta;
+  const int loads = max(n0, n1);
 
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA producer
     if (loads > 0 && elect_one()) {
       const uint32_t qb = smem_u32(q_full);
-      const bool both = NT == 2 && n1 > 0, first = NT == 1 || n0 > 0;
-      mbar_arrive_expect_tx(qb, uint32_t(int(first) + int(both)) * (D / 64) * 128u * uint32_t(G * rpt));
-      for (int tt = 0; tt < NT; ++tt) {
-        if (tt == 0 ? !first : !both) continue;
+      const bool first = n0 > 0, second = n1 > 0;
+      mbar_arrive_expect_tx(qb, uint32_t(int(first) + int(second)) * (D / 64) * 128u * uint32_t(G * rpt));
+      for (int tt = 0; tt < 2; ++tt) {
+        if (tt == 0 ? !first : !second) continue;
         for (int c = 0; c < D / 64; ++c)
           tma_load_3d(smem_u32(sQ + tt * Cfg::kTile + c * Cfg::kAtom), &tmQ, qb, c * 64, kvh * G,
-                      seg.q0 + (seg.tile * NT + tt) * rpt);
+                      seg.q0 + (seg.tile * 2 + tt) * rpt);
       }
       int nk = 0, nv = 0;
       for (int j = 0; j < loads; ++j) {
@@ -293,30 +299,27 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
     if (loads > 0 && elect_one()) {
       constexpr uint32_t idesc_s = idesc_bf16(128, 128);
       constexpr uint32_t idesc_o = idesc_bf16(128, D) | (1u << 16);  // B is MN-major
-      const uint64_t dq = sw128_desc(smem_u32(sQ)), dv = v_desc(smem_u32(sV));
+      const uint64_t dq = sw128_desc(smem_u32(sQ)), dv = v_desc(smem_u32(sV), Cfg::kAtom);
       const uint32_t q_lo = uint32_t(dq), hi = uint32_t(dq >> 32);  // the high words agree: 1024-byte strides, same swizzle
       const uint32_t k_lo = uint32_t(sw128_desc(smem_u32(sK))), v_lo = uint32_t(dv);
       bool ok = mbar_wait(smem_u32(q_full), 0, p.err, kErrTimeoutMma);
       auto count = [&](int tt) { return tt == 0 ? n0 : n1; };
       auto issue_s = [&](int tt, int it) {
-        const int j = key_tile(tt, it), ks = j % KS;
+        const int ks = it % KS;
         const uint32_t d = tmem_base + uint32_t(tt * 128);
-        const uint32_t qt = q_lo + uint32_t((NT == 2 ? tt : 0) * (Cfg::kTile >> 4)), kt = k_lo + uint32_t(ks * (Cfg::kTile >> 4));
+        const uint32_t qt = q_lo + uint32_t(tt * (Cfg::kTile >> 4)), kt = k_lo + uint32_t(ks * (Cfg::kTile >> 4));
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t c = uint32_t((kk >> 2) * (Cfg::kAtom >> 4) + 2 * (kk & 3));
           umma_bf16_lo(d, qt + c, kt + c, hi, idesc_s, kk != 0);
         }
         umma_commit(smem_u32(&s_full[tt]));
-        if (NT == 1 || tt == 1 || it >= n1) umma_commit(smem_u32(&k_empty[ks]));  // the tile's last user
+        if (tt == 1 || it >= n1) umma_commit(smem_u32(&k_empty[ks]));  // the tile's last user
       };
-      auto wait_k = [&](int tt, int it) {
-        const int j = key_tile(tt, it);
-        return mbar_wait(smem_u32(&k_full[j % KS]), (j / KS) & 1, p.err, kErrTimeoutMma);
-      };
+      auto wait_k = [&](int it) { return mbar_wait(smem_u32(&k_full[it % KS]), (it / KS) & 1, p.err, kErrTimeoutMma); };
       for (int tt = 0; tt < 2 && ok; ++tt)
         if (count(tt) > 0) {
-          ok = wait_k(tt, 0);
+          ok = wait_k(0);
           if (!ok) break;
           tc_fence_after();
           issue_s(tt, 0);
@@ -327,11 +330,11 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
         for (int tt = 0; tt < 2; ++tt) {
           const int n = count(tt);
           if (it >= n) continue;
-          const int j = key_tile(tt, it), vs = j % VS;
+          const int vs = it % VS;
           // the next K lands long before this tile's weights are ready: waited for first, so that P V and the next S
           // go out back to back
-          if (it + 1 < n && !wait_k(tt, it + 1)) { ok = false; break; }
-          if (!mbar_wait(smem_u32(&v_full[vs]), (j / VS) & 1, p.err, kErrTimeoutMma)) { ok = false; break; }
+          if (it + 1 < n && !wait_k(it + 1)) { ok = false; break; }
+          if (!mbar_wait(smem_u32(&v_full[vs]), (it / VS) & 1, p.err, kErrTimeoutMma)) { ok = false; break; }
           if (!mbar_wait(smem_u32(&p_full[tt]), it & 1, p.err, kErrTimeoutMma)) { ok = false; break; }
           tc_fence_after();
           const uint32_t d = tmem_base + 256u + uint32_t(tt * D), pt = tmem_base + uint32_t(tt * 128);
@@ -339,7 +342,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)  // 16 keys a step: 2048 bytes of every box
             umma_bf16_ts_lo(d, pt + uint32_t(kk * 8), vt + uint32_t(kk * 128), hi, idesc_o, it != 0 || kk != 0);
-          if (NT == 1 || tt == 1 || it >= n1) umma_commit(smem_u32(&v_empty[vs]));
+          if (tt == 1 || it >= n1) umma_commit(smem_u32(&v_empty[vs]));
           if (it + 1 == n) umma_commit(smem_u32(&o_done[tt]));
           else issue_s(tt, it + 1);
         }
@@ -361,7 +364,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     for (int it = 0; it < n; ++it) {
-      const int j = key_tile(t, it), key0 = (ta + j) * 128;
+      const int key0 = (ta + it) * 128;
       if (!mbar_wait_warp(smem_u32(&s_full[t]), it & 1, p.err, kErrTimeoutSoftmax)) { ok = false; break; }
       tc_fence_after();
       if (live) {
@@ -369,20 +372,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(tS + uint32_t(c * 32), *reinterpret_cast<uint32_t(*)[32]>(&x[c * 32]));
         tmem_ld_wait();
-        if constexpr (GEN) {
-          if (p.cap_out > 0.f) {
-#pragma unroll
-            for (int c = 0; c < 128; ++c) x[c] = __float_as_uint(capped(__uint_as_float(x[c]), p.cap_in, p.cap_out));
-          } else {
-#pragma unroll
-            for (int c = 0; c < 128; ++c) x[c] = __float_as_uint(__uint_as_float(x[c]) * p.scale_log2);
-          }
-          if (a.slope) {
-            const float at = where - float(key0);
-#pragma unroll
-            for (int c = 0; c < 128; ++c) x[c] = __float_as_uint(fmaf(-slope2, fabsf(at - float(c)), __uint_as_float(x[c])));
-          }
-        }
+        if constexpr (GEN) general_scores(x, p, a.slope != nullptr, slope2, where - float(key0));
         const int seen = lim - key0;
         if (!__all_sync(0xffffffffu, seen >= 128)) {
 #pragma unroll
@@ -441,14 +431,14 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
       }
       // rows of V that no row of the CTA sees, zeroed by the first group that uses the tile
       const int vz = lmax - key0;
-      if (vz < 128 && (NT == 1 || t == 0 || it >= n0)) {
-        if (!mbar_wait_warp(smem_u32(&v_full[j % VS]), (j / VS) & 1, p.err, kErrTimeoutSoftmax)) { ok = false; break; }
+      if (vz < 128 && (t == 0 || it >= n0)) {
+        if (!mbar_wait_warp(smem_u32(&v_full[it % VS]), (it / VS) & 1, p.err, kErrTimeoutSoftmax)) { ok = false; break; }
         if (row >= vz)
 #pragma unroll
           for (int c = 0; c < D / 64; ++c)
 #pragma unroll
             for (int v = 0; v < 8; ++v)
-              *reinterpret_cast<uint4*>(sV + (j % VS) * Cfg::kTile + c * Cfg::kAtom + row * 128 + v * 16) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(sV + (it % VS) * Cfg::kTile + c * Cfg::kAtom + row * 128 + v * 16) = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
       }
       tc_fence_before();
@@ -456,75 +446,28 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
       if (lane == 0) mbar_arrive(smem_u32(&p_full[t]));
     }
 
-    // ---- the end of the key range. `mine`: this group stores rows (both, or the first after the halves have met)
+    // ---- the end of the key range
     if (n > 0 && ok) ok = mbar_wait_warp(smem_u32(&o_done[t]), 0, p.err, kErrTimeoutSoftmax);
-    bool mine = NT == 2 || t == 0;
-    float c0 = 1.f, c1 = 0.f;  // factors of the own and of the odd half's O
-    const float4* other = reinterpret_cast<const float4*>(sK) + row;  // [D / 4][128 rows]
-    if constexpr (NT == 1) {
-      // the odd half goes through the K ring, which both halves' MMAs have read by then
-      if (t == 1 && n1 > 0) {
-        if (ok && n0 > 0) ok = mbar_wait_warp(smem_u32(&o_done[0]), 0, p.err, kErrTimeoutSoftmax);
-        if (ok && live) {
-          tc_fence_after();
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32(tO + uint32_t(c * 32), o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int v = 0; v < 8; ++v)
-              reinterpret_cast<uint4*>(sK)[(c * 8 + v) * 128 + row] = make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
-          }
-        }
-        s_ml[row] = make_float2(m, l);
-      }
-      if (n1 > 0) asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (t == 0 && n1 > 0) {
-        const float2 ml = s_ml[row];
-        const float top = fmaxf(m, ml.x), base = top == -INFINITY ? 0.f : top;
-        c0 = ex2_approx(m - base);
-        c1 = ex2_approx(ml.x - base);
-        l = l * c0 + ml.y * c1;
-        m = top;
-      }
-    }
-    if (mine && ok) {
+    if (ok) {
       tc_fence_after();
       const bool whole = p.splits == 1;
-      const int covered = NT == 2 ? (ta + n) * 128 : tb * 128;  // keys behind the last tile of this row's sums
+      const int covered = (ta + n) * 128;  // keys behind the last tile of this row's sums
       const int last = min(lmax, covered);
-      uint8_t* stage = sQ + (NT == 2 ? t : 0) * Cfg::kTile;  // Q has been read; [row][D] bf16, chunks swizzled by the row
+      uint8_t* stage = sQ + t * Cfg::kTile;  // Q has been read; [row][D] bf16, chunks swizzled by the row
       const float inv = whole ? (l > 0.f || l != l ? 1.f / l : 0.f) : 1.f;
       const long long at = (long long)blockIdx.z * a.q_rows + seg.q0 + i;  // row of the partial sums
       float4* po = reinterpret_cast<float4*>(p.part_o + (at * a.heads + head) * D);
       float bad = 0.f;
-      if (live && n0 + n1 > 0) {
+      if (live && n > 0) {
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           float o[32];
           uint32_t raw[32];
-          if (NT == 2 ? n > 0 : true) {
-            tmem_ld32(tO + uint32_t(c * 32), raw);
-            tmem_ld_wait();
-          }
-#pragma unroll
-          for (int v = 0; v < 32; ++v) o[v] = n > 0 && c0 > 0.f ? __uint_as_float(raw[v]) * c0 : 0.f;
-          if (NT == 1 && n1 > 0) {
-#pragma unroll
-            for (int v = 0; v < 8; ++v) {
-              const float4 q = other[(c * 8 + v) * 128];
-              if (c1 > 0.f) {
-                o[4 * v] = fmaf(q.x, c1, o[4 * v]);
-                o[4 * v + 1] = fmaf(q.y, c1, o[4 * v + 1]);
-                o[4 * v + 2] = fmaf(q.z, c1, o[4 * v + 2]);
-                o[4 * v + 3] = fmaf(q.w, c1, o[4 * v + 3]);
-              }
-            }
-          }
+          tmem_ld32(tO + uint32_t(c * 32), raw);
+          tmem_ld_wait();
 #pragma unroll
           for (int v = 0; v < 32; ++v) {
-            if (lim == 0) o[v] = 0.f;
+            o[v] = lim > 0 ? __uint_as_float(raw[v]) : 0.f;
             bad = fmaf(o[v], 0.f, bad);
             o[v] *= inv;
           }
@@ -577,7 +520,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
         constexpr int per = 32 / (D / 8);
         for (int rr = lane / (D / 8); rr < 32; rr += per) {
           const int srow = quad * 32 + rr, sr = srow / G, sg = srow - sr * G, c = lane % (D / 8);
-          const int si = seg.tile * NT * rpt + (NT == 2 ? t * rpt : 0) + sr;
+          const int si = (seg.tile * 2 + t) * rpt + sr;
           if (sr >= rpt || si >= seg.nq) continue;
           const uint4 v = *reinterpret_cast<const uint4*>(stage + srow * (D * 2) + ((c ^ (srow & 7)) << 4));
           *reinterpret_cast<uint4*>(a.o + (seg.q0 + si) * a.o_row + (kvh * G + sg) * a.o_head + c * 8) = v;
@@ -590,6 +533,339 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem_base, 512);
+}
+
+// ------------------------------------------------------------------------------------------
+// Few rows over many keys: HBM-bound. One tile of up to 128 (row, head) pairs per CTA, key tiles of 64, two CTAs to an SM
+// (256 columns of tensor memory and at most 113 KB of shared memory each), so that one CTA's start and end run under the
+// other's loads. K and V tiles come through one ring in the order in which the MMAs use them: K0 K1 V0 K2 V1 ... The
+// scores of tile j + 1 are computed while the softmax works on tile j. Q takes only the rows it has: the MMA's other
+// rows read what follows in shared memory, and nothing reads their results.
+// Tensor memory (256 columns): [0, 64) and [64, 128) S of even and odd tiles, P over them   [128, 128 + d) O
+// ------------------------------------------------------------------------------------------
+constexpr int kRowKeys = 64, kRowSlotsMost = 12, kRowThreads = 192;
+constexpr uint32_t kRowSmem = 113 * 1024, kRowBars = 8 * (2 * kRowSlotsMost + 8) + 64;
+
+// Place of a key tile's K and V in the ring's order, for n tiles
+__device__ __forceinline__ int place_k(int j) { return j == 0 ? 0 : 2 * j - 1; }
+__device__ __forceinline__ int place_v(int j, int n) { return j + 1 < n ? 2 * j + 2 : 2 * j + 1; }
+
+template <int D, bool GEN>
+__global__ void __launch_bounds__(kRowThreads, 2)
+    packed_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PackedParams p) {
+  constexpr uint32_t kSlot = kRowKeys * D * 2, kBox = kRowKeys * 128;  // a tile of K or V; its boxes of 64 values
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t q_box = uint32_t((p.G * p.rpt + 7) & ~7) * 128u;
+  const int T = p.slots;
+  uint8_t* sQ = smem;
+  uint8_t* ring = sQ + q_box * (D / 64);
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + T * kSlot);  // [T]
+  uint64_t* empty = full + kRowSlotsMost;                          // [T]
+  uint64_t* q_full = empty + kRowSlotsMost;
+  uint64_t* s_full = q_full + 1;   // [2]
+  uint64_t* p_full = s_full + 2;   // [2]
+  uint64_t* pv_done = p_full + 2;  // a phase per key tile
+  uint64_t* o_done = pv_done + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_done + 1);
+  int* s_lim = reinterpret_cast<int*>(tmem_slot + 1);
+  Segment* s_seg = reinterpret_cast<Segment*>(s_lim + 1);
+
+  const dit_packed_attention& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = lane_id();
+  const int kvh = blockIdx.y, G = p.G, rpt = p.rpt;
+
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 256);
+    tmem_relinquish();
+  } else if (threadIdx.x == 64) {
+    *s_lim = 0;
+    for (int i = 0; i < T; ++i) {
+      mbar_init(smem_u32(&full[i]), 1);
+      mbar_init(smem_u32(&empty[i]), 1);
+    }
+    mbar_init(smem_u32(q_full), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&s_full[i]), 1);
+      mbar_init(smem_u32(&p_full[i]), 4);
+    }
+    mbar_init(smem_u32(pv_done), 1);
+    mbar_init(smem_u32(o_done), 1);
+    fence_mbar_init();
+  }
+  pdl_wait();
+  if (warp == 0) {
+    const Segment g = find_tile(a, rpt, blockIdx.x);
+    if (lane == 0) *s_seg = g;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // only now: a kernel that starts early on this SM finds this CTA's tensor memory taken, never the other way round
+  pdl_trigger();
+  const uint32_t tmem_base = *tmem_slot;
+  const Segment seg = *s_seg;
+
+  // a softmax thread's row: query row `i` of the segment, head `head`, seeing `lim` keys
+  const int quad = warp & 3, row = quad * 32 + lane;
+  const int r = row / G, g = row - r * G;
+  const int i = seg.tile * rpt + r, head = kvh * G + g;
+  const bool valid = warp >= 2 && seg.tile >= 0 && r < rpt && i < seg.nq;
+  int lim = 0;
+  if (warp >= 2) {
+    if (valid) lim = a.visible ? min(max(__ldg(a.visible + seg.q0 + i), 0), seg.nk) : seg.nk;
+    const int top = __reduce_max_sync(0xffffffffu, lim);
+    if (lane == 0 && top > 0) atomicMax(s_lim, top);
+  }
+  __syncthreads();
+  const int lmax = *s_lim, tiles = (lmax + kRowKeys - 1) / kRowKeys;
+  const int ta = int((long long)tiles * blockIdx.z / p.splits), tb = int((long long)tiles * (blockIdx.z + 1) / p.splits);
+  const int n = tb - ta;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ TMA producer
+    if (n > 0 && elect_one()) {
+      const uint32_t qb = smem_u32(q_full);
+      mbar_arrive_expect_tx(qb, (D / 64) * 128u * uint32_t(G * rpt));
+      for (int c = 0; c < D / 64; ++c)
+        tma_load_3d(smem_u32(sQ + c * q_box), &tmQ, qb, c * 64, kvh * G, seg.q0 + seg.tile * rpt);
+      int x = 0;
+      bool ok = true;
+      auto load = [&](const CUtensorMap* m, int j) {
+        const int slot = x % T;
+        if (!mbar_wait(smem_u32(&empty[slot]), ((x / T) & 1) ^ 1, p.err, kErrTimeoutProducer)) { ok = false; return; }
+        const uint32_t fb = smem_u32(&full[slot]);
+        mbar_arrive_expect_tx(fb, kSlot);
+        for (int c = 0; c < D / 64; ++c)
+          tma_load_3d(smem_u32(ring + slot * kSlot + c * kBox), m, fb, c * 64, kvh, seg.k0 + (ta + j) * kRowKeys);
+        ++x;
+      };
+      load(&tmK, 0);
+      for (int j = 0; j < n && ok; ++j) {
+        if (j + 1 < n) load(&tmK, j + 1);
+        if (ok) load(&tmV, j);
+      }
+      // every issued copy lands before the CTA exits, whatever the error word says
+      mbar_wait_cluster(qb, 0, p.err, kErrTimeoutDrain, 4 * kWaitLimitNs, false);
+      for (int y = max(0, x - T); y < x; ++y)
+        mbar_wait_cluster(smem_u32(&full[y % T]), (y / T) & 1, p.err, kErrTimeoutDrain, 4 * kWaitLimitNs, false);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA issuer
+    if (n > 0 && elect_one()) {
+      constexpr uint32_t idesc_s = idesc_bf16(128, kRowKeys);
+      constexpr uint32_t idesc_o = idesc_bf16(128, D) | (1u << 16);  // B is MN-major
+      const uint64_t dq = sw128_desc(smem_u32(sQ));
+      const uint32_t q_lo = uint32_t(dq), hi = uint32_t(dq >> 32);
+      const uint32_t k_lo = uint32_t(sw128_desc(smem_u32(ring))), v_lo = uint32_t(v_desc(smem_u32(ring), kBox));
+      auto landed = [&](int x) { return mbar_wait(smem_u32(&full[x % T]), (x / T) & 1, p.err, kErrTimeoutMma); };
+      auto issue_s = [&](int j) {
+        const int x = place_k(j);
+        const uint32_t kt = k_lo + uint32_t((x % T) * (kSlot >> 4)), d = tmem_base + uint32_t((j & 1) * kRowKeys);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_bf16_lo(d, q_lo + uint32_t((kk >> 2) * (q_box >> 4) + 2 * (kk & 3)),
+                       kt + uint32_t((kk >> 2) * (kBox >> 4) + 2 * (kk & 3)), hi, idesc_s, kk != 0);
+        umma_commit(smem_u32(&s_full[j & 1]));
+        umma_commit(smem_u32(&empty[x % T]));
+      };
+      bool ok = mbar_wait(smem_u32(q_full), 0, p.err, kErrTimeoutMma);
+      for (int j = 0; j < 2 && j < n && ok; ++j) {
+        ok = landed(place_k(j));
+        if (!ok) break;
+        tc_fence_after();
+        issue_s(j);
+      }
+      for (int j = 0; j < n && ok; ++j) {
+        const int x = place_v(j, n);
+        if (!landed(x) || !mbar_wait(smem_u32(&p_full[j & 1]), (j >> 1) & 1, p.err, kErrTimeoutMma)) break;
+        tc_fence_after();
+        const uint32_t vt = v_lo + uint32_t((x % T) * (kSlot >> 4)), pt = tmem_base + uint32_t((j & 1) * kRowKeys);
+#pragma unroll
+        for (int kk = 0; kk < kRowKeys / 16; ++kk)
+          umma_bf16_ts_lo(tmem_base + 128u, pt + uint32_t(kk * 8), vt + uint32_t(kk * 128), hi, idesc_o, j != 0 || kk != 0);
+        umma_commit(smem_u32(&empty[x % T]));
+        umma_commit(smem_u32(pv_done));
+        if (j + 2 < n) {
+          if (!landed(place_k(j + 2))) break;
+          tc_fence_after();
+          issue_s(j + 2);
+        }
+      }
+      // every MMA has completed before tensor memory is given back (also where a wait gave up)
+      umma_commit(smem_u32(o_done));
+      mbar_wait_cluster(smem_u32(o_done), 0, p.err, kErrTimeoutDrain, 4 * kWaitLimitNs, false);
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax warps, one row per thread
+    const uint32_t lane_off = uint32_t(quad * 32) << 16;
+    const uint32_t tO = tmem_base + lane_off + 128u;
+    const bool live = __any_sync(0xffffffffu, lim > 0);  // warps without a row that sees a key only keep the barriers
+    const float where = float(i + seg.nk - seg.nq);      // the row's place among the keys
+    float slope2 = 0.f;
+    if constexpr (GEN)
+      if (a.slope && valid) slope2 = 1.4426950408889634f * __ldg(a.slope + head);
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      const int key0 = (ta + j) * kRowKeys;
+      const uint32_t tS = tmem_base + lane_off + uint32_t((j & 1) * kRowKeys);
+      if (!mbar_wait_warp(smem_u32(&s_full[j & 1]), (j >> 1) & 1, p.err, kErrTimeoutSoftmax)) { ok = false; break; }
+      tc_fence_after();
+      if (live) {
+        uint32_t x[64];
+        tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
+        tmem_ld32(tS + 32u, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
+        tmem_ld_wait();
+        if constexpr (GEN) general_scores(x, p, a.slope != nullptr, slope2, where - float(key0));
+        const int seen = lim - key0;
+        if (!__all_sync(0xffffffffu, seen >= kRowKeys)) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            if (c >= seen) x[c] = 0xff800000u;
+        }
+        float m4[4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) m4[v] = fmax3(__uint_as_float(x[v]), __uint_as_float(x[v + 4]), __uint_as_float(x[v + 8]));
+#pragma unroll
+        for (int c = 12; c < 60; c += 8)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) m4[v] = fmax3(m4[v], __uint_as_float(x[c + v]), __uint_as_float(x[c + 4 + v]));
+        float mx = fmax3(fmax3(m4[0], m4[1], m4[2]), m4[3], __uint_as_float(x[60]));
+        mx = fmax3(mx, fmaxf(__uint_as_float(x[61]), __uint_as_float(x[62])), __uint_as_float(x[63]));
+        if constexpr (!GEN) mx *= p.scale_log2;
+        float alpha = 1.f;
+        if (mx > m + kRescaleStep) {  // also on the first tile with a key (m = -inf)
+          alpha = ex2_approx(m - mx);
+          m = mx;
+        }
+        const float base = m == -INFINITY ? 0.f : m;  // nothing seen yet: weights 2^-inf = 0
+        const float scale = GEN ? 1.f : p.scale_log2;
+        const uint64_t scale2 = f2_pack(scale, scale), neg2 = f2_pack(-base, -base);
+        uint64_t sum2[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int v = 0; v < 16; ++v) {
+            const int k0 = c * 32 + 2 * v;
+            const uint64_t s2 = f2_pack(__uint_as_float(x[k0]), __uint_as_float(x[k0 + 1]));
+            const uint64_t e2 = GEN ? f2_add(s2, neg2) : f2_fma(s2, scale2, neg2);
+            const float w0 = ex2_approx(f2_lo(e2)), w1 = ex2_approx(f2_hi(e2));
+            sum2[v & 3] = f2_add(sum2[v & 3], f2_pack(w0, w1));
+            pk[v] = pack_bf16x2(w0, w1);
+          }
+          tmem_st16(tS + uint32_t(c * 16), pk);
+        }
+        const uint64_t s4 = f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3]));
+        l = fmaf(l, alpha, f2_lo(s4) + f2_hi(s4));
+        if (j > 0 && __any_sync(0xffffffffu, alpha < 1.0f)) {
+          // O holds earlier tiles: the last P V must be done. (This S came after the P V before that one, so its phase is the
+          // barrier's current one or has just completed, and the parity tells the two apart.)
+          if (!mbar_wait_warp(smem_u32(pv_done), (j - 1) & 1, p.err, kErrTimeoutSoftmax)) { ok = false; break; }
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tO + uint32_t(c * 32), o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int v = 0; v < 32; ++v) o[v] = __float_as_uint(__uint_as_float(o[v]) * alpha);
+            tmem_st32(tO + uint32_t(c * 32), o);
+          }
+        }
+        tmem_st_wait();
+      }
+      // rows of V that no row of the CTA sees
+      const int vz = lmax - key0;
+      if (vz < kRowKeys) {
+        const int x = place_v(j, n);
+        if (!mbar_wait_warp(smem_u32(&full[x % T]), (x / T) & 1, p.err, kErrTimeoutSoftmax)) { ok = false; break; }
+        if ((row >> 1) >= vz) {  // two threads to a key's row
+          uint8_t* at = ring + (x % T) * kSlot + (row >> 1) * 128 + (row & 1) * 64;
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) *reinterpret_cast<uint4*>(at + c * kBox + v * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&p_full[j & 1]));
+    }
+
+    if (n > 0 && ok) ok = mbar_wait_warp(smem_u32(o_done), 0, p.err, kErrTimeoutSoftmax);
+    const bool any = __any_sync(0xffffffffu, valid);
+    if (ok && any) {
+      tc_fence_after();
+      const bool whole = p.splits == 1;
+      const int covered = tb * kRowKeys, last = min(lmax, covered);
+      const float inv = whole ? (l > 0.f || l != l ? 1.f / l : 0.f) : 1.f;
+      const long long at = ((long long)blockIdx.z * a.q_rows + seg.q0 + i) * a.heads + head;  // of the partial sums
+      uint16_t* po = a.o + (seg.q0 + i) * a.o_row + head * a.o_head;
+      float bad = 0.f;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t raw[32];
+        if (n > 0) {
+          tmem_ld32(tO + uint32_t(c * 32), raw);
+          tmem_ld_wait();
+        }
+        float o[32];
+#pragma unroll
+        for (int v = 0; v < 32; ++v) {
+          o[v] = n > 0 && lim > 0 ? __uint_as_float(raw[v]) : 0.f;
+          bad = fmaf(o[v], 0.f, bad);
+          o[v] *= inv;
+        }
+        if (!valid) continue;
+        if (whole) {
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            *reinterpret_cast<uint4*>(po + c * 32 + v * 8) =
+                make_uint4(pack_bf16x2(o[8 * v], o[8 * v + 1]), pack_bf16x2(o[8 * v + 2], o[8 * v + 3]),
+                           pack_bf16x2(o[8 * v + 4], o[8 * v + 5]), pack_bf16x2(o[8 * v + 6], o[8 * v + 7]));
+        } else if (n > 0) {
+#pragma unroll
+          for (int v = 0; v < 8; ++v)
+            reinterpret_cast<float4*>(p.part_o + at * D)[c * 8 + v] = make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+        }
+      }
+      if (valid) {
+        if (!whole) p.part_ml[at] = make_float2(m == -INFINITY && l != l ? 0.f : m, l);  // scores all NaN: seen
+        else if (a.lse)
+          a.lse[(long long)head * a.q_rows + seg.q0 + i] =
+              l > 0.f || l != l ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+      }
+      // rows with something that is not finite beside keys they do not see
+      unsigned again = __ballot_sync(0xffffffffu, valid && bad != 0.f && lim < last);
+      while (again) {
+        const int src = __ffs(again) - 1;
+        again &= again - 1;
+        const int si = __shfl_sync(0xffffffffu, i, src), sh = __shfl_sync(0xffffffffu, head, src);
+        const int end = __shfl_sync(0xffffffffu, min(lim, covered), src);
+        const float sm = __shfl_sync(0xffffffffu, m == -INFINITY ? 0.f : m, src), sinv = __shfl_sync(0xffffffffu, inv, src);
+        float acc[D / 32];
+        resum_row<D, GEN>(p, seg.q0 + si, seg.k0, ta * kRowKeys, end, sh, kvh, __shfl_sync(0xffffffffu, where, src), sm, acc);
+        if (whole) {
+          uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + (seg.q0 + si) * a.o_row + sh * a.o_head + lane * (D / 32));
+#pragma unroll
+          for (int v = 0; v < D / 64; ++v) dst[v] = pack_bf16x2(acc[2 * v] * sinv, acc[2 * v + 1] * sinv);
+        } else {
+          float* dst = p.part_o + (((long long)blockIdx.z * a.q_rows + seg.q0 + si) * a.heads + sh) * D + lane * (D / 32);
+#pragma unroll
+          for (int v = 0; v < D / 32; ++v) dst[v] = acc[v];
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem_base, 256);
 }
 
 // The parts of a split key range joined, a warp per (row, head): weights 2^(m_z - max m), parts without a key skipped
@@ -640,11 +916,12 @@ __global__ void __launch_bounds__(256) packed_join_kernel(const __grid_constant_
     a.lse[(long long)head * a.q_rows + q] = l > 0.f || l != l ? (top + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
-// Tiles, CTAs and key splits of a call. Segments of few rows (no more than a tile holds, on average) take one tile per
-// CTA. The key range is split where the tiles leave SMs idle: one wave's worth for whole tiles, several for single
-// rows, whose segments are of unlike length; never below four key tiles to a part of an average segment.
+// Tiles, CTAs and key splits of a call. Segments whose rows fit one tile, on average, go to the few-rows kernel, in tiles of
+// the average's rows (32 (row, head) pairs at least: a tile's rows are shared memory). The key range is split where the
+// tiles leave SMs idle.
 struct PackedPlan {
-  int G, rpt, nt, splits;
+  int G, rpt, slots, splits;
+  bool few;
   long long tiles;
   size_t part_bytes;
 };
@@ -652,13 +929,30 @@ PackedPlan packed_plan(int q_rows, int k_rows, int segments, int heads, int kv_h
   PackedPlan r{};
   r.G = heads / kv_heads;
   r.rpt = 128 / r.G;
-  r.nt = (long long)q_rows <= (long long)segments * r.rpt ? 1 : 2;
-  const long long rows = (long long)r.nt * r.rpt;
+  r.few = (long long)q_rows <= (long long)segments * r.rpt;
+  if (r.few) r.rpt = std::min(r.rpt, std::max(32 / r.G, std::max(1, (q_rows + segments - 1) / segments)));
+  const long long rows = (r.few ? 1LL : 2LL) * r.rpt;
   r.tiles = std::min<long long>((q_rows + segments * (rows - 1)) / rows, q_rows);
+  const uint32_t q_bytes = uint32_t((r.G * r.rpt + 7) / 8 * 8) * d * 2;
+  r.slots = std::min<int>(kRowSlotsMost, int((kRowSmem - 1024 - kRowBars - q_bytes) / (kRowKeys * d * 2)));
   const long long units = r.tiles * kv_heads, sms = std::max(num_sms(), 1);
-  const long long key_tiles = (k_rows / segments + 127) / 128;
-  const long long want = r.nt == 1 ? (4 * sms + units - 1) / units : sms / units;
-  r.splits = int(std::max<long long>(1, std::min<long long>({want, key_tiles / 4, (long long)kMaxSplits})));
+  const long long keys = k_rows / segments;
+  // Few rows, two CTAs to an SM: with fewer tiles than those, one wave of parts of 256 keys at least (1 row, 24 heads, 1088 keys:
+  // 16.0 us whole, 10.9 in four; 32 tiles over 4000 keys: 45.2 whole, 15.9 in eight, 22.0 in twelve, which is more than a
+  // wave); with more, six waves of parts of 1024 keys at least, which evens out unlike lengths (512 tiles over 2048 to 8192
+  // keys: 257 us whole, 229 in four, 253 in eight). Whole tiles: only where a wave of them would fit twice.
+  long long want, least;
+  if (!r.few) {
+    want = sms / units;
+    least = 512;
+  } else if (units <= 2 * sms) {
+    want = 2 * sms / units;
+    least = 256;
+  } else {
+    want = (12 * sms + units - 1) / units;
+    least = 1024;
+  }
+  r.splits = int(std::max<long long>(1, std::min<long long>({want, keys / least, (long long)kMaxSplits})));
   r.part_bytes = r.splits > 1 ? (size_t(r.splits) * q_rows * heads * (size_t(d) * 4 + 8) + 255) / 256 * 256 : 0;
   return r;
 }
@@ -675,21 +969,29 @@ bool packed_map(CUtensorMap* m, const void* base, int d, int heads, int rows, lo
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int NT, bool GEN>
+template <int D, bool FEW, bool GEN>
 int packed_go(const PackedParams& p, const PackedPlan& pl, cudaStream_t st) {
-  using Cfg = PackedCfg<D, NT>;
   const dit_packed_attention& a = p.a;
+  constexpr int kKeys = FEW ? kRowKeys : 128;
   CUtensorMap tq, tk, tv;
   const bool keys = a.k_rows > 0;  // none: the maps are not read
   if (!packed_map(&tq, a.q, D, a.heads, a.q_rows, a.q_head, a.q_row, pl.G, pl.rpt) ||
-      !packed_map(&tk, keys ? a.k : a.q, D, a.kv_heads, keys ? a.k_rows : 1, keys ? a.k_head : a.q_head, a.k_row, 1, 128) ||
-      !packed_map(&tv, keys ? a.v : a.q, D, a.kv_heads, keys ? a.k_rows : 1, keys ? a.v_head : a.q_head, a.v_row, 1, 128))
+      !packed_map(&tk, keys ? a.k : a.q, D, a.kv_heads, keys ? a.k_rows : 1, keys ? a.k_head : a.q_head, a.k_row, 1, kKeys) ||
+      !packed_map(&tv, keys ? a.v : a.q, D, a.kv_heads, keys ? a.k_rows : 1, keys ? a.v_head : a.q_head, a.v_row, 1, kKeys))
     return DIT_ECUDA;
-  auto kern = packed_kernel<D, NT, GEN>;
-  if (!smem_attr_once(reinterpret_cast<const void*>(kern), Cfg::kSmem)) return DIT_ECUDA;
-  if (launch_pdl(kern, dim3(unsigned(pl.tiles), unsigned(a.kv_heads), unsigned(p.splits)), dim3(kPackedThreads), Cfg::kSmem,
-                 st, 1, tq, tk, tv, p) != cudaSuccess)
-    return DIT_ECUDA;
+  const dim3 grid(unsigned(pl.tiles), unsigned(a.kv_heads), unsigned(p.splits));
+  cudaError_t e;
+  if constexpr (FEW) {
+    auto kern = packed_rows_kernel<D, GEN>;
+    if (!smem_attr_once(reinterpret_cast<const void*>(kern), kRowSmem)) return DIT_ECUDA;
+    e = launch_pdl(kern, grid, dim3(kRowThreads), kRowSmem, st, 1, tq, tk, tv, p);
+  } else {
+    using Cfg = PackedCfg<D>;
+    auto kern = packed_kernel<D, GEN>;
+    if (!smem_attr_once(reinterpret_cast<const void*>(kern), Cfg::kSmem)) return DIT_ECUDA;
+    e = launch_pdl(kern, grid, dim3(kPackedThreads), Cfg::kSmem, st, 1, tq, tk, tv, p);
+  }
+  if (e != cudaSuccess) return DIT_ECUDA;
   if (p.splits > 1) {
     const long long units = (long long)a.q_rows * a.heads;
     if (launch_pdl(packed_join_kernel<D>, dim3(unsigned((units + 7) / 8)), dim3(256), 0, st, 1, p) != cudaSuccess) return DIT_ECUDA;
@@ -700,8 +1002,8 @@ int packed_go(const PackedParams& p, const PackedPlan& pl, cudaStream_t st) {
 template <int D>
 int packed_kind(const PackedParams& p, const PackedPlan& pl, cudaStream_t st) {
   const bool gen = p.cap_out > 0.f || p.a.slope;
-  if (pl.nt == 1) return gen ? packed_go<D, 1, true>(p, pl, st) : packed_go<D, 1, false>(p, pl, st);
-  return gen ? packed_go<D, 2, true>(p, pl, st) : packed_go<D, 2, false>(p, pl, st);
+  if (pl.few) return gen ? packed_go<D, true, true>(p, pl, st) : packed_go<D, true, false>(p, pl, st);
+  return gen ? packed_go<D, false, true>(p, pl, st) : packed_go<D, false, false>(p, pl, st);
 }
 
 bool packed_al16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
@@ -738,6 +1040,7 @@ int packed_attention_launch(const dit_packed_attention& a, void* ws, size_t ws_b
   p.a = a;
   p.G = pl.G;
   p.rpt = pl.rpt;
+  p.slots = pl.slots;
   p.splits = pl.splits > 1 && ws && ws_bytes >= pl.part_bytes ? pl.splits : 1;
   p.part_o = static_cast<float*>(ws);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + size_t(p.splits) * a.q_rows * a.heads * a.head_dim);
