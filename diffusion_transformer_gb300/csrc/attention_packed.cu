@@ -12,8 +12,9 @@
 // r, head g of the G), so K and V are read once for all of them. K and V are rows of any stride: both come by TMA as
 // [keys, d] boxes, and V enters its MMA as an MN-major operand, so nothing is transposed in memory. CTAs find their segment
 // by a scan over q_start: no lengths on the host, and a captured graph serves other lengths. packed_kernel takes two tiles
-// of a segment per CTA, roles as in the joint attention: warp 0 loads, warp 1 issues the MMAs, warps 2-5 and 6-9 turn the
-// scores of the two tiles into weights, so that one tile's exponentials overlap the other's MMAs. packed_rows_kernel takes
+// of a segment per CTA: warp 0 loads, warp 1 issues the MMAs, warps 2-9 and 10-17 turn the scores of the two tiles into
+// weights, so that one tile's exponentials overlap the other's MMAs; a row's 128 keys of a tile are two threads' work, who
+// exchange their maxima through shared memory (eight warps with whole rows: PLAIN8 us where these take PLAIN16). packed_rows_kernel takes
 // segments of few rows, two CTAs to an SM. Where there are too few tiles for the SMs the key range is split over CTAs
 // (blockIdx.z) and a second kernel joins the parts in order.
 // Masked places: weights of masked keys are zero, the rows of V behind the last key that any row of the CTA sees are
@@ -21,7 +22,8 @@
 // its tile held keys that it does not see is summed again over its own keys (resum_row): NaN or infinity in a masked
 // place never reaches it.
 //
-// Tensor memory (512 columns): [0, 128) S0, P0 over it   [128, 256) S1 / P1   [256, 256 + d) O0   [256 + d, 256 + 2 d) O1
+// Tensor memory (512 columns): [0, 128) S0, P0 over it: 32 columns at 0 for keys
+// 0-63, 32 at 64 for keys 64-127   [128, 256) S1 / P1   [256, 256 + d) O0   [256 + d, 256 + 2 d) O1
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -40,7 +42,7 @@ namespace {
 
 constexpr float kRescaleStep = 8.0f;  // log2 units: the running maximum moves only past this, so weights stay below 2^8
 constexpr int kMaxSplits = 32;
-constexpr int kPackedThreads = 320;
+constexpr int kPackedThreads = 64 + 32 * 16;  // loader, MMA issuer, sixteen softmax warps
 
 struct PackedParams {
   dit_packed_attention a;
@@ -58,8 +60,9 @@ struct PackedCfg {
   static constexpr uint32_t kTile = 128 * D * 2;  // 128 rows of q, k or v
   static constexpr uint32_t kAtom = 128 * 128;    // [128 rows x 64 bf16], 128-byte swizzled
   static constexpr int kKS = D == 128 ? 3 : 4, kVS = D == 128 ? 2 : 4;
-  static constexpr int kBars = 2 + 2 * kKS + 2 * kVS + 6;
-  static constexpr uint32_t kSmem = 1024 + (2 + kKS + kVS) * kTile + kBars * 8 + 64;
+  static constexpr int kBars = 2 + 2 * kKS + 2 * kVS + 8;
+  // (768: what a base on 256 bytes can be off the tiles' 1024)
+  static constexpr uint32_t kSmem = 768 + (2 + kKS + kVS) * kTile + kBars * 8 + 64 + 2 * 2 * 128 * 4;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
   static_assert(kSmem > 114 * 1024, "one CTA per SM: each takes all of tensor memory");
 };
@@ -96,6 +99,18 @@ __device__ __forceinline__ void general_scores(uint32_t (&x)[N], const PackedPar
 #pragma unroll
     for (int c = 0; c < N; ++c) x[c] = __float_as_uint(fmaf(-slope2, fabsf(at - float(c)), __uint_as_float(x[c])));
   }
+}
+
+__device__ __forceinline__ float max64(const uint32_t (&x)[64]) {
+  float m4[4];
+#pragma unroll
+  for (int v = 0; v < 4; ++v) m4[v] = fmax3(__uint_as_float(x[v]), __uint_as_float(x[v + 4]), __uint_as_float(x[v + 8]));
+#pragma unroll
+  for (int c = 12; c < 60; c += 8)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) m4[v] = fmax3(m4[v], __uint_as_float(x[c + v]), __uint_as_float(x[c + 4 + v]));
+  const float a = fmax3(m4[0], m4[1], m4[2]), b = fmax3(m4[3], __uint_as_float(x[60]), __uint_as_float(x[61]));
+  return fmaxf(a, fmax3(b, __uint_as_float(x[62]), __uint_as_float(x[63])));
 }
 
 struct Segment {
@@ -182,7 +197,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PackedParams p) {
   using Cfg = PackedCfg<D>;
   constexpr int KS = Cfg::kKS, VS = Cfg::kVS;
-  extern __shared__ uint8_t smem_raw[];
+  extern __shared__ __align__(256) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
   uint8_t* sK = sQ + 2 * Cfg::kTile;
@@ -194,11 +209,13 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
   uint64_t* v_full = k_empty + KS;   // [VS]
   uint64_t* v_empty = v_full + VS;   // [VS]
   uint64_t* s_full = v_empty + VS;   // [2]
-  uint64_t* p_full = s_full + 2;     // [2]
+  uint64_t* p_half = s_full + 2;     // [2] the first half of each key half's weights stored
+  uint64_t* p_full = p_half + 2;     // [2]
   uint64_t* o_done = p_full + 2;     // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_done + 2);
   int* s_lim = reinterpret_cast<int*>(tmem_slot + 1);              // [2] keys that any row of the tile sees
   Segment* s_seg = reinterpret_cast<Segment*>(s_lim + 2);          // 20 bytes
+  float* s_max = reinterpret_cast<float*>(tmem_slot + 16);  // [2 tiles][2 key halves][128 rows]
 
   const dit_packed_attention& a = p.a;
   const int warp = threadIdx.x >> 5, lane = lane_id();
@@ -222,7 +239,8 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(smem_u32(&s_full[t]), 1);
-      mbar_init(smem_u32(&p_full[t]), 4);  // one arrival per warp of the tile's group
+      mbar_init(smem_u32(&p_half[t]), 8);  // one arrival per warp of the tile's group
+      mbar_init(smem_u32(&p_full[t]), 8);
       mbar_init(smem_u32(&o_done[t]), 1);
     }
     fence_mbar_init();
@@ -232,7 +250,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
   if (seg.tile < 0) return;  // more CTAs than tiles: the bound counts a part-filled tile for every segment
 
   // a softmax thread's row: query row `i` of the segment, head `head`, seeing `lim` keys
-  const int t = (warp - 2) >> 2, quad = warp & 3, row = quad * 32 + lane;
+  const int t = (warp - 2) >> 3, half = ((warp - 2) >> 2) & 1, quad = warp & 3, row = quad * 32 + lane;
   const int r = row / G, g = row - r * G;
   const int i = (seg.tile * 2 + t) * rpt + r;
   const int head = kvh * G + g;
@@ -335,13 +353,21 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
           // go out back to back
           if (it + 1 < n && !wait_k(it + 1)) { ok = false; break; }
           if (!mbar_wait(smem_u32(&v_full[vs]), (it / VS) & 1, p.err, kErrTimeoutMma)) { ok = false; break; }
-          if (!mbar_wait(smem_u32(&p_full[tt]), it & 1, p.err, kErrTimeoutMma)) { ok = false; break; }
-          tc_fence_after();
           const uint32_t d = tmem_base + 256u + uint32_t(tt * D), pt = tmem_base + uint32_t(tt * 128);
           const uint32_t vt = v_lo + uint32_t(vs * (Cfg::kTile >> 4));
+          // in two halves: the 32 keys of each key half whose weights are stored first, then the others
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)  // 16 keys a step: 2048 bytes of every box
-            umma_bf16_ts_lo(d, pt + uint32_t(kk * 8), vt + uint32_t(kk * 128), hi, idesc_o, it != 0 || kk != 0);
+          for (int h = 0; h < 2; ++h) {
+            if (!mbar_wait(smem_u32(h == 0 ? &p_half[tt] : &p_full[tt]), it & 1, p.err, kErrTimeoutMma)) { ok = false; break; }
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {  // 16 keys a step: 2048 bytes of every box
+              if (((kk & 3) >> 1) != h) continue;
+              umma_bf16_ts_lo(d, pt + uint32_t((kk >> 2) * 64 + (kk & 3) * 8), vt + uint32_t(kk * 128), hi, idesc_o,
+                              it != 0 || kk != 0);
+            }
+          }
+          if (!ok) break;
           if (tt == 1 || it >= n1) umma_commit(smem_u32(&v_empty[vs]));
           if (it + 1 == n) umma_commit(smem_u32(&o_done[tt]));
           else issue_s(tt, it + 1);
@@ -351,11 +377,13 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
       mbar_wait_cluster(smem_u32(drain), 0, p.err, kErrTimeoutDrain, 4 * kWaitLimitNs, false);
     }
   } else {
-    // ------------------------------------------------------------------ softmax warps, one row per thread
+    // ------------------------------------------------------------------ softmax warps: a row's 64 keys per thread
     const uint32_t lane_off = uint32_t(quad * 32) << 16;
-    const uint32_t tS = tmem_base + lane_off + uint32_t(t * 128);
-    const uint32_t tO = tmem_base + lane_off + 256u + uint32_t(t * D);
+    const uint32_t tS = tmem_base + lane_off + uint32_t(t * 128 + half * 64);
+    const uint32_t tO = tmem_base + lane_off + 256u + uint32_t(t * D + half * (D / 2));  // this thread's half of O
     const int n = t == 0 ? n0 : n1;
+    const int pair = 1 + t * 4 + quad;  // named barrier of the two warps that share 32 rows
+    auto meet = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory"); };
     const bool live = __any_sync(0xffffffffu, lim > 0);  // warps without a row that sees a key only keep the barriers
     const float where = float(i + seg.nk - seg.nq);      // the row's place among the keys
     float slope2 = 0.f;
@@ -365,42 +393,67 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
     bool ok = true;
     for (int it = 0; it < n; ++it) {
       const int key0 = (ta + it) * 128;
+      // rows of V that no row of the CTA sees, zeroed by the first group that uses the tile
+      const int vz = lmax - key0;
+      if (vz < 128 && (t == 0 || it >= n0)) {
+        if (!mbar_wait_warp(smem_u32(&v_full[it % VS]), (it / VS) & 1, p.err, kErrTimeoutSoftmax)) { ok = false; break; }
+        if (row >= vz) {
+          uint8_t* at = sV + (it % VS) * Cfg::kTile + row * 128 + (D == 128 ? half * Cfg::kAtom : half * 64);
+#pragma unroll
+          for (int v = 0; v < (D == 128 ? 8 : 4); ++v) *reinterpret_cast<uint4*>(at + v * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+      }
       if (!mbar_wait_warp(smem_u32(&s_full[t]), it & 1, p.err, kErrTimeoutSoftmax)) { ok = false; break; }
       tc_fence_after();
       if (live) {
-        uint32_t x[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(tS + uint32_t(c * 32), *reinterpret_cast<uint32_t(*)[32]>(&x[c * 32]));
+        uint32_t x[64];
+        tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
+        tmem_ld32(tS + 32u, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
         tmem_ld_wait();
-        if constexpr (GEN) general_scores(x, p, a.slope != nullptr, slope2, where - float(key0));
-        const int seen = lim - key0;
-        if (!__all_sync(0xffffffffu, seen >= 128)) {
+        const int first = key0 + half * 64;
+        if constexpr (GEN) general_scores(x, p, a.slope != nullptr, slope2, where - float(first));
+        const int seen = lim - first;
+        if (!__all_sync(0xffffffffu, seen >= 64)) {
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
+          for (int c = 0; c < 64; ++c)
             if (c >= seen) x[c] = 0xff800000u;
         }
-        float m8[8];
-#pragma unroll
-        for (int v = 0; v < 8; ++v) m8[v] = fmax3(__uint_as_float(x[v]), __uint_as_float(x[v + 8]), __uint_as_float(x[v + 16]));
-#pragma unroll
-        for (int c = 24; c < 120; c += 16)
-#pragma unroll
-          for (int v = 0; v < 8; ++v) m8[v] = fmax3(m8[v], __uint_as_float(x[c + v]), __uint_as_float(x[c + 8 + v]));
-#pragma unroll
-        for (int v = 0; v < 8; ++v) m8[v] = fmaxf(m8[v], __uint_as_float(x[120 + v]));
-        float mx = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
+        float mx = max64(x);
         if constexpr (!GEN) mx *= p.scale_log2;
+        // the row's maximum over both halves of the keys. (One place per row: the other warp has read it before this
+        // tile's weights are complete, without which there is no next tile of scores.)
+        s_max[(t * 2 + half) * 128 + row] = mx;
+        meet();
+        mx = fmaxf(mx, s_max[(t * 2 + (half ^ 1)) * 128 + row]);
         float alpha = 1.f;
         if (mx > m + kRescaleStep) {  // also on the first tile with a key (m = -inf)
           alpha = ex2_approx(m - mx);
           m = mx;
+        }
+        if (it > 0 && __any_sync(0xffffffffu, alpha < 1.0f)) {
+          // O holds earlier tiles; this S came after the P V before it, which is done. (Eight columns at a time: the scores
+          // keep their registers.)
+#pragma unroll 1
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t o[8];
+            tmem_ld8(tO + uint32_t(c * 8), o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int v = 0; v < 8; ++v) o[v] = __float_as_uint(__uint_as_float(o[v]) * alpha);
+            tmem_st8(tO + uint32_t(c * 8), o);
+          }
+          // both warps' halves of O before the first product adds to them
+          tmem_st_wait();
+          tc_fence_before();
+          meet();
         }
         const float base = m == -INFINITY ? 0.f : m;  // nothing seen yet: weights 2^-inf = 0
         const float scale = GEN ? 1.f : p.scale_log2;
         const uint64_t scale2 = f2_pack(scale, scale), neg2 = f2_pack(-base, -base);
         uint64_t sum2[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 2; ++c) {
           uint32_t pk[16];
 #pragma unroll
           for (int v = 0; v < 16; ++v) {
@@ -412,59 +465,51 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
             pk[v] = pack_bf16x2(w0, w1);
           }
           tmem_st16(tS + uint32_t(c * 16), pk);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(c == 0 ? &p_half[t] : &p_full[t]));
         }
         const uint64_t s4 = f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3]));
         l = fmaf(l, alpha, f2_lo(s4) + f2_hi(s4));
-        if (it > 0 && __any_sync(0xffffffffu, alpha < 1.0f)) {
-          // O holds earlier tiles; this S came after the P V before it, which is done
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32(tO + uint32_t(c * 32), o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int v = 0; v < 32; ++v) o[v] = __float_as_uint(__uint_as_float(o[v]) * alpha);
-            tmem_st32(tO + uint32_t(c * 32), o);
-          }
+      } else {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&p_half[t]));
+          mbar_arrive(smem_u32(&p_full[t]));
         }
-        tmem_st_wait();
       }
-      // rows of V that no row of the CTA sees, zeroed by the first group that uses the tile
-      const int vz = lmax - key0;
-      if (vz < 128 && (t == 0 || it >= n0)) {
-        if (!mbar_wait_warp(smem_u32(&v_full[it % VS]), (it / VS) & 1, p.err, kErrTimeoutSoftmax)) { ok = false; break; }
-        if (row >= vz)
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c)
-#pragma unroll
-            for (int v = 0; v < 8; ++v)
-              *reinterpret_cast<uint4*>(sV + (it % VS) * Cfg::kTile + c * Cfg::kAtom + row * 128 + v * 16) = make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&p_full[t]));
     }
 
     // ---- the end of the key range
     if (n > 0 && ok) ok = mbar_wait_warp(smem_u32(&o_done[t]), 0, p.err, kErrTimeoutSoftmax);
+    // (a warp that gave up still meets the other: what follows has the same barriers whatever happened)
+    uint8_t* stage = sQ + t * Cfg::kTile;  // Q has been read; [row][D] bf16, chunks swizzled by the row
+    float* s_sum = reinterpret_cast<float*>(stage);  // [2][128], before the rows
+    if (n > 0) {
+      meet();  // a last tile's maximum has been read
+      s_sum[half * 128 + row] = l;
+      meet();
+      l += s_sum[(half ^ 1) * 128 + row];
+      meet();
+    }
     if (ok) {
       tc_fence_after();
       const bool whole = p.splits == 1;
       const int covered = (ta + n) * 128;  // keys behind the last tile of this row's sums
       const int last = min(lmax, covered);
-      uint8_t* stage = sQ + t * Cfg::kTile;  // Q has been read; [row][D] bf16, chunks swizzled by the row
       const float inv = whole ? (l > 0.f || l != l ? 1.f / l : 0.f) : 1.f;
-      const long long at = (long long)blockIdx.z * a.q_rows + seg.q0 + i;  // row of the partial sums
-      float4* po = reinterpret_cast<float4*>(p.part_o + (at * a.heads + head) * D);
+      const long long at = ((long long)blockIdx.z * a.q_rows + seg.q0 + i) * a.heads + head;  // of the partial sums
+      float4* po = reinterpret_cast<float4*>(p.part_o + at * D + half * (D / 2));
       float bad = 0.f;
       if (live && n > 0) {
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          float o[32];
+        for (int c = 0; c < D / 64; ++c) {
           uint32_t raw[32];
           tmem_ld32(tO + uint32_t(c * 32), raw);
           tmem_ld_wait();
+          float o[32];
 #pragma unroll
           for (int v = 0; v < 32; ++v) {
             o[v] = lim > 0 ? __uint_as_float(raw[v]) : 0.f;
@@ -474,7 +519,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
           if (whole) {
 #pragma unroll
             for (int v = 0; v < 4; ++v)
-              *reinterpret_cast<uint4*>(stage + row * (D * 2) + (((c * 4 + v) ^ (row & 7)) << 4)) =
+              *reinterpret_cast<uint4*>(stage + row * (D * 2) + (((half * (D / 16) + c * 4 + v) ^ (row & 7)) << 4)) =
                   make_uint4(pack_bf16x2(o[8 * v], o[8 * v + 1]), pack_bf16x2(o[8 * v + 2], o[8 * v + 3]),
                              pack_bf16x2(o[8 * v + 4], o[8 * v + 5]), pack_bf16x2(o[8 * v + 6], o[8 * v + 7]));
           } else if (valid) {
@@ -482,7 +527,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
             for (int v = 0; v < 8; ++v) po[c * 8 + v] = make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
           }
         }
-        // rows with something that is not finite beside keys they do not see
+        // rows with something that is not finite (in this half of O) beside keys they do not see
         unsigned again = __ballot_sync(0xffffffffu, valid && bad != 0.f && lim < last);
         while (again) {
           const int src = __ffs(again) - 1;
@@ -492,6 +537,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
           const float sm = __shfl_sync(0xffffffffu, m == -INFINITY ? 0.f : m, src), sinv = __shfl_sync(0xffffffffu, inv, src);
           float acc[D / 32];
           resum_row<D, GEN>(p, seg.q0 + si, seg.k0, ta * 128, end, sh, kvh, __shfl_sync(0xffffffffu, where, src), sm, acc);
+          if ((lane >> 4) != half) continue;  // each warp its half of the row
           if (whole) {
             const int srow = quad * 32 + src, at2 = lane * (D / 32) * 2;  // byte of the row
             uint32_t* dst = reinterpret_cast<uint32_t*>(stage + srow * (D * 2) + (((at2 >> 4) ^ (srow & 7)) << 4) + (at2 & 15));
@@ -505,27 +551,28 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
         }
       } else if (whole) {
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c)
-          *reinterpret_cast<uint4*>(stage + row * (D * 2) + ((c ^ (row & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+        for (int c = 0; c < D / 16; ++c)
+          *reinterpret_cast<uint4*>(stage + row * (D * 2) + (((half * (D / 16) + c) ^ (row & 7)) << 4)) = make_uint4(0, 0, 0, 0);
       }
-      if (valid) {
-        if (!whole) p.part_ml[at * a.heads + head] = make_float2(m == -INFINITY && l != l ? 0.f : m, l);  // scores all NaN: seen
+      if (valid && half == 0) {
+        if (!whole) p.part_ml[at] = make_float2(m == -INFINITY && l != l ? 0.f : m, l);  // scores all NaN: seen
         else if (a.lse)
           a.lse[(long long)head * a.q_rows + seg.q0 + i] =
               l > 0.f || l != l ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
       }
-      if (whole) {
-        // whole rows out of the staged tile: D / 8 lanes of 16 bytes to a row; each warp its own 32 rows
-        __syncwarp();
-        constexpr int per = 32 / (D / 8);
-        for (int rr = lane / (D / 8); rr < 32; rr += per) {
+    }
+    if (p.splits == 1) {
+      // whole rows out of the staged tile: D / 8 lanes of 16 bytes to a row; each warp every other row of the pair's 32
+      meet();
+      constexpr int per = 32 / (D / 8);
+      if (ok)
+        for (int rr = lane / (D / 8) + half * per; rr < 32; rr += 2 * per) {
           const int srow = quad * 32 + rr, sr = srow / G, sg = srow - sr * G, c = lane % (D / 8);
           const int si = (seg.tile * 2 + t) * rpt + sr;
           if (sr >= rpt || si >= seg.nq) continue;
           const uint4 v = *reinterpret_cast<const uint4*>(stage + srow * (D * 2) + ((c ^ (srow & 7)) << 4));
           *reinterpret_cast<uint4*>(a.o + (seg.q0 + si) * a.o_row + (kvh * G + sg) * a.o_head + c * 8) = v;
         }
-      }
     }
   }
 
@@ -555,7 +602,7 @@ __global__ void __launch_bounds__(kRowThreads, 2)
     packed_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PackedParams p) {
   constexpr uint32_t kSlot = kRowKeys * D * 2, kBox = kRowKeys * 128;  // a tile of K or V; its boxes of 64 values
-  extern __shared__ uint8_t smem_raw[];
+  extern __shared__ __align__(256) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t q_box = uint32_t((p.G * p.rpt + 7) & ~7) * 128u;
   const int T = p.slots;
@@ -725,15 +772,7 @@ __global__ void __launch_bounds__(kRowThreads, 2)
           for (int c = 0; c < 64; ++c)
             if (c >= seen) x[c] = 0xff800000u;
         }
-        float m4[4];
-#pragma unroll
-        for (int v = 0; v < 4; ++v) m4[v] = fmax3(__uint_as_float(x[v]), __uint_as_float(x[v + 4]), __uint_as_float(x[v + 8]));
-#pragma unroll
-        for (int c = 12; c < 60; c += 8)
-#pragma unroll
-          for (int v = 0; v < 4; ++v) m4[v] = fmax3(m4[v], __uint_as_float(x[c + v]), __uint_as_float(x[c + 4 + v]));
-        float mx = fmax3(fmax3(m4[0], m4[1], m4[2]), m4[3], __uint_as_float(x[60]));
-        mx = fmax3(mx, fmaxf(__uint_as_float(x[61]), __uint_as_float(x[62])), __uint_as_float(x[63]));
+        float mx = max64(x);
         if constexpr (!GEN) mx *= p.scale_log2;
         float alpha = 1.f;
         if (mx > m + kRescaleStep) {  // also on the first tile with a key (m = -inf)
