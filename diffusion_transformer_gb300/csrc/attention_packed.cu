@@ -50,7 +50,6 @@ struct PackedParams {
   int splits, slots;  // CTAs along the keys; ring slots of the few-rows kernel
   float scale_log2;  // scale log2(e)
   float cap_in, cap_out;  // 2 scale log2(e) / cap and cap log2(e); cap_out = 0: no cap
-  float cap_scale, cap_reach;  // scale / cap, and the largest sum of products that kTanhReach allows
   float* part_o;   // [split][q_rows][heads][d]
   float2* part_ml;  // [split][q_rows][heads]: running maximum (log2 units) and sum
   int* err;
@@ -86,45 +85,36 @@ __device__ __forceinline__ float capped(float s, float cap_in, float cap_out) {
   return fmaf(-2.f * cap_out, rcp_approx(1.f + ex2_approx(s * cap_in)), cap_out);
 }
 
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
+// Two capped scores at once, c tanh t = c - 2 c / (1 + e^2t): one reciprocal serves both (1 / a = b / ab). e^2t is held below
+// 2^60, where tanh is 1 to the last place, so that the product stays finite. A NaN takes both with it: masked places are
+// cleared before. (9 sequences, capped, 254 us; a quotient for each 266; tanh as a polynomial of degree 15 on the FMA pipe,
+// which two-value instructions take two cycles of, 285.)
+__device__ __forceinline__ void capped2(float& a, float& b, float cap_in, float cap_out) {
+  float x = a * cap_in, y = b * cap_in;
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(60.f));
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(y) : "f"(60.f));
+  const float ea = 1.f + ex2_approx(x), eb = 1.f + ex2_approx(y);
+  const float r = -2.f * cap_out * rcp_approx(ea * eb);
+  a = fmaf(r, eb, cap_out);
+  b = fmaf(r, ea, cap_out);
 }
 
-// tanh t = t P(t^2) for |t| <= 1.35, P of degree 7: fitted here to the smallest largest error (9.3e-8; 2e-7 with fp32's
-// roundings, what the exponential form has too). On the FMA pipe, two values at a time: 5 issue slots a score where the
-// exponential and the quotient are two of the 16 special-function results an SM makes per cycle.
-constexpr float kTanhReach = 1.35f;
-__device__ __forceinline__ uint64_t tanh_times2(uint64_t t, uint64_t c) {  // c tanh t
-  constexpr float k[8] = {0.9999987891f, -0.3332989736f, 0.1330467012f, -0.0528753296f,
-                          0.0195838624f, -0.0059749846f, 0.0012365844f, -0.0001225817f};
-  const uint64_t u = f2_mul(t, t);
-  uint64_t y = f2_fma(u, f2_pack(k[7], k[7]), f2_pack(k[6], k[6]));
-#pragma unroll
-  for (int i = 5; i >= 0; --i) y = f2_fma(y, u, f2_pack(k[i], k[i]));
-  return f2_mul(f2_mul(t, c), y);
-}
-
-// Raw sums of products into scores in log2 units: cap, then the distance bias (`at`: the row's place less the first key's)
 template <int N>
-__device__ __forceinline__ void general_scores(uint32_t (&x)[N], const PackedParams& p, bool bias, float slope2, float at) {
+__device__ __forceinline__ void general_scores(uint32_t (&x)[N], const PackedParams& p, bool bias, float slope2, float at,
+                                               int seen, bool all) {
   auto val = [&](int c) { return __uint_as_float(x[c]); };
   if (p.cap_out > 0.f) {
-    float top = 0.f;
+    if (!all) {
 #pragma unroll
-    for (int c = 0; c < N; c += 2) top = fmax3(top, fabsf(val(c)), fabsf(val(c + 1)));
-    if (__all_sync(0xffffffffu, top <= p.cap_reach)) {  // (NaN stays NaN either way)
-      const uint64_t k2 = f2_pack(p.cap_scale, p.cap_scale), c2 = f2_pack(p.cap_out, p.cap_out);
+      for (int c = 0; c < N; ++c)
+        if (c >= seen) x[c] = 0u;
+    }
 #pragma unroll
-      for (int c = 0; c < N; c += 2) {
-        const uint64_t y = tanh_times2(f2_mul(f2_pack(val(c), val(c + 1)), k2), c2);
-        x[c] = uint32_t(y);
-        x[c + 1] = uint32_t(y >> 32);
-      }
-    } else {
-#pragma unroll
-      for (int c = 0; c < N; ++c) x[c] = __float_as_uint(capped(val(c), p.cap_in, p.cap_out));
+    for (int c = 0; c < N; c += 2) {
+      float u = val(c), v = val(c + 1);
+      capped2(u, v, p.cap_in, p.cap_out);
+      x[c] = __float_as_uint(u);
+      x[c + 1] = __float_as_uint(v);
     }
   }
   const float scale = p.cap_out > 0.f ? 1.f : p.scale_log2;
@@ -453,9 +443,10 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
         tmem_ld32(tS + 32u, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
         tmem_ld_wait();
         const int first = key0 + half * 64;
-        if constexpr (GEN) general_scores(x, p, a.slope != nullptr, slope2, where - float(first));
         const int seen = lim - first;
-        if (!__all_sync(0xffffffffu, seen >= 64)) {
+        const bool all = __all_sync(0xffffffffu, seen >= 64);
+        if constexpr (GEN) general_scores(x, p, a.slope != nullptr, slope2, where - float(first), seen, all);
+        if (!all) {
 #pragma unroll
           for (int c = 0; c < 64; ++c)
             if (c >= seen) x[c] = 0xff800000u;
@@ -806,9 +797,10 @@ __global__ void __launch_bounds__(kRowThreads, 2)
         tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
         tmem_ld32(tS + 32u, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
         tmem_ld_wait();
-        if constexpr (GEN) general_scores(x, p, a.slope != nullptr, slope2, where - float(key0));
         const int seen = lim - key0;
-        if (!__all_sync(0xffffffffu, seen >= kRowKeys)) {
+        const bool all = __all_sync(0xffffffffu, seen >= kRowKeys);
+        if constexpr (GEN) general_scores(x, p, a.slope != nullptr, slope2, where - float(key0), seen, all);
+        if (!all) {
 #pragma unroll
           for (int c = 0; c < 64; ++c)
             if (c >= seen) x[c] = 0xff800000u;
@@ -1111,6 +1103,9 @@ size_t dit_attention_packed_workspace_bytes(int q_rows, int k_rows, int segments
 
 }  // extern "C"
 
+#ifndef MODE
+#define MODE 1
+#endif
 namespace dit {
 
 int packed_attention_launch(const dit_packed_attention& a, void* ws, size_t ws_bytes, int* err, cudaStream_t st) {
@@ -1129,8 +1124,6 @@ int packed_attention_launch(const dit_packed_attention& a, void* ws, size_t ws_b
   if (a.cap > 0.f) {
     p.cap_in = float(2.0 * a.scale * log2e / a.cap);
     p.cap_out = float(a.cap * log2e);
-    p.cap_scale = a.scale / a.cap;
-    p.cap_reach = kTanhReach * (a.cap / a.scale);
   }
   p.err = err;
   return a.head_dim == 64 ? packed_kind<64>(p, pl, st) : packed_kind<128>(p, pl, st);
