@@ -289,3 +289,22 @@ def test_binding_refusals():
         with pytest.raises((TypeError, ValueError, D.DitError)):
             D.dit_attention_packed(*args, **kw)
     D.dit_check()
+
+
+@pytest.mark.parametrize("cap", [1.0, 38.0, 39.0, 50.0, 55.0, 56.0, 90.0, 1000.0])
+@pytest.mark.parametrize("sign", [-1.0, 1.0])
+def test_caps_reached_on_either_side(cap, sign):
+    # every score near its cap, above or below: the weights stay in range whatever maximum they are taken against
+    g = np.random.default_rng(int(cap))
+    d, n, H = 64, 300, 2
+    k = np.abs(g.standard_normal((n, H, d))) + 0.5
+    q = torch.from_numpy((sign * 40.0 * (np.abs(g.standard_normal((n, H, d))) + 0.5)).astype(np.float32)).bfloat16()
+    k, v = torch.from_numpy(k.astype(np.float32)).bfloat16(), _bf16(g, n, H, d)
+    scale = 0.125 * cap / 50.0
+    vis = np.minimum(np.arange(n) + 1, 200).astype(np.int32)
+    for slope in (None, np.array([0.5, 2.0 ** -8])):
+        o, lse = torch.empty_like(q).cuda(), torch.empty(H, n, device="cuda")
+        D.dit_attention_packed(q.cuda(), k.cuda(), v.cuda(), o, visible=dev(vis), scale=scale, cap=cap, lse=lse,
+                               slope=None if slope is None else dev(slope.astype(np.float32)))
+        D.dit_check()
+        _check(o, lse, q, k, v, [0, n], [0, n], vis, scale, cap, slope)
