@@ -256,7 +256,8 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
 
   pdl_wait();
   if (warp == 0) {
-    const Segment g = find_tile(a, 2 * rpt, blockIdx.x);
+    // from the last tile: where rows see the keys before them, the long ones start first
+    const Segment g = find_tile(a, 2 * rpt, gridDim.x - 1 - blockIdx.x);
     if (lane == 0) *s_seg = g;
   } else if (threadIdx.x == 32) {
     s_lim[0] = s_lim[1] = 0;
@@ -527,13 +528,13 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
     if (n > 0 && ok) ok = mbar_wait_warp(smem_u32(&o_done[t]), 0, p.err, kErrTimeoutSoftmax);
     // (a warp that gave up still meets the other: what follows has the same barriers whatever happened)
     uint8_t* stage = sQ + t * Cfg::kTile;  // Q has been read; [row][D] bf16, chunks swizzled by the row
-    float* s_sum = reinterpret_cast<float*>(stage);  // [2][128], before the rows
     if (n > 0) {
+      // the row's sum over both halves, through the places of the maxima (the staged rows of other warps lie over everything
+      // else that is free)
       meet();  // a last tile's maximum has been read
-      s_sum[half * 128 + row] = l;
+      s_max[(t * 2 + half) * 128 + row] = l;
       meet();
-      l += s_sum[(half ^ 1) * 128 + row];
-      meet();
+      l += s_max[(t * 2 + (half ^ 1)) * 128 + row];
     }
     if (ok) {
       tc_fence_after();

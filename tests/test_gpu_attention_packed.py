@@ -308,3 +308,60 @@ def test_caps_reached_on_either_side(cap, sign):
                                slope=None if slope is None else dev(slope.astype(np.float32)))
         D.dit_check()
         _check(o, lse, q, k, v, [0, n], [0, n], vis, scale, cap, slope)
+
+
+WORK = {  # many tiles, long and short ones side by side, one tile over many keys
+    "long": ([900], [900], 48, 48, 64),
+    "ragged": ([500, 1, 0, 640, 129, 300], [500, 40, 9, 700, 129, 1000], 48, 48, 64),
+    "groups": ([400, 700, 90], [400, 700, 2000], 64, 32, 128),
+    "one-unit": ([130], [60000], 1, 1, 64),
+    "many": ([130] * 40, [130] * 40, 32, 32, 64),
+}
+
+
+@pytest.mark.parametrize("name", list(WORK))
+@pytest.mark.parametrize("mask", ["all", "causal", "any"])
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (20.0, True)])
+def test_many_tiles(name, mask, cap, bias):
+    qlens, klens, heads, kv, d = WORK[name]
+    g = np.random.default_rng(len(name))
+    qs, ks = _starts(qlens, 1), _starts(klens, 2)
+    n = D.dit_attention_packed_workspace_bytes(qs[-1] + 3, ks[-1] + 3, len(qlens), heads, kv, d)
+    q, k, v = _bf16(g, qs[-1] + 3, heads, d, gain=2.0), _bf16(g, ks[-1] + 3, kv, d), _bf16(g, ks[-1] + 3, kv, d)
+    vis = _visible(mask, qlens, klens, g)
+    if vis is not None:
+        vis = np.concatenate([[9], vis, [9] * 3]).astype(np.int32)
+    v[ks[-1]:], v[:2] = float("nan"), float("inf")
+    slope = 2.0 ** -np.linspace(1, 9, heads) if bias else None
+    outs = []
+    for fill in (0, 255):
+        o, lse = torch.full_like(q, 3.0).cuda(), torch.full((heads, q.shape[0]), 3.0, device="cuda")
+        D.dit_attention_packed(q.cuda(), k.cuda(), v.cuda(), o, dev(np.array(qs, np.int32)), dev(np.array(ks, np.int32)),
+                               visible=None if vis is None else dev(vis), cap=cap, lse=lse,
+                               slope=None if slope is None else dev(slope.astype(np.float32)),
+                               ws=torch.full((max(n, 16),), fill, dtype=torch.uint8, device="cuda"))
+        D.dit_check()
+        outs.append((o, lse))
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+    for out in (o[:1], o[qs[-1]:], lse[:, :1], lse[:, qs[-1]:]):
+        assert (out == 3).all()
+    few = [0, heads // 2, heads - 1] if heads > 3 else list(range(heads))  # the oracle's time
+    keys = [h * kv // heads for h in few]
+    _check(o[:, few], lse[few], q[:, few], k[:, keys], v[:, keys], qs, ks, vis, d ** -0.5, cap,
+           None if slope is None else slope[few])
+
+
+def test_many_tiles_what_is_masked_never_matters():
+    g = np.random.default_rng(3)
+    H, d, n = 48, 64, 900
+    q, k, v = _bf16(g, n, H, d), _bf16(g, n, H, d), _bf16(g, n, H, d)
+    vis = (np.arange(n) + 1).astype(np.int32)
+    ws = torch.empty(max(16, D.dit_attention_packed_workspace_bytes(n, n, 1, H, H, d)), dtype=torch.uint8, device="cuda")
+    out = torch.empty_like(q).cuda()
+    vb, kb = v.clone(), k.clone()
+    vb[500::97], kb[501::97] = float("nan"), float("inf")
+    D.dit_attention_packed(q.cuda(), kb.cuda(), vb.cuda(), out, visible=dev(vis), ws=ws)
+    D.dit_check()
+    few = [0, 20, 47]
+    _check(out[:500, few], None, q[:500, few], k[:, few], v[:, few], [0, 500], [0, n], vis[:500], d ** -0.5, 0.0, None)
+    assert torch.isnan(out[500:].float()).any(-1).all()
