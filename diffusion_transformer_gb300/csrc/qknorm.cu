@@ -24,7 +24,6 @@ namespace dit {
 namespace {
 
 constexpr int kQkThreads = 256;
-constexpr int kQkMaxRows = 32;   // rows of a chunk at most
 constexpr int kQkMaxCtas = 320;  // CTAs of the backward pass at most: each leaves one row of partial sums
 
 struct QkArgs {
@@ -36,6 +35,7 @@ struct QkArgs {
   int heads[2];
   int d, rows, rows_per_chunk, row_chunks;  // rows of a batch entry, of a chunk; chunks of a batch entry
   int chunks;
+  int row_groups;  // groups of lanes that share a row's heads
   int lanes, units, turned;  // lanes of a head (a power of two), its units, those of them that turn
   float eps;
   float* partial;  // backward: [CTA][q, k][d]
@@ -48,18 +48,15 @@ struct QkArgs {
 // neighbouring lanes, NU units on each, so its sum of squares is a butterfly within a warp and the values stay in
 // registers between the sum and the turn. The CTA's groups of lanes go through the heads of a few rows, U heads
 // in flight each; the rows' cosines and sines are worked out once into shared memory.
-// Heads in flight per group. Two, and four CTAs to an SM in the forward pass: 26.8 us at 4224 rows of 24 + 24 heads
-// in bf16, against 30.0 with four heads and two CTAs; backward, two heads and two CTAs: 50 us, one head 61.
-__host__ __device__ constexpr int qk_flight(int nu) {
-  return nu > 1 ? 1 : 2;
-}
+// Heads of a lane's registers at a time (and as many on their way): two of eight values, one of sixteen
+__host__ __device__ constexpr int qk_flight(int nu, int vals) { return nu == 1 && vals <= 8 ? 2 : 1; }
 template <typename T, int VE, bool HALVES, int NU, bool GRAD>
 struct QkCfg {
   static constexpr bool kTwo = HALVES || VE == 1;
   static constexpr int kTurn = HALVES ? VE : (VE == 1 ? 1 : VE / 2);  // pairs of a turned unit
   static constexpr int kVals = kTwo ? 2 * VE : VE;
   static constexpr int kPiece = kTurn < 4 ? kTurn : 4;  // angles per shared-memory access
-  static constexpr int kU = qk_flight(NU);
+  static constexpr int kU = qk_flight(NU, kVals);
 };
 
 // n = kPiece floats at 4 n bytes alignment
@@ -111,101 +108,115 @@ __global__ void __launch_bounds__(kQkThreads, VE > 1 && NU == 1 ? (GRAD ? 2 : 4)
   for (int chunk = blockIdx.x; chunk < a.chunks; chunk += gridDim.x) {
     const int b = chunk / a.row_chunks, t0 = (chunk - b * a.row_chunks) * a.rows_per_chunk;
     const int nrows = min(a.rows_per_chunk, a.rows - t0);
+    const int row = group / a.row_groups, phase = group - row * a.row_groups;  // this group's row of the chunk, its first head
+    const bool here = row < nrows;
     bool angles = false;
+    float c[NU][kTurn], sn[NU][kTurn];  // the row's cosines and sines of this lane's pairs
 #pragma unroll
     for (int z = 0; z < 2; ++z) {
       const int heads = a.heads[z];
       if (heads == 0) continue;  // the same for the CTA
-      const T* x = static_cast<const T*>(a.x[z]) + b * a.xb[z] + t0 * a.xr[z];
-      const T* dy = GRAD ? static_cast<const T*>(a.dy[z]) + b * a.yb[z] + t0 * a.yr[z] : nullptr;
-      T* out = static_cast<T*>(a.out[z]) + b * a.ob[z] + t0 * a.orow[z];
+      const long long first = here ? (long long)row : 0;
+      const T* x = static_cast<const T*>(a.x[z]) + b * a.xb[z] + (t0 + first) * a.xr[z] + phase * a.xh[z];
+      const T* dy = GRAD ? static_cast<const T*>(a.dy[z]) + b * a.yb[z] + (t0 + first) * a.yr[z] + phase * a.yh[z] : nullptr;
+      T* out = static_cast<T*>(a.out[z]) + b * a.ob[z] + (t0 + first) * a.orow[z] + phase * a.oh[z];
+      const long long xd = a.row_groups * a.xh[z], yd = a.row_groups * a.yh[z], od = a.row_groups * a.oh[z];
+      int left_in = here ? heads - phase : 0, left_out = left_in;  // heads of the row from the next one on
+      // heads loaded, and the ones before them turned while they come
+      struct Batch {
+        R v[kU][NU][kTwo ? 2 : 1], e[GRAD ? kU : 1][NU][kTwo ? 2 : 1];
+      };
+      auto fetch = [&](Batch& q) {
+#pragma unroll
+        for (int k = 0; k < kU; ++k) {
+          const T *px = x + k * xd, *py = GRAD ? dy + k * yd : nullptr;
+#pragma unroll
+          for (int n = 0; n < NU; ++n) {
+#pragma unroll
+            for (int i = 0; i < (kTwo ? 2 : 1); ++i) {
+              q.v[k][n][i] = R{};
+              if constexpr (GRAD) q.e[k][n][i] = R{};
+            }
+            if (left_in <= k * a.row_groups || !live[n]) continue;
+            q.v[k][n][0] = rot_load<T, VE>(px + off[n]);
+            if constexpr (kTwo)
+              if (turn[n]) q.v[k][n][1] = rot_load<T, VE>(px + off[n] + far);
+            if constexpr (GRAD) {
+              q.e[k][n][0] = rot_load<T, VE>(py + off[n]);
+              if constexpr (kTwo)
+                if (turn[n]) q.e[k][n][1] = rot_load<T, VE>(py + off[n] + far);
+            }
+          }
+        }
+        left_in -= kU * a.row_groups;
+        x += kU * xd;
+        if constexpr (GRAD) dy += kU * yd;
+      };
+      const int rounds = (heads + a.row_groups * kU - 1) / (a.row_groups * kU);
+      Batch next;
+      fetch(next);
       float w[NU][kVals];
 #pragma unroll
       for (int n = 0; n < NU; ++n)
 #pragma unroll
         for (int j = 0; j < kVals; ++j)
           w[n][j] = a.w[z] && live[n] && (j < VE || turn[n]) ? __ldg(a.w[z] + off[n] + (j < VE ? j : far + j - VE)) : 1.f;
-      // the group's heads of the chunk: every `groups`-th, its row, head and addresses stepped along
-      const int r0 = group / heads, dr = groups / heads, dh = groups - dr * heads;
-      int at = group - r0 * heads, row = r0;
-      x += r0 * a.xr[z] + at * a.xh[z];
-      out += r0 * a.orow[z] + at * a.oh[z];
-      const long long xs = dr * a.xr[z] + dh * a.xh[z], xw = a.xr[z] - heads * a.xh[z];
-      const long long os = dr * a.orow[z] + dh * a.oh[z], ow = a.orow[z] - heads * a.oh[z];
-      long long ys = 0, yw = 0;
-      if constexpr (GRAD) {
-        dy += r0 * a.yr[z] + at * a.yh[z];
-        ys = dr * a.yr[z] + dh * a.yh[z];
-        yw = a.yr[z] - heads * a.yh[z];
+      if (!angles) {  // once per chunk, behind the first loads
+        if (chunk != int(blockIdx.x)) __syncthreads();  // the last chunk's angles have been read
+        for (int k = threadIdx.x; k < nrows * pairs; k += kQkThreads) {
+          const int f = k / nrows, r = k - f * nrows;  // neighbours share a pair: its plan entry is one constant
+          const int32_t p = __ldg(a.pos + ((long long)b * a.rows + t0 + r) * a.plan.axes + a.plan.axis[f]);
+          const float2 t = rot_cos_sin(p, a.plan.turns[f], a.plan.amplitude);
+          const int u = f / kTurn, j = f - u * kTurn;
+          const int place = r * pairs + (j / kPiece) * (kPiece * turned) + u * kPiece + j % kPiece;
+          sc[place] = t.x;
+          ss[place] = GRAD ? -t.y : t.y;
+        }
+        __syncthreads();
+        angles = true;
+#pragma unroll
+        for (int n = 0; n < NU; ++n) {
+#pragma unroll
+          for (int i = 0; i < kTurn / kPiece; ++i) {
+#pragma unroll
+            for (int j = 0; j < kPiece; ++j) {
+              c[n][i * kPiece + j] = 1.f;
+              sn[n][i * kPiece + j] = 0.f;
+            }
+            if (turn[n]) {
+              const int at = int(first) * pairs + (u0 + n * a.lanes) * kPiece + i * kPiece * turned;
+              ld_piece<kPiece>(sc + at, c[n] + i * kPiece);
+              ld_piece<kPiece>(ss + at, sn[n] + i * kPiece);
+            }
+          }
+        }
       }
-      const int rounds = (nrows * heads + groups * kU - 1) / (groups * kU);
+      // the turn of one unit: (p, q) -> (p c - q s, p s + q c)
+      auto spin = [&](float* m, int n) {
+#pragma unroll
+        for (int f = 0; f < kTurn; ++f) {
+          const int p0 = kTwo ? f : 2 * f, p1 = kTwo ? VE + f : 2 * f + 1;
+          const float u = m[p0], v = m[p1];
+          m[p0] = u * c[n][f] - v * sn[n][f];
+          m[p1] = u * sn[n][f] + v * c[n][f];
+        }
+      };
       for (int round = 0; round < rounds; ++round) {
-        R v[kU][NU][kTwo ? 2 : 1], e[GRAD ? kU : 1][NU][kTwo ? 2 : 1];
-        int angle[kU];  // the row's place among the angles
-        T* po[kU];
-        bool ok[kU];
+        Batch q = next;
+        if (round + 1 < rounds) fetch(next);
 #pragma unroll
         for (int k = 0; k < kU; ++k) {
-          ok[k] = row < nrows;
-          angle[k] = ok[k] ? row * pairs : 0;
-          po[k] = out;
-          const T *px = x, *py = dy;
-          at += dh;
-          row += dr;
-          x += xs;
-          out += os;
-          if constexpr (GRAD) dy += ys;
-          if (at >= heads) {
-            at -= heads;
-            ++row;
-            x += xw;
-            out += ow;
-            if constexpr (GRAD) dy += yw;
-          }
-#pragma unroll
-          for (int n = 0; n < NU; ++n) {
-#pragma unroll
-            for (int i = 0; i < (kTwo ? 2 : 1); ++i) {
-              v[k][n][i] = R{};
-              if constexpr (GRAD) e[k][n][i] = R{};
-            }
-            if (!ok[k] || !live[n]) continue;
-            v[k][n][0] = rot_load<T, VE>(px + off[n]);
-            if constexpr (kTwo)
-              if (turn[n]) v[k][n][1] = rot_load<T, VE>(px + off[n] + far);
-            if constexpr (GRAD) {
-              e[k][n][0] = rot_load<T, VE>(py + off[n]);
-              if constexpr (kTwo)
-                if (turn[n]) e[k][n][1] = rot_load<T, VE>(py + off[n] + far);
-            }
-          }
-        }
-        if (!angles) {  // once per chunk, behind the first loads
-          if (chunk != int(blockIdx.x)) __syncthreads();  // the last chunk's angles have been read
-          for (int k = threadIdx.x; k < nrows * pairs; k += kQkThreads) {
-            const int f = k / nrows, r = k - f * nrows;  // neighbours share a pair: its plan entry is one constant
-            const int32_t p = __ldg(a.pos + ((long long)b * a.rows + t0 + r) * a.plan.axes + a.plan.axis[f]);
-            const float2 t = rot_cos_sin(p, a.plan.turns[f], a.plan.amplitude);
-            const int u = f / kTurn, j = f - u * kTurn;
-            const int place = r * pairs + (j / kPiece) * (kPiece * turned) + u * kPiece + j % kPiece;
-            sc[place] = t.x;
-            ss[place] = GRAD ? -t.y : t.y;
-          }
-          __syncthreads();
-          angles = true;
-        }
-#pragma unroll
-        for (int k = 0; k < kU; ++k) {
+          const bool ok = left_out > k * a.row_groups;
           float y[NU][kVals];
           float sum = 0.f;
 #pragma unroll
           for (int n = 0; n < NU; ++n) {
             float h[VE];
-            rot_values<T, VE>(v[k][n][0], h);
+            rot_values<T, VE>(q.v[k][n][0], h);
 #pragma unroll
             for (int j = 0; j < VE; ++j) y[n][j] = h[j];
             if constexpr (kTwo) {
-              rot_values<T, VE>(v[k][n][1], h);
+              rot_values<T, VE>(q.v[k][n][1], h);
 #pragma unroll
               for (int j = 0; j < VE; ++j) y[n][VE + j] = h[j];
             }
@@ -216,30 +227,12 @@ __global__ void __launch_bounds__(kQkThreads, VE > 1 && NU == 1 ? (GRAD ? 2 : 4)
           for (int o = 16; o > 0; o >>= 1)
             if (o < a.lanes) sum += __shfl_xor_sync(0xffffffffu, sum, o);
           const float r = rsqrtf(fmaf(sum, inv_d, a.eps));
-          // the turn of one unit: (p, q) -> (p c - q s, p s + q c)
-          auto spin = [&](float* m, int n) {
-            const float* pc = sc + angle[k] + (u0 + n * a.lanes) * kPiece;
-            const float* ps = ss + angle[k] + (u0 + n * a.lanes) * kPiece;
-#pragma unroll
-            for (int i = 0; i < kTurn / kPiece; ++i) {
-              float c[kPiece], s[kPiece];
-              ld_piece<kPiece>(pc + i * kPiece * turned, c);
-              ld_piece<kPiece>(ps + i * kPiece * turned, s);
-#pragma unroll
-              for (int j = 0; j < kPiece; ++j) {
-                const int f = i * kPiece + j, p0 = kTwo ? f : 2 * f, p1 = kTwo ? VE + f : 2 * f + 1;
-                const float p = m[p0], q = m[p1];
-                m[p0] = p * c[j] - q * s[j];
-                m[p1] = p * s[j] + q * c[j];
-              }
-            }
-          };
           if constexpr (!GRAD) {
 #pragma unroll
             for (int n = 0; n < NU; ++n) {
 #pragma unroll
               for (int j = 0; j < kVals; ++j) y[n][j] = y[n][j] * r * w[n][j];
-              if (turn[n]) spin(y[n], n);
+              spin(y[n], n);  // (a unit that passes: by the cosine 1)
             }
           } else {
             float g[NU][kVals];
@@ -247,19 +240,19 @@ __global__ void __launch_bounds__(kQkThreads, VE > 1 && NU == 1 ? (GRAD ? 2 : 4)
 #pragma unroll
             for (int n = 0; n < NU; ++n) {
               float h[VE];
-              rot_values<T, VE>(e[k][n][0], h);
+              rot_values<T, VE>(q.e[k][n][0], h);
 #pragma unroll
               for (int j = 0; j < VE; ++j) g[n][j] = h[j];
               if constexpr (kTwo) {
-                rot_values<T, VE>(e[k][n][1], h);
+                rot_values<T, VE>(q.e[k][n][1], h);
 #pragma unroll
                 for (int j = 0; j < VE; ++j) g[n][VE + j] = h[j];
               }
-              if (turn[n]) spin(g[n], n);
+              spin(g[n], n);
 #pragma unroll
               for (int j = 0; j < kVals; ++j) {
                 y[n][j] *= r;
-                if (ok[k]) acc[GRAD ? z : 0][n][j] = fmaf(g[n][j], y[n][j], acc[GRAD ? z : 0][n][j]);
+                if (ok) acc[GRAD ? z : 0][n][j] = fmaf(g[n][j], y[n][j], acc[GRAD ? z : 0][n][j]);
                 g[n][j] *= w[n][j];
                 dot = fmaf(g[n][j], y[n][j], dot);
               }
@@ -273,22 +266,25 @@ __global__ void __launch_bounds__(kQkThreads, VE > 1 && NU == 1 ? (GRAD ? 2 : 4)
 #pragma unroll
               for (int j = 0; j < kVals; ++j) y[n][j] = r * (g[n][j] - y[n][j] * dot);
           }
-          if (!ok[k]) continue;
+          if (!ok) continue;
+          T* po = out + k * od;
 #pragma unroll
           for (int n = 0; n < NU; ++n) {
             if (!live[n]) continue;
             float h[VE];
 #pragma unroll
             for (int j = 0; j < VE; ++j) h[j] = y[n][j];
-            rot_store<T, VE>(po[k] + off[n], rot_raw<T, VE>(h));
+            rot_store<T, VE>(po + off[n], rot_raw<T, VE>(h));
             if constexpr (kTwo)
               if (turn[n]) {
 #pragma unroll
                 for (int j = 0; j < VE; ++j) h[j] = y[n][VE + j];
-                rot_store<T, VE>(po[k] + off[n] + far, rot_raw<T, VE>(h));
+                rot_store<T, VE>(po + off[n] + far, rot_raw<T, VE>(h));
               }
           }
         }
+        left_out -= kU * a.row_groups;
+        out += kU * od;
       }
     }
   }
@@ -434,21 +430,13 @@ int qk_launch(const dit_rotary_plan* plan, const int heads[2], const Tensor x[2]
   const int per_lane = a.units <= 32 ? 1 : (a.units <= 64 ? 2 : 8);
   while (a.lanes * per_lane < a.units) a.lanes *= 2;
   const int groups = kQkThreads / a.lanes, all = heads[0] + heads[1];
-  // Rows of a chunk: few heads left over in the last round of q's and of k's (a round costs the same half empty), a
-  // round's worth for the angles and the barrier, and chunks for every SM several times over. (4224 rows of 24 + 24
-  // heads: 40 us with 3 rows to a chunk, where 8 take 27.)
-  const int flight = groups * qk_flight(per_lane);
-  const long long most = std::max(1LL, std::min<long long>(std::min(kQkMaxRows, rows), (long long)batch * rows / (3LL * num_sms())));
-  long long per = 1;
-  double least = 0;
-  for (long long n = 1; n <= most; ++n) {
-    double rounds = 1;
-    for (int z = 0; z < 2; ++z) rounds += double((n * heads[z] + flight - 1) / flight);
-    if (n == 1 || rounds / n < least) {
-      least = rounds / n;
-      per = n;
-    }
-  }
+  // Groups of a row, and so rows of a chunk: one where there are rows enough, more while the chunks do not fill the SMs three
+  // times over and the row has heads for them
+  const int most = std::max(heads[0], heads[1]);
+  a.row_groups = 1;
+  while (2 * a.row_groups <= std::min(groups, most) && (long long)batch * rows * a.row_groups < 3LL * num_sms() * groups)
+    a.row_groups *= 2;
+  const long long per = std::min<long long>(groups / a.row_groups, rows);
   if (per * all > 0x7fffffffLL / 4) return DIT_EUNSUPPORTED;
   a.rows_per_chunk = int(per);
   a.row_chunks = int((rows + per - 1) / per);

@@ -132,9 +132,13 @@ def test_backward(name, dtype, B, T, Hq, Hk):
         _check(outs[z], dx, gate, dtype)
         _check(got[z], dw, gate_w, torch.float32)
     assert torch.equal(m.cpu(), qkv) and torch.equal(e.cpu(), grad)
+    same = _backward(plan, q, k, dq, dk, dev(pos), dev(wq), dev(wk), *outs, eps=1e-3)
+    assert torch.equal(got[0], same[0]) and torch.equal(got[1], same[1])  # one call's sums have one order
     again = _backward(plan, q, k, dq, dk, dev(pos), dev(wq), dev(wk), eps=1e-3)  # over the gradients; v's columns stay
     assert torch.equal(dq, outs[0]) and torch.equal(dk, outs[1]) and torch.equal(e[:, :, Hq + Hk:].cpu(), grad[:, :, Hq + Hk:])
-    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+    for z, w in ((0, wq), (1, wk)):  # (of other strides another: batches of dense rows are one)
+        _, dw, _, gate_w = _expect_grad(spec, x[:, :, cut[z]], dy[:, :, cut[z]], w, 1e-3, pos)
+        _check(again[z], dw, gate_w, torch.float32)
     D.dit_check()
 
 
