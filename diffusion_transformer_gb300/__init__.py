@@ -836,25 +836,27 @@ _grad_struct = struct.Struct("@PPPiqqqqqqqqq")  # dit_rotary_grad
 
 def _rotary_grad(x, dy, dx, dev, name):
     """(dit_rotary_grad, type, shape) of the heads x, the gradient dy of their output and the place of theirs."""
-    kind = _kinds.get(getattr(x, "dtype", None))
+    dtype = getattr(x, "dtype", None)
+    kind = _kinds.get(dtype)
     if kind is None or x.get_device() != dev:
         raise _wrong(x, dev, name)
+    shape = x.shape
+    if len(shape) not in (3, 4):
+        raise ValueError(f"{name}: expected [batch, rows, heads, head_dim] or [rows, heads, head_dim]")
     strides = []
     for t in (x, dy, dx):
-        if getattr(t, "dtype", None) is not x.dtype or t.get_device() != dev:
+        if getattr(t, "dtype", None) is not dtype or t.get_device() != dev:
             raise _wrong(t, dev, name)
-        if t.shape != x.shape:
+        if t.shape != shape:
             raise ValueError(f"{name}: expected gradients like the input")
         s = t.stride()
-        if len(s) not in (3, 4):
-            raise ValueError(f"{name}: expected [batch, rows, heads, head_dim] or [rows, heads, head_dim]")
-        if s[-1] != 1 and x.shape[-1] > 1:
+        if s[-1] != 1 and shape[-1] > 1:
             raise ValueError(f"{name}: the last dimension must be dense")
-        strides += [s[0] if len(s) == 4 else 0, s[-3], s[-2]]
+        strides += s[:-1] if len(s) == 4 else (0, s[0], s[1])
     try:
-        return _grad_struct.pack(x.data_ptr(), dy.data_ptr(), dx.data_ptr(), x.shape[-2], *strides), kind, x.shape
+        return _grad_struct.pack(x.data_ptr(), dy.data_ptr(), dx.data_ptr(), shape[-2], *strides), kind, shape
     except struct.error:
-        raise ValueError(f"{name}: {x.shape[-2]} heads") from None
+        raise ValueError(f"{name}: {shape[-2]} heads") from None
 
 
 def dit_qknorm_rotary_backward(plan: RotaryPlan, q, k, dq, dk, pos, q_norm=None, k_norm=None, dq_out=None, dk_out=None,
@@ -873,10 +875,11 @@ def dit_qknorm_rotary_backward(plan: RotaryPlan, q, k, dq, dk, pos, q_norm=None,
     _fits(batch, rows, dim)
     if ws is not None and (ws.get_device() != dev or not ws.is_contiguous()):
         raise ValueError("ws: expected a contiguous CUDA tensor on the current device")
-    w = [_head_weights(t, dim, dev, n) for t, n in ((q_norm, "q_norm"), (k_norm, "k_norm"), (q_norm_grad, "q_norm_grad"),
-                                                    (k_norm_grad, "k_norm_grad"))]
-    rc = lib().dit_qknorm_rotary_backward(plan.ref, a, c, w[0], w[1], eps, kind, batch, rows, dim,
-                                          _positions(plan, pos, batch * rows, dev), w[2], w[3],
+    rc = lib().dit_qknorm_rotary_backward(plan.ref, a, c, _head_weights(q_norm, dim, dev, "q_norm"),
+                                          _head_weights(k_norm, dim, dev, "k_norm"), eps, kind, batch, rows, dim,
+                                          _positions(plan, pos, batch * rows, dev),
+                                          _head_weights(q_norm_grad, dim, dev, "q_norm_grad"),
+                                          _head_weights(k_norm_grad, dim, dev, "k_norm_grad"),
                                           None if ws is None else ws.data_ptr(),
                                           0 if ws is None else ws.numel() * ws.element_size(), st)
     if rc:

@@ -430,11 +430,11 @@ int qk_launch(const dit_rotary_plan* plan, const int heads[2], const Tensor x[2]
   const int per_lane = a.units <= 32 ? 1 : (a.units <= 64 ? 2 : 8);
   while (a.lanes * per_lane < a.units) a.lanes *= 2;
   const int groups = kQkThreads / a.lanes, all = heads[0] + heads[1];
-  // Groups of a row, and so rows of a chunk: one where there are rows enough, more while the chunks do not fill the SMs three
-  // times over and the row has heads for them
+  // Groups of a row, and so rows of a chunk: one where there are rows enough, more while there are fewer chunks than the SMs
+  // hold half of (forward: two to an SM, backward: one) and the row has heads for them
   const int most = std::max(heads[0], heads[1]);
   a.row_groups = 1;
-  while (2 * a.row_groups <= std::min(groups, most) && (long long)batch * rows * a.row_groups < 3LL * num_sms() * groups)
+  while (2 * a.row_groups <= std::min(groups, most) && (long long)batch * rows * a.row_groups < (grad ? 1LL : 2LL) * num_sms() * groups)
     a.row_groups *= 2;
   const long long per = std::min<long long>(groups / a.row_groups, rows);
   if (per * all > 0x7fffffffLL / 4) return DIT_EUNSUPPORTED;
