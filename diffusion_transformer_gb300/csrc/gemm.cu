@@ -924,7 +924,8 @@ __global__ void __launch_bounds__(GemmCfg<BN, B8, PAIR, EPI>::kThreads, 1)
       // PAIR (bf16): both CTAs' copies complete on the first CTA's barrier, which expects both.
       // PAIR (int8): each CTA's copies complete on its own barrier, which its converters wait on.
       constexpr bool kLocalFull = !PAIR || B8;
-      constexpr uint32_t kOwnBytes = Cfg::kABytes + (B8 ? Cfg::kB8Bytes + Cfg::kSBytes : Cfg::kBLoad);
+      constexpr uint32_t kAllBytes = Cfg::kABytes + (B8 ? Cfg::kB8Bytes + Cfg::kSBytes : Cfg::kBLoad);
+      const uint32_t own_bytes = EPI == kEpiFull && p.a_box > 0 ? uint32_t(p.a_box) * BK * 2 + Cfg::kBLoad : kAllBytes;
       const uint32_t full0 = kLocalFull ? smem_u32(&full[0]) : mapa_shared(smem_u32(&full[0]), 0);
       for (int it = 0; it < items && ok; ++it) {
         const WorkItem w = unit_item(p, unit, it, units, tiles, KB);
@@ -934,7 +935,7 @@ __global__ void __launch_bounds__(GemmCfg<BN, B8, PAIR, EPI>::kThreads, 1)
         for (int kb = w.k0; kb < w.k1; ++kb) {
           if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1, p.err, kErrTimeoutProducer)) { ok = false; break; }
           const uint32_t fb = full0 + uint32_t(stage) * 8u;
-          if (kLocalFull || rank == 0) mbar_arrive_expect_tx(smem_u32(&full[stage]), (kLocalFull ? 1 : 2) * kOwnBytes);
+          if (kLocalFull || rank == 0) mbar_arrive_expect_tx(smem_u32(&full[stage]), (kLocalFull ? 1 : 2) * own_bytes);
           // concatenated operands: the second A/B past the K boundary, the second B past the N boundary
           const bool k2 = p.k_split > 0 && kb * BK >= p.k_split;
           const bool n2 = p.n_split > 0 && nb * BN >= p.n_split;
@@ -1640,7 +1641,11 @@ int gemm_full_launch(const uint16_t* a, long long lda, const uint16_t* b, long l
     p.parts_ld = parts_ld(p.N);
   }
   Maps m;
-  if (!tmap_bf16(&m.a, a, p.K, p.M, lda, BM) || !tmap_bf16(&m.b, b, p.K, p.N, ldb, f.pair ? f.bn / 2 : f.bn)) return DIT_ECUDA;
+  // few rows: boxes of those alone (rows past the tensor's cost the copy engine more than rows that are there: 8 rows of
+  // K = 3072 against 18432 of W take 31.8 us in boxes of 128 rows, 23.5 in boxes of 8)
+  p.a_box = !f.pair && p.M < BM ? (p.M + 7) / 8 * 8 : 0;
+  if (!tmap_bf16(&m.a, a, p.K, p.M, lda, p.a_box ? p.a_box : BM) || !tmap_bf16(&m.b, b, p.K, p.N, ldb, f.pair ? f.bn / 2 : f.bn))
+    return DIT_ECUDA;
   m.s = m.a2 = m.a;
   m.b2 = m.b;
   const int rc = launch_bf16(m, f.bn, kEpiFull, p, f.pair, stream);

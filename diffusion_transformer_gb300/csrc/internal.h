@@ -86,6 +86,7 @@ struct GemmParams {
   const void* residual;
   long long ldr;
   int activation, out_f32, vec, gate_rows;
+  int a_box;  // rows of a TMA box of A where one row tile holds them all (0: 128); the tile's other rows are never stored
   int k_parts;
   float* parts;
   long long parts_ld;
