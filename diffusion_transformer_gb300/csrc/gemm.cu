@@ -1481,8 +1481,8 @@ __global__ void __launch_bounds__(256) full_join_kernel(const __grid_constant__ 
 }
 
 // A few rows against the weight, which is read once: HBM-bound on the plain cores, where a tile of 128 rows would have the
-// tensor cores multiply zeros and its 128-byte pieces of rows keep HBM at 3.6 TB/s (18432 x 3072: 1, 2 and 4 rows 19.8, 23.7 and
-// 26.5 us, as tiles 31 to 32; 8 rows 54 us, as tiles 32). A warp takes kVecRows rows of W, a lane
+// tensor cores multiply zeros (18432 x 3072: 1, 2 and 4 rows 19.8, 23.7 and 26.5 us, as tiles 23.4; 4096 x 4096: 8.3, 11.1 and
+// 12.9, as tiles 12; 512 x 14000: 6.4, 6.8 and 7.6, as tiles 10): up to two rows, or four of a small weight. A warp takes kVecRows rows of W, a lane
 // 16 bytes of each at a time, so a warp reads 512 consecutive bytes; a (L1 or L2) is read once for all of them. 2^split warps
 // of a CTA divide K between them, for few outputs. Sums in fp32, two per row and product (packed pairs), joined over the
 // lanes by a butterfly and over the warps in order.
@@ -1567,6 +1567,8 @@ __global__ void __launch_bounds__(256) full_rows_kernel(const __grid_constant__ 
   else static_cast<uint16_t*>(p.out)[m * p.ldo + n] = uint16_t(pack_bf16x2(y[0], 0.f));
 }
 
+bool few_rows(int M, int N, int K) { return M <= 2 || (M <= kVecMost && (long long)N * K <= 8 << 20); }
+
 int full_rows_launch(const uint16_t* a, long long lda, const uint16_t* w, long long ldw, const GemmParams& p, cudaStream_t st) {
   // K is divided while the CTAs do not fill the SMs four times over and a warp keeps 16 rounds of loads
   const int groups = (p.N + kVecRows - 1) / kVecRows;
@@ -1576,7 +1578,6 @@ int full_rows_launch(const uint16_t* a, long long lda, const uint16_t* w, long l
   cudaError_t e;
   if (p.M == 1) e = launch_pdl(full_rows_kernel<1>, grid, block, 0, st, 1, p, a, lda, w, ldw, split);
   else if (p.M == 2) e = launch_pdl(full_rows_kernel<2>, grid, block, 0, st, 1, p, a, lda, w, ldw, split);
-  else if (p.M <= 4) e = launch_pdl(full_rows_kernel<4>, grid, block, 0, st, 1, p, a, lda, w, ldw, split);
   else e = launch_pdl(full_rows_kernel<kVecMost>, grid, block, 0, st, 1, p, a, lda, w, ldw, split);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? DIT_OK : DIT_ECUDA;
 }
@@ -1584,7 +1585,7 @@ int full_rows_launch(const uint16_t* a, long long lda, const uint16_t* w, long l
 // Tile and division of the k-blocks, by an estimate of time fitted to 18 sizes on a GB300: rounds of work items over the
 // units (SMs, or pairs), a round as long as its k-blocks or as an epilogue (which overlaps the next round's k-blocks), the
 // last epilogue, the launch; for divided k-blocks the joining kernel and its bytes; never below what HBM takes for the
-// operands (tiles read it at 4.2 TB/s, those of 64 rows of W at 2.8). Measured best and chosen, us: 16 x 512 x 14000 10.0 / 10.0, 100 x 512 x 6144 8.6 / 8.6,
+// operands (tiles read it at 6 TB/s, those of 64 rows of W at 5.5). Measured best and chosen, us: 16 x 2048 x 14000 15.8 / 17.1, 8 x 18432 x 3072 23.4 / 24.1,
 // 333 x 1024 x 4096 11.9 / 11.9, 1088 x 4096 x 1024 15.0 / 15.1, 2627 x 3968 x 11200 155 / 155, 4224 x 12288 x 3072 171 / 171.
 struct FullPlan {
   int bn, parts;
@@ -1598,7 +1599,7 @@ FullPlan full_plan(int M, int N, int K) {
   };
   const Shape shapes[] = {{256, 256, 0.30f, 6.4f}, {128, 256, 0.177f, 3.7f}, {256, 128, 0.36f, 6.7f}, {128, 128, 0.21f, 4.3f},
                           {64, 128, 0.168f, 2.3f}};
-  const float hbm = 2.f * K * (float(M) + float(N)) / 4.2e6f;
+  const float hbm = 2.f * K * (float(M) + float(N)) / 6e6f;
   FullPlan best{64, 1, false};
   float least = 0.f;
   for (const Shape& s : shapes) {
@@ -1609,7 +1610,7 @@ FullPlan full_plan(int M, int N, int K) {
     for (int parts = 1; parts <= 32 && (parts == 1 || (tiles * parts <= units && KB / parts >= 4)); ++parts) {
       const float rounds = float((tiles * parts + units - 1) / units);
       const float main = std::max(s.kblock * float((KB + parts - 1) / parts), rounds > 1 ? s.epilogue : 0.f);
-      float t = std::max(rounds * main, s.bn == 64 ? 1.5f * hbm : hbm) + s.epilogue + 2.f;
+      float t = std::max(rounds * main, s.bn == 64 ? 1.1f * hbm : hbm) + s.epilogue + 2.f;
       if (parts > 1) t += 2.5f + float(parts) * float(M) * float(N) * 4.f / 3.5e6f;
       if (least == 0.f || t < least) {
         least = t;
@@ -1624,7 +1625,7 @@ long long parts_ld(int N) { return (N + 3) / 4 * 4; }
 }  // namespace
 
 size_t gemm_full_scratch_bytes(int M, int N, int K) {
-  if (M <= kVecMost) return 0;
+  if (few_rows(M, N, K)) return 0;
   const FullPlan f = full_plan(M, N, K);
   return f.parts > 1 ? size_t(f.parts) * M * parts_ld(N) * sizeof(float) : 0;
 }
@@ -1633,7 +1634,7 @@ int gemm_full_launch(const uint16_t* a, long long lda, const uint16_t* b, long l
                      size_t ws_bytes, cudaStream_t stream) {
   GemmParams p = p0;
   p.k_parts = 1;
-  if (p.M <= kVecMost) return full_rows_launch(a, lda, b, ldb, p, stream);
+  if (few_rows(p.M, p.N, p.K)) return full_rows_launch(a, lda, b, ldb, p, stream);
   const FullPlan f = full_plan(p.M, p.N, p.K);
   if (f.parts > 1 && ws && ws_bytes >= gemm_full_scratch_bytes(p.M, p.N, p.K)) {
     p.k_parts = f.parts;
