@@ -795,7 +795,7 @@ def _head_weights(t, dim, dev, name):
         return None
     if getattr(t, "dtype", None) is not _torch_mod.float32:
         raise TypeError(f"{name}: expected float32")
-    if t.get_device() != dev or not t.is_contiguous() or t.numel() != dim:
+    if t.get_device() != dev or t.numel() != dim or not t.is_contiguous():
         raise ValueError(f"{name}: expected {dim} dense values on the current device")
     return t.data_ptr()
 
@@ -840,21 +840,32 @@ def _rotary_grad(x, dy, dx, dev, name):
     kind = _kinds.get(dtype)
     if kind is None or x.get_device() != dev:
         raise _wrong(x, dev, name)
-    shape = x.shape
-    if len(shape) not in (3, 4):
-        raise ValueError(f"{name}: expected [batch, rows, heads, head_dim] or [rows, heads, head_dim]")
-    strides = []
-    for t in (x, dy, dx):
-        if getattr(t, "dtype", None) is not dtype or t.get_device() != dev:
-            raise _wrong(t, dev, name)
-        if t.shape != shape:
+    shape, sx = x.shape, x.stride()
+    if getattr(dy, "dtype", None) is not dtype or dy.get_device() != dev:
+        raise _wrong(dy, dev, name)
+    sy, so = dy.stride(), None
+    if dx is dy:
+        so = sy
+    elif getattr(dx, "dtype", None) is not dtype or dx.get_device() != dev:
+        raise _wrong(dx, dev, name)
+    else:
+        so = dx.stride()
+        if dx.shape != shape:
             raise ValueError(f"{name}: expected gradients like the input")
-        s = t.stride()
-        if s[-1] != 1 and shape[-1] > 1:
-            raise ValueError(f"{name}: the last dimension must be dense")
-        strides += s[:-1] if len(s) == 4 else (0, s[0], s[1])
+    if dy.shape != shape:
+        raise ValueError(f"{name}: expected gradients like the input")
+    if len(shape) == 4:
+        (bx, rx, hx, ex), (by, ry, hy, ey), (bo, ro, ho, eo) = sx, sy, so
+    elif len(shape) == 3:
+        (rx, hx, ex), (ry, hy, ey), (ro, ho, eo) = sx, sy, so
+        bx = by = bo = 0
+    else:
+        raise ValueError(f"{name}: expected [batch, rows, heads, head_dim] or [rows, heads, head_dim]")
+    if (ex != 1 or ey != 1 or eo != 1) and shape[-1] > 1:
+        raise ValueError(f"{name}: the last dimension must be dense")
     try:
-        return _grad_struct.pack(x.data_ptr(), dy.data_ptr(), dx.data_ptr(), shape[-2], *strides), kind, shape
+        return (_grad_struct.pack(x.data_ptr(), dy.data_ptr(), dx.data_ptr(), shape[-2], bx, rx, hx, by, ry, hy, bo, ro, ho),
+                kind, shape)
     except struct.error:
         raise ValueError(f"{name}: {shape[-2]} heads") from None
 
@@ -1098,18 +1109,19 @@ def dit_attention_qknorm(dims: DitDims, R: int, q, k, vt, q_norm, k_norm, o, ws=
 _packed_struct = struct.Struct("@" + "P" * 9 + "q" * 8 + "i" * 6 + "ff")  # dit_packed_attention
 
 
-def _heads_of(t, name, dev, shape=None):
-    """(pointer, row stride, head stride) of bf16 [rows, heads, head_dim] with dense heads."""
+def _heads_of(t, name, dev, shape):
+    """(pointer, row stride, head stride, shape) of bf16 [rows, heads, head_dim] with dense heads, of `shape` if given."""
     if getattr(t, "dtype", None) is not _torch_mod.bfloat16:
         raise TypeError(f"{name}: expected a bfloat16 tensor")
+    mine = t.shape
     if t.get_device() != dev:
         raise ValueError(f"{name}: expected a CUDA tensor on the current device")
-    if len(t.shape) != 3 or (shape is not None and t.shape != shape):
+    if len(mine) != 3 or (shape is not None and mine != shape):
         raise ValueError(f"{name}: expected [rows, heads, head_dim]{'' if shape is None else ' ' + str(list(shape))}")
-    s = t.stride()
-    if s[2] != 1:
+    row, head, dense = t.stride()
+    if dense != 1:
         raise ValueError(f"{name}: the last dimension must be dense")
-    return t.data_ptr(), s[0], s[1]
+    return t.data_ptr(), row, head, mine
 
 
 def _dense(t, dtype, n, name, dev):
@@ -1118,7 +1130,7 @@ def _dense(t, dtype, n, name, dev):
         return 0
     if getattr(t, "dtype", None) is not dtype:
         raise TypeError(f"{name}: expected {dtype}")
-    if t.get_device() != dev or not t.is_contiguous() or t.numel() != n:
+    if t.get_device() != dev or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name}: expected {n} dense values on the current device")
     return t.data_ptr()
 
@@ -1137,12 +1149,11 @@ def dit_attention_packed(q, k, v, o, q_start=None, k_start=None, visible=None, s
     lse [heads, q_rows] fp32 or None. ws: scratch of dit_attention_packed_workspace_bytes or None."""
     dev, st = _current(stream)
     torch = _torch_mod
-    pq, qr, qh = _heads_of(q, "q", dev)
-    pk, kr, kh = _heads_of(k, "k", dev)
-    pv, vr, vh = _heads_of(v, "v", dev, k.shape)
-    po, orow, oh = _heads_of(o, "o", dev, q.shape)
-    q_rows, heads, d = q.shape
-    k_rows, kv_heads, dk = k.shape
+    pq, qr, qh, shape = _heads_of(q, "q", dev, None)
+    pk, kr, kh, keys = _heads_of(k, "k", dev, None)
+    pv, vr, vh, _ = (pk, kr, kh, keys) if v is k else _heads_of(v, "v", dev, keys)
+    po, orow, oh, _ = _heads_of(o, "o", dev, shape)
+    (q_rows, heads, d), (k_rows, kv_heads, dk) = shape, keys
     if dk != d:
         raise ValueError("q and k: expected one head_dim")
     segments = 1
@@ -1214,34 +1225,38 @@ def dit_linear_epilogue(a, w, out, bias=None, activation: str = "none", gate=Non
     act = _activations.get(activation)
     if act is None:
         raise ValueError(f"activation: expected one of {', '.join(_activations)}")
-    if a.dim() != 2 or w.dim() != 2:
-        raise ValueError("a, w: expected matrices")
-    (M, K), N = a.shape, w.shape[0]
-    _fits(M, K, N)
-    pa, ka, lda = _matrix(a, M, K, dev, "a")
-    pw, kw, ldw = _matrix(w, N, K, dev, "w")
-    if ka != DIT_BF16 or kw != DIT_BF16:
-        raise TypeError("a, w: expected bfloat16")
+    if getattr(a, "dtype", None) is not torch.bfloat16 or getattr(w, "dtype", None) is not torch.bfloat16:
+        raise TypeError("a, w: expected bfloat16 tensors")
+    sa, sw = a.shape, w.shape
+    if len(sa) != 2 or len(sw) != 2 or sa[1] != sw[1]:
+        raise ValueError("a, w: expected [M, K] and [N, K]")
+    (M, K), N = sa, sw[0]
+    if M > _INT_MAX or K > _INT_MAX or N > _INT_MAX:
+        _fits(M, K, N)
+    pa, _, lda = _matrix(a, M, K, dev, "a")
+    pw, _, ldw = _matrix(w, N, K, dev, "w")
     po, ko, ldo = _matrix(out, M, N, dev, "out")
-    pr = ldr = pg = ldg = rows = 0
+    pr = ldr = pg = pm = ldg = rows = 0
     if residual is not None:
-        pr, kr, ldr = _matrix(residual, M, N, dev, "residual")
+        pr, kr, ldr = (po, ko, ldo) if residual is out else _matrix(residual, M, N, dev, "residual")
         if kr != ko:
             raise TypeError("residual: expected the output's type")
     if gate is not None:
         rows = gate.shape[0]
-        _fits(rows)
+        if rows > _INT_MAX:
+            _fits(rows)
         pg, kg, ldg = _matrix(gate, rows, N, dev, "gate")
         if kg != DIT_F32 or rows < 1:
             raise TypeError("gate: expected float32 [rows, N]")
-        if gate_map is None and rows != 1:
+        if gate_map is not None:
+            pm = _dense(gate_map, torch.int32, M, "gate_map", dev)
+        elif rows != 1:
             raise ValueError("gate_map: expected with more than one gate row")
     elif gate_map is not None:
         raise ValueError("gate_map: without a gate")
     if ws is not None and (ws.get_device() != dev or not ws.is_contiguous()):
         raise ValueError("ws: expected a contiguous CUDA tensor on the current device")
-    e = _epilogue_struct.pack(_dense(bias, torch.float32, N, "bias", dev), pg, _dense(gate_map, torch.int32, M, "gate_map", dev),
-                              pr, ldg, ldr, rows, act)
+    e = _epilogue_struct.pack(0 if bias is None else _dense(bias, torch.float32, N, "bias", dev), pg, pm, pr, ldg, ldr, rows, act)
     rc = lib().dit_linear_epilogue(pa, M, lda, K, pw, N, ldw, e, po, ko, ldo, None if ws is None else ws.data_ptr(),
                                    0 if ws is None else ws.numel() * ws.element_size(), st)
     if rc:
