@@ -14,7 +14,8 @@
 // by a scan over q_start: no lengths on the host, and a captured graph serves other lengths. packed_kernel takes two tiles
 // of a segment per CTA: warp 0 loads, warp 1 issues the MMAs, warps 2-9 and 10-17 turn the scores of the two tiles into
 // weights, so that one tile's exponentials overlap the other's MMAs; a row's 128 keys of a tile are two threads' work, who
-// exchange their maxima through shared memory (eight warps with whole rows: PLAIN8 us where these take PLAIN16). packed_rows_kernel takes
+// exchange their maxima through shared memory (4224 rows of 24 heads of 128: 178 us with eight warps of whole rows, 163 so:
+// 1350 TFLOP/s, the GPU at its power limit). packed_rows_kernel takes
 // segments of few rows, two CTAs to an SM. Where there are too few tiles for the SMs the key range is split over CTAs
 // (blockIdx.z) and a second kernel joins the parts in order.
 // Masked places: weights of masked keys are zero, the rows of V behind the last key that any row of the CTA sees are
@@ -194,7 +195,7 @@ __device__ Segment find_tile(const dit_packed_attention& a, int rows, int x) {
 // The weighted sum of V over the keys [j0, j1) that a row does see, on the plain cores: only for rows that the matrix
 // product left not finite beside keys they do not see (0 x NaN). A warp per row; lane l ends with values l D / 32 and on.
 template <int D, bool GEN>
-__device__ __noinline__ void resum_row(const PackedParams& p, int q_at, int k0, int j0, int j1, int head, int kvh, float where,
+__device__ __noinline__ void resum_row(const PackedParams& p, int q_at, int k0, int j0, int j1, int head, int kvh, int place,
                                        float m, float (&acc)[D / 32]) {
   constexpr int V = D / 32;
   const dit_packed_attention& a = p.a;
@@ -216,7 +217,7 @@ __device__ __noinline__ void resum_row(const PackedParams& p, int q_at, int k0, 
     float x = s * p.scale_log2;
     if constexpr (GEN) {
       if (p.cap_out > 0.f) x = capped(s, p.cap_in, p.cap_out);
-      if (a.slope) x = fmaf(-1.4426950408889634f * __ldg(a.slope + head), fabsf(where - float(j)), x);
+      if (a.slope) x = fmaf(-1.4426950408889634f * __ldg(a.slope + head), fabsf(float(place - j)), x);
     }
     const float w = ex2_approx(x - m);
 #pragma unroll
@@ -419,7 +420,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
     const int pair = 1 + t * 4 + quad;  // named barrier of the two warps that share 32 rows
     auto meet = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory"); };
     const bool live = __any_sync(0xffffffffu, lim > 0);  // warps without a row that sees a key only keep the barriers
-    const float where = float(i + seg.nk - seg.nq);      // the row's place among the keys
+    const int place = i + seg.nk - seg.nq;               // the row's place among the keys
     float slope2 = 0.f;
     if constexpr (GEN)
       if (a.slope && valid) slope2 = 1.4426950408889634f * __ldg(a.slope + head);
@@ -427,8 +428,9 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
     // C = 80 the weights are taken against a fixed maximum, C or where that is less 110 - C: they lie within 2^50, and at the
     // row's best key above 2^-110. Neither the row's own maximum nor the exchange of it is needed (9 sequences, capped: 253
     // us with, 232 without).
-    const bool fixed = GEN && p.cap_out > 0.f && p.cap_out <= 80.f;
-    float m = fixed ? fminf(p.cap_out, 110.f - p.cap_out) -slope2 * fmaxf(0.f, where - float(lim - 1)) : -INFINITY, l = 0.f;
+    // (A negative slope grows with the distance: no such bound.)
+    const bool fixed = GEN && p.cap_out > 0.f && p.cap_out <= 80.f && __all_sync(0xffffffffu, slope2 >= 0.f);
+    float m = fixed ? fminf(p.cap_out, 110.f - p.cap_out) -slope2 * float(max(0, place - lim + 1)) : -INFINITY, l = 0.f;
     bool ok = true;
     for (int it = 0; it < n; ++it) {
       const int key0 = (ta + it) * 128;
@@ -453,7 +455,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
         const int first = key0 + half * 64;
         const int seen = lim - first;
         const bool all = __all_sync(0xffffffffu, seen >= 64);
-        if constexpr (GEN) general_scores(x, p, a.slope != nullptr, slope2, where - float(first), seen, all);
+        if constexpr (GEN) general_scores(x, p, a.slope != nullptr, slope2, float(place - first), seen, all);
         if (!all) {
 #pragma unroll
           for (int c = 0; c < 64; ++c)
@@ -578,7 +580,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
           const int end = __shfl_sync(0xffffffffu, min(lim, covered), src);
           const float sm = __shfl_sync(0xffffffffu, m == -INFINITY ? 0.f : m, src), sinv = __shfl_sync(0xffffffffu, inv, src);
           float acc[D / 32];
-          resum_row<D, GEN>(p, seg.q0 + si, seg.k0, ta * 128, end, sh, kvh, __shfl_sync(0xffffffffu, where, src), sm, acc);
+          resum_row<D, GEN>(p, seg.q0 + si, seg.k0, ta * 128, end, sh, kvh, __shfl_sync(0xffffffffu, place, src), sm, acc);
           if ((lane >> 4) != half) continue;  // each warp its half of the row
           if (whole) {
             const int srow = quad * 32 + src, at2 = lane * (D / 32) * 2;  // byte of the row
@@ -791,7 +793,7 @@ __global__ void __launch_bounds__(kRowThreads, 2)
     const uint32_t lane_off = uint32_t(quad * 32) << 16;
     const uint32_t tO = tmem_base + lane_off + 128u;
     const bool live = __any_sync(0xffffffffu, lim > 0);  // warps without a row that sees a key only keep the barriers
-    const float where = float(i + seg.nk - seg.nq);      // the row's place among the keys
+    const int place = i + seg.nk - seg.nq;               // the row's place among the keys
     float slope2 = 0.f;
     if constexpr (GEN)
       if (a.slope && valid) slope2 = 1.4426950408889634f * __ldg(a.slope + head);
@@ -809,7 +811,7 @@ __global__ void __launch_bounds__(kRowThreads, 2)
         tmem_ld_wait();
         const int seen = lim - key0;
         const bool all = __all_sync(0xffffffffu, seen >= kRowKeys);
-        if constexpr (GEN) general_scores(x, p, a.slope != nullptr, slope2, where - float(key0), seen, all);
+        if constexpr (GEN) general_scores(x, p, a.slope != nullptr, slope2, float(place - key0), seen, all);
         if (!all) {
 #pragma unroll
           for (int c = 0; c < 64; ++c)
@@ -930,7 +932,7 @@ __global__ void __launch_bounds__(kRowThreads, 2)
         const int end = __shfl_sync(0xffffffffu, min(lim, covered), src);
         const float sm = __shfl_sync(0xffffffffu, m == -INFINITY ? 0.f : m, src), sinv = __shfl_sync(0xffffffffu, inv, src);
         float acc[D / 32];
-        resum_row<D, GEN>(p, seg.q0 + si, seg.k0, ta * kRowKeys, end, sh, kvh, __shfl_sync(0xffffffffu, where, src), sm, acc);
+        resum_row<D, GEN>(p, seg.q0 + si, seg.k0, ta * kRowKeys, end, sh, kvh, __shfl_sync(0xffffffffu, place, src), sm, acc);
         if (whole) {
           uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + (seg.q0 + si) * a.o_row + sh * a.o_head + lane * (D / 32));
 #pragma unroll
@@ -1144,6 +1146,8 @@ int packed_attention_check(const dit_packed_attention* a, const void* ws) {
   const int rc = packed_sizes(a->q_rows, a->k_rows, a->segments, a->heads, a->kv_heads, a->head_dim);
   if (rc != DIT_OK) return rc;
   if (!(a->scale > 0.f) || !std::isfinite(a->scale) || !(a->cap >= 0.f) || !std::isfinite(a->cap)) return DIT_EINVAL;
+  // what the kernels are handed in log2 units
+  if (a->scale > 2e38f || (a->cap > 0.f && (a->cap > 2e38f || !std::isfinite(float(3.0 * a->scale / a->cap))))) return DIT_EINVAL;
   if (a->q_rows == 0 || a->segments == 0) return DIT_OK;
   if (a->segments > 1 && (!a->q_start || !a->k_start)) return DIT_EINVAL;
   if ((a->q_start == nullptr) != (a->k_start == nullptr)) return DIT_EINVAL;

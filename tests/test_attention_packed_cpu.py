@@ -66,7 +66,7 @@ def test_refusals(L):
     for n in ("lse", "q_start", "k_start", "visible", "slope"):
         assert _call(L, **{n: (1 << 18) + 2}) == -1, n
     for kw in (dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(cap=-1.0),
-               dict(cap=float("nan")), dict(cap=float("inf")), dict(q_start=0), dict(k_start=0), dict(q_start=0, k_start=0),
+               dict(cap=float("nan")), dict(cap=float("inf")), dict(cap=1e-39), dict(scale=3e38), dict(cap=3e38), dict(q_start=0), dict(k_start=0), dict(q_start=0, k_start=0),
                dict(segments=1, q_start=0), dict(q_rows=-1), dict(k_rows=-1), dict(segments=-1), dict(heads=0),
                dict(kv_heads=0), dict(head_dim=0), dict(o=1 << 12), dict(o=1 << 13), dict(o=1 << 14)):
         assert _call(L, **kw) == -1, kw

@@ -365,3 +365,17 @@ def test_many_tiles_what_is_masked_never_matters():
     few = [0, 20, 47]
     _check(out[:500, few], None, q[:500, few], k[:, few], v[:, few], [0, 500], [0, n], vis[:500], d ** -0.5, 0.0, None)
     assert torch.isnan(out[500:].float()).any(-1).all()
+
+
+@pytest.mark.parametrize("rows", [1, 300])
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+def test_far_keys_preferred(rows, cap):
+    # negative slopes: the bias grows with the distance, far past what a cap bounds
+    g = np.random.default_rng(rows)
+    d, n, H = 64, 900, 4
+    q, k, v = _bf16(g, rows, H, d), _bf16(g, n, 2, d), _bf16(g, n, 2, d)
+    slope = np.array([-0.5, 0.25, -0.01, 0.0])
+    o, lse = torch.empty_like(q).cuda(), torch.empty(H, rows, device="cuda")
+    D.dit_attention_packed(q.cuda(), k.cuda(), v.cuda(), o, cap=cap, lse=lse, slope=dev(slope.astype(np.float32)))
+    D.dit_check()
+    _check(o, lse, q, k, v, [0, rows], [0, n], None, 0.125, cap, slope)
