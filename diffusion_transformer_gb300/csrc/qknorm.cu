@@ -8,7 +8,9 @@
 //
 // What bounds it: HBM. Forward: each value read once and written once. Backward: x and dy read once, dx written
 // once; dw is summed in registers along the rows a thread meets, over the CTA's groups in shared memory, and over
-// the CTAs by a second small kernel, each in a fixed order, so a call's result does not depend on timing.
+// the CTAs by a second small kernel, each in a fixed order, so a call's result does not depend on timing. 4224 rows of
+// 24 + 24 heads of 128 in bf16: 20.7 us forward (5.0 TB/s, instruction issue at 0.69 of a cycle), 35 backward (4.4 TB/s); one row
+// 3.3 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -46,9 +48,11 @@ struct QkArgs {
 // A unit is what one lane holds of a head, as in the rotary kernel: VE consecutive values, with their VE partners
 // in the split-halves layout (VE = 1: one pair, or one value that does not turn). A head stands on `lanes`
 // neighbouring lanes, NU units on each, so its sum of squares is a butterfly within a warp and the values stay in
-// registers between the sum and the turn. The CTA's groups of lanes go through the heads of a few rows, U heads
-// in flight each; the rows' cosines and sines are worked out once into shared memory.
-// Heads of a lane's registers at a time (and as many on their way): two of eight values, one of sixteen
+// registers between the sum and the turn. A CTA takes a chunk of rows, whose cosines and sines it works out once into shared
+// memory; a group of lanes takes one of them (or shares it with others) and keeps its units' angles in registers through
+// the row's heads. (4224 rows of 24 + 24 heads in bf16: 26.8 us with groups that stepped through heads of several rows,
+// 24.0 with the next heads loaded ahead, 20.7 with a row to a group.)
+// Heads in a lane's registers at a time (and as many on their way): two of eight values, one of sixteen
 __host__ __device__ constexpr int qk_flight(int nu, int vals) { return nu == 1 && vals <= 8 ? 2 : 1; }
 template <typename T, int VE, bool HALVES, int NU, bool GRAD>
 struct QkCfg {
