@@ -427,10 +427,12 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
     // Capped scores lie within the cap C (log2 units) of 0, or with a bias of what the nearest key that the row sees loses: up to
     // C = 80 the weights are taken against a fixed maximum, C or where that is less 110 - C: they lie within 2^50, and at the
     // row's best key above 2^-110. Neither the row's own maximum nor the exchange of it is needed (9 sequences, capped: 253
-    // us with, 232 without).
+    // us with, 232 without). The nearest key lies behind the row where the row's place is past what it sees, and ahead of it
+    // where there are more rows than keys and the place is negative.
     // (A negative slope grows with the distance: no such bound.)
     const bool fixed = GEN && p.cap_out > 0.f && p.cap_out <= 80.f && __all_sync(0xffffffffu, slope2 >= 0.f);
-    float m = fixed ? fminf(p.cap_out, 110.f - p.cap_out) -slope2 * float(max(0, place - lim + 1)) : -INFINITY, l = 0.f;
+    float m = -INFINITY, l = 0.f;
+    if (fixed) m = fminf(p.cap_out, 110.f - p.cap_out) - slope2 * float(max(max(0, place - lim + 1), -place));
     bool ok = true;
     for (int it = 0; it < n; ++it) {
       const int key0 = (ta + it) * 128;

@@ -379,3 +379,20 @@ def test_far_keys_preferred(rows, cap):
     D.dit_attention_packed(q.cuda(), k.cuda(), v.cuda(), o, cap=cap, lse=lse, slope=dev(slope.astype(np.float32)))
     D.dit_check()
     _check(o, lse, q, k, v, [0, rows], [0, n], None, 0.125, cap, slope)
+
+
+@pytest.mark.parametrize("rows,n", [(700, 300), (3000, 1100), (40, 9)])
+@pytest.mark.parametrize("cap", [0.0, 20.0, 50.0])
+def test_more_rows_than_keys_with_a_bias(rows, n, cap):
+    # the first rows' places lie before the first key: even their nearest key is far, and the row still has its weights
+    g = np.random.default_rng(rows + n)
+    d, H = 64, 4
+    q, k, v = _bf16(g, rows, H, d), _bf16(g, n, 4, d), _bf16(g, n, 4, d)
+    slope = np.array([0.5, 2.0 ** -8, 2.0, 0.0])
+    vis = g.integers(0, n + 1, rows).astype(np.int32)
+    for visible in (None, vis):
+        o, lse = torch.empty_like(q).cuda(), torch.empty(H, rows, device="cuda")
+        D.dit_attention_packed(q.cuda(), k.cuda(), v.cuda(), o, cap=cap, lse=lse, slope=dev(slope.astype(np.float32)),
+                               visible=None if visible is None else dev(visible))
+        D.dit_check()
+        _check(o, lse, q, k, v, [0, rows], [0, n], visible, 0.125, cap, slope)
