@@ -16,7 +16,7 @@
 // weights, so that one tile's exponentials overlap the other's MMAs; a row's 128 keys of a tile are two threads' work, who
 // exchange their maxima through shared memory (4224 rows of 24 heads of 128: 178 us with eight warps of whole rows, 163 so:
 // 1350 TFLOP/s, the GPU at its power limit). packed_rows_kernel takes
-// segments of few rows, two CTAs to an SM. Where there are too few tiles for the SMs the key range is split over CTAs
+// segments of few rows or short ones, two CTAs to an SM. Where there are too few tiles for the SMs the key range is split over CTAs
 // (blockIdx.z) and a second kernel joins the parts in order.
 // Masked places: weights of masked keys are zero, the rows of V behind the last key that any row of the CTA sees are
 // zeroed in shared memory (they may be the next segment's, or anything), and a row whose result is not finite while
@@ -629,7 +629,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
 }
 
 // ------------------------------------------------------------------------------------------
-// Few rows over many keys: HBM-bound. One tile of up to 128 (row, head) pairs per CTA, key tiles of 64, two CTAs to an SM
+// Few rows over many keys, HBM-bound, and short segments, bound by a CTA's start and end. One tile of up to 128 (row, head) pairs per CTA, key tiles of 64, two CTAs to an SM
 // (256 columns of tensor memory and at most 113 KB of shared memory each), so that one CTA's start and end run under the
 // other's loads. K and V tiles come through one ring in the order in which the MMAs use them: K0 K1 V0 K2 V1 ... The
 // scores of tile j + 1 are computed while the softmax works on tile j. Q takes only the rows it has: the MMA's other
@@ -1003,7 +1003,10 @@ __global__ void __launch_bounds__(256) packed_join_kernel(const __grid_constant_
 }
 
 // Tiles, CTAs and key splits of a call. Segments whose rows fit one tile, on average, go to the few-rows kernel, in tiles of
-// the average's rows (32 (row, head) pairs at least: a tile's rows are shared memory). The key range is split where the
+// the average's rows (32 (row, head) pairs at least: a tile's rows are shared memory); so do segments of 1024 keys at most on
+// average, where the start and the end of a CTA cost more than K and V read once for two tiles saves (whole tiles against few
+// rows: 300 rows and keys 12.5 and 8.5 us, 600 in 24 heads 15.2 and 12.9, 7 x 800 91 and 78, 64 x 583 114 and 104; 1088 in 24
+// heads 21.6 and 22.9, 4224 163 and 182). The key range is split where the
 // tiles leave SMs idle.
 struct PackedPlan {
   int G, rpt, slots, splits;
@@ -1015,7 +1018,8 @@ PackedPlan packed_plan(int q_rows, int k_rows, int segments, int heads, int kv_h
   PackedPlan r{};
   r.G = heads / kv_heads;
   r.rpt = 128 / r.G;
-  r.few = (long long)q_rows <= (long long)segments * r.rpt;
+  const bool tall = (long long)q_rows > (long long)segments * r.rpt;
+  r.few = !tall || k_rows <= 1024LL * segments;
   if (r.few) r.rpt = std::min(r.rpt, std::max(32 / r.G, std::max(1, (q_rows + segments - 1) / segments)));
   const long long rows = (r.few ? 1LL : 2LL) * r.rpt;
   r.tiles = std::min<long long>((q_rows + segments * (rows - 1)) / rows, q_rows);
@@ -1026,11 +1030,15 @@ PackedPlan packed_plan(int q_rows, int k_rows, int segments, int heads, int kv_h
   // Few rows, two CTAs to an SM: with fewer tiles than those, one wave of parts of 256 keys at least (1 row, 24 heads, 1088 keys:
   // 16.0 us whole, 10.9 in four; 32 tiles over 4000 keys: 45.2 whole, 15.9 in eight, 22.0 in twelve, which is more than a
   // wave); with more, six waves of parts of 1024 keys at least, which evens out unlike lengths (512 tiles over 2048 to 8192
-  // keys: 257 us whole, 229 in four, 253 in eight). Whole tiles: only where a wave of them would fit twice.
+  // keys: 257 us whole, 229 in four, 253 in eight). Short segments of several tiles:
+  // only where there are an eighth of the SMs' tiles at most (600 rows and keys, 24 heads: 12.9 us whole, 22.4 in two; 1000 in
+  // one head: 15.6 whole, 13.3 in three). Whole tiles: only where a wave of them would fit twice.
   long long want, least;
   if (!r.few) {
     want = sms / units;
     least = 512;
+  } else if (tall && 8 * units > sms) {
+    want = least = 1;
   } else if (units <= 2 * sms) {
     want = 2 * sms / units;
     least = 256;

@@ -396,3 +396,90 @@ def test_more_rows_than_keys_with_a_bias(rows, n, cap):
                                visible=None if visible is None else dev(visible))
         D.dit_check()
         _check(o, lse, q, k, v, [0, rows], [0, n], visible, 0.125, cap, slope)
+
+
+LIB = D
+
+
+class _Behind:
+    """The library over caches that go on behind the last sequence, with NaN there: key segments count as long ones, so
+    tall segments run in whole tiles however few keys they have."""
+
+    dit_check = staticmethod(LIB.dit_check)
+
+    @staticmethod
+    def more(segments):
+        return 1025 * segments
+
+    def dit_attention_packed_workspace_bytes(self, q_rows, k_rows, segments, *rest):
+        return LIB.dit_attention_packed_workspace_bytes(q_rows, k_rows + self.more(segments), segments, *rest)
+
+    def dit_attention_packed(self, q, k, v, o, at=None, kt=None, **kw):
+        if at is None:
+            at, kt = (dev(np.array([0, t.shape[0]], np.int32)) for t in (q, k))
+        rows = self.more(at.numel() - 1)
+        k, v = (torch.cat([t, t.new_full((rows, *t.shape[1:]), float("nan"))]) for t in (k, v))
+        LIB.dit_attention_packed(q, k, v, o, at, kt, **kw)
+
+
+@pytest.fixture
+def behind(monkeypatch):
+    monkeypatch.setitem(globals(), "D", _Behind())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens", ["past", "pair", "ragged"])
+@pytest.mark.parametrize("heads,kv", [(2, 2), (6, 2), (5, 1)])
+@pytest.mark.parametrize("mask", ["all", "causal", "any"])
+def test_whole_tiles_lengths_masks_and_heads(behind, d, lens, heads, kv, mask):
+    test_lengths_masks_and_heads(d, lens, heads, kv, mask)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("mask", ["none", "text", "causal"])
+def test_whole_tiles_long_segments(behind, d, mask):
+    test_long_segments(d, mask)
+
+
+def test_whole_tiles_what_is_masked_never_matters(behind):
+    test_what_is_masked_never_matters(260)
+    test_many_tiles_what_is_masked_never_matters()
+
+
+@pytest.mark.parametrize("cap", [1.0, 38.0, 39.0, 50.0, 55.0, 56.0, 90.0, 1000.0])
+@pytest.mark.parametrize("sign", [-1.0, 1.0])
+def test_whole_tiles_caps_reached_on_either_side(behind, cap, sign):
+    test_caps_reached_on_either_side(cap, sign)
+
+
+@pytest.mark.parametrize("name", list(WORK))
+@pytest.mark.parametrize("mask", ["all", "causal", "any"])
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (20.0, True)])
+def test_whole_tiles_many(behind, name, mask, cap, bias):
+    test_many_tiles(name, mask, cap, bias)
+
+
+@pytest.mark.parametrize("cap", [0.0, 20.0, 50.0])
+def test_whole_tiles_biases(behind, cap):
+    test_far_keys_preferred(300, cap)
+    test_more_rows_than_keys_with_a_bias(700, 300, cap)
+
+
+def test_whole_tiles_far_scores(behind):
+    test_far_scores_and_one_dominant_key()
+
+
+def test_whole_tiles_of_columns_and_head_major():
+    g = np.random.default_rng(9)
+    H, Hk, d, n = 6, 3, 64, 190
+    m = _bf16(g, n + 1025, H + 2 * Hk, d)
+    m[n:] = float("nan")
+    m = m.cuda()
+    q, k, v, o = m[:n, :H], m[:, H:H + Hk], m[:, H + Hk:], torch.empty(n, H, d, dtype=torch.bfloat16, device="cuda")
+    at = dev(np.array([0, n], np.int32))
+    D.dit_attention_packed(q, k, v, o, at, at)
+    _check(o, None, q, k[:n], v[:n], [0, n], [0, n], None, d ** -0.5, 0.0, None)
+    heads = [t.transpose(0, 1).contiguous().transpose(0, 1) for t in (q, k, v, o)]
+    D.dit_attention_packed(*heads, at, at)
+    assert torch.equal(heads[3], o)
+    D.dit_check()
