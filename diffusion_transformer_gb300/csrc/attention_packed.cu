@@ -45,12 +45,21 @@ constexpr float kRescaleStep = 8.0f;  // log2 units: the running maximum moves o
 constexpr int kMaxSplits = 32;
 constexpr int kPackedThreads = 64 + 32 * 16;  // loader, MMA issuer, sixteen softmax warps
 
+// What a call's scores go through. kCapped also serves a bias without a cap; its error is a few 2^-24 of the cap, so caps of
+// more than kWideLog2 log2 units (where that is 4e-5, what the sums of the products may be off by) go by kWide, whose
+// error is relative to the score. (9 sequences of 811 to 1943 rows, 16 heads of 64 over 4: 255 us under a cap of 177, 259 under
+// 178 and up; two of 2489 and 2829 rows, 24 heads of 128: 286 and 319; with a score past a quarter of its cap in every
+// warp 436 and 464.)
+enum Scores : int { kPlain = 0, kCapped = 1, kWide = 2 };
+constexpr float kWideLog2 = 256.f, kFixedLog2 = 80.f;
+
 struct PackedParams {
   dit_packed_attention a;
   int G, rpt;  // query heads per key head, query rows of a tile
   int splits, slots;  // CTAs along the keys; ring slots of the few-rows kernel
   float scale_log2;  // scale log2(e)
   float cap_in, cap_out;  // 2 scale log2(e) / cap and cap log2(e); cap_out = 0: no cap
+  float cap_arg;  // scale / cap
   float* part_o;   // [split][q_rows][heads][d]
   float2* part_ml;  // [split][q_rows][heads]: running maximum (log2 units) and sum
   int* err;
@@ -86,6 +95,23 @@ __device__ __forceinline__ float capped(float s, float cap_in, float cap_out) {
   return fmaf(-2.f * cap_out, rcp_approx(1.f + ex2_approx(s * cap_in)), cap_out);
 }
 
+// The same for any cap, with an error relative to the score: up to t = scale s / cap = 1/2 the odd series of tanh around 0,
+// x (1 - t^2 / 3 + 2 t^4 / 15 - ... + 21844 t^12 / 6081075) with x the uncapped score (the next term is below 2^-23 of it),
+// above it c (1 - 2 / (1 + e^2|t|)) with the sign of s, at least 0.46 c. (With c - 2 c / (1 + e^2t) throughout, scores of a few
+// units were off by 0.02 under a cap of 1e5 and by 1.7 under 1e7.)
+__device__ __forceinline__ float capped_wide(float s, const PackedParams& p) {
+  const float t = s * p.cap_arg, z = t * t;
+  float f = fmaf(z, 21844.f / 6081075.f, -1382.f / 155925.f);
+  f = fmaf(z, f, 62.f / 2835.f);
+  f = fmaf(z, f, -17.f / 315.f);
+  f = fmaf(z, f, 2.f / 15.f);
+  f = fmaf(z, f, -1.f / 3.f);
+  f = fmaf(z, f, 1.f);
+  const float e = ex2_approx(-fabsf(s * p.cap_in));
+  const float far = p.cap_out * fmaf(-2.f * e, rcp_approx(1.f + e), 1.f);
+  return fabsf(t) < 0.5f ? s * p.scale_log2 * f : copysignf(far, s);
+}
+
 // Two capped scores at once, c tanh t = c - 2 c / (1 + e^2t): one reciprocal serves both (1 / a = b / ab). e^2t is held below
 // 2^60, where tanh is 1 to the last place, so that the product stays finite. A NaN takes both with it: masked places are
 // cleared before. (9 sequences, capped, 254 us; a quotient for each 266; tanh as a polynomial of degree 15 on the FMA pipe,
@@ -102,11 +128,28 @@ __device__ __forceinline__ void capped2(float& a, float& b, float cap_in, float 
 
 // Raw sums of products into scores in log2 units: cap, then the distance bias (`at`: the row's place less the first
 // key's; the row sees the first `seen` of the N, `all`: every row of the warp sees all)
-template <int N>
+template <int N, int KIND>
 __device__ __forceinline__ void general_scores(uint32_t (&x)[N], const PackedParams& p, bool bias, float slope2, float at,
                                                int seen, bool all) {
   auto val = [&](int c) { return __uint_as_float(x[c]); };
-  if (p.cap_out > 0.f) {
+  if constexpr (KIND == kWide) {
+    // mostly every score of a warp is far below such a cap: up to t = 1/4 five terms of the series do (the sixth is below
+    // 2^-26 of the score)
+    float top = 0.f;
+#pragma unroll
+    for (int c = 0; c < N; c += 2) top = fmax3(top, fabsf(val(c)), fabsf(val(c + 1)));
+    if (__all_sync(0xffffffffu, top * p.cap_arg <= 0.25f)) {
+#pragma unroll
+      for (int c = 0; c < N; ++c) {
+        const float t = val(c) * p.cap_arg, z = t * t;
+        const float f = fmaf(z, fmaf(z, fmaf(z, 62.f / 2835.f, -17.f / 315.f), 2.f / 15.f), -1.f / 3.f);
+        x[c] = __float_as_uint(val(c) * p.scale_log2 * fmaf(z, f, 1.f));
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < N; ++c) x[c] = __float_as_uint(capped_wide(val(c), p));
+    }
+  } else if (p.cap_out > 0.f) {
     if (!all) {
 #pragma unroll
       for (int c = 0; c < N; ++c)
@@ -194,7 +237,7 @@ __device__ Segment find_tile(const dit_packed_attention& a, int rows, int x) {
 
 // The weighted sum of V over the keys [j0, j1) that a row does see, on the plain cores: only for rows that the matrix
 // product left not finite beside keys they do not see (0 x NaN). A warp per row; lane l ends with values l D / 32 and on.
-template <int D, bool GEN>
+template <int D, int KIND>
 __device__ __noinline__ void resum_row(const PackedParams& p, int q_at, int k0, int j0, int j1, int head, int kvh, int place,
                                        float m, float (&acc)[D / 32]) {
   constexpr int V = D / 32;
@@ -215,8 +258,9 @@ __device__ __noinline__ void resum_row(const PackedParams& p, int q_at, int k0, 
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     float x = s * p.scale_log2;
-    if constexpr (GEN) {
-      if (p.cap_out > 0.f) x = capped(s, p.cap_in, p.cap_out);
+    if constexpr (KIND != kPlain) {
+      if constexpr (KIND == kWide) x = capped_wide(s, p);
+      else if (p.cap_out > 0.f) x = capped(s, p.cap_in, p.cap_out);
       if (a.slope) x = fmaf(-1.4426950408889634f * __ldg(a.slope + head), fabsf(float(place - j)), x);
     }
     const float w = ex2_approx(x - m);
@@ -225,11 +269,12 @@ __device__ __noinline__ void resum_row(const PackedParams& p, int q_at, int k0, 
   }
 }
 
-template <int D, bool GEN>
+template <int D, int KIND>
 __global__ void __launch_bounds__(kPackedThreads, 1)
     packed_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PackedParams p) {
   using Cfg = PackedCfg<D>;
+  constexpr bool GEN = KIND != kPlain;
   constexpr int KS = Cfg::kKS, VS = Cfg::kVS;
   extern __shared__ __align__(256) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -425,12 +470,12 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
     if constexpr (GEN)
       if (a.slope && valid) slope2 = 1.4426950408889634f * __ldg(a.slope + head);
     // Capped scores lie within the cap C (log2 units) of 0, or with a bias of what the nearest key that the row sees loses: up to
-    // C = 80 the weights are taken against a fixed maximum, C or where that is less 110 - C: they lie within 2^50, and at the
+    // kFixedLog2 the weights are taken against a fixed maximum, C or where that is less 110 - C: they lie within 2^50, and at the
     // row's best key above 2^-110. Neither the row's own maximum nor the exchange of it is needed (9 sequences, capped: 253
     // us with, 232 without). The nearest key lies behind the row where the row's place is past what it sees, and ahead of it
     // where there are more rows than keys and the place is negative.
     // (A negative slope grows with the distance: no such bound.)
-    const bool fixed = GEN && p.cap_out > 0.f && p.cap_out <= 80.f && __all_sync(0xffffffffu, slope2 >= 0.f);
+    const bool fixed = KIND == kCapped && p.cap_out > 0.f && p.cap_out <= kFixedLog2 && __all_sync(0xffffffffu, slope2 >= 0.f);
     float m = -INFINITY, l = 0.f;
     if (fixed) m = fminf(p.cap_out, 110.f - p.cap_out) - slope2 * float(max(max(0, place - lim + 1), -place));
     bool ok = true;
@@ -457,7 +502,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
         const int first = key0 + half * 64;
         const int seen = lim - first;
         const bool all = __all_sync(0xffffffffu, seen >= 64);
-        if constexpr (GEN) general_scores(x, p, a.slope != nullptr, slope2, float(place - first), seen, all);
+        if constexpr (GEN) general_scores<64, KIND>(x, p, a.slope != nullptr, slope2, float(place - first), seen, all);
         if (!all) {
 #pragma unroll
           for (int c = 0; c < 64; ++c)
@@ -582,7 +627,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
           const int end = __shfl_sync(0xffffffffu, min(lim, covered), src);
           const float sm = __shfl_sync(0xffffffffu, m == -INFINITY ? 0.f : m, src), sinv = __shfl_sync(0xffffffffu, inv, src);
           float acc[D / 32];
-          resum_row<D, GEN>(p, seg.q0 + si, seg.k0, ta * 128, end, sh, kvh, __shfl_sync(0xffffffffu, place, src), sm, acc);
+          resum_row<D, KIND>(p, seg.q0 + si, seg.k0, ta * 128, end, sh, kvh, __shfl_sync(0xffffffffu, place, src), sm, acc);
           if ((lane >> 4) != half) continue;  // each warp its half of the row
           if (whole) {
             const int srow = quad * 32 + src, at2 = lane * (D / 32) * 2;  // byte of the row
@@ -643,10 +688,11 @@ constexpr uint32_t kRowSmem = 113 * 1024, kRowBars = 8 * (2 * kRowSlotsMost + 8)
 __device__ __forceinline__ int place_k(int j) { return j == 0 ? 0 : 2 * j - 1; }
 __device__ __forceinline__ int place_v(int j, int n) { return j + 1 < n ? 2 * j + 2 : 2 * j + 1; }
 
-template <int D, bool GEN>
+template <int D, int KIND>
 __global__ void __launch_bounds__(kRowThreads, 2)
     packed_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PackedParams p) {
+  constexpr bool GEN = KIND != kPlain;
   constexpr uint32_t kSlot = kRowKeys * D * 2, kBox = kRowKeys * 128;  // a tile of K or V; its boxes of 64 values
   extern __shared__ __align__(256) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -813,7 +859,7 @@ __global__ void __launch_bounds__(kRowThreads, 2)
         tmem_ld_wait();
         const int seen = lim - key0;
         const bool all = __all_sync(0xffffffffu, seen >= kRowKeys);
-        if constexpr (GEN) general_scores(x, p, a.slope != nullptr, slope2, float(place - key0), seen, all);
+        if constexpr (GEN) general_scores<64, KIND>(x, p, a.slope != nullptr, slope2, float(place - key0), seen, all);
         if (!all) {
 #pragma unroll
           for (int c = 0; c < 64; ++c)
@@ -934,7 +980,7 @@ __global__ void __launch_bounds__(kRowThreads, 2)
         const int end = __shfl_sync(0xffffffffu, min(lim, covered), src);
         const float sm = __shfl_sync(0xffffffffu, m == -INFINITY ? 0.f : m, src), sinv = __shfl_sync(0xffffffffu, inv, src);
         float acc[D / 32];
-        resum_row<D, GEN>(p, seg.q0 + si, seg.k0, ta * kRowKeys, end, sh, kvh, __shfl_sync(0xffffffffu, place, src), sm, acc);
+        resum_row<D, KIND>(p, seg.q0 + si, seg.k0, ta * kRowKeys, end, sh, kvh, __shfl_sync(0xffffffffu, place, src), sm, acc);
         if (whole) {
           uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + (seg.q0 + si) * a.o_row + sh * a.o_head + lane * (D / 32));
 #pragma unroll
@@ -1063,7 +1109,7 @@ bool packed_map(CUtensorMap* m, const void* base, int d, int heads, int rows, lo
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool FEW, bool GEN>
+template <int D, bool FEW, int KIND>
 int packed_go(const PackedParams& p, const PackedPlan& pl, cudaStream_t st) {
   const dit_packed_attention& a = p.a;
   constexpr int kKeys = FEW ? kRowKeys : 128;
@@ -1076,12 +1122,12 @@ int packed_go(const PackedParams& p, const PackedPlan& pl, cudaStream_t st) {
   const dim3 grid(unsigned(pl.tiles), unsigned(a.kv_heads), unsigned(p.splits));
   cudaError_t e;
   if constexpr (FEW) {
-    auto kern = packed_rows_kernel<D, GEN>;
+    auto kern = packed_rows_kernel<D, KIND>;
     if (!smem_attr_once(reinterpret_cast<const void*>(kern), kRowSmem)) return DIT_ECUDA;
     e = launch_pdl(kern, grid, dim3(kRowThreads), kRowSmem, st, 1, tq, tk, tv, p);
   } else {
     using Cfg = PackedCfg<D>;
-    auto kern = packed_kernel<D, GEN>;
+    auto kern = packed_kernel<D, KIND>;
     if (!smem_attr_once(reinterpret_cast<const void*>(kern), Cfg::kSmem)) return DIT_ECUDA;
     e = launch_pdl(kern, grid, dim3(kPackedThreads), Cfg::kSmem, st, 1, tq, tk, tv, p);
   }
@@ -1093,11 +1139,14 @@ int packed_go(const PackedParams& p, const PackedPlan& pl, cudaStream_t st) {
   return cudaGetLastError() == cudaSuccess ? DIT_OK : DIT_ECUDA;
 }
 
-template <int D>
+template <int D, bool FEW>
 int packed_kind(const PackedParams& p, const PackedPlan& pl, cudaStream_t st) {
-  const bool gen = p.cap_out > 0.f || p.a.slope;
-  if (pl.few) return gen ? packed_go<D, true, true>(p, pl, st) : packed_go<D, true, false>(p, pl, st);
-  return gen ? packed_go<D, false, true>(p, pl, st) : packed_go<D, false, false>(p, pl, st);
+  if (p.cap_out > kWideLog2) return packed_go<D, FEW, kWide>(p, pl, st);
+  return p.cap_out > 0.f || p.a.slope ? packed_go<D, FEW, kCapped>(p, pl, st) : packed_go<D, FEW, kPlain>(p, pl, st);
+}
+template <int D>
+int packed_rows(const PackedParams& p, const PackedPlan& pl, cudaStream_t st) {
+  return pl.few ? packed_kind<D, true>(p, pl, st) : packed_kind<D, false>(p, pl, st);
 }
 
 bool packed_al16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
@@ -1146,9 +1195,10 @@ int packed_attention_launch(const dit_packed_attention& a, void* ws, size_t ws_b
   if (a.cap > 0.f) {
     p.cap_in = float(2.0 * a.scale * log2e / a.cap);
     p.cap_out = float(a.cap * log2e);
+    p.cap_arg = float(double(a.scale) / a.cap);
   }
   p.err = err;
-  return a.head_dim == 64 ? packed_kind<64>(p, pl, st) : packed_kind<128>(p, pl, st);
+  return a.head_dim == 64 ? packed_rows<64>(p, pl, st) : packed_rows<128>(p, pl, st);
 }
 
 int packed_attention_check(const dit_packed_attention* a, const void* ws) {

@@ -1,0 +1,100 @@
+"""Packed attention where a cap is far above the scores, on the GPU against the oracle in 64 bits.
+
+Gate. A score is d exact products summed in fp32: off by d 2^-23 sum |q k| scale; its cap, bias and maximum and the
+exponential are off by at most 2^-20 (1 + |x| + bias), |x| the score under its cap. The cap itself is in no term: a score far
+below it is as good as without it. Weights round to bf16 (2^-8), sums over n keys are fp32 (n 2^-23)."""
+
+import numpy as np
+import pytest
+import torch
+
+import diffusion_transformer_gb300 as D
+import oracle as O
+from tests.gpu_util import dev
+
+pytestmark = pytest.mark.gpu
+
+
+def _bf16(g, *shape, gain=1.0):
+    return torch.from_numpy((gain * g.standard_normal(shape)).astype(np.float32)).bfloat16()
+
+
+def _np(t):
+    return t.double().cpu().numpy()
+
+
+def _gate(q, k, nk, mag, scale, cap, slope):
+    big = max((np.abs(q[:, h]) @ np.abs(k[:, h * k.shape[1] // q.shape[1]]).T).max() for h in range(q.shape[1])) * scale
+    far = (np.abs(slope).max() if slope is not None else 0.0) * max(len(q), nk)
+    t = q.shape[2] * 2.0 ** -23 * big + 2.0 ** -20 * (1 + (min(big, cap) if cap else big) + far)
+    return t, (2.0 ** -8 + 3 * t + nk * 2.0 ** -22) * mag
+
+
+def _check(o, lse, q, k, v, vis, scale, cap, slope):
+    q, k, v, got = _np(q), _np(k), _np(v), _np(o)
+    ref, rlse, mag = O.attention_packed(q, k, v, [0, len(q)], [0, len(k)], vis, scale, cap, slope)
+    t, gate = _gate(q, k, len(k), mag, scale, cap, slope)
+    off = np.abs(got - ref)
+    assert (off <= gate + 2.0 ** -8 * (np.abs(ref) + gate)).all(), float(np.nanmax(off / (gate + 1e-300)))
+    if lse is not None:
+        gl, none = _np(lse), np.isneginf(rlse)
+        assert np.array_equal(np.isneginf(gl), none)
+        gl, rl = gl[~none], rlse[~none]
+        assert (np.abs(gl - rl) <= t + len(k) * 2.0 ** -23 + 2.0 ** -20 * (1 + np.abs(rl))).all(), float(np.abs(gl - rl).max())
+
+
+def _ws(q, k):
+    n = D.dit_attention_packed_workspace_bytes(q.shape[0], k.shape[0], 1, q.shape[1], k.shape[1], q.shape[2])
+    return torch.empty(max(16, n), dtype=torch.uint8, device="cuda")
+
+
+ROWS = [3, 200]  # the few-rows kernel, and whole tiles (more rows than a tile's over more than 1024 keys)
+KEYS = 1100
+
+
+@pytest.mark.parametrize("cap", [60.0, 177.0, 178.0, 1e3, 1e4, 1e5, 1e6, 1e7, 1e12, 1e30, 2e38])
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("d", [64, 128])
+def test_scores_far_below_their_cap(cap, rows, d):
+    g = np.random.default_rng(rows + d)
+    q, k, v = _bf16(g, rows, 2, d, gain=2.0), _bf16(g, KEYS, 2, d), _bf16(g, KEYS, 2, d)
+    vis = g.integers(0, KEYS + 1, rows).astype(np.int32)
+    for slope in (None, np.array([0.25, 2.0 ** -6])):
+        for ws in (None, _ws(q, k)):
+            o, lse = torch.empty_like(q).cuda(), torch.empty(2, rows, device="cuda")
+            D.dit_attention_packed(q.cuda(), k.cuda(), v.cuda(), o, visible=dev(vis), cap=cap, lse=lse, ws=ws,
+                                   slope=None if slope is None else dev(slope.astype(np.float32)))
+            D.dit_check()
+            _check(o, lse, q, k, v, vis, d ** -0.5, cap, slope)
+
+
+@pytest.mark.parametrize("cap", [60.0, 300.0, 1e4])
+@pytest.mark.parametrize("rows", ROWS)
+def test_scores_around_a_large_cap(cap, rows):
+    # from far below the cap to three times it on either side, half of it among them
+    g = np.random.default_rng(rows)
+    d = 64
+    q, k, v = _bf16(g, rows, 2, d), torch.zeros(KEYS, 2, d), _bf16(g, KEYS, 2, d)
+    q[:] = 0
+    q[:, :, 0] = 1
+    k[:, :, 0] = torch.from_numpy(cap * np.concatenate([np.linspace(-3, 3, KEYS - 200), np.linspace(-0.01, 0.01, 200)])[:, None])
+    k = k.bfloat16()
+    o, lse = torch.empty_like(q).cuda(), torch.empty(2, rows, device="cuda")
+    D.dit_attention_packed(q.cuda(), k.cuda(), v.cuda(), o, scale=1.0, cap=cap, lse=lse)
+    D.dit_check()
+    _check(o, lse, q, k, v, None, 1.0, cap, None)
+
+
+@pytest.mark.parametrize("rows", ROWS)
+def test_what_is_masked_never_matters_under_a_large_cap(rows):
+    g = np.random.default_rng(7)
+    d = 128
+    q, k, v = _bf16(g, rows, 2, d, gain=2.0), _bf16(g, KEYS, 2, d), _bf16(g, KEYS, 2, d)
+    vis = (np.arange(rows) + 300).astype(np.int32)
+    kb, vb = k.clone(), v.clone()
+    kb[302:], vb[301:] = float("nan"), float("inf")  # rows 0 and 1 see neither; their neighbours in the tile do
+    o = torch.empty_like(q).cuda()
+    D.dit_attention_packed(q.cuda(), kb.cuda(), vb.cuda(), o, visible=dev(vis), cap=1e6)
+    D.dit_check()
+    _check(o[:2], None, q[:2], k, v, vis[:2], d ** -0.5, 1e6, None)
+    assert not torch.isfinite(o[2:].float()).any()
