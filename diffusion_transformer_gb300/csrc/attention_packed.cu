@@ -235,11 +235,13 @@ __device__ Segment find_tile(const dit_packed_attention& a, int rows, int x) {
   return Segment{0, 0, 0, 0, -1};
 }
 
-// The weighted sum of V over the keys [j0, j1) that a row does see, on the plain cores: only for rows that the matrix
-// product left not finite beside keys they do not see (0 x NaN). A warp per row; lane l ends with values l D / 32 and on.
+// f times the weighted sum of V over the keys [j0, j1) that a row does see, on the plain cores: only for rows that the matrix
+// product left not finite beside keys they do not see (0 x NaN), or (`own`) under a fixed maximum, where weights above 1 may
+// have taken the product past fp32: those are weighed against the row's own maximum, f (1 / sum) taken along.
+// A warp per row; lane l ends with values l D / 32 and on.
 template <int D, int KIND>
 __device__ __noinline__ void resum_row(const PackedParams& p, int q_at, int k0, int j0, int j1, int head, int kvh, int place,
-                                       float m, float (&acc)[D / 32]) {
+                                       float m, float f, bool own, float (&acc)[D / 32]) {
   constexpr int V = D / 32;
   const dit_packed_attention& a = p.a;
   const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) + q_at * a.q_row + head * a.q_head + lane_id() * V;
@@ -251,7 +253,7 @@ __device__ __noinline__ void resum_row(const PackedParams& p, int q_at, int k0, 
     qv[i] = __bfloat162float(q[i]);
     acc[i] = 0.f;
   }
-  for (int j = j0; j < j1; ++j) {
+  auto score = [&](int j) {
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) s = fmaf(qv[i], __bfloat162float(k[(k0 + (long long)j) * a.k_row + i]), s);
@@ -263,9 +265,21 @@ __device__ __noinline__ void resum_row(const PackedParams& p, int q_at, int k0, 
       else if (p.cap_out > 0.f) x = capped(s, p.cap_in, p.cap_out);
       if (a.slope) x = fmaf(-1.4426950408889634f * __ldg(a.slope + head), fabsf(float(place - j)), x);
     }
-    const float w = ex2_approx(x - m);
+    return x;
+  };
+  if (own) {
+    float top = -INFINITY;
+    for (int j = j0; j < j1; ++j) top = fmaxf(top, score(j));
+    f *= ex2_approx(top - m);
+    m = top;
+  }
+  for (int j = j0; j < j1; ++j) {
+    const float w = ex2_approx(score(j) - m) * f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = fmaf(w, __bfloat162float(v[(k0 + (long long)j) * a.v_row + i]), acc[i]);
+    for (int i = 0; i < V; ++i) {
+      const float y = __bfloat162float(v[(k0 + (long long)j) * a.v_row + i]);
+      acc[i] = isinf(y) ? acc[i] + y : fmaf(w, y, acc[i]);  // (whose weight may have underflowed, and is above 0 all the same)
+    }
   }
 }
 
@@ -470,14 +484,17 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
     if constexpr (GEN)
       if (a.slope && valid) slope2 = 1.4426950408889634f * __ldg(a.slope + head);
     // Capped scores lie within the cap C (log2 units) of 0, or with a bias of what the nearest key that the row sees loses: up to
-    // kFixedLog2 the weights are taken against a fixed maximum, C or where that is less 110 - C: they lie within 2^50, and at the
-    // row's best key above 2^-110. Neither the row's own maximum nor the exchange of it is needed (9 sequences, capped: 253
-    // us with, 232 without). The nearest key lies behind the row where the row's place is past what it sees, and ahead of it
+    // kFixedLog2 the weights are taken against a fixed maximum, C or where that is less 80 - C: they lie within 2^80, and at the
+    // row's best key above 2^-80, so that neither keys 2^46 below it nor values of V down to 2^-46 are lost to fp32's least.
+    // Values of V so large that a weight takes them past its largest leave the row not finite, and resum_row mends it. (Parts of a
+    // split range go without: both halves of a row would have to agree on its maximum again.) Neither the row's own maximum nor the
+    // exchange of it is needed (9 sequences, capped: 253 us with, 232 without). The nearest key lies behind the row where the row's place is past what it sees, and ahead of it
     // where there are more rows than keys and the place is negative.
     // (A negative slope grows with the distance: no such bound.)
-    const bool fixed = KIND == kCapped && p.cap_out > 0.f && p.cap_out <= kFixedLog2 && __all_sync(0xffffffffu, slope2 >= 0.f);
+    const bool fixed = KIND == kCapped && p.cap_out > 0.f && p.cap_out <= kFixedLog2 && p.splits == 1 &&
+                       __all_sync(0xffffffffu, slope2 >= 0.f);
     float m = -INFINITY, l = 0.f;
-    if (fixed) m = fminf(p.cap_out, 110.f - p.cap_out) - slope2 * float(max(max(0, place - lim + 1), -place));
+    if (fixed) m = fminf(p.cap_out, 80.f - p.cap_out) - slope2 * float(max(max(0, place - lim + 1), -place));
     bool ok = true;
     for (int it = 0; it < n; ++it) {
       const int key0 = (ta + it) * 128;
@@ -618,8 +635,9 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
             for (int v = 0; v < 8; ++v) po[c * 8 + v] = make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
           }
         }
-        // rows with something that is not finite (in this half of O) beside keys they do not see
-        unsigned again = __ballot_sync(0xffffffffu, valid && bad != 0.f && lim < last);
+        // rows with something that is not finite (in this half of O) beside keys they do not see, or by their weights
+        // (where the sum of these is a number: else the scores are none)
+        unsigned again = __ballot_sync(0xffffffffu, valid && bad != 0.f && (lim < last || (fixed && l == l)));
         while (again) {
           const int src = __ffs(again) - 1;
           again &= again - 1;
@@ -627,13 +645,14 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
           const int end = __shfl_sync(0xffffffffu, min(lim, covered), src);
           const float sm = __shfl_sync(0xffffffffu, m == -INFINITY ? 0.f : m, src), sinv = __shfl_sync(0xffffffffu, inv, src);
           float acc[D / 32];
-          resum_row<D, KIND>(p, seg.q0 + si, seg.k0, ta * 128, end, sh, kvh, __shfl_sync(0xffffffffu, place, src), sm, acc);
+          resum_row<D, KIND>(p, seg.q0 + si, seg.k0, ta * 128, end, sh, kvh, __shfl_sync(0xffffffffu, place, src), sm, sinv, fixed,
+                             acc);
           if ((lane >> 4) != half) continue;  // each warp its half of the row
           if (whole) {
             const int srow = quad * 32 + src, at2 = lane * (D / 32) * 2;  // byte of the row
             uint32_t* dst = reinterpret_cast<uint32_t*>(stage + srow * (D * 2) + (((at2 >> 4) ^ (srow & 7)) << 4) + (at2 & 15));
 #pragma unroll
-            for (int v = 0; v < D / 64; ++v) dst[v] = pack_bf16x2(acc[2 * v] * sinv, acc[2 * v + 1] * sinv);
+            for (int v = 0; v < D / 64; ++v) dst[v] = pack_bf16x2(acc[2 * v], acc[2 * v + 1]);
           } else {
             float* dst = p.part_o + (((long long)blockIdx.z * a.q_rows + seg.q0 + si) * a.heads + sh) * D + lane * (D / 32);
 #pragma unroll
@@ -980,11 +999,12 @@ __global__ void __launch_bounds__(kRowThreads, 2)
         const int end = __shfl_sync(0xffffffffu, min(lim, covered), src);
         const float sm = __shfl_sync(0xffffffffu, m == -INFINITY ? 0.f : m, src), sinv = __shfl_sync(0xffffffffu, inv, src);
         float acc[D / 32];
-        resum_row<D, KIND>(p, seg.q0 + si, seg.k0, ta * kRowKeys, end, sh, kvh, __shfl_sync(0xffffffffu, place, src), sm, acc);
+        resum_row<D, KIND>(p, seg.q0 + si, seg.k0, ta * kRowKeys, end, sh, kvh, __shfl_sync(0xffffffffu, place, src), sm, sinv, false,
+                           acc);
         if (whole) {
           uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + (seg.q0 + si) * a.o_row + sh * a.o_head + lane * (D / 32));
 #pragma unroll
-          for (int v = 0; v < D / 64; ++v) dst[v] = pack_bf16x2(acc[2 * v] * sinv, acc[2 * v + 1] * sinv);
+          for (int v = 0; v < D / 64; ++v) dst[v] = pack_bf16x2(acc[2 * v], acc[2 * v + 1]);
         } else {
           float* dst = p.part_o + (((long long)blockIdx.z * a.q_rows + seg.q0 + si) * a.heads + sh) * D + lane * (D / 32);
 #pragma unroll

@@ -98,3 +98,45 @@ def test_what_is_masked_never_matters_under_a_large_cap(rows):
     D.dit_check()
     _check(o[:2], None, q[:2], k, v, vis[:2], d ** -0.5, 1e6, None)
     assert not torch.isfinite(o[2:].float()).any()
+
+
+@pytest.mark.parametrize("power", [100, 40, -40])
+@pytest.mark.parametrize("sign", [-1.0, 1.0])
+@pytest.mark.parametrize("rows,keys", [(200, 1100), (300, 6000), (3, 700)])
+def test_values_far_from_one_under_a_cap(power, sign, rows, keys):
+    # every score near its cap, above or below: weights taken against something else than the row's maximum leave V its range
+    g = np.random.default_rng(rows)
+    d, H = 64, 2
+    q = (sign * 40.0 * (np.abs(g.standard_normal((rows, H, d))) + 0.5)).astype(np.float32)
+    k = (np.abs(g.standard_normal((keys, H, d))) + 0.5).astype(np.float32)
+    q, k, v = torch.from_numpy(q).bfloat16(), torch.from_numpy(k).bfloat16(), _bf16(g, keys, H, d, gain=2.0 ** power)
+    vis = g.integers(1, keys + 1, rows).astype(np.int32)
+    for cap in (50.0, 55.0):
+        for slope in (None, np.array([0.5, 2.0 ** -8])):
+            for ws in (None, _ws(q, k)):
+                o, lse = torch.empty_like(q).cuda(), torch.empty(H, rows, device="cuda")
+                D.dit_attention_packed(q.cuda(), k.cuda(), v.cuda(), o, visible=dev(vis), cap=cap, lse=lse, ws=ws,
+                                       slope=None if slope is None else dev(slope.astype(np.float32)))
+                D.dit_check()
+                _check(o, lse, q, k, v, vis, d ** -0.5, cap, slope)
+
+
+def test_infinities_that_a_row_does_see_under_a_cap():
+    g = np.random.default_rng(3)
+    d, rows, H = 64, 200, 1
+    q, k, v = _bf16(g, rows, H, d, gain=40.0), _bf16(g, KEYS, H, d), _bf16(g, KEYS, H, d)
+    vis = np.where(np.arange(rows) % 2, 500, 400).astype(np.int32)
+    v[450, 0, 3], v[20, 0, 40], k[470] = float("inf"), float("-inf"), 0.0
+    o = torch.empty_like(q).cuda()
+    D.dit_attention_packed(q.cuda(), k.cuda(), v.cuda(), o, visible=dev(vis), cap=50.0)
+    D.dit_check()
+    got = o.float().cpu().numpy()[:, 0]
+    assert np.isposinf(got[1::2, 3]).all() and np.isneginf(got[:, 40]).all() and np.isfinite(got[::2, :40]).all()
+    assert np.isfinite(np.delete(got, [3, 40], 1)).all()
+    keep = [c for c in range(d) if c not in (3, 40)]
+    clean = v.clone()
+    clean[450, 0, 3], clean[20, 0, 40] = 0.0, 0.0
+    ref, _, mag = O.attention_packed(_np(q), _np(k), _np(clean), [0, rows], [0, KEYS], vis, 0.125, 50.0, None)
+    _, gate = _gate(_np(q), _np(k), KEYS, mag, 0.125, 50.0, None)
+    off = np.abs(got - ref[:, 0])[:, keep]
+    assert (off <= (gate + 2.0 ** -8 * (np.abs(ref) + gate))[:, 0][:, keep]).all()
