@@ -914,7 +914,11 @@ __global__ void __launch_bounds__(kRowThreads, 2)
         if (j > 0 && __any_sync(0xffffffffu, alpha < 1.0f)) {
           // O holds earlier tiles: the last P V must be done. (This S came after the P V before that one, so its phase is the
           // barrier's current one or has just completed, and the parity tells the two apart.)
-          if (!mbar_wait_warp(smem_u32(pv_done), (j - 1) & 1, p.err, kErrTimeoutSoftmax)) { ok = false; break; }
+          if (!mbar_wait_warp(smem_u32(pv_done), (j - 1) & 1, p.err, kErrTimeoutSoftmax)) {
+            tmem_st_wait();  // the weights' stores land before tensor memory is given back
+            ok = false;
+            break;
+          }
           tc_fence_after();
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
