@@ -47,8 +47,8 @@ constexpr int kPackedThreads = 64 + 32 * 16;  // loader, MMA issuer, sixteen sof
 
 // What a call's scores go through. kCapped also serves a bias without a cap; its error is a few 2^-24 of the cap, so caps of
 // more than kWideLog2 log2 units (where that is 4e-5, what the sums of the products may be off by) go by kWide, whose
-// error is relative to the score. (9 sequences of 811 to 1943 rows, 16 heads of 64 over 4: 255 us under a cap of 177, 259 under
-// 178 and up; two of 2489 and 2829 rows, 24 heads of 128: 286 and 319; with a score past a quarter of its cap in every
+// error is relative to the score. (9 sequences of 811 to 1943 rows, 16 heads of 64 over 4: 257 us under a cap of 177, 268 under
+// 178 and up; two of 2489 and 2829 rows, 24 heads of 128: 288 and 323; with a score past a quarter of its cap in every
 // warp 436 and 464.)
 enum Scores : int { kPlain = 0, kCapped = 1, kWide = 2 };
 constexpr float kWideLog2 = 256.f, kFixedLog2 = 80.f;
@@ -283,6 +283,23 @@ __device__ __noinline__ void resum_row(const PackedParams& p, int q_at, int k0, 
   }
 }
 
+// The rest of the key tiles for a warp whose wait gave up at tile `it`, while the other of its row pair may have seen its own
+// end: it passes the barriers of the pair as that one does. Both know the maxima of the tiles before and so the same m, and
+// both read the same two places here: `own`, which stays as it was, and `theirs`, which the other leaves alone once it has met
+// this one, because the scores of tile it + 1 wait for this warp's weights. So both take the same turn at every rescale,
+// until the other gives up as well, at the next tile at the latest. (Costs the warps that go on nothing but registers: 9
+// sequences of 16 heads of 64, plain, 132.9 us without, 136.5 with; two of 24 heads of 128 158.4 and 158.3. Joining the two
+// verdicts at every tile's barrier: 134.9 and 163.2.)
+__device__ __noinline__ void attend_meetings(const float* own, const float* theirs, int pair, int it, int n, float m) {
+  for (; it < n; ++it) {
+    asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+    const float mx = fmaxf(*reinterpret_cast<const volatile float*>(own), *reinterpret_cast<const volatile float*>(theirs));
+    const bool up = mx > m + kRescaleStep;
+    if (up) m = mx;
+    if (__any_sync(0xffffffffu, up) && it > 0) asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+  }
+}
+
 template <int D, int KIND>
 __global__ void __launch_bounds__(kPackedThreads, 1)
     packed_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -496,7 +513,8 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
     float m = -INFINITY, l = 0.f;
     if (fixed) m = fminf(p.cap_out, 80.f - p.cap_out) - slope2 * float(max(max(0, place - lim + 1), -place));
     bool ok = true;
-    for (int it = 0; it < n; ++it) {
+    int it = 0;
+    for (; it < n; ++it) {
       const int key0 = (ta + it) * 128;
       // rows of V that no row of the CTA sees, zeroed by the first group that uses the tile
       const int vz = lmax - key0;
@@ -591,8 +609,10 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
     }
 
     // ---- the end of the key range
+    if (!ok && live && !fixed)
+      attend_meetings(s_max + (t * 2 + half) * 128 + row, s_max + (t * 2 + (half ^ 1)) * 128 + row, pair, it, n, m);
     if (n > 0 && ok) ok = mbar_wait_warp(smem_u32(&o_done[t]), 0, p.err, kErrTimeoutSoftmax);
-    // (a warp that gave up still meets the other: what follows has the same barriers whatever happened)
+    // (what follows has the same barriers whatever happened, as the tiles had: attend_meetings)
     uint8_t* stage = sQ + t * Cfg::kTile;  // Q has been read; [row][D] bf16, chunks swizzled by the row
     if (n > 0) {
       // the row's sum over both halves, through the places of the maxima (the staged rows of other warps lie over everything

@@ -10,7 +10,13 @@ from tests.gpu_util import dev
 
 pytestmark = pytest.mark.gpu
 
-JOBS = {  # few rows over parts of a key range, short segments
+JOBS = {  # whole tiles under a running and a fixed maximum, a part of them without keys, parts of a key range, few rows
+    "plain": dict(rows=1500, keys=1500, heads=8, kv=8, d=128),
+    "groups": dict(rows=700, keys=3000, heads=12, kv=3, d=64),
+    "biased": dict(rows=1100, keys=1300, heads=6, kv=6, d=128, bias=True, causal=True),
+    "capped": dict(rows=1100, keys=1300, heads=6, kv=2, d=64, cap=50.0, causal=True),
+    "wide": dict(rows=600, keys=1300, heads=4, kv=4, d=128, cap=1000.0),
+    "parts": dict(rows=300, keys=6000, heads=1, kv=1, d=64, ws=True),
     "rows": dict(rows=9, keys=9000, heads=16, kv=4, d=128, ws=True, bias=True),
     "short": dict(rows=300, keys=300, heads=8, kv=8, d=64, causal=True),
 }
