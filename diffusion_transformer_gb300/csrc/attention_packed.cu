@@ -1218,9 +1218,6 @@ size_t dit_attention_packed_workspace_bytes(int q_rows, int k_rows, int segments
 
 }  // extern "C"
 
-#ifndef MODE
-#define MODE 1
-#endif
 namespace dit {
 
 int packed_attention_launch(const dit_packed_attention& a, void* ws, size_t ws_bytes, int* err, cudaStream_t st) {
