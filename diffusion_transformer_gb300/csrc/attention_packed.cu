@@ -1110,7 +1110,7 @@ PackedPlan packed_plan(int q_rows, int k_rows, int segments, int heads, int kv_h
   r.rpt = 128 / r.G;
   const bool tall = (long long)q_rows > (long long)segments * r.rpt;
   r.few = !tall || k_rows <= 1024LL * segments;
-  if (r.few) r.rpt = std::min(r.rpt, std::max(32 / r.G, std::max(1, (q_rows + segments - 1) / segments)));
+  if (r.few) r.rpt = std::min(r.rpt, std::max(32 / r.G, std::max(1, int(((long long)q_rows + segments - 1) / segments))));
   const long long rows = (r.few ? 1LL : 2LL) * r.rpt;
   r.tiles = std::min<long long>((q_rows + segments * (rows - 1)) / rows, q_rows);
   const uint32_t q_bytes = uint32_t((r.G * r.rpt + 7) / 8 * 8) * d * 2;
