@@ -64,7 +64,7 @@ def draw(rng):
     op = rng.choice(["heads", "attend", "attend", "linear"])
     if op == "heads":
         d = rng.choice([32, 64, 80, 96, 128, 256])
-        widths = rng.choice([str(d), str(d // 4 * 2), str(3 * d // 8 * 2), "%d,%d,%d" % (d // 8, d // 16 * 7, d // 16 * 7)])
+        widths = rng.choice([str(d), str(d // 4 * 2), str(3 * d // 8 * 2), "%d,%d,%d" % (d // 8, d // 32 * 14, d // 32 * 14)])  # even ones
         while True:
             B, T, Hq = rng.choice([1, 1, 2, 3, 5]), _log(rng, 1, 20000), rng.choice([1, 3, 6, 8, 12, 24, 32])
             Hk = rng.choice([h for h in (1, 2, 3, 4, 8, 24) if h <= Hq])
