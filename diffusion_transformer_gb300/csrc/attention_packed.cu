@@ -505,13 +505,15 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
     // row's best key above 2^-80, so that neither keys 2^46 below it nor values of V down to 2^-46 are lost to fp32's least.
     // Values of V so large that a weight takes them past its largest leave the row not finite, and resum_row mends it. (Parts of a
     // split range go without: both halves of a row would have to agree on its maximum again.) Neither the row's own maximum nor the
-    // exchange of it is needed (9 sequences, capped: 253 us with, 232 without). The nearest key lies behind the row where the row's place is past what it sees, and ahead of it
-    // where there are more rows than keys and the place is negative.
-    // (A negative slope grows with the distance: no such bound.)
+    // exchange of it is needed (9 sequences, capped: 253 us with, 232 without). The nearest key lies behind the row where the
+    // row's place is past what it sees, and ahead of it where there are more rows than keys and the place is negative.
+    // (A negative slope grows with the distance: no such bound. And past 2^20 that key's bias, which scores and maximum round
+    // apart, would leave their difference too few places.)
+    const float near = slope2 * float(max(max(0, place - lim + 1), -place));
     const bool fixed = KIND == kCapped && p.cap_out > 0.f && p.cap_out <= kFixedLog2 && p.splits == 1 &&
-                       __all_sync(0xffffffffu, slope2 >= 0.f);
+                       __all_sync(0xffffffffu, slope2 >= 0.f && near <= 0x1p20f);
     float m = -INFINITY, l = 0.f;
-    if (fixed) m = fminf(p.cap_out, 80.f - p.cap_out) - slope2 * float(max(max(0, place - lim + 1), -place));
+    if (fixed) m = fminf(p.cap_out, 80.f - p.cap_out) - near;
     bool ok = true;
     int it = 0;
     for (; it < n; ++it) {

@@ -140,3 +140,21 @@ def test_infinities_that_a_row_does_see_under_a_cap():
     _, gate = _gate(_np(q), _np(k), KEYS, mag, 0.125, 50.0, None)
     off = np.abs(got - ref[:, 0])[:, keep]
     assert (off <= (gate + 2.0 ** -8 * (np.abs(ref) + gate))[:, 0][:, keep]).all()
+
+
+@pytest.mark.parametrize("slope", [1e4, 1e7, 1e12])
+@pytest.mark.parametrize("cap", [0.0, 20.0, 1000.0])
+@pytest.mark.parametrize("rows", ROWS)
+def test_steep_biases_leave_the_nearest_key(slope, cap, rows):
+    # rows past what they see: their nearest key is a hundred places away and outweighs all others
+    g = np.random.default_rng(5)
+    d = 64
+    q, k, v = _bf16(g, rows, 2, d), _bf16(g, KEYS, 2, d), _bf16(g, KEYS, 2, d)
+    vis = (np.arange(rows) + KEYS - rows - 100 + g.integers(0, 90, rows)).astype(np.int32)
+    o, lse = torch.empty_like(q).cuda(), torch.empty(2, rows, device="cuda")
+    D.dit_attention_packed(q.cuda(), k.cuda(), v.cuda(), o, visible=dev(vis), cap=cap, lse=lse,
+                           slope=torch.full((2,), slope, device="cuda"))
+    D.dit_check()
+    assert torch.equal(o.cpu(), v[torch.from_numpy(vis).long() - 1])
+    far = (np.arange(rows) + KEYS - rows - vis + 1)[None] * slope
+    assert (np.abs(_np(lse) + far) <= 100 + 2.0 ** -20 * far).all()
