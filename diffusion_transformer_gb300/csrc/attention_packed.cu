@@ -20,8 +20,8 @@
 // (blockIdx.z) and a second kernel joins the parts in order.
 // Masked places: weights of masked keys are zero, the rows of V behind the last key that any row of the CTA sees are
 // zeroed in shared memory (they may be the next segment's, or anything), and a row whose result is not finite while
-// its tile held keys that it does not see is summed again over its own keys (resum_row): NaN or infinity in a masked
-// place never reaches it.
+// its tile held keys that it does not see is summed again over its own keys, unless what it sees makes it so (mend_rows): NaN or
+// infinity in a masked place never reaches it.
 //
 // Tensor memory (512 columns): [0, 128) S0, P0 over it: 32 columns at 0 for keys
 // 0-63, 32 at 64 for keys 64-127   [128, 256) S1 / P1   [256, 256 + d) O0   [256 + d, 256 + 2 d) O1
@@ -235,12 +235,60 @@ __device__ Segment find_tile(const dit_packed_attention& a, int rows, int x) {
   return Segment{0, 0, 0, 0, -1};
 }
 
+// Whether resum_row would find anything else than the product did, which left the columns `nan` and `inf` (a bit for each of a
+// lane's D / 32) of a row that sees the keys [j0, j1): a column is as it should be where values of V that the row sees make it
+// so. (4224 causal rows of 24 heads with an infinite V in the sixth key: 172 ms with every row summed again, 0.5 with this look
+// at V first, 0.13 where all is finite; 9 capped sequences 251, 0.7 and 0.24.) A warp per row.
+template <int D>
+__device__ __forceinline__ bool resum_helps(const PackedParams& p, int k0, int j0, int j1, int kvh, unsigned nan, unsigned inf) {
+  constexpr int V = D / 32;
+  const uint16_t* v = p.a.v + kvh * p.a.v_head + lane_id() * V;
+  unsigned none = 0, up = 0, down = 0;  // of the values seen so far, by column: NaN, an infinity of either sign
+  auto wrong = [&] { return (inf & ~(none | up | down)) | (nan & ~(none | (up & down))); };
+  for (int base = j0; base < j1; base += 32) {
+    if (!__any_sync(0xffffffffu, wrong())) return false;
+#pragma unroll 4
+    for (int j = base; j < min(base + 32, j1); ++j) {
+      uint32_t u[V / 2];
+      const uint16_t* at = v + (k0 + (long long)j) * p.a.v_row;
+      if constexpr (V == 4) {
+        const uint2 x = *reinterpret_cast<const uint2*>(at);
+        u[0] = x.x; u[1] = x.y;
+      } else {
+        u[0] = *reinterpret_cast<const uint32_t*>(at);
+      }
+#pragma unroll
+      for (int c = 0; c < V; ++c) {
+        const unsigned h = (u[c >> 1] >> ((c & 1) * 16)) & 0xffffu;
+        none |= unsigned((h & 0x7fffu) > 0x7f80u) << c;
+        up |= unsigned(h == 0x7f80u) << c;
+        down |= unsigned(h == 0xff80u) << c;
+      }
+    }
+  }
+  return __any_sync(0xffffffffu, wrong());
+}
+
+// Which of 32 columns of this lane's row of O are NaN, and which infinite
+__device__ __forceinline__ uint2 odd_columns(uint32_t taddr) {
+  uint32_t raw[32];
+  tmem_ld32(taddr, raw);
+  tmem_ld_wait();
+  uint2 b = make_uint2(0, 0);
+#pragma unroll
+  for (int v = 0; v < 32; ++v) {
+    b.x |= unsigned((raw[v] & 0x7fffffffu) > 0x7f800000u) << v;
+    b.y |= unsigned((raw[v] & 0x7fffffffu) == 0x7f800000u) << v;
+  }
+  return b;
+}
+
 // f times the weighted sum of V over the keys [j0, j1) that a row does see, on the plain cores: only for rows that the matrix
 // product left not finite beside keys they do not see (0 x NaN), or (`own`) under a fixed maximum, where weights above 1 may
 // have taken the product past fp32: those are weighed against the row's own maximum, f (1 / sum) taken along.
 // A warp per row; lane l ends with values l D / 32 and on.
 template <int D, int KIND>
-__device__ __noinline__ void resum_row(const PackedParams& p, int q_at, int k0, int j0, int j1, int head, int kvh, int place,
+__device__ __forceinline__ void resum_row(const PackedParams& p, int q_at, int k0, int j0, int j1, int head, int kvh, int place,
                                        float m, float f, bool own, float (&acc)[D / 32]) {
   constexpr int V = D / 32;
   const dit_packed_attention& a = p.a;
@@ -283,17 +331,63 @@ __device__ __noinline__ void resum_row(const PackedParams& p, int q_at, int k0, 
   }
 }
 
+// The rows `rows` of a warp whose product, in the `cols` columns from `first` on (at tO in tensor memory), is not finite: summed
+// again where that helps, and put where a row's result goes: the staged tile (null: the output itself), or the part's sums.
+// i, j1 (the end of the keys that it sees), m and f are those of the lane's row. (A function of its own, with few arguments: the
+// key loop keeps its registers. 9 capped sequences 229 us with the loop in place, 219 so.)
+template <int D, int KIND>
+__device__ __noinline__ void mend_rows(const PackedParams& p, unsigned rows, const Segment& seg, int i, int j0, int j1, int kvh, float m, float f, bool own, uint32_t tO, int first, int cols, uint8_t* stage) {
+  constexpr int V = D / 32;
+  const dit_packed_attention& a = p.a;
+  const int lane = lane_id(), col = lane * V;
+  const int quad_row = int(threadIdx.x >> 5 & 3) * 32;  // of the tile: the warp's first
+  const int q = seg.q0 + i, k0 = seg.k0, place = i + seg.nk - seg.nq, head = kvh * p.G + (quad_row + lane) % p.G;
+  const bool mine = col >= first && col < first + cols;
+  __syncwarp();  // the rows' own stores come first
+  for (; rows; rows &= rows - 1) {
+    const int src = __ffs(rows) - 1;
+    auto of_row = [&](auto x) { return __shfl_sync(0xffffffffu, x, src); };
+    unsigned nan = 0, inf = 0;  // of this lane's columns
+    for (int c = 0; c < cols; c += 32) {
+      const uint2 b = odd_columns(tO + uint32_t(c));
+      const unsigned bn = of_row(b.x), bi = of_row(b.y);
+      if (mine && (col - first) / 32 == c / 32) {
+        nan = bn >> ((col - first) & 31) & ((1u << V) - 1);
+        inf = bi >> ((col - first) & 31) & ((1u << V) - 1);
+      }
+    }
+    const int sq = of_row(q), sh = of_row(head), end = of_row(j1);
+    if (!resum_helps<D>(p, k0, j0, end, kvh, nan, inf)) continue;
+    float acc[V];
+    resum_row<D, KIND>(p, sq, k0, j0, end, sh, kvh, of_row(place), of_row(m == -INFINITY ? 0.f : m), of_row(f), own, acc);
+    if (!mine) continue;
+    if (p.splits > 1) {
+      float* dst = p.part_o + (((long long)blockIdx.z * a.q_rows + sq) * a.heads + sh) * D + col;
+#pragma unroll
+      for (int v = 0; v < V; ++v) dst[v] = acc[v];
+    } else {
+      const int row = quad_row + src, at = col * 2;  // byte of the row
+      uint32_t* dst = reinterpret_cast<uint32_t*>(stage ? stage + row * (D * 2) + (((at >> 4) ^ (row & 7)) << 4) + (at & 15)
+                                                        : reinterpret_cast<uint8_t*>(a.o + sq * a.o_row + sh * a.o_head + col));
+#pragma unroll
+      for (int v = 0; v < V / 2; ++v) dst[v] = pack_bf16x2(acc[2 * v], acc[2 * v + 1]);
+    }
+  }
+}
+
 // The rest of the key tiles for a warp whose wait gave up at tile `it`, while the other of its row pair may have seen its own
 // end: it passes the barriers of the pair as that one does. Both know the maxima of the tiles before and so the same m, and
 // both read the same two places here: `own`, which stays as it was, and `theirs`, which the other leaves alone once it has met
 // this one, because the scores of tile it + 1 wait for this warp's weights. So both take the same turn at every rescale,
-// until the other gives up as well, at the next tile at the latest. (Costs the warps that go on nothing but registers: 9
-// sequences of 16 heads of 64, plain, 132.9 us without, 136.5 with; two of 24 heads of 128 158.4 and 158.3. Joining the two
-// verdicts at every tile's barrier: 134.9 and 163.2.)
-__device__ __noinline__ void attend_meetings(const float* own, const float* theirs, int pair, int it, int n, float m) {
+// until the other gives up as well, at the next tile at the latest. (Joining the two verdicts at every tile's barrier instead: 163
+// us for two sequences of 24 heads of 128 that take 158 without, and with this.)
+__device__ __noinline__ void attend_meetings(const volatile float* s_max, int it, int n, float m) {
+  const int warp = int(threadIdx.x >> 5) - 2, pair = 1 + (warp >> 3) * 4 + ((warp + 2) & 3);  // as in packed_kernel
+  const volatile float* own = s_max + (warp >> 2) * 128 + ((warp + 2) & 3) * 32 + lane_id();
+  const volatile float* theirs = s_max + ((warp >> 2) ^ 1) * 128 + ((warp + 2) & 3) * 32 + lane_id();
   for (; it < n; ++it) {
     asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
-    const float mx = fmaxf(*reinterpret_cast<const volatile float*>(own), *reinterpret_cast<const volatile float*>(theirs));
+    const float mx = fmaxf(*own, *theirs);
     const bool up = mx > m + kRescaleStep;
     if (up) m = mx;
     if (__any_sync(0xffffffffu, up) && it > 0) asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
@@ -612,7 +706,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
 
     // ---- the end of the key range
     if (!ok && live && !fixed)
-      attend_meetings(s_max + (t * 2 + half) * 128 + row, s_max + (t * 2 + (half ^ 1)) * 128 + row, pair, it, n, m);
+      attend_meetings(s_max, it, n, m);
     if (n > 0 && ok) ok = mbar_wait_warp(smem_u32(&o_done[t]), 0, p.err, kErrTimeoutSoftmax);
     // (what follows has the same barriers whatever happened, as the tiles had: attend_meetings)
     uint8_t* stage = sQ + t * Cfg::kTile;  // Q has been read; [row][D] bf16, chunks swizzled by the row
@@ -657,30 +751,12 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
             for (int v = 0; v < 8; ++v) po[c * 8 + v] = make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
           }
         }
-        // rows with something that is not finite (in this half of O) beside keys they do not see, or by their weights
-        // (where the sum of these is a number: else the scores are none)
-        unsigned again = __ballot_sync(0xffffffffu, valid && bad != 0.f && (lim < last || (fixed && l == l)));
-        while (again) {
-          const int src = __ffs(again) - 1;
-          again &= again - 1;
-          const int si = __shfl_sync(0xffffffffu, i, src), sh = __shfl_sync(0xffffffffu, head, src);
-          const int end = __shfl_sync(0xffffffffu, min(lim, covered), src);
-          const float sm = __shfl_sync(0xffffffffu, m == -INFINITY ? 0.f : m, src), sinv = __shfl_sync(0xffffffffu, inv, src);
-          float acc[D / 32];
-          resum_row<D, KIND>(p, seg.q0 + si, seg.k0, ta * 128, end, sh, kvh, __shfl_sync(0xffffffffu, place, src), sm, sinv, fixed,
-                             acc);
-          if ((lane >> 4) != half) continue;  // each warp its half of the row
-          if (whole) {
-            const int srow = quad * 32 + src, at2 = lane * (D / 32) * 2;  // byte of the row
-            uint32_t* dst = reinterpret_cast<uint32_t*>(stage + srow * (D * 2) + (((at2 >> 4) ^ (srow & 7)) << 4) + (at2 & 15));
-#pragma unroll
-            for (int v = 0; v < D / 64; ++v) dst[v] = pack_bf16x2(acc[2 * v], acc[2 * v + 1]);
-          } else {
-            float* dst = p.part_o + (((long long)blockIdx.z * a.q_rows + seg.q0 + si) * a.heads + sh) * D + lane * (D / 32);
-#pragma unroll
-            for (int v = 0; v < D / 32; ++v) dst[v] = acc[v];
-          }
-        }
+        // rows with something that is not finite (in this half of O) beside keys they do not see, or by their weights; where
+        // the weights' sum is NaN already, it is for scores that the row sees
+        unsigned again = __ballot_sync(0xffffffffu, valid && bad != 0.f && l == l && (lim < last || fixed));
+        if (again)
+          mend_rows<D, KIND>(p, again, *s_seg, i, ta * 128, min(lim, covered), kvh, m, inv, fixed, tO,
+                             half * (D / 2), D / 2, stage);
       } else if (whole) {
 #pragma unroll
         for (int c = 0; c < D / 16; ++c)
@@ -1017,26 +1093,10 @@ __global__ void __launch_bounds__(kRowThreads, 2)
               l > 0.f || l != l ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
       }
       // rows with something that is not finite beside keys they do not see
-      unsigned again = __ballot_sync(0xffffffffu, valid && bad != 0.f && lim < last);
-      while (again) {
-        const int src = __ffs(again) - 1;
-        again &= again - 1;
-        const int si = __shfl_sync(0xffffffffu, i, src), sh = __shfl_sync(0xffffffffu, head, src);
-        const int end = __shfl_sync(0xffffffffu, min(lim, covered), src);
-        const float sm = __shfl_sync(0xffffffffu, m == -INFINITY ? 0.f : m, src), sinv = __shfl_sync(0xffffffffu, inv, src);
-        float acc[D / 32];
-        resum_row<D, KIND>(p, seg.q0 + si, seg.k0, ta * kRowKeys, end, sh, kvh, __shfl_sync(0xffffffffu, place, src), sm, sinv, false,
-                           acc);
-        if (whole) {
-          uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + (seg.q0 + si) * a.o_row + sh * a.o_head + lane * (D / 32));
-#pragma unroll
-          for (int v = 0; v < D / 64; ++v) dst[v] = pack_bf16x2(acc[2 * v], acc[2 * v + 1]);
-        } else {
-          float* dst = p.part_o + (((long long)blockIdx.z * a.q_rows + seg.q0 + si) * a.heads + sh) * D + lane * (D / 32);
-#pragma unroll
-          for (int v = 0; v < D / 32; ++v) dst[v] = acc[v];
-        }
-      }
+      unsigned again = __ballot_sync(0xffffffffu, valid && bad != 0.f && l == l && lim < last);
+      if (again)
+        mend_rows<D, KIND>(p, again, *s_seg, i, ta * kRowKeys, min(lim, covered), kvh, m, inv, false, tO, 0,
+                           D, nullptr);
     }
   }
 

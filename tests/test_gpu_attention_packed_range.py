@@ -158,3 +158,58 @@ def test_steep_biases_leave_the_nearest_key(slope, cap, rows):
     assert torch.equal(o.cpu(), v[torch.from_numpy(vis).long() - 1])
     far = (np.arange(rows) + KEYS - rows - vis + 1)[None] * slope
     assert (np.abs(_np(lse) + far) <= 100 + 2.0 ** -20 * far).all()
+
+
+@pytest.mark.parametrize("cap", [0.0, 50.0, 1000.0])
+@pytest.mark.parametrize("rows", ROWS)
+def test_columns_not_finite_on_either_side_of_the_mask(rows, cap):
+    # by column of V, key 200 seen by all rows and key 600 by none of the first half: what is seen decides alone
+    g = np.random.default_rng(11)
+    d, inf, nan = 64, float("inf"), float("nan")
+    q, k, v = _bf16(g, rows, 1, d), _bf16(g, KEYS, 1, d), _bf16(g, KEYS, 1, d)
+    half = rows // 2
+    vis = np.where(np.arange(rows) < half, 500, 900).astype(np.int32)
+    clean = v.clone()
+    for c, (seen, hidden) in enumerate([(0.5, nan), (0.5, inf), (nan, nan), (inf, nan), (-inf, inf), (inf, 0.5), (nan, 0.5), (inf, inf)]):
+        v[200, 0, c], v[600, 0, c] = seen, hidden
+    v[201, 0, 8], v[200, 0, 8], v[600, 0, 8] = inf, -inf, inf  # both infinities seen: NaN
+    o = torch.empty_like(q).cuda()
+    for ws in (None, _ws(q, k)):
+        D.dit_attention_packed(q.cuda(), k.cuda(), v.cuda(), o.fill_(9), visible=dev(vis), cap=cap, ws=ws)
+        D.dit_check()
+        got = o.float().cpu().numpy()[:half, 0]
+        assert np.isfinite(got[:, :2]).all() and np.isnan(got[:, [2, 6, 8]]).all()
+        assert np.isposinf(got[:, [3, 5, 7]]).all() and np.isneginf(got[:, 4]).all() and np.isfinite(got[:, 9:]).all()
+        clean[200, 0, :2] = 0.5
+        ref, _, mag = O.attention_packed(_np(q[:half]), _np(k), _np(clean), [0, half], [0, KEYS], vis[:half], 0.125, cap, None)
+        _, gate = _gate(_np(q[:half]), _np(k), KEYS, mag, 0.125, cap, None)
+        off = np.abs(got - ref[:, 0])
+        for c in [0, 1] + list(range(9, d)):
+            assert (off[:, c] <= (gate + 2.0 ** -8 * (np.abs(ref) + gate))[:, 0, c]).all(), c
+
+
+def test_rows_that_are_not_finite_cost_no_more_than_others_by_much():
+    # NaN scores, and infinities that rows do see, leave nothing to sum again
+    g = torch.Generator().manual_seed(2)
+    rn = lambda *s: torch.randn(*s, generator=g).bfloat16().cuda()  # noqa: E731
+    n, H, d = 4096, 8, 64
+    q, k, v = rn(n, H, d), rn(n, H, d), rn(n, H, d)
+    vis, o = torch.arange(1, n + 1, dtype=torch.int32, device="cuda"), torch.empty(n, H, d, dtype=torch.bfloat16, device="cuda")
+
+    def ms(cap):
+        run = lambda: D.dit_attention_packed(q, k, v, o, visible=vis, cap=cap)  # noqa: E731
+        run()
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        run(), run()
+        b.record()
+        torch.cuda.synchronize()
+        return a.elapsed_time(b) / 2
+
+    v[5, :, 7] = float("inf")
+    assert ms(0.0) < 20 and ms(50.0) < 20  # 60 to 100 ms with all rows summed again
+    assert torch.isposinf(o[6:, :, 7]).all() and torch.isfinite(o[:, :, 8:].float()).all()
+    q[:] = float("nan")
+    assert ms(0.0) < 20 and ms(50.0) < 20
+    assert torch.isnan(o.float()).all()
+    D.dit_check()
