@@ -14,7 +14,7 @@
 // by a scan over q_start: no lengths on the host, and a captured graph serves other lengths. packed_kernel takes two tiles
 // of a segment per CTA: warp 0 loads, warp 1 issues the MMAs, warps 2-9 and 10-17 turn the scores of the two tiles into
 // weights, so that one tile's exponentials overlap the other's MMAs; a row's 128 keys of a tile are two threads' work, who
-// exchange their maxima through shared memory (4224 rows of 24 heads of 128: 178 us with eight warps of whole rows, 163 so:
+// exchange their maxima through shared memory (4224 rows of 24 heads of 128: 178 us with eight warps of whole rows, 162 so:
 // 1350 TFLOP/s, the GPU at its power limit). packed_rows_kernel takes
 // segments of few rows or short ones, two CTAs to an SM. Where there are too few tiles for the SMs the key range is split over CTAs
 // (blockIdx.z) and a second kernel joins the parts in order.
@@ -47,9 +47,9 @@ constexpr int kPackedThreads = 64 + 32 * 16;  // loader, MMA issuer, sixteen sof
 
 // What a call's scores go through. kCapped also serves a bias without a cap; its error is a few 2^-24 of the cap, so caps of
 // more than kWideLog2 log2 units (where that is 4e-5, what the sums of the products may be off by) go by kWide, whose
-// error is relative to the score. (9 sequences of 811 to 1943 rows, 16 heads of 64 over 4: 257 us under a cap of 177, 268 under
-// 178 and up; two of 2489 and 2829 rows, 24 heads of 128: 288 and 323; with a score past a quarter of its cap in every
-// warp 436 and 464.)
+// error is relative to the score. (9 sequences of 811 to 1943 rows, 16 heads of 64 over 4: 246 us under a cap of 177, 257 under
+// 178 and up; two of 2489 and 2829 rows, 24 heads of 128: 284 and 322; with a score past a quarter of its cap in every
+// warp 431 and 506.)
 enum Scores : int { kPlain = 0, kCapped = 1, kWide = 2 };
 constexpr float kWideLog2 = 256.f, kFixedLog2 = 80.f;
 
@@ -114,8 +114,8 @@ __device__ __forceinline__ float capped_wide(float s, const PackedParams& p) {
 
 // Two capped scores at once, c tanh t = c - 2 c / (1 + e^2t): one reciprocal serves both (1 / a = b / ab). e^2t is held below
 // 2^60, where tanh is 1 to the last place, so that the product stays finite. A NaN takes both with it: masked places are
-// cleared before. (9 sequences, capped, 254 us; a quotient for each 266; tanh as a polynomial of degree 15 on the FMA pipe,
-// which two-value instructions take two cycles of, 285.)
+// cleared before. (9 capped sequences with a quotient for each: 5 % more; with tanh as a polynomial of degree 15 on the FMA pipe, which
+// two-value instructions take two cycles of, 12 % more.)
 __device__ __forceinline__ void capped2(float& a, float& b, float cap_in, float cap_out) {
   float x = a * cap_in, y = b * cap_in;
   asm("min.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(60.f));
@@ -334,7 +334,7 @@ __device__ __forceinline__ void resum_row(const PackedParams& p, int q_at, int k
 // The rows `rows` of a warp whose product, in the `cols` columns from `first` on (at tO in tensor memory), is not finite: summed
 // again where that helps, and put where a row's result goes: the staged tile (null: the output itself), or the part's sums.
 // i, j1 (the end of the keys that it sees), m and f are those of the lane's row. (A function of its own, with few arguments: the
-// key loop keeps its registers. 9 capped sequences 229 us with the loop in place, 219 so.)
+// key loop keeps its registers. 9 capped sequences 229 us with the loop in place, 220 so.)
 template <int D, int KIND>
 __device__ __noinline__ void mend_rows(const PackedParams& p, unsigned rows, const Segment& seg, int i, int j0, int j1, int kvh, float m, float f, bool own, uint32_t tO, int first, int cols, uint8_t* stage) {
   constexpr int V = D / 32;
@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
     // row's best key above 2^-80, so that neither keys 2^46 below it nor values of V down to 2^-46 are lost to fp32's least.
     // Values of V so large that a weight takes them past its largest leave the row not finite, and resum_row mends it. (Parts of a
     // split range go without: both halves of a row would have to agree on its maximum again.) Neither the row's own maximum nor the
-    // exchange of it is needed (9 sequences, capped: 253 us with, 232 without). The nearest key lies behind the row where the
+    // exchange of it is needed (9 sequences, capped: 246 us with, 220 without). The nearest key lies behind the row where the
     // row's place is past what it sees, and ahead of it where there are more rows than keys and the place is negative.
     // (A negative slope grows with the distance: no such bound. And past 2^20 that key's bias, which scores and maximum round
     // apart, would leave their difference too few places.)
@@ -727,6 +727,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
       const long long at = ((long long)blockIdx.z * a.q_rows + seg.q0 + i) * a.heads + head;  // of the partial sums
       float4* po = reinterpret_cast<float4*>(p.part_o + at * D + half * (D / 2));
       float bad = 0.f;
+      unsigned again = 0;
       if (live && n > 0) {
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
@@ -753,10 +754,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
         }
         // rows with something that is not finite (in this half of O) beside keys they do not see, or by their weights; where
         // the weights' sum is NaN already, it is for scores that the row sees
-        unsigned again = __ballot_sync(0xffffffffu, valid && bad != 0.f && l == l && (lim < last || fixed));
-        if (again)
-          mend_rows<D, KIND>(p, again, *s_seg, i, ta * 128, min(lim, covered), kvh, m, inv, fixed, tO,
-                             half * (D / 2), D / 2, stage);
+        again = __ballot_sync(0xffffffffu, valid && bad != 0.f && l == l && (lim < last || fixed));
       } else if (whole) {
 #pragma unroll
         for (int c = 0; c < D / 16; ++c)
@@ -768,6 +766,9 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
           a.lse[(long long)head * a.q_rows + seg.q0 + i] =
               l > 0.f || l != l ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
       }
+      // (here, behind the stores of lse: right behind the vote, two sequences of 24 heads of 128 take 161 us, so 157)
+      if (again)
+        mend_rows<D, KIND>(p, again, *s_seg, i, ta * 128, min(lim, covered), kvh, m, inv, fixed, tO, half * (D / 2), D / 2, stage);
     }
     if (p.splits == 1) {
       // whole rows out of the staged tile: D / 8 lanes of 16 bytes to a row; each warp every other row of the pair's 32
