@@ -697,7 +697,8 @@ DIT_API int dit_attention_qknorm(const dit_dims* dims, int R, const uint16_t* q,
  * of one product. bf16 in and out; scores, softmax and sums in fp32, the weights rounded to bf16 for the product with V.
  * head_dim 64 or 128; heads a multiple of kv_heads, at most 128 times it. scale > 0, cap >= 0, finite. o must not overlap
  * the inputs. ws: optional scratch of dit_attention_packed_workspace_bytes (16-byte aligned) for splitting long key ranges
- * over the SMs where there are few rows (0 bytes where that does not pay); with it a result differs by the order of fp32 additions only.
+ * over the SMs where there are few rows (0 bytes where that does not pay); with it a result differs by the order of fp32 additions and by
+ * the weights' roundings, which go by each part's own maximum. A cap far above the scores is as good as none.
  * q_rows = 0 or segments = 0: nothing to do. */
 typedef struct {
   const uint16_t *q, *k, *v;
