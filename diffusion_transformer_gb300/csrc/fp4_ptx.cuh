@@ -34,25 +34,6 @@ __device__ __forceinline__ float4 ld_shared_cluster_v4(uint32_t addr) {
   return v;
 }
 
-// Wait for what is in flight (copies into this CTA, MMAs on its operands) whatever the error word says, for at most
-// kWaitLimitNs: a CTA that gives up must not leave while they still land. (The timer is slow to read, so only a wait
-// that lasts looks at it.)
-__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity, int* err) {
-  if (mbar_try_wait(bar, parity)) return;
-  const uint64_t t0 = globaltimer_ns();
-  for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it)
-    if ((it & 31u) == 0 && globaltimer_ns() - t0 > kWaitLimitNs) {
-      atomicCAS(err, 0, kErrTimeoutDrain);
-      return;
-    }
-}
-// For copies that no barrier of this CTA will ever count (their pair gave up in between): a millisecond is a
-// thousand times what one takes.
-__device__ __forceinline__ void outlast_copies() {
-  const uint64_t t0 = globaltimer_ns();
-  while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
-}
-
 // 32 TMEM lanes x 16 consecutive columns (see tmem_ld32).
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(

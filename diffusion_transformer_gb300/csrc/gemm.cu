@@ -966,12 +966,13 @@ __global__ void __launch_bounds__(GemmCfg<BN, B8, PAIR, EPI>::kThreads, 1)
           if (++stage == S) { stage = 0; phase ^= 1; }
         }
       }
-      // every issued copy must have landed before the CTA exits (PAIR bf16: the first CTA's barriers
-      // count the second's copies too, and the second waits for the first before it exits)
-      if (kLocalFull || rank == 0)
+      // every issued copy must have landed before the CTA exits, whatever the error word says (PAIR bf16: the first CTA's
+      // barriers count the second's copies too, and the second waits for the first before it exits; they do not count those
+      // that one of them issued after the other gave up)
+      if (!kLocalFull && aborted(p.err)) outlast_copies();
+      else if (kLocalFull || rank == 0)
         for (int s = 0; s < S; ++s)
-          if (issued_mask & (1u << s))
-            mbar_wait(smem_u32(&full[s]), (last_parity >> s) & 1u, p.err, kErrTimeoutDrain);
+          if (issued_mask & (1u << s)) mbar_drain(smem_u32(&full[s]), (last_parity >> s) & 1u, p.err);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------- MMA issuer
@@ -1035,7 +1036,7 @@ __global__ void __launch_bounds__(GemmCfg<BN, B8, PAIR, EPI>::kThreads, 1)
       // all MMAs issued by this thread complete before TMEM is released
       if constexpr (PAIR) umma_commit_pair(smem_u32(drain));
       else umma_commit(smem_u32(drain));
-      mbar_wait(smem_u32(drain), 0, p.err, kErrTimeoutDrain);
+      mbar_drain(smem_u32(drain), 0, p.err);
     }
   } else if (warp < Cfg::kConvWarp0) {
     // ------------------------------------------------------------- epilogue warps
