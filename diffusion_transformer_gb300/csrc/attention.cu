@@ -284,12 +284,12 @@ __global__ void __launch_bounds__(AttnSplit<D, MODE>::kThreads, 1)
         }
         s += j1 - j0;
       }
-      // every issued copy lands before the CTA exits
-      if (nq > 0) mbar_wait(smem_u32(q_full), (nq - 1) & 1, p.err, kErrTimeoutDrain);
+      // every issued copy lands before the CTA exits, whatever the error word says
+      if (nq > 0) mbar_drain(smem_u32(q_full), (nq - 1) & 1, p.err);
       for (int i = nk - 2 < 0 ? 0 : nk - 2; i < nk; ++i)
-        mbar_wait(smem_u32(&k_full[i & 1]), (i >> 1) & 1, p.err, kErrTimeoutDrain);
+        mbar_drain(smem_u32(&k_full[i & 1]), (i >> 1) & 1, p.err);
       for (int i = nv - 2 < 0 ? 0 : nv - 2; i < nv; ++i)
-        mbar_wait(smem_u32(&v_full[i & 1]), (i >> 1) & 1, p.err, kErrTimeoutDrain);
+        mbar_drain(smem_u32(&v_full[i & 1]), (i >> 1) & 1, p.err);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer
@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(AttnSplit<D, MODE>::kThreads, 1)
         s += n;
       }
       umma_commit(smem_u32(drain));
-      mbar_wait(smem_u32(drain), 0, p.err, kErrTimeoutDrain);
+      mbar_drain(smem_u32(drain), 0, p.err);
     }
   } else if (fixed) {
     // ------------------------------------------------------------------ softmax warps, fixed max
